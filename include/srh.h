@@ -535,6 +535,174 @@ int srh_check_error(srh_ctx* ctx);
  */
 int srh_selftest_wait_timeout(srh_ctx* ctx, int limit_us, srh_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Paged 8-bit KV cache (no counterpart on the pages, whose rows are fp32 and
+ * whose context length is one for all sequences): requests of different
+ * lengths share a pool of blocks of tokens; rows are held as e4m3 codes with
+ * one scale per (block, head). A serving step is
+ *
+ *   kv8_resize     block tables and slot maps from the new request lengths
+ *                  (growth, and truncation of rejected tokens);
+ *   kv8_norm_rope  RMS norm of every query and key head, position rotation;
+ *   kv8_append     the new rows into the cache;
+ *   kv8_attend     attention of 1..n query tokens per request over it.
+ *
+ * A kv8_cache holds the geometry and the scratch; the pool itself is the
+ * caller's (one per layer, any number of layers on one handle and one table):
+ *   codes  uint8 e4m3 [n_blocks][n_kv_heads][block_tokens][head_dim], 16-byte
+ *          aligned, block_stride bytes from one block to the next
+ *   scale  fp32 [n_blocks][n_kv_heads]; a value is code * scale. A scale lies
+ *          in [2^-64, 2^64] (kv8_append writes powers of two in that range;
+ *          an appended value that would need a larger one is saturated)
+ *   table  int32 [batch][max_blocks]: block of tokens [j * block_tokens, ...)
+ *          of each request
+ *   len    int32 [batch]: tokens of each request
+ * Requests are indexed 0 .. n_req-1 with n_req <= batch. Packed per-token
+ * arrays hold request b's rows at cu[b] .. cu[b+1]-1 (int32 cu [n_req+1],
+ * ascending, cu[0] >= 0); rows outside every request are not touched.
+ *
+ * Device-side guards: a length, a table entry, a cu value or a slot outside
+ * its range is never followed; the rows concerned are left out (an attention
+ * reads such a block as absent) and kv8_check_error() reports it.
+ * Calls on one handle share its scratch: order them on one stream or by
+ * events, captured graphs included (two graphs of one handle must not replay
+ * at the same time). The calls run on the handle's device whatever device is
+ * current, allocate nothing, and may be captured. A handle is not thread-safe.
+ */
+typedef struct kv8_cache kv8_cache;
+
+typedef struct {
+    int batch;               /* table rows, 1 .. 4096 */
+    int n_kv_heads;          /* 1 .. 256 */
+    int head_dim;            /* 128, 256 or 512 */
+    int block_tokens;        /* 16, 32, 64 or 128 */
+    int n_blocks;            /* blocks of the pool, >= 1 */
+    int max_blocks;          /* blocks a request may hold; max_blocks * block_tokens <= 2^30 */
+    int shared_kv;           /* 1: latent rows, V = K (one pool of codes) */
+    long long block_stride;  /* bytes between blocks of codes, a multiple of 16; 0: dense */
+} kv8_config;
+
+/* One layer's pool. v_* are ignored with shared_kv. */
+typedef struct {
+    uint8_t* k_codes;
+    float* k_scale;
+    uint8_t* v_codes;
+    float* v_scale;
+} kv8_pool;
+
+/* Makes a handle on the current device (scratch of about 40 MB).
+ * Errors: SRH_ERR_INVALID, SRH_ERR_NOMEM, SRH_ERR_CUDA (kv8_last_error(NULL)). */
+int kv8_create(const kv8_config* cfg, kv8_cache** out);
+
+/* Waits for the handle's device and frees the handle. NULL is a no-op. */
+void kv8_destroy(kv8_cache* c);
+
+/*
+ * Brings request b from d_len[b] to d_new_len[b] tokens (more or fewer).
+ *   d_new_len     [n_req] int32, 0 .. max_blocks * block_tokens
+ *   d_len         [n_req] int32, in: lengths now; out: d_new_len
+ *   d_table       [batch][max_blocks] int32, in/out: released entries become -1
+ *   d_free        [n_blocks] int32, in/out: a stack of free block ids
+ *   d_n_free      [1] int32, in/out: its depth
+ *   d_cu          [n_req + 1] int32 out: cu[b+1] - cu[b] = max(0, new - old)
+ *   d_pos, d_slot [cap] int32 / int64 out, both or neither NULL (then cap is
+ *                 0): position of each new token in its request, and its slot
+ *                 table[b][pos / block_tokens] * block_tokens + pos % block_tokens
+ * Blocks are released first, so that the first of them (by request, then by
+ * block) is on top of the stack, then taken from the top in the same order:
+ * growing and shrinking back restores the stack. All or nothing: when a length
+ * is out of range, a released entry is no block, the free blocks or cap do not
+ * suffice, nothing changes, d_cu is all zeros, and kv8_check_error() returns
+ * SRH_ERR_NOMEM (too few free blocks) or SRH_ERR_BOUNDS.
+ */
+int kv8_resize(kv8_cache* c, const int32_t* d_new_len, int n_req, int32_t* d_len, int32_t* d_table, int32_t* d_free,
+               int32_t* d_n_free, int32_t* d_cu, int32_t* d_pos, int64_t* d_slot, int cap, srh_stream_t stream);
+
+/* Heads of one kind in kv8_norm_rope. Strides are in elements, multiples of 8;
+ * bases are 16-byte aligned; heads of a row are dense. */
+typedef struct {
+    const uint16_t* x;       /* bf16 [n_tok] rows of [n_heads][head_dim] */
+    long long x_row;
+    uint16_t* out;           /* bf16; may be x itself (same row stride, no slots) */
+    long long out_row;
+    const float* weight;     /* fp32 [head_dim], 16-byte aligned, or NULL (ones) */
+    int n_heads;             /* 0: no heads of this kind */
+    const int64_t* slot;     /* NULL: token t's row is row t of out; else row slot[t]: a negative
+                                slot skips the token. Slots of one call are distinct */
+    long long n_slots;       /* rows of out, with slot */
+} kv8_heads;
+
+/*
+ * Per head: y = x * rsqrt(mean(x^2) + eps) * weight, then the pairs (a, b) of
+ * dims [rot_off, rot_off + rot_dim) turn to (a cos t - b sin t, a sin t + b cos t),
+ * t = pos * inv_freq[i] for pair i: dims 2i and 2i+1 (KV8_ROPE_PAIRS) or i and
+ * i + rot_dim/2 (KV8_ROPE_HALVES) from rot_off. Queries and keys in one launch
+ * (an indexer's queries and keys, or an attention's). The angle is reduced to
+ * a turn in 64-bit fixed point, so far positions lose nothing.
+ *   d_pos       [n_tok] int32 (any value)
+ *   d_inv_freq  [rot_dim / 2] double, finite; NULL only with rot_dim 0
+ *   head_dim    8 .. 512, a multiple of 8; rot_dim a multiple of 16 and
+ *               rot_off of 8, rot_off + rot_dim <= head_dim
+ *   eps         >= 0, finite
+ * A slot >= n_slots is skipped and reported as SRH_ERR_BOUNDS.
+ */
+#define KV8_ROPE_PAIRS 0
+#define KV8_ROPE_HALVES 1
+int kv8_norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_tok, int head_dim, const int32_t* d_pos,
+                  const double* d_inv_freq, int rot_dim, int rot_off, int style, float eps, srh_stream_t stream);
+
+/*
+ * Writes the last cu[b+1] - cu[b] tokens of each request (positions
+ * len[b] - (cu[b+1] - cu[b]) .. len[b]-1, with d_len the lengths kv8_resize
+ * left) into the cache.
+ *   d_k, d_v  bf16 rows [n_rows] of [n_kv_heads][head_dim], 16-byte aligned,
+ *             row strides in elements, multiples of 8; d_v ignored with shared_kv
+ *   n_rows    rows of d_k / d_v: cu[n_req] <= n_rows
+ * Per (block, head): scale = 2^e with the smallest e for which the block's
+ * largest magnitude is <= 448 * 2^e, code = e4m3(x / scale) (to nearest, ties to
+ * even). A block that held tokens of the request before keeps the larger of its
+ * scale and the new one; if it grows, the codes held are rescaled (exact but
+ * for values that fall below e4m3's smallest normal). The first token of a
+ * block starts its scale anew. Values that are not finite are stored as 0,
+ * values beyond 448 * 2^64 saturate; both are reported as SRH_ERR_RANGE.
+ * A block being written must belong to one request only (copy a shared, partly
+ * filled block first).
+ */
+int kv8_append(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
+               int n_req, const uint16_t* d_k, long long k_row, const uint16_t* d_v, long long v_row, int n_rows,
+               srh_stream_t stream);
+
+/*
+ * Attention of each request's last tokens over its cache:
+ *   o_{i,h} = sum_t softmax_t(scale * <q_{i,h}, K_t>) V_t
+ * for query row i of request b at position p = len[b] - (cu[b+1] - cu[b]) + i,
+ * over tokens t <= p (and t > p - window with window > 0); query head h reads
+ * KV head h / (n_heads / n_kv_heads). A row that sees no token gives zeros.
+ *   d_q, d_out  bf16 [n_rows] rows of [n_heads][head_dim], 16-byte aligned, row
+ *               strides in elements, multiples of 8; d_out is not d_q
+ *   n_heads     a multiple of n_kv_heads; n_rows * n_heads <= 2^30
+ *   scale       finite; window >= 0
+ * Precision: fp32 scores, statistics and sums. Queries enter the products as
+ * two e4m3 terms per value (bf16's 8 significant bits; a value below about
+ * 2^-9 of its row's largest keeps 2^-17 of that largest), weights as two
+ * e4m3 terms each (about 9 bits; weights below 2^-17 of the row's largest
+ * contribution are dropped from the value sum). Codes of tokens below len must
+ * not be NaN codes (kv8_append writes none); what lies behind a request's
+ * length, in its last block or elsewhere, is not used.
+ */
+int kv8_attend(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
+               int n_req, const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,
+               uint16_t* d_out, long long out_row, srh_stream_t stream);
+
+/* Waits for the handle's device and reports its sticky error word: SRH_OK,
+ * SRH_ERR_NOMEM, SRH_ERR_BOUNDS, SRH_ERR_TIMEOUT or SRH_ERR_RANGE (first match
+ * in that order), or SRH_ERR_CUDA. The word is cleared after it is read. */
+int kv8_check_error(kv8_cache* c);
+
+/* Detail of the last failing call on the handle (NULL: of kv8_create). */
+const char* kv8_last_error(kv8_cache* c);
+
 /* Static text for a return code. */
 const char* srh_error_string(int code);
 

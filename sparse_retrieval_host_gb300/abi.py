@@ -33,6 +33,8 @@ SRH_FLAG_TEST_FAIL_HOST_ALLOC = 1
 KV_DIM = 512
 WINDOW = 128
 SRH_NOALLOC_MAX_BATCH = 64
+KV8_ROPE_PAIRS = 0
+KV8_ROPE_HALVES = 1
 SRH_NOALLOC_MAX_N = 1 << 30
 
 
@@ -75,6 +77,22 @@ class SrhAdaptive(ctypes.Structure):
     """srh_adaptive: the hit-rate policy of the staging capacity."""
     _fields_ = [(name, ctypes.c_int) for name in
                 ("enabled", "g_min", "g_max", "g_init", "epoch", "lo_permille", "hi_permille", "delta")]
+
+
+class Kv8Config(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in
+                ("batch", "n_kv_heads", "head_dim", "block_tokens", "n_blocks", "max_blocks", "shared_kv")]
+    _fields_ += [("block_stride", ctypes.c_longlong)]
+
+
+class Kv8Pool(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("k_codes", "k_scale", "v_codes", "v_scale")]
+
+
+class Kv8Heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_row", ctypes.c_longlong), ("out", ctypes.c_void_p),
+                ("out_row", ctypes.c_longlong), ("weight", ctypes.c_void_p), ("n_heads", ctypes.c_int),
+                ("slot", ctypes.c_void_p), ("n_slots", ctypes.c_longlong)]
 
 
 class SrhError(RuntimeError):
@@ -121,6 +139,15 @@ SIGNATURES = [
     ("srh_hostloop_wait", _i, [_vp, _ll]),
     ("srh_hostloop_sync", _i, [_vp]),
     ("srh_hostloop_destroy", None, [_vp]),
+    ("kv8_create", _i, [ctypes.POINTER(Kv8Config), ctypes.POINTER(_vp)]),
+    ("kv8_destroy", None, [_vp]),
+    ("kv8_resize", _i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp]),
+    ("kv8_norm_rope", _i, [_vp, ctypes.POINTER(Kv8Heads), ctypes.POINTER(Kv8Heads), _i, _i, _vp, _vp, _i, _i, _i, _f,
+                           _vp]),
+    ("kv8_append", _i, [_vp, ctypes.POINTER(Kv8Pool), _vp, _vp, _vp, _i, _vp, _ll, _vp, _ll, _i, _vp]),
+    ("kv8_attend", _i, [_vp, ctypes.POINTER(Kv8Pool), _vp, _vp, _vp, _i, _vp, _ll, _i, _i, _f, _i, _vp, _ll, _vp]),
+    ("kv8_check_error", _i, [_vp]),
+    ("kv8_last_error", ctypes.c_char_p, [_vp]),
     ("srh_error_string", ctypes.c_char_p, [_i]),
     ("srh_last_error", ctypes.c_char_p, [_vp]),
 ]
@@ -349,6 +376,50 @@ def srh_hostloop_sync(ctx, lp) -> None:
 
 def srh_hostloop_destroy(lp) -> None:
     load().srh_hostloop_destroy(lp)
+
+
+def _check_kv8(rc: int, where: str, cache=None) -> None:
+    if rc != SRH_OK:
+        raise SrhError(rc, where, load().kv8_last_error(cache).decode(errors="replace"))
+
+
+def kv8_create(cfg: Kv8Config) -> int:
+    out = _vp()
+    _check_kv8(load().kv8_create(ctypes.byref(cfg), ctypes.byref(out)), "kv8_create")
+    return out.value
+
+
+def kv8_destroy(cache) -> None:
+    load().kv8_destroy(cache)
+
+
+def kv8_resize(cache, new_len, n_req, length, table, free, n_free, cu, pos, slot, cap, stream=None) -> None:
+    _check_kv8(load().kv8_resize(cache, _ptr(new_len), n_req, _ptr(length), _ptr(table), _ptr(free), _ptr(n_free),
+                                 _ptr(cu), _ptr(pos), _ptr(slot), cap, _stream(stream)), "kv8_resize", cache)
+
+
+def kv8_norm_rope(cache, q, k, n_tok, head_dim, pos, inv_freq, rot_dim, rot_off, style, eps, stream=None) -> None:
+    """q, k: Kv8Heads or None."""
+    ref = lambda h: None if h is None else ctypes.byref(h)
+    _check_kv8(load().kv8_norm_rope(cache, ref(q), ref(k), n_tok, head_dim, _ptr(pos), _ptr(inv_freq), rot_dim, rot_off,
+                                    style, float(eps), _stream(stream)), "kv8_norm_rope", cache)
+
+
+def kv8_append(cache, pool: Kv8Pool, table, length, cu, n_req, k, k_row, v, v_row, n_rows, stream=None) -> None:
+    _check_kv8(load().kv8_append(cache, ctypes.byref(pool), _ptr(table), _ptr(length), _ptr(cu), n_req, _ptr(k), k_row,
+                                 _ptr(v), v_row, n_rows, _stream(stream)), "kv8_append", cache)
+
+
+def kv8_attend(cache, pool: Kv8Pool, table, length, cu, n_req, q, q_row, n_rows, n_heads, scale, window, out, out_row,
+               stream=None) -> None:
+    _check_kv8(load().kv8_attend(cache, ctypes.byref(pool), _ptr(table), _ptr(length), _ptr(cu), n_req, _ptr(q), q_row,
+                                 n_rows, n_heads, float(scale), window, _ptr(out), out_row, _stream(stream)),
+               "kv8_attend", cache)
+
+
+def kv8_check_error(cache) -> int:
+    """Returns the code (does not raise): SRH_OK, SRH_ERR_NOMEM, SRH_ERR_BOUNDS, SRH_ERR_TIMEOUT or SRH_ERR_RANGE."""
+    return load().kv8_check_error(cache)
 
 
 def srh_check_error(ctx) -> int:

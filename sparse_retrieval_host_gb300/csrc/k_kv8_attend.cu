@@ -1,0 +1,1011 @@
+// Attention over the paged 8-bit cache (kv8_attend), on the 5th-generation
+// tensor cores straight from the e4m3 codes.
+//
+//   o_r = sum_t w_rt V_t / sum_t w_rt,  w_rt = exp(scale <q_r, K_t>),
+//   K_t = kc_t * ks(block of t), V_t = vc_t * vs(block of t)
+//
+// Tokens are the M dimension of both products, so a cache row never leaves the
+// form it is stored in:
+//   S^T[t, r]  = kc[t, :] . q[r, :]      A = code tile (K-major), B = queries
+//   O^T[d, r] += vc[:, d] . p[:, r]      A = the same kind of tile read MN-major
+// kind::f8f6f4 takes 8-bit operands on both sides. A query row is scaled by a
+// power of two to a largest magnitude in [128, 256) and split into two e4m3
+// terms, hi = e4m3(q), lo = e4m3(q - hi): 4 + 4 significant bits, which is bf16
+// exactly (below 2^-9 of the row's largest the absolute error is 2^-17 of it).
+// Weights are split the same way. The two terms are two columns of one MMA (N =
+// 2 * rows), so a tile is read from shared memory once for both.
+//
+// Block scales: ks multiplies the score, one factor per thread (thread = TMEM
+// lane = token). vs goes into the exponent: u = s + log2(vs), p = 2^(u - ref), so
+// the column p holds what the token contributes, and the rounding of p is
+// relative to the largest contribution; the softmax sum takes p / vs in fp32.
+//
+// The running reference `ref` of a row is kept 2^6 below its maximum, and is
+// moved only when a tile exceeds it by 2^8 (e4m3 ends at 448): one vote of the
+// 128 threads per tile; the maximum itself, the rescaling of the sums and of
+// O^T in TMEM only happen when the vote says so (the first tile, then rarely).
+//
+// Work: a "row tile" is RT of the (token, head) rows that share a KV head of a
+// request; its tokens are cut into tiles of 128. Every (request, KV head, row
+// tile, token tile) is a unit; CTA i of n takes units [i U / n, (i + 1) U / n),
+// found from the lengths on the device, so ragged batches and single long
+// requests both fill the SMs and nothing depends on host knowledge of lengths.
+// An item whose units fall to several CTAs leaves fp32 partial sums, which a
+// second kernel joins in order (no atomics: results repeat bit for bit).
+//
+// Roles (192 threads): warps 0-3 softmax (thread = token; also queries in and
+// outputs out), warp 4 TMA (one box per block of tokens and 128 values, into a
+// ring of tile slots), warp 5 MMA issue. QK of tile j + 1 is issued before PV of
+// tile j. Every wait is bounded; on a timeout the CTA records it, lets its
+// copies and MMAs end, frees TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv8_internal.cuh"
+#include "umma.cuh"
+
+namespace srh {
+namespace kv8 {
+namespace {
+
+using namespace umma;
+
+constexpr int kTile = 128;               // tokens per tile
+constexpr int kThreads = 192;
+constexpr int kSoft = 128;               // softmax threads
+constexpr float kLow = -1e30f;           // reference of a row that has seen no token
+constexpr float kHead = 6.f;             // the reference stays 2^6 below the maximum ...
+constexpr float kRoom = 8.f;             // ... and moves when a weight would pass 2^8
+
+// DB: head_dim / 128. RT: rows per row tile. SHARED: V = K.
+template <int DB_, int RT_, bool SHARED_>
+struct Shape {
+    static constexpr int DB = DB_, RT = RT_;
+    static constexpr bool SHARED = SHARED_;
+    static constexpr int N = 2 * RT;                       // hi and lo columns
+    // O^T's hi and lo columns stay apart where TMEM has room for both
+    static constexpr bool CAT = DB * N + N <= 512;
+    static constexpr int ON = CAT ? N : RT;                // O^T columns per 128 dims
+    static constexpr int COLS = N + DB * ON;
+    static constexpr int ALLOC = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static constexpr int kTileBytes = DB * kTile * 128;
+    static constexpr int kQBytes = DB * N * 128;
+    static constexpr int kPBytes = kTile * N;
+    static constexpr int kPitch = CAT ? N : RT;            // bytes of one token's row of p
+    static constexpr int CTAS = DB == 1 ? 2 : 1;           // per SM
+    static constexpr int SLOTS = DB == 1 ? (RT == 64 ? 4 : 5) : DB == 2 ? 4 : RT == 16 ? 3 : 2;
+    static constexpr int kOffQ = SLOTS * kTileBytes;
+    static constexpr int kOffP = kOffQ + kQBytes;
+    static constexpr int kOffBars = kOffP + kPBytes;
+};
+
+struct Args {
+    const uint16_t* q;
+    uint16_t* out;
+    long long q_row, out_row;
+    const int32_t* cu;
+    const int32_t* len;
+    const int32_t* table;
+    const float* ks;
+    const float* vs;
+    float* part_o;
+    float* part_ml;
+    int4* meta;
+    uint32_t* err;
+    int n_req, n_rows, heads, kv_heads, group;   // group = heads / kv_heads
+    int bs_log2, n_blocks, max_blocks;
+    float scale_log2;
+    int window;                                  // 0: none
+};
+
+// ---------------------------------------------------------------- the split of the work
+struct Request {
+    int q0, nq, len;
+    int nrt;           // row tiles
+    int tlo, nt;       // first token tile, token tiles (at least 1)
+};
+
+template <int RT>
+__device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
+    Request r;
+    const int c0 = a.cu[b], c1 = a.cu[b + 1], n = a.len[b], most = a.max_blocks << a.bs_log2;
+    r.q0 = min(max(c0, 0), a.n_rows);
+    r.nq = min(max(c1, r.q0), a.n_rows) - r.q0;
+    r.len = min(max(n, 0), most);
+    if (c0 != r.q0 || c1 != r.q0 + r.nq || n != r.len) *bad = true;
+    r.nrt = (r.nq * a.group + RT - 1) / RT;
+    const int p0 = r.len - r.nq;                                   // position of the first query
+    r.tlo = a.window ? max(0, p0 - a.window + 1) / kTile : 0;
+    r.nt = max(1, (r.len + kTile - 1) / kTile - r.tlo);
+    return r;
+}
+__device__ __forceinline__ long long units(const Args& a, const Request& r) {
+    return (long long)r.nrt * a.kv_heads * r.nt;
+}
+
+// One CTA's share of one item.
+struct Segment {
+    int b, h, rt;
+    int row0, nr;        // rows of the row tile in the request's (token, head) order
+    int t0, n;           // first token tile and tiles to run (0: no row sees any of them)
+    int slot;            // -1: the whole item; else the partial's slot
+    int parts;           // CTAs of the item, when it begins here and goes on
+    Request r;
+};
+
+// Walks the units [u, u1) that a CTA owns. Every role walks on its own.
+template <int RT>
+struct Walker {
+    long long u, u1, U;
+    long long off;       // u's place in request b
+    int b, n_cta, cta;
+    Request r;
+
+    __device__ __forceinline__ bool next(const Args& a, Segment* s) {
+        if (u >= u1) return false;
+        bool bad = false;
+        while (off >= units(a, r)) {
+            off -= units(a, r);
+            r = request<RT>(a, ++b, &bad);
+        }
+        const long long item = off / r.nt;
+        const int t_off = (int)(off - item * r.nt);
+        const int take = (int)min((long long)(r.nt - t_off), u1 - u);
+        const int i = (int)(item % r.nrt);
+        s->b = b;
+        s->h = (int)(item / r.nrt);
+        // row tiles from both ends in turn: neighbours then have the same work on
+        // average (a causal row tile has fewer tokens the earlier it is)
+        s->rt = (i & 1) ? r.nrt - 1 - (i >> 1) : (i >> 1);
+        s->row0 = s->rt * RT;
+        s->nr = min(RT, r.nq * a.group - s->row0);
+        s->r = r;
+        // token tiles that any of these rows sees
+        const int p_hi = r.len - r.nq + (s->row0 + s->nr - 1) / a.group;
+        const int p_lo = r.len - r.nq + s->row0 / a.group;
+        const int first = a.window ? max(0, p_lo - a.window + 1) / kTile : 0;
+        const int last = p_hi < 0 ? 0 : p_hi / kTile + 1;
+        const int lo = max(r.tlo + t_off, first), hi = min(r.tlo + t_off + take, last);
+        s->t0 = lo;
+        s->n = max(0, hi - lo);
+        s->slot = -1;
+        s->parts = 0;
+        if (take != r.nt) {
+            s->slot = 2 * cta + (t_off == 0);
+            if (t_off == 0) {
+                const long long end = u + r.nt - 1;                // the item's last unit
+                s->parts = (int)(((end + 1) * n_cta - 1) / U) - cta + 1;
+            }
+        }
+        u += take;
+        off += take;
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------- small device helpers
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+// Shared-memory descriptor of an MN-major operand whose rows (one per K index)
+// are PITCH = 32, 64 or 128 bytes with the swizzle of that width: groups of 8
+// rows along K follow each other; one group spans the whole M or N extent.
+template <int PITCH>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
+    uint64_t d = desc_sw128(saddr, 16, 8 * PITCH);
+    d &= ~((uint64_t)7 << 61);
+    d |= (uint64_t)(PITCH == 128 ? 2 : PITCH == 64 ? 4 : 6) << 61;
+    return d;
+}
+// Byte offset of 16-byte chunk c of row r in such an operand.
+template <int PITCH>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
+    const uint32_t x = PITCH == 128 ? (r & 7u) : PITCH == 64 ? ((r >> 1) & 3u) : ((r >> 2) & 1u);
+    return r * PITCH + ((c ^ x) << 4);
+}
+// Two e4m3 terms of each of four values: hi and lo codes, one byte each.
+__device__ __forceinline__ void split4(float v0, float v1, float v2, float v3, uint32_t* hi, uint32_t* lo) {
+    const __half2 a = __floats2half2_rn(v0, v1), b = __floats2half2_rn(v2, v3);
+    const uint32_t ha = __nv_cvt_halfraw2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hb = __nv_cvt_halfraw2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
+    const __half2 ra = __hsub2(a, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ha, __NV_E4M3)));
+    const __half2 rb = __hsub2(b, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hb, __NV_E4M3)));
+    const uint32_t la = __nv_cvt_halfraw2_to_fp8x2(ra, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t lb = __nv_cvt_halfraw2_to_fp8x2(rb, __NV_SATFINITE, __NV_E4M3);
+    *hi = ha | (hb << 16);
+    *lo = la | (lb << 16);
+}
+
+template <typename S>
+struct Bars {
+    uint64_t full[S::SLOTS];     // a tile's bytes landed
+    uint64_t empty[S::SLOTS];    // the MMAs that read it completed
+    uint64_t q_full;             // the queries are in shared memory
+    uint64_t s_full;             // S^T of a tile is in TMEM
+    uint64_t s_free;             // the softmax warps have it in registers
+    uint64_t p_full;             // the weights are in shared memory (and O^T is rescaled)
+    uint64_t pv_done;            // PV completed
+    uint64_t drain;
+    long long warp_sums[33];
+    long long start_off;
+    int start_b;
+    uint32_t tmem_base;
+    int abort;
+    alignas(16) float ref[S::RT];     // reference exponent of each row
+    alignas(16) float fac[S::RT];     // 2^(old reference - new)
+    alignas(16) float qs[S::RT];      // query scale * softmax scale * log2 e
+    float part[4][S::RT];             // per-warp maxima, then sums
+    float sum[S::RT];
+    int pos[S::RT];                   // position of the row's token; -1: no row
+    long long row_at[S::RT];          // its offset in out
+};
+
+template <typename S>
+constexpr int smem_bytes() {
+    return S::kOffBars + (int)sizeof(Bars<S>) + 1024;
+}
+
+// The column sums over a warp of v[RT]: lane i gets column i (and i + 32).
+template <int RT>
+__device__ __forceinline__ void column_sums(float (&v)[RT], int lane, float* out) {
+    if (RT == 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    }
+    constexpr int W = RT < 32 ? RT : 32;
+#pragma unroll
+    for (int g = 0; g < RT; g += W) {
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < o; ++i) {
+                const bool up = lane & o;
+                const float send = up ? v[g + i] : v[g + i + o], keep = up ? v[g + i + o] : v[g + i];
+                v[g + i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        }
+        if (lane < W) out[g + lane] = v[g];
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+template <typename S>
+__global__ void __launch_bounds__(kThreads, S::CTAS)
+attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+              const __grid_constant__ Args a) {
+    constexpr int DB = S::DB, RT = S::RT, N = S::N;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    Bars<S>& bs = *reinterpret_cast<Bars<S>*>(sm + S::kOffBars);
+    volatile int* abort = &bs.abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n_grid = gridDim.x, cta = blockIdx.x;
+
+    // ------------------------------------------------------------ this CTA's units
+    Walker<RT> w;
+    bool bad = false;
+    {
+        const int per = (a.n_req + kThreads - 1) / kThreads;
+        const int b0 = min(a.n_req, tid * per), b1 = min(a.n_req, b0 + per);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += units(a, request<RT>(a, b, &bad));
+        long long U;
+        const long long incl = block_scan(mine, bs.warp_sums, &U);
+        const int n = (int)min((long long)n_grid, U);
+        if (cta >= n) {                                    // nothing to do (every thread)
+            if (tid == 0) a.meta[cta] = make_int4(0, 0, 0, 0);
+            return;
+        }
+        w.U = U;
+        w.n_cta = n;
+        w.cta = cta;
+        w.u = U * cta / n;
+        w.u1 = U * (cta + 1) / n;
+        long long at = incl - mine;
+        if (w.u >= at && w.u < incl) {
+            for (int b = b0;; ++b) {
+                const long long k = units(a, request<RT>(a, b, &bad));
+                if (w.u < at + k) {
+                    bs.start_b = b;
+                    bs.start_off = w.u - at;
+                    break;
+                }
+                at += k;
+            }
+        }
+    }
+    if (cta == 0 && bad) atomicOr(a.err, kErrBounds);
+    if (tid == 0) {
+        for (int s = 0; s < S::SLOTS; ++s) {
+            mbar_init(&bs.full[s], 1);
+            mbar_init(&bs.empty[s], 1);
+        }
+        mbar_init(&bs.q_full, kSoft);
+        mbar_init(&bs.s_full, 1);
+        mbar_init(&bs.s_free, kSoft);
+        mbar_init(&bs.p_full, kSoft);
+        mbar_init(&bs.pv_done, 1);
+        mbar_init(&bs.drain, 1);
+        bs.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 5) tmem_alloc(&bs.tmem_base, S::ALLOC);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    w.b = bs.start_b;
+    w.off = bs.start_off;
+    bad = false;
+    w.r = request<RT>(a, w.b, &bad);
+    const uint32_t tmem = bs.tmem_base;
+    const uint32_t tm_s = tmem, tm_o = tmem + N;
+
+    bool ok = true;
+    Segment sg;
+    if (warp == 4) {
+        // ======================================================== TMA
+        uint32_t it = 0;                                   // tiles requested
+        const int bpt = kTile >> a.bs_log2;                // blocks per tile
+        auto load = [&](int tile, bool is_v) -> bool {
+            const int s = it % S::SLOTS;
+            const bool got = it < S::SLOTS || mbar_wait_abort(&bs.empty[s], ((it / S::SLOTS) + 1) & 1, abort) > 0;
+            if (!__all_sync(0xffffffffu, got)) return false;
+            const int bsz = 1 << a.bs_log2;
+            const int nb = min(bpt, (sg.r.len - tile * kTile + bsz - 1) >> a.bs_log2);
+            if (lane == 0) mbar_arrive_expect_tx(&bs.full[s], (uint32_t)(nb * bsz * DB * 128));
+            __syncwarp();
+            if (lane < nb * DB) {
+                const int pg = lane / DB, db = lane % DB;
+                const int id = a.table[(size_t)sg.b * a.max_blocks + (size_t)tile * bpt + pg];
+                const uint32_t dst = smem_u32(sm + s * S::kTileBytes) + db * (kTile * 128) + pg * bsz * 128;
+                // an id that is no block reads as zeros (out of the tensor's range)
+                tma_load_4d(dst, is_v ? &vmap : &kmap, db * 128, 0, sg.h, id < 0 ? a.n_blocks : min(id, a.n_blocks),
+                            &bs.full[s]);
+            }
+            __syncwarp();
+            ++it;
+            return true;
+        };
+        while (ok && w.next(a, &sg)) {
+            for (int j = 0; ok && j < sg.n; ++j) {
+                ok = load(sg.t0 + j, false);
+                if (!S::SHARED && ok && j > 0) ok = load(sg.t0 + j - 1, true);
+            }
+            if (!S::SHARED && ok && sg.n > 0) ok = load(sg.t0 + sg.n - 1, true);
+        }
+        if (!ok)   // every copy issued lands before the CTA may leave
+            for (uint32_t i = it > S::SLOTS ? it - S::SLOTS : 0; i < it; ++i)
+                mbar_wait(&bs.full[i % S::SLOTS], (i / S::SLOTS) & 1);
+    } else if (warp == 5) {
+        // ======================================================== MMA issue
+        if (lane == 0) {
+            constexpr uint32_t id_qk = idesc_f32acc(0, 0, 0, kTile, N);          // e4m3, both K-major
+            constexpr uint32_t id_pv = idesc_f32acc(0, 1, 1, 128, S::ON);        // both MN-major
+            const uint32_t q0 = smem_u32(sm + S::kOffQ), p0 = smem_u32(sm + S::kOffP);
+            uint32_t it = 0, g = 0, segs = 0;              // tiles taken, token tiles, segments with tiles
+            uint32_t v_slot = 0;                           // slot of the tile whose PV is due
+            auto pv = [&](uint32_t gt, bool first) -> bool {
+                if (mbar_wait_abort(&bs.p_full, gt & 1, abort) <= 0) return false;
+                if (!S::SHARED) {
+                    v_slot = it % S::SLOTS;
+                    if (mbar_wait_abort(&bs.full[v_slot], (it / S::SLOTS) & 1, abort) <= 0) return false;
+                    ++it;
+                }
+                tc_fence_after();
+                const uint32_t v0 = smem_u32(sm + v_slot * S::kTileBytes);
+#pragma unroll
+                for (int mb = 0; mb < DB; ++mb)
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 32; ++kk) {
+                        const uint64_t va = desc_sw128(v0 + mb * (kTile * 128) + kk * 32 * 128, 16, 1024);
+                        const uint32_t acc = !first || kk > 0;
+                        mma_f8(tm_o + mb * S::ON, va, desc_rows<S::kPitch>(p0 + kk * 32 * S::kPitch), id_pv, acc);
+                        if (!S::CAT)
+                            mma_f8(tm_o + mb * S::ON, va,
+                                   desc_rows<S::kPitch>(p0 + kTile * S::kPitch + kk * 32 * S::kPitch), id_pv, 1);
+                    }
+                mma_commit(&bs.empty[v_slot]);
+                mma_commit(&bs.pv_done);
+                return true;
+            };
+            while (ok && w.next(a, &sg)) {
+                if (sg.n == 0) continue;
+                ok = mbar_wait_abort(&bs.q_full, segs & 1, abort) > 0;
+                ++segs;
+                uint32_t next_v = 0;
+                for (int j = 0; ok && j < sg.n; ++j) {
+                    const uint32_t s = it % S::SLOTS;
+                    if (mbar_wait_abort(&bs.full[s], (it / S::SLOTS) & 1, abort) <= 0 ||
+                        (g > 0 && mbar_wait_abort(&bs.s_free, (g - 1) & 1, abort) <= 0)) {
+                        ok = false;
+                        break;
+                    }
+                    ++it;
+                    tc_fence_after();
+                    const uint32_t k0 = smem_u32(sm + s * S::kTileBytes);
+#pragma unroll
+                    for (int kk = 0; kk < DB * 4; ++kk)
+                        mma_f8(tm_s, desc_sw128(k0 + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024),
+                               desc_sw128(q0 + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024), id_qk, kk > 0);
+                    if (!S::SHARED) mma_commit(&bs.empty[s]);
+                    mma_commit(&bs.s_full);
+                    ++g;
+                    if (j > 0) {
+                        v_slot = next_v;
+                        ok = pv(g - 2, j == 1);
+                    }
+                    next_v = s;
+                }
+                if (ok) {
+                    v_slot = next_v;
+                    ok = pv(g - 1, sg.n == 1);
+                }
+            }
+            // every MMA issued completes before TMEM is freed
+            mma_commit(&bs.drain);
+            if (!mbar_wait(&bs.drain, 0)) ok = false;
+        }
+    } else {
+        // ======================================================== softmax
+        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        const uint32_t my_s = tm_s + lane_base, my_o = tm_o + lane_base;
+        unsigned char* qsm = sm + S::kOffQ;
+        unsigned char* psm = sm + S::kOffP;
+        uint32_t g = 0, it = 0;                            // token tiles, tiles of the ring
+        bool fail = false, ids_bad = false, begun = false;
+        // (ks, log2 vs, 1 / vs) of this thread's token in a tile; a token that is
+        // not there or has no block: (0, -inf, 0)
+        auto scales = [&](int tile, float* ks, float* lv, float* iv) {
+            const int t = tile * kTile + tid;
+            *ks = 0.f;
+            *lv = -INFINITY;
+            *iv = 0.f;
+            if (t >= sg.r.len) return;
+            const int id = a.table[(size_t)sg.b * a.max_blocks + (t >> a.bs_log2)];
+            if (id < 0 || id >= a.n_blocks) {
+                ids_bad = true;
+                return;
+            }
+            const size_t at = (size_t)id * a.kv_heads + sg.h;
+            *ks = __ldg(a.ks + at);
+            const float vs = S::SHARED ? *ks : __ldg(a.vs + at);
+            *lv = lg2(vs);
+            *iv = 1.f / vs;
+        };
+        float l[RT];
+        while (w.next(a, &sg)) {
+            if (sg.parts) begun = true;
+            if (sg.parts && tid == 0) a.meta[cta] = make_int4(sg.b, sg.h, sg.rt, sg.parts);
+            soft_sync();                                   // the last segment's shared arrays are read
+            const int p_first = sg.r.len - sg.r.nq;
+            if (tid < RT) {
+                const int row = sg.row0 + tid, tok = row / a.group, hd = sg.h * a.group + row % a.group;
+                const bool on = tid < sg.nr;
+                bs.pos[tid] = on ? p_first + tok : -1;
+                bs.row_at[tid] = (long long)(sg.r.q0 + tok) * a.out_row + (long long)hd * (DB * 128);
+                // a column without a row is held at weight 0 by a reference out of reach
+                bs.ref[tid] = on ? kLow : -kLow;
+            }
+            if (sg.n > 0) {
+                // queries: a warp per row, 4 values per lane and 128 dims
+                constexpr int U = RT / 4 < 4 ? RT / 4 : 4;
+                for (int r0 = warp; r0 < RT; r0 += 4 * U) {
+                    uint2 x[U][DB];
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int r = r0 + 4 * i;
+                        const int row = sg.row0 + r, tok = row / a.group, hd = sg.h * a.group + row % a.group;
+                        const uint16_t* p = a.q + (size_t)(sg.r.q0 + tok) * a.q_row + (size_t)hd * (DB * 128) + lane * 4;
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+                            x[i][d] = r < sg.nr ? __ldg(reinterpret_cast<const uint2*>(p + d * 128)) : make_uint2(0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int r = r0 + 4 * i;
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+                            m = max(m, max(max(x[i][d].x & 0x7fffu, (x[i][d].x >> 16) & 0x7fffu),
+                                           max(x[i][d].y & 0x7fffu, (x[i][d].y >> 16) & 0x7fffu)));
+                        m = __reduce_max_sync(0xffffffffu, m);
+                        const int e = min(max((int)(m >> 7) - 127 - 7, -120), 120);
+                        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                        if (lane == 0)   // a row that is not finite has no result: NaN
+                            bs.qs[r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                                    : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) {
+                            uint32_t hi, lo;
+                            split4(__uint_as_float(x[i][d].x << 16) * inv, __uint_as_float(x[i][d].x & 0xffff0000u) * inv,
+                                   __uint_as_float(x[i][d].y << 16) * inv, __uint_as_float(x[i][d].y & 0xffff0000u) * inv,
+                                   &hi, &lo);
+                            unsigned char* q = qsm + d * (N * 128) + (lane & 3) * 4;
+                            *reinterpret_cast<uint32_t*>(q + sw128(r, lane >> 2)) = hi;
+                            *reinterpret_cast<uint32_t*>(q + sw128(RT + r, lane >> 2)) = lo;
+                        }
+                    }
+                }
+                fence_async_smem();
+                mbar_arrive(&bs.q_full);
+            }
+            soft_sync();
+#pragma unroll
+            for (int c = 0; c < RT; ++c) l[c] = 0.f;
+            const int win = a.window ? a.window : 1 << 30;
+            const int p_lo = bs.pos[0], p_hi = bs.pos[sg.nr - 1];
+            float ks, lv, iv;
+            if (sg.n > 0) scales(sg.t0, &ks, &lv, &iv);
+            bool stop = false;
+            for (int j = 0; j < sg.n; ++j, ++g) {
+                const int t0 = (sg.t0 + j) * kTile, t = t0 + tid;
+                float ks_n = 0.f, lv_n = 0.f, iv_n = 0.f;
+                if (j + 1 < sg.n) scales(sg.t0 + j + 1, &ks_n, &lv_n, &iv_n);
+                if (mbar_wait_abort(&bs.s_full, g & 1, abort) <= 0) fail = true;
+                tc_fence_after();
+                float x[RT];
+#pragma unroll
+                for (int c = 0; c < RT; c += 16) {
+                    float hi[16], lo[16];
+                    tmem_ld16(my_s + c, hi);
+                    tmem_ld16(my_s + RT + c, lo);
+                    tmem_ld_wait();
+                    tmem_regs_ready(hi);
+                    tmem_regs_ready(lo);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[c + i] = hi[i] + lo[i];
+                }
+                tc_fence_before();
+                mbar_arrive(&bs.s_free);
+                float most = kLow;
+                const bool edge = t0 + kTile - 1 > p_lo || t0 <= p_hi - win;
+#pragma unroll
+                for (int c = 0; c < RT; c += 4) {
+                    const float4 s4 = *reinterpret_cast<const float4*>(&bs.qs[c]);
+                    const float4 r4 = *reinterpret_cast<const float4*>(&bs.ref[c]);
+                    x[c] = fmaf(x[c] * s4.x, ks, lv);
+                    x[c + 1] = fmaf(x[c + 1] * s4.y, ks, lv);
+                    x[c + 2] = fmaf(x[c + 2] * s4.z, ks, lv);
+                    x[c + 3] = fmaf(x[c + 3] * s4.w, ks, lv);
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int p = bs.pos[c + i];
+                            if (t > p || t <= p - win) x[c + i] = -INFINITY;
+                        }
+                    }
+                    most = fmaxf(most, fmaxf(fmaxf(x[c] - r4.x, x[c + 1] - r4.y), fmaxf(x[c + 2] - r4.z, x[c + 3] - r4.w)));
+                }
+                if (soft_any(most > kRoom || fail)) {
+                    // new references: the maximum of the tile's 128 tokens per row
+                    float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < RT; ++c) {
+                        const float m = warp_max(x[c]);
+                        if (lane == (c & 31)) (c < 32 ? m0 : m1) = m;
+                    }
+                    if (lane < RT) bs.part[warp][lane] = m0;
+                    if (RT > 32) bs.part[warp][(lane + 32) % RT] = m1;
+                    if (soft_any(fail)) {                  // the same answer for all 128 threads
+                        stop = true;
+                        break;
+                    }
+                    if (tid < RT) {
+                        const float m = fmaxf(fmaxf(bs.part[0][tid], bs.part[1][tid]), fmaxf(bs.part[2][tid], bs.part[3][tid]));
+                        const float was = bs.ref[tid];
+                        float now = was;
+                        if (m - was > kRoom) now = m - kHead;
+                        bs.ref[tid] = now;
+                        bs.fac[tid] = now == was ? 1.f : ex2(was - now);
+                    }
+                    soft_sync();
+#pragma unroll
+                    for (int c = 0; c < RT; ++c) l[c] *= bs.fac[c];
+                    if (j > 0) {
+                        if (mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
+                        tc_fence_after();
+#pragma unroll
+                        for (int mb = 0; mb < DB; ++mb)
+#pragma unroll
+                            for (int c = 0; c < S::ON; c += 16) {
+                                float o[16];
+                                tmem_ld16(my_o + mb * S::ON + c, o);
+                                tmem_ld_wait();
+                                tmem_regs_ready(o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] *= bs.fac[(c + i) % RT];
+                                tmem_st16(my_o + mb * S::ON + c, o);
+                            }
+                        tmem_st_wait();
+                        tc_fence_before();
+                    }
+                }
+                // the weights of the last tile have been read
+                if (g > 0 && mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
+#pragma unroll
+                for (int c = 0; c < RT; c += 16) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 r4 = *reinterpret_cast<const float4*>(&bs.ref[c + i]);
+                        const float v0 = ex2(x[c + i] - r4.x), v1 = ex2(x[c + i + 1] - r4.y);
+                        const float v2 = ex2(x[c + i + 2] - r4.z), v3 = ex2(x[c + i + 3] - r4.w);
+                        l[c + i] = fmaf(v0, iv, l[c + i]);
+                        l[c + i + 1] = fmaf(v1, iv, l[c + i + 1]);
+                        l[c + i + 2] = fmaf(v2, iv, l[c + i + 2]);
+                        l[c + i + 3] = fmaf(v3, iv, l[c + i + 3]);
+                        split4(v0, v1, v2, v3, &hi[i / 4], &lo[i / 4]);
+                    }
+                    unsigned char* ph = psm + chunk_at<S::kPitch>(tid, c / 16);
+                    unsigned char* pl = S::CAT ? psm + chunk_at<S::kPitch>(tid, RT / 16 + c / 16) : ph + kTile * S::kPitch;
+                    *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                if (t0 + kTile > sg.r.len) {
+                    // rows behind the request: whatever lies there must not meet a weight of 0 as NaN
+                    const uint32_t vi = S::SHARED ? it + sg.n - 1 : it + 2 * sg.n - 1;
+                    const uint32_t s = vi % S::SLOTS;
+                    if (mbar_wait_abort(&bs.full[s], (vi / S::SLOTS) & 1, abort) <= 0) fail = true;
+                    if (t >= sg.r.len) {
+#pragma unroll
+                        for (int i = 0; i < DB * 8; ++i)
+                            *reinterpret_cast<uint4*>(sm + s * S::kTileBytes + (i >> 3) * (kTile * 128) + tid * 128 +
+                                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_async_smem();
+                mbar_arrive(&bs.p_full);
+                ks = ks_n;
+                lv = lv_n;
+                iv = iv_n;
+            }
+            if (stop) {
+                ok = false;
+                break;
+            }
+            it += sg.n * (S::SHARED ? 1 : 2);
+            // ---------------------------------------------------- out
+            if (sg.n > 0) {
+                column_sums<RT>(l, lane, bs.part[warp]);
+                if (mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
+                tc_fence_after();
+            }
+            soft_sync();
+            if (tid < RT) {
+                const float sum = sg.n > 0 ? (bs.part[0][tid] + bs.part[1][tid]) + (bs.part[2][tid] + bs.part[3][tid]) : 0.f;
+                bs.sum[tid] = sg.slot >= 0 ? sum : sum == 0.f ? 0.f : 1.f / sum;
+                if (sg.slot >= 0)
+                    reinterpret_cast<float2*>(a.part_ml)[(size_t)sg.slot * RT + tid] = make_float2(bs.ref[tid], sum);
+            }
+            soft_sync();
+            if (sg.n > 0 || sg.slot < 0) {
+#pragma unroll
+                for (int mb = 0; mb < DB; ++mb)
+#pragma unroll
+                    for (int c = 0; c < RT; c += 16) {
+                        if (c >= sg.nr) break;
+                        float o[16];
+                        if (sg.n > 0) {
+                            tmem_ld16(my_o + mb * S::ON + c, o);
+                            if (S::CAT) {
+                                float o2[16];
+                                tmem_ld16(my_o + mb * S::ON + RT + c, o2);
+                                tmem_ld_wait();
+                                tmem_regs_ready(o);
+                                tmem_regs_ready(o2);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] += o2[i];
+                            } else {
+                                tmem_ld_wait();
+                                tmem_regs_ready(o);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (c + i >= sg.nr) break;
+                            if (sg.slot < 0) {
+                                const __nv_bfloat16 v = __float2bfloat16_rn(bs.sum[c + i] == 0.f ? 0.f : o[i] * bs.sum[c + i]);
+                                a.out[bs.row_at[c + i] + mb * 128 + tid] = __bfloat16_as_ushort(v);
+                            } else {
+                                a.part_o[(((size_t)sg.slot * RT + c + i) * DB + mb) * 128 + tid] = o[i];
+                            }
+                        }
+                    }
+                tc_fence_before();
+            }
+        }
+        if (fail) ok = false;
+        if (ids_bad) atomicOr(a.err, kErrBounds);
+        if (!begun && tid == 0) a.meta[cta] = make_int4(0, 0, 0, 0);
+    }
+
+    // ------------------------------------------------------------ teardown
+    tc_fence_before();
+    const bool failed = __syncthreads_or(!ok);
+    if (failed && tid == 0) atomicOr(a.err, kErrTimeout);
+    pdl_trigger();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::ALLOC);
+    }
+}
+
+// ---------------------------------------------------------------- joining split items
+// A task is one row of one split item: its parts' references m_i and sums l_i
+// give weights 2^(m_i - max m); out = sum w_i O_i / sum w_i l_i, in part order.
+// 256 threads: D / 4 threads hold 4 values each, and the parts are shared out
+// among the groups of D / 4.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxParts = 1024;
+
+template <int DB, int RT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int n_cta) {
+    constexpr int VT = DB * 32;                       // threads per part
+    constexpr int PG = kJoinThreads / VT;             // parts at a time
+    __shared__ long long warp_sums[33];
+    __shared__ int items[kMaxParts];                  // CTAs that begin a split item
+    __shared__ float wt[kMaxParts];
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ float4 acc_s[PG > 1 ? kJoinThreads : 1];
+    const int tid = threadIdx.x;
+    pdl_wait();
+    // every CTA lists the split items (at most one per attention CTA)
+    int n_items = 0;
+    for (int base = 0; base < n_cta; base += kJoinThreads) {
+        const int i = base + tid;
+        const bool on = i < n_cta && a.meta[i].w > 0;
+        long long total;
+        const long long incl = block_scan(on, warp_sums, &total);
+        if (on) items[n_items + (int)incl - 1] = i;
+        n_items += (int)total;
+    }
+    __syncthreads();
+    for (int task = blockIdx.x; task < n_items * RT; task += gridDim.x) {
+        const int c0 = items[task / RT], row = task % RT;
+        const int4 it = a.meta[c0];                   // request, KV head, row tile, parts
+        bool bad = false;
+        const Request r = request<RT>(a, it.x, &bad);
+        const int rr = it.z * RT + row;
+        if (rr >= r.nq * a.group) continue;           // uniform
+        const int parts = it.w;
+        const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+        // part i's slot: the first CTA's trailing segment, the others' leading one
+        auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)); };
+        float m = kLow;
+        for (int i = tid; i < parts; i += kJoinThreads) {
+            const float2 v = __ldcg(&ml[slot(i) * RT + row]);
+            if (v.y != 0.f) m = fmaxf(m, v.x);
+        }
+        m = warp_max(m);
+        if ((tid & 31) == 0) red[tid >> 5] = m;
+        __syncthreads();
+        m = red[0];
+#pragma unroll
+        for (int i = 1; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[i]);
+        __syncthreads();
+        float sum = 0.f;
+        for (int i = tid; i < parts; i += kJoinThreads) {
+            const float2 v = __ldcg(&ml[slot(i) * RT + row]);
+            const float f = v.y != 0.f ? ex2(v.x - m) : 0.f;    // a part with no weight is not read
+            wt[i] = f;
+            if (v.y != 0.f) sum = fmaf(f, v.y, sum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if ((tid & 31) == 0) red[tid >> 5] = sum;
+        __syncthreads();
+        sum = red[0];
+#pragma unroll
+        for (int i = 1; i < kJoinThreads / 32; ++i) sum += red[i];
+        const int v = tid % VT, pg = tid / VT;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = pg; i < parts; i += PG) {
+            const float f = wt[i];
+            if (f == 0.f) continue;
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * RT + row) * (DB * 128)) + v);
+            acc.x = fmaf(f, o.x, acc.x);
+            acc.y = fmaf(f, o.y, acc.y);
+            acc.z = fmaf(f, o.z, acc.z);
+            acc.w = fmaf(f, o.w, acc.w);
+        }
+        if (PG > 1) {
+            acc_s[tid] = acc;
+            __syncthreads();
+            if (pg == 0)
+#pragma unroll
+                for (int i = 1; i < PG; ++i) {
+                    const float4 o = acc_s[i * VT + v];
+                    acc.x += o.x;
+                    acc.y += o.y;
+                    acc.z += o.z;
+                    acc.w += o.w;
+                }
+        }
+        if (pg == 0) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            const int tok = rr / a.group, hd = it.y * a.group + rr % a.group;
+            uint2 o;
+            memcpy(&o.x, &lo, 4);
+            memcpy(&o.y, &hi, 4);
+            *reinterpret_cast<uint2*>(a.out + (size_t)(r.q0 + tok) * a.out_row + (size_t)hd * (DB * 128) + v * 4) = o;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host side
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn() {
+    static EncodeTiled fn = []() -> EncodeTiled {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Codes as [n_blocks][heads][tokens][head_dim] bytes, in boxes of one block of
+// one head x 128 values with the 128-byte swizzle.
+bool encode_codes(CUtensorMap* m, const Cache& c, const uint8_t* base) {
+    const EncodeTiled enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t D = c.cfg.head_dim, bs = c.cfg.block_tokens;
+    const cuuint64_t dims[4] = {D, bs, (cuuint64_t)c.cfg.n_kv_heads, (cuuint64_t)c.cfg.n_blocks};
+    const cuuint64_t strides[3] = {D, D * bs, (cuuint64_t)c.block_stride};
+    const cuuint32_t box[4] = {128, (cuuint32_t)bs, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename S>
+cudaError_t run(const Cache& c, const CUtensorMap& km, const CUtensorMap& vm, const Args& a, cudaStream_t st) {
+    const int grid = S::CTAS * c.sm_count;
+    static_assert(S::CTAS * smem_bytes<S>() <= 232448 + (S::CTAS - 1) * 1024, "the CTAs of an SM must fit its shared memory");
+    if ((size_t)grid * 2 * S::RT * S::DB * 128 > c.part_o_floats || (size_t)grid * 4 * S::RT > c.part_ml_floats ||
+        (size_t)grid > c.meta_n || grid > kMaxParts)
+        return cudaErrorInvalidValue;
+    attend_kernel<S><<<grid, kThreads, smem_bytes<S>(), st>>>(km, vm, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_k(join_kernel<S::DB, S::RT>, dim3((unsigned)(2 * c.sm_count)), dim3(kJoinThreads), 0, st, true, a, grid);
+}
+
+template <int DB, bool SHARED>
+cudaError_t run_rows(int rows, const Cache& c, const CUtensorMap& km, const CUtensorMap& vm, const Args& a, cudaStream_t st) {
+    if (rows <= 16) return run<Shape<DB, 16, SHARED>>(c, km, vm, a, st);
+    if (rows <= 32) return run<Shape<DB, 32, SHARED>>(c, km, vm, a, st);
+    return run<Shape<DB, 64, SHARED>>(c, km, vm, a, st);
+}
+
+template <int DB, int RT, bool SHARED>
+cudaError_t set_one() {
+    using S = Shape<DB, RT, SHARED>;
+    return cudaFuncSetAttribute(attend_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<S>());
+}
+template <int DB, bool SHARED>
+cudaError_t set_rows() {
+    cudaError_t e = set_one<DB, 16, SHARED>();
+    if (e == cudaSuccess) e = set_one<DB, 32, SHARED>();
+    if (e == cudaSuccess) e = set_one<DB, 64, SHARED>();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t set_attend_attrs() {
+    cudaError_t e = set_rows<1, false>();
+    if (e == cudaSuccess) e = set_rows<1, true>();
+    if (e == cudaSuccess) e = set_rows<2, false>();
+    if (e == cudaSuccess) e = set_rows<2, true>();
+    if (e == cudaSuccess) e = set_rows<4, false>();
+    if (e == cudaSuccess) e = set_rows<4, true>();
+    return e;
+}
+
+void attend_scratch(int sm_count, int head_dim, size_t* o_floats, size_t* ml_floats, size_t* meta) {
+    const size_t grid = (size_t)sm_count * (head_dim == 128 ? 2 : 1);
+    *o_floats = grid * 2 * 64 * head_dim;
+    *ml_floats = grid * 4 * 64;
+    *meta = grid;
+}
+
+cudaError_t launch_attend(const Cache& c, const kv8_pool& pool, const int32_t* table, const int32_t* len,
+                          const int32_t* cu, int n_req, const uint16_t* q, long long q_row, int n_rows, int n_heads,
+                          float scale, int window, uint16_t* out, long long out_row, cudaStream_t st) {
+    CUtensorMap km, vm;
+    const bool shared = c.cfg.shared_kv;
+    if (!encode_codes(&km, c, pool.k_codes) || !encode_codes(&vm, c, shared ? pool.k_codes : pool.v_codes))
+        return cudaErrorNotSupported;
+    Args a{};
+    a.q = q;
+    a.out = out;
+    a.q_row = q_row;
+    a.out_row = out_row;
+    a.cu = cu;
+    a.len = len;
+    a.table = table;
+    a.ks = pool.k_scale;
+    a.vs = shared ? pool.k_scale : pool.v_scale;
+    a.part_o = c.d_part_o;
+    a.part_ml = c.d_part_ml;
+    a.meta = c.d_meta;
+    a.err = c.d_err;
+    a.n_req = n_req;
+    a.n_rows = n_rows;
+    a.heads = n_heads;
+    a.kv_heads = c.cfg.n_kv_heads;
+    a.group = n_heads / c.cfg.n_kv_heads;
+    a.bs_log2 = c.bs_log2;
+    a.n_blocks = c.cfg.n_blocks;
+    a.max_blocks = c.cfg.max_blocks;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.window = window;
+    // rows of an average request's KV head, in the smallest row tile that holds them
+    const long long rows = (long long)a.group * ((n_rows + n_req - 1) / n_req);
+    const int rt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    switch (c.d_blocks * 2 + shared) {
+        case 2: return run_rows<1, false>(rt, c, km, vm, a, st);
+        case 3: return run_rows<1, true>(rt, c, km, vm, a, st);
+        case 4: return run_rows<2, false>(rt, c, km, vm, a, st);
+        case 5: return run_rows<2, true>(rt, c, km, vm, a, st);
+        case 8: return run_rows<4, false>(rt, c, km, vm, a, st);
+        case 9: return run_rows<4, true>(rt, c, km, vm, a, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace kv8
+}  // namespace srh

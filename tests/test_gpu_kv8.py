@@ -1,0 +1,735 @@
+"""The paged 8-bit cache (kv8_*) against plain 64-bit implementations: block
+tables and slots, norm + rotation, quantised append, attention, and a serving
+loop of all four."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+FP8 = torch.float8_e4m3fn
+NAN_CODE = 0x7F
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+def _abi():
+    from sparse_retrieval_host_gb300 import abi
+    return abi
+
+
+def _paged(**kw):
+    from sparse_retrieval_host_gb300.paged import PagedKV8
+    return PagedKV8(**kw)
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _bf16(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+
+# ---------------------------------------------------------------------------------------------- resize
+class ResizeOracle:
+    """The free stack and the tables in plain Python."""
+
+    def __init__(self, batch, bs, n_blocks):
+        self.bs, self.free = bs, list(range(n_blocks - 1, -1, -1))
+        self.len, self.table = [0] * batch, [[] for _ in range(batch)]
+
+    def resize(self, new):
+        bs = self.bs
+        gone = []
+        for b, n in enumerate(new):
+            need = -(-n // bs)
+            gone += self.table[b][need:]
+            self.table[b] = self.table[b][:need]
+        self.free += gone[::-1]
+        cu, pos, slot = [0], [], []
+        for b, n in enumerate(new):
+            while len(self.table[b]) < -(-n // bs):
+                self.table[b].append(self.free.pop())
+            for p in range(self.len[b], n):
+                pos.append(p)
+                slot.append(self.table[b][p // bs] * bs + p % bs)
+            self.len[b] = n
+            cu.append(len(pos))
+        return cu, pos, slot
+
+
+def _same_tables(c, o, n):
+    assert c.len[:n].tolist() == o.len[:n]
+    table = c.table.tolist()
+    for b in range(n):
+        assert table[b] == o.table[b] + [-1] * (c.max_blocks - len(o.table[b])), b
+    assert int(c.n_free) == len(o.free)
+    assert c.free[:len(o.free)].tolist() == o.free
+
+
+@pytest.mark.parametrize("batch,bs,most,steps", [(1, 16, 40, 8), (7, 16, 300, 12), (33, 64, 700, 8), (1500, 32, 70, 4),
+                                                 (4096, 16, 33, 3), (3, 128, 9000, 4)])
+def test_resize_follows_the_oracle(batch, bs, most, steps):
+    rng = np.random.default_rng(batch * 131 + bs)
+    max_blocks = -(-most // bs)
+    n_blocks = batch * max_blocks
+    c = _paged(batch=batch, n_kv_heads=1, head_dim=128, block_tokens=bs, n_blocks=n_blocks, max_blocks=max_blocks)
+    o = ResizeOracle(batch, bs, n_blocks)
+    for step in range(steps):
+        new = rng.integers(0, most + 1, batch)
+        if step % 3 == 1:       # a decode step: one token more where there is room
+            new = np.minimum(np.array(o.len) + 1, most)
+        if step % 3 == 2:       # some requests end
+            new[rng.random(batch) < 0.5] = 0
+        room = int(np.maximum(new - np.array(o.len), 0).sum())
+        extra = int(rng.integers(0, 3))
+        cu, pos, slot = (torch.full((k,), -7, dtype=t, device="cuda") for k, t in
+                         ((batch + 1, torch.int32), (room + extra, torch.int32), (room + extra, torch.int64)))
+        c.resize(_i32(new.tolist()), room + extra, out=(cu, pos, slot))
+        want = o.resize(new.tolist())
+        assert cu.tolist() == want[0]
+        if room + extra:
+            assert pos.tolist() == want[1] + [-7] * extra and slot.tolist() == want[2] + [-7] * extra
+        _same_tables(c, o, batch)
+        assert c.check_error() == 0
+    c.close()
+
+
+def test_resize_shrinks_back_exactly_and_reuses_in_order():
+    c = _paged(batch=3, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=32, max_blocks=10)
+    c.resize(_i32([20, 0, 40]), 60)
+    table, free = c.table.clone(), c.free[:int(c.n_free)].clone()
+    c.resize(_i32([100, 33, 41]), 200)
+    c.resize(_i32([20, 0, 40]))
+    assert torch.equal(c.table, table) and torch.equal(c.free[:int(c.n_free)], free)
+    assert c.check_error() == 0
+    c.close()
+
+
+def test_resize_only_some_requests_leaves_the_others():
+    c = _paged(batch=4, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=32, max_blocks=8)
+    c.resize(_i32([17, 5, 90, 16]), 128)
+    before, lens = c.table.clone(), c.len.clone()
+    c.resize(_i32([40, 2]), 23)
+    assert torch.equal(c.table[2:], before[2:]) and torch.equal(c.len[2:], lens[2:])
+    assert c.len.tolist() == [40, 2, 90, 16]
+    c.close()
+
+
+@pytest.mark.parametrize("why", ["blocks", "cap", "negative", "long", "bad_len", "bad_entry", "depth"])
+def test_resize_refuses_whole_calls(why):
+    abi = _abi()
+    c = _paged(batch=3, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=8, max_blocks=6)
+    c.resize(_i32([30, 10, 0]), 40)
+    new, cap, code = [40, 10, 20], 64, abi.SRH_ERR_BOUNDS
+    if why == "blocks":
+        new, cap, code = [90, 60, 10], 200, abi.SRH_ERR_NOMEM
+    elif why == "cap":
+        cap = 29
+    elif why == "negative":
+        new = [40, -1, 20]
+    elif why == "long":
+        new = [97, 10, 20]
+    elif why == "bad_len":
+        c.len[1] = -5
+    elif why == "bad_entry":
+        new = [30, 0, 0]
+        c.table[1, 0] = 99
+    elif why == "depth":
+        c.n_free.fill_(9)
+    table, lens, free, n_free = c.table.clone(), c.len.clone(), c.free.clone(), c.n_free.clone()
+    cu, pos, slot = c.resize(_i32(new), cap, out=(_i32([5] * 4), _i32([-7] * cap), torch.full((cap,), -7, device="cuda")))
+    assert cu.tolist() == [0] * 4 and (pos == -7).all() and (slot == -7).all()
+    assert torch.equal(c.table, table) and torch.equal(c.len, lens) and torch.equal(c.free, free)
+    assert torch.equal(c.n_free, n_free)
+    assert c.check_error() == code and c.check_error() == abi.SRH_OK
+    c.close()
+
+
+# ---------------------------------------------------------------------------------------------- norm + rotation
+def _norm_oracle(x, w, pos, freq, rot, off, style, eps):
+    """(value, bound on what the norm and rotation may be off before rounding)."""
+    x = x.double()
+    y = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+    if w is not None:
+        y = y * w.double()
+    mag = y.abs()
+    if rot:
+        ang = pos.double()[:, None] * freq[None]
+        cos, sin = torch.cos(ang)[:, None], torch.sin(ang)[:, None]
+        i = torch.arange(rot // 2, device=x.device)
+        a, b = (off + 2 * i, off + 2 * i + 1) if style == "pairs" else (off + i, off + rot // 2 + i)
+        out, m = y.clone(), mag.clone()
+        out[..., a] = y[..., a] * cos - y[..., b] * sin
+        out[..., b] = y[..., a] * sin + y[..., b] * cos
+        m[..., a] = m[..., b] = mag[..., a] + mag[..., b]
+        y, mag = out, m
+    return y, mag
+
+
+def _norm_tol(y, mag, d):
+    # bf16 output 2^-8; fp32 before it: a sum of d squares in a tree and a chain of 8 (relative (8 + 10) 2^-24 in the
+    # sum, half of it in its root), rsqrt 2 ulp, three products, cos and sin within 2^-22 (their argument is a
+    # fraction rounded to 2^-24), two products and a sum: under 40 * 2^-24 of the magnitudes
+    return 2.0 ** -8 * y.abs() + 2.0 ** -18 * mag
+
+
+@pytest.mark.parametrize("style", ["pairs", "halves"])
+@pytest.mark.parametrize("T,H,Hk,D,rot,off", [(1, 1, 1, 128, 128, 0), (5, 64, 1, 512, 64, 448), (3, 24, 1, 128, 64, 64),
+                                              (257, 32, 8, 128, 128, 0), (31, 7, 3, 96, 32, 8), (64, 12, 2, 64, 64, 0),
+                                              (700, 5, 1, 256, 256, 0), (2, 3, 2, 80, 80, 0), (9, 2, 1, 8, 0, 0),
+                                              (4, 600, 2, 64, 16, 40)])
+def test_norm_rope(style, T, H, Hk, D, rot, off):
+    g = _gen(T * 7 + D + rot)
+    c = _paged(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=1, max_blocks=1)
+    row = torch.randn((T, (H + 2 * Hk) * D), generator=g, device="cuda") * torch.exp(
+        3 * torch.randn((T, 1), generator=g, device="cuda"))
+    row = row.bfloat16()
+    q, k = row[:, :H * D].view(T, H, D), row[:, H * D:(H + Hk) * D].view(T, Hk, D)
+    kept = row.clone()
+    w = 1 + 0.3 * torch.randn(D, generator=g, device="cuda")
+    pos = torch.randint(-1000, 1 << 20, (T,), generator=g, device="cuda", dtype=torch.int32)
+    pos[0] = 0
+    freq = 500000.0 ** (-torch.arange(0, max(rot, 2), 2, device="cuda", dtype=torch.float64) / max(rot, 1))[:rot // 2]
+    oq, ok = c.norm_rope(q, k, pos=pos, inv_freq=freq, rot_dim=rot, rot_off=off, style=style, eps=1e-5, q_weight=w)
+    for got, x, ww in ((oq, q, w), (ok, k, None)):
+        y, mag = _norm_oracle(x, ww, pos, freq, rot, off, style, 1e-5)
+        assert ((got.double() - y).abs() <= _norm_tol(y, mag, D)).all()
+    assert torch.equal(row, kept) and c.check_error() == 0
+    # in place, on a strided row, the same bits
+    c.norm_rope(q, None, pos=pos, inv_freq=freq, rot_dim=rot, rot_off=off, style=style, eps=1e-5, q_weight=w, q_out=q)
+    assert torch.equal(q, oq) and torch.equal(row[:, H * D:], kept[:, H * D:])
+    c.close()
+
+
+def test_norm_rope_writes_rows_to_slots():
+    abi = _abi()
+    g = _gen(3)
+    c = _paged(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=1, max_blocks=1)
+    k = _bf16(g, 6, 2, 128)
+    pos, freq = _i32([5, 1, 2, 3, 9, 4]), torch.rand(32, generator=g, device="cuda", dtype=torch.float64)
+    kw = dict(pos=pos, inv_freq=freq, rot_dim=64, style="halves")
+    _, plain = c.norm_rope(None, k, **kw)
+    out = torch.full((8, 2, 128), 3.0, device="cuda").bfloat16()
+    slot = torch.tensor([7, 0, -1, 3, -(1 << 40), 2], device="cuda")
+    c.norm_rope(None, k, k_out=out, k_slot=slot, **kw)
+    want = torch.full_like(out, 3.0)
+    for t, s in enumerate(slot.tolist()):
+        if s >= 0:
+            want[s] = plain[t]
+    assert torch.equal(out, want) and c.check_error() == abi.SRH_OK
+    slot[1], slot[0] = 8, 1 << 40          # past the end: left out and reported
+    out.fill_(3.0)
+    c.norm_rope(None, k, k_out=out, k_slot=slot, **kw)
+    assert (out[[0, 1, 4, 5, 6, 7]] == 3).all() and torch.equal(out[3], plain[3])
+    assert c.check_error() == abi.SRH_ERR_BOUNDS
+    c.close()
+
+
+# ---------------------------------------------------------------------------------------------- append
+def _e4m3(v):
+    m, e = torch.frexp(v)
+    # 2^k from its bits: pow on the GPU is not exact at whole exponents
+    step = ((((e - 1).clamp(min=-6) - 3).long() + 1023) << 52).view(torch.float64)
+    return torch.round(v / step) * step
+
+
+class AppendOracle:
+    """Values (codes) and scales of a pool, block by block."""
+
+    def __init__(self, codes, scale):
+        self.code, self.scale = codes.view(FP8).double().clone(), scale.double().clone()
+
+    def append(self, rows, first, n, table, bs):
+        """rows [n, Hk, D] fp64 to positions first .. of the request with blocks `table`."""
+        at = 0
+        while at < n:
+            p = first + at
+            blk, o = table[p // bs], p % bs
+            m = min(bs - o, n - at)
+            x = rows[at:at + m].transpose(0, 1)
+            amax = x.abs().amax((1, 2))
+            want = torch.full_like(amax, 2.0 ** -64)
+            for h in range(amax.numel()):
+                a = float(amax[h])
+                e = -64
+                while e < 64 and a > 448 * 2.0 ** e:
+                    e += 1
+                want[h] = 2.0 ** e
+            if o:
+                new = torch.maximum(want, self.scale[blk])
+                f = (self.scale[blk] / new)[:, None, None]
+                self.code[blk, :, :o] = _e4m3(self.code[blk, :, :o] * f)
+                want = new
+            self.scale[blk] = want
+            self.code[blk, :, o:o + m] = _e4m3((x / want[:, None, None]).clamp(-448, 448))
+            at += m
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("B,Hk,D,bs,counts", [
+    (1, 1, 128, 16, [[1], [1], [15], [2], [40]]),
+    (3, 2, 256, 32, [[5, 0, 70], [1, 1, 1], [27, 31, 0], [1, 1, 1], [1, 64, 33]]),
+    (5, 1, 512, 64, [[64, 63, 65, 1, 0], [1, 1, 1, 1, 1], [1, 0, 130, 2, 200]]),
+    (40, 4, 128, 16, [[3] * 40, [1] * 40, [1] * 40, [17] * 40]),
+    (2, 8, 128, 128, [[300, 1], [129, 500]]),
+])
+def test_append(shared, B, Hk, D, bs, counts):
+    g = _gen(B + D + bs)
+    longest = max(sum(c[b] for c in counts) for b in range(B))
+    mb = -(-longest // bs)
+    c = _paged(batch=B, n_kv_heads=Hk, head_dim=D, block_tokens=bs, n_blocks=B * mb + 2, max_blocks=mb, shared_kv=shared)
+    for t in [c.k_codes[0], c.v_codes[0]]:
+        t.fill_(NAN_CODE)
+    for t in [c.k_scale[0], c.v_scale[0]]:
+        t.fill_(float("nan"))
+    ora = {p: AppendOracle(torch.zeros_like(t[0]), torch.ones_like(s[0]))
+           for p, t, s in (("k", c.k_codes, c.k_scale), ("v", c.v_codes, c.v_scale))}
+    ln = [0] * B
+    written = torch.zeros((B * mb + 2, bs), dtype=torch.bool)
+    for step, n in enumerate(counts):
+        T = sum(n)
+        first = list(ln)
+        ln = [a + b for a, b in zip(ln, n)]
+        cu, _, _ = c.resize(_i32(ln), T)
+        # rows of growing size, so that begun blocks' scales grow; a padding row behind
+        big = torch.exp(2 * torch.randn((T + 2, 1, 1), generator=g, device="cuda") + 2 * step)
+        wide = (torch.randn((T + 2, 2 * Hk * D), generator=g, device="cuda").view(T + 2, 2, Hk * D) * big).bfloat16()
+        k, v = wide[:, 0].view(T + 2, Hk, D), wide[:, 1].view(T + 2, Hk, D)
+        k[T:] = float("nan")
+        c.append(k, None if shared else v, cu)
+        table, at = c.table.tolist(), 0
+        for b in range(B):
+            for p, x in (("k", k), ("v", v)):
+                if p == "k" or not shared:
+                    ora[p].append(x[at:at + n[b]].double(), first[b], n[b], table[b], bs)
+            at += n[b]
+            for q in range(first[b], ln[b]):
+                written[table[b][q // bs], q % bs] = True
+        for p, codes, scale in (("k", c.k_codes[0], c.k_scale[0]), ("v", c.v_codes[0], c.v_scale[0])):
+            if p == "v" and shared:
+                continue
+            got = codes.view(FP8).double()
+            m = written.cuda()[:, None, :, None].expand_as(got)
+            used = written.any(1).cuda()
+            # exact: dividing by a power of two rounds nothing, e4m3 rounds to nearest even
+            assert torch.equal(scale.double()[used], ora[p].scale[used]), (step, p)
+            assert torch.equal(got[m], ora[p].code[m]), (step, p)
+            assert (codes[~m] == NAN_CODE).all() and torch.isnan(scale[~used]).all()
+    assert c.check_error() == 0
+    c.close()
+
+
+def test_append_again_changes_nothing():
+    g = _gen(5)
+    c = _paged(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=20, max_blocks=8)
+    cu, _, _ = c.resize(_i32([20, 9]), 29)
+    c.append(_bf16(g, 29, 2, 128), _bf16(g, 29, 2, 128), cu)
+    cu, _, _ = c.resize(_i32([50, 12]), 33)
+    k, v = _bf16(g, 33, 2, 128) * 9, _bf16(g, 33, 2, 128)
+    c.append(k, v, cu)
+    held = [t.clone() for t in (c.k_codes[0], c.k_scale[0], c.v_codes[0], c.v_scale[0])]
+    c.append(k, v, cu)
+    assert all(torch.equal(a, b) for a, b in zip(held, (c.k_codes[0], c.k_scale[0], c.v_codes[0], c.v_scale[0])))
+    c.close()
+
+
+def test_append_extremes_and_reports():
+    abi = _abi()
+    c = _paged(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=2, max_blocks=2, shared_kv=True)
+    cu, _, _ = c.resize(_i32([3]), 3)
+    x = torch.zeros((3, 1, 128), device="cuda").bfloat16()
+    c.append(x, None, cu)                                   # all zero: the smallest scale, zero codes
+    assert float(c.k_scale[0][c.table[0, 0], 0]) == 2.0 ** -64 and c.check_error() == 0
+    x[0, 0, :4] = torch.tensor([448.0, -449.0, 2.0 ** -9, 1e-30])
+    c.append(x, None, cu)
+    blk = int(c.table[0, 0])
+    # bf16's step between 256 and 512 is 2, and 449 is a tie: 448 = 224 * 2 is the even side, so 448 * 1 still holds it
+    assert float(c.k_scale[0][blk, 0]) == 1.0
+    assert c.k_codes[0].view(FP8)[blk, 0, 0, :4].float().tolist() == [448.0, -448.0, 2.0 ** -9, 0.0]
+    x[0, 0, 1] = -450.0                                     # the next value does not fit
+    c.append(x, None, cu)
+    assert float(c.k_scale[0][blk, 0]) == 2.0
+    assert c.k_codes[0].view(FP8)[blk, 0, 0, :4].float().tolist() == [224.0, -224.0, 0.0, 0.0]
+    x.zero_()
+    x[0, 0, 0], x[1, 0, 1], x[2, 0, 2] = float("inf"), float("nan"), 1.0
+    c.append(x, None, cu)
+    got = c.k_codes[0].view(FP8)[blk, 0, :3, :3].float() * c.k_scale[0][blk, 0]
+    assert got.tolist() == [[0, 0, 0], [0, 0, 0], [0, 0, 1]]
+    assert c.check_error() == abi.SRH_ERR_RANGE
+    x[0, 0, 0] = 3e38
+    c.append(x, None, cu)
+    assert float(c.k_scale[0][blk, 0]) == 2.0 ** 64 and float(c.k_codes[0].view(FP8)[blk, 0, 0, 0]) == 448.0
+    assert c.check_error() == abi.SRH_ERR_RANGE
+    c.close()
+
+
+def test_append_leaves_out_what_is_out_of_bounds():
+    abi = _abi()
+    g = _gen(8)
+    c = _paged(batch=3, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=9, max_blocks=3, shared_kv=True)
+    cu, _, _ = c.resize(_i32([20, 20, 20]), 60)
+    k = _bf16(g, 60, 1, 128)
+    for spoil in ("table", "len", "cu"):
+        c.k_codes[0].zero_()
+        table, ln, cu2 = c.table.clone(), c.len.clone(), cu.clone()
+        if spoil == "table":
+            c.table[1] = _i32([9, -1, 5])
+        elif spoil == "len":
+            c.len[1] = 49
+        else:
+            cu2[2] = 61
+        c.append(k, None, cu2)
+        assert c.check_error() == abi.SRH_ERR_BOUNDS
+        c.table.copy_(table)
+        c.len.copy_(ln)
+        touched = (c.k_codes[0].view(9, -1) != 0).any(1)
+        for b in ((0, 2) if spoil != "cu" else (0,)):
+            assert touched[c.table[b, :2].long()].all()
+        assert not touched[c.table[1, :2].long()].any()
+    c.close()
+
+
+# ---------------------------------------------------------------------------------------------- attention
+def _filled(lens, Hk, D, bs, shared, seed, gap=0, spread=2, pow2=True):
+    """A cache whose requests hold random codes; everything else is NaN codes and NaN scales."""
+    g = _gen(seed)
+    need = [-(-n // bs) for n in lens]
+    total = sum(need) + 3
+    order = torch.randperm(total, generator=g, device="cuda").tolist()
+    mb = max(need + [1]) + 1
+    buf, flat = {}, Hk * bs * D
+    # gap: K and V of a block side by side with room between
+    both = torch.full((total, 2, flat + gap), NAN_CODE, dtype=torch.uint8, device="cuda")
+    for i, p in enumerate("kv"):
+        if p == "v" and shared:
+            continue
+        buf[p + "_codes"] = both[:, i, :flat].view(total, Hk, bs, D)
+        buf[p + "_scale"] = torch.full((total, Hk), float("nan"), device="cuda")
+    c = _paged(batch=len(lens), n_kv_heads=Hk, head_dim=D, block_tokens=bs, n_blocks=total, max_blocks=mb, shared_kv=shared,
+               buffers=buf)
+    c.len.copy_(_i32(lens))
+    at = 0
+    for b, n in enumerate(lens):
+        ids = order[at:at + need[b]]
+        at += need[b]
+        if not ids:
+            continue
+        c.table[b, :need[b]] = _i32(ids)
+        for p in "k" if shared else "kv":
+            codes, scale = buf[p + "_codes"], buf[p + "_scale"]
+            x = torch.randn((need[b], Hk, bs, D), generator=g, device="cuda") * 60
+            y = x.clamp(-448, 448).to(FP8).view(torch.uint8)
+            t = torch.arange(need[b] * bs, device="cuda").view(need[b], 1, bs, 1) < n
+            codes[ids] = torch.where(t, y, torch.full_like(y, NAN_CODE))
+            e = torch.randint(-spread, spread + 1, (need[b], Hk), generator=g, device="cuda").float()
+            s = torch.exp2(e - 6)
+            scale[ids] = s if pow2 else s * (1 + torch.rand(s.shape, generator=g, device="cuda"))
+    return c, g
+
+
+def _check_attend(c, q, cu, out, scale, window):
+    """Every value within what the number formats allow.
+
+    Weights are rounded to two e4m3 terms: relative 2^-4 * 2^-4 (and 2^-11 on the way, in fp16), or, for small ones, half of
+    the smallest step 2^-9 where the row's largest weight is at least 2^6 (the reference lies 2^6 below a maximum and moves
+    when one passes 2^8): 2^-16 of the largest w * vs per code. Queries are two e4m3 terms: exact, or 2^-17 of the row's
+    largest times the sum of |K|; scores are fp32 sums of D products and a few fp32 steps on values up to |s|:
+    (D + 8) 2^-24 of sum |q K| covers them. Weight errors reach the output through sum w |V| / l. bf16 output: 2^-8."""
+    D, Hk, bs = c.D, c.Hk, c.bs
+    H = q.shape[1]
+    G = H // Hk
+    cul, ln = cu.tolist(), c.len.tolist()
+    for b in range(len(cul) - 1):
+        nq, n = cul[b + 1] - cul[b], ln[b]
+        if nq == 0:
+            continue
+        got = out[cul[b]:cul[b + 1]].double()
+        y = q[cul[b]:cul[b + 1]].double().view(nq, Hk, G, D).permute(1, 2, 0, 3)
+        if n == 0:
+            assert (got == 0).all()
+            continue
+        ids = c.table[b, :-(-n // bs)].long()
+        kc, vc = (t[0][ids].view(FP8).double().permute(1, 0, 2, 3).reshape(Hk, -1, D)[:, :n] for t in (c.k_codes, c.v_codes))
+        ks, vs = (t[0][ids].double().t().repeat_interleave(bs, 1)[:, :n] for t in (c.k_scale, c.v_scale))
+        k, v = kc * ks[..., None], vc * vs[..., None]
+        s = torch.einsum("hgid,htd->hgit", y, k) * scale
+        s_abs = torch.einsum("hgid,htd->hgit", y.abs(), k.abs()) * abs(scale)
+        k_sum = k.abs().sum(-1)[:, None, None, :] * abs(scale)
+        pos = torch.arange(n - nq, n, device="cuda")[:, None]
+        t = torch.arange(n, device="cuda")[None]
+        see = (t <= pos) & ((t > pos - window) if window else torch.ones_like(t, dtype=torch.bool))
+        s = s.masked_fill(~see, float("-inf"))
+        m = s.amax(-1, keepdim=True)
+        w = torch.exp(s - torch.where(m == float("-inf"), 0.0, m))
+        l = w.sum(-1, keepdim=True)
+        ok = l > 0
+        w = torch.where(ok, w / l, 0.0)
+        want = torch.einsum("hgit,htd->hgid", w, v)
+        eps_s = (D + 8) * 2.0 ** -24 * s_abs + 2.0 ** -17 * y.abs().amax(-1)[..., None] * k_sum
+        rel = 2.0 ** -8 + 2.0 ** -11 + 2 * (eps_s * see).amax(-1, keepdim=True)
+        contrib = (w * vs[:, None, None, :]).amax(-1, keepdim=True)
+        tol = rel * torch.einsum("hgit,htd->hgid", w, v.abs())
+        tol += 2.0 ** -16 * contrib * torch.einsum("hgit,htd->hgid", see.double().expand_as(w), vc.abs())
+        tol += 2.0 ** -8 * want.abs()
+        want, tol = (z.permute(2, 0, 1, 3).reshape(nq, H, D) for z in (want, tol))
+        bad = ~((got - want).abs() <= tol)
+        assert not bad.any(), (b, int(bad.sum()), float((got - want).abs().max()), float(want.abs().max()))
+
+
+def _attend(lens, nq, H, Hk, D, bs, shared, window=0, seed=0, pad=0, scale=None, **kw):
+    c, g = _filled(lens, Hk, D, bs, shared, seed, **kw)
+    cu = _i32(np.concatenate([[0], np.cumsum(nq)]).tolist())
+    T = sum(nq) + pad
+    q = torch.randn((T, H, D), generator=g, device="cuda")
+    q = (q * torch.exp(torch.randn((T, H, 1), generator=g, device="cuda"))).bfloat16()
+    out = torch.full((T, H, D), 7.0, device="cuda").bfloat16()
+    scale = D ** -0.5 / 4 if scale is None else scale
+    c.attend(q, cu, scale=scale, window=window, out=out)
+    assert c.check_error() == 0
+    _check_attend(c, q, cu, out, scale, window)
+    assert (out[sum(nq):] == 7).all()
+    c.close()
+
+
+@pytest.mark.parametrize("D,shared", [(128, False), (128, True), (256, False), (256, True), (512, True), (512, False)])
+@pytest.mark.parametrize("G", [1, 16, 17, 40])
+def test_attend_one_tile(D, shared, G):
+    _attend([100], [1], G, 1, D, 16, shared, seed=D + G)
+
+
+@pytest.mark.parametrize("D,shared", [(128, False), (256, False), (512, True), (128, True), (512, False)])
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+def test_attend_decode_lengths(D, shared, bs):
+    lens = [1, 2, 15, 16, 17, 127, 128, 129, 255, 0, 1000, 3001, bs, bs + 1, 640]
+    _attend(lens, [1] * len(lens), 8, 2, D, bs, shared, seed=bs + D, pad=2)
+
+
+@pytest.mark.parametrize("H,Hk,D,shared,bs", [(8, 1, 128, False, 16), (6, 2, 128, False, 32), (64, 1, 512, True, 64),
+                                              (16, 4, 256, False, 128), (65, 1, 128, True, 16), (5, 5, 256, True, 64),
+                                              (128, 1, 512, True, 64), (64, 2, 512, False, 32)])
+def test_attend_several_queries(H, Hk, D, shared, bs):
+    lens = [1, 40, 128, 130, 300, 1111, 7, 64, 513]
+    nq = [1, 4, 128, 5, 0, 3, 7, 2, 130]
+    _attend(lens, nq, H, Hk, D, bs, shared, seed=H, pad=1)
+
+
+@pytest.mark.parametrize("window", [1, 2, 100, 128, 129, 1000])
+@pytest.mark.parametrize("D,shared,q", [(128, False, 1), (128, False, 150), (512, True, 3), (256, True, 40)])
+def test_attend_window(window, D, shared, q):
+    lens = [q, q + 1, 128 + q, 700, 2049 + q]
+    _attend(lens, [min(q, n) for n in lens], 8, 2, D, 32, shared, window=window, seed=window)
+
+
+@pytest.mark.parametrize("D,shared", [(128, False), (512, True)])
+def test_attend_one_long_request_is_split_and_joined(D, shared):
+    _attend([50001], [1], 16, 1, D, 64, shared, seed=1)
+    _attend([9000, 1, 0, 20000], [2, 1, 1, 5], 8, 1, D, 64, shared, seed=2)
+
+
+def test_attend_rows_before_the_request_see_nothing():
+    # more queries than tokens: the first rows lie before the request
+    _attend([3, 0, 129], [5, 2, 140], 8, 2, 128, 16, False, seed=4)
+    _attend([3, 0, 129], [5, 2, 140], 64, 1, 512, 16, True, seed=4, window=7)
+
+
+@pytest.mark.parametrize("D,shared", [(128, False), (256, False), (512, True)])
+def test_attend_scales_far_apart_and_strided_blocks(D, shared):
+    # scales are not powers of two here, and blocks' contributions differ by up to 2^40
+    _attend([700, 33, 1500], [1, 2, 3], 8, 2, D, 32, shared, seed=9, spread=20, pow2=False, gap=48,
+            scale=2.0 ** -14)
+
+
+@pytest.mark.parametrize("D,shared", [(128, False), (512, True)])
+def test_attend_peaked_and_flat_scores(D, shared):
+    _attend([1000, 300], [1, 4], 16, 2, D, 16, shared, seed=11, scale=2.0)     # one token takes all
+    _attend([1000, 300], [1, 4], 16, 2, D, 16, shared, seed=12, scale=0.0)     # a plain mean
+    _attend([1000, 300], [1, 4], 16, 2, D, 16, shared, seed=13, scale=-0.02)
+
+
+def test_attend_rising_scores_move_the_reference():
+    # keys grow along the request, so every tile raises the maximum
+    c, g = _filled([2000], 1, 128, 16, False, 21, spread=0)
+    ids = c.table[0, :125].long()
+    c.k_codes[0][ids] = torch.full((125, 1, 16, 128), 8.0, device="cuda").to(FP8).view(torch.uint8)
+    c.k_scale[0][ids] = (torch.arange(125, device="cuda").float()[:, None] + 1) / 64
+    q = torch.ones((1, 3, 128), device="cuda").bfloat16() * _i32([1, -1, 3]).bfloat16()[None, :, None]
+    cu = _i32([0, 1])
+    out = c.attend(q, cu, scale=128 ** -0.5)
+    assert c.check_error() == 0
+    _check_attend(c, q, cu, out, 128 ** -0.5, 0)
+    c.close()
+
+
+def test_attend_bad_rows_stay_alone():
+    """Queries that are not finite give NaN in their rows only."""
+    c, g = _filled([300, 200], 2, 128, 16, False, 31)
+    q = _bf16(g, 5, 8, 128)
+    cu = _i32([0, 3, 5])
+    clean = c.attend(q, cu, scale=0.05)
+    q2 = q.clone()
+    q2[1, 2, 5], q2[3, 7, 0] = float("nan"), float("inf")
+    out = c.attend(q2, cu, scale=0.05)
+    assert torch.isnan(out[1, 2]).all() and torch.isnan(out[3, 7]).all()
+    keep = torch.ones((5, 8), dtype=torch.bool, device="cuda")
+    keep[1, 2] = keep[3, 7] = False
+    assert torch.equal(out[keep], clean[keep])
+    c.close()
+
+
+def test_attend_reports_bad_tables_and_lengths():
+    abi = _abi()
+    c, g = _filled([300, 200], 1, 128, 16, True, 41)
+    q, cu = _bf16(g, 2, 4, 128), _i32([0, 1, 2])
+    good = c.attend(q, cu, scale=0.05)
+    table = c.table.clone()
+    c.table[0, 3], c.table[0, 5] = c.n_blocks, -2          # blocks that are not there: read as absent
+    out = c.attend(q, cu, scale=0.05)
+    assert c.check_error() == abi.SRH_ERR_BOUNDS
+    assert torch.isfinite(out).all() and torch.equal(out[1], good[1]) and not torch.equal(out[0], good[0])
+    c.table.copy_(table)
+    c.len[0] = 1 << 30
+    out = c.attend(q, cu, scale=0.05)
+    assert c.check_error() == abi.SRH_ERR_BOUNDS and torch.equal(out[1], good[1])
+    c.len[0] = 300
+    out = c.attend(q, _i32([0, 1, 9]), scale=0.05)
+    assert c.check_error() == abi.SRH_ERR_BOUNDS and torch.equal(out, good)
+    out = torch.full_like(q, 5.0)
+    c.attend(q, _i32([-4, 1, 2]), scale=0.05, out=out)
+    assert c.check_error() == abi.SRH_ERR_BOUNDS and torch.equal(out, good)
+    c.close()
+
+
+def test_attend_repeats_bit_for_bit_on_streams_and_in_graphs():
+    c, g = _filled([5000, 77, 1300], 2, 128, 32, False, 51)
+    q, cu = _bf16(g, 6, 16, 128), _i32([0, 1, 4, 6])
+    want = c.attend(q, cu, scale=0.08)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        assert torch.equal(c.attend(q, cu, scale=0.08), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    a = torch.zeros_like(q)
+    c.attend(q, cu, scale=0.08, out=a, stream=s)
+    s.synchronize()
+    assert torch.equal(a, want)
+    # captured: other lengths and queries, same graph
+    out, graph = torch.zeros_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        c.attend(q, cu, scale=0.08, out=out)
+    for ln in ([5000, 77, 1300], [4999, 12, 640]):
+        c.len.copy_(_i32(ln))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_attend(c, q, cu, out, 0.08, 0)
+    assert c.check_error() == 0
+    c.close()
+
+
+# ---------------------------------------------------------------------------------------------- together
+@pytest.mark.parametrize("H,Hk,D,shared,rot,off,style", [(8, 2, 128, False, 128, 0, "halves"),
+                                                         (64, 1, 512, True, 64, 448, "pairs")])
+def test_a_serving_loop(H, Hk, D, shared, rot, off, style):
+    """Prompts, decode steps with drafted tokens and their rejection, requests that
+    end and start, two layers on one table: the attention agrees with the plain
+    one over the values that the cache should hold."""
+    rng = np.random.default_rng(7)
+    g = _gen(7)
+    B, bs, mb, layers = 5, 32, 24, 2
+    c = _paged(batch=B, n_kv_heads=Hk, head_dim=D, block_tokens=bs, n_blocks=70, max_blocks=mb, shared_kv=shared,
+               layers=layers)
+    freq = 10000.0 ** (-torch.arange(0, rot, 2, device="cuda", dtype=torch.float64) / rot)
+    w = 1 + 0.1 * torch.randn(D, generator=g, device="cuda")
+    ora = [{p: AppendOracle(t[i], s[i]) for p, t, s in (("k", c.k_codes, c.k_scale), ("v", c.v_codes, c.v_scale))}
+           for i in range(layers)]
+    ln = [0] * B
+    for step in range(9):
+        if step == 0:
+            new = [200, 33, 1, 150, 64]
+        elif step % 3 == 2:
+            new = [max(1, n - int(rng.integers(0, 4))) for n in ln]       # drafted tokens rejected
+        else:
+            new = [n + int(rng.integers(1, 5)) for n in ln]
+        if step == 4:
+            new[1] = 0                                                    # a request ends ...
+        if step == 5:
+            new[1] = 300                                                  # ... and another takes its place
+        T = sum(max(0, a - b) for a, b in zip(new, ln))
+        cu, pos, slot = c.resize(_i32(new), T)
+        if not T:
+            ln = new
+            continue
+        qkv = _bf16(g, T, (H + 2 * Hk) * D)
+        q, k = c.norm_rope(qkv[:, :H * D].view(T, H, D), qkv[:, H * D:(H + Hk) * D].view(T, Hk, D), pos=pos, inv_freq=freq,
+                           rot_dim=rot, rot_off=off, style=style, q_weight=w, k_weight=w)
+        want, mag = _norm_oracle(qkv[:, H * D:(H + Hk) * D].view(T, Hk, D), w, pos, freq, rot, off, style, 1e-6)
+        assert ((k.double() - want).abs() <= _norm_tol(want, mag, D)).all()
+        v = qkv[:, (H + Hk) * D:].view(T, Hk, D)
+        cul, table = cu.tolist(), c.table.tolist()
+        for layer in range(layers):
+            kk, vv = (k, v) if layer == 0 else (-k, v * 2)
+            c.append(kk, None if shared else vv, cu, layer=layer)
+            out = c.attend(q, cu, scale=D ** -0.5, layer=layer)
+            for b in range(B):
+                n = cul[b + 1] - cul[b]
+                for p, x in (("k", kk), ("v", vv)):
+                    if p == "k" or not shared:
+                        ora[layer][p].append(x[cul[b]:cul[b + 1]].double(), new[b] - n, n, table[b], bs)
+            for p, codes, scale in (("k", c.k_codes, c.k_scale), ("v", c.v_codes, c.v_scale)):
+                if p == "v" and shared:
+                    continue
+                for b in range(B):
+                    for j in range(-(-new[b] // bs)):
+                        m = min(bs, new[b] - j * bs)
+                        assert torch.equal(scale[layer][table[b][j]].double(), ora[layer][p].scale[table[b][j]])
+                        assert torch.equal(codes[layer][table[b][j]][:, :m].view(FP8).double(),
+                                           ora[layer][p].code[table[b][j]][:, :m])
+            one = type("OneLayer", (), dict(D=D, Hk=Hk, bs=bs, len=c.len, table=c.table,
+                                            k_codes=[c.k_codes[layer]], v_codes=[c.v_codes[layer]],
+                                            k_scale=[c.k_scale[layer]], v_scale=[c.v_scale[layer]]))
+            _check_attend(one, q, cu, out, D ** -0.5, 0)
+        ln = new
+        assert c.check_error() == 0
+    c.close()
+
+
+def test_a_captured_step():
+    """resize, append and attend in one CUDA graph, replayed with new lengths."""
+    g = _gen(77)
+    c = _paged(batch=4, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=80, max_blocks=20)
+    cu, _, _ = c.resize(_i32([100, 3, 40, 250]), 393)
+    c.append(_bf16(g, 393, 2, 128), _bf16(g, 393, 2, 128), cu)
+    new = c.len + 1
+    cu, pos, slot = _i32([0] * 5), _i32([0] * 4), torch.zeros(4, dtype=torch.int64, device="cuda")
+    k, v, q = _bf16(g, 4, 2, 128), _bf16(g, 4, 2, 128), _bf16(g, 4, 8, 128)
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.resize(new, 4, out=(cu, pos, slot))
+        c.append(k, v, cu)
+        c.attend(q, cu, scale=0.09, out=out)
+    for step in range(20):
+        for t in (k, v, q):
+            t.copy_(_bf16(g, *t.shape))
+        new.copy_(c.len + 1)
+        graph.replay()
+        assert pos.tolist() == (new - 1).tolist() and cu.tolist() == [0, 1, 2, 3, 4]
+        _check_attend(c, q, cu, out, 0.09, 0)
+    assert c.len.tolist() == [120, 23, 60, 270] and c.check_error() == 0
+    c.close()
