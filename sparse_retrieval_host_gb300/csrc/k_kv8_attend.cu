@@ -33,10 +33,10 @@
 // An item whose units fall to several CTAs leaves fp32 partial sums, which a
 // second kernel joins in order (no atomics: results repeat bit for bit).
 //
-// Roles (192 threads): warps 0-3 softmax (thread = token; also queries in and
-// outputs out), warp 4 TMA (one box per block of tokens and 128 values, into a
-// ring of tile slots), warp 5 MMA issue. QK of tile j + 1 is issued before PV of
-// tile j. Every wait is bounded; on a timeout the CTA records it, lets its
+// Roles: 4 to 16 softmax warps (a thread holds one token and 16 or 32 rows;
+// they also bring queries in and outputs out), one TMA warp (one box per block
+// of tokens and 128 values, into a ring of tile slots), one MMA warp. QK of tile
+// j + 1 is issued before PV of tile j. Every wait is bounded; on a timeout the CTA records it, lets its
 // copies and MMAs end, frees TMEM and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -52,8 +52,6 @@ namespace {
 using namespace umma;
 
 constexpr int kTile = 128;               // tokens per tile
-constexpr int kThreads = 192;
-constexpr int kSoft = 128;               // softmax threads
 constexpr float kLow = -1e30f;           // reference of a row that has seen no token
 constexpr float kHead = 6.f;             // the reference stays 2^6 below the maximum ...
 constexpr float kRoom = 8.f;             // ... and moves when a weight would pass 2^8
@@ -73,8 +71,13 @@ struct Shape {
     static constexpr int kQBytes = DB * N * 128;
     static constexpr int kPBytes = kTile * N;
     static constexpr int kPitch = CAT ? N : RT;            // bytes of one token's row of p
-    static constexpr int CTAS = DB == 1 ? 2 : 1;           // per SM
-    static constexpr int SLOTS = DB == 1 ? (RT == 64 ? 4 : 5) : DB == 2 ? 4 : RT == 16 ? 3 : 2;
+    static constexpr int CTAS = DB == 1 || (DB == 2 && RT == 16) ? 2 : 1;   // per SM
+    static constexpr int SLOTS = DB == 1 ? (RT == 64 ? 4 : 5) : DB == 2 ? (RT == 16 ? 3 : 4) : RT == 16 ? 3 : 2;
+    // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the columns
+    static constexpr int CT = DB == 1 && RT == 64 ? 32 : 16;
+    static constexpr int CG = RT / CT;
+    static constexpr int SOFT = 128 * CG;                  // softmax threads
+    static constexpr int THREADS = SOFT + 64;
     static constexpr int kOffQ = SLOTS * kTileBytes;
     static constexpr int kOffP = kOffQ + kQBytes;
     static constexpr int kOffBars = kOffP + kPBytes;
@@ -185,13 +188,18 @@ struct Walker {
 };
 
 // ---------------------------------------------------------------- small device helpers
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+// Barrier of the softmax threads, and one that tells them all whether any said yes.
+template <int SOFT>
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("bar.sync 1, %0;\n" ::"n"(SOFT) : "memory");
+}
+template <int SOFT>
 __device__ __forceinline__ bool soft_any(bool v) {
     uint32_t r;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "n"(SOFT)
         : "memory");
     return r != 0;
 }
@@ -276,6 +284,11 @@ struct Bars {
     float sum[S::RT];
     int pos[S::RT];                   // position of the row's token; -1: no row
     long long row_at[S::RT];          // its offset in out
+    // the softmax warps' walk, kept here for registers' sake: thread 0 takes the
+    // next segment while the others may still read the last one
+    Walker<S::RT> walk;
+    Segment seg[2];
+    int more[2];
 };
 
 template <typename S>
@@ -283,7 +296,7 @@ constexpr int smem_bytes() {
     return S::kOffBars + (int)sizeof(Bars<S>) + 1024;
 }
 
-// The column sums over a warp of v[RT]: lane i gets column i (and i + 32).
+// The column sums over a warp of v[RT], RT = 16 or 32: lane i writes column i.
 template <int RT>
 __device__ __forceinline__ void column_sums(float (&v)[RT], int lane, float* out) {
     if (RT == 16) {
@@ -308,10 +321,11 @@ __device__ __forceinline__ void column_sums(float (&v)[RT], int lane, float* out
 
 // ---------------------------------------------------------------- the kernel
 template <typename S>
-__global__ void __launch_bounds__(kThreads, S::CTAS)
+__global__ void __launch_bounds__(S::THREADS, S::CTAS)
 attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const __grid_constant__ Args a) {
-    constexpr int DB = S::DB, RT = S::RT, N = S::N;
+    constexpr int DB = S::DB, RT = S::RT, N = S::N, CT = S::CT, SOFT = S::SOFT;
+    constexpr int kWarpTma = SOFT / 32, kWarpMma = kWarpTma + 1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     Bars<S>& bs = *reinterpret_cast<Bars<S>*>(sm + S::kOffBars);
@@ -323,7 +337,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     Walker<RT> w;
     bool bad = false;
     {
-        const int per = (a.n_req + kThreads - 1) / kThreads;
+        const int per = (a.n_req + S::THREADS - 1) / S::THREADS;
         const int b0 = min(a.n_req, tid * per), b1 = min(a.n_req, b0 + per);
         long long mine = 0;
         for (int b = b0; b < b1; ++b) mine += units(a, request<RT>(a, b, &bad));
@@ -358,16 +372,16 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             mbar_init(&bs.full[s], 1);
             mbar_init(&bs.empty[s], 1);
         }
-        mbar_init(&bs.q_full, kSoft);
+        mbar_init(&bs.q_full, SOFT);
         mbar_init(&bs.s_full, 1);
-        mbar_init(&bs.s_free, kSoft);
-        mbar_init(&bs.p_full, kSoft);
+        mbar_init(&bs.s_free, SOFT);
+        mbar_init(&bs.p_full, SOFT);
         mbar_init(&bs.pv_done, 1);
         mbar_init(&bs.drain, 1);
         bs.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc(&bs.tmem_base, S::ALLOC);
+    if (warp == kWarpMma) tmem_alloc(&bs.tmem_base, S::ALLOC);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -379,8 +393,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const uint32_t tm_s = tmem, tm_o = tmem + N;
 
     bool ok = true;
-    Segment sg;
-    if (warp == 4) {
+    Segment sg{};
+    if (warp == kWarpTma) {
         // ======================================================== TMA
         uint32_t it = 0;                                   // tiles requested
         const int bpt = kTile >> a.bs_log2;                // blocks per tile
@@ -414,7 +428,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         if (!ok)   // every copy issued lands before the CTA may leave
             for (uint32_t i = it > S::SLOTS ? it - S::SLOTS : 0; i < it; ++i)
                 mbar_wait(&bs.full[i % S::SLOTS], (i / S::SLOTS) & 1);
-    } else if (warp == 5) {
+    } else if (warp == kWarpMma) {
         // ======================================================== MMA issue
         if (lane == 0) {
             constexpr uint32_t id_qk = idesc_f32acc(0, 0, 0, kTile, N);          // e4m3, both K-major
@@ -485,62 +499,65 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
     } else {
         // ======================================================== softmax
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const uint32_t my_s = tm_s + lane_base, my_o = tm_o + lane_base;
+        const int quad = warp & 3, col0 = (warp >> 2) * CT;    // TMEM lanes of this warp, first column
+        const int tok = quad * 32 + lane;                      // token of the tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t my_s = tm_s + lane_base + col0, my_o = tm_o + lane_base + col0;
         unsigned char* qsm = sm + S::kOffQ;
         unsigned char* psm = sm + S::kOffP;
         uint32_t g = 0, it = 0;                            // token tiles, tiles of the ring
         bool fail = false, ids_bad = false, begun = false;
-        // (ks, log2 vs, 1 / vs) of this thread's token in a tile; a token that is
-        // not there or has no block: (0, -inf, 0)
-        auto scales = [&](int tile, float* ks, float* lv, float* iv) {
-            const int t = tile * kTile + tid;
-            *ks = 0.f;
-            *lv = -INFINITY;
-            *iv = 0.f;
-            if (t >= sg.r.len) return;
-            const int id = a.table[(size_t)sg.b * a.max_blocks + (t >> a.bs_log2)];
-            if (id < 0 || id >= a.n_blocks) {
-                ids_bad = true;
-                return;
+        float l[CT];
+        if (tid == 0) bs.walk = w;
+        for (int turn = 0;; turn ^= 1) {
+            const Segment& sg = bs.seg[turn];
+            if (tid == 0) {
+                const bool more = bs.walk.next(a, &bs.seg[turn]);
+                bs.more[turn] = more;
+                if (more && sg.parts) {
+                    begun = true;
+                    a.meta[cta] = make_int4(sg.b, sg.h, sg.rt, sg.parts);
+                }
             }
-            const size_t at = (size_t)id * a.kv_heads + sg.h;
-            *ks = __ldg(a.ks + at);
-            const float vs = S::SHARED ? *ks : __ldg(a.vs + at);
-            *lv = lg2(vs);
-            *iv = 1.f / vs;
-        };
-        float l[RT];
-        while (w.next(a, &sg)) {
-            if (sg.parts) begun = true;
-            if (sg.parts && tid == 0) a.meta[cta] = make_int4(sg.b, sg.h, sg.rt, sg.parts);
-            soft_sync();                                   // the last segment's shared arrays are read
-            const int p_first = sg.r.len - sg.r.nq;
+            soft_sync<SOFT>();                             // also: the last segment's shared arrays are read
+            if (!bs.more[turn]) break;
+            const int n = sg.n, len = sg.r.len;
+            // the block id of this thread's token in a tile (-1: no token)
+            auto block_of = [&](int j) -> int {
+                const int t = (sg.t0 + j) * kTile + tok;
+                if (j >= n || t >= len) return -1;
+                return __ldg(a.table + (size_t)sg.b * a.max_blocks + (t >> a.bs_log2));
+            };
+            // block ids run two tiles ahead of their use and scales one, so that
+            // neither load is waited for
+            const int id_0 = block_of(0);
+            int id_1 = block_of(1);
+            const int p_first = len - sg.r.nq;
             if (tid < RT) {
-                const int row = sg.row0 + tid, tok = row / a.group, hd = sg.h * a.group + row % a.group;
+                const int row = sg.row0 + tid, qt = row / a.group, hd = sg.h * a.group + row % a.group;
                 const bool on = tid < sg.nr;
-                bs.pos[tid] = on ? p_first + tok : -1;
-                bs.row_at[tid] = (long long)(sg.r.q0 + tok) * a.out_row + (long long)hd * (DB * 128);
+                bs.pos[tid] = on ? p_first + qt : -1;
+                bs.row_at[tid] = (long long)(sg.r.q0 + qt) * a.out_row + (long long)hd * (DB * 128);
                 // a column without a row is held at weight 0 by a reference out of reach
                 bs.ref[tid] = on ? kLow : -kLow;
             }
-            if (sg.n > 0) {
+            if (n > 0) {
                 // queries: a warp per row, 4 values per lane and 128 dims
-                constexpr int U = RT / 4 < 4 ? RT / 4 : 4;
-                for (int r0 = warp; r0 < RT; r0 += 4 * U) {
+                constexpr int W = SOFT / 32, U = RT / W < 4 ? RT / W : 4;
+                for (int r0 = warp; r0 < RT; r0 += W * U) {
                     uint2 x[U][DB];
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
-                        const int r = r0 + 4 * i;
-                        const int row = sg.row0 + r, tok = row / a.group, hd = sg.h * a.group + row % a.group;
-                        const uint16_t* p = a.q + (size_t)(sg.r.q0 + tok) * a.q_row + (size_t)hd * (DB * 128) + lane * 4;
+                        const int r = r0 + W * i;
+                        const int row = sg.row0 + r, qt = row / a.group, hd = sg.h * a.group + row % a.group;
+                        const uint16_t* p = a.q + (size_t)(sg.r.q0 + qt) * a.q_row + (size_t)hd * (DB * 128) + lane * 4;
 #pragma unroll
                         for (int d = 0; d < DB; ++d)
                             x[i][d] = r < sg.nr ? __ldg(reinterpret_cast<const uint2*>(p + d * 128)) : make_uint2(0, 0);
                     }
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
-                        const int r = r0 + 4 * i;
+                        const int r = r0 + W * i;
                         uint32_t m = 0;
 #pragma unroll
                         for (int d = 0; d < DB; ++d)
@@ -567,40 +584,56 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 fence_async_smem();
                 mbar_arrive(&bs.q_full);
             }
-            soft_sync();
+            float ks_raw = 0.f, vs_raw = 0.f;
+            bool has = id_0 >= 0 && id_0 < a.n_blocks;
+            auto load_scales = [&](int id) {
+                if (id < 0 || id >= a.n_blocks) return;
+                const size_t at = (size_t)id * a.kv_heads + sg.h;
+                ks_raw = __ldg(a.ks + at);
+                vs_raw = S::SHARED ? ks_raw : __ldg(a.vs + at);
+            };
+            load_scales(id_0);
+            soft_sync<SOFT>();
 #pragma unroll
-            for (int c = 0; c < RT; ++c) l[c] = 0.f;
+            for (int c = 0; c < CT; ++c) l[c] = 0.f;
             const int win = a.window ? a.window : 1 << 30;
             const int p_lo = bs.pos[0], p_hi = bs.pos[sg.nr - 1];
-            float ks, lv, iv;
-            if (sg.n > 0) scales(sg.t0, &ks, &lv, &iv);
             bool stop = false;
-            for (int j = 0; j < sg.n; ++j, ++g) {
-                const int t0 = (sg.t0 + j) * kTile, t = t0 + tid;
-                float ks_n = 0.f, lv_n = 0.f, iv_n = 0.f;
-                if (j + 1 < sg.n) scales(sg.t0 + j + 1, &ks_n, &lv_n, &iv_n);
+            for (int j = 0; j < n; ++j, ++g) {
+                const int t0 = (sg.t0 + j) * kTile, t = t0 + tok;
+                // this tile's (ks, log2 vs, 1 / vs); (0, -inf, 0) without a token or block
+                float ks = 0.f, lv = -INFINITY, iv = 0.f;
+                if (has) {
+                    ks = ks_raw;
+                    lv = lg2(vs_raw);
+                    iv = __fdividef(1.f, vs_raw);
+                } else if (t < len) {
+                    ids_bad = true;
+                }
+                has = id_1 >= 0 && id_1 < a.n_blocks;
+                load_scales(id_1);
+                id_1 = block_of(j + 2);
                 if (mbar_wait_abort(&bs.s_full, g & 1, abort) <= 0) fail = true;
                 tc_fence_after();
-                float x[RT];
-#pragma unroll
-                for (int c = 0; c < RT; c += 16) {
-                    float hi[16], lo[16];
-                    tmem_ld16(my_s + c, hi);
-                    tmem_ld16(my_s + RT + c, lo);
+                float x[CT];
+                {
+                    float hi[CT], lo[CT];
+                    tmem_ld<CT>(my_s, hi);
+                    tmem_ld<CT>(my_s + RT, lo);
                     tmem_ld_wait();
-                    tmem_regs_ready(hi);
-                    tmem_regs_ready(lo);
+                    tmem_regs_ready_n<CT>(hi);
+                    tmem_regs_ready_n<CT>(lo);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[c + i] = hi[i] + lo[i];
+                    for (int i = 0; i < CT; ++i) x[i] = hi[i] + lo[i];
                 }
                 tc_fence_before();
                 mbar_arrive(&bs.s_free);
                 float most = kLow;
                 const bool edge = t0 + kTile - 1 > p_lo || t0 <= p_hi - win;
 #pragma unroll
-                for (int c = 0; c < RT; c += 4) {
-                    const float4 s4 = *reinterpret_cast<const float4*>(&bs.qs[c]);
-                    const float4 r4 = *reinterpret_cast<const float4*>(&bs.ref[c]);
+                for (int c = 0; c < CT; c += 4) {
+                    const float4 s4 = *reinterpret_cast<const float4*>(&bs.qs[col0 + c]);
+                    const float4 r4 = *reinterpret_cast<const float4*>(&bs.ref[col0 + c]);
                     x[c] = fmaf(x[c] * s4.x, ks, lv);
                     x[c + 1] = fmaf(x[c + 1] * s4.y, ks, lv);
                     x[c + 2] = fmaf(x[c + 2] * s4.z, ks, lv);
@@ -608,52 +641,68 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     if (edge) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int p = bs.pos[c + i];
+                            const int p = bs.pos[col0 + c + i];
                             if (t > p || t <= p - win) x[c + i] = -INFINITY;
                         }
                     }
                     most = fmaxf(most, fmaxf(fmaxf(x[c] - r4.x, x[c + 1] - r4.y), fmaxf(x[c + 2] - r4.z, x[c + 3] - r4.w)));
                 }
-                if (soft_any(most > kRoom || fail)) {
+                if (soft_any<SOFT>(most > kRoom || fail)) {
                     // new references: the maximum of the tile's 128 tokens per row
-                    float m0 = -INFINITY, m1 = -INFINITY;
+                    float m = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < RT; ++c) {
-                        const float m = warp_max(x[c]);
-                        if (lane == (c & 31)) (c < 32 ? m0 : m1) = m;
+                    for (int c = 0; c < CT; ++c) {
+                        const float mc = warp_max(x[c]);
+                        if (lane == c) m = mc;
                     }
-                    if (lane < RT) bs.part[warp][lane] = m0;
-                    if (RT > 32) bs.part[warp][(lane + 32) % RT] = m1;
-                    if (soft_any(fail)) {                  // the same answer for all 128 threads
+                    if (lane < CT) bs.part[quad][col0 + lane] = m;
+                    if (soft_any<SOFT>(fail)) {            // the same answer for every softmax thread
                         stop = true;
                         break;
                     }
                     if (tid < RT) {
-                        const float m = fmaxf(fmaxf(bs.part[0][tid], bs.part[1][tid]), fmaxf(bs.part[2][tid], bs.part[3][tid]));
+                        const float mt = fmaxf(fmaxf(bs.part[0][tid], bs.part[1][tid]), fmaxf(bs.part[2][tid], bs.part[3][tid]));
                         const float was = bs.ref[tid];
                         float now = was;
-                        if (m - was > kRoom) now = m - kHead;
+                        if (mt - was > kRoom) now = mt - kHead;
                         bs.ref[tid] = now;
                         bs.fac[tid] = now == was ? 1.f : ex2(was - now);
                     }
-                    soft_sync();
-#pragma unroll
-                    for (int c = 0; c < RT; ++c) l[c] *= bs.fac[c];
+                    soft_sync<SOFT>();
                     if (j > 0) {
                         if (mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
                         tc_fence_after();
+                    }
+                    // sums and outputs of the 16 rows around one that moved
+#pragma unroll
+                    for (int c = 0; c < CT; c += 16) {
+                        float f[16];
+                        bool moved = false;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 f4 = *reinterpret_cast<const float4*>(&bs.fac[col0 + c + i]);
+                            f[i] = f4.x; f[i + 1] = f4.y; f[i + 2] = f4.z; f[i + 3] = f4.w;
+                            moved = moved || f4.x != 1.f || f4.y != 1.f || f4.z != 1.f || f4.w != 1.f;
+                        }
+                        if (!moved) continue;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) l[c + i] *= f[i];
+                        if (j == 0) continue;
 #pragma unroll
                         for (int mb = 0; mb < DB; ++mb)
 #pragma unroll
-                            for (int c = 0; c < S::ON; c += 16) {
+                            for (int half = 0; half < (S::CAT ? 2 : 1); ++half) {
+                                const uint32_t at = my_o + mb * S::ON + half * RT + c;
                                 float o[16];
-                                tmem_ld16(my_o + mb * S::ON + c, o);
+                                tmem_ld16(at, o);
                                 tmem_ld_wait();
                                 tmem_regs_ready(o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= bs.fac[(c + i) % RT];
-                                tmem_st16(my_o + mb * S::ON + c, o);
+                                for (int i = 0; i < 16; ++i) o[i] *= f[i];
+                                tmem_st16(at, o);
                             }
+                    }
+                    if (j > 0) {
                         tmem_st_wait();
                         tc_fence_before();
                     }
@@ -661,11 +710,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 // the weights of the last tile have been read
                 if (g > 0 && mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
 #pragma unroll
-                for (int c = 0; c < RT; c += 16) {
+                for (int c = 0; c < CT; c += 16) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
-                        const float4 r4 = *reinterpret_cast<const float4*>(&bs.ref[c + i]);
+                        const float4 r4 = *reinterpret_cast<const float4*>(&bs.ref[col0 + c + i]);
                         const float v0 = ex2(x[c + i] - r4.x), v1 = ex2(x[c + i + 1] - r4.y);
                         const float v2 = ex2(x[c + i + 2] - r4.z), v3 = ex2(x[c + i + 3] - r4.w);
                         l[c + i] = fmaf(v0, iv, l[c + i]);
@@ -674,56 +723,53 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         l[c + i + 3] = fmaf(v3, iv, l[c + i + 3]);
                         split4(v0, v1, v2, v3, &hi[i / 4], &lo[i / 4]);
                     }
-                    unsigned char* ph = psm + chunk_at<S::kPitch>(tid, c / 16);
-                    unsigned char* pl = S::CAT ? psm + chunk_at<S::kPitch>(tid, RT / 16 + c / 16) : ph + kTile * S::kPitch;
+                    const int ch = (col0 + c) / 16;
+                    unsigned char* ph = psm + chunk_at<S::kPitch>(tok, ch);
+                    unsigned char* pl = S::CAT ? psm + chunk_at<S::kPitch>(tok, RT / 16 + ch) : ph + kTile * S::kPitch;
                     *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                if (t0 + kTile > sg.r.len) {
+                if (t0 + kTile > len) {
                     // rows behind the request: whatever lies there must not meet a weight of 0 as NaN
-                    const uint32_t vi = S::SHARED ? it + sg.n - 1 : it + 2 * sg.n - 1;
+                    const uint32_t vi = S::SHARED ? it + n - 1 : it + 2 * n - 1;
                     const uint32_t s = vi % S::SLOTS;
                     if (mbar_wait_abort(&bs.full[s], (vi / S::SLOTS) & 1, abort) <= 0) fail = true;
-                    if (t >= sg.r.len) {
-#pragma unroll
-                        for (int i = 0; i < DB * 8; ++i)
-                            *reinterpret_cast<uint4*>(sm + s * S::kTileBytes + (i >> 3) * (kTile * 128) + tid * 128 +
+                    if (t >= len) {
+                        for (int i = warp >> 2; i < DB * 8; i += S::CG)
+                            *reinterpret_cast<uint4*>(sm + s * S::kTileBytes + (i >> 3) * (kTile * 128) + tok * 128 +
                                                       (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 fence_async_smem();
                 mbar_arrive(&bs.p_full);
-                ks = ks_n;
-                lv = lv_n;
-                iv = iv_n;
             }
             if (stop) {
                 ok = false;
                 break;
             }
-            it += sg.n * (S::SHARED ? 1 : 2);
+            it += n * (S::SHARED ? 1 : 2);
             // ---------------------------------------------------- out
-            if (sg.n > 0) {
-                column_sums<RT>(l, lane, bs.part[warp]);
+            if (n > 0) {
+                column_sums<CT>(l, lane, &bs.part[quad][col0]);
                 if (mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
                 tc_fence_after();
             }
-            soft_sync();
+            soft_sync<SOFT>();
             if (tid < RT) {
-                const float sum = sg.n > 0 ? (bs.part[0][tid] + bs.part[1][tid]) + (bs.part[2][tid] + bs.part[3][tid]) : 0.f;
+                const float sum = n > 0 ? (bs.part[0][tid] + bs.part[1][tid]) + (bs.part[2][tid] + bs.part[3][tid]) : 0.f;
                 bs.sum[tid] = sg.slot >= 0 ? sum : sum == 0.f ? 0.f : 1.f / sum;
                 if (sg.slot >= 0)
                     reinterpret_cast<float2*>(a.part_ml)[(size_t)sg.slot * RT + tid] = make_float2(bs.ref[tid], sum);
             }
-            soft_sync();
-            if (sg.n > 0 || sg.slot < 0) {
+            soft_sync<SOFT>();
+            if (n > 0 || sg.slot < 0) {
 #pragma unroll
-                for (int mb = 0; mb < DB; ++mb)
+                for (int c = 0; c < CT; c += 16) {
+                    if (col0 + c >= sg.nr) break;
 #pragma unroll
-                    for (int c = 0; c < RT; c += 16) {
-                        if (c >= sg.nr) break;
+                    for (int mb = 0; mb < DB; ++mb) {
                         float o[16];
-                        if (sg.n > 0) {
+                        if (n > 0) {
                             tmem_ld16(my_o + mb * S::ON + c, o);
                             if (S::CAT) {
                                 float o2[16];
@@ -743,15 +789,17 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            if (c + i >= sg.nr) break;
+                            const int r = col0 + c + i;
+                            if (r >= sg.nr) break;
                             if (sg.slot < 0) {
-                                const __nv_bfloat16 v = __float2bfloat16_rn(bs.sum[c + i] == 0.f ? 0.f : o[i] * bs.sum[c + i]);
-                                a.out[bs.row_at[c + i] + mb * 128 + tid] = __bfloat16_as_ushort(v);
+                                const __nv_bfloat16 v = __float2bfloat16_rn(bs.sum[r] == 0.f ? 0.f : o[i] * bs.sum[r]);
+                                a.out[bs.row_at[r] + mb * 128 + tok] = __bfloat16_as_ushort(v);
                             } else {
-                                a.part_o[(((size_t)sg.slot * RT + c + i) * DB + mb) * 128 + tid] = o[i];
+                                a.part_o[(((size_t)sg.slot * RT + r) * DB + mb) * 128 + tok] = o[i];
                             }
                         }
                     }
+                }
                 tc_fence_before();
             }
         }
@@ -765,7 +813,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const bool failed = __syncthreads_or(!ok);
     if (failed && tid == 0) atomicOr(a.err, kErrTimeout);
     pdl_trigger();
-    if (warp == 5) {
+    if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, S::ALLOC);
     }
@@ -917,7 +965,7 @@ cudaError_t run(const Cache& c, const CUtensorMap& km, const CUtensorMap& vm, co
     if ((size_t)grid * 2 * S::RT * S::DB * 128 > c.part_o_floats || (size_t)grid * 4 * S::RT > c.part_ml_floats ||
         (size_t)grid > c.meta_n || grid > kMaxParts)
         return cudaErrorInvalidValue;
-    attend_kernel<S><<<grid, kThreads, smem_bytes<S>(), st>>>(km, vm, a);
+    attend_kernel<S><<<grid, S::THREADS, smem_bytes<S>(), st>>>(km, vm, a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_k(join_kernel<S::DB, S::RT>, dim3((unsigned)(2 * c.sm_count)), dim3(kJoinThreads), 0, st, true, a, grid);
@@ -956,7 +1004,7 @@ cudaError_t set_attend_attrs() {
 }
 
 void attend_scratch(int sm_count, int head_dim, size_t* o_floats, size_t* ml_floats, size_t* meta) {
-    const size_t grid = (size_t)sm_count * (head_dim == 128 ? 2 : 1);
+    const size_t grid = (size_t)sm_count * (head_dim <= 256 ? 2 : 1);   // CTAs of the widest grid
     *o_floats = grid * 2 * 64 * head_dim;
     *ml_floats = grid * 4 * 64;
     *meta = grid;
