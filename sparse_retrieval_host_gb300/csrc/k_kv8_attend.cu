@@ -20,10 +20,12 @@
 // the column p holds what the token contributes, and the rounding of p is
 // relative to the largest contribution; the softmax sum takes p / vs in fp32.
 //
-// The running reference `ref` of a row is kept 2^6 below its maximum, and is
-// moved only when a tile exceeds it by 2^8 (e4m3 ends at 448): one vote of the
-// 128 threads per tile; the maximum itself, the rescaling of the sums and of
-// O^T in TMEM only happen when the vote says so (the first tile, then rarely).
+// The running reference `ref` of a row is set 2^5 below its maximum, and is
+// moved only when a weight would pass 2^8.75 (e4m3 ends at 448): one vote of the
+// softmax threads per tile; the maximum itself, the rescaling of the sums and
+// of O^T in TMEM only happen when the vote says so (the first tile, then the
+// more rarely the more tokens a row has seen). Weights down to 2^-10 keep
+// half a step of e4m3's smallest, 2^-15 of the row's largest.
 //
 // Work: a "row tile" is RT of the (token, head) rows that share a KV head of a
 // request; its tokens are cut into tiles of 128. Every (request, KV head, row
@@ -52,9 +54,10 @@ namespace {
 using namespace umma;
 
 constexpr int kTile = 128;               // tokens per tile
+constexpr int kSlotBytes = kTile * 128;  // 128 tokens x 128 dims
 constexpr float kLow = -1e30f;           // reference of a row that has seen no token
-constexpr float kHead = 6.f;             // the reference stays 2^6 below the maximum ...
-constexpr float kRoom = 8.f;             // ... and moves when a weight would pass 2^8
+constexpr float kHead = 5.f;             // the reference is set 2^5 below the maximum ...
+constexpr float kRoom = 8.75f;           // ... and moves when a weight would pass 2^8.75 = 431
 
 // DB: head_dim / 128. RT: rows per row tile. SHARED: V = K.
 template <int DB_, int RT_, bool SHARED_>
@@ -67,18 +70,20 @@ struct Shape {
     static constexpr int ON = CAT ? N : RT;                // O^T columns per 128 dims
     static constexpr int COLS = N + DB * ON;
     static constexpr int ALLOC = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static constexpr int kTileBytes = DB * kTile * 128;
     static constexpr int kQBytes = DB * N * 128;
     static constexpr int kPBytes = kTile * N;
     static constexpr int kPitch = CAT ? N : RT;            // bytes of one token's row of p
     static constexpr int CTAS = DB == 1 || (DB == 2 && RT == 16) ? 2 : 1;   // per SM
-    static constexpr int SLOTS = DB == 1 ? (RT == 64 ? 4 : 5) : DB == 2 ? (RT == 16 ? 3 : 4) : RT == 16 ? 3 : 2;
+    // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
+    // tile j is given back, so two tiles must fit
+    static constexpr int SLOTS = DB == 1 ? (RT == 64 ? 4 : 5) : DB == 2 ? (RT == 16 ? 6 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
+    static_assert(SLOTS >= 2 * DB, "two tiles must fit the ring");
     // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the columns
     static constexpr int CT = DB == 1 && RT == 64 ? 32 : 16;
     static constexpr int CG = RT / CT;
     static constexpr int SOFT = 128 * CG;                  // softmax threads
     static constexpr int THREADS = SOFT + 64;
-    static constexpr int kOffQ = SLOTS * kTileBytes;
+    static constexpr int kOffQ = SLOTS * kSlotBytes;
     static constexpr int kOffP = kOffQ + kQBytes;
     static constexpr int kOffBars = kOffP + kPBytes;
 };
@@ -106,8 +111,24 @@ struct Args {
 struct Request {
     int q0, nq, len;
     int nrt;           // row tiles
-    int tlo, nt;       // first token tile, token tiles (at least 1)
+    int pairs;         // of row tiles, per KV head
+    int P;             // units of a pair: at least the token tiles of its two row tiles
 };
+
+// Token tiles that any row of row tile rt sees, from *first on.
+template <int RT>
+__device__ __forceinline__ int tiles_of(const Args& a, const Request& r, int rt, int* first) {
+    const int c = r.len - r.nq;                                    // position of the first query
+    const int p_lo = c + rt * RT / a.group, p_hi = c + min(r.nq - 1, ((rt + 1) * RT - 1) / a.group);
+    *first = a.window ? max(0, p_lo - a.window + 1) / kTile : 0;
+    return max(0, (p_hi < 0 ? 0 : p_hi / kTile + 1) - *first);
+}
+// The same, but at least 1: a row tile that sees nothing has its zeros to write.
+template <int RT>
+__device__ __forceinline__ int units_of(const Args& a, const Request& r, int rt) {
+    int first;
+    return max(1, tiles_of<RT>(a, r, rt, &first));
+}
 
 template <int RT>
 __device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
@@ -118,20 +139,28 @@ __device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
     r.len = min(max(n, 0), most);
     if (c0 != r.q0 || c1 != r.q0 + r.nq || n != r.len) *bad = true;
     r.nrt = (r.nq * a.group + RT - 1) / RT;
-    const int p0 = r.len - r.nq;                                   // position of the first query
-    r.tlo = a.window ? max(0, p0 - a.window + 1) / kTile : 0;
-    r.nt = max(1, (r.len + kTile - 1) / kTile - r.tlo);
+    // A causal row tile has the more tokens the later it is; row tiles k and
+    // nrt - 1 - k together have the same, up to one tile for the rounding (or
+    // up to twice a window's tiles), so pairs are units of equal work.
+    r.pairs = (r.nrt + 1) >> 1;
+    r.P = 0;
+    if (r.nrt == 1) r.P = units_of<RT>(a, r, 0);
+    else if (r.nrt == 2 || (r.nrt > 2 && !a.window))
+        r.P = units_of<RT>(a, r, 0) + units_of<RT>(a, r, r.nrt - 1) + (r.nrt > 2);
+    else if (r.nrt > 2)
+        r.P = 2 * min(max(1, (r.len + kTile - 1) / kTile),
+                      (int)(((long long)a.window + RT / a.group + 1) / kTile) + 2);
     return r;
 }
 __device__ __forceinline__ long long units(const Args& a, const Request& r) {
-    return (long long)r.nrt * a.kv_heads * r.nt;
+    return (long long)r.pairs * a.kv_heads * r.P;
 }
 
-// One CTA's share of one item.
+// One CTA's share of one item (a row tile of a KV head of a request).
 struct Segment {
     int b, h, rt;
     int row0, nr;        // rows of the row tile in the request's (token, head) order
-    int t0, n;           // first token tile and tiles to run (0: no row sees any of them)
+    int t0, n;           // first token tile and tiles to run (0: no row sees any)
     int slot;            // -1: the whole item; else the partial's slot
     int parts;           // CTAs of the item, when it begins here and goes on
     Request r;
@@ -146,44 +175,53 @@ struct Walker {
     Request r;
 
     __device__ __forceinline__ bool next(const Args& a, Segment* s) {
-        if (u >= u1) return false;
-        bool bad = false;
-        while (off >= units(a, r)) {
-            off -= units(a, r);
-            r = request<RT>(a, ++b, &bad);
-        }
-        const long long item = off / r.nt;
-        const int t_off = (int)(off - item * r.nt);
-        const int take = (int)min((long long)(r.nt - t_off), u1 - u);
-        const int i = (int)(item % r.nrt);
-        s->b = b;
-        s->h = (int)(item / r.nrt);
-        // row tiles from both ends in turn: neighbours then have the same work on
-        // average (a causal row tile has fewer tokens the earlier it is)
-        s->rt = (i & 1) ? r.nrt - 1 - (i >> 1) : (i >> 1);
-        s->row0 = s->rt * RT;
-        s->nr = min(RT, r.nq * a.group - s->row0);
-        s->r = r;
-        // token tiles that any of these rows sees
-        const int p_hi = r.len - r.nq + (s->row0 + s->nr - 1) / a.group;
-        const int p_lo = r.len - r.nq + s->row0 / a.group;
-        const int first = a.window ? max(0, p_lo - a.window + 1) / kTile : 0;
-        const int last = p_hi < 0 ? 0 : p_hi / kTile + 1;
-        const int lo = max(r.tlo + t_off, first), hi = min(r.tlo + t_off + take, last);
-        s->t0 = lo;
-        s->n = max(0, hi - lo);
-        s->slot = -1;
-        s->parts = 0;
-        if (take != r.nt) {
-            s->slot = 2 * cta + (t_off == 0);
-            if (t_off == 0) {
-                const long long end = u + r.nt - 1;                // the item's last unit
-                s->parts = (int)(((end + 1) * n_cta - 1) / U) - cta + 1;
+        while (u < u1) {
+            bool bad = false;
+            while (off >= units(a, r)) {
+                off -= units(a, r);
+                r = request<RT>(a, ++b, &bad);
             }
+            const long long head = (long long)r.pairs * r.P;
+            const int h = (int)(off / head);
+            const long long in = off - h * head;
+            const int k = (int)(in / r.P), o = (int)(in - (long long)k * r.P);
+            // the later row tile of the pair first, then the earlier, then nothing
+            const int big = r.nrt - 1 - k, nb = units_of<RT>(a, r, big);
+            int rt = big, at = o, n = nb;
+            if (o >= nb) {
+                rt = k;
+                at = o - nb;
+                n = k < big ? units_of<RT>(a, r, k) : 0;
+            }
+            if (at >= n) {
+                const long long skip = min((long long)(r.P - o), u1 - u);
+                u += skip;
+                off += skip;
+                continue;
+            }
+            const int take = (int)min((long long)(n - at), u1 - u);
+            s->b = b;
+            s->h = h;
+            s->rt = rt;
+            s->row0 = rt * RT;
+            s->nr = min(RT, r.nq * a.group - s->row0);
+            s->r = r;
+            int first;
+            const int tiles = tiles_of<RT>(a, r, rt, &first);
+            s->t0 = first + at;
+            s->n = min(take, max(0, tiles - at));
+            s->slot = -1;
+            s->parts = 0;
+            if (take != n) {
+                s->slot = 2 * cta + (at == 0);
+                if (at == 0)                                       // the CTA of the item's last unit
+                    s->parts = (int)(((u + n) * n_cta - 1) / U) - cta + 1;
+            }
+            u += take;
+            off += take;
+            return true;
         }
-        u += take;
-        off += take;
-        return true;
+        return false;
     }
 };
 
@@ -203,9 +241,40 @@ __device__ __forceinline__ bool soft_any(bool v) {
         : "memory");
     return r != 0;
 }
+// One arrival per warp, after all its lanes (arrivals of one barrier are taken
+// one by one: 512 of them held the last one up by some 1,000 cycles).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
 __device__ __forceinline__ float warp_max(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(v));
+    return r;
+}
+// Pairs of fp32 values in one 64-bit register (one instruction for both).
+using u64 = unsigned long long;
+__device__ __forceinline__ u64 pack(float a, float b) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(u64 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -217,6 +286,13 @@ __device__ __forceinline__ float lg2(float x) {
     float r;
     asm("lg2.approx.f32 %0, %1;\n" : "=f"(r) : "f"(x));
     return r;
+}
+// One lane of the (converged) warp; the same one every time, as commits follow
+// the MMAs of the thread that issued them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -277,7 +353,7 @@ struct Bars {
     int start_b;
     uint32_t tmem_base;
     int abort;
-    alignas(16) float ref[S::RT];     // reference exponent of each row
+    alignas(16) float nref[S::RT];    // minus the reference exponent of each row
     alignas(16) float fac[S::RT];     // 2^(old reference - new)
     alignas(16) float qs[S::RT];      // query scale * softmax scale * log2 e
     float part[4][S::RT];             // per-warp maxima, then sums
@@ -372,10 +448,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             mbar_init(&bs.full[s], 1);
             mbar_init(&bs.empty[s], 1);
         }
-        mbar_init(&bs.q_full, SOFT);
+        mbar_init(&bs.q_full, SOFT / 32);
         mbar_init(&bs.s_full, 1);
-        mbar_init(&bs.s_free, SOFT);
-        mbar_init(&bs.p_full, SOFT);
+        mbar_init(&bs.s_free, SOFT / 32);
+        mbar_init(&bs.p_full, SOFT / 32);
         mbar_init(&bs.pv_done, 1);
         mbar_init(&bs.drain, 1);
         bs.abort = 0;
@@ -396,26 +472,27 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     Segment sg{};
     if (warp == kWarpTma) {
         // ======================================================== TMA
-        uint32_t it = 0;                                   // tiles requested
-        const int bpt = kTile >> a.bs_log2;                // blocks per tile
+        uint32_t it = 0;                                   // blocks of 128 dims requested
+        const int bpt = kTile >> a.bs_log2, bsz = 1 << a.bs_log2;
         auto load = [&](int tile, bool is_v) -> bool {
-            const int s = it % S::SLOTS;
-            const bool got = it < S::SLOTS || mbar_wait_abort(&bs.empty[s], ((it / S::SLOTS) + 1) & 1, abort) > 0;
-            if (!__all_sync(0xffffffffu, got)) return false;
-            const int bsz = 1 << a.bs_log2;
             const int nb = min(bpt, (sg.r.len - tile * kTile + bsz - 1) >> a.bs_log2);
-            if (lane == 0) mbar_arrive_expect_tx(&bs.full[s], (uint32_t)(nb * bsz * DB * 128));
-            __syncwarp();
-            if (lane < nb * DB) {
-                const int pg = lane / DB, db = lane % DB;
-                const int id = a.table[(size_t)sg.b * a.max_blocks + (size_t)tile * bpt + pg];
-                const uint32_t dst = smem_u32(sm + s * S::kTileBytes) + db * (kTile * 128) + pg * bsz * 128;
+            int id = 0;
+            if (lane < nb) {
+                id = __ldg(a.table + (size_t)sg.b * a.max_blocks + (size_t)tile * bpt + lane);
                 // an id that is no block reads as zeros (out of the tensor's range)
-                tma_load_4d(dst, is_v ? &vmap : &kmap, db * 128, 0, sg.h, id < 0 ? a.n_blocks : min(id, a.n_blocks),
-                            &bs.full[s]);
+                if (id < 0 || id > a.n_blocks) id = a.n_blocks;
             }
-            __syncwarp();
-            ++it;
+            for (int d = 0; d < DB; ++d) {
+                const int s = it % S::SLOTS;
+                const bool got = it < S::SLOTS || mbar_wait_abort(&bs.empty[s], ((it / S::SLOTS) + 1) & 1, abort) > 0;
+                if (!__all_sync(0xffffffffu, got)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(&bs.full[s], (uint32_t)(nb * bsz * 128));
+                __syncwarp();
+                if (lane < nb)
+                    tma_load_4d(smem_u32(sm + s * kSlotBytes) + lane * bsz * 128, is_v ? &vmap : &kmap, d * 128, 0, sg.h, id,
+                                &bs.full[s]);
+                ++it;
+            }
             return true;
         };
         while (ok && w.next(a, &sg)) {
@@ -430,73 +507,82 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 mbar_wait(&bs.full[i % S::SLOTS], (i / S::SLOTS) & 1);
     } else if (warp == kWarpMma) {
         // ======================================================== MMA issue
-        if (lane == 0) {
-            constexpr uint32_t id_qk = idesc_f32acc(0, 0, 0, kTile, N);          // e4m3, both K-major
-            constexpr uint32_t id_pv = idesc_f32acc(0, 1, 1, 128, S::ON);        // both MN-major
-            const uint32_t q0 = smem_u32(sm + S::kOffQ), p0 = smem_u32(sm + S::kOffP);
-            uint32_t it = 0, g = 0, segs = 0;              // tiles taken, token tiles, segments with tiles
-            uint32_t v_slot = 0;                           // slot of the tile whose PV is due
-            auto pv = [&](uint32_t gt, bool first) -> bool {
-                if (mbar_wait_abort(&bs.p_full, gt & 1, abort) <= 0) return false;
-                if (!S::SHARED) {
-                    v_slot = it % S::SLOTS;
-                    if (mbar_wait_abort(&bs.full[v_slot], (it / S::SLOTS) & 1, abort) <= 0) return false;
-                    ++it;
-                }
-                tc_fence_after();
-                const uint32_t v0 = smem_u32(sm + v_slot * S::kTileBytes);
+        // The whole warp walks and waits, one elected lane issues: descriptors then
+        // stay in uniform registers (a lane of its own took 58 cycles per MMA to
+        // issue, this way 40; N = 64 and 128 run at 48 and 64, the rate at which
+        // their operands leave shared memory).
+        constexpr uint32_t id_qk = idesc_f32acc(0, 0, 0, kTile, N);              // e4m3, both K-major
+        constexpr uint32_t id_pv = idesc_f32acc(0, 1, 1, 128, S::ON);            // both MN-major
+        const uint32_t r0 = smem_u32(sm);
+        const uint64_t qd = desc_sw128(smem_u32(sm + S::kOffQ), 16, 1024), pd = desc_rows<S::kPitch>(smem_u32(sm + S::kOffP));
+        uint32_t it = 0, g = 0, segs = 0;                  // blocks taken, token tiles, segments with tiles
+        auto got = [&](uint64_t* bar, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, mbar_wait_abort(bar, parity, abort) > 0);
+        };
+        // PV of tile gt, whose K blocks began at block `k_it` of the ring
+        auto pv = [&](uint32_t gt, bool first, uint32_t k_it) -> bool {
+            if (!got(&bs.p_full, gt & 1)) return false;
 #pragma unroll
-                for (int mb = 0; mb < DB; ++mb)
+            for (int mb = 0; mb < DB; ++mb) {
+                const uint32_t i = S::SHARED ? k_it + mb : it + mb, s = i % S::SLOTS;
+                if (!S::SHARED && !got(&bs.full[s], (i / S::SLOTS) & 1)) return false;
+                tc_fence_after();
+                const uint64_t vd = desc_sw128(r0 + s * kSlotBytes, 16, 1024);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 32; ++kk) {
-                        const uint64_t va = desc_sw128(v0 + mb * (kTile * 128) + kk * 32 * 128, 16, 1024);
-                        const uint32_t acc = !first || kk > 0;
-                        mma_f8(tm_o + mb * S::ON, va, desc_rows<S::kPitch>(p0 + kk * 32 * S::kPitch), id_pv, acc);
+                        mma_f8(tm_o + mb * S::ON, vd + kk * (32 * 128 / 16), pd + kk * (32 * S::kPitch / 16), id_pv,
+                               !first || kk > 0);
                         if (!S::CAT)
-                            mma_f8(tm_o + mb * S::ON, va,
-                                   desc_rows<S::kPitch>(p0 + kTile * S::kPitch + kk * 32 * S::kPitch), id_pv, 1);
+                            mma_f8(tm_o + mb * S::ON, vd + kk * (32 * 128 / 16),
+                                   pd + (kTile * S::kPitch + kk * 32 * S::kPitch) / 16, id_pv, 1);
                     }
-                mma_commit(&bs.empty[v_slot]);
-                mma_commit(&bs.pv_done);
-                return true;
-            };
-            while (ok && w.next(a, &sg)) {
-                if (sg.n == 0) continue;
-                ok = mbar_wait_abort(&bs.q_full, segs & 1, abort) > 0;
-                ++segs;
-                uint32_t next_v = 0;
-                for (int j = 0; ok && j < sg.n; ++j) {
-                    const uint32_t s = it % S::SLOTS;
-                    if (mbar_wait_abort(&bs.full[s], (it / S::SLOTS) & 1, abort) <= 0 ||
-                        (g > 0 && mbar_wait_abort(&bs.s_free, (g - 1) & 1, abort) <= 0)) {
+                    mma_commit(&bs.empty[s]);
+                    if (mb == DB - 1) mma_commit(&bs.pv_done);
+                }
+                __syncwarp();
+            }
+            if (!S::SHARED) it += DB;
+            return true;
+        };
+        while (ok && w.next(a, &sg)) {
+            if (sg.n == 0) continue;
+            ok = got(&bs.q_full, segs & 1);
+            ++segs;
+            uint32_t k_it = 0;
+            for (int j = 0; ok && j < sg.n; ++j) {
+                if (g > 0) ok = got(&bs.s_free, (g - 1) & 1);
+                const uint32_t k_new = it;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const uint32_t s = (it + d) % S::SLOTS;
+                    if (!ok || !got(&bs.full[s], ((it + d) / S::SLOTS) & 1)) {
                         ok = false;
                         break;
                     }
-                    ++it;
                     tc_fence_after();
-                    const uint32_t k0 = smem_u32(sm + s * S::kTileBytes);
+                    const uint64_t kd = desc_sw128(r0 + s * kSlotBytes, 16, 1024);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < DB * 4; ++kk)
-                        mma_f8(tm_s, desc_sw128(k0 + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024),
-                               desc_sw128(q0 + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024), id_qk, kk > 0);
-                    if (!S::SHARED) mma_commit(&bs.empty[s]);
-                    mma_commit(&bs.s_full);
-                    ++g;
-                    if (j > 0) {
-                        v_slot = next_v;
-                        ok = pv(g - 2, j == 1);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f8(tm_s, kd + kk * 2, qd + (d * N * 128 + kk * 32) / 16, id_qk, (d | kk) != 0);
+                        if (!S::SHARED) mma_commit(&bs.empty[s]);
+                        if (d == DB - 1) mma_commit(&bs.s_full);
                     }
-                    next_v = s;
+                    __syncwarp();
                 }
-                if (ok) {
-                    v_slot = next_v;
-                    ok = pv(g - 1, sg.n == 1);
-                }
+                if (!ok) break;
+                it += DB;
+                ++g;
+                if (j > 0) ok = pv(g - 2, j == 1, k_it);
+                k_it = k_new;
             }
-            // every MMA issued completes before TMEM is freed
-            mma_commit(&bs.drain);
-            if (!mbar_wait(&bs.drain, 0)) ok = false;
+            if (ok) ok = pv(g - 1, sg.n == 1, k_it);
         }
+        // every MMA issued completes before TMEM is freed
+        if (elect_one()) mma_commit(&bs.drain);
+        __syncwarp();
+        if (!mbar_wait(&bs.drain, 0)) ok = false;
     } else {
         // ======================================================== softmax
         const int quad = warp & 3, col0 = (warp >> 2) * CT;    // TMEM lanes of this warp, first column
@@ -505,19 +591,19 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const uint32_t my_s = tm_s + lane_base + col0, my_o = tm_o + lane_base + col0;
         unsigned char* qsm = sm + S::kOffQ;
         unsigned char* psm = sm + S::kOffP;
-        uint32_t g = 0, it = 0;                            // token tiles, tiles of the ring
-        bool fail = false, ids_bad = false, begun = false;
-        float l[CT];
-        if (tid == 0) bs.walk = w;
+        uint32_t g = 0, it = 0;                            // token tiles, blocks of the ring
+        bool fail = false, ids_bad = false;
+        u64 l2[CT / 2];                                    // sums of p / vs, two rows each
+        if (tid == 0) {
+            bs.walk = w;
+            a.meta[cta] = make_int4(0, 0, 0, 0);           // no split item begins here, so far
+        }
         for (int turn = 0;; turn ^= 1) {
             const Segment& sg = bs.seg[turn];
             if (tid == 0) {
                 const bool more = bs.walk.next(a, &bs.seg[turn]);
                 bs.more[turn] = more;
-                if (more && sg.parts) {
-                    begun = true;
-                    a.meta[cta] = make_int4(sg.b, sg.h, sg.rt, sg.parts);
-                }
+                if (more && sg.parts) a.meta[cta] = make_int4(sg.b, sg.h, sg.rt, sg.parts);
             }
             soft_sync<SOFT>();                             // also: the last segment's shared arrays are read
             if (!bs.more[turn]) break;
@@ -539,7 +625,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 bs.pos[tid] = on ? p_first + qt : -1;
                 bs.row_at[tid] = (long long)(sg.r.q0 + qt) * a.out_row + (long long)hd * (DB * 128);
                 // a column without a row is held at weight 0 by a reference out of reach
-                bs.ref[tid] = on ? kLow : -kLow;
+                bs.nref[tid] = on ? -kLow : kLow;
             }
             if (n > 0) {
                 // queries: a warp per row, 4 values per lane and 128 dims
@@ -582,7 +668,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     }
                 }
                 fence_async_smem();
-                mbar_arrive(&bs.q_full);
+                warp_arrive(&bs.q_full, lane);
             }
             float ks_raw = 0.f, vs_raw = 0.f;
             bool has = id_0 >= 0 && id_0 < a.n_blocks;
@@ -595,9 +681,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             load_scales(id_0);
             soft_sync<SOFT>();
 #pragma unroll
-            for (int c = 0; c < CT; ++c) l[c] = 0.f;
-            const int win = a.window ? a.window : 1 << 30;
-            const int p_lo = bs.pos[0], p_hi = bs.pos[sg.nr - 1];
+            for (int c = 0; c < CT / 2; ++c) l2[c] = 0;
             bool stop = false;
             for (int j = 0; j < n; ++j, ++g) {
                 const int t0 = (sg.t0 + j) * kTile, t = t0 + tok;
@@ -615,37 +699,47 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 id_1 = block_of(j + 2);
                 if (mbar_wait_abort(&bs.s_full, g & 1, abort) <= 0) fail = true;
                 tc_fence_after();
+                constexpr int LD = CT == 32 ? 8 : 16;      // columns per load: what the registers hold beside x and l2
                 float x[CT];
-                {
-                    float hi[CT], lo[CT];
-                    tmem_ld<CT>(my_s, hi);
-                    tmem_ld<CT>(my_s + RT, lo);
-                    tmem_ld_wait();
-                    tmem_regs_ready_n<CT>(hi);
-                    tmem_regs_ready_n<CT>(lo);
-#pragma unroll
-                    for (int i = 0; i < CT; ++i) x[i] = hi[i] + lo[i];
-                }
-                tc_fence_before();
-                mbar_arrive(&bs.s_free);
                 float most = kLow;
-                const bool edge = t0 + kTile - 1 > p_lo || t0 <= p_hi - win;
+                const int win = a.window ? a.window : 1 << 30;
+                const bool edge = t0 + kTile - 1 > bs.pos[0] || t0 <= bs.pos[sg.nr - 1] - win;
+                const u64 ks2 = pack(ks, ks), lv2 = pack(lv, lv);
+#pragma unroll
+                for (int c = 0; c < CT; c += LD) {
+                    float hi[LD], lo[LD];
+                    tmem_ld<LD>(my_s + c, hi);
+                    tmem_ld<LD>(my_s + RT + c, lo);
+                    tmem_ld_wait();
+                    tmem_regs_ready_n<LD>(hi);
+                    tmem_regs_ready_n<LD>(lo);
+                    if (c + LD == CT) {
+                        tc_fence_before();
+                        warp_arrive(&bs.s_free, lane);
+                    }
+#pragma unroll
+                    for (int i = 0; i < LD; i += 4) {
+                        const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(&bs.qs[col0 + c + i]);
+                        const u64 a0 = fma2(mul2(add2(pack(hi[i], hi[i + 1]), pack(lo[i], lo[i + 1])), s4.x), ks2, lv2);
+                        const u64 a1 = fma2(mul2(add2(pack(hi[i + 2], hi[i + 3]), pack(lo[i + 2], lo[i + 3])), s4.y), ks2, lv2);
+                        unpack(a0, x[c + i], x[c + i + 1]);
+                        unpack(a1, x[c + i + 2], x[c + i + 3]);
+                    }
+                }
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        const int p = bs.pos[col0 + c];
+                        if (t > p || t <= p - win) x[c] = -INFINITY;
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < CT; c += 4) {
-                    const float4 s4 = *reinterpret_cast<const float4*>(&bs.qs[col0 + c]);
-                    const float4 r4 = *reinterpret_cast<const float4*>(&bs.ref[col0 + c]);
-                    x[c] = fmaf(x[c] * s4.x, ks, lv);
-                    x[c + 1] = fmaf(x[c + 1] * s4.y, ks, lv);
-                    x[c + 2] = fmaf(x[c + 2] * s4.z, ks, lv);
-                    x[c + 3] = fmaf(x[c + 3] * s4.w, ks, lv);
-                    if (edge) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int p = bs.pos[col0 + c + i];
-                            if (t > p || t <= p - win) x[c + i] = -INFINITY;
-                        }
-                    }
-                    most = fmaxf(most, fmaxf(fmaxf(x[c] - r4.x, x[c + 1] - r4.y), fmaxf(x[c + 2] - r4.z, x[c + 3] - r4.w)));
+                    const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&bs.nref[col0 + c]);
+                    float y0, y1, y2, y3;
+                    unpack(add2(pack(x[c], x[c + 1]), r4.x), y0, y1);
+                    unpack(add2(pack(x[c + 2], x[c + 3]), r4.y), y2, y3);
+                    most = fmaxf(most, fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
                 }
                 if (soft_any<SOFT>(most > kRoom || fail)) {
                     // new references: the maximum of the tile's 128 tokens per row
@@ -662,10 +756,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     }
                     if (tid < RT) {
                         const float mt = fmaxf(fmaxf(bs.part[0][tid], bs.part[1][tid]), fmaxf(bs.part[2][tid], bs.part[3][tid]));
-                        const float was = bs.ref[tid];
+                        const float was = -bs.nref[tid];
                         float now = was;
                         if (mt - was > kRoom) now = mt - kHead;
-                        bs.ref[tid] = now;
+                        bs.nref[tid] = -now;
                         bs.fac[tid] = now == was ? 1.f : ex2(was - now);
                     }
                     soft_sync<SOFT>();
@@ -673,40 +767,38 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         if (mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
                         tc_fence_after();
                     }
-                    // sums and outputs of the 16 rows around one that moved
+                    // sums and outputs of the 8 rows around one that moved
 #pragma unroll
-                    for (int c = 0; c < CT; c += 16) {
-                        float f[16];
-                        bool moved = false;
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const float4 f4 = *reinterpret_cast<const float4*>(&bs.fac[col0 + c + i]);
-                            f[i] = f4.x; f[i + 1] = f4.y; f[i + 2] = f4.z; f[i + 3] = f4.w;
-                            moved = moved || f4.x != 1.f || f4.y != 1.f || f4.z != 1.f || f4.w != 1.f;
-                        }
-                        if (!moved) continue;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) l[c + i] *= f[i];
+                    for (int c = 0; c < CT; c += 8) {
+                        const ulonglong2 fa = *reinterpret_cast<const ulonglong2*>(&bs.fac[col0 + c]);
+                        const ulonglong2 fb = *reinterpret_cast<const ulonglong2*>(&bs.fac[col0 + c + 4]);
+                        const u64 one = pack(1.f, 1.f);
+                        if (fa.x == one && fa.y == one && fb.x == one && fb.y == one) continue;
+                        l2[c / 2] = mul2(l2[c / 2], fa.x);
+                        l2[c / 2 + 1] = mul2(l2[c / 2 + 1], fa.y);
+                        l2[c / 2 + 2] = mul2(l2[c / 2 + 2], fb.x);
+                        l2[c / 2 + 3] = mul2(l2[c / 2 + 3], fb.y);
                         if (j == 0) continue;
-#pragma unroll
-                        for (int mb = 0; mb < DB; ++mb)
-#pragma unroll
-                            for (int half = 0; half < (S::CAT ? 2 : 1); ++half) {
-                                const uint32_t at = my_o + mb * S::ON + half * RT + c;
-                                float o[16];
-                                tmem_ld16(at, o);
-                                tmem_ld_wait();
-                                tmem_regs_ready(o);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= f[i];
-                                tmem_st16(at, o);
-                            }
+#pragma unroll 1
+                        for (int i = 0; i < DB * (S::CAT ? 2 : 1); ++i) {
+                            const uint32_t at = my_o + (S::CAT ? (i >> 1) * S::ON + (i & 1) * RT : i * S::ON) + c;
+                            float o[8];
+                            tmem_ld<8>(at, o);
+                            tmem_ld_wait();
+                            tmem_regs_ready_n<8>(o);
+                            unpack(mul2(pack(o[0], o[1]), fa.x), o[0], o[1]);
+                            unpack(mul2(pack(o[2], o[3]), fa.y), o[2], o[3]);
+                            unpack(mul2(pack(o[4], o[5]), fb.x), o[4], o[5]);
+                            unpack(mul2(pack(o[6], o[7]), fb.y), o[6], o[7]);
+                            tmem_st<8>(at, o);
+                        }
                     }
                     if (j > 0) {
                         tmem_st_wait();
                         tc_fence_before();
                     }
                 }
+                const u64 iv2 = pack(iv, iv);
                 // the weights of the last tile have been read
                 if (g > 0 && mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
 #pragma unroll
@@ -714,13 +806,13 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
-                        const float4 r4 = *reinterpret_cast<const float4*>(&bs.ref[col0 + c + i]);
-                        const float v0 = ex2(x[c + i] - r4.x), v1 = ex2(x[c + i + 1] - r4.y);
-                        const float v2 = ex2(x[c + i + 2] - r4.z), v3 = ex2(x[c + i + 3] - r4.w);
-                        l[c + i] = fmaf(v0, iv, l[c + i]);
-                        l[c + i + 1] = fmaf(v1, iv, l[c + i + 1]);
-                        l[c + i + 2] = fmaf(v2, iv, l[c + i + 2]);
-                        l[c + i + 3] = fmaf(v3, iv, l[c + i + 3]);
+                        const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&bs.nref[col0 + c + i]);
+                        float y0, y1, y2, y3;
+                        unpack(add2(pack(x[c + i], x[c + i + 1]), r4.x), y0, y1);
+                        unpack(add2(pack(x[c + i + 2], x[c + i + 3]), r4.y), y2, y3);
+                        const float v0 = ex2(y0), v1 = ex2(y1), v2 = ex2(y2), v3 = ex2(y3);
+                        l2[(c + i) / 2] = fma2(pack(v0, v1), iv2, l2[(c + i) / 2]);
+                        l2[(c + i) / 2 + 1] = fma2(pack(v2, v3), iv2, l2[(c + i) / 2 + 1]);
                         split4(v0, v1, v2, v3, &hi[i / 4], &lo[i / 4]);
                     }
                     const int ch = (col0 + c) / 16;
@@ -731,25 +823,29 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 }
                 if (t0 + kTile > len) {
                     // rows behind the request: whatever lies there must not meet a weight of 0 as NaN
-                    const uint32_t vi = S::SHARED ? it + n - 1 : it + 2 * n - 1;
-                    const uint32_t s = vi % S::SLOTS;
-                    if (mbar_wait_abort(&bs.full[s], (vi / S::SLOTS) & 1, abort) <= 0) fail = true;
-                    if (t >= len) {
-                        for (int i = warp >> 2; i < DB * 8; i += S::CG)
-                            *reinterpret_cast<uint4*>(sm + s * S::kTileBytes + (i >> 3) * (kTile * 128) + tok * 128 +
-                                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    // (the request's last tile, so the last of the segment: its V blocks end the segment's)
+                    const uint32_t v0 = it + (S::SHARED ? n - 1 : 2 * n - 1) * DB;
+                    for (int d = 0; d < DB; ++d) {
+                        const uint32_t s = (v0 + d) % S::SLOTS;
+                        if (mbar_wait_abort(&bs.full[s], ((v0 + d) / S::SLOTS) & 1, abort) <= 0) fail = true;
+                        if (t >= len)
+                            for (int i = warp >> 2; i < 8; i += S::CG)
+                                *reinterpret_cast<uint4*>(sm + s * kSlotBytes + tok * 128 + i * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 fence_async_smem();
-                mbar_arrive(&bs.p_full);
+                warp_arrive(&bs.p_full, lane);
             }
             if (stop) {
                 ok = false;
                 break;
             }
-            it += n * (S::SHARED ? 1 : 2);
+            it += n * (S::SHARED ? DB : 2 * DB);
             // ---------------------------------------------------- out
             if (n > 0) {
+                float l[CT];
+#pragma unroll
+                for (int c = 0; c < CT; c += 2) unpack(l2[c / 2], l[c], l[c + 1]);
                 column_sums<CT>(l, lane, &bs.part[quad][col0]);
                 if (mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
                 tc_fence_after();
@@ -759,7 +855,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 const float sum = n > 0 ? (bs.part[0][tid] + bs.part[1][tid]) + (bs.part[2][tid] + bs.part[3][tid]) : 0.f;
                 bs.sum[tid] = sg.slot >= 0 ? sum : sum == 0.f ? 0.f : 1.f / sum;
                 if (sg.slot >= 0)
-                    reinterpret_cast<float2*>(a.part_ml)[(size_t)sg.slot * RT + tid] = make_float2(bs.ref[tid], sum);
+                    reinterpret_cast<float2*>(a.part_ml)[(size_t)sg.slot * RT + tid] = make_float2(-bs.nref[tid], sum);
             }
             soft_sync<SOFT>();
             if (n > 0 || sg.slot < 0) {
@@ -805,7 +901,6 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         if (fail) ok = false;
         if (ids_bad) atomicOr(a.err, kErrBounds);
-        if (!begun && tid == 0) a.meta[cta] = make_int4(0, 0, 0, 0);
     }
 
     // ------------------------------------------------------------ teardown

@@ -446,8 +446,8 @@ def _check_attend(c, q, cu, out, scale, window):
     """Every value within what the number formats allow.
 
     Weights are rounded to two e4m3 terms: relative 2^-4 * 2^-4 (and 2^-11 on the way, in fp16), or, for small ones, half of
-    the smallest step 2^-9 where the row's largest weight is at least 2^6 (the reference lies 2^6 below a maximum and moves
-    when one passes 2^8): 2^-16 of the largest w * vs per code. Queries are two e4m3 terms: exact, or 2^-17 of the row's
+    the smallest step 2^-9 where the row's largest weight is at least 2^5 (the reference is set 2^5 below the maximum):
+    2^-15 of the largest w * vs per code. Queries are two e4m3 terms: exact, or 2^-17 of the row's
     largest times the sum of |K|; scores are fp32 sums of D products and a few fp32 steps on values up to |s|:
     (D + 8) 2^-24 of sum |q K| covers them. Weight errors reach the output through sum w |V| / l. bf16 output: 2^-8."""
     D, Hk, bs = c.D, c.Hk, c.bs
@@ -484,7 +484,7 @@ def _check_attend(c, q, cu, out, scale, window):
         rel = 2.0 ** -8 + 2.0 ** -11 + 2 * (eps_s * see).amax(-1, keepdim=True)
         contrib = (w * vs[:, None, None, :]).amax(-1, keepdim=True)
         tol = rel * torch.einsum("hgit,htd->hgid", w, v.abs())
-        tol += 2.0 ** -16 * contrib * torch.einsum("hgit,htd->hgid", see.double().expand_as(w), vc.abs())
+        tol += 2.0 ** -15 * contrib * torch.einsum("hgit,htd->hgid", see.double().expand_as(w), vc.abs())
         tol += 2.0 ** -8 * want.abs()
         want, tol = (z.permute(2, 0, 1, 3).reshape(nq, H, D) for z in (want, tol))
         bad = ~((got - want).abs() <= tol)
