@@ -77,7 +77,7 @@ struct Shape {
     // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
     // tile j is given back, so two tiles must fit
     static constexpr int SLOTS = DB == 1 ? (RT == 64 ? 4 : 5) : DB == 2 ? (RT == 16 ? 6 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
-    static_assert(SLOTS >= 2 * DB, "two tiles must fit the ring");
+    static_assert(SLOTS >= 2 * DB && SLOTS / DB + 2 < 8, "two tiles must fit the ring, and fewer than the scales held");
     // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the columns
     static constexpr int CT = DB == 1 && RT == 64 ? 32 : 16;
     static constexpr int CG = RT / CT;
@@ -163,7 +163,7 @@ struct Segment {
     int t0, n;           // first token tile and tiles to run (0: no row sees any)
     int slot;            // -1: the whole item; else the partial's slot
     int parts;           // CTAs of the item, when it begins here and goes on
-    Request r;
+    int q0, nq, len;     // the request's first row, rows and tokens
 };
 
 // Walks the units [u, u1) that a CTA owns. Every role walks on its own.
@@ -205,7 +205,9 @@ struct Walker {
             s->rt = rt;
             s->row0 = rt * RT;
             s->nr = min(RT, r.nq * a.group - s->row0);
-            s->r = r;
+            s->q0 = r.q0;
+            s->nq = r.nq;
+            s->len = r.len;
             int first;
             const int tiles = tiles_of<RT>(a, r, rt, &first);
             s->t0 = first + at;
@@ -338,10 +340,16 @@ __device__ __forceinline__ void split4(float v0, float v1, float v2, float v3, u
     *lo = la | (lb << 16);
 }
 
+constexpr int kSegs = 4;     // segments handed on ahead of their use
+constexpr int kScales = 8;   // token tiles whose block scales are held: more than the ring holds tiles
+
 template <typename S>
 struct Bars {
-    uint64_t full[S::SLOTS];     // a tile's bytes landed
+    uint64_t full[S::SLOTS];     // a block's bytes landed
     uint64_t empty[S::SLOTS];    // the MMAs that read it completed
+    uint64_t seg_full[kSegs];    // a segment is written
+    uint64_t seg_empty[kSegs];   // the MMA warp and the softmax warps have done with it
+    uint64_t sc_full[kScales];   // a tile's block scales are written
     uint64_t q_full;             // the queries are in shared memory
     uint64_t s_full;             // S^T of a tile is in TMEM
     uint64_t s_free;             // the softmax warps have it in registers
@@ -353,6 +361,7 @@ struct Bars {
     int start_b;
     uint32_t tmem_base;
     int abort;
+    alignas(16) float4 sc[kScales][8];   // (ks, log2 vs, 1 / vs) of a tile's blocks
     alignas(16) float nref[S::RT];    // minus the reference exponent of each row
     alignas(16) float fac[S::RT];     // 2^(old reference - new)
     alignas(16) float qs[S::RT];      // query scale * softmax scale * log2 e
@@ -360,11 +369,7 @@ struct Bars {
     float sum[S::RT];
     int pos[S::RT];                   // position of the row's token; -1: no row
     long long row_at[S::RT];          // its offset in out
-    // the softmax warps' walk, kept here for registers' sake: thread 0 takes the
-    // next segment while the others may still read the last one
-    Walker<S::RT> walk;
-    Segment seg[2];
-    int more[2];
+    Segment seg[kSegs];
 };
 
 template <typename S>
@@ -448,6 +453,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             mbar_init(&bs.full[s], 1);
             mbar_init(&bs.empty[s], 1);
         }
+        for (int k = 0; k < kSegs; ++k) {
+            mbar_init(&bs.seg_full[k], 1);
+            mbar_init(&bs.seg_empty[k], 2);
+        }
+        for (int k = 0; k < kScales; ++k) mbar_init(&bs.sc_full[k], 1);
         mbar_init(&bs.q_full, SOFT / 32);
         mbar_init(&bs.s_full, 1);
         mbar_init(&bs.s_free, SOFT / 32);
@@ -461,27 +471,32 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    w.b = bs.start_b;
-    w.off = bs.start_off;
-    bad = false;
-    w.r = request<RT>(a, w.b, &bad);
     const uint32_t tmem = bs.tmem_base;
     const uint32_t tm_s = tmem, tm_o = tmem + N;
 
     bool ok = true;
-    Segment sg{};
     if (warp == kWarpTma) {
         // ======================================================== TMA
-        uint32_t it = 0;                                   // blocks of 128 dims requested
+        // Also walks the CTA's units and hands its segments on, and brings the block
+        // scales of each token tile (the tile's few blocks, a lane each).
+        Segment sg{};
+        w.b = bs.start_b;
+        w.off = bs.start_off;
+        w.r = request<RT>(a, w.b, &bad);
+        uint32_t it = 0, g = 0;                            // blocks of 128 dims requested, token tiles
+        bool ids_bad = false;
         const int bpt = kTile >> a.bs_log2, bsz = 1 << a.bs_log2;
-        auto load = [&](int tile, bool is_v) -> bool {
-            const int nb = min(bpt, (sg.r.len - tile * kTile + bsz - 1) >> a.bs_log2);
-            int id = 0;
-            if (lane < nb) {
-                id = __ldg(a.table + (size_t)sg.b * a.max_blocks + (size_t)tile * bpt + lane);
-                // an id that is no block reads as zeros (out of the tensor's range)
-                if (id < 0 || id > a.n_blocks) id = a.n_blocks;
-            }
+        auto id_at = [&](int tile) -> int {                // this lane's block of a tile (-1: none there)
+            const int at = tile * bpt + lane;
+            if (lane >= bpt || at * bsz >= sg.len) return -1;
+            const int id = __ldg(a.table + (size_t)sg.b * a.max_blocks + at);
+            // an id that is no block reads as zeros (out of the tensor's range)
+            if (id >= 0 && id < a.n_blocks) return id;
+            ids_bad = true;
+            return a.n_blocks;
+        };
+        auto load = [&](int id, bool is_v) -> bool {
+            const int nb = __popc(__ballot_sync(0xffffffffu, id >= 0));
             for (int d = 0; d < DB; ++d) {
                 const int s = it % S::SLOTS;
                 const bool got = it < S::SLOTS || mbar_wait_abort(&bs.empty[s], ((it / S::SLOTS) + 1) & 1, abort) > 0;
@@ -495,13 +510,48 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
             return true;
         };
-        while (ok && w.next(a, &sg)) {
-            for (int j = 0; ok && j < sg.n; ++j) {
-                ok = load(sg.t0 + j, false);
-                if (!S::SHARED && ok && j > 0) ok = load(sg.t0 + j - 1, true);
+        for (uint32_t k = 0; ok; ++k) {
+            const bool more = w.next(a, &sg);
+            const bool got = k < kSegs || mbar_wait_abort(&bs.seg_empty[k % kSegs], ((k / kSegs) + 1) & 1, abort) > 0;
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
             }
-            if (!S::SHARED && ok && sg.n > 0) ok = load(sg.t0 + sg.n - 1, true);
+            if (!more) {
+                sg.b = -1;
+                sg.n = 0;
+            }
+            if (lane == 0) {
+                bs.seg[k % kSegs] = sg;
+                mbar_arrive(&bs.seg_full[k % kSegs]);
+            }
+            __syncwarp();
+            if (!more) break;
+            int id = sg.n > 0 ? id_at(sg.t0) : -1, id_v = -1;
+            for (int j = 0; ok && j < sg.n; ++j, ++g) {
+                const int id_next = j + 1 < sg.n ? id_at(sg.t0 + j + 1) : -1;
+                float ks = 0.f, vs = 0.f;
+                const bool there = id >= 0 && id < a.n_blocks;
+                if (there) {
+                    const size_t at = (size_t)id * a.kv_heads + sg.h;
+                    ks = __ldg(a.ks + at);
+                    vs = S::SHARED ? ks : __ldg(a.vs + at);
+                }
+                ok = load(id, false);
+                if (!ok) break;
+                // (tile g - kScales was read before the slot just taken came free)
+                if (lane < bpt)
+                    bs.sc[g % kScales][lane] = there ? make_float4(ks, lg2(vs), __fdividef(1.f, vs), 0.f)
+                                                     : make_float4(0.f, -INFINITY, 0.f, 0.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bs.sc_full[g % kScales]);
+                if (!S::SHARED && j > 0) ok = load(id_v, true);
+                id_v = id;
+                id = id_next;
+            }
+            if (!S::SHARED && ok && sg.n > 0) ok = load(id_v, true);
         }
+        if (ids_bad) atomicOr(a.err, kErrBounds);
         if (!ok)   // every copy issued lands before the CTA may leave
             for (uint32_t i = it > S::SLOTS ? it - S::SLOTS : 0; i < it; ++i)
                 mbar_wait(&bs.full[i % S::SLOTS], (i / S::SLOTS) & 1);
@@ -545,12 +595,18 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             if (!S::SHARED) it += DB;
             return true;
         };
-        while (ok && w.next(a, &sg)) {
-            if (sg.n == 0) continue;
+        for (uint32_t k = 0; ok; ++k) {
+            ok = got(&bs.seg_full[k % kSegs], (k / kSegs) & 1);
+            if (!ok) break;
+            const int n = bs.seg[k % kSegs].n;
+            const bool last = bs.seg[k % kSegs].b < 0;
+            warp_arrive(&bs.seg_empty[k % kSegs], lane);
+            if (last) break;
+            if (n == 0) continue;
             ok = got(&bs.q_full, segs & 1);
             ++segs;
             uint32_t k_it = 0;
-            for (int j = 0; ok && j < sg.n; ++j) {
+            for (int j = 0; ok && j < n; ++j) {
                 if (g > 0) ok = got(&bs.s_free, (g - 1) & 1);
                 const uint32_t k_new = it;
 #pragma unroll
@@ -577,7 +633,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 if (j > 0) ok = pv(g - 2, j == 1, k_it);
                 k_it = k_new;
             }
-            if (ok) ok = pv(g - 1, sg.n == 1, k_it);
+            if (ok) ok = pv(g - 1, n == 1, k_it);
         }
         // every MMA issued completes before TMEM is freed
         if (elect_one()) mma_commit(&bs.drain);
@@ -592,119 +648,89 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         unsigned char* qsm = sm + S::kOffQ;
         unsigned char* psm = sm + S::kOffP;
         uint32_t g = 0, it = 0;                            // token tiles, blocks of the ring
-        bool fail = false, ids_bad = false;
+        bool fail = false;
         u64 l2[CT / 2];                                    // sums of p / vs, two rows each
-        if (tid == 0) {
-            bs.walk = w;
-            a.meta[cta] = make_int4(0, 0, 0, 0);           // no split item begins here, so far
-        }
-        for (int turn = 0;; turn ^= 1) {
-            const Segment& sg = bs.seg[turn];
-            if (tid == 0) {
-                const bool more = bs.walk.next(a, &bs.seg[turn]);
-                bs.more[turn] = more;
-                if (more && sg.parts) a.meta[cta] = make_int4(sg.b, sg.h, sg.rt, sg.parts);
+        // queries: a warp per row, 4 values per lane and 128 dims
+        constexpr int W = SOFT / 32, RPW = RT / W;
+        uint2 qx[RPW][DB];
+        auto load_q = [&](const Segment& sg) {
+#pragma unroll
+            for (int i = 0; i < RPW; ++i) {
+                const int r = warp + W * i;
+                const int row = sg.row0 + r, qt = row / a.group, hd = sg.h * a.group + row % a.group;
+                const uint16_t* p = a.q + (size_t)(sg.q0 + qt) * a.q_row + (size_t)hd * (DB * 128) + lane * 4;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    qx[i][d] = r < sg.nr ? __ldg(reinterpret_cast<const uint2*>(p + d * 128)) : make_uint2(0, 0);
             }
-            soft_sync<SOFT>();                             // also: the last segment's shared arrays are read
-            if (!bs.more[turn]) break;
-            const int n = sg.n, len = sg.r.len;
-            // the block id of this thread's token in a tile (-1: no token)
-            auto block_of = [&](int j) -> int {
-                const int t = (sg.t0 + j) * kTile + tok;
-                if (j >= n || t >= len) return -1;
-                return __ldg(a.table + (size_t)sg.b * a.max_blocks + (t >> a.bs_log2));
-            };
-            // block ids run two tiles ahead of their use and scales one, so that
-            // neither load is waited for
-            const int id_0 = block_of(0);
-            int id_1 = block_of(1);
-            const int p_first = len - sg.r.nq;
+        };
+        if (tid == 0) a.meta[cta] = make_int4(0, 0, 0, 0); // no split item begins here, so far
+        if (mbar_wait_abort(&bs.seg_full[0], 0, abort) <= 0) fail = true;
+        else if (bs.seg[0].n > 0) load_q(bs.seg[0]);
+        for (uint32_t k = 0;; ++k) {
+            const Segment& sg = bs.seg[k % kSegs];
+            if (soft_any<SOFT>(fail)) {                    // also: the last segment's shared arrays are read
+                ok = false;
+                break;
+            }
+            if (k > 0 && tid == 0) mbar_arrive(&bs.seg_empty[(k - 1) % kSegs]);
+            if (sg.b < 0) break;
+            const int n = sg.n, len = sg.len;
+            if (tid == 0 && sg.parts) a.meta[cta] = make_int4(sg.b, sg.h, sg.rt, sg.parts);
             if (tid < RT) {
                 const int row = sg.row0 + tid, qt = row / a.group, hd = sg.h * a.group + row % a.group;
                 const bool on = tid < sg.nr;
-                bs.pos[tid] = on ? p_first + qt : -1;
-                bs.row_at[tid] = (long long)(sg.r.q0 + qt) * a.out_row + (long long)hd * (DB * 128);
+                bs.pos[tid] = on ? len - sg.nq + qt : -1;
+                bs.row_at[tid] = (long long)(sg.q0 + qt) * a.out_row + (long long)hd * (DB * 128);
                 // a column without a row is held at weight 0 by a reference out of reach
                 bs.nref[tid] = on ? -kLow : kLow;
             }
             if (n > 0) {
-                // queries: a warp per row, 4 values per lane and 128 dims
-                constexpr int W = SOFT / 32, U = RT / W < 4 ? RT / W : 4;
-                for (int r0 = warp; r0 < RT; r0 += W * U) {
-                    uint2 x[U][DB];
 #pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        const int r = r0 + W * i;
-                        const int row = sg.row0 + r, qt = row / a.group, hd = sg.h * a.group + row % a.group;
-                        const uint16_t* p = a.q + (size_t)(sg.r.q0 + qt) * a.q_row + (size_t)hd * (DB * 128) + lane * 4;
+                for (int i = 0; i < RPW; ++i) {
+                    const int r = warp + W * i;
+                    uint32_t m = 0;
 #pragma unroll
-                        for (int d = 0; d < DB; ++d)
-                            x[i][d] = r < sg.nr ? __ldg(reinterpret_cast<const uint2*>(p + d * 128)) : make_uint2(0, 0);
-                    }
+                    for (int d = 0; d < DB; ++d)
+                        m = max(m, max(max(qx[i][d].x & 0x7fffu, (qx[i][d].x >> 16) & 0x7fffu),
+                                       max(qx[i][d].y & 0x7fffu, (qx[i][d].y >> 16) & 0x7fffu)));
+                    m = __reduce_max_sync(0xffffffffu, m);
+                    const int e = min(max((int)(m >> 7) - 127 - 7, -120), 120);
+                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                    if (lane == 0)   // a row that is not finite has no result: NaN
+                        bs.qs[r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                                : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
 #pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        const int r = r0 + W * i;
-                        uint32_t m = 0;
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-                            m = max(m, max(max(x[i][d].x & 0x7fffu, (x[i][d].x >> 16) & 0x7fffu),
-                                           max(x[i][d].y & 0x7fffu, (x[i][d].y >> 16) & 0x7fffu)));
-                        m = __reduce_max_sync(0xffffffffu, m);
-                        const int e = min(max((int)(m >> 7) - 127 - 7, -120), 120);
-                        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                        if (lane == 0)   // a row that is not finite has no result: NaN
-                            bs.qs[r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)
-                                                    : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            uint32_t hi, lo;
-                            split4(__uint_as_float(x[i][d].x << 16) * inv, __uint_as_float(x[i][d].x & 0xffff0000u) * inv,
-                                   __uint_as_float(x[i][d].y << 16) * inv, __uint_as_float(x[i][d].y & 0xffff0000u) * inv,
-                                   &hi, &lo);
-                            unsigned char* q = qsm + d * (N * 128) + (lane & 3) * 4;
-                            *reinterpret_cast<uint32_t*>(q + sw128(r, lane >> 2)) = hi;
-                            *reinterpret_cast<uint32_t*>(q + sw128(RT + r, lane >> 2)) = lo;
-                        }
+                    for (int d = 0; d < DB; ++d) {
+                        uint32_t hi, lo;
+                        split4(__uint_as_float(qx[i][d].x << 16) * inv, __uint_as_float(qx[i][d].x & 0xffff0000u) * inv,
+                               __uint_as_float(qx[i][d].y << 16) * inv, __uint_as_float(qx[i][d].y & 0xffff0000u) * inv,
+                               &hi, &lo);
+                        unsigned char* q = qsm + d * (N * 128) + (lane & 3) * 4;
+                        *reinterpret_cast<uint32_t*>(q + sw128(r, lane >> 2)) = hi;
+                        *reinterpret_cast<uint32_t*>(q + sw128(RT + r, lane >> 2)) = lo;
                     }
                 }
                 fence_async_smem();
                 warp_arrive(&bs.q_full, lane);
             }
-            float ks_raw = 0.f, vs_raw = 0.f;
-            bool has = id_0 >= 0 && id_0 < a.n_blocks;
-            auto load_scales = [&](int id) {
-                if (id < 0 || id >= a.n_blocks) return;
-                const size_t at = (size_t)id * a.kv_heads + sg.h;
-                ks_raw = __ldg(a.ks + at);
-                vs_raw = S::SHARED ? ks_raw : __ldg(a.vs + at);
-            };
-            load_scales(id_0);
             soft_sync<SOFT>();
 #pragma unroll
             for (int c = 0; c < CT / 2; ++c) l2[c] = 0;
             bool stop = false;
             for (int j = 0; j < n; ++j, ++g) {
                 const int t0 = (sg.t0 + j) * kTile, t = t0 + tok;
-                // this tile's (ks, log2 vs, 1 / vs); (0, -inf, 0) without a token or block
-                float ks = 0.f, lv = -INFINITY, iv = 0.f;
-                if (has) {
-                    ks = ks_raw;
-                    lv = lg2(vs_raw);
-                    iv = __fdividef(1.f, vs_raw);
-                } else if (t < len) {
-                    ids_bad = true;
-                }
-                has = id_1 >= 0 && id_1 < a.n_blocks;
-                load_scales(id_1);
-                id_1 = block_of(j + 2);
-                if (mbar_wait_abort(&bs.s_full, g & 1, abort) <= 0) fail = true;
+                if (mbar_wait_abort(&bs.s_full, g & 1, abort) <= 0 ||
+                    mbar_wait_abort(&bs.sc_full[g % kScales], (g / kScales) & 1, abort) <= 0)
+                    fail = true;
+                const float4 sc = bs.sc[g % kScales][tok >> a.bs_log2];   // (0, -inf, 0) without a block
                 tc_fence_after();
-                constexpr int LD = CT == 32 ? 8 : 16;      // columns per load: what the registers hold beside x and l2
+                constexpr int LD = CT == 32 ? 8 : 16;
                 float x[CT];
                 float most = kLow;
                 const int win = a.window ? a.window : 1 << 30;
                 const bool edge = t0 + kTile - 1 > bs.pos[0] || t0 <= bs.pos[sg.nr - 1] - win;
-                const u64 ks2 = pack(ks, ks), lv2 = pack(lv, lv);
+                const u64 ks2 = pack(sc.x, sc.x), lv2 = pack(sc.y, sc.y);
 #pragma unroll
                 for (int c = 0; c < CT; c += LD) {
                     float hi[LD], lo[LD];
@@ -758,7 +784,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         const float mt = fmaxf(fmaxf(bs.part[0][tid], bs.part[1][tid]), fmaxf(bs.part[2][tid], bs.part[3][tid]));
                         const float was = -bs.nref[tid];
                         float now = was;
-                        if (mt - was > kRoom) now = mt - kHead;
+                        if (mt - was > kHead) now = mt - kHead;     // every row that grew, while at it
                         bs.nref[tid] = -now;
                         bs.fac[tid] = now == was ? 1.f : ex2(was - now);
                     }
@@ -798,7 +824,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         tc_fence_before();
                     }
                 }
-                const u64 iv2 = pack(iv, iv);
+                const u64 iv2 = pack(sc.z, sc.z);
                 // the weights of the last tile have been read
                 if (g > 0 && mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
 #pragma unroll
@@ -841,6 +867,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 break;
             }
             it += n * (S::SHARED ? DB : 2 * DB);
+            // the next segment's queries are asked for before this one's outputs
+            if (mbar_wait_abort(&bs.seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1, abort) <= 0) fail = true;
+            else if (bs.seg[(k + 1) % kSegs].n > 0) load_q(bs.seg[(k + 1) % kSegs]);
             // ---------------------------------------------------- out
             if (n > 0) {
                 float l[CT];
@@ -900,7 +929,6 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
         }
         if (fail) ok = false;
-        if (ids_bad) atomicOr(a.err, kErrBounds);
     }
 
     // ------------------------------------------------------------ teardown
@@ -917,9 +945,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 // ---------------------------------------------------------------- joining split items
 // A task is one row of one split item: its parts' references m_i and sums l_i
 // give weights 2^(m_i - max m); out = sum w_i O_i / sum w_i l_i, in part order.
-// 256 threads: D / 4 threads hold 4 values each, and the parts are shared out
-// among the groups of D / 4.
-constexpr int kJoinThreads = 256;
+// D / 4 threads hold 4 values each, and the parts are shared out among the
+// groups of D / 4.
+constexpr int kJoinThreads = 512;
 constexpr int kMaxParts = 1024;
 
 template <int DB, int RT>
