@@ -591,7 +591,8 @@ typedef struct {
     float* v_scale;
 } kv8_pool;
 
-/* Makes a handle on the current device (scratch of about 40 MB).
+/* Makes a handle on the current device (scratch: 60 MB, or 120 MB with
+ * head_dim 512).
  * Errors: SRH_ERR_INVALID, SRH_ERR_NOMEM, SRH_ERR_CUDA (kv8_last_error(NULL)). */
 int kv8_create(const kv8_config* cfg, kv8_cache** out);
 

@@ -11,29 +11,34 @@
 // kind::f8f6f4 takes 8-bit operands on both sides. A query row is scaled by a
 // power of two to a largest magnitude in [128, 256) and split into two e4m3
 // terms, hi = e4m3(q), lo = e4m3(q - hi): 4 + 4 significant bits, which is bf16
-// exactly (below 2^-9 of the row's largest the absolute error is 2^-17 of it).
-// Weights are split the same way. The two terms are two columns of one MMA (N =
-// 2 * rows), so a tile is read from shared memory once for both.
+// exactly. Weights are split the same way. The two terms are two columns of one
+// MMA (N = 2 * rows), so a tile is read from shared memory once for both; having
+// columns of its own, the second term is held 16 times larger, which takes
+// e4m3's smallest steps 16 times further down.
 //
 // Block scales: ks multiplies the score, one factor per thread (thread = TMEM
 // lane = token). vs goes into the exponent: u = s + log2(vs), p = 2^(u - ref), so
 // the column p holds what the token contributes, and the rounding of p is
 // relative to the largest contribution; the softmax sum takes p / vs in fp32.
 //
-// The running reference `ref` of a row is set 2^5 below its maximum, and is
-// moved only when a weight would pass 2^8.75 (e4m3 ends at 448): one vote of the
-// softmax threads per tile; the maximum itself, the rescaling of the sums and
-// of O^T in TMEM only happen when the vote says so (the first tile, then the
-// more rarely the more tokens a row has seen). Weights down to 2^-10 keep
-// half a step of e4m3's smallest, 2^-15 of the row's largest.
+// The running reference of a row is set so that its maximum's weight is 2 (2^5
+// where the second terms are not scaled), and is moved only when a weight
+// would pass 2^8.75 (e4m3 ends at 448): one vote of the softmax threads per tile;
+// the maximum itself, the rescaling of the sums and of O^T in TMEM only happen
+// when the vote says so (the first tile, then the more rarely the more tokens a
+// row has seen). The smallest half step is 2^-15 of the row's largest weight.
 //
 // Work: a "row tile" is RT of the (token, head) rows that share a KV head of a
 // request; its tokens are cut into tiles of 128. Every (request, KV head, row
-// tile, token tile) is a unit; CTA i of n takes units [i U / n, (i + 1) U / n),
-// found from the lengths on the device, so ragged batches and single long
-// requests both fill the SMs and nothing depends on host knowledge of lengths.
-// An item whose units fall to several CTAs leaves fp32 partial sums, which a
-// second kernel joins in order (no atomics: results repeat bit for bit).
+// tile, token tile) is a unit. The U units, counted from the lengths on the
+// device, are cut into chunks of equal numbers: 12/16 of them into one chunk
+// per CTA, 3/16 and 1/16 into as many smaller ones that CTAs take as they come
+// free (SMs run at different speeds: with one chunk each, the last CTA of a
+// bandwidth-bound batch ended 8 % after the average, of a prompt chunk 45 %). So ragged
+// batches and single long requests both fill the SMs, and nothing depends on
+// host knowledge of lengths. An item whose units fall into several chunks leaves
+// fp32 partial sums, which a second kernel joins in chunk order: who ran a
+// chunk does not show, and results repeat bit for bit.
 //
 // Roles: 4 to 16 softmax warps (a thread holds one token and 16 or 32 rows;
 // they also bring queries in and outputs out), one TMA warp (one box per block
@@ -56,8 +61,12 @@ using namespace umma;
 constexpr int kTile = 128;               // tokens per tile
 constexpr int kSlotBytes = kTile * 128;  // 128 tokens x 128 dims
 constexpr float kLow = -1e30f;           // reference of a row that has seen no token
-constexpr float kHead = 5.f;             // the reference is set 2^5 below the maximum ...
-constexpr float kRoom = 8.75f;           // ... and moves when a weight would pass 2^8.75 = 431
+constexpr float kRoom = 8.75f;           // a row's reference moves when a weight would pass 2^8.75 = 431
+constexpr float kLoScale = 16.f;         // factor of a second term that has columns of its own
+
+// Rounds of chunks and where they begin, in sixteenths of the units.
+constexpr int kRounds = 3;
+__device__ __forceinline__ int cut(int r) { return r == 0 ? 0 : r == 1 ? 12 : r == 2 ? 15 : 16; }
 
 // DB: head_dim / 128. RT: rows per row tile. SHARED: V = K.
 template <int DB_, int RT_, bool SHARED_>
@@ -68,6 +77,9 @@ struct Shape {
     // O^T's hi and lo columns stay apart where TMEM has room for both
     static constexpr bool CAT = DB * N + N <= 512;
     static constexpr int ON = CAT ? N : RT;                // O^T columns per 128 dims
+    // weights of a row's maximum: where the second terms are scaled by 16, 2^-10 / 16
+    // is the smallest half step, else 2^-10; either way 2^-15 of the maximum
+    static constexpr float HEAD = CAT ? 1.f : 5.f;
     static constexpr int COLS = N + DB * ON;
     static constexpr int ALLOC = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static constexpr int kQBytes = DB * N * 128;
@@ -100,6 +112,7 @@ struct Args {
     float* part_o;
     float* part_ml;
     int4* meta;
+    int* ctrl;                                   // [0] chunks handed out, [1] chunks of this call
     uint32_t* err;
     int n_req, n_rows, heads, kv_heads, group;   // group = heads / kv_heads
     int bs_log2, n_blocks, max_blocks;
@@ -119,7 +132,11 @@ struct Request {
 template <int RT>
 __device__ __forceinline__ int tiles_of(const Args& a, const Request& r, int rt, int* first) {
     const int c = r.len - r.nq;                                    // position of the first query
-    const int p_lo = c + rt * RT / a.group, p_hi = c + min(r.nq - 1, ((rt + 1) * RT - 1) / a.group);
+    int p_lo = c, p_hi = c + r.nq - 1;
+    if (r.nrt > 1) {
+        p_lo = c + rt * RT / a.group;
+        p_hi = c + min(r.nq - 1, ((rt + 1) * RT - 1) / a.group);
+    }
     *first = a.window ? max(0, p_lo - a.window + 1) / kTile : 0;
     return max(0, (p_hi < 0 ? 0 : p_hi / kTile + 1) - *first);
 }
@@ -153,25 +170,48 @@ __device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
     return r;
 }
 __device__ __forceinline__ long long units(const Args& a, const Request& r) {
-    return (long long)r.pairs * a.kv_heads * r.P;
+    return (long long)r.pairs * r.P * a.kv_heads;
 }
 
-// One CTA's share of one item (a row tile of a KV head of a request).
+// A chunk's share of one item (a row tile of a KV head of a request).
 struct Segment {
-    int b, h, rt;
+    int b, h;            // b < 0: no more segments
     int row0, nr;        // rows of the row tile in the request's (token, head) order
     int t0, n;           // first token tile and tiles to run (0: no row sees any)
     int slot;            // -1: the whole item; else the partial's slot
-    int parts;           // CTAs of the item, when it begins here and goes on
     int q0, nq, len;     // the request's first row, rows and tokens
 };
 
-// Walks the units [u, u1) that a CTA owns. Every role walks on its own.
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The chunks of U units for n CTAs: `rounds` rounds of n chunks.
+struct Chunks {
+    long long U;
+    int n, rounds;
+    __device__ __forceinline__ long long round_begin(int r) const { return rounds == 1 ? (r ? U : 0) : U * cut(r) / 16; }
+    __device__ __forceinline__ long long begin(int v) const {    // first unit of chunk v (v = n * rounds: U)
+        const int r = v / n, i = v - r * n;
+        if (r >= rounds) return U;
+        const long long s = round_begin(r);
+        return s + div_ll((round_begin(r + 1) - s) * i, n);
+    }
+    __device__ __forceinline__ int of(long long u) const {       // the chunk that holds unit u
+        int r = 0;
+        while (r + 1 < rounds && u >= round_begin(r + 1)) ++r;
+        const long long s = round_begin(r);
+        return r * n + (int)div_ll((u - s + 1) * n - 1, round_begin(r + 1) - s);
+    }
+};
+
+// Walks the units [u, u1) of chunk v; u is unit `off` of request b.
 template <int RT>
 struct Walker {
-    long long u, u1, U;
-    long long off;       // u's place in request b
-    int b, n_cta, cta;
+    Chunks ch;
+    long long u, u1;
+    long long off;
+    int b, v;
     Request r;
 
     __device__ __forceinline__ bool next(const Args& a, Segment* s) {
@@ -182,9 +222,9 @@ struct Walker {
                 r = request<RT>(a, ++b, &bad);
             }
             const long long head = (long long)r.pairs * r.P;
-            const int h = (int)(off / head);
+            const int h = (int)div_ll(off, head);
             const long long in = off - h * head;
-            const int k = (int)(in / r.P), o = (int)(in - (long long)k * r.P);
+            const int k = (int)div_ll(in, r.P), o = (int)(in - (long long)k * r.P);
             // the later row tile of the pair first, then the earlier, then nothing
             const int big = r.nrt - 1 - k, nb = units_of<RT>(a, r, big);
             int rt = big, at = o, n = nb;
@@ -202,7 +242,6 @@ struct Walker {
             const int take = (int)min((long long)(n - at), u1 - u);
             s->b = b;
             s->h = h;
-            s->rt = rt;
             s->row0 = rt * RT;
             s->nr = min(RT, r.nq * a.group - s->row0);
             s->q0 = r.q0;
@@ -213,11 +252,10 @@ struct Walker {
             s->t0 = first + at;
             s->n = min(take, max(0, tiles - at));
             s->slot = -1;
-            s->parts = 0;
             if (take != n) {
-                s->slot = 2 * cta + (at == 0);
-                if (at == 0)                                       // the CTA of the item's last unit
-                    s->parts = (int)(((u + n) * n_cta - 1) / U) - cta + 1;
+                s->slot = 2 * v + (at == 0);
+                if (at == 0)       // the item goes on in the next chunks: for the join
+                    a.meta[v] = make_int4((ch.of(u + n - 1) - v + 1) | (s->nr << 16), r.q0, s->row0, h);
             }
             u += take;
             off += take;
@@ -327,13 +365,19 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
     const uint32_t x = PITCH == 128 ? (r & 7u) : PITCH == 64 ? ((r >> 1) & 3u) : ((r >> 2) & 1u);
     return r * PITCH + ((c ^ x) << 4);
 }
-// Two e4m3 terms of each of four values: hi and lo codes, one byte each.
+// Two e4m3 terms of each of four values, a byte each; the second times 16 if SCALED.
+template <bool SCALED>
 __device__ __forceinline__ void split4(float v0, float v1, float v2, float v3, uint32_t* hi, uint32_t* lo) {
     const __half2 a = __floats2half2_rn(v0, v1), b = __floats2half2_rn(v2, v3);
     const uint32_t ha = __nv_cvt_halfraw2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
     const uint32_t hb = __nv_cvt_halfraw2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
-    const __half2 ra = __hsub2(a, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ha, __NV_E4M3)));
-    const __half2 rb = __hsub2(b, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hb, __NV_E4M3)));
+    __half2 ra = __hsub2(a, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ha, __NV_E4M3)));
+    __half2 rb = __hsub2(b, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hb, __NV_E4M3)));
+    if (SCALED) {
+        const __half2 f = __float2half2_rn(kLoScale);
+        ra = __hmul2(ra, f);
+        rb = __hmul2(rb, f);
+    }
     const uint32_t la = __nv_cvt_halfraw2_to_fp8x2(ra, __NV_SATFINITE, __NV_E4M3);
     const uint32_t lb = __nv_cvt_halfraw2_to_fp8x2(rb, __NV_SATFINITE, __NV_E4M3);
     *hi = ha | (hb << 16);
@@ -357,8 +401,7 @@ struct Bars {
     uint64_t pv_done;            // PV completed
     uint64_t drain;
     long long warp_sums[33];
-    long long start_off;
-    int start_b;
+    long long before[S::THREADS];     // units before each thread's requests
     uint32_t tmem_base;
     int abort;
     alignas(16) float4 sc[kScales][8];   // (ks, log2 vs, 1 / vs) of a tile's blocks
@@ -414,38 +457,21 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n_grid = gridDim.x, cta = blockIdx.x;
 
-    // ------------------------------------------------------------ this CTA's units
-    Walker<RT> w;
+    // ------------------------------------------------------------ the units
+    Chunks ch;
+    const int per = (a.n_req + S::THREADS - 1) / S::THREADS;       // requests per thread (at most 22)
     bool bad = false;
     {
-        const int per = (a.n_req + S::THREADS - 1) / S::THREADS;
         const int b0 = min(a.n_req, tid * per), b1 = min(a.n_req, b0 + per);
         long long mine = 0;
         for (int b = b0; b < b1; ++b) mine += units(a, request<RT>(a, b, &bad));
-        long long U;
-        const long long incl = block_scan(mine, bs.warp_sums, &U);
-        const int n = (int)min((long long)n_grid, U);
-        if (cta >= n) {                                    // nothing to do (every thread)
-            if (tid == 0) a.meta[cta] = make_int4(0, 0, 0, 0);
-            return;
-        }
-        w.U = U;
-        w.n_cta = n;
-        w.cta = cta;
-        w.u = U * cta / n;
-        w.u1 = U * (cta + 1) / n;
-        long long at = incl - mine;
-        if (w.u >= at && w.u < incl) {
-            for (int b = b0;; ++b) {
-                const long long k = units(a, request<RT>(a, b, &bad));
-                if (w.u < at + k) {
-                    bs.start_b = b;
-                    bs.start_off = w.u - at;
-                    break;
-                }
-                at += k;
-            }
-        }
+        const long long incl = block_scan(mine, bs.warp_sums, &ch.U);
+        ch.n = (int)min((long long)n_grid, ch.U);
+        // rounds of smaller chunks only where each still has units
+        ch.rounds = ch.U >= 16ll * ch.n ? kRounds : 1;
+        if (cta == 0 && tid == 0) a.ctrl[1] = ch.n * ch.rounds;
+        if (cta >= ch.n) return;                           // nothing to do (every thread)
+        bs.before[tid] = incl - mine;
     }
     if (cta == 0 && bad) atomicOr(a.err, kErrBounds);
     if (tid == 0) {
@@ -480,9 +506,37 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // Also walks the CTA's units and hands its segments on, and brings the block
         // scales of each token tile (the tile's few blocks, a lane each).
         Segment sg{};
-        w.b = bs.start_b;
-        w.off = bs.start_off;
-        w.r = request<RT>(a, w.b, &bad);
+        Walker<RT> w;
+        w.ch = ch;
+        // to the first unit of chunk v
+        auto seek = [&](int v) {
+            w.v = v;
+            w.u = ch.begin(v);
+            w.u1 = ch.begin(v + 1);
+            int lo = 0, hi = S::THREADS;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (bs.before[mid] <= w.u) lo = mid;
+                else hi = mid;
+            }
+            // the last thread at or below u owns it (those after it with nothing have the same sum: the
+            // search ends at the last of them, whose requests, if any, begin at u)
+            const int b0 = lo * per, b = b0 + lane;
+            long long k = lane < per && b < a.n_req ? units(a, request<RT>(a, b, &bad)) : 0, incl = k;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            const long long rel = w.u - bs.before[lo];
+            const int mine = __ffs(__ballot_sync(0xffffffffu, rel < incl)) - 1;
+            w.b = b0 + mine;
+            w.off = rel - __shfl_sync(0xffffffffu, incl - k, mine);
+            w.r = request<RT>(a, w.b, &bad);
+            if (lane == 0) a.meta[v] = make_int4(0, 0, 0, 0);      // no item goes on from this chunk, so far
+            __syncwarp();
+        };
+        seek(cta);
         uint32_t it = 0, g = 0;                            // blocks of 128 dims requested, token tiles
         bool ids_bad = false;
         const int bpt = kTile >> a.bs_log2, bsz = 1 << a.bs_log2;
@@ -511,7 +565,15 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             return true;
         };
         for (uint32_t k = 0; ok; ++k) {
-            const bool more = w.next(a, &sg);
+            bool more = w.next(a, &sg);
+            while (!more && ch.rounds > 1) {               // the next chunk that nobody has
+                int v = 0;
+                if (lane == 0) v = ch.n + atomicAdd(a.ctrl, 1);
+                v = __shfl_sync(0xffffffffu, v, 0);
+                if (v >= ch.n * ch.rounds) break;
+                seek(v);
+                more = w.next(a, &sg);
+            }
             const bool got = k < kSegs || mbar_wait_abort(&bs.seg_empty[k % kSegs], ((k / kSegs) + 1) & 1, abort) > 0;
             if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
@@ -664,7 +726,6 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     qx[i][d] = r < sg.nr ? __ldg(reinterpret_cast<const uint2*>(p + d * 128)) : make_uint2(0, 0);
             }
         };
-        if (tid == 0) a.meta[cta] = make_int4(0, 0, 0, 0); // no split item begins here, so far
         if (mbar_wait_abort(&bs.seg_full[0], 0, abort) <= 0) fail = true;
         else if (bs.seg[0].n > 0) load_q(bs.seg[0]);
         for (uint32_t k = 0;; ++k) {
@@ -676,7 +737,6 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             if (k > 0 && tid == 0) mbar_arrive(&bs.seg_empty[(k - 1) % kSegs]);
             if (sg.b < 0) break;
             const int n = sg.n, len = sg.len;
-            if (tid == 0 && sg.parts) a.meta[cta] = make_int4(sg.b, sg.h, sg.rt, sg.parts);
             if (tid < RT) {
                 const int row = sg.row0 + tid, qt = row / a.group, hd = sg.h * a.group + row % a.group;
                 const bool on = tid < sg.nr;
@@ -703,7 +763,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                     for (int d = 0; d < DB; ++d) {
                         uint32_t hi, lo;
-                        split4(__uint_as_float(qx[i][d].x << 16) * inv, __uint_as_float(qx[i][d].x & 0xffff0000u) * inv,
+                        split4<true>(__uint_as_float(qx[i][d].x << 16) * inv, __uint_as_float(qx[i][d].x & 0xffff0000u) * inv,
                                __uint_as_float(qx[i][d].y << 16) * inv, __uint_as_float(qx[i][d].y & 0xffff0000u) * inv,
                                &hi, &lo);
                         unsigned char* q = qsm + d * (N * 128) + (lane & 3) * 4;
@@ -730,7 +790,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 float most = kLow;
                 const int win = a.window ? a.window : 1 << 30;
                 const bool edge = t0 + kTile - 1 > bs.pos[0] || t0 <= bs.pos[sg.nr - 1] - win;
-                const u64 ks2 = pack(sc.x, sc.x), lv2 = pack(sc.y, sc.y);
+                const u64 ks2 = pack(sc.x, sc.x), lv2 = pack(sc.y, sc.y), lo_f = pack(1.f / kLoScale, 1.f / kLoScale);
 #pragma unroll
                 for (int c = 0; c < CT; c += LD) {
                     float hi[LD], lo[LD];
@@ -746,8 +806,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                     for (int i = 0; i < LD; i += 4) {
                         const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(&bs.qs[col0 + c + i]);
-                        const u64 a0 = fma2(mul2(add2(pack(hi[i], hi[i + 1]), pack(lo[i], lo[i + 1])), s4.x), ks2, lv2);
-                        const u64 a1 = fma2(mul2(add2(pack(hi[i + 2], hi[i + 3]), pack(lo[i + 2], lo[i + 3])), s4.y), ks2, lv2);
+                        const u64 a0 = fma2(mul2(fma2(pack(lo[i], lo[i + 1]), lo_f, pack(hi[i], hi[i + 1])), s4.x), ks2, lv2);
+                        const u64 a1 = fma2(mul2(fma2(pack(lo[i + 2], lo[i + 3]), lo_f, pack(hi[i + 2], hi[i + 3])), s4.y), ks2, lv2);
                         unpack(a0, x[c + i], x[c + i + 1]);
                         unpack(a1, x[c + i + 2], x[c + i + 3]);
                     }
@@ -784,7 +844,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         const float mt = fmaxf(fmaxf(bs.part[0][tid], bs.part[1][tid]), fmaxf(bs.part[2][tid], bs.part[3][tid]));
                         const float was = -bs.nref[tid];
                         float now = was;
-                        if (mt - was > kHead) now = mt - kHead;     // every row that grew, while at it
+                        if (mt - was > S::HEAD) now = mt - S::HEAD;     // every row that grew, while at it
                         bs.nref[tid] = -now;
                         bs.fac[tid] = now == was ? 1.f : ex2(was - now);
                     }
@@ -839,7 +899,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         const float v0 = ex2(y0), v1 = ex2(y1), v2 = ex2(y2), v3 = ex2(y3);
                         l2[(c + i) / 2] = fma2(pack(v0, v1), iv2, l2[(c + i) / 2]);
                         l2[(c + i) / 2 + 1] = fma2(pack(v2, v3), iv2, l2[(c + i) / 2 + 1]);
-                        split4(v0, v1, v2, v3, &hi[i / 4], &lo[i / 4]);
+                        split4<S::CAT>(v0, v1, v2, v3, &hi[i / 4], &lo[i / 4]);
                     }
                     const int ch = (col0 + c) / 16;
                     unsigned char* ph = psm + chunk_at<S::kPitch>(tok, ch);
@@ -880,48 +940,57 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 tc_fence_after();
             }
             soft_sync<SOFT>();
+            const int slot = sg.slot, nr = sg.nr;
             if (tid < RT) {
                 const float sum = n > 0 ? (bs.part[0][tid] + bs.part[1][tid]) + (bs.part[2][tid] + bs.part[3][tid]) : 0.f;
-                bs.sum[tid] = sg.slot >= 0 ? sum : sum == 0.f ? 0.f : 1.f / sum;
-                if (sg.slot >= 0)
-                    reinterpret_cast<float2*>(a.part_ml)[(size_t)sg.slot * RT + tid] = make_float2(-bs.nref[tid], sum);
+                bs.sum[tid] = sum == 0.f ? 0.f : 1.f / sum;
+                if (slot >= 0)
+                    reinterpret_cast<float2*>(a.part_ml)[(size_t)slot * RT + tid] = make_float2(-bs.nref[tid], sum);
             }
             soft_sync<SOFT>();
-            if (n > 0 || sg.slot < 0) {
+            // (a part without tiles has the sum 0, by which the join leaves it out)
+            if (n > 0 || slot < 0) {
 #pragma unroll
-                for (int c = 0; c < CT; c += 16) {
-                    if (col0 + c >= sg.nr) break;
+                for (int c = 0; c < CT; c += 8) {
+                    const int rows = min(8, nr - col0 - c);
+                    if (rows <= 0) break;
+                    float inv[8];
+                    uint16_t* at[8];
 #pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        inv[i] = bs.sum[col0 + c + i];
+                        at[i] = a.out + bs.row_at[col0 + c + i] + tok;
+                    }
+                    float* po = a.part_o + ((size_t)max(slot, 0) * RT + col0 + c) * (DB * 128) + tok;
+#pragma unroll 1
                     for (int mb = 0; mb < DB; ++mb) {
-                        float o[16];
-                        if (n > 0) {
-                            tmem_ld16(my_o + mb * S::ON + c, o);
-                            if (S::CAT) {
-                                float o2[16];
-                                tmem_ld16(my_o + mb * S::ON + RT + c, o2);
-                                tmem_ld_wait();
-                                tmem_regs_ready(o);
-                                tmem_regs_ready(o2);
+                        float o[8];
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] += o2[i];
+                        for (int i = 0; i < 8; ++i) o[i] = 0.f;
+                        if (n > 0) {
+                            tmem_ld<8>(my_o + mb * S::ON + c, o);
+                            if (S::CAT) {
+                                float o2[8];
+                                tmem_ld<8>(my_o + mb * S::ON + RT + c, o2);
+                                tmem_ld_wait();
+                                tmem_regs_ready_n<8>(o);
+                                tmem_regs_ready_n<8>(o2);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] = fmaf(o2[i], 1.f / kLoScale, o[i]);
                             } else {
                                 tmem_ld_wait();
-                                tmem_regs_ready(o);
+                                tmem_regs_ready_n<8>(o);
                             }
+                        }
+                        if (slot < 0) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (i < rows)
+                                    at[i][mb * 128] = __bfloat16_as_ushort(__float2bfloat16_rn(inv[i] == 0.f ? 0.f : o[i] * inv[i]));
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int r = col0 + c + i;
-                            if (r >= sg.nr) break;
-                            if (sg.slot < 0) {
-                                const __nv_bfloat16 v = __float2bfloat16_rn(bs.sum[r] == 0.f ? 0.f : o[i] * bs.sum[r]);
-                                a.out[bs.row_at[r] + mb * 128 + tok] = __bfloat16_as_ushort(v);
-                            } else {
-                                a.part_o[(((size_t)sg.slot * RT + r) * DB + mb) * 128 + tok] = o[i];
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                if (i < rows) po[i * (DB * 128) + mb * 128] = o[i];
                         }
                     }
                 }
@@ -943,108 +1012,128 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- joining split items
-// A task is one row of one split item: its parts' references m_i and sums l_i
-// give weights 2^(m_i - max m); out = sum w_i O_i / sum w_i l_i, in part order.
-// D / 4 threads hold 4 values each, and the parts are shared out among the
-// groups of D / 4.
-constexpr int kJoinThreads = 512;
-constexpr int kMaxParts = 1024;
+// Row r of a split item: its parts' references m_i and sums l_i give weights
+// 2^(m_i - max m); out = sum w_i O_i / sum w_i l_i, in part order. A job is 128
+// dims of one row: 4 per lane of a warp. Items of few parts give a warp a job
+// each; of an item of many (one long request), a CTA's 8 warps share a job's
+// parts and add up in warp order. Latency-bound: a chain of three loads.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kFewParts = 12;
+constexpr int kMaxChunks = 1024;
 
-template <int DB, int RT>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int n_cta) {
-    constexpr int VT = DB * 32;                       // threads per part
-    constexpr int PG = kJoinThreads / VT;             // parts at a time
-    __shared__ long long warp_sums[33];
-    __shared__ int items[kMaxParts];                  // CTAs that begin a split item
-    __shared__ float wt[kMaxParts];
-    __shared__ float red[kJoinThreads / 32];
-    __shared__ float4 acc_s[PG > 1 ? kJoinThreads : 1];
-    const int tid = threadIdx.x;
-    pdl_wait();
-    // every CTA lists the split items (at most one per attention CTA)
-    int n_items = 0;
-    for (int base = 0; base < n_cta; base += kJoinThreads) {
-        const int i = base + tid;
-        const bool on = i < n_cta && a.meta[i].w > 0;
-        long long total;
-        const long long incl = block_scan(on, warp_sums, &total);
-        if (on) items[n_items + (int)incl - 1] = i;
-        n_items += (int)total;
-    }
-    __syncthreads();
-    for (int task = blockIdx.x; task < n_items * RT; task += gridDim.x) {
-        const int c0 = items[task / RT], row = task % RT;
-        const int4 it = a.meta[c0];                   // request, KV head, row tile, parts
-        bool bad = false;
-        const Request r = request<RT>(a, it.x, &bad);
-        const int rr = it.z * RT + row;
-        if (rr >= r.nq * a.group) continue;           // uniform
-        const int parts = it.w;
-        const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-        // part i's slot: the first CTA's trailing segment, the others' leading one
-        auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)); };
-        float m = kLow;
-        for (int i = tid; i < parts; i += kJoinThreads) {
-            const float2 v = __ldcg(&ml[slot(i) * RT + row]);
-            if (v.y != 0.f) m = fmaxf(m, v.x);
+// Weighted sum of parts [p0, p1) for 4 dims per lane; every lane gets sum w_i l_i.
+template <int RT>
+__device__ __forceinline__ float4 join_parts(const Args& a, int v0, int parts, int row, int dims, int d, int p0, int p1,
+                                             float m, float* sum_out) {
+    const int lane = threadIdx.x & 31;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+    // part i's slot: the first chunk's trailing segment, the others' leading one
+    auto slot = [&](int i) { return (size_t)(2 * (v0 + i) + (i == 0)); };
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int base = p0; base < p1; base += 32) {
+        float w = 0.f;
+        if (base + lane < p1) {
+            const float2 v = __ldcg(&ml[slot(base + lane) * RT + row]);
+            if (v.y != 0.f) {                              // a part with no weight is not read
+                w = ex2(v.x - m);
+                sum = fmaf(w, v.y, sum);
+            }
         }
-        m = warp_max(m);
-        if ((tid & 31) == 0) red[tid >> 5] = m;
-        __syncthreads();
-        m = red[0];
-#pragma unroll
-        for (int i = 1; i < kJoinThreads / 32; ++i) m = fmaxf(m, red[i]);
-        __syncthreads();
-        float sum = 0.f;
-        for (int i = tid; i < parts; i += kJoinThreads) {
-            const float2 v = __ldcg(&ml[slot(i) * RT + row]);
-            const float f = v.y != 0.f ? ex2(v.x - m) : 0.f;    // a part with no weight is not read
-            wt[i] = f;
-            if (v.y != 0.f) sum = fmaf(f, v.y, sum);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if ((tid & 31) == 0) red[tid >> 5] = sum;
-        __syncthreads();
-        sum = red[0];
-#pragma unroll
-        for (int i = 1; i < kJoinThreads / 32; ++i) sum += red[i];
-        const int v = tid % VT, pg = tid / VT;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = pg; i < parts; i += PG) {
-            const float f = wt[i];
+        const int n = min(32, p1 - base);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float f = __shfl_sync(0xffffffffu, w, i);
             if (f == 0.f) continue;
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * RT + row) * (DB * 128)) + v);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(base + i) * RT + row) * dims + d) + lane);
             acc.x = fmaf(f, o.x, acc.x);
             acc.y = fmaf(f, o.y, acc.y);
             acc.z = fmaf(f, o.z, acc.z);
             acc.w = fmaf(f, o.w, acc.w);
         }
-        if (PG > 1) {
-            acc_s[tid] = acc;
-            __syncthreads();
-            if (pg == 0)
+    }
 #pragma unroll
-                for (int i = 1; i < PG; ++i) {
-                    const float4 o = acc_s[i * VT + v];
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    *sum_out = sum;
+    return acc;
+}
+
+template <int DB, int RT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
+    __shared__ long long warp_sums[33];
+    __shared__ int4 item[kMaxChunks];                 // split items: (parts | rows << 16, first row of out, row, head)
+    __shared__ int chunk[kMaxChunks];                 // the chunk each begins in
+    __shared__ int first[kMaxChunks + 1];             // CTA jobs before each
+    __shared__ float4 acc_s[kJoinWarps][32];
+    __shared__ float sum_s[kJoinWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
+    const int n_chunks = min(a.ctrl[1], kMaxChunks);
+    if (blockIdx.x == 0 && tid == 0) a.ctrl[0] = 0;   // for the next call
+    int n_items = 0, n_jobs = 0;
+    for (int base = 0; base < n_chunks; base += kJoinThreads) {
+        const int i = base + tid;
+        int4 it = i < n_chunks ? __ldcg(&a.meta[i]) : make_int4(0, 0, 0, 0);
+        const int parts = it.x & 0xffff, jobs = (it.x >> 16) * DB;
+        const int cta_jobs = parts <= kFewParts ? (jobs + kJoinWarps - 1) / kJoinWarps : jobs;
+        // items in the high half, jobs in the low one
+        long long total;
+        const long long incl = block_scan(parts ? (1ll << 32) + cta_jobs : 0, warp_sums, &total);
+        if (parts) {
+            const int k = n_items + (int)(incl >> 32) - 1;
+            item[k] = it;
+            chunk[k] = i;
+            first[k] = n_jobs + (int)(incl & 0xffffffff) - cta_jobs;
+        }
+        n_items += (int)(total >> 32);
+        n_jobs += (int)(total & 0xffffffff);
+    }
+    __syncthreads();
+    for (int job = blockIdx.x; job < n_jobs; job += gridDim.x) {
+        const int k = last_not_above(first, n_items, job);
+        const int4 it = item[k];
+        const int parts = it.x & 0xffff, nr = it.x >> 16, v0 = chunk[k];
+        const bool shared_job = parts > kFewParts;
+        const int j = shared_job ? job - first[k] : (job - first[k]) * kJoinWarps + warp;
+        if (j >= nr * DB) continue;                   // a warp without a job (never in a shared one)
+        const int row = j / DB, d = (j - row * DB) * 128;
+        float m = kLow;
+        for (int i = lane; i < parts; i += 32) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + (size_t)(2 * (v0 + i) + (i == 0)) * RT + row);
+            if (v.y != 0.f) m = fmaxf(m, v.x);
+        }
+        m = warp_max(m);
+        const int p0 = shared_job ? parts * warp / kJoinWarps : 0;
+        const int p1 = shared_job ? parts * (warp + 1) / kJoinWarps : parts;
+        float sum;
+        float4 acc = join_parts<RT>(a, v0, parts, row, DB * 128, d, p0, p1, m, &sum);
+        if (shared_job) {
+            acc_s[warp][lane] = acc;
+            if (lane == 0) sum_s[warp] = sum;
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int i = 1; i < kJoinWarps; ++i) {
+                    const float4 o = acc_s[i][lane];
                     acc.x += o.x;
                     acc.y += o.y;
                     acc.z += o.z;
                     acc.w += o.w;
+                    sum += sum_s[i];
                 }
+            }
+            __syncthreads();
+            if (warp) continue;
         }
-        if (pg == 0) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            const int tok = rr / a.group, hd = it.y * a.group + rr % a.group;
-            uint2 o;
-            memcpy(&o.x, &lo, 4);
-            memcpy(&o.y, &hi, 4);
-            *reinterpret_cast<uint2*>(a.out + (size_t)(r.q0 + tok) * a.out_row + (size_t)hd * (DB * 128) + v * 4) = o;
-        }
-        __syncthreads();
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        const int rr = it.z + row, tok = rr / a.group, hd = it.w * a.group + rr % a.group;
+        uint2 o;
+        memcpy(&o.x, &lo, 4);
+        memcpy(&o.y, &hi, 4);
+        *reinterpret_cast<uint2*>(a.out + (size_t)(it.y + tok) * a.out_row + (size_t)hd * (DB * 128) + d + lane * 4) = o;
     }
 }
 
@@ -1085,13 +1174,14 @@ template <typename S>
 cudaError_t run(const Cache& c, const CUtensorMap& km, const CUtensorMap& vm, const Args& a, cudaStream_t st) {
     const int grid = S::CTAS * c.sm_count;
     static_assert(S::CTAS * smem_bytes<S>() <= 232448 + (S::CTAS - 1) * 1024, "the CTAs of an SM must fit its shared memory");
-    if ((size_t)grid * 2 * S::RT * S::DB * 128 > c.part_o_floats || (size_t)grid * 4 * S::RT > c.part_ml_floats ||
-        (size_t)grid > c.meta_n || grid > kMaxParts)
+    const size_t chunks = (size_t)grid * kRounds;
+    if (chunks * 2 * S::RT * S::DB * 128 > c.part_o_floats || chunks * 4 * S::RT > c.part_ml_floats || chunks > c.meta_n ||
+        chunks > kMaxChunks)
         return cudaErrorInvalidValue;
     attend_kernel<S><<<grid, S::THREADS, smem_bytes<S>(), st>>>(km, vm, a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_k(join_kernel<S::DB, S::RT>, dim3((unsigned)(2 * c.sm_count)), dim3(kJoinThreads), 0, st, true, a, grid);
+    return launch_k(join_kernel<S::DB, S::RT>, dim3((unsigned)(4 * c.sm_count)), dim3(kJoinThreads), 0, st, true, a);
 }
 
 template <int DB, bool SHARED>
@@ -1128,9 +1218,10 @@ cudaError_t set_attend_attrs() {
 
 void attend_scratch(int sm_count, int head_dim, size_t* o_floats, size_t* ml_floats, size_t* meta) {
     const size_t grid = (size_t)sm_count * (head_dim <= 256 ? 2 : 1);   // CTAs of the widest grid
-    *o_floats = grid * 2 * 64 * head_dim;
-    *ml_floats = grid * 4 * 64;
-    *meta = grid;
+    const size_t slots = grid * kRounds * 2;
+    *o_floats = slots * 64 * head_dim / (head_dim == 256 ? 2 : 1);   // 64 rows run one CTA per SM there
+    *ml_floats = slots * 2 * 64;
+    *meta = grid * kRounds;
 }
 
 cudaError_t launch_attend(const Cache& c, const kv8_pool& pool, const int32_t* table, const int32_t* len,
@@ -1153,6 +1244,7 @@ cudaError_t launch_attend(const Cache& c, const kv8_pool& pool, const int32_t* t
     a.part_o = c.d_part_o;
     a.part_ml = c.d_part_ml;
     a.meta = c.d_meta;
+    a.ctrl = c.d_ctrl;
     a.err = c.d_err;
     a.n_req = n_req;
     a.n_rows = n_rows;

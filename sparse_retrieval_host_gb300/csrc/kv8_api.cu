@@ -120,6 +120,8 @@ int kv8_create(const kv8_config* cfg, kv8_cache** out) {
         if (e == cudaSuccess) e = cudaMalloc(&c->d_part_o, c->part_o_floats * sizeof(float));
         if (e == cudaSuccess) e = cudaMalloc(&c->d_part_ml, c->part_ml_floats * sizeof(float));
         if (e == cudaSuccess) e = cudaMalloc(&c->d_meta, c->meta_n * sizeof(int4));
+        if (e == cudaSuccess) e = cudaMalloc(&c->d_ctrl, 2 * sizeof(int));
+        if (e == cudaSuccess) e = cudaMemset(c->d_ctrl, 0, 2 * sizeof(int));
     }
     if (e != cudaSuccess) {
         const int rc = e == cudaErrorMemoryAllocation ? SRH_ERR_NOMEM : SRH_ERR_CUDA;
@@ -140,6 +142,7 @@ void kv8_destroy(kv8_cache* c) {
         cudaFree(c->d_part_o);
         cudaFree(c->d_part_ml);
         cudaFree(c->d_meta);
+        cudaFree(c->d_ctrl);
     }
     delete c;
 }

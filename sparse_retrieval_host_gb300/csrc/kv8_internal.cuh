@@ -20,7 +20,8 @@ struct Cache {
     uint32_t* d_err = nullptr;
     float* d_part_o = nullptr;      // partial outputs of split attention items
     float* d_part_ml = nullptr;     // their maxima and sums
-    int4* d_meta = nullptr;         // split items, by the CTA that begins them
+    int4* d_meta = nullptr;         // split items, by the chunk that they begin in
+    int* d_ctrl = nullptr;          // the attention's chunk counter and count
     size_t part_o_floats = 0;       // sizes of the three, which the launcher checks
     size_t part_ml_floats = 0;
     size_t meta_n = 0;
