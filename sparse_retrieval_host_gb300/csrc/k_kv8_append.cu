@@ -11,8 +11,8 @@
 // are needed. Units are found from the requests' lengths by prefix sums that
 // each CTA builds in shared memory. A value is read once (kept in registers
 // between the maximum and the rounding) and written once: HBM-bound for
-// prompts, latency for decode steps. A unit of few rows (decode) is done by one
-// warp, eight to a CTA; one of many rows by the whole CTA.
+// prompts, latency for decode steps. A unit of up to 512 vectors (16 per lane) is
+// done by one warp, eight to a CTA; a larger one by the whole CTA.
 #include "kv8_internal.cuh"
 
 namespace srh {
@@ -223,15 +223,16 @@ cudaError_t launch_append(const Cache& c, const kv8_pool& pool, const int32_t* t
     // a request's n rows touch at most ceil(n / bs) + 1 blocks
     const long long most = ((long long)n_rows >> c.bs_log2) + 2ll * n_req;
     const long long units = (most < n_rows ? most : n_rows) * a.heads * a.parts;
-    // vectors of an average unit: up to 4 per lane of a warp go to warps
+    // vectors of an average unit: up to 16 per lane go to a warp (no barriers, and a CTA's 8 units overlap)
     const long long blocks_lo = ((long long)n_rows + (1 << c.bs_log2) - 1) >> c.bs_log2;
     const long long rows_avg = n_rows / (blocks_lo > n_req ? blocks_lo : n_req);
-    const bool by_warp = (rows_avg << a.dv_log2) <= 128;
-    const long long per = by_warp ? kThreads / 32 : 1;
+    const long long vecs = rows_avg << a.dv_log2;
+    const long long per = vecs <= 512 ? kThreads / 32 : 1;
     long long grid = (units + per - 1) / per;
     if (grid > 8ll * c.sm_count) grid = 8ll * c.sm_count;
     const size_t smem = (size_t)(n_req + 1) * sizeof(int);
-    if (by_warp) append_kernel<32, 4><<<(unsigned)grid, kThreads, smem, st>>>(a);
+    if (vecs <= 128) append_kernel<32, 4><<<(unsigned)grid, kThreads, smem, st>>>(a);
+    else if (vecs <= 512) append_kernel<32, 16><<<(unsigned)grid, kThreads, smem, st>>>(a);
     else append_kernel<kThreads, 8><<<(unsigned)grid, kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }

@@ -169,9 +169,9 @@ __device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
                       (int)(((long long)a.window + RT / a.group + 1) / kTile) + 2);
     return r;
 }
-__device__ __forceinline__ long long units(const Args& a, const Request& r) {
-    return (long long)r.pairs * r.P * a.kv_heads;
-}
+// (a call holds at most kMaxUnits: the kernel checks the sum in 64 bits)
+constexpr int kMaxUnits = 1 << 30;
+__device__ __forceinline__ int units(const Args& a, const Request& r) { return r.pairs * r.P * a.kv_heads; }
 
 // A chunk's share of one item (a row tile of a KV head of a request).
 struct Segment {
@@ -182,35 +182,32 @@ struct Segment {
     int q0, nq, len;     // the request's first row, rows and tokens
 };
 
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
-    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// The chunks of U units for n CTAs: `rounds` rounds of n chunks.
+// The chunks of U units for n CTAs: rounds of n chunks whose sizes differ by at
+// most one. Held in shared memory, for the TMA warp.
 struct Chunks {
-    long long U;
     int n, rounds;
-    __device__ __forceinline__ long long round_begin(int r) const { return rounds == 1 ? (r ? U : 0) : U * cut(r) / 16; }
-    __device__ __forceinline__ long long begin(int v) const {    // first unit of chunk v (v = n * rounds: U)
-        const int r = v / n, i = v - r * n;
-        if (r >= rounds) return U;
-        const long long s = round_begin(r);
-        return s + div_ll((round_begin(r + 1) - s) * i, n);
+    int at[kRounds + 1];       // first unit of each round
+    int base[kRounds], rem[kRounds];
+
+    __device__ __forceinline__ int begin(int v) const {          // first unit of chunk v; v = n * rounds: U
+        const int r = (v >= n) + (v >= 2 * n);
+        if (v >= n * rounds) return at[rounds];
+        const int i = v - r * n;
+        return at[r] + i * base[r] + min(i, rem[r]);
     }
-    __device__ __forceinline__ int of(long long u) const {       // the chunk that holds unit u
-        int r = 0;
-        while (r + 1 < rounds && u >= round_begin(r + 1)) ++r;
-        const long long s = round_begin(r);
-        return r * n + (int)div_ll((u - s + 1) * n - 1, round_begin(r + 1) - s);
+    __device__ __forceinline__ int of(int u) const {             // the chunk that holds unit u
+        const int r = (rounds > 1 && u >= at[1]) + (rounds > 2 && u >= at[2]);
+        const uint32_t x = u - at[r], big = base[r] + 1, t = rem[r] * big;
+        return r * n + (int)(x < t ? x / big : rem[r] + (x - t) / (uint32_t)base[r]);
     }
 };
 
 // Walks the units [u, u1) of chunk v; u is unit `off` of request b.
 template <int RT>
 struct Walker {
-    Chunks ch;
-    long long u, u1;
-    long long off;
+    const Chunks* ch;
+    int u, u1;
+    int off;
     int b, v;
     Request r;
 
@@ -221,10 +218,9 @@ struct Walker {
                 off -= units(a, r);
                 r = request<RT>(a, ++b, &bad);
             }
-            const long long head = (long long)r.pairs * r.P;
-            const int h = (int)div_ll(off, head);
-            const long long in = off - h * head;
-            const int k = (int)div_ll(in, r.P), o = (int)(in - (long long)k * r.P);
+            const int pair = (uint32_t)off / (uint32_t)r.P, o = off - pair * r.P;
+            const int h = r.pairs == 1 ? pair : (uint32_t)pair / (uint32_t)r.pairs;
+            const int k = pair - h * r.pairs;
             // the later row tile of the pair first, then the earlier, then nothing
             const int big = r.nrt - 1 - k, nb = units_of<RT>(a, r, big);
             int rt = big, at = o, n = nb;
@@ -234,12 +230,12 @@ struct Walker {
                 n = k < big ? units_of<RT>(a, r, k) : 0;
             }
             if (at >= n) {
-                const long long skip = min((long long)(r.P - o), u1 - u);
+                const int skip = min(r.P - o, u1 - u);
                 u += skip;
                 off += skip;
                 continue;
             }
-            const int take = (int)min((long long)(n - at), u1 - u);
+            const int take = min(n - at, u1 - u);
             s->b = b;
             s->h = h;
             s->row0 = rt * RT;
@@ -255,7 +251,7 @@ struct Walker {
             if (take != n) {
                 s->slot = 2 * v + (at == 0);
                 if (at == 0)       // the item goes on in the next chunks: for the join
-                    a.meta[v] = make_int4((ch.of(u + n - 1) - v + 1) | (s->nr << 16), r.q0, s->row0, h);
+                    a.meta[v] = make_int4((ch->of(u + n - 1) - v + 1) | (s->nr << 16), r.q0, s->row0, h);
             }
             u += take;
             off += take;
@@ -316,6 +312,13 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
     u64 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
+}
+// Eight values times the eight factors of two 16-byte loads.
+__device__ __forceinline__ void scale8(float (&v)[8], const ulonglong2& fa, const ulonglong2& fb) {
+    unpack(mul2(pack(v[0], v[1]), fa.x), v[0], v[1]);
+    unpack(mul2(pack(v[2], v[3]), fa.y), v[2], v[3]);
+    unpack(mul2(pack(v[4], v[5]), fb.x), v[4], v[5]);
+    unpack(mul2(pack(v[6], v[7]), fb.y), v[6], v[7]);
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -401,17 +404,19 @@ struct Bars {
     uint64_t pv_done;            // PV completed
     uint64_t drain;
     long long warp_sums[33];
-    long long before[S::THREADS];     // units before each thread's requests
+    int before[S::THREADS];           // units before each thread's requests
+    Chunks ch;
     uint32_t tmem_base;
     int abort;
     alignas(16) float4 sc[kScales][8];   // (ks, log2 vs, 1 / vs) of a tile's blocks
-    alignas(16) float nref[S::RT];    // minus the reference exponent of each row
+    // of each row; what the outputs of a segment still need while the next begins, twice
+    alignas(16) float nref[2][S::RT]; // minus the reference exponent
     alignas(16) float fac[S::RT];     // 2^(old reference - new)
     alignas(16) float qs[S::RT];      // query scale * softmax scale * log2 e
     float part[4][S::RT];             // per-warp maxima, then sums
     float sum[S::RT];
     int pos[S::RT];                   // position of the row's token; -1: no row
-    long long row_at[S::RT];          // its offset in out
+    long long row_at[2][S::RT];       // its offset in out
     Segment seg[kSegs];
 };
 
@@ -458,20 +463,42 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int n_grid = gridDim.x, cta = blockIdx.x;
 
     // ------------------------------------------------------------ the units
-    Chunks ch;
     const int per = (a.n_req + S::THREADS - 1) / S::THREADS;       // requests per thread (at most 22)
     bool bad = false;
+    int U, n_cta;
     {
         const int b0 = min(a.n_req, tid * per), b1 = min(a.n_req, b0 + per);
-        long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += units(a, request<RT>(a, b, &bad));
-        const long long incl = block_scan(mine, bs.warp_sums, &ch.U);
-        ch.n = (int)min((long long)n_grid, ch.U);
-        // rounds of smaller chunks only where each still has units
-        ch.rounds = ch.U >= 16ll * ch.n ? kRounds : 1;
-        if (cta == 0 && tid == 0) a.ctrl[1] = ch.n * ch.rounds;
-        if (cta >= ch.n) return;                           // nothing to do (every thread)
-        bs.before[tid] = incl - mine;
+        long long mine = 0, total;
+        for (int b = b0; b < b1; ++b) {
+            const Request r = request<RT>(a, b, &bad);
+            mine += (long long)r.pairs * r.P * a.kv_heads;
+        }
+        const long long incl = block_scan(mine, bs.warp_sums, &total);
+        if (total > kMaxUnits) {                           // too much for one call: reported, nothing written
+            if (tid == 0) atomicOr(a.err, kErrBounds);
+            total = 0;
+        }
+        U = (int)total;
+        n_cta = min(n_grid, U);
+        // rounds of smaller chunks only where even the smallest still has 4 units
+        const int rounds = U >= 64 * n_cta ? kRounds : 1;
+        if (cta == 0 && tid == 0) a.ctrl[1] = n_cta * rounds;
+        if (cta >= n_cta) return;                          // nothing to do (every thread)
+        bs.before[tid] = (int)(incl - mine);
+        if (tid == 0) {
+            bs.ch.n = n_cta;
+            bs.ch.rounds = rounds;
+        }
+        if (tid <= kRounds) {
+            auto begin = [&](int r) { return rounds == 1 ? (r ? U : 0) : (int)((long long)U * cut(r) / 16); };
+            const int at = begin(tid);
+            bs.ch.at[tid] = at;
+            if (tid < kRounds) {
+                const uint32_t n = begin(tid + 1) - at;
+                bs.ch.base[tid] = n / (uint32_t)n_cta;
+                bs.ch.rem[tid] = n % (uint32_t)n_cta;
+            }
+        }
     }
     if (cta == 0 && bad) atomicOr(a.err, kErrBounds);
     if (tid == 0) {
@@ -507,7 +534,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // scales of each token tile (the tile's few blocks, a lane each).
         Segment sg{};
         Walker<RT> w;
-        w.ch = ch;
+        const Chunks& ch = bs.ch;
+        w.ch = &ch;
         // to the first unit of chunk v
         auto seek = [&](int v) {
             w.v = v;
@@ -519,19 +547,23 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 if (bs.before[mid] <= w.u) lo = mid;
                 else hi = mid;
             }
-            // the last thread at or below u owns it (those after it with nothing have the same sum: the
-            // search ends at the last of them, whose requests, if any, begin at u)
-            const int b0 = lo * per, b = b0 + lane;
-            long long k = lane < per && b < a.n_req ? units(a, request<RT>(a, b, &bad)) : 0, incl = k;
+            // the last thread at or below u owns it (threads without units have the next one's sum)
+            const int b0 = lo * per, rel = w.u - bs.before[lo];
+            w.b = b0;
+            w.off = rel;
+            if (per > 1) {
+                const int b = b0 + lane;
+                const int k = lane < per && b < a.n_req ? units(a, request<RT>(a, b, &bad)) : 0;
+                int incl = k;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += up;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                const int mine = __ffs(__ballot_sync(0xffffffffu, rel < incl)) - 1;
+                w.b = b0 + mine;
+                w.off = rel - __shfl_sync(0xffffffffu, incl - k, mine);
             }
-            const long long rel = w.u - bs.before[lo];
-            const int mine = __ffs(__ballot_sync(0xffffffffu, rel < incl)) - 1;
-            w.b = b0 + mine;
-            w.off = rel - __shfl_sync(0xffffffffu, incl - k, mine);
             w.r = request<RT>(a, w.b, &bad);
             if (lane == 0) a.meta[v] = make_int4(0, 0, 0, 0);      // no item goes on from this chunk, so far
             __syncwarp();
@@ -726,55 +758,60 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     qx[i][d] = r < sg.nr ? __ldg(reinterpret_cast<const uint2*>(p + d * 128)) : make_uint2(0, 0);
             }
         };
+        // Segment k's rows into shared memory, the queries from the registers.
+        auto stage = [&](const Segment& sg, uint32_t k) {
+            if (tid < RT) {
+                const int row = sg.row0 + tid, qt = row / a.group, hd = sg.h * a.group + row % a.group;
+                const bool on = tid < sg.nr;
+                bs.pos[tid] = on ? sg.len - sg.nq + qt : -1;
+                bs.row_at[k & 1][tid] = (long long)(sg.q0 + qt) * a.out_row + (long long)hd * (DB * 128);
+                // a column without a row is held at weight 0 by a reference out of reach
+                bs.nref[k & 1][tid] = on ? -kLow : kLow;
+            }
+            if (sg.n == 0) return;
+#pragma unroll
+            for (int i = 0; i < RPW; ++i) {
+                const int r = warp + W * i;
+                uint32_t m = 0;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    m = max(m, max(max(qx[i][d].x & 0x7fffu, (qx[i][d].x >> 16) & 0x7fffu),
+                                   max(qx[i][d].y & 0x7fffu, (qx[i][d].y >> 16) & 0x7fffu)));
+                m = __reduce_max_sync(0xffffffffu, m);
+                const int e = min(max((int)(m >> 7) - 127 - 7, -120), 120);
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                if (lane == 0)   // a row that is not finite has no result: NaN
+                    bs.qs[r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)
+                                            : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    uint32_t hi, lo;
+                    split4<true>(__uint_as_float(qx[i][d].x << 16) * inv, __uint_as_float(qx[i][d].x & 0xffff0000u) * inv,
+                                 __uint_as_float(qx[i][d].y << 16) * inv, __uint_as_float(qx[i][d].y & 0xffff0000u) * inv,
+                                 &hi, &lo);
+                    unsigned char* q = qsm + d * (N * 128) + (lane & 3) * 4;
+                    *reinterpret_cast<uint32_t*>(q + sw128(r, lane >> 2)) = hi;
+                    *reinterpret_cast<uint32_t*>(q + sw128(RT + r, lane >> 2)) = lo;
+                }
+            }
+            fence_async_smem();
+            warp_arrive(&bs.q_full, lane);
+        };
         if (mbar_wait_abort(&bs.seg_full[0], 0, abort) <= 0) fail = true;
-        else if (bs.seg[0].n > 0) load_q(bs.seg[0]);
+        else {
+            if (bs.seg[0].n > 0) load_q(bs.seg[0]);
+            if (bs.seg[0].b >= 0) stage(bs.seg[0], 0);
+        }
         for (uint32_t k = 0;; ++k) {
             const Segment& sg = bs.seg[k % kSegs];
-            if (soft_any<SOFT>(fail)) {                    // also: the last segment's shared arrays are read
+            if (soft_any<SOFT>(fail)) {                    // also: the rows are staged
                 ok = false;
                 break;
             }
             if (k > 0 && tid == 0) mbar_arrive(&bs.seg_empty[(k - 1) % kSegs]);
             if (sg.b < 0) break;
             const int n = sg.n, len = sg.len;
-            if (tid < RT) {
-                const int row = sg.row0 + tid, qt = row / a.group, hd = sg.h * a.group + row % a.group;
-                const bool on = tid < sg.nr;
-                bs.pos[tid] = on ? len - sg.nq + qt : -1;
-                bs.row_at[tid] = (long long)(sg.q0 + qt) * a.out_row + (long long)hd * (DB * 128);
-                // a column without a row is held at weight 0 by a reference out of reach
-                bs.nref[tid] = on ? -kLow : kLow;
-            }
-            if (n > 0) {
-#pragma unroll
-                for (int i = 0; i < RPW; ++i) {
-                    const int r = warp + W * i;
-                    uint32_t m = 0;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        m = max(m, max(max(qx[i][d].x & 0x7fffu, (qx[i][d].x >> 16) & 0x7fffu),
-                                       max(qx[i][d].y & 0x7fffu, (qx[i][d].y >> 16) & 0x7fffu)));
-                    m = __reduce_max_sync(0xffffffffu, m);
-                    const int e = min(max((int)(m >> 7) - 127 - 7, -120), 120);
-                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                    if (lane == 0)   // a row that is not finite has no result: NaN
-                        bs.qs[r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u)
-                                                : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        uint32_t hi, lo;
-                        split4<true>(__uint_as_float(qx[i][d].x << 16) * inv, __uint_as_float(qx[i][d].x & 0xffff0000u) * inv,
-                               __uint_as_float(qx[i][d].y << 16) * inv, __uint_as_float(qx[i][d].y & 0xffff0000u) * inv,
-                               &hi, &lo);
-                        unsigned char* q = qsm + d * (N * 128) + (lane & 3) * 4;
-                        *reinterpret_cast<uint32_t*>(q + sw128(r, lane >> 2)) = hi;
-                        *reinterpret_cast<uint32_t*>(q + sw128(RT + r, lane >> 2)) = lo;
-                    }
-                }
-                fence_async_smem();
-                warp_arrive(&bs.q_full, lane);
-            }
-            soft_sync<SOFT>();
+            float* const nref = bs.nref[k & 1];
 #pragma unroll
             for (int c = 0; c < CT / 2; ++c) l2[c] = 0;
             bool stop = false;
@@ -819,15 +856,17 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         if (t > p || t <= p - win) x[c] = -INFINITY;
                     }
                 }
+                if (j > 0) {
 #pragma unroll
-                for (int c = 0; c < CT; c += 4) {
-                    const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&bs.nref[col0 + c]);
-                    float y0, y1, y2, y3;
-                    unpack(add2(pack(x[c], x[c + 1]), r4.x), y0, y1);
-                    unpack(add2(pack(x[c + 2], x[c + 3]), r4.y), y2, y3);
-                    most = fmaxf(most, fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
+                    for (int c = 0; c < CT; c += 4) {
+                        const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&nref[col0 + c]);
+                        float y0, y1, y2, y3;
+                        unpack(add2(pack(x[c], x[c + 1]), r4.x), y0, y1);
+                        unpack(add2(pack(x[c + 2], x[c + 3]), r4.y), y2, y3);
+                        most = fmaxf(most, fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
+                    }
                 }
-                if (soft_any<SOFT>(most > kRoom || fail)) {
+                if (j == 0 || soft_any<SOFT>(most > kRoom || fail)) {
                     // new references: the maximum of the tile's 128 tokens per row
                     float m = -INFINITY;
 #pragma unroll
@@ -842,10 +881,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     }
                     if (tid < RT) {
                         const float mt = fmaxf(fmaxf(bs.part[0][tid], bs.part[1][tid]), fmaxf(bs.part[2][tid], bs.part[3][tid]));
-                        const float was = -bs.nref[tid];
+                        const float was = -nref[tid];
                         float now = was;
                         if (mt - was > S::HEAD) now = mt - S::HEAD;     // every row that grew, while at it
-                        bs.nref[tid] = -now;
+                        nref[tid] = -now;
                         bs.fac[tid] = now == was ? 1.f : ex2(was - now);
                     }
                     soft_sync<SOFT>();
@@ -865,18 +904,23 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         l2[c / 2 + 2] = mul2(l2[c / 2 + 2], fb.x);
                         l2[c / 2 + 3] = mul2(l2[c / 2 + 3], fb.y);
                         if (j == 0) continue;
+                        constexpr int KO = DB * (S::CAT ? 2 : 1);          // 8-column pieces of these rows
 #pragma unroll 1
-                        for (int i = 0; i < DB * (S::CAT ? 2 : 1); ++i) {
-                            const uint32_t at = my_o + (S::CAT ? (i >> 1) * S::ON + (i & 1) * RT : i * S::ON) + c;
-                            float o[8];
+                        for (int i = 0; i < KO; i += 2) {
+                            const uint32_t at = my_o + i * (S::CAT ? RT : S::ON) + c;
+                            const uint32_t at2 = at + (S::CAT ? RT : S::ON);   // (CAT: hi and lo alternate, RT apart)
+                            float o[8], p[8];
                             tmem_ld<8>(at, o);
+                            if (KO > 1) tmem_ld<8>(at2, p);
                             tmem_ld_wait();
                             tmem_regs_ready_n<8>(o);
-                            unpack(mul2(pack(o[0], o[1]), fa.x), o[0], o[1]);
-                            unpack(mul2(pack(o[2], o[3]), fa.y), o[2], o[3]);
-                            unpack(mul2(pack(o[4], o[5]), fb.x), o[4], o[5]);
-                            unpack(mul2(pack(o[6], o[7]), fb.y), o[6], o[7]);
+                            scale8(o, fa, fb);
                             tmem_st<8>(at, o);
+                            if (KO > 1) {
+                                tmem_regs_ready_n<8>(p);
+                                scale8(p, fa, fb);
+                                tmem_st<8>(at2, p);
+                            }
                         }
                     }
                     if (j > 0) {
@@ -892,7 +936,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
-                        const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&bs.nref[col0 + c + i]);
+                        const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&nref[col0 + c + i]);
                         float y0, y1, y2, y3;
                         unpack(add2(pack(x[c + i], x[c + i + 1]), r4.x), y0, y1);
                         unpack(add2(pack(x[c + i + 2], x[c + i + 3]), r4.y), y2, y3);
@@ -927,25 +971,31 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 break;
             }
             it += n * (S::SHARED ? DB : 2 * DB);
-            // the next segment's queries are asked for before this one's outputs
+            // the next segment's queries, so that its first product runs during the outputs
+            const Segment& next = bs.seg[(k + 1) % kSegs];
+            bool go = false;
             if (mbar_wait_abort(&bs.seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1, abort) <= 0) fail = true;
-            else if (bs.seg[(k + 1) % kSegs].n > 0) load_q(bs.seg[(k + 1) % kSegs]);
-            // ---------------------------------------------------- out
+            else go = next.b >= 0;
+            if (go && next.n > 0) load_q(next);
             if (n > 0) {
                 float l[CT];
 #pragma unroll
                 for (int c = 0; c < CT; c += 2) unpack(l2[c / 2], l[c], l[c + 1]);
                 column_sums<CT>(l, lane, &bs.part[quad][col0]);
-                if (mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
-                tc_fence_after();
             }
-            soft_sync<SOFT>();
+            soft_sync<SOFT>();                             // every warp is through with this segment's rows
+            if (go) stage(next, k + 1);
             const int slot = sg.slot, nr = sg.nr;
             if (tid < RT) {
                 const float sum = n > 0 ? (bs.part[0][tid] + bs.part[1][tid]) + (bs.part[2][tid] + bs.part[3][tid]) : 0.f;
                 bs.sum[tid] = sum == 0.f ? 0.f : 1.f / sum;
                 if (slot >= 0)
-                    reinterpret_cast<float2*>(a.part_ml)[(size_t)slot * RT + tid] = make_float2(-bs.nref[tid], sum);
+                    reinterpret_cast<float2*>(a.part_ml)[(size_t)slot * RT + tid] = make_float2(-nref[tid], sum);
+            }
+            // ---------------------------------------------------- out
+            if (n > 0) {
+                if (mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
+                tc_fence_after();
             }
             soft_sync<SOFT>();
             // (a part without tiles has the sum 0, by which the join leaves it out)
@@ -959,7 +1009,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         inv[i] = bs.sum[col0 + c + i];
-                        at[i] = a.out + bs.row_at[col0 + c + i] + tok;
+                        at[i] = a.out + bs.row_at[k & 1][col0 + c + i] + tok;
                     }
                     float* po = a.part_o + ((size_t)max(slot, 0) * RT + col0 + c) * (DB * 128) + tok;
 #pragma unroll 1

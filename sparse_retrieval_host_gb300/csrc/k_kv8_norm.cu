@@ -64,13 +64,37 @@ __device__ __forceinline__ void load_w(const float* w, int e, float (&v)[8]) {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// LPH lanes per head, VPL vectors of 8 values per lane.
-template <int LPH, int VPL>
+// LPH lanes per head, VPL vectors of 8 values per lane, HPG heads of a group at
+// a time: their loads are all issued before the first is used, the first ones
+// before the token's angles are computed.
+template <int LPH, int VPL, int HPG>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ Args a) {
     __shared__ float2 cs[256];          // (cos, sin) of this token's pairs
     const int tid = threadIdx.x;
     const int t = blockIdx.x;
     const int half = a.rot_dim >> 1;
+    const int lane = tid % LPH, group = tid / LPH;
+    constexpr int kGroups = kThreads / LPH;
+    const int total = a.part[0].n_heads + a.part[1].n_heads;
+    const int h0 = blockIdx.y * a.heads_per_cta;
+    const int h1 = min(total, h0 + a.heads_per_cta);
+    uint4 own[HPG][VPL];
+    // heads base + i * kGroups of this group; a head past the end loads nothing
+    auto load = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < HPG; ++i) {
+            const int g = base + i * kGroups;
+            const bool is_k = g >= a.part[0].n_heads;
+            const uint16_t* x = (is_k ? a.part[1].x + (size_t)t * a.part[1].x_row : a.part[0].x + (size_t)t * a.part[0].x_row) +
+                                (size_t)(is_k ? g - a.part[0].n_heads : g) * a.vecs * 8;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int v = lane + j * LPH;
+                own[i][j] = g < h1 && v < a.vecs ? *reinterpret_cast<const uint4*>(x + v * 8) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    load(h0 + group);
     if (tid < half) {
         double turn = a.inv_freq[tid] * 0.15915494309189533576888;   // 1 / (2 pi)
         turn -= floor(turn);
@@ -82,86 +106,81 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         cs[tid] = make_float2(c, s);
     }
     __syncthreads();
-    const int lane = tid % LPH, group = tid / LPH;
-    constexpr int kGroups = kThreads / LPH;
-    const int total = a.part[0].n_heads + a.part[1].n_heads;
-    const int h1 = min(total, (int)(blockIdx.y + 1) * a.heads_per_cta);
-    for (int h0 = blockIdx.y * a.heads_per_cta + group; h0 - group < h1; h0 += kGroups) {
-        // every group of a warp goes through the shuffles; those without a head store nothing
-        const bool on = h0 < h1;
-        const bool is_k = on && h0 >= a.part[0].n_heads;
-        const kv8_heads& p = a.part[is_k ? 1 : 0];
-        const int h = is_k ? h0 - a.part[0].n_heads : h0;
-        long long row = t;
-        bool keep = on;
-        if (on && p.slot) {
-            row = p.slot[t];
-            if (row < 0) keep = false;
-            else if (row >= p.n_slots) {
-                keep = false;
-                if (lane == 0) atomicOr(a.err, kErrBounds);
-            }
-        }
-        const uint16_t* x = p.x + (size_t)t * p.x_row + (size_t)h * a.vecs * 8;
-        uint4 own[VPL], other[VPL];
-        float ss = 0.f;
+    for (int first = h0; first < h1; first += kGroups * HPG) {
+        if (first > h0) load(first + group);
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int v = lane + j * LPH, e = v * 8 - a.rot_off;
-            own[j] = other[j] = make_uint4(0, 0, 0, 0);
-            if (keep && v < a.vecs) {
-                own[j] = *reinterpret_cast<const uint4*>(x + v * 8);
-                if (!a.pairs && e >= 0 && e < a.rot_dim)
-                    other[j] = *reinterpret_cast<const uint4*>(x + v * 8 + (e < half ? half : -half));
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            float f[8];
-            unpack(own[j], f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-        }
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        __syncwarp();                   // in place: every load of the warp's heads before any store
-        const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
-        if (!keep) continue;
-        uint16_t* out = p.out + (size_t)row * p.out_row + (size_t)h * a.vecs * 8;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int v = lane + j * LPH, e = v * 8 - a.rot_off;
-            if (v >= a.vecs) continue;
-            float f[8], w[8];
-            unpack(own[j], f);
-            load_w(p.weight, v * 8, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= r * w[i];
-            if (e >= 0 && e < a.rot_dim) {
-                if (a.pairs) {
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float2 k = cs[(e + i) >> 1];
-                        const float u = f[i], z = f[i + 1];
-                        f[i] = u * k.x - z * k.y;
-                        f[i + 1] = u * k.y + z * k.x;
-                    }
-                } else {
-                    const bool first = e < half;
-                    const int eo = first ? e : e - half;
-                    float g[8];
-                    unpack(other[j], g);
-                    load_w(p.weight, v * 8 + (first ? half : -half), w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 k = cs[eo + i];
-                        const float z = g[i] * (r * w[i]);
-                        f[i] = first ? f[i] * k.x - z * k.y : z * k.y + f[i] * k.x;
-                    }
+        for (int i = 0; i < HPG; ++i) {
+            // every group of a warp goes through the shuffles; those without a head store nothing
+            const int g = first + group + i * kGroups;
+            if (first + i * kGroups >= h1) break;               // the same for the whole CTA
+            const bool is_k = g >= a.part[0].n_heads;
+            const kv8_heads& p = a.part[is_k ? 1 : 0];
+            const int h = is_k ? g - a.part[0].n_heads : g;
+            bool keep = g < h1;
+            long long row = t;
+            if (keep && p.slot) {
+                row = p.slot[t];
+                if (row < 0) keep = false;
+                else if (row >= p.n_slots) {
+                    keep = false;
+                    if (lane == 0) atomicOr(a.err, kErrBounds);
                 }
             }
-            *reinterpret_cast<uint4*>(out + v * 8) =
-                make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+            const uint16_t* x = p.x + (size_t)t * p.x_row + (size_t)h * a.vecs * 8;
+            uint4 other[VPL];
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int v = lane + j * LPH, e = v * 8 - a.rot_off;
+                other[j] = make_uint4(0, 0, 0, 0);
+                if (keep && !a.pairs && v < a.vecs && e >= 0 && e < a.rot_dim)
+                    other[j] = *reinterpret_cast<const uint4*>(x + v * 8 + (e < half ? half : -half));
+                float f[8];
+                unpack(own[i][j], f);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) ss = fmaf(f[q], f[q], ss);
+            }
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            __syncwarp();               // in place: every load of this head before any store to it
+            const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
+            if (!keep) continue;
+            uint16_t* out = p.out + (size_t)row * p.out_row + (size_t)h * a.vecs * 8;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int v = lane + j * LPH, e = v * 8 - a.rot_off;
+                if (v >= a.vecs) continue;
+                float f[8], w[8];
+                unpack(own[i][j], f);
+                load_w(p.weight, v * 8, w);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) f[q] *= r * w[q];
+                if (e >= 0 && e < a.rot_dim) {
+                    if (a.pairs) {
+#pragma unroll
+                        for (int q = 0; q < 8; q += 2) {
+                            const float2 k = cs[(e + q) >> 1];
+                            const float u = f[q], z = f[q + 1];
+                            f[q] = u * k.x - z * k.y;
+                            f[q + 1] = u * k.y + z * k.x;
+                        }
+                    } else {
+                        const bool low = e < half;
+                        const int eo = low ? e : e - half;
+                        float z[8];
+                        unpack(other[j], z);
+                        load_w(p.weight, v * 8 + (low ? half : -half), w);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float2 k = cs[eo + q];
+                            const float y = z[q] * (r * w[q]);
+                            f[q] = low ? f[q] * k.x - y * k.y : y * k.y + f[q] * k.x;
+                        }
+                    }
+                }
+                *reinterpret_cast<uint4*>(out + v * 8) =
+                    make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+            }
         }
     }
 }
@@ -193,10 +212,10 @@ cudaError_t launch_norm_rope(const Cache& c, const kv8_heads& q, const kv8_heads
     while (per > groups && (long long)n_tok * ((heads + per - 1) / per) < 4ll * c.sm_count) per = (per + 1) / 2;
     a.heads_per_cta = per;
     const dim3 grid((unsigned)n_tok, (unsigned)((heads + per - 1) / per));
-    if (lph == 8) norm_rope_kernel<8, 1><<<grid, kThreads, 0, st>>>(a);
-    else if (lph == 16) norm_rope_kernel<16, 1><<<grid, kThreads, 0, st>>>(a);
-    else if (a.vecs <= 32) norm_rope_kernel<32, 1><<<grid, kThreads, 0, st>>>(a);
-    else norm_rope_kernel<32, 2><<<grid, kThreads, 0, st>>>(a);
+    if (lph == 8) norm_rope_kernel<8, 1, 4><<<grid, kThreads, 0, st>>>(a);
+    else if (lph == 16) norm_rope_kernel<16, 1, 4><<<grid, kThreads, 0, st>>>(a);
+    else if (a.vecs <= 32) norm_rope_kernel<32, 1, 4><<<grid, kThreads, 0, st>>>(a);
+    else norm_rope_kernel<32, 2, 2><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

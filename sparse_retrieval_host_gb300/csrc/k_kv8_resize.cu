@@ -44,6 +44,47 @@ struct Args {
     int fill_here;
 };
 
+// block_scan of three values at once.
+__device__ __forceinline__ void block_scan3(long long& x, long long& y, long long& z, long long (*warp_sums)[33],
+                                            long long* tx, long long* ty, long long* tz) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long ux = __shfl_up_sync(0xffffffffu, x, o), uy = __shfl_up_sync(0xffffffffu, y, o),
+                        uz = __shfl_up_sync(0xffffffffu, z, o);
+        if (lane >= o) {
+            x += ux;
+            y += uy;
+            z += uz;
+        }
+    }
+    if (lane == 31) {
+        warp_sums[0][warp] = x;
+        warp_sums[1][warp] = y;
+        warp_sums[2][warp] = z;
+    }
+    __syncthreads();
+    if (warp < 3) {
+        long long w = lane < nw ? warp_sums[warp][lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += u;
+        }
+        warp_sums[warp][lane] = w;
+    }
+    __syncthreads();
+    if (warp > 0) {
+        x += warp_sums[0][warp - 1];
+        y += warp_sums[1][warp - 1];
+        z += warp_sums[2][warp - 1];
+    }
+    *tx = warp_sums[0][nw - 1];
+    *ty = warp_sums[1][nw - 1];
+    *tz = warp_sums[2][nw - 1];
+    __syncthreads();
+}
+
 // Position and slot of new token i (request b of the prefix sums cu, whose
 // length after the call is new_len).
 __device__ __forceinline__ void put_token(const Args& a, int i, int b, int begin, int count, int new_len) {
@@ -58,7 +99,8 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     int* rel = sums;                    // [n_req + 1] released blocks before each request
     int* alc = rel + a.n_req + 1;       // taken blocks
     int* tok = alc + a.n_req + 1;       // new tokens
-    __shared__ long long warp_sums[33];
+    int* kept = tok + a.n_req + 1;      // blocks that stay: min(have, need)
+    __shared__ long long warp_sums[3][33];
     const int tid = threadIdx.x, nt = blockDim.x;
     const int most = a.max_blocks << a.bs_log2;
     const int bs1 = (1 << a.bs_log2) - 1;
@@ -67,27 +109,27 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     bool bad = false;
     for (int base = 0; base < a.n_req; base += nt) {
         const int b = base + tid;
-        int r = 0, q = 0, t = 0;
+        int r = 0, q = 0, t = 0, stay = 0;
         if (b < a.n_req) {
             const int was = a.len[b], will = a.new_len[b];
             if (was < 0 || was > most || will < 0 || will > most) {
                 bad = true;
             } else {
                 const int have = (was + bs1) >> a.bs_log2, need = (will + bs1) >> a.bs_log2;
+                stay = min(have, need);
                 r = max(0, have - need);
                 q = max(0, need - have);
                 t = max(0, will - was);
             }
         }
-        long long tr, ta, tn;
-        const long long sr = block_scan(r, warp_sums, &tr);
-        const long long sa = block_scan(q, warp_sums, &ta);
-        const long long sn = block_scan(t, warp_sums, &tn);
+        long long tr, ta, tn, sr = r, sa = q, sn = t;
+        block_scan3(sr, sa, sn, warp_sums, &tr, &ta, &tn);
         if (b < a.n_req) {
             // truncated only where a total makes the call fail below
             rel[b] = (int)(R + sr - r);
             alc[b] = (int)(A + sa - q);
             tok[b] = (int)(N + sn - t);
+            kept[b] = stay;
         }
         R += tr;
         A += ta;
@@ -107,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
         // a released entry that is no block fails the call before anything changes
         for (int i = tid; i < (int)R; i += nt) {
             const int b = last_not_above(rel, a.n_req, i);
-            const int j = ((a.new_len[b] + bs1) >> a.bs_log2) + i - rel[b];
+            const int j = kept[b] + i - rel[b];
             const int id = a.table[(size_t)b * a.max_blocks + j];
             if (id < 0 || id >= a.n_blocks) bad = true;
         }
@@ -122,16 +164,17 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     const int top = depth + (int)R;
     for (int i = tid; i < (int)R; i += nt) {
         const int b = last_not_above(rel, a.n_req, i);
-        const int j = ((a.new_len[b] + bs1) >> a.bs_log2) + i - rel[b];
+        const int j = kept[b] + i - rel[b];
         int32_t* e = a.table + (size_t)b * a.max_blocks + j;
         a.free_ids[top - 1 - i] = *e;
         *e = -1;
     }
     __syncthreads();
+#pragma unroll 4
     for (int k = tid; k < (int)A; k += nt) {
         const int b = last_not_above(alc, a.n_req, k);
-        const int j = ((a.len[b] + bs1) >> a.bs_log2) + k - alc[b];
-        int id = a.free_ids[top - 1 - k];
+        const int j = kept[b] + k - alc[b];
+        int id = __ldcg(a.free_ids + top - 1 - k);     // (written above by other threads, in L2)
         if (id < 0 || id >= a.n_blocks) {   // the caller's stack holds something else
             atomicOr(a.err, kErrBounds);
             id = -1;
@@ -172,7 +215,7 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const Args a) {
 
 cudaError_t set_resize_attrs() {
     return cudaFuncSetAttribute(resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                3 * (kMaxBatch + 1) * (int)sizeof(int));
+                                4 * (kMaxBatch + 1) * (int)sizeof(int));
 }
 
 cudaError_t launch_resize(const Cache& c, const int32_t* new_len, int n_req, int32_t* len, int32_t* table,
@@ -197,7 +240,7 @@ cudaError_t launch_resize(const Cache& c, const int32_t* new_len, int n_req, int
     // enough threads for the requests and for the tokens written here, in whole warps
     int nt = 128;
     while (nt < kThreads && (nt < n_req || (a.fill_here && 2 * nt < cap))) nt *= 2;
-    resize_kernel<<<1, nt, 3 * (n_req + 1) * sizeof(int), st>>>(a);
+    resize_kernel<<<1, nt, 4 * (n_req + 1) * sizeof(int), st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.fill_here || !pos) return e;
     return launch_k(fill_kernel, dim3((unsigned)((cap + kFillThreads - 1) / kFillThreads)), dim3(kFillThreads),

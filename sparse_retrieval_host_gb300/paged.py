@@ -25,6 +25,14 @@ _STYLES = {"pairs": abi.KV8_ROPE_PAIRS, "halves": abi.KV8_ROPE_HALVES}
 _BF16 = (torch.bfloat16, torch.int16)      # int16: bf16 bit patterns, as DecodeStep holds them
 
 
+def _public_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the current stream's handle without making a Stream object (2 us of a 10 us call)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+
+
 class PagedKV8:
     """Cache of ``layers`` layers for up to ``batch`` requests of up to
     ``max_blocks * block_tokens`` tokens each.
@@ -105,7 +113,7 @@ class PagedKV8:
     # ------------------------------------------------------------------ checks
     def _s(self, stream) -> int:
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _current_stream(self.device.index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     def _rows(self, t: torch.Tensor, name: str, heads: Optional[int] = None, dim: Optional[int] = None) -> int:
