@@ -5,16 +5,20 @@
 //   a' = a cos t - b sin t,  b' = a sin t + b cos t,  t = pos * f_i.
 //
 // One read and one write of each value: HBM-bound for many tokens, latency for
-// a few. A head is held by a group of 8, 16 or 32 lanes, 8 values (one 16-byte
-// load) per lane and vector; the sum of squares is a shuffle tree. In the
-// HALVES style a value's partner lies rot_dim / 2 further on, in another lane:
-// that vector is loaded a second time (from L1) at the same moment as the
-// first, which needs no exchange between lanes and no case for odd widths.
+// a few. A warp takes a token's heads (or a share of them, when tokens are few),
+// 8, 16 or 32 lanes to a head, 8 values (one 16-byte load) per lane and vector.
+// A lane holds the same dims of every head, so weight, cos and sin come down to
+// two factors per value in registers, made once per token and kind of head:
+//   out_i = r x_i A_i + r x_partner(i) B_i.
+// (With a CTA per token and 2-3 heads per lane the factors cost more instructions
+// than the heads: 35 M against 9 M for 6,143 tokens of 40 heads, 56 us.)
+// In the HALVES style a value's partner lies rot_dim / 2 further on, in another
+// lane: that vector is loaded a second time (from L1), which needs no exchange
+// between lanes and no case for odd widths.
 //
 // The angle: t / 2 pi modulo 1 is all that matters. f_i / 2 pi is held as a
 // 64-bit fraction of a turn, so pos * f_i wraps by itself in integer arithmetic
 // and keeps 2^-64 * pos of a turn; fp32 would lose 0.06 rad at position 10^6.
-// cos and sin of a token are computed once per CTA and shared by its heads.
 #include <cuda_bf16.h>
 
 #include "kv8_internal.cuh"
@@ -23,7 +27,7 @@ namespace srh {
 namespace kv8 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Args {
     kv8_heads part[2];
@@ -36,7 +40,7 @@ struct Args {
     int rot_off, rot_dim;
     int pairs;         // style
     float eps;
-    int heads_per_cta;
+    int heads_per_warp, splits;
 };
 
 __device__ __forceinline__ void unpack(const uint4& u, float (&v)[8]) {
@@ -64,122 +68,154 @@ __device__ __forceinline__ void load_w(const float* w, int e, float (&v)[8]) {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// LPH lanes per head, VPL vectors of 8 values per lane, HPG heads of a group at
-// a time: their loads are all issued before the first is used, the first ones
-// before the token's angles are computed.
-template <int LPH, int VPL, int HPG>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ Args a) {
-    __shared__ float2 cs[256];          // (cos, sin) of this token's pairs
-    const int tid = threadIdx.x;
-    const int t = blockIdx.x;
+// LPH lanes per head, VPL vectors of 8 values per lane; a group of lanes loads
+// HPG heads before it uses the first.
+template <int LPH, int VPL, int HPG, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) norm_rope_kernel(const __grid_constant__ Args a) {
+    constexpr int kWarps = kThreads / 32, G = 32 / LPH;    // heads of a warp at a time
+    __shared__ unsigned long long step[256];               // turns per position, as 64-bit fractions
+    __shared__ alignas(16) float cosv[kWarps][256], sinv[kWarps][256];
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int half = a.rot_dim >> 1;
-    const int lane = tid % LPH, group = tid / LPH;
-    constexpr int kGroups = kThreads / LPH;
-    const int total = a.part[0].n_heads + a.part[1].n_heads;
-    const int h0 = blockIdx.y * a.heads_per_cta;
-    const int h1 = min(total, h0 + a.heads_per_cta);
-    uint4 own[HPG][VPL];
-    // heads base + i * kGroups of this group; a head past the end loads nothing
-    auto load = [&](int base) {
-#pragma unroll
-        for (int i = 0; i < HPG; ++i) {
-            const int g = base + i * kGroups;
-            const bool is_k = g >= a.part[0].n_heads;
-            const uint16_t* x = (is_k ? a.part[1].x + (size_t)t * a.part[1].x_row : a.part[0].x + (size_t)t * a.part[0].x_row) +
-                                (size_t)(is_k ? g - a.part[0].n_heads : g) * a.vecs * 8;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const int v = lane + j * LPH;
-                own[i][j] = g < h1 && v < a.vecs ? *reinterpret_cast<const uint4*>(x + v * 8) : make_uint4(0, 0, 0, 0);
-            }
-        }
-    };
-    load(h0 + group);
-    if (tid < half) {
-        double turn = a.inv_freq[tid] * 0.15915494309189533576888;   // 1 / (2 pi)
+    for (int i = tid; i < half; i += kThreads) {
+        double turn = a.inv_freq[i] * 0.15915494309189533576888;   // 1 / (2 pi)
         turn -= floor(turn);
-        const unsigned long long step = (unsigned long long)(turn * 18446744073709551616.0);
-        const unsigned long long at = (unsigned long long)(long long)a.pos[t] * step;
+        step[i] = (unsigned long long)(turn * 18446744073709551616.0);
+    }
+    __syncthreads();
+    const long long task = (long long)blockIdx.x * kWarps + warp;
+    if (task >= (long long)a.n_tok * a.splits) return;     // whole warps
+    const int t = (int)(task / a.splits);
+    const int w0 = (int)(task - (long long)t * a.splits) * a.heads_per_warp;
+    const int w1 = min(a.part[0].n_heads + a.part[1].n_heads, w0 + a.heads_per_warp);
+    const int lane = tid % LPH, group = (tid & 31) / LPH;
+    for (int i = tid & 31; i < half; i += 32) {
+        const unsigned long long at = (unsigned long long)(long long)a.pos[t] * step[i];
         // the top 32 bits as a signed fraction of a turn, in units of half a turn
         float s, c;
         sincospif((float)(int)(uint32_t)(at >> 32) * 4.656612873077392578125e-10f, &s, &c);
-        cs[tid] = make_float2(c, s);
+        cosv[warp][i] = c;
+        sinv[warp][i] = s;
     }
-    __syncthreads();
-    for (int first = h0; first < h1; first += kGroups * HPG) {
-        if (first > h0) load(first + group);
+    __syncwarp();
+    bool turned[VPL];                   // this lane's vector lies in the rotated dims
 #pragma unroll
-        for (int i = 0; i < HPG; ++i) {
-            // every group of a warp goes through the shuffles; those without a head store nothing
-            const int g = first + group + i * kGroups;
-            if (first + i * kGroups >= h1) break;               // the same for the whole CTA
-            const bool is_k = g >= a.part[0].n_heads;
-            const kv8_heads& p = a.part[is_k ? 1 : 0];
-            const int h = is_k ? g - a.part[0].n_heads : g;
-            bool keep = g < h1;
-            long long row = t;
-            if (keep && p.slot) {
-                row = p.slot[t];
-                if (row < 0) keep = false;
-                else if (row >= p.n_slots) {
-                    keep = false;
-                    if (lane == 0) atomicOr(a.err, kErrBounds);
+    for (int j = 0; j < VPL; ++j) {
+        const int e = (lane + j * LPH) * 8 - a.rot_off;
+        turned[j] = e >= 0 && e < a.rot_dim;
+    }
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        const kv8_heads& p = a.part[kind];
+        const int shift = kind ? a.part[0].n_heads : 0;
+        const int h0 = max(0, w0 - shift), h1 = min(p.n_heads, w1 - shift);
+        if (h0 >= h1) continue;
+        long long row = t;
+        if (p.slot) {
+            row = p.slot[t];
+            if (row < 0) continue;
+            if (row >= p.n_slots) {
+                if ((tid & 31) == 0) atomicOr(a.err, kErrBounds);
+                continue;
+            }
+        }
+        const uint16_t* x = p.x + (size_t)t * p.x_row;
+        uint16_t* out = p.out + (size_t)row * p.out_row;
+        // the factors of this lane's dims
+        float A[VPL][8], B[VPL][8];
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int v = lane + j * LPH, e = v * 8 - a.rot_off;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) A[j][q] = B[j][q] = 0.f;
+            if (v >= a.vecs) continue;
+            load_w(p.weight, v * 8, A[j]);
+            if (!turned[j]) continue;
+            if (a.pairs) {
+#pragma unroll
+                for (int q = 0; q < 8; q += 2) {
+                    const float c = cosv[warp][(e + q) >> 1], s = sinv[warp][(e + q) >> 1];
+                    const float u = A[j][q], z = A[j][q + 1];
+                    A[j][q] = u * c;
+                    B[j][q] = -z * s;
+                    A[j][q + 1] = z * c;
+                    B[j][q + 1] = u * s;
+                }
+            } else {
+                const bool low = e < half;
+                const int eo = low ? e : e - half;
+                load_w(p.weight, v * 8 + (low ? half : -half), B[j]);
+#pragma unroll
+                for (int q = 0; q < 8; q += 4) {
+                    const float4 c = *reinterpret_cast<const float4*>(&cosv[warp][eo + q]);
+                    const float4 s = *reinterpret_cast<const float4*>(&sinv[warp][eo + q]);
+                    const float sg = low ? -1.f : 1.f;
+                    A[j][q] *= c.x; A[j][q + 1] *= c.y; A[j][q + 2] *= c.z; A[j][q + 3] *= c.w;
+                    B[j][q] *= sg * s.x; B[j][q + 1] *= sg * s.y; B[j][q + 2] *= sg * s.z; B[j][q + 3] *= sg * s.w;
                 }
             }
-            const uint16_t* x = p.x + (size_t)t * p.x_row + (size_t)h * a.vecs * 8;
-            uint4 other[VPL];
-            float ss = 0.f;
+        }
+        for (int first = h0; first < h1; first += G * HPG) {
+            uint4 own[HPG][VPL];
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const int v = lane + j * LPH, e = v * 8 - a.rot_off;
-                other[j] = make_uint4(0, 0, 0, 0);
-                if (keep && !a.pairs && v < a.vecs && e >= 0 && e < a.rot_dim)
-                    other[j] = *reinterpret_cast<const uint4*>(x + v * 8 + (e < half ? half : -half));
-                float f[8];
-                unpack(own[i][j], f);
+            for (int i = 0; i < HPG; ++i) {
+                const int h = first + group + i * G;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) ss = fmaf(f[q], f[q], ss);
+                for (int j = 0; j < VPL; ++j) {
+                    const int v = lane + j * LPH;
+                    own[i][j] = h < h1 && v < a.vecs ? *reinterpret_cast<const uint4*>(x + (size_t)(h * a.vecs + v) * 8)
+                                                     : make_uint4(0, 0, 0, 0);
+                }
             }
 #pragma unroll
-            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            __syncwarp();               // in place: every load of this head before any store to it
-            const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
-            if (!keep) continue;
-            uint16_t* out = p.out + (size_t)row * p.out_row + (size_t)h * a.vecs * 8;
+            for (int i = 0; i < HPG; ++i) {
+                if (first + i * G >= h1) break;            // the same for the whole warp
+                const int h = first + group + i * G;
+                uint4 other[VPL];                          // the partners: in L1 by now
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const int v = lane + j * LPH, e = v * 8 - a.rot_off;
-                if (v >= a.vecs) continue;
-                float f[8], w[8];
-                unpack(own[i][j], f);
-                load_w(p.weight, v * 8, w);
+                for (int j = 0; j < VPL; ++j) {
+                    const int v = lane + j * LPH;
+                    other[j] = make_uint4(0, 0, 0, 0);
+                    if (h < h1 && v < a.vecs && !a.pairs && turned[j])
+                        other[j] = *reinterpret_cast<const uint4*>(x + (size_t)(h * a.vecs + v) * 8 +
+                                                                   (v * 8 - a.rot_off < half ? half : -half));
+                }
+                float ss = 0.f;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) f[q] *= r * w[q];
-                if (e >= 0 && e < a.rot_dim) {
-                    if (a.pairs) {
+                for (int j = 0; j < VPL; ++j) {
+                    float f[8];
+                    unpack(own[i][j], f);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) ss = fmaf(f[q], f[q], ss);
+                }
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                __syncwarp();           // in place: every load of this head before any store to it
+                const float r = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    const int v = lane + j * LPH;
+                    float f[8], z[8];
+                    unpack(own[i][j], f);
+                    unpack(other[j], z);                   // zeros where nothing is rotated
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        f[q] *= r;
+                        z[q] *= r;
+                    }
+                    if (a.pairs && turned[j]) {
 #pragma unroll
                         for (int q = 0; q < 8; q += 2) {
-                            const float2 k = cs[(e + q) >> 1];
-                            const float u = f[q], z = f[q + 1];
-                            f[q] = u * k.x - z * k.y;
-                            f[q + 1] = u * k.y + z * k.x;
-                        }
-                    } else {
-                        const bool low = e < half;
-                        const int eo = low ? e : e - half;
-                        float z[8];
-                        unpack(other[j], z);
-                        load_w(p.weight, v * 8 + (low ? half : -half), w);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float2 k = cs[eo + q];
-                            const float y = z[q] * (r * w[q]);
-                            f[q] = low ? f[q] * k.x - y * k.y : y * k.y + f[q] * k.x;
+                            z[q] = f[q + 1];
+                            z[q + 1] = f[q];
                         }
                     }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) f[q] = fmaf(f[q], A[j][q], z[q] * B[j][q]);
+                    if (h < h1 && v < a.vecs)
+                        *reinterpret_cast<uint4*>(out + (size_t)(h * a.vecs + v) * 8) =
+                            make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
                 }
-                *reinterpret_cast<uint4*>(out + v * 8) =
-                    make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
             }
         }
     }
@@ -204,18 +240,22 @@ cudaError_t launch_norm_rope(const Cache& c, const kv8_heads& q, const kv8_heads
     a.pairs = style == KV8_ROPE_PAIRS;
     a.eps = eps;
     const int lph = a.vecs <= 8 ? 8 : a.vecs <= 16 ? 16 : 32;
-    const int groups = kThreads / lph;
-    // a CTA takes a token's heads; while that leaves SMs short of CTAs the heads
-    // are split (each CTA computes the token's angles again, a few hundred cycles)
-    const int heads = q.n_heads + k.n_heads;
+    // a warp takes a token's heads; while that leaves SMs short of warps they are
+    // split (each warp makes the token's angles and factors again)
+    const int heads = q.n_heads + k.n_heads, at_once = 32 / lph;
     int per = heads;
-    while (per > groups && (long long)n_tok * ((heads + per - 1) / per) < 4ll * c.sm_count) per = (per + 1) / 2;
-    a.heads_per_cta = per;
-    const dim3 grid((unsigned)n_tok, (unsigned)((heads + per - 1) / per));
-    if (lph == 8) norm_rope_kernel<8, 1, 4><<<grid, kThreads, 0, st>>>(a);
-    else if (lph == 16) norm_rope_kernel<16, 1, 4><<<grid, kThreads, 0, st>>>(a);
-    else if (a.vecs <= 32) norm_rope_kernel<32, 1, 4><<<grid, kThreads, 0, st>>>(a);
-    else norm_rope_kernel<32, 2, 2><<<grid, kThreads, 0, st>>>(a);
+    while (per > at_once && (long long)n_tok * ((heads + per - 1) / per) < 64ll * c.sm_count) per = (per + 1) / 2;
+    a.heads_per_warp = per;
+    a.splits = (heads + per - 1) / per;
+    const long long warps = (long long)n_tok * a.splits;
+    const unsigned grid = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
+    // CTAs per SM: bytes in flight come from warps (one prompt chunk of 6,143 tokens
+    // x 40 heads x 128: 36 us with 16 warps, 31 with 32); two vectors a lane need more
+    // registers, and a decode step is latency-bound either way
+    if (lph == 8) norm_rope_kernel<8, 1, 4, 8><<<grid, kThreads, 0, st>>>(a);
+    else if (lph == 16) norm_rope_kernel<16, 1, 4, 8><<<grid, kThreads, 0, st>>>(a);
+    else if (a.vecs <= 32) norm_rope_kernel<32, 1, 4, 8><<<grid, kThreads, 0, st>>>(a);
+    else norm_rope_kernel<32, 2, 2, 5><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
