@@ -88,10 +88,13 @@ struct Shape {
     static constexpr int CTAS = DB == 1 || (DB == 2 && RT == 16) ? 2 : 1;   // per SM
     // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
     // tile j is given back, so two tiles must fit
-    static constexpr int SLOTS = DB == 1 ? (RT == 64 ? 4 : 5) : DB == 2 ? (RT == 16 ? 6 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
+    static constexpr int SLOTS = DB == 1 ? 5 : DB == 2 ? (RT == 16 ? 6 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
     static_assert(SLOTS >= 2 * DB && SLOTS / DB + 2 < 8, "two tiles must fit the ring, and fewer than the scales held");
-    // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the columns
-    static constexpr int CT = DB == 1 && RT == 64 ? 32 : 16;
+    // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the
+    // columns. (32 columns a thread, for 64-row tiles with two CTAs per SM, need more
+    // than the 96 registers there are: a prompt chunk of 128-dim heads took 610 us
+    // with them and takes 580 with tiles of 32 rows.)
+    static constexpr int CT = 16;
     static constexpr int CG = RT / CT;
     static constexpr int SOFT = 128 * CG;                  // softmax threads
     static constexpr int THREADS = SOFT + 64;
@@ -320,6 +323,11 @@ __device__ __forceinline__ void scale8(float (&v)[8], const ulonglong2& fa, cons
     unpack(mul2(pack(v[4], v[5]), fb.x), v[4], v[5]);
     unpack(mul2(pack(v[6], v[7]), fb.y), v[6], v[7]);
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
@@ -416,6 +424,7 @@ struct Bars {
     float part[4][S::RT];             // per-warp maxima, then sums
     float sum[S::RT];
     int pos[S::RT];                   // position of the row's token; -1: no row
+    alignas(8) int2 span;             // positions of the first and the last row
     long long row_at[2][S::RT];       // its offset in out
     Segment seg[kSegs];
 };
@@ -425,27 +434,20 @@ constexpr int smem_bytes() {
     return S::kOffBars + (int)sizeof(Bars<S>) + 1024;
 }
 
-// The column sums over a warp of v[RT], RT = 16 or 32: lane i writes column i.
-template <int RT>
-__device__ __forceinline__ void column_sums(float (&v)[RT], int lane, float* out) {
-    if (RT == 16) {
+// The sums over a warp of 16 columns: lane i writes column i.
+__device__ __forceinline__ void column_sums(float (&v)[16], int lane, float* out) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
-    }
-    constexpr int W = RT < 32 ? RT : 32;
+    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
 #pragma unroll
-    for (int g = 0; g < RT; g += W) {
+    for (int o = 8; o > 0; o >>= 1) {
 #pragma unroll
-        for (int o = W / 2; o > 0; o >>= 1) {
-#pragma unroll
-            for (int i = 0; i < o; ++i) {
-                const bool up = lane & o;
-                const float send = up ? v[g + i] : v[g + i + o], keep = up ? v[g + i + o] : v[g + i];
-                v[g + i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-            }
+        for (int i = 0; i < o; ++i) {
+            const bool up = lane & o;
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
-        if (lane < W) out[g + lane] = v[g];
     }
+    if (lane < 16) out[lane] = v[0];
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -764,6 +766,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 const int row = sg.row0 + tid, qt = row / a.group, hd = sg.h * a.group + row % a.group;
                 const bool on = tid < sg.nr;
                 bs.pos[tid] = on ? sg.len - sg.nq + qt : -1;
+                if (tid == 0) bs.span.x = sg.len - sg.nq + qt;
+                if (tid == sg.nr - 1) bs.span.y = sg.len - sg.nq + qt;
                 bs.row_at[k & 1][tid] = (long long)(sg.q0 + qt) * a.out_row + (long long)hd * (DB * 128);
                 // a column without a row is held at weight 0 by a reference out of reach
                 bs.nref[k & 1][tid] = on ? -kLow : kLow;
@@ -822,57 +826,60 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     fail = true;
                 const float4 sc = bs.sc[g % kScales][tok >> a.bs_log2];   // (0, -inf, 0) without a block
                 tc_fence_after();
-                constexpr int LD = CT == 32 ? 8 : 16;
-                float x[CT];
-                float most = kLow;
                 const int win = a.window ? a.window : 1 << 30;
-                const bool edge = t0 + kTile - 1 > bs.pos[0] || t0 <= bs.pos[sg.nr - 1] - win;
-                const u64 ks2 = pack(sc.x, sc.x), lv2 = pack(sc.y, sc.y), lo_f = pack(1.f / kLoScale, 1.f / kLoScale);
-#pragma unroll
-                for (int c = 0; c < CT; c += LD) {
-                    float hi[LD], lo[LD];
-                    tmem_ld<LD>(my_s + c, hi);
-                    tmem_ld<LD>(my_s + RT + c, lo);
+                const int2 span = bs.span;
+                const bool edge = t0 + kTile - 1 > span.x || t0 <= span.y - win;
+                const u64 ks2 = pack(sc.x, sc.x), lv2 = pack(sc.y, sc.y);
+                // exponents: score * log2 e + log2 vs, -inf where not seen
+                float x[CT], most = kLow;
+                {
+                    float lo[CT];
+                    tmem_ld16(my_s, x);
+                    tmem_ld16(my_s + RT, lo);
                     tmem_ld_wait();
-                    tmem_regs_ready_n<LD>(hi);
-                    tmem_regs_ready_n<LD>(lo);
-                    if (c + LD == CT) {
-                        tc_fence_before();
-                        warp_arrive(&bs.s_free, lane);
-                    }
+                    tmem_regs_ready(x);
+                    tmem_regs_ready(lo);
+                    tc_fence_before();
+                    warp_arrive(&bs.s_free, lane);
+                    const u64 lo_f = pack(1.f / kLoScale, 1.f / kLoScale);
 #pragma unroll
-                    for (int i = 0; i < LD; i += 4) {
-                        const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(&bs.qs[col0 + c + i]);
-                        const u64 a0 = fma2(mul2(fma2(pack(lo[i], lo[i + 1]), lo_f, pack(hi[i], hi[i + 1])), s4.x), ks2, lv2);
-                        const u64 a1 = fma2(mul2(fma2(pack(lo[i + 2], lo[i + 3]), lo_f, pack(hi[i + 2], hi[i + 3])), s4.y), ks2, lv2);
-                        unpack(a0, x[c + i], x[c + i + 1]);
-                        unpack(a1, x[c + i + 2], x[c + i + 3]);
+                    for (int i = 0; i < CT; i += 4) {
+                        const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(&bs.qs[col0 + i]);
+                        const u64 a0 = fma2(pack(lo[i], lo[i + 1]), lo_f, pack(x[i], x[i + 1]));
+                        const u64 a1 = fma2(pack(lo[i + 2], lo[i + 3]), lo_f, pack(x[i + 2], x[i + 3]));
+                        unpack(fma2(mul2(a0, s4.x), ks2, lv2), x[i], x[i + 1]);
+                        unpack(fma2(mul2(a1, s4.y), ks2, lv2), x[i + 2], x[i + 3]);
                     }
                 }
                 if (edge) {
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        const int p = bs.pos[col0 + c];
-                        if (t > p || t <= p - win) x[c] = -INFINITY;
+                    for (int i = 0; i < CT; ++i) {
+                        const int p = bs.pos[col0 + i];
+                        if (t > p || t <= p - win) x[i] = -INFINITY;
                     }
                 }
-                if (j > 0) {
+                // the same relative to the rows' references, now
+                auto above = [&](float (&y)[CT]) {
 #pragma unroll
-                    for (int c = 0; c < CT; c += 4) {
-                        const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&nref[col0 + c]);
-                        float y0, y1, y2, y3;
-                        unpack(add2(pack(x[c], x[c + 1]), r4.x), y0, y1);
-                        unpack(add2(pack(x[c + 2], x[c + 3]), r4.y), y2, y3);
-                        most = fmaxf(most, fmaxf(fmaxf(y0, y1), fmaxf(y2, y3)));
+                    for (int i = 0; i < CT; i += 4) {
+                        const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&nref[col0 + i]);
+                        unpack(add2(pack(x[i], x[i + 1]), r4.x), y[i], y[i + 1]);
+                        unpack(add2(pack(x[i + 2], x[i + 3]), r4.y), y[i + 2], y[i + 3]);
                     }
+                };
+                float y[CT];
+                if (j > 0) {
+                    above(y);
+#pragma unroll
+                    for (int i = 0; i < CT; i += 2) most = max3(most, y[i], y[i + 1]);
                 }
                 if (j == 0 || soft_any<SOFT>(most > kRoom || fail)) {
                     // new references: the maximum of the tile's 128 tokens per row
                     float m = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        const float mc = warp_max(x[c]);
-                        if (lane == c) m = mc;
+                    for (int i = 0; i < CT; ++i) {
+                        const float mc = warp_max(x[i]);
+                        if (lane == i) m = mc;
                     }
                     if (lane < CT) bs.part[quad][col0 + lane] = m;
                     if (soft_any<SOFT>(fail)) {            // the same answer for every softmax thread
@@ -927,25 +934,21 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         tmem_st_wait();
                         tc_fence_before();
                     }
+                    above(y);
                 }
                 const u64 iv2 = pack(sc.z, sc.z);
                 // the weights of the last tile have been read
                 if (g > 0 && mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
-#pragma unroll
-                for (int c = 0; c < CT; c += 16) {
+                {
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const ulonglong2 r4 = *reinterpret_cast<const ulonglong2*>(&nref[col0 + c + i]);
-                        float y0, y1, y2, y3;
-                        unpack(add2(pack(x[c + i], x[c + i + 1]), r4.x), y0, y1);
-                        unpack(add2(pack(x[c + i + 2], x[c + i + 3]), r4.y), y2, y3);
-                        const float v0 = ex2(y0), v1 = ex2(y1), v2 = ex2(y2), v3 = ex2(y3);
-                        l2[(c + i) / 2] = fma2(pack(v0, v1), iv2, l2[(c + i) / 2]);
-                        l2[(c + i) / 2 + 1] = fma2(pack(v2, v3), iv2, l2[(c + i) / 2 + 1]);
+                    for (int i = 0; i < CT; i += 4) {
+                        const float v0 = ex2(y[i]), v1 = ex2(y[i + 1]), v2 = ex2(y[i + 2]), v3 = ex2(y[i + 3]);
+                        l2[i / 2] = fma2(pack(v0, v1), iv2, l2[i / 2]);
+                        l2[i / 2 + 1] = fma2(pack(v2, v3), iv2, l2[i / 2 + 1]);
                         split4<S::CAT>(v0, v1, v2, v3, &hi[i / 4], &lo[i / 4]);
                     }
-                    const int ch = (col0 + c) / 16;
+                    const int ch = col0 / 16;
                     unsigned char* ph = psm + chunk_at<S::kPitch>(tok, ch);
                     unsigned char* pl = S::CAT ? psm + chunk_at<S::kPitch>(tok, RT / 16 + ch) : ph + kTile * S::kPitch;
                     *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -981,7 +984,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 float l[CT];
 #pragma unroll
                 for (int c = 0; c < CT; c += 2) unpack(l2[c / 2], l[c], l[c + 1]);
-                column_sums<CT>(l, lane, &bs.part[quad][col0]);
+                column_sums(l, lane, &bs.part[quad][col0]);
             }
             soft_sync<SOFT>();                             // every warp is through with this segment's rows
             if (go) stage(next, k + 1);
@@ -1237,8 +1240,10 @@ cudaError_t run(const Cache& c, const CUtensorMap& km, const CUtensorMap& vm, co
 template <int DB, bool SHARED>
 cudaError_t run_rows(int rows, const Cache& c, const CUtensorMap& km, const CUtensorMap& vm, const Args& a, cudaStream_t st) {
     if (rows <= 16) return run<Shape<DB, 16, SHARED>>(c, km, vm, a, st);
-    if (rows <= 32) return run<Shape<DB, 32, SHARED>>(c, km, vm, a, st);
-    return run<Shape<DB, 64, SHARED>>(c, km, vm, a, st);
+    // (128-dim heads run two CTAs per SM, which leaves registers for 32 rows)
+    if constexpr (DB > 1)
+        if (rows > 32) return run<Shape<DB, 64, SHARED>>(c, km, vm, a, st);
+    return run<Shape<DB, 32, SHARED>>(c, km, vm, a, st);
 }
 
 template <int DB, int RT, bool SHARED>
@@ -1250,7 +1255,8 @@ template <int DB, bool SHARED>
 cudaError_t set_rows() {
     cudaError_t e = set_one<DB, 16, SHARED>();
     if (e == cudaSuccess) e = set_one<DB, 32, SHARED>();
-    if (e == cudaSuccess) e = set_one<DB, 64, SHARED>();
+    if constexpr (DB > 1)
+        if (e == cudaSuccess) e = set_one<DB, 64, SHARED>();
     return e;
 }
 
