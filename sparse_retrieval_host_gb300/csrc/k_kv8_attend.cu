@@ -85,10 +85,12 @@ struct Shape {
     static constexpr int kQBytes = DB * N * 128;
     static constexpr int kPBytes = kTile * N;
     static constexpr int kPitch = CAT ? N : RT;            // bytes of one token's row of p
-    static constexpr int CTAS = DB == 1 || (DB == 2 && RT == 16) ? 2 : 1;   // per SM
+    // CTAs per SM: four hide more of a decode step's latencies than fewer with longer
+    // rings do (64 requests of up to 16,384 tokens: 201 us; three 207, two 221)
+    static constexpr int CTAS = DB == 1 ? (RT == 16 ? 4 : 2) : DB == 2 && RT == 16 ? 2 : 1;
     // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
     // tile j is given back, so two tiles must fit
-    static constexpr int SLOTS = DB == 1 ? 5 : DB == 2 ? (RT == 16 ? 6 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
+    static constexpr int SLOTS = DB == 1 ? (RT == 16 ? 2 : 5) : DB == 2 ? (RT == 16 ? 6 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
     static_assert(SLOTS >= 2 * DB && SLOTS / DB + 2 < 8, "two tiles must fit the ring, and fewer than the scales held");
     // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the
     // columns. (32 columns a thread, for 64-row tiles with two CTAs per SM, need more
@@ -254,7 +256,7 @@ struct Walker {
             if (take != n) {
                 s->slot = 2 * v + (at == 0);
                 if (at == 0)       // the item goes on in the next chunks: for the join
-                    a.meta[v] = make_int4((ch->of(u + n - 1) - v + 1) | (s->nr << 16), r.q0, s->row0, h);
+                    a.meta[v] = make_int4((ch->of(u + n - 1) - v + 1) | (s->nr << 12) | (h << 20), r.q0, s->row0, 0);
             }
             u += take;
             off += take;
@@ -465,44 +467,59 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int n_grid = gridDim.x, cta = blockIdx.x;
 
     // ------------------------------------------------------------ the units
+    // Prefix sums over the requests: of a few by the TMA warp alone while the others
+    // set up, of many by every thread.
     const int per = (a.n_req + S::THREADS - 1) / S::THREADS;       // requests per thread (at most 22)
+    const bool few = a.n_req <= 32;
     bool bad = false;
-    int U, n_cta;
-    {
-        const int b0 = min(a.n_req, tid * per), b1 = min(a.n_req, b0 + per);
-        long long mine = 0, total;
+    if (warp == kWarpTma && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&kmap) : "memory");
+        if (!S::SHARED) asm volatile("prefetch.tensormap [%0];\n" ::"l"(&vmap) : "memory");
+    }
+    if (!few || warp == kWarpTma) {
+        const int i = few ? lane : tid;
+        const int b0 = min(a.n_req, i * per), b1 = min(a.n_req, b0 + per);
+        long long mine = 0, incl, total;
         for (int b = b0; b < b1; ++b) {
             const Request r = request<RT>(a, b, &bad);
             mine += (long long)r.pairs * r.P * a.kv_heads;
         }
-        const long long incl = block_scan(mine, bs.warp_sums, &total);
+        if (few) {
+            incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            total = __shfl_sync(0xffffffffu, incl, 31);
+        } else {
+            incl = block_scan(mine, bs.warp_sums, &total);
+        }
+        if (cta == 0 && bad) atomicOr(a.err, kErrBounds);
         if (total > kMaxUnits) {                           // too much for one call: reported, nothing written
-            if (tid == 0) atomicOr(a.err, kErrBounds);
+            if (i == 0) atomicOr(a.err, kErrBounds);
             total = 0;
         }
-        U = (int)total;
-        n_cta = min(n_grid, U);
+        const int U = (int)total, n_cta = min(n_grid, U);
         // rounds of smaller chunks only where even the smallest still has 4 units
         const int rounds = U >= 64 * n_cta ? kRounds : 1;
-        if (cta == 0 && tid == 0) a.ctrl[1] = n_cta * rounds;
-        if (cta >= n_cta) return;                          // nothing to do (every thread)
-        bs.before[tid] = (int)(incl - mine);
-        if (tid == 0) {
+        bs.before[i] = (int)(incl - mine);
+        if (i == 0) {
             bs.ch.n = n_cta;
             bs.ch.rounds = rounds;
+            if (cta == 0) a.ctrl[1] = n_cta * rounds;
         }
-        if (tid <= kRounds) {
+        if (i <= kRounds && cta < n_cta) {
             auto begin = [&](int r) { return rounds == 1 ? (r ? U : 0) : (int)((long long)U * cut(r) / 16); };
-            const int at = begin(tid);
-            bs.ch.at[tid] = at;
-            if (tid < kRounds) {
-                const uint32_t n = begin(tid + 1) - at;
-                bs.ch.base[tid] = n / (uint32_t)n_cta;
-                bs.ch.rem[tid] = n % (uint32_t)n_cta;
+            const int at = begin(i);
+            bs.ch.at[i] = at;
+            if (i < kRounds) {
+                const uint32_t n = begin(i + 1) - at;
+                bs.ch.base[i] = n / (uint32_t)n_cta;
+                bs.ch.rem[i] = n % (uint32_t)n_cta;
             }
         }
     }
-    if (cta == 0 && bad) atomicOr(a.err, kErrBounds);
     if (tid == 0) {
         for (int s = 0; s < S::SLOTS; ++s) {
             mbar_init(&bs.full[s], 1);
@@ -527,6 +544,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bs.tmem_base;
+    if (cta >= bs.ch.n) {                                  // nothing to do (every thread)
+        if (warp == kWarpMma) tmem_dealloc(tmem, S::ALLOC);
+        return;
+    }
     const uint32_t tm_s = tmem, tm_o = tmem + N;
 
     bool ok = true;
@@ -543,7 +564,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             w.v = v;
             w.u = ch.begin(v);
             w.u1 = ch.begin(v + 1);
-            int lo = 0, hi = S::THREADS;
+            int lo = 0, hi = min(a.n_req, S::THREADS);
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (bs.before[mid] <= w.u) lo = mid;
@@ -1073,7 +1094,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kFewParts = 12;
-constexpr int kMaxChunks = 1024;
+constexpr int kMaxChunks = 1920;   // 4 CTAs x 160 SMs x 3 rounds; a part count fits 12 bits
 
 // Weighted sum of parts [p0, p1) for 4 dims per lane; every lane gets sum w_i l_i.
 template <int RT>
@@ -1115,8 +1136,8 @@ __device__ __forceinline__ float4 join_parts(const Args& a, int v0, int parts, i
 template <int DB, int RT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
     __shared__ long long warp_sums[33];
-    __shared__ int4 item[kMaxChunks];                 // split items: (parts | rows << 16, first row of out, row, head)
-    __shared__ int chunk[kMaxChunks];                 // the chunk each begins in
+    // split items: (parts | rows << 12 | KV head << 20, first row of out, row, chunk it begins in)
+    __shared__ int4 item[kMaxChunks];
     __shared__ int first[kMaxChunks + 1];             // CTA jobs before each
     __shared__ float4 acc_s[kJoinWarps][32];
     __shared__ float sum_s[kJoinWarps];
@@ -1128,15 +1149,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int base = 0; base < n_chunks; base += kJoinThreads) {
         const int i = base + tid;
         int4 it = i < n_chunks ? __ldcg(&a.meta[i]) : make_int4(0, 0, 0, 0);
-        const int parts = it.x & 0xffff, jobs = (it.x >> 16) * DB;
+        const int parts = it.x & 0xfff, jobs = ((it.x >> 12) & 0xff) * DB;
         const int cta_jobs = parts <= kFewParts ? (jobs + kJoinWarps - 1) / kJoinWarps : jobs;
         // items in the high half, jobs in the low one
         long long total;
         const long long incl = block_scan(parts ? (1ll << 32) + cta_jobs : 0, warp_sums, &total);
         if (parts) {
             const int k = n_items + (int)(incl >> 32) - 1;
+            it.w = i;
             item[k] = it;
-            chunk[k] = i;
             first[k] = n_jobs + (int)(incl & 0xffffffff) - cta_jobs;
         }
         n_items += (int)(total >> 32);
@@ -1146,7 +1167,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int job = blockIdx.x; job < n_jobs; job += gridDim.x) {
         const int k = last_not_above(first, n_items, job);
         const int4 it = item[k];
-        const int parts = it.x & 0xffff, nr = it.x >> 16, v0 = chunk[k];
+        const int parts = it.x & 0xfff, nr = (it.x >> 12) & 0xff, v0 = it.w;
         const bool shared_job = parts > kFewParts;
         const int j = shared_job ? job - first[k] : (job - first[k]) * kJoinWarps + warp;
         if (j >= nr * DB) continue;                   // a warp without a job (never in a shared one)
@@ -1182,7 +1203,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
         const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-        const int rr = it.z + row, tok = rr / a.group, hd = it.w * a.group + rr % a.group;
+        const int rr = it.z + row, tok = rr / a.group, hd = (it.x >> 20) * a.group + rr % a.group;
         uint2 o;
         memcpy(&o.x, &lo, 4);
         memcpy(&o.y, &hi, 4);
@@ -1272,12 +1293,29 @@ cudaError_t set_attend_attrs() {
     return e;
 }
 
+namespace {
+template <int DB, int RT>
+void scratch_of(size_t sm_count, size_t* o_floats, size_t* ml_floats, size_t* meta) {
+    using S = Shape<DB, RT, false>;
+    const size_t chunks = S::CTAS * sm_count * kRounds;
+    const auto most = [](size_t* v, size_t n) { *v = *v < n ? n : *v; };
+    most(o_floats, chunks * 2 * RT * DB * 128);
+    most(ml_floats, chunks * 2 * RT * 2);
+    most(meta, chunks);
+}
+template <int DB>
+void scratch_of_dim(size_t sm_count, size_t* o_floats, size_t* ml_floats, size_t* meta) {
+    scratch_of<DB, 16>(sm_count, o_floats, ml_floats, meta);
+    scratch_of<DB, 32>(sm_count, o_floats, ml_floats, meta);
+    if (DB > 1) scratch_of<DB, 64>(sm_count, o_floats, ml_floats, meta);
+}
+}  // namespace
+
 void attend_scratch(int sm_count, int head_dim, size_t* o_floats, size_t* ml_floats, size_t* meta) {
-    const size_t grid = (size_t)sm_count * (head_dim <= 256 ? 2 : 1);   // CTAs of the widest grid
-    const size_t slots = grid * kRounds * 2;
-    *o_floats = slots * 64 * head_dim / (head_dim == 256 ? 2 : 1);   // 64 rows run one CTA per SM there
-    *ml_floats = slots * 2 * 64;
-    *meta = grid * kRounds;
+    *o_floats = *ml_floats = *meta = 0;
+    if (head_dim == 128) scratch_of_dim<1>(sm_count, o_floats, ml_floats, meta);
+    else if (head_dim == 256) scratch_of_dim<2>(sm_count, o_floats, ml_floats, meta);
+    else scratch_of_dim<4>(sm_count, o_floats, ml_floats, meta);
 }
 
 cudaError_t launch_attend(const Cache& c, const kv8_pool& pool, const int32_t* table, const int32_t* len,
