@@ -1263,7 +1263,9 @@ cudaError_t run(const Cache& c, const CUtensorMap& km, const CUtensorMap& vm, Ar
     attend_kernel<S><<<grid, S::THREADS, smem_bytes<S>(), st>>>(km, vm, a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_k(join_kernel<S::DB, S::RT>, dim3((unsigned)(4 * c.sm_count)), dim3(kJoinThreads), 0, st, true, a);
+    const cudaError_t j = launch_k(join_kernel<S::DB, S::RT>, dim3((unsigned)(4 * c.sm_count)), dim3(kJoinThreads), 0, st, true, a);
+    if (j != cudaSuccess) cudaMemsetAsync(c.d_ctrl, 0, 2 * sizeof(int), st);   // what the join does for the next call
+    return j;
 }
 
 template <int DB, bool SHARED>
@@ -1357,7 +1359,7 @@ cudaError_t launch_attend(const Cache& c, const kv8_pool& pool, const int32_t* t
     a.n_blocks = c.cfg.n_blocks;
     a.max_blocks = c.cfg.max_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.window = window;
+    a.window = window < (1 << 30) ? window : 0;            // (a request is at most 2^30 tokens long)
     // rows of an average request's KV head, in the smallest row tile that holds them
     const long long rows = (long long)a.group * ((n_rows + n_req - 1) / n_req);
     const int rt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;

@@ -138,13 +138,14 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     const int depth = *a.n_free;
     if (depth < 0 || depth > a.n_blocks || R > a.n_blocks - depth || N > 0x7fffffffll) bad = true;
     if (a.pos && N > a.cap) bad = true;
-    const bool none = !bad && A > depth + R;
     if (tid == 0) {
         rel[a.n_req] = (int)R;
         alc[a.n_req] = (int)A;
         tok[a.n_req] = (int)N;
     }
-    bad = __syncthreads_or(bad || none);
+    bad = __syncthreads_or(bad);
+    const bool none = !bad && A > depth + R;           // the same in every thread
+    bad = bad || none;
     if (!bad) {
         // a released entry that is no block fails the call before anything changes
         for (int i = tid; i < (int)R; i += nt) {
@@ -157,7 +158,6 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     }
     if (bad) {
         for (int b = tid; b <= a.n_req; b += nt) a.cu[b] = 0;
-        // `none` is the same in every thread unless another check failed too
         if (tid == 0) atomicOr(a.err, none ? kErrNoBlocks : kErrBounds);
         return;
     }

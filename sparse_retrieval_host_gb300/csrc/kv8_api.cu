@@ -1,5 +1,6 @@
 // Host side of the paged 8-bit cache's C ABI (kv8_*): handles, argument checks,
 // launches. Every call runs on the handle's device, whichever is current.
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <new>
@@ -108,9 +109,15 @@ int kv8_create(const kv8_config* cfg, kv8_cache** out) {
     cudaError_t e = cudaGetDevice(&c->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device);
     if (e == cudaSuccess) {
+        // once per device: 18 calls of a few microseconds
+        static std::atomic<uint64_t> set{0};
+        const uint64_t bit = c->device < 64 ? 1ull << c->device : 0;
         where = "kernel attributes";
-        e = kv8::set_attend_attrs();
-        if (e == cudaSuccess) e = kv8::set_resize_attrs();
+        if (!bit || !(set.load() & bit)) {
+            e = kv8::set_attend_attrs();
+            if (e == cudaSuccess) e = kv8::set_resize_attrs();
+            if (e == cudaSuccess) set.fetch_or(bit);
+        }
     }
     if (e == cudaSuccess) {
         where = "device scratch";

@@ -116,6 +116,14 @@ class PagedKV8:
             return _current_stream(self.device.index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
+    def _empty(self, shape, dtype, stream) -> torch.Tensor:
+        """A new output of a call on ``stream``: its memory belongs to that stream."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        s = torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(s):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
     def _rows(self, t: torch.Tensor, name: str, heads: Optional[int] = None, dim: Optional[int] = None) -> int:
         """Row stride (elements) of a bf16 [rows][heads][dim] tensor with dense rows."""
         if t.dtype not in _BF16 or t.dim() != 3 or t.device != self.device:
@@ -155,9 +163,9 @@ class PagedKV8:
         if n_new < 0:
             raise ValueError("n_new must be >= 0")
         if out is None:
-            cu = torch.empty(n + 1, dtype=torch.int32, device=self.device)
-            pos = torch.empty(n_new, dtype=torch.int32, device=self.device) if n_new else None
-            slot = torch.empty(n_new, dtype=torch.int64, device=self.device) if n_new else None
+            cu = self._empty(n + 1, torch.int32, stream)
+            pos = self._empty(n_new, torch.int32, stream) if n_new else None
+            slot = self._empty(n_new, torch.int64, stream) if n_new else None
         else:
             cu, pos, slot = out
             self._ints(cu, "cu", n + 1)
@@ -204,7 +212,7 @@ class PagedKV8:
                 if out is None:
                     raise ValueError(f"{name}_slot needs {name}_out")
             if out is None:
-                out = torch.empty((n, x.shape[1], d), dtype=x.dtype, device=self.device)
+                out = self._empty((n, x.shape[1], d), x.dtype, stream)
             out_row = self._rows(out, name + "_out", x.shape[1], d)
             if slot is None and out.shape[0] != n:
                 raise ValueError(f"{name}_out must have a row per token")
@@ -241,7 +249,7 @@ class PagedKV8:
         n = self._requests(cu)
         qr = self._rows(q, "q", None, self.D)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+            out = self._empty(q.shape, q.dtype, stream)
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
         orow = self._rows(out, "out", None, self.D)

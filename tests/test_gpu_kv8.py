@@ -733,3 +733,111 @@ def test_a_captured_step():
         _check_attend(c, q, cu, out, 0.09, 0)
     assert c.len.tolist() == [120, 23, 60, 270] and c.check_error() == 0
     c.close()
+
+
+# ---------------------------------------------------------------------------------------------- further shapes and uses
+@pytest.mark.parametrize("n_req", [33, 200, 1500])
+def test_attend_many_requests(n_req):
+    rng = np.random.default_rng(n_req)
+    lens = rng.integers(0, 90, n_req)
+    nq = np.minimum(rng.integers(0, 4, n_req), lens)
+    _attend(lens.tolist(), nq.tolist(), 4, 2, 128, 16, False, seed=n_req, pad=1)
+
+
+@pytest.mark.parametrize("D,shared,G,q", [(128, False, 3, 700), (512, True, 64, 9), (512, False, 5, 90), (256, False, 33, 20),
+                                          (256, True, 1, 1000), (128, True, 100, 7)])
+@pytest.mark.parametrize("window", [0, 300, 2 ** 31 - 1])
+def test_attend_many_row_tiles(D, shared, G, q, window):
+    _attend([q + 5, 2 * q, 130, q // 2], [q, q, 1, q // 2 + 3], G, 1, D, 32, shared, window=window, seed=G, pad=3)
+
+
+def test_attend_rows_that_come_into_sight_late():
+    """Windows of one row tile that begin in different tiles: a row's reference is
+    set by a tile that is not the segment's first."""
+    _attend([1200], [600], 1, 1, 128, 16, False, window=40, seed=5)
+    _attend([1200], [60], 8, 1, 256, 16, True, window=3, seed=6)
+
+
+def test_attend_strided_queries_and_outputs():
+    c, g = _filled([300, 77], 2, 128, 16, False, 61)
+    row = _bf16(g, 5, 3, 8, 128)                           # queries between other things, outputs too
+    q, cu = row[:, 1], _i32([0, 3, 5])
+    want = c.attend(q.contiguous(), cu, scale=0.06)
+    out = torch.full((5, 2, 8, 128), 9.0, device="cuda").bfloat16()
+    c.attend(q, cu, scale=0.06, out=out[:, 1])
+    assert torch.equal(out[:, 1], want) and (out[:, 0] == 9).all()
+    one = row[:1, 1].expand(5, 8, 128)                     # the same query five times, without copies
+    assert torch.equal(c.attend(one, cu, scale=0.06), c.attend(one.contiguous(), cu, scale=0.06))
+    bits = q.contiguous().view(torch.int16)                # bit patterns, as DecodeStep holds them
+    assert torch.equal(c.attend(bits, cu, scale=0.06).view(torch.bfloat16), want)
+    c.close()
+
+
+def test_two_caches_on_two_streams():
+    a, ga = _filled([4000, 900], 2, 128, 16, False, 71)
+    b, gb = _filled([3000, 50, 700], 1, 512, 64, True, 72)
+    qa, qb = _bf16(ga, 2, 16, 128), _bf16(gb, 3, 64, 512)
+    ca, cb = _i32([0, 1, 2]), _i32([0, 1, 2, 3])
+    wa, wb = a.attend(qa, ca, scale=0.08), b.attend(qb, cb, scale=0.03)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(20):
+        outs.append((a.attend(qa, ca, scale=0.08, stream=sa), b.attend(qb, cb, scale=0.03, stream=sb.cuda_stream)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, wa) and torch.equal(y, wb) for x, y in outs)
+    a.close()
+    b.close()
+
+
+def test_block_table_order_does_not_show():
+    """The same rows in other blocks give the same bits."""
+    c, g = _filled([500, 260], 2, 128, 16, False, 81)
+    q, cu = _bf16(g, 3, 8, 128), _i32([0, 1, 3])
+    want = c.attend(q, cu, scale=0.07)
+    perm = torch.randperm(c.n_blocks, generator=g, device="cuda")
+    for t in (c.k_codes[0], c.v_codes[0], c.k_scale[0], c.v_scale[0]):
+        t[perm] = t.clone()
+    c.table.copy_(torch.where(c.table >= 0, perm[c.table.clamp(min=0).long()].int(), c.table))
+    assert torch.equal(c.attend(q, cu, scale=0.07), want)
+    c.close()
+
+
+def test_refusals():
+    abi = _abi()
+    c = _paged(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=8, max_blocks=4)
+    s = _paged(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=8, max_blocks=4, shared_kv=True)
+    g = _gen(1)
+    q, k, cu = _bf16(g, 3, 4, 128), _bf16(g, 3, 2, 128), _i32([0, 1, 3])
+    freq, pos = torch.ones(16, dtype=torch.float64, device="cuda"), _i32([1, 2, 3])
+    value = [lambda: c.attend(q[:, :, ::2], cu, scale=1.0), lambda: c.attend(q.float(), cu, scale=1.0),
+             lambda: c.attend(q, cu.long(), scale=1.0), lambda: c.attend(q, _i32([0]), scale=1.0),
+             lambda: c.attend(q, _i32([0, 1, 2, 3]), scale=1.0), lambda: c.attend(q.cpu(), cu, scale=1.0),
+             lambda: c.attend(q, cu, scale=1.0, out=q[:2]), lambda: c.append(k, None, cu), lambda: s.append(k, k, cu),
+             lambda: c.append(k, k[:2], cu), lambda: c.append(q, q, cu), lambda: c.resize(_i32([1, 2, 3])),
+             lambda: c.resize(_i32([1, 2]), -1), lambda: c.norm_rope(q, style="spiral"), lambda: c.norm_rope(),
+             lambda: c.norm_rope(q, k[:2]), lambda: c.norm_rope(q, pos=pos, inv_freq=freq, rot_dim=64),
+             lambda: c.norm_rope(q, q_slot=pos.long()), lambda: c.norm_rope(q, q_weight=freq)]
+    for f in value:
+        with pytest.raises(ValueError):
+            f()
+    code = [lambda: c.attend(_bf16(g, 3, 3, 128), cu, scale=1.0), lambda: c.attend(q, cu, scale=float("nan")),
+            lambda: c.attend(q, cu, scale=1.0, window=-1), lambda: c.attend(q, cu, scale=1.0, out=q),
+            lambda: c.norm_rope(q, pos=pos, inv_freq=freq[:12], rot_dim=24), lambda: c.norm_rope(q, eps=-1.0),
+            lambda: c.norm_rope(q, pos=pos, inv_freq=freq, rot_dim=32, rot_off=100),
+            lambda: c.norm_rope(_bf16(g, 3, 4, 20)), lambda: c.norm_rope(_bf16(g, 3, 1, 520)),
+            lambda: c.norm_rope(q, q_out=q, q_slot=pos.long()),
+            lambda: c.attend(_bf16(g, 3, 4 * 128 + 4)[:, 4:].view(3, 4, 128), cu, scale=1.0)]
+    for f in code:
+        with pytest.raises(abi.SrhError) as ei:
+            f()
+        assert ei.value.code == abi.SRH_ERR_INVALID and str(ei.value)
+    assert c.check_error() == 0
+    # nothing to do is no error
+    empty = torch.empty((0, 4, 128), dtype=torch.bfloat16, device="cuda")
+    assert c.attend(empty, cu, scale=1.0).shape == empty.shape
+    c.append(empty[:, :2], empty[:, :2], cu)
+    c.norm_rope(empty)
+    c.close()
+    s.close()
+    c.close()
