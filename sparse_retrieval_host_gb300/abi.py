@@ -393,30 +393,6 @@ def kv8_destroy(cache) -> None:
     load().kv8_destroy(cache)
 
 
-def kv8_resize(cache, new_len, n_req, length, table, free, n_free, cu, pos, slot, cap, stream=None) -> None:
-    _check_kv8(load().kv8_resize(cache, _ptr(new_len), n_req, _ptr(length), _ptr(table), _ptr(free), _ptr(n_free),
-                                 _ptr(cu), _ptr(pos), _ptr(slot), cap, _stream(stream)), "kv8_resize", cache)
-
-
-def kv8_norm_rope(cache, q, k, n_tok, head_dim, pos, inv_freq, rot_dim, rot_off, style, eps, stream=None) -> None:
-    """q, k: Kv8Heads or None."""
-    ref = lambda h: None if h is None else ctypes.byref(h)
-    _check_kv8(load().kv8_norm_rope(cache, ref(q), ref(k), n_tok, head_dim, _ptr(pos), _ptr(inv_freq), rot_dim, rot_off,
-                                    style, float(eps), _stream(stream)), "kv8_norm_rope", cache)
-
-
-def kv8_append(cache, pool: Kv8Pool, table, length, cu, n_req, k, k_row, v, v_row, n_rows, stream=None) -> None:
-    _check_kv8(load().kv8_append(cache, ctypes.byref(pool), _ptr(table), _ptr(length), _ptr(cu), n_req, _ptr(k), k_row,
-                                 _ptr(v), v_row, n_rows, _stream(stream)), "kv8_append", cache)
-
-
-def kv8_attend(cache, pool: Kv8Pool, table, length, cu, n_req, q, q_row, n_rows, n_heads, scale, window, out, out_row,
-               stream=None) -> None:
-    _check_kv8(load().kv8_attend(cache, ctypes.byref(pool), _ptr(table), _ptr(length), _ptr(cu), n_req, _ptr(q), q_row,
-                                 n_rows, n_heads, float(scale), window, _ptr(out), out_row, _stream(stream)),
-               "kv8_attend", cache)
-
-
 def kv8_check_error(cache) -> int:
     """Returns the code (does not raise): SRH_OK, SRH_ERR_NOMEM, SRH_ERR_BOUNDS, SRH_ERR_TIMEOUT or SRH_ERR_RANGE."""
     return load().kv8_check_error(cache)

@@ -15,6 +15,7 @@ tensors and names streams. Calls on one cache are ordered by the caller.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -107,10 +108,19 @@ class PagedKV8:
                 codes.append(c)
                 scale.append(tensor(part + "_scale", (n_blocks, n_kv_heads), torch.float32,
                                     lambda: torch.ones((n_blocks, n_kv_heads), device=self.device)))
-            self._pool.append(abi.Kv8Pool(self.k_codes[-1].data_ptr(), self.k_scale[-1].data_ptr(),
-                                          self.v_codes[-1].data_ptr(), self.v_scale[-1].data_ptr()))
+            pool = abi.Kv8Pool(self.k_codes[-1].data_ptr(), self.k_scale[-1].data_ptr(),
+                               self.v_codes[-1].data_ptr(), self.v_scale[-1].data_ptr())
+            self._pool.append(ctypes.byref(pool))
+        # what every call passes, taken once: the cache's own tensors stay where they are
+        self._lib = abi.load()
+        self._index = self.device.index
+        self._table, self._len = self.table.data_ptr(), self.len.data_ptr()
+        self._free, self._n_free = self.free.data_ptr(), self.n_free.data_ptr()
 
     # ------------------------------------------------------------------ checks
+    def _raise(self, rc: int, where: str) -> None:
+        raise abi.SrhError(rc, where, self._lib.kv8_last_error(self.cache).decode(errors="replace"))
+
     def _s(self, stream) -> int:
         if stream is None:
             return _current_stream(self.device.index)
@@ -126,7 +136,7 @@ class PagedKV8:
 
     def _rows(self, t: torch.Tensor, name: str, heads: Optional[int] = None, dim: Optional[int] = None) -> int:
         """Row stride (elements) of a bf16 [rows][heads][dim] tensor with dense rows."""
-        if t.dtype not in _BF16 or t.dim() != 3 or t.device != self.device:
+        if t.dtype not in _BF16 or t.dim() != 3 or t.get_device() != self._index:
             raise ValueError(f"{name} must be bf16 [rows][heads][dim] on {self.device}")
         n, h, d = t.shape
         if (heads is not None and h != heads) or (dim is not None and d != dim):
@@ -137,7 +147,7 @@ class PagedKV8:
         return st[0] if n > 1 else h * d
 
     def _ints(self, t: torch.Tensor, name: str, n: Optional[int] = None, dtype=torch.int32) -> None:
-        if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or t.device != self.device:
+        if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or t.get_device() != self._index:
             raise ValueError(f"{name} must be a dense 1-d {dtype} on {self.device}")
         if n is not None and t.shape[0] != n:
             raise ValueError(f"{name} must have {n} entries")
@@ -174,8 +184,11 @@ class PagedKV8:
                 self._ints(slot, "slot", n_new, torch.int64)
             else:
                 pos = slot = None
-        abi.kv8_resize(self.cache, new_len, n, self.len, self.table, self.free, self.n_free, cu, pos, slot, n_new,
-                       self._s(stream))
+        rc = self._lib.kv8_resize(self.cache, new_len.data_ptr(), n, self._len, self._table, self._free, self._n_free,
+                                  cu.data_ptr(), pos.data_ptr() if n_new else None, slot.data_ptr() if n_new else None,
+                                  n_new, self._s(stream))
+        if rc:
+            self._raise(rc, "kv8_resize")
         return cu, pos, slot
 
     def norm_rope(self, q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None, *, pos=None, inv_freq=None,
@@ -221,8 +234,11 @@ class PagedKV8:
                                       0 if slot is None else out.shape[0]))
             outs.append(out)
         if n:
-            abi.kv8_norm_rope(self.cache, parts[0], parts[1], n, d, pos if rot_dim else None, inv_freq if rot_dim else None,
-                              rot_dim, rot_off, _STYLES[style], eps, self._s(stream))
+            rc = self._lib.kv8_norm_rope(self.cache, parts[0], parts[1], n, d, pos.data_ptr() if rot_dim else None,
+                                         inv_freq.data_ptr() if rot_dim else None, rot_dim, rot_off, _STYLES[style], eps,
+                                         self._s(stream))
+            if rc:
+                self._raise(rc, "kv8_norm_rope")
         return outs[0], outs[1]
 
     def append(self, k: torch.Tensor, v: Optional[torch.Tensor], cu: torch.Tensor, *, layer: int = 0, stream=None) -> None:
@@ -238,8 +254,10 @@ class PagedKV8:
             if v.shape[0] != k.shape[0]:
                 raise ValueError("k and v must have the same rows")
         if k.shape[0]:
-            abi.kv8_append(self.cache, self._pool[layer], self.table, self.len, cu, n, k, kr, v, vr, k.shape[0],
-                           self._s(stream))
+            rc = self._lib.kv8_append(self.cache, self._pool[layer], self._table, self._len, cu.data_ptr(), n, k.data_ptr(),
+                                      kr, None if v is None else v.data_ptr(), vr, k.shape[0], self._s(stream))
+            if rc:
+                self._raise(rc, "kv8_append")
 
     def attend(self, q: torch.Tensor, cu: torch.Tensor, *, scale: float, window: int = 0, out=None, layer: int = 0,
                stream=None) -> torch.Tensor:
@@ -254,8 +272,10 @@ class PagedKV8:
             raise ValueError("out must have q's shape")
         orow = self._rows(out, "out", None, self.D)
         if q.shape[0]:
-            abi.kv8_attend(self.cache, self._pool[layer], self.table, self.len, cu, n, q, qr, q.shape[0], q.shape[1], scale,
-                           window, out, orow, self._s(stream))
+            rc = self._lib.kv8_attend(self.cache, self._pool[layer], self._table, self._len, cu.data_ptr(), n, q.data_ptr(),
+                                      qr, q.shape[0], q.shape[1], scale, window, out.data_ptr(), orow, self._s(stream))
+            if rc:
+                self._raise(rc, "kv8_attend")
         return out
 
     # ------------------------------------------------------------------ status
