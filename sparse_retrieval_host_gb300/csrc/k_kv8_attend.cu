@@ -507,7 +507,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             if (i == 0) atomicOr(a.err, kErrBounds);
             total = 0;
         }
-        const int U = (int)total, n_cta = min(n_grid, U);
+        // as few CTAs as keep the largest share the same: fewer parts to join
+        const int U = (int)total, most = (U + n_grid - 1) / n_grid;
+        const int n_cta = U ? (U + most - 1) / most : 0;
         // rounds of smaller chunks only where even the smallest still has 4 units
         const int rounds = U >= 64 * n_cta ? kRounds : 1;
         bs.before[i] = (int)(incl - mine);
@@ -1096,9 +1098,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 // Row r of a split item: its parts' references m_i and sums l_i give weights
 // 2^(m_i - max m); out = sum w_i O_i / sum w_i l_i, in part order. A job is 128
 // dims of one row: 4 per lane of a warp. Items of few parts give a warp a job
-// each; of an item of many (one long request), a CTA's 8 warps share a job's
+// each; of an item of many (one long request), a CTA's warps share a job's
 // parts and add up in warp order. Latency-bound: a chain of three loads.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kFewParts = 12;
 constexpr int kMaxChunks = 1920;   // 4 CTAs x 160 SMs x 3 rounds; a part count fits 12 bits
@@ -1147,7 +1149,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     __shared__ int4 item[kMaxChunks];
     __shared__ int first[kMaxChunks + 1];             // CTA jobs before each
     __shared__ float4 acc_s[kJoinWarps][32];
-    __shared__ float sum_s[kJoinWarps];
+    __shared__ float sum_s[kJoinWarps], max_s[kJoinWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     const int n_chunks = min(a.ctrl[1], kMaxChunks);
@@ -1180,9 +1182,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         if (j >= nr * DB) continue;                   // a warp without a job (never in a shared one)
         const int row = j / DB, d = (j - row * DB) * 128;
         float m = kLow;
-        for (int i = lane; i < parts; i += 32) {
+        auto see = [&](int i) {
             const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + (size_t)(2 * (v0 + i) + (i == 0)) * RT + row);
             if (v.y != 0.f) m = fmaxf(m, v.x);
+        };
+        if (shared_job) {
+            for (int i = tid; i < parts; i += kJoinThreads) see(i);
+            m = warp_max(m);
+            if (lane == 0) max_s[warp] = m;
+            __syncthreads();
+            m = max_s[lane % kJoinWarps];
+        } else {
+            for (int i = lane; i < parts; i += 32) see(i);
         }
         m = warp_max(m);
         const int p0 = shared_job ? parts * warp / kJoinWarps : 0;
