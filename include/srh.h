@@ -554,7 +554,8 @@ int srh_selftest_wait_timeout(srh_ctx* ctx, int limit_us, srh_stream_t stream);
  *          aligned, block_stride bytes from one block to the next
  *   scale  fp32 [n_blocks][n_kv_heads]; a value is code * scale. A scale lies
  *          in [2^-64, 2^64] (kv8_append writes powers of two in that range;
- *          an appended value that would need a larger one is saturated)
+ *          an appended value that would need a larger one is saturated;
+ *          kv8_attend reads a V scale below 2^-64, 0 included, as 2^-64)
  *   table  int32 [batch][max_blocks]: block of tokens [j * block_tokens, ...)
  *          of each request
  *   len    int32 [batch]: tokens of each request

@@ -666,6 +666,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 ok = load(id, false);
                 if (!ok) break;
                 // (tile g - kScales was read before the slot just taken came free)
+                vs = vs < 5.421010862427522e-20f ? 5.421010862427522e-20f : vs;   // 2^-64: a scale of 0 too
                 if (lane < bpt)
                     bs.sc[g % kScales][lane] = there ? make_float4(ks, lg2(vs), __fdividef(1.f, vs), 0.f)
                                                      : make_float4(0.f, -INFINITY, 0.f, 0.f);

@@ -841,3 +841,16 @@ def test_refusals():
     c.close()
     s.close()
     c.close()
+
+
+def test_attend_scales_of_zero():
+    """A block of zeros with a scale of 0: its tokens still take part in the softmax."""
+    c, g = _filled([64, 40], 1, 128, 16, False, 97, spread=0)
+    blk = int(c.table[0, 1])
+    c.v_scale[0][blk] = 0
+    c.v_codes[0][blk] = 0
+    c.k_scale[0][int(c.table[1, 0])] = 0
+    q, cu = _bf16(g, 2, 4, 128), _i32([0, 1, 2])
+    out = c.attend(q, cu, scale=0.02)
+    _check_attend(c, q, cu, out, 0.02, 0)
+    c.close()
