@@ -40,11 +40,11 @@
 // fp32 partial sums, which a second kernel joins in chunk order: who ran a
 // chunk does not show, and results repeat bit for bit.
 //
-// Roles: 4 to 16 softmax warps (a thread holds one token and 16 or 32 rows;
-// they also bring queries in and outputs out), one TMA warp (one box per block
-// of tokens and 128 values, into a ring of tile slots), one MMA warp. QK of tile
-// j + 1 is issued before PV of tile j. Every wait is bounded; on a timeout the CTA records it, lets its
-// copies and MMAs end, frees TMEM and returns.
+// Roles: 4 to 16 softmax warps (a thread holds one token and 16 rows; they also
+// bring queries in and outputs out), one TMA warp (one box per block of tokens
+// and 128 values, into a ring of 16 KB slots), one MMA warp. QK of tile j + 1 is
+// issued before PV of tile j. Every wait is bounded; on a timeout the CTA records
+// it, lets its copies and MMAs end, frees TMEM and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -94,8 +94,8 @@ struct Shape {
     static_assert(SLOTS >= 2 * DB && SLOTS / DB + 2 < 8, "two tiles must fit the ring, and fewer than the scales held");
     // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the
     // columns. (32 columns a thread, for 64-row tiles with two CTAs per SM, need more
-    // than the 96 registers there are: a prompt chunk of 128-dim heads took 610 us
-    // with them and takes 580 with tiles of 32 rows.)
+    // than the 96 registers there are: a prompt chunk of 128-dim heads took 613 us
+    // with them and takes 545 with tiles of 32 rows.)
     static constexpr int CT = 16;
     static constexpr int CG = RT / CT;
     static constexpr int SOFT = 128 * CG;                  // softmax threads
@@ -832,7 +832,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             fence_async_smem();
             warp_arrive(&bs.q_full, lane);
         };
-        if (mbar_wait_abort(&bs.seg_full[0], 0, abort) <= 0) fail = true;
+        // (what a warp does after a failed wait, all its lanes do: collectives follow)
+        auto warp_got = [&](uint64_t* bar, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, mbar_wait_abort(bar, parity, abort) > 0);
+        };
+        if (!warp_got(&bs.seg_full[0], 0)) fail = true;
         else {
             if (bs.seg[0].n > 0) load_q(bs.seg[0]);
             if (bs.seg[0].b >= 0) stage(bs.seg[0], 0);
@@ -943,22 +947,21 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         l2[c / 2 + 3] = mul2(l2[c / 2 + 3], fb.y);
                         if (j == 0) continue;
                         constexpr int KO = DB * (S::CAT ? 2 : 1);          // 8-column pieces of these rows
+                        static_assert(KO % 2 == 0, "taken two at a time");
 #pragma unroll 1
                         for (int i = 0; i < KO; i += 2) {
                             const uint32_t at = my_o + i * (S::CAT ? RT : S::ON) + c;
                             const uint32_t at2 = at + (S::CAT ? RT : S::ON);   // (CAT: hi and lo alternate, RT apart)
                             float o[8], p[8];
                             tmem_ld<8>(at, o);
-                            if (KO > 1) tmem_ld<8>(at2, p);
+                            tmem_ld<8>(at2, p);
                             tmem_ld_wait();
                             tmem_regs_ready_n<8>(o);
                             scale8(o, fa, fb);
                             tmem_st<8>(at, o);
-                            if (KO > 1) {
-                                tmem_regs_ready_n<8>(p);
-                                scale8(p, fa, fb);
-                                tmem_st<8>(at2, p);
-                            }
+                            tmem_regs_ready_n<8>(p);
+                            scale8(p, fa, fb);
+                            tmem_st<8>(at2, p);
                         }
                     }
                     if (j > 0) {
@@ -1008,7 +1011,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             // the next segment's queries, so that its first product runs during the outputs
             const Segment& next = bs.seg[(k + 1) % kSegs];
             bool go = false;
-            if (mbar_wait_abort(&bs.seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1, abort) <= 0) fail = true;
+            if (!warp_got(&bs.seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1)) fail = true;
             else go = next.b >= 0;
             if (go && next.n > 0) load_q(next);
             if (n > 0) {
