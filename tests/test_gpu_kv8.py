@@ -843,6 +843,43 @@ def test_refusals():
     c.close()
 
 
+def test_blocks_past_four_gigabytes():
+    """Blocks whose codes lie beyond 32-bit offsets: written, read back, attended."""
+    n_blocks, Hk, bs = 34000, 8, 128                       # 131,072 bytes a block
+    c = _paged(batch=2, n_kv_heads=Hk, head_dim=128, block_tokens=bs, n_blocks=n_blocks, max_blocks=40, shared_kv=True)
+    g = _gen(91)
+    c.free.copy_(torch.arange(n_blocks, dtype=torch.int32, device="cuda"))       # the last block on top
+    cu, _, slot = c.resize(_i32([700, 300]), 1000)
+    assert int(c.table[0, 0]) == n_blocks - 1 and int(slot.max()) >= n_blocks * bs - bs
+    k = _bf16(g, 1000, Hk, 128)
+    c.append(k, None, cu)
+    ids = c.table[0, :6].long()
+    got = (c.k_codes[0][ids].view(FP8).float() * c.k_scale[0][ids][:, :, None, None]).transpose(1, 2).reshape(-1, Hk, 128)[:700]
+    # e4m3 after a power of two: 2^-4 of the value, or half of 2^-9 steps of the block's scale
+    tol = 2.0 ** -4 * k[:700].float().abs() + 2.0 ** -10 * float(c.k_scale[0][ids].max())
+    assert ((got - k[:700].float()).abs() <= tol).all()
+    q, cq = _bf16(g, 3, 16, 128), _i32([0, 1, 3])
+    out = c.attend(q, cq, scale=0.08)
+    assert c.check_error() == 0
+    _check_attend(c, q, cq, out, 0.08, 0)
+    c.close()
+
+
+def test_attend_chunks_taken_as_ctas_come_free():
+    """Enough work that chunks are handed out while the kernel runs: the same bits
+    every time, and the formula's values."""
+    c, g = _filled([30000 + 77 * b for b in range(12)], 16, 128, 128, True, 95, spread=0)
+    q, cu = _bf16(g, 12, 32, 128), _i32(list(range(13)))
+    want = c.attend(q, cu, scale=0.01)
+    for _ in range(4):
+        assert torch.equal(c.attend(q, cu, scale=0.01), want)
+    one = type("Some", (), dict(D=128, Hk=16, bs=128, len=c.len[[0, 11]], table=c.table[[0, 11]], k_codes=c.k_codes,
+                                v_codes=c.v_codes, k_scale=c.k_scale, v_scale=c.v_scale))
+    _check_attend(one, q[[0, 11]], _i32([0, 1, 2]), want[[0, 11]], 0.01, 0)
+    assert c.check_error() == 0
+    c.close()
+
+
 def test_attend_scales_of_zero():
     """A block of zeros with a scale of 0: its tokens still take part in the softmax."""
     c, g = _filled([64, 40], 1, 128, 16, False, 97, spread=0)
