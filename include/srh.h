@@ -616,7 +616,8 @@ void kv8_destroy(kv8_cache* c);
  * growing and shrinking back restores the stack. All or nothing: when a length
  * is out of range, a released entry is no block, the free blocks or cap do not
  * suffice, nothing changes, d_cu is all zeros, and kv8_check_error() returns
- * SRH_ERR_NOMEM (too few free blocks) or SRH_ERR_BOUNDS.
+ * SRH_ERR_NOMEM (too few free blocks) or SRH_ERR_BOUNDS. Users of a block are
+ * not counted: each request that gives an entry up pushes its block.
  */
 int kv8_resize(kv8_cache* c, const int32_t* d_new_len, int n_req, int32_t* d_len, int32_t* d_table, int32_t* d_free,
                int32_t* d_n_free, int32_t* d_cu, int32_t* d_pos, int64_t* d_slot, int cap, srh_stream_t stream);

@@ -70,6 +70,8 @@ class PagedKV8:
             inner = (block_tokens * head_dim, head_dim, 1)
             if t.dtype != torch.uint8 or tuple(t.shape) != shape or t.stride()[1:] != inner or t.device != self.device:
                 raise ValueError(f"{name} must be uint8 {shape} on {self.device}, dense within a block")
+            if n_blocks > 1 and t.stride(0) < t[0].numel():
+                raise ValueError(f"{name}: blocks must not overlap")
             if stride and n_blocks > 1 and t.stride(0) != stride:
                 raise ValueError("k_codes and v_codes must have the same block stride")
             stride = t.stride(0) if n_blocks > 1 else 0

@@ -891,3 +891,13 @@ def test_attend_scales_of_zero():
     out = c.attend(q, cu, scale=0.02)
     _check_attend(c, q, cu, out, 0.02, 0)
     c.close()
+
+
+def test_pools_whose_blocks_overlap_are_refused():
+    """A pool of repeated blocks (stride 0) or of overlapping ones: writes would meet, or leave the tensor."""
+    flat = torch.zeros(4 * 16 * 128, dtype=torch.uint8, device="cuda")
+    for stride in (0, 16, 16 * 128 - 16):
+        t = flat.as_strided((4, 1, 16, 128), (stride, 16 * 128, 128, 1))
+        with pytest.raises(ValueError, match="overlap"):
+            _paged(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=4, max_blocks=4, shared_kv=True,
+                   buffers={"k_codes": t})
