@@ -1162,7 +1162,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int base = 0; base < n_chunks; base += kJoinThreads) {
         const int i = base + tid;
         int4 it = i < n_chunks ? __ldcg(&a.meta[i]) : make_int4(0, 0, 0, 0);
-        const int parts = it.x & 0xfff, jobs = ((it.x >> 12) & 0xff) * DB;
+        int parts = it.x & 0xfff;
+        const int nr = (it.x >> 12) & 0xff, jobs = nr * DB;
+        // (when every CTA gave up on a wait, chunks nobody took still hold an earlier call's items)
+        if (nr > RT || (it.x >> 20) >= a.kv_heads || parts > n_chunks - i || it.y + (it.z + nr - 1) / a.group >= a.n_rows)
+            parts = 0;
         const int cta_jobs = parts <= kFewParts ? (jobs + kJoinWarps - 1) / kJoinWarps : jobs;
         // items in the high half, jobs in the low one
         long long total;
