@@ -901,3 +901,32 @@ def test_pools_whose_blocks_overlap_are_refused():
         with pytest.raises(ValueError, match="overlap"):
             _paged(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=4, max_blocks=4, shared_kv=True,
                    buffers={"k_codes": t})
+
+
+@pytest.mark.parametrize("D,H,Hk,T", [(128, 5, 3, 7001), (64, 3, 0, 9000), (512, 3, 1, 2500), (256, 1, 1, 6000), (24, 1, 2, 11000)])
+def test_norm_ranges_cross_tokens(D, H, Hk, T):
+    """Warps whose heads belong to several tokens and to both kinds, begin and end inside one, with tokens left out."""
+    g = _gen(101 + D)
+    c = _paged(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=1, max_blocks=1)
+    q, k = _bf16(g, T, H, D), _bf16(g, T, max(Hk, 1), D)
+    w = torch.randn(D, generator=g, device="cuda")
+    rot = 16 * (D // 32)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda").int()
+    freq = 10000.0 ** (-torch.arange(rot // 2, device="cuda").double() / max(rot // 2, 1))
+    slot = torch.arange(T, device="cuda")
+    slot[::3] = -1
+    k_out = torch.full((T, max(Hk, 1), D), 7.0, dtype=torch.bfloat16, device="cuda")
+    kw = dict(pos=pos, inv_freq=freq, rot_dim=rot, rot_off=8 if D > 16 else 0, style="halves", eps=1e-5, q_weight=w)
+    if Hk:
+        kw.update(k_out=k_out, k_slot=slot)
+    qo, _ = c.norm_rope(q, k if Hk else None, **kw)
+    args = (pos, freq, rot, kw["rot_off"], "halves", 1e-5)
+    want, mag = _norm_oracle(q, w, *args)
+    assert ((qo.double() - want).abs() <= _norm_tol(want, mag, D)).all()
+    if Hk:
+        want, mag = _norm_oracle(k, None, *args)
+        on = slot >= 0
+        assert ((k_out.double() - want).abs() <= _norm_tol(want, mag, D))[on].all()
+        assert (k_out[~on] == 7).all()
+    assert c.check_error() == 0
+    c.close()
