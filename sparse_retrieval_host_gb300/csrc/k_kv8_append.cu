@@ -14,7 +14,7 @@
 // prompts, latency for decode steps. A unit of up to 512 vectors of 8 values (16
 // per lane) is done by one warp, eight to a CTA, without barriers; a larger one by
 // the whole CTA (prompts of 10,000 rows x 8 heads x 128 in blocks of 32: 15 us by
-// warps, 36 by CTAs; 4.3 TB/s against 6.8 measured for a copy).
+// warps, 36 by CTAs; 4.5 TB/s against 6.8 measured for a copy).
 #include "kv8_internal.cuh"
 
 namespace srh {
@@ -280,7 +280,10 @@ cudaError_t launch_append(const Cache& c, const kv8_pool& pool, const int32_t* t
     const long long vecs = rows_avg << a.dv_log2;
     const long long per = vecs <= 512 ? kThreads / 32 : 1;
     long long grid = (units + per - 1) / per;
-    if (grid > 8ll * c.sm_count) grid = 8ll * c.sm_count;
+    // no more CTAs of 16 vectors per lane than fit at once: each finds the units anew
+    // (the prompts at the top 14.7 us, 15.4 with up to 8 per SM)
+    const long long per_sm = vecs > 128 && vecs <= 512 ? 2 : 8;
+    if (grid > per_sm * c.sm_count) grid = per_sm * c.sm_count;
     const size_t smem = (size_t)(n_req + 1) * sizeof(int);
     if (vecs <= 128) append_kernel<32, 4><<<(unsigned)grid, kThreads, smem, st>>>(a);
     else if (vecs <= 512) append_kernel<32, 16><<<(unsigned)grid, kThreads, smem, st>>>(a);
