@@ -432,9 +432,10 @@ struct Bars {
     alignas(16) float qs[S::RT];      // query scale * softmax scale * log2 e
     float part[4][S::RT];             // per-warp maxima, then sums
     float sum[S::RT];
-    int pos[S::RT];                   // position of the row's token; -1: no row
-    alignas(8) int2 span;             // positions of the first and the last row
-    long long row_at[2][S::RT];       // its offset in out
+    // of each segment handed on: rows' (row of q and out, head) and tokens' positions (-1: no row)
+    alignas(16) int2 row[kSegs][S::RT];
+    alignas(16) int pos[kSegs][S::RT];
+    int2 span[kSegs];                 // positions of the first and the last row
     Segment seg[kSegs];
 };
 
@@ -647,6 +648,18 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 sg.b = -1;
                 sg.n = 0;
             }
+            if (more) {
+                // its rows, here, where no one waits for the divisions
+                for (int r = lane; r < RT; r += 32) {
+                    const bool on = r < sg.nr;
+                    const int row = sg.row0 + r, qt = on ? row / a.group : 0, p = sg.len - sg.nq + qt;
+                    bs.row[k % kSegs][r] = make_int2(sg.q0 + qt, sg.h * a.group + (on ? row - qt * a.group : 0));
+                    bs.pos[k % kSegs][r] = on ? p : -1;
+                    if (r == 0) bs.span[k % kSegs].x = p;
+                    if (r == sg.nr - 1) bs.span[k % kSegs].y = p;
+                }
+                __syncwarp();
+            }
             if (lane == 0) {
                 bs.seg[k % kSegs] = sg;
                 mbar_arrive(&bs.seg_full[k % kSegs]);
@@ -780,12 +793,12 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // queries: a warp per row, 4 values per lane and 128 dims
         constexpr int W = SOFT / 32, RPW = RT / W;
         uint2 qx[RPW][DB];
-        auto load_q = [&](const Segment& sg) {
+        auto load_q = [&](const Segment& sg, uint32_t k) {
 #pragma unroll
             for (int i = 0; i < RPW; ++i) {
                 const int r = warp + W * i;
-                const int row = sg.row0 + r, qt = row / a.group, hd = sg.h * a.group + row % a.group;
-                const uint16_t* p = a.q + (size_t)(sg.q0 + qt) * a.q_row + (size_t)hd * (DB * 128) + lane * 4;
+                const int2 at = bs.row[k % kSegs][r];
+                const uint16_t* p = a.q + (size_t)at.x * a.q_row + (size_t)at.y * (DB * 128) + lane * 4;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
                     qx[i][d] = r < sg.nr ? __ldg(reinterpret_cast<const uint2*>(p + d * 128)) : make_uint2(0, 0);
@@ -794,14 +807,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // Segment k's rows into shared memory, the queries from the registers.
         auto stage = [&](const Segment& sg, uint32_t k) {
             if (tid < RT) {
-                const int row = sg.row0 + tid, qt = row / a.group, hd = sg.h * a.group + row % a.group;
-                const bool on = tid < sg.nr;
-                bs.pos[tid] = on ? sg.len - sg.nq + qt : -1;
-                if (tid == 0) bs.span.x = sg.len - sg.nq + qt;
-                if (tid == sg.nr - 1) bs.span.y = sg.len - sg.nq + qt;
-                bs.row_at[k & 1][tid] = (long long)(sg.q0 + qt) * a.out_row + (long long)hd * (DB * 128);
                 // a column without a row is held at weight 0 by a reference out of reach
-                bs.nref[k & 1][tid] = on ? -kLow : kLow;
+                bs.nref[k & 1][tid] = tid < sg.nr ? -kLow : kLow;
             }
             if (sg.n == 0) return;
 #pragma unroll
@@ -838,7 +845,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         };
         if (!warp_got(&bs.seg_full[0], 0)) fail = true;
         else {
-            if (bs.seg[0].n > 0) load_q(bs.seg[0]);
+            if (bs.seg[0].n > 0) load_q(bs.seg[0], 0);
             if (bs.seg[0].b >= 0) stage(bs.seg[0], 0);
         }
         for (uint32_t k = 0;; ++k) {
@@ -862,7 +869,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 const float4 sc = bs.sc[g % kScales][tok >> a.bs_log2];   // (0, -inf, 0) without a block
                 tc_fence_after();
                 const int win = a.window ? a.window : 1 << 30;
-                const int2 span = bs.span;
+                const int2 span = bs.span[k % kSegs];
                 const bool edge = t0 + kTile - 1 > span.x || t0 <= span.y - win;
                 const u64 ks2 = pack(sc.x, sc.x), lv2 = pack(sc.y, sc.y);
                 // exponents: score * log2 e + log2 vs, -inf where not seen
@@ -889,7 +896,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 if (edge) {
 #pragma unroll
                     for (int i = 0; i < CT; ++i) {
-                        const int p = bs.pos[col0 + i];
+                        const int p = bs.pos[k % kSegs][col0 + i];
                         if (t > p || t <= p - win) x[i] = -INFINITY;
                     }
                 }
@@ -1013,7 +1020,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             bool go = false;
             if (!warp_got(&bs.seg_full[(k + 1) % kSegs], ((k + 1) / kSegs) & 1)) fail = true;
             else go = next.b >= 0;
-            if (go && next.n > 0) load_q(next);
+            if (go && next.n > 0) load_q(next, k + 1);
             if (n > 0) {
                 float l[CT];
 #pragma unroll
@@ -1046,7 +1053,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         inv[i] = bs.sum[col0 + c + i];
-                        at[i] = a.out + bs.row_at[k & 1][col0 + c + i] + tok;
+                        const int2 row = bs.row[k % kSegs][col0 + c + i];
+                        at[i] = a.out + (size_t)row.x * a.out_row + (size_t)row.y * (DB * 128) + tok;
                     }
                     float* po = a.part_o + ((size_t)max(slot, 0) * RT + col0 + c) * (DB * 128) + tok;
 #pragma unroll 1
