@@ -127,6 +127,7 @@ struct Args {
     int n_req, n_rows, heads, kv_heads, group;   // group = heads / kv_heads
     int bs_log2, n_blocks, max_blocks;
     float scale_log2;
+    unsigned long long per_group;                // ceil(2^64 / group); 0 for a group of 1
     int window;                                  // 0: none
     int switch_units;                            // units that stand for a segment's start and end
 };
@@ -139,14 +140,20 @@ struct Request {
     int P;             // units of a pair: at least the token tiles of its two row tiles, and switch_units
 };
 
+// x / group for 0 <= x < 2^32: with m = ceil(2^64 / group), x m / 2^64 exceeds x / group
+// by less than x / 2^64, which is less than the 1 / group up to the next integer.
+__device__ __forceinline__ int by_group(const Args& a, int x) {
+    return a.group == 1 ? x : (int)__umul64hi((unsigned long long)(uint32_t)x, a.per_group);
+}
+
 // Token tiles that any row of row tile rt sees, from *first on.
 template <int RT>
 __device__ __forceinline__ int tiles_of(const Args& a, const Request& r, int rt, int* first) {
     const int c = r.len - r.nq;                                    // position of the first query
     int p_lo = c, p_hi = c + r.nq - 1;
     if (r.nrt > 1) {
-        p_lo = c + rt * RT / a.group;
-        p_hi = c + min(r.nq - 1, ((rt + 1) * RT - 1) / a.group);
+        p_lo = c + by_group(a, rt * RT);
+        p_hi = c + min(r.nq - 1, by_group(a, (rt + 1) * RT - 1));
     }
     *first = a.window ? max(0, p_lo - a.window + 1) / kTile : 0;
     return max(0, (p_hi < 0 ? 0 : p_hi / kTile + 1) - *first);
@@ -652,7 +659,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 // its rows, here, where no one waits for the divisions
                 for (int r = lane; r < RT; r += 32) {
                     const bool on = r < sg.nr;
-                    const int row = sg.row0 + r, qt = on ? row / a.group : 0, p = sg.len - sg.nq + qt;
+                    const int row = sg.row0 + r, qt = on ? by_group(a, row) : 0, p = sg.len - sg.nq + qt;
                     bs.row[k % kSegs][r] = make_int2(sg.q0 + qt, sg.h * a.group + (on ? row - qt * a.group : 0));
                     bs.pos[k % kSegs][r] = on ? p : -1;
                     if (r == 0) bs.span[k % kSegs].x = p;
@@ -1382,6 +1389,7 @@ cudaError_t launch_attend(const Cache& c, const kv8_pool& pool, const int32_t* t
     a.heads = n_heads;
     a.kv_heads = c.cfg.n_kv_heads;
     a.group = n_heads / c.cfg.n_kv_heads;
+    a.per_group = a.group == 1 ? 0 : ~0ull / (unsigned)a.group + 1;
     a.bs_log2 = c.bs_log2;
     a.n_blocks = c.cfg.n_blocks;
     a.max_blocks = c.cfg.max_blocks;
