@@ -243,7 +243,7 @@ cudaError_t launch_resize(const Cache& c, const int32_t* new_len, int n_req, int
     resize_kernel<<<1, nt, 4 * (n_req + 1) * sizeof(int), st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.fill_here || !pos) return e;
-    return launch_k(fill_kernel, dim3((unsigned)((cap + kFillThreads - 1) / kFillThreads)), dim3(kFillThreads),
+    return launch_k(fill_kernel, dim3((unsigned)((cap + (long long)kFillThreads - 1) / kFillThreads)), dim3(kFillThreads),
                     (n_req + 1) * sizeof(int), st, true, a);
 }
 

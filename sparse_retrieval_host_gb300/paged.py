@@ -208,6 +208,8 @@ class PagedKV8:
             raise ValueError("q or k must be bf16 [tokens][heads][dim]")
         n, _, d = first.shape
         if rot_dim:
+            if pos is None or inv_freq is None:
+                raise ValueError("rot_dim needs pos and inv_freq")
             self._ints(pos, "pos", n)
             self._ints(inv_freq, "inv_freq", rot_dim // 2, torch.float64)
         parts, outs = [], []
@@ -227,10 +229,11 @@ class PagedKV8:
                 if out is None:
                     raise ValueError(f"{name}_slot needs {name}_out")
             if out is None:
-                out = self._empty((n, x.shape[1], d), x.dtype, stream)
-            out_row = self._rows(out, name + "_out", x.shape[1], d)
-            if slot is None and out.shape[0] != n:
-                raise ValueError(f"{name}_out must have a row per token")
+                out, out_row = self._empty(x.shape, x.dtype, stream), x.shape[1] * d
+            else:
+                out_row = self._rows(out, name + "_out", x.shape[1], d)
+                if slot is None and out.shape[0] != n:
+                    raise ValueError(f"{name}_out must have a row per token")
             parts.append(abi.Kv8Heads(x.data_ptr(), row, out.data_ptr(), out_row, None if w is None else w.data_ptr(),
                                       x.shape[1], None if slot is None else slot.data_ptr(),
                                       0 if slot is None else out.shape[0]))
@@ -269,10 +272,11 @@ class PagedKV8:
         n = self._requests(cu)
         qr = self._rows(q, "q", None, self.D)
         if out is None:
-            out = self._empty(q.shape, q.dtype, stream)
+            out, orow = self._empty(q.shape, q.dtype, stream), q.shape[1] * self.D
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
-        orow = self._rows(out, "out", None, self.D)
+        else:
+            orow = self._rows(out, "out", None, self.D)
         if q.shape[0]:
             rc = self._lib.kv8_attend(self.cache, self._pool[layer], self._table, self._len, cu.data_ptr(), n, q.data_ptr(),
                                       qr, q.shape[0], q.shape[1], scale, window, out.data_ptr(), orow, self._s(stream))

@@ -930,3 +930,13 @@ def test_norm_ranges_cross_tokens(D, H, Hk, T):
         assert (k_out[~on] == 7).all()
     assert c.check_error() == 0
     c.close()
+
+
+def test_rotation_without_positions_is_refused():
+    g = _gen(111)
+    c = _paged(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=1, max_blocks=1)
+    q, pos, freq = _bf16(g, 3, 2, 128), _i32([0, 1, 2]), torch.ones(16, dtype=torch.float64, device="cuda")
+    for kw in ({}, {"pos": pos}, {"inv_freq": freq}):
+        with pytest.raises(ValueError, match="rot_dim needs"):
+            c.norm_rope(q, rot_dim=32, **kw)
+    c.close()
