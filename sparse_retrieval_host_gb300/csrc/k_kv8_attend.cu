@@ -86,7 +86,7 @@ struct Shape {
     static constexpr int kPBytes = kTile * N;
     static constexpr int kPitch = CAT ? N : RT;            // bytes of one token's row of p
     // CTAs per SM: four hide more of a decode step's latencies than fewer with longer
-    // rings do (64 requests of up to 16,384 tokens: 201 us; three 207, two 221)
+    // rings do (64 requests of up to 16,384 tokens: 201 us, now 199; three 207, two 221)
     static constexpr int CTAS = DB == 1 ? (RT == 16 ? 4 : 2) : DB == 2 && RT == 16 ? 2 : 1;
     // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
     // tile j is given back, so two tiles must fit
@@ -95,7 +95,7 @@ struct Shape {
     // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the
     // columns. (32 columns a thread, for 64-row tiles with two CTAs per SM, need more
     // than the 96 registers there are: a prompt chunk of 128-dim heads took 613 us
-    // with them and takes 545 with tiles of 32 rows.)
+    // with them and took 545 with tiles of 32 rows at the time, now 536.)
     static constexpr int CT = 16;
     static constexpr int CG = RT / CT;
     static constexpr int SOFT = 128 * CG;                  // softmax threads
