@@ -592,7 +592,7 @@ typedef struct {
     float* v_scale;
 } kv8_pool;
 
-/* Makes a handle on the current device (scratch: 30, 60 or 120 MB with
+/* Makes a handle on the current device (scratch: 30, 30 or 40 MB with
  * head_dim 128, 256 or 512).
  * Errors: SRH_ERR_INVALID, SRH_ERR_NOMEM, SRH_ERR_CUDA (kv8_last_error(NULL)). */
 int kv8_create(const kv8_config* cfg, kv8_cache** out);

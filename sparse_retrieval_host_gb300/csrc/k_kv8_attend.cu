@@ -31,12 +31,11 @@
 // Work: a "row tile" is RT of the (token, head) rows that share a KV head of a
 // request; its tokens are cut into tiles of 128. Every (request, KV head, row
 // tile, token tile) is a unit. The U units, counted from the lengths on the
-// device, are cut into chunks of equal numbers: 12/16 of them into one chunk
-// per CTA, 3/16 and 1/16 into as many smaller ones that CTAs take as they come
+// device, are cut into chunks of equal numbers, one per CTA. Of many units 12/16
+// are cut so, 3/16 and 1/16 into as many smaller chunks that CTAs take as they come
 // free (SMs run at different speeds: with one chunk each, the last CTA of a
-// bandwidth-bound batch ended 8 % after the average, of a prompt chunk 45 %). So ragged
-// batches and single long requests both fill the SMs, and nothing depends on
-// host knowledge of lengths. An item whose units fall into several chunks leaves
+// bandwidth-bound batch ended 8 % after the average). So ragged batches and single
+// long requests both fill the SMs, and nothing depends on host knowledge of lengths. An item whose units fall into several chunks leaves
 // fp32 partial sums, which a second kernel joins in chunk order: who ran a
 // chunk does not show, and results repeat bit for bit.
 //
@@ -66,6 +65,7 @@ constexpr float kLoScale = 16.f;         // factor of a second term that has col
 
 // Rounds of chunks and where they begin, in sixteenths of the units.
 constexpr int kRounds = 3;
+constexpr int kRoundsFrom = 192;   // units per CTA
 __device__ __forceinline__ int cut(int r) { return r == 0 ? 0 : r == 1 ? 12 : r == 2 ? 15 : 16; }
 
 // DB: head_dim / 128. RT: rows per row tile. SHARED: V = K.
@@ -88,6 +88,10 @@ struct Shape {
     // CTAs per SM: four hide more of a decode step's latencies than fewer with longer
     // rings do (64 requests of up to 16,384 tokens: 201 us, now 199; three 207, two 221)
     static constexpr int CTAS = DB == 1 ? (RT == 16 ? 4 : 2) : DB == 2 && RT == 16 ? 2 : 1;
+    // rounds of chunks, where a CTA's switches between segments overlap other CTAs' tiles
+    // (alone on its SM a CTA is better off with one chunk: 64 requests of 32,768 latent
+    // rows 277 us, 329 in rounds; prompts of 512 tokens of 256-dim heads 649 and 676)
+    static constexpr int ROUNDS = CTAS > 1 ? kRounds : 1;
     // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
     // tile j is given back, so two tiles must fit
     static constexpr int SLOTS = DB == 1 ? (RT == 16 ? 2 : 5) : DB == 2 ? (RT == 16 ? 6 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
@@ -518,8 +522,11 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // as few CTAs as keep the largest share the same: fewer parts to join
         const int U = (int)total, most = (U + n_grid - 1) / n_grid;
         const int n_cta = U ? (U + most - 1) / most : 0;
-        // rounds of smaller chunks only where even the smallest still has 4 units
-        const int rounds = U >= 64 * n_cta ? kRounds : 1;
+        // rounds of smaller chunks only where their switches are few beside their units: from
+        // about 200 per CTA on (the prompt chunk, with 400: 536 us, 557 without; decode of
+        // 256-dim heads with 220: 689 and 699; of 128-dim heads with 245 equal, with 113
+        // 379 and 376, with 85 292 and 284)
+        const int rounds = S::ROUNDS > 1 && U / kRoundsFrom >= n_cta ? S::ROUNDS : 1;
         bs.before[i] = (int)(incl - mine);
         if (i == 0) {
             bs.ch.n = n_cta;
@@ -1290,7 +1297,7 @@ cudaError_t run(const Cache& c, const CUtensorMap& km, const CUtensorMap& vm, Ar
     a.switch_units = S::SWITCH;
     const int grid = S::CTAS * c.sm_count;
     static_assert(S::CTAS * smem_bytes<S>() <= 232448 + (S::CTAS - 1) * 1024, "the CTAs of an SM must fit its shared memory");
-    const size_t chunks = (size_t)grid * kRounds;
+    const size_t chunks = (size_t)grid * S::ROUNDS;
     if (chunks * 2 * S::RT * S::DB * 128 > c.part_o_floats || chunks * 4 * S::RT > c.part_ml_floats || chunks > c.meta_n ||
         chunks > kMaxChunks)
         return cudaErrorInvalidValue;
@@ -1341,7 +1348,7 @@ namespace {
 template <int DB, int RT>
 void scratch_of(size_t sm_count, size_t* o_floats, size_t* ml_floats, size_t* meta) {
     using S = Shape<DB, RT, false>;
-    const size_t chunks = S::CTAS * sm_count * kRounds;
+    const size_t chunks = S::CTAS * sm_count * S::ROUNDS;
     const auto most = [](size_t* v, size_t n) { *v = *v < n ? n : *v; };
     most(o_floats, chunks * 2 * RT * DB * 128);
     most(ml_floats, chunks * 2 * RT * 2);

@@ -940,3 +940,18 @@ def test_rotation_without_positions_is_refused():
         with pytest.raises(ValueError, match="rot_dim needs"):
             c.norm_rope(q, rot_dim=32, **kw)
     c.close()
+
+
+def test_attend_prompt_in_rounds():
+    """A prompt of so many units (2,000 row tiles of 4 KV heads) that the last quarter is handed out while the kernel runs."""
+    c, g = _filled([4000], 4, 128, 64, True, 113, spread=1)
+    q, cu = _bf16(g, 4000, 64, 128), _i32([0, 4000])
+    want = c.attend(q, cu, scale=0.02)
+    for _ in range(3):
+        assert torch.equal(c.attend(q, cu, scale=0.02), want)
+    for at in (2, 777, 2001, 4000):                        # the last two rows that see `at` tokens
+        part = type("Some", (), dict(D=128, Hk=4, bs=64, len=_i32([at]), table=c.table, k_codes=c.k_codes, v_codes=c.v_codes,
+                                     k_scale=c.k_scale, v_scale=c.v_scale))
+        _check_attend(part, q[at - 2:at], _i32([0, 2]), want[at - 2:at], 0.02, 0)
+    assert c.check_error() == 0
+    c.close()
