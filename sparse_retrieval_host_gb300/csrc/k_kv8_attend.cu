@@ -86,11 +86,11 @@ struct Shape {
     static constexpr int kPBytes = kTile * N;
     static constexpr int kPitch = CAT ? N : RT;            // bytes of one token's row of p
     // CTAs per SM: four hide more of a decode step's latencies than fewer with longer
-    // rings do (64 requests of up to 16,384 tokens: 201 us, now 199; three 207, two 221)
+    // rings do (64 requests of up to 16,384 tokens: 201 us; three 207, two 221)
     static constexpr int CTAS = DB == 1 ? (RT == 16 ? 4 : 2) : DB == 2 && RT == 16 ? 2 : 1;
     // rounds of chunks, where a CTA's switches between segments overlap other CTAs' tiles
     // (alone on its SM a CTA is better off with one chunk: 64 requests of 32,768 latent
-    // rows 277 us, 329 in rounds; prompts of 512 tokens of 256-dim heads 649 and 676)
+    // rows 275 us, 329 in rounds; prompts of 512 tokens of 256-dim heads 646 and 676)
     static constexpr int ROUNDS = CTAS > 1 ? kRounds : 1;
     // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
     // tile j is given back, so two tiles must fit
