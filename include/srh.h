@@ -690,9 +690,9 @@ int kv8_append(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const
  *   scale       finite; window >= 0
  * Precision: fp32 scores, statistics and sums. Queries enter the products as
  * two e4m3 terms per value (bf16's 8 significant bits; a value below about
- * 2^-9 of its row's largest keeps 2^-17 of that largest), weights as two
- * e4m3 terms each (about 9 bits; weights below 2^-15 of the row's largest
- * contribution are dropped from the value sum). Codes of tokens below len must
+ * 2^-13 of its row's largest keeps 2^-21 of that largest), weights as three e5m2
+ * terms each: within 2^-9 of the weight, or 2^-27 of the row's largest contribution
+ * (weight times V's scale). Codes of tokens below len must
  * not be NaN codes (kv8_append writes none); what lies behind a request's
  * length, in its last block or elsewhere, is not used.
  */

@@ -11,22 +11,27 @@
 // kind::f8f6f4 takes 8-bit operands on both sides. A query row is scaled by a
 // power of two to a largest magnitude in [128, 256) and split into two e4m3
 // terms, hi = e4m3(q), lo = e4m3(q - hi): 4 + 4 significant bits, which is bf16
-// exactly. Weights are split the same way. The two terms are two columns of one
-// MMA (N = 2 * rows), so a tile is read from shared memory once for both; having
-// columns of its own, the second term is held 16 times larger, which takes
-// e4m3's smallest steps 16 times further down.
+// exactly. The two terms are two columns of one MMA (N = 2 * rows), so a tile is
+// read from shared memory once for both; having columns of its own, the second
+// term is held 16 times larger, which takes e4m3's smallest steps 16 times
+// further down.
 //
 // Block scales: ks multiplies the score, one factor per thread (thread = TMEM
 // lane = token). vs goes into the exponent: u = s + log2(vs), p = 2^(u - ref), so
 // the column p holds what the token contributes, and the rounding of p is
 // relative to the largest contribution; the softmax sum takes p / vs in fp32.
 //
-// The running reference of a row is set so that its maximum's weight is 2 (2^5
-// where the second terms are not scaled), and is moved only when a weight
-// would pass 2^8.75 (e4m3 ends at 448): one vote of the softmax threads per tile;
-// the maximum itself, the rescaling of the sums and of O^T in TMEM only happen
-// when the vote says so (the first tile, then the more rarely the more tokens a
-// row has seen). The smallest half step is 2^-15 of the row's largest weight.
+// Weights are rounded to fp16 and split into three e5m2 terms, p = hi + mid + lo:
+// within 2^-9 (half of bf16's step), or half of e5m2's smallest step, 2^-17. The
+// running reference of a row is set so that its maximum's weight is 2^10, and is moved
+// only when a weight would pass 2^15.75 (e5m2 ends at 57,344): what a small weight may
+// lose is 2^-27 of the row's largest contribution, so that 131,072 tokens behind one
+// that takes nearly all lose 2^-10 of it together at the very most. (Two e4m3 terms
+// reach 2^-15 only, below which the long tail of a row with one large weight came out
+// as nothing: 8,192 tokens with a tenth of the weight between them lost all of it.)
+// One vote of the softmax threads per tile says whether a reference moves; the
+// maximum itself, the rescaling of the sums and of O^T in TMEM only happen then (the
+// first tile, then the more rarely the more tokens a row has seen).
 //
 // Work: a "row tile" is RT of the (token, head) rows that share a KV head of a
 // request; its tokens are cut into tiles of 128. Every (request, KV head, row
@@ -60,8 +65,9 @@ using namespace umma;
 constexpr int kTile = 128;               // tokens per tile
 constexpr int kSlotBytes = kTile * 128;  // 128 tokens x 128 dims
 constexpr float kLow = -1e30f;           // reference of a row that has seen no token
-constexpr float kRoom = 8.75f;           // a row's reference moves when a weight would pass 2^8.75 = 431
-constexpr float kLoScale = 16.f;         // factor of a second term that has columns of its own
+constexpr float kHead = 10.f;            // log2 of the weight that a new reference gives a row's maximum
+constexpr float kRoom = 15.75f;          // a row's reference moves when a weight would pass 2^15.75 = 55,109
+constexpr float kLoScale = 16.f;         // factor of a query's second term
 
 // Rounds of chunks and where they begin, in sixteenths of the units.
 constexpr int kRounds = 3;
@@ -74,17 +80,28 @@ struct Shape {
     static constexpr int DB = DB_, RT = RT_;
     static constexpr bool SHARED = SHARED_;
     static constexpr int N = 2 * RT;                       // hi and lo columns
-    // O^T's hi and lo columns stay apart where TMEM has room for both
-    static constexpr bool CAT = DB * N + N <= 512;
-    static constexpr int ON = CAT ? N : RT;                // O^T columns per 128 dims
-    // weights of a row's maximum: where the second terms are scaled by 16, 2^-10 / 16
-    // is the smallest half step, else 2^-10; either way 2^-15 of the maximum
-    static constexpr float HEAD = CAT ? 1.f : 5.f;
-    static constexpr int COLS = N + DB * ON;
+    // The three terms of the weights are columns of one PV product where TMEM has room
+    // for O^T's three parts (a fourth of zeros fills 16-row tiles up to whole 32-byte
+    // rows). Else (64 rows of 512 dims) hi and mid are for the first TWO times 128 dims,
+    // as far as the room goes, and terms follow each other into the same columns
+    // otherwise (32 requests of 32,768 latent rows: 162 us; with TWO = 0 169).
+    static constexpr bool CAT = 3 * DB * RT + N <= 512;
+    static constexpr int ON = !CAT ? RT : RT == 16 ? 64 : 3 * RT;   // O^T columns per 128 dims
+    static constexpr int TWO = CAT ? 0 : 2;
+    // O^T's first column of 128 dims: hi, then mid and lo RT columns further on each, where apart
+    static __host__ __device__ constexpr int o_at(int mb) { return CAT ? mb * ON : (mb + (mb < TWO ? mb : TWO)) * RT; }
+    static constexpr int COLS = N + DB * ON + TWO * RT;
     static constexpr int ALLOC = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static constexpr int kQBytes = DB * N * 128;
-    static constexpr int kPBytes = kTile * N;
-    static constexpr int kPitch = CAT ? N : RT;            // bytes of one token's row of p
+    static constexpr int kPitch = RT == 64 ? 64 : 32;      // bytes of one token's row of a part of p
+    static constexpr int kPart = kTile * kPitch;           // parts: a term each, or two of 16-row tiles
+    static constexpr int kPBytes = (RT == 16 ? 2 : 3) * kPart;
+    // byte offset of 16-byte piece c of token t's weights, pieces of hi first, then mid, lo
+    static __device__ __forceinline__ uint32_t p_at(uint32_t t, uint32_t c) {
+        constexpr uint32_t per = kPitch / 16;
+        const uint32_t x = kPitch == 64 ? ((t >> 1) & 3u) : ((t >> 2) & 1u);
+        return (c / per) * kPart + t * kPitch + ((c % per ^ x) << 4);
+    }
     // CTAs per SM: four hide more of a decode step's latencies than fewer with longer
     // rings do (64 requests of up to 16,384 tokens: 201 us; three 207, two 221)
     static constexpr int CTAS = DB == 1 ? (RT == 16 ? 4 : 2) : DB == 2 && RT == 16 ? 2 : 1;
@@ -94,7 +111,7 @@ struct Shape {
     static constexpr int ROUNDS = CTAS > 1 ? kRounds : 1;
     // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
     // tile j is given back, so two tiles must fit
-    static constexpr int SLOTS = DB == 1 ? (RT == 16 ? 2 : 5) : DB == 2 ? (RT == 16 ? 6 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
+    static constexpr int SLOTS = DB == 1 ? (RT == 16 ? 2 : 5) : DB == 2 ? (RT == 16 ? 5 : 9) : RT == 16 ? 12 : RT == 32 ? 10 : 8;
     static_assert(SLOTS >= 2 * DB && SLOTS / DB + 2 < 8, "two tiles must fit the ring, and fewer than the scales held");
     // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the
     // columns. (32 columns a thread, for 64-row tiles with two CTAs per SM, need more
@@ -380,39 +397,54 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
-// Shared-memory descriptor of an MN-major operand whose rows (one per K index)
-// are PITCH = 32, 64 or 128 bytes with the swizzle of that width: groups of 8
-// rows along K follow each other; one group spans the whole M or N extent.
+// Shared-memory descriptor of an MN-major operand in parts of PITCH = 32 or 64 bytes
+// along M or N with the swizzle of that width: a row per K index, groups of 8 rows
+// follow each other along K; the next part lies `part` bytes further on.
 template <int PITCH>
-__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
-    uint64_t d = desc_sw128(saddr, 16, 8 * PITCH);
+__device__ __forceinline__ uint64_t desc_parts(uint32_t saddr, uint32_t part) {
+    uint64_t d = desc_sw128(saddr, part, 8 * PITCH);
     d &= ~((uint64_t)7 << 61);
-    d |= (uint64_t)(PITCH == 128 ? 2 : PITCH == 64 ? 4 : 6) << 61;
+    d |= (uint64_t)(PITCH == 64 ? 4 : 6) << 61;
     return d;
 }
-// Byte offset of 16-byte chunk c of row r in such an operand.
-template <int PITCH>
-__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
-    const uint32_t x = PITCH == 128 ? (r & 7u) : PITCH == 64 ? ((r >> 1) & 3u) : ((r >> 2) & 1u);
-    return r * PITCH + ((c ^ x) << 4);
-}
-// Two e4m3 terms of each of four values, a byte each; the second times 16 if SCALED.
-template <bool SCALED>
+// Two e4m3 terms of each of four values, a byte each; the second times kLoScale.
 __device__ __forceinline__ void split4(float v0, float v1, float v2, float v3, uint32_t* hi, uint32_t* lo) {
     const __half2 a = __floats2half2_rn(v0, v1), b = __floats2half2_rn(v2, v3);
     const uint32_t ha = __nv_cvt_halfraw2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
     const uint32_t hb = __nv_cvt_halfraw2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
     __half2 ra = __hsub2(a, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ha, __NV_E4M3)));
     __half2 rb = __hsub2(b, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hb, __NV_E4M3)));
-    if (SCALED) {
-        const __half2 f = __float2half2_rn(kLoScale);
-        ra = __hmul2(ra, f);
-        rb = __hmul2(rb, f);
-    }
+    const __half2 f = __float2half2_rn(kLoScale);
+    ra = __hmul2(ra, f);
+    rb = __hmul2(rb, f);
     const uint32_t la = __nv_cvt_halfraw2_to_fp8x2(ra, __NV_SATFINITE, __NV_E4M3);
     const uint32_t lb = __nv_cvt_halfraw2_to_fp8x2(rb, __NV_SATFINITE, __NV_E4M3);
     *hi = ha | (hb << 16);
     *lo = la | (lb << 16);
+}
+// Three e5m2 terms of each of four values >= 0 (rounded to fp16 first), a byte each. An
+// e5m2 code is the upper byte of an fp16 value: the first two terms are cut off, which
+// leaves exact remainders, the third is rounded to nearest. Together they are within 2^-9
+// (or 2^-17) of the value. (All three rounded hold fp16 exactly, for four more conversions:
+// the prompt chunk 634 us; this way 592.)
+__device__ __forceinline__ void split4_e5m2(float v0, float v1, float v2, float v3, uint32_t (&out)[3]) {
+    __half2 a = __floats2half2_rn(v0, v1), b = __floats2half2_rn(v2, v3);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t wa, wb;
+        memcpy(&wa, &a, 4);
+        memcpy(&wb, &b, 4);
+        out[i] = __byte_perm(wa, wb, 0x7531);
+        wa &= 0xff00ff00u;
+        wb &= 0xff00ff00u;
+        __half2 ca, cb;
+        memcpy(&ca, &wa, 4);
+        memcpy(&cb, &wb, 4);
+        a = __hsub2(a, ca);
+        b = __hsub2(b, cb);
+    }
+    out[2] = __nv_cvt_halfraw2_to_fp8x2(a, __NV_SATFINITE, __NV_E5M2) |
+             (uint32_t)__nv_cvt_halfraw2_to_fp8x2(b, __NV_SATFINITE, __NV_E5M2) << 16;
 }
 
 constexpr int kSegs = 4;     // segments handed on ahead of their use
@@ -716,9 +748,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // issue, this way 40; N = 64 and 128 run at 48 and 64, the rate at which
         // their operands leave shared memory).
         constexpr uint32_t id_qk = idesc_f32acc(0, 0, 0, kTile, N);              // e4m3, both K-major
-        constexpr uint32_t id_pv = idesc_f32acc(0, 1, 1, 128, S::ON);            // both MN-major
+        constexpr uint32_t id_pv = idesc_f32acc(0, 1, 1, 128, S::ON) | (1u << 10);   // both MN-major, B is e5m2
+        constexpr uint32_t id_two = idesc_f32acc(0, 1, 1, 128, 2 * RT) | (1u << 10);
         const uint32_t r0 = smem_u32(sm);
-        const uint64_t qd = desc_sw128(smem_u32(sm + S::kOffQ), 16, 1024), pd = desc_rows<S::kPitch>(smem_u32(sm + S::kOffP));
+        const uint64_t qd = desc_sw128(smem_u32(sm + S::kOffQ), 16, 1024), pd = desc_parts<S::kPitch>(smem_u32(sm + S::kOffP), S::kPart);
         uint32_t it = 0, g = 0, segs = 0;                  // blocks taken, token tiles, segments with tiles
         auto got = [&](uint64_t* bar, uint32_t parity) {
             return (bool)__all_sync(0xffffffffu, mbar_wait_abort(bar, parity, abort) > 0);
@@ -735,11 +768,14 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 32; ++kk) {
-                        mma_f8(tm_o + mb * S::ON, vd + kk * (32 * 128 / 16), pd + kk * (32 * S::kPitch / 16), id_pv,
-                               !first || kk > 0);
-                        if (!S::CAT)
-                            mma_f8(tm_o + mb * S::ON, vd + kk * (32 * 128 / 16),
-                                   pd + (kTile * S::kPitch + kk * 32 * S::kPitch) / 16, id_pv, 1);
+                        const uint64_t ad = vd + kk * (32 * 128 / 16);
+                        const uint32_t o = tm_o + S::o_at(mb);
+                        mma_f8(o, ad, pd + kk * (32 * S::kPitch / 16), mb < S::TWO ? id_two : id_pv, !first || kk > 0);
+                        if (!S::CAT) {
+#pragma unroll
+                            for (int i = mb < S::TWO ? 2 : 1; i < 3; ++i)
+                                mma_f8(o, ad, pd + (i * S::kPart + kk * 32 * S::kPitch) / 16, id_pv, 1);
+                        }
                     }
                     mma_commit(&bs.empty[s]);
                     if (mb == DB - 1) mma_commit(&bs.pv_done);
@@ -842,7 +878,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
                     uint32_t hi, lo;
-                    split4<true>(__uint_as_float(qx[i][d].x << 16) * inv, __uint_as_float(qx[i][d].x & 0xffff0000u) * inv,
+                    split4(__uint_as_float(qx[i][d].x << 16) * inv, __uint_as_float(qx[i][d].x & 0xffff0000u) * inv,
                                  __uint_as_float(qx[i][d].y << 16) * inv, __uint_as_float(qx[i][d].y & 0xffff0000u) * inv,
                                  &hi, &lo);
                     unsigned char* q = qsm + d * (N * 128) + (lane & 3) * 4;
@@ -857,6 +893,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         auto warp_got = [&](uint64_t* bar, uint32_t parity) {
             return (bool)__all_sync(0xffffffffu, mbar_wait_abort(bar, parity, abort) > 0);
         };
+        if (RT == 16)   // the fourth columns of 16-row tiles, for good (before the first weights' fence)
+            *reinterpret_cast<uint4*>(psm + S::p_at(tok, 3)) = make_uint4(0, 0, 0, 0);
         if (!warp_got(&bs.seg_full[0], 0)) fail = true;
         else {
             if (bs.seg[0].n > 0) load_q(bs.seg[0], 0);
@@ -946,7 +984,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         const float mt = fmaxf(fmaxf(bs.part[0][tid], bs.part[1][tid]), fmaxf(bs.part[2][tid], bs.part[3][tid]));
                         const float was = -nref[tid];
                         float now = was;
-                        if (mt - was > S::HEAD) now = mt - S::HEAD;     // every row that grew, while at it
+                        if (mt - was > kHead) now = mt - kHead;     // every row that grew, while at it
                         nref[tid] = -now;
                         bs.fac[tid] = now == was ? 1.f : ex2(was - now);
                     }
@@ -967,22 +1005,21 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         l2[c / 2 + 2] = mul2(l2[c / 2 + 2], fb.x);
                         l2[c / 2 + 3] = mul2(l2[c / 2 + 3], fb.y);
                         if (j == 0) continue;
-                        constexpr int KO = DB * (S::CAT ? 2 : 1);          // 8-column pieces of these rows
-                        static_assert(KO % 2 == 0, "taken two at a time");
+                        // pieces of 8 columns, RT apart: the three terms of 128 dims, or any two
+                        constexpr int KP = S::CAT ? 3 : 2, GROUPS = S::CAT ? DB : (DB + S::TWO) / 2;
 #pragma unroll 1
-                        for (int i = 0; i < KO; i += 2) {
-                            const uint32_t at = my_o + i * (S::CAT ? RT : S::ON) + c;
-                            const uint32_t at2 = at + (S::CAT ? RT : S::ON);   // (CAT: hi and lo alternate, RT apart)
-                            float o[8], p[8];
-                            tmem_ld<8>(at, o);
-                            tmem_ld<8>(at2, p);
+                        for (int i0 = 0; i0 < GROUPS; ++i0) {
+                            const uint32_t at = my_o + i0 * (S::CAT ? S::ON : 2 * RT) + c;
+                            float o[KP][8];
+#pragma unroll
+                            for (int i = 0; i < KP; ++i) tmem_ld<8>(at + i * RT, o[i]);
                             tmem_ld_wait();
-                            tmem_regs_ready_n<8>(o);
-                            scale8(o, fa, fb);
-                            tmem_st<8>(at, o);
-                            tmem_regs_ready_n<8>(p);
-                            scale8(p, fa, fb);
-                            tmem_st<8>(at2, p);
+#pragma unroll
+                            for (int i = 0; i < KP; ++i) {
+                                tmem_regs_ready_n<8>(o[i]);
+                                scale8(o[i], fa, fb);
+                                tmem_st<8>(at + i * RT, o[i]);
+                            }
                         }
                     }
                     if (j > 0) {
@@ -995,19 +1032,21 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 // the weights of the last tile have been read
                 if (g > 0 && mbar_wait_abort(&bs.pv_done, (g - 1) & 1, abort) <= 0) fail = true;
                 {
-                    uint32_t hi[4], lo[4];
+                    uint32_t w[3][4];
 #pragma unroll
                     for (int i = 0; i < CT; i += 4) {
                         const float v0 = ex2(y[i]), v1 = ex2(y[i + 1]), v2 = ex2(y[i + 2]), v3 = ex2(y[i + 3]);
                         l2[i / 2] = fma2(pack(v0, v1), iv2, l2[i / 2]);
                         l2[i / 2 + 1] = fma2(pack(v2, v3), iv2, l2[i / 2 + 1]);
-                        split4<S::CAT>(v0, v1, v2, v3, &hi[i / 4], &lo[i / 4]);
+                        uint32_t term[3];
+                        split4_e5m2(v0, v1, v2, v3, term);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) w[k][i / 4] = term[k];
                     }
-                    const int ch = col0 / 16;
-                    unsigned char* ph = psm + chunk_at<S::kPitch>(tok, ch);
-                    unsigned char* pl = S::CAT ? psm + chunk_at<S::kPitch>(tok, RT / 16 + ch) : ph + kTile * S::kPitch;
-                    *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        *reinterpret_cast<uint4*>(psm + S::p_at(tok, i * S::CG + col0 / 16)) =
+                            make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
                 }
                 if (t0 + kTile > len) {
                     // rows behind the request: whatever lies there must not meet a weight of 0 as NaN
@@ -1077,15 +1116,22 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                         for (int i = 0; i < 8; ++i) o[i] = 0.f;
                         if (n > 0) {
-                            tmem_ld<8>(my_o + mb * S::ON + c, o);
-                            if (S::CAT) {
+                            tmem_ld<8>(my_o + S::o_at(mb) + c, o);
+                            if (S::CAT || mb < S::TWO) {
                                 float o2[8];
-                                tmem_ld<8>(my_o + mb * S::ON + RT + c, o2);
+                                tmem_ld<8>(my_o + S::o_at(mb) + RT + c, o2);
                                 tmem_ld_wait();
                                 tmem_regs_ready_n<8>(o);
                                 tmem_regs_ready_n<8>(o2);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) o[i] = fmaf(o2[i], 1.f / kLoScale, o[i]);
+                                for (int i = 0; i < 8; ++i) o[i] += o2[i];
+                                if (S::CAT) {
+                                    tmem_ld<8>(my_o + S::o_at(mb) + 2 * RT + c, o2);
+                                    tmem_ld_wait();
+                                    tmem_regs_ready_n<8>(o2);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) o[i] += o2[i];
+                                }
                             } else {
                                 tmem_ld_wait();
                                 tmem_regs_ready_n<8>(o);

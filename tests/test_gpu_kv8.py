@@ -955,3 +955,78 @@ def test_attend_prompt_in_rounds():
         _check_attend(part, q[at - 2:at], _i32([0, 2]), want[at - 2:at], 0.02, 0)
     assert c.check_error() == 0
     c.close()
+
+
+# ---------------------------------------------------------------------------------------------- rows with a long tail
+def _tail(n, D, shared, G, depth, sd, bs=64, batch=1, outlier=0):
+    """`batch` requests over the same n tokens: the first takes about exp(depth) times the weight of another one, whose scores
+    spread by sd. Rows differ in how far. With `outlier`, a block's V scale is 2^outlier larger and its codes are 0 in the
+    upper half of the dims."""
+    from types import SimpleNamespace
+    g = _gen(n + D + G)
+    nb = -(-n // bs)
+    rows = torch.randn((nb * bs, D), generator=g, device="cuda") * 0.3 + 1
+    key = rows if shared else torch.randn((nb * bs, D), generator=g, device="cuda")
+    key[:, 0] = sd * torch.randn(nb * bs, generator=g, device="cuda")
+    rows[0] = 0
+    key[0, 0] = depth
+    scale = torch.ones((nb, 1), device="cuda")
+    kc = key.to(FP8).view(torch.uint8).view(nb, 1, bs, D)
+    vc = kc if shared else rows.to(FP8).view(torch.uint8).view(nb, 1, bs, D)
+    vs = scale if shared else scale.clone()
+    if outlier:
+        at = nb // 2
+        vs[at] = 2.0 ** outlier
+        vc[at, :, :, D // 2:] = 0
+    buf = dict(k_codes=kc, k_scale=scale, v_codes=vc, v_scale=vs) if not shared else dict(k_codes=kc, k_scale=scale)
+    c = _paged(batch=batch, n_kv_heads=1, head_dim=D, block_tokens=bs, n_blocks=nb, max_blocks=nb, shared_kv=shared, buffers=buf)
+    c.table.copy_(torch.arange(nb, device="cuda").int().expand(batch, nb))
+    c.len.fill_(n)
+    q = torch.zeros((G, D), device="cuda")
+    q[:, 0] = 0.9 + 0.3 * torch.arange(G, device="cuda") / G
+    q = q.bfloat16()
+    # the formula in 64 bits
+    k = kc.view(FP8).double().view(-1, D)[:n]
+    v = vc.view(FP8).double().view(-1, D)[:n]
+    w = torch.softmax(q.double() @ k.t(), -1)
+    f = vs.double().repeat_interleave(bs)[:n]
+    want, mag = (w * f) @ v, (w * f) @ v.abs()
+    # Weights: fp16 (2^-11), then three terms, of which the last is rounded at 2^-9; scores here are one product of at most
+    # 16, in fp32 (2^-24 * 16 and as much again for the steps behind it, and 2^-22 of the exponential): under 2^-11 with
+    # fp16's. Steps of 2^-16 where the row's largest contribution is at least 2^10: 2^-27 of it per code. Sums of n / 32 steps
+    # for each of three terms, 2^-23 each (they may truncate). bf16 output: 2^-8.
+    tol = (2.0 ** -9 + 2 * 2.0 ** -11 + 3 * n / 32 * 2.0 ** -23) * mag + 2.0 ** -8 * want.abs()
+    tol += 2.0 ** -27 * (w * f).amax(-1, keepdim=True) * v.abs().sum(0)
+    return SimpleNamespace(c=c, q=q, want=want, tol=tol, mag=mag)
+
+
+@pytest.mark.parametrize("D,shared,G", [(128, False, 8), (128, True, 32), (256, False, 4), (256, True, 24), (256, False, 64),
+                                        (512, True, 64), (512, True, 16), (512, False, 32)])
+@pytest.mark.parametrize("n,depth,sd", [(8192, 11.0, 0.0), (32768, 10.0, 0.0), (32768, 10.0, 0.3), (32768, 11.0, 1.0),
+                                        (131072, 12.0, 0.3)])
+def test_attend_keeps_the_tail_behind_one_large_weight(D, shared, G, n, depth, sd):
+    """A first token with a large part of the weight (an attention sink) over a long flat tail, alone (cut into many parts)
+    and in a batch (whole requests to a CTA): the tail's weights are far below the largest and count together."""
+    got = []
+    for batch in (1, 320):
+        t = _tail(n, D, shared, G, depth, sd, batch=batch)
+        out = t.c.attend(t.q.expand(batch, G, D), _i32(list(range(batch + 1))), scale=1.0).double()
+        assert t.c.check_error() == 0
+        bad = ~((out - t.want).abs() <= t.tol)
+        assert not bad.any(), (batch, float(((out - t.want).abs() / t.mag).nan_to_num().max()))
+        got.append(out[-1])
+        t.c.close()
+    assert ((got[0] - got[1]).abs() <= 2 * t.tol).all()
+
+
+@pytest.mark.parametrize("D,G", [(128, 8), (128, 32), (256, 64), (512, 64), (512, 16)])
+@pytest.mark.parametrize("outlier", [11, 15])
+def test_attend_keeps_what_stands_beside_a_block_of_large_values(D, G, outlier):
+    t = _tail(4096, D, False, G, 2.0, 1.0, outlier=outlier)
+    out = t.c.attend(t.q[None], _i32([0, 1]), scale=1.0)[0].double()
+    assert t.c.check_error() == 0
+    assert ((out - t.want).abs() <= t.tol).all()
+    # (the bound says something there: 2^-8 + 2^-9 + 2^-10, and 2^-27 * 2^15 of a weight of at most about e^4.3 times the mean,
+    # for each of the tokens: under 2^-12 * 75, 2.6 % in all)
+    assert (t.tol[:, D // 2:] < 0.03 * t.want[:, D // 2:].abs()).all()
+    t.c.close()

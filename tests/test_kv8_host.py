@@ -41,3 +41,15 @@ def test_null_handles(abi):
     assert lib.kv8_create(None, None) == abi.SRH_ERR_INVALID
     assert lib.kv8_check_error(None) == abi.SRH_ERR_INVALID
     lib.kv8_destroy(None)
+
+
+def test_three_terms_hold_a_weight():
+    """What the attention's weights are split into: two e5m2 terms cut off an fp16 value and one rounded are within 2^-9 of
+    it, or half of e5m2's smallest step."""
+    import torch
+    h = torch.arange(0x7B00, dtype=torch.int16).view(torch.float16)        # up to 57,344
+    rest = h.clone()
+    for _ in range(2):
+        rest = (rest.float() - (rest.view(torch.int16) & -256).view(torch.float16).float()).half()
+    rest = rest.double() - rest.to(torch.float8_e5m2).double()
+    assert (rest.abs() <= (2.0 ** -9 * h.double()).clamp(min=2.0 ** -17)).all()
