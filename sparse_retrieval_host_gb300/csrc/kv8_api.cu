@@ -129,6 +129,8 @@ int kv8_create(const kv8_config* cfg, kv8_cache** out) {
         if (e == cudaSuccess) e = cudaMalloc(&c->d_meta, c->meta_n * sizeof(int4));
         if (e == cudaSuccess) e = cudaMalloc(&c->d_ctrl, 2 * sizeof(int));
         if (e == cudaSuccess) e = cudaMemset(c->d_ctrl, 0, 2 * sizeof(int));
+        // the clears run on the legacy stream, which streams that do not block do not wait for
+        if (e == cudaSuccess) e = cudaStreamSynchronize(0);
     }
     if (e != cudaSuccess) {
         const int rc = e == cudaErrorMemoryAllocation ? SRH_ERR_NOMEM : SRH_ERR_CUDA;

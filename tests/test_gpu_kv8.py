@@ -1030,3 +1030,28 @@ def test_attend_keeps_what_stands_beside_a_block_of_large_values(D, G, outlier):
     # for each of the tokens: under 2^-12 * 75, 2.6 % in all)
     assert (t.tol[:, D // 2:] < 0.03 * t.want[:, D // 2:].abs()).all()
     t.c.close()
+
+
+def test_a_cache_made_beside_a_busy_default_stream():
+    """The handle's own clears are over when it is there: its first call on a stream that does not wait for the default one
+    finds them done."""
+    c, g = _filled([5000, 77], 2, 128, 32, False, 121)
+    q, cu2 = _bf16(g, 2, 16, 128), _i32([0, 1, 2])
+    want = c.attend(q, cu2, scale=0.08)
+    x = torch.randn((8192, 8192), device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(40):                                     # some 25 ms
+        y = x @ x
+    busy = torch.cuda.Event()
+    busy.record()
+    buf = dict(k_codes=c.k_codes[0], k_scale=c.k_scale[0], v_codes=c.v_codes[0], v_scale=c.v_scale[0], table=c.table, len=c.len,
+               free=c.free, n_free=c.n_free)
+    with torch.cuda.stream(side):
+        d = _paged(batch=2, n_kv_heads=2, head_dim=128, block_tokens=32, n_blocks=c.n_blocks, max_blocks=c.max_blocks, buffers=buf)
+        assert busy.query()                                 # the clears come behind that work, and creation waits for them
+        out = d.attend(q, cu2, scale=0.08)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and d.check_error() == 0 and y.shape == x.shape
+    d.close()
+    c.close()
