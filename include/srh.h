@@ -610,7 +610,9 @@ void kv8_destroy(kv8_cache* c);
  *   d_cu          [n_req + 1] int32 out: cu[b+1] - cu[b] = max(0, new - old)
  *   d_pos, d_slot [cap] int32 / int64 out, both or neither NULL (then cap is
  *                 0): position of each new token in its request, and its slot
- *                 table[b][pos / block_tokens] * block_tokens + pos % block_tokens
+ *                 table[b][pos / block_tokens] * block_tokens + pos % block_tokens.
+ *                 Slots behind the last new token, all of them after a refusal, are
+ *                 left negative (kv8_norm_rope skips such), their positions as they were
  * Blocks are released first, so that the first of them (by request, then by
  * block) is on top of the stack, then taken from the top in the same order:
  * growing and shrinking back restores the stack. All or nothing: when a length

@@ -94,6 +94,12 @@ __device__ __forceinline__ void put_token(const Args& a, int i, int b, int begin
     a.slot[i] = ((int64_t)id << a.bs_log2) + (p & ((1 << a.bs_log2) - 1));
 }
 
+// A slot behind the last new token must not look like one: an earlier call's, or whatever
+// a new array holds, becomes -1 (a negative one is left).
+__device__ __forceinline__ void no_token(const Args& a, int i) {
+    if (a.slot[i] >= 0) a.slot[i] = -1;
+}
+
 __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     extern __shared__ int sums[];
     int* rel = sums;                    // [n_req + 1] released blocks before each request
@@ -159,6 +165,8 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     if (bad) {
         for (int b = tid; b <= a.n_req; b += nt) a.cu[b] = 0;
         if (tid == 0) atomicOr(a.err, none ? kErrNoBlocks : kErrBounds);
+        if (a.pos && a.fill_here)
+            for (int i = tid; i < a.cap; i += nt) no_token(a, i);
         return;
     }
     const int top = depth + (int)R;
@@ -195,17 +203,20 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
         const int b = last_not_above(tok, a.n_req, i);
         put_token(a, i, b, tok[b], tok[b + 1] - tok[b], a.new_len[b]);
     }
+    for (int i = (int)N + tid; i < a.cap; i += nt) no_token(a, i);
 }
 
-// Positions and slots of more than kInlineTokens tokens, after resize_kernel.
+// Positions and slots of more than kInlineTokens tokens, after resize_kernel (which has
+// left cu all 0 where it refused).
 __global__ void __launch_bounds__(kFillThreads) fill_kernel(const Args a) {
     extern __shared__ int tok[];
     pdl_wait();
     const int N = a.cu[a.n_req];
+    const int i = blockIdx.x * kFillThreads + threadIdx.x;
+    if (i >= N && i < a.cap) no_token(a, i);
     if ((int)(blockIdx.x * kFillThreads) >= N) return;
     for (int b = threadIdx.x; b <= a.n_req; b += kFillThreads) tok[b] = a.cu[b];
     __syncthreads();
-    const int i = blockIdx.x * kFillThreads + threadIdx.x;
     if (i >= N) return;
     const int b = last_not_above(tok, a.n_req, i);
     put_token(a, i, b, tok[b], tok[b + 1] - tok[b], a.len[b]);

@@ -167,7 +167,8 @@ class PagedKV8:
         blocks taken or given back. ``n_new``: room for new tokens (their number,
         or more). Returns ``cu`` int32 [n + 1] and, with ``n_new``, ``pos`` int32 and
         ``slot`` int64 of the new tokens (else None, None); ``out`` gives the
-        three tensors to write. Asynchronous; see kv8_resize for refusals."""
+        three tensors to write. Slots behind the last new token (all of them after
+        a refusal) are negative. Asynchronous; see kv8_resize for refusals."""
         self._ints(new_len, "new_len")
         n = new_len.shape[0]
         if not 1 <= n <= self.batch:

@@ -1055,3 +1055,42 @@ def test_a_cache_made_beside_a_busy_default_stream():
     assert torch.equal(out, want) and d.check_error() == 0 and y.shape == x.shape
     d.close()
     c.close()
+
+
+@pytest.mark.parametrize("room", [40, 5000])               # one CTA, and a grid of its own
+def test_slots_behind_the_last_token_name_no_row(room):
+    """Arrays with room for more tokens than there are, used again and again as in a captured step: rows that are padding
+    go nowhere, after a refused call too."""
+    abi = _abi()
+    g = _gen(131)
+    c = _paged(batch=3, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=400, max_blocks=400)
+    x, pos0 = _bf16(g, room, 1, 128), torch.zeros(room, dtype=torch.int32, device="cuda")
+    held = torch.full((400 * 16, 1, 128), 5.0, device="cuda").bfloat16()
+    out = (_i32([0] * 4), pos0, torch.full((room,), 3, dtype=torch.int64, device="cuda"))      # as memory used before
+    for new, n in (([30, 4, 0], 34), ([31, 5, 1], 3), ([31, 5, 1], 0), ([room, 5, 1], room - 31), ([-1, 9, 9], 0),
+                   ([32 + room, 5, 1], 32), ([0, 0, 0], 0)):
+        cu, pos, slot = c.resize(_i32(new), room, out=out)
+        code = abi.SRH_ERR_BOUNDS if new[0] < 0 else abi.SRH_OK
+        assert c.check_error() == code and int(cu[3]) == n
+        assert (slot[n:] == -1).all() and (slot[:n] >= 0).all()
+        held.fill_(5.0)
+        c.norm_rope(x, q_out=held, q_slot=slot)
+        rows = torch.zeros(400 * 16, dtype=torch.bool, device="cuda")
+        rows[slot[:n]] = True
+        assert (held[~rows] == 5).all() and c.check_error() == abi.SRH_OK
+    # refused for its cap: the slots of the call before name nothing either
+    c.resize(_i32([20, 0, 0]), room, out=out)
+    c.resize(_i32([20 + room + 1, 0, 0]), room, out=out)
+    assert c.check_error() == abi.SRH_ERR_BOUNDS and (out[2] == -1).all()
+    c.close()
+
+
+def test_new_slot_arrays_hold_no_old_rows():
+    c = _paged(batch=2, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=64, max_blocks=64)
+    for n in (300, 9000):
+        old = [torch.full((n,), 7, dtype=torch.int64, device="cuda") for _ in range(8)]
+        del old                                             # (the allocator hands their memory out again)
+        _, _, slot = c.resize(_i32([2, 1]), n)
+        assert (slot[:3] >= 0).all() and (slot[3:] < 0).all()
+        c.resize(_i32([0, 0]))
+    c.close()
