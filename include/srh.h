@@ -616,8 +616,8 @@ void kv8_destroy(kv8_cache* c);
  * Blocks are released first, so that the first of them (by request, then by
  * block) is on top of the stack, then taken from the top in the same order:
  * growing and shrinking back restores the stack. All or nothing: when a length
- * is out of range, a released entry is no block, the free blocks or cap do not
- * suffice, nothing changes, d_cu is all zeros, and kv8_check_error() returns
+ * is out of range, a released or a taken entry is no block, the free blocks or cap
+ * do not suffice, nothing of these changes, d_cu is all zeros, and kv8_check_error() returns
  * SRH_ERR_NOMEM (too few free blocks) or SRH_ERR_BOUNDS. Users of a block are
  * not counted: each request that gives an entry up pushes its block.
  */

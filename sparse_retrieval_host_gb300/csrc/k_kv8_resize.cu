@@ -153,11 +153,17 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     const bool none = !bad && A > depth + R;           // the same in every thread
     bad = bad || none;
     if (!bad) {
-        // a released entry that is no block fails the call before anything changes
+        // a released or taken entry that is no block fails the call before anything changes
         for (int i = tid; i < (int)R; i += nt) {
             const int b = last_not_above(rel, a.n_req, i);
             const int j = kept[b] + i - rel[b];
             const int id = a.table[(size_t)b * a.max_blocks + j];
+            if (id < 0 || id >= a.n_blocks) bad = true;
+        }
+        // (the first R taken are the released ones)
+#pragma unroll 4
+        for (int k = (int)R + tid; k < (int)A; k += nt) {
+            const int id = __ldcg(a.free_ids + depth + (int)R - 1 - k);
             if (id < 0 || id >= a.n_blocks) bad = true;
         }
         bad = __syncthreads_or(bad);
@@ -182,12 +188,8 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const Args a) {
     for (int k = tid; k < (int)A; k += nt) {
         const int b = last_not_above(alc, a.n_req, k);
         const int j = kept[b] + k - alc[b];
-        int id = __ldcg(a.free_ids + top - 1 - k);     // (written above by other threads, in L2)
-        if (id < 0 || id >= a.n_blocks) {   // the caller's stack holds something else
-            atomicOr(a.err, kErrBounds);
-            id = -1;
-        }
-        a.table[(size_t)b * a.max_blocks + j] = id;
+        // (the first ones written above by other threads, in L2)
+        a.table[(size_t)b * a.max_blocks + j] = __ldcg(a.free_ids + top - 1 - k);
     }
     __syncthreads();
     for (int b = tid; b < a.n_req; b += nt) {

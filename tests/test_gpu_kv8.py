@@ -1094,3 +1094,28 @@ def test_new_slot_arrays_hold_no_old_rows():
         assert (slot[:3] >= 0).all() and (slot[3:] < 0).all()
         c.resize(_i32([0, 0]))
     c.close()
+
+
+@pytest.mark.parametrize("bad", [99, -1, 1 << 30])
+@pytest.mark.parametrize("new", [[33, 10, 20], [200, 0, 0], [0, 40, 200]])
+def test_resize_refuses_a_stack_that_holds_no_block(bad, new):
+    """An id to be taken that names no block: refused as a whole, as the other causes are; one deeper down is not looked at."""
+    abi = _abi()
+    c = _paged(batch=3, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=40, max_blocks=16)
+    c.resize(_i32([30, 10, 0]), 40)
+    have, need = [2, 1, 0], [-(-n // 16) for n in new]
+    taken = sum(max(0, a - b) for a, b in zip(need, have)) - sum(max(0, b - a) for a, b in zip(need, have))
+    depth = int(c.n_free)
+    for at in (depth - 1, depth - taken):                   # the first and the last one from the stack
+        good = c.free.clone()
+        c.free[at] = bad
+        before = [t.clone() for t in (c.table, c.len, c.free, c.n_free)]
+        cu, pos, slot = c.resize(_i32(new), 300)
+        assert cu.tolist() == [0] * 4 and (slot < 0).all()
+        assert all(torch.equal(a, b) for a, b in zip(before, (c.table, c.len, c.free, c.n_free)))
+        assert c.check_error() == abi.SRH_ERR_BOUNDS
+        c.free.copy_(good)
+    c.free[depth - taken - 1] = bad
+    c.resize(_i32(new), 300)
+    assert c.check_error() == abi.SRH_OK and c.len.tolist() == new
+    c.close()
