@@ -684,8 +684,10 @@ int kv8_append(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const
  * for query row i of request b at position p = len[b] - (cu[b+1] - cu[b]) + i,
  * over tokens t <= p (and t > p - window with window > 0); query head h reads
  * KV head h / (n_heads / n_kv_heads). A row that sees no token gives zeros.
- * (A call of more than 2^30 tiles of 128 tokens x 16 to 64 rows of a KV head, far
- * more than a minute of work, writes nothing: SRH_ERR_BOUNDS.)
+ * Rows of a request whose length is out of range are left as they are, as are rows
+ * of d_out outside [0, n_rows) that cu names. A call whose cu descends anywhere
+ * writes nothing, nor does one of more than 2^30 tiles of 128 tokens x 16 to 64 rows
+ * of a KV head, far more than a minute of work. All of these: SRH_ERR_BOUNDS.
  *   d_q, d_out  bf16 [n_rows] rows of [n_heads][head_dim], 16-byte aligned, row
  *               strides in elements, multiples of 8; d_out is not d_q
  *   n_heads     a multiple of n_kv_heads; n_rows * n_heads <= 2^30

@@ -191,9 +191,13 @@ __device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
     Request r;
     const int c0 = a.cu[b], c1 = a.cu[b + 1], n = a.len[b], most = a.max_blocks << a.bs_log2;
     r.q0 = min(max(c0, 0), a.n_rows);
-    r.nq = min(max(c1, r.q0), a.n_rows) - r.q0;
-    r.len = min(max(n, 0), most);
-    if (c0 != r.q0 || c1 != r.q0 + r.nq || n != r.len) *bad = true;
+    r.nq = min(max(c1, r.q0), a.n_rows) - r.q0;               // (rows outside q are not there)
+    r.len = n;
+    if (c0 != r.q0 || c1 != r.q0 + r.nq) *bad = true;
+    if (n < 0 || n > most) {                                  // no such request
+        *bad = true;
+        r.nq = r.len = 0;
+    }
     r.nrt = (r.nq * a.group + RT - 1) / RT;
     // A causal row tile has the more tokens the later it is; row tiles k and
     // nrt - 1 - k together have the same, up to one tile for the rounding (or
@@ -534,6 +538,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int b = b0; b < b1; ++b) {
             const Request r = request<RT>(a, b, &bad);
             mine += (long long)r.pairs * r.P * a.kv_heads;
+            // where cu descends, requests may share rows of out: refused like too much work
+            if (a.cu[b + 1] < a.cu[b]) mine += 2ll * kMaxUnits;
         }
         if (few) {
             incl = mine;
@@ -547,7 +553,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             incl = block_scan(mine, bs.warp_sums, &total);
         }
         if (cta == 0 && bad) atomicOr(a.err, kErrBounds);
-        if (total > kMaxUnits) {                           // too much for one call: reported, nothing written
+        if (total > kMaxUnits) {                           // reported, nothing written
             if (i == 0) atomicOr(a.err, kErrBounds);
             total = 0;
         }

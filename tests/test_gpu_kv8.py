@@ -1119,3 +1119,32 @@ def test_resize_refuses_a_stack_that_holds_no_block(bad, new):
     c.resize(_i32(new), 300)
     assert c.check_error() == abi.SRH_OK and c.len.tolist() == new
     c.close()
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 3, 8], [0, 5, 3, 4, 8], [8, 0], [0, 8, 8, 7] + [8] * 60])
+def test_attend_refuses_rows_that_two_requests_would_write(cu):
+    abi = _abi()
+    n = len(cu) - 1
+    c, g = _filled([60 + b for b in range(n)], 2, 128, 16, False, 141)
+    q, out = _bf16(g, 8, 8, 128), torch.full((8, 8, 128), 7.0, device="cuda").bfloat16()
+    c.attend(q, _i32(cu), scale=0.05, out=out)
+    assert c.check_error() == abi.SRH_ERR_BOUNDS and (out == 7).all()
+    c.attend(q, _i32(sorted(cu)), scale=0.05, out=out)
+    assert c.check_error() == 0
+    _check_attend(c, q, _i32(sorted(cu)), out, 0.05, 0)
+    c.close()
+
+
+@pytest.mark.parametrize("bad", [-1, 321, 1 << 30, -(1 << 31)])
+def test_attend_leaves_out_requests_of_impossible_lengths(bad):
+    abi = _abi()
+    c, g = _filled([300, 200, 290], 1, 128, 16, True, 151)
+    assert c.max_blocks * 16 == 320
+    q, cu = _bf16(g, 6, 4, 128), _i32([0, 1, 4, 6])
+    good = c.attend(q, cu, scale=0.05)
+    c.len[1] = bad
+    out = torch.full_like(q, 7.0)
+    c.attend(q, cu, scale=0.05, out=out)
+    assert c.check_error() == abi.SRH_ERR_BOUNDS
+    assert (out[1:4] == 7).all() and torch.equal(out[:1], good[:1]) and torch.equal(out[4:], good[4:])
+    c.close()
