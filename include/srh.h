@@ -650,7 +650,9 @@ typedef struct {
  *   head_dim    8 .. 512, a multiple of 8; rot_dim a multiple of 16 and
  *               rot_off of 8, rot_off + rot_dim <= head_dim
  *   eps         >= 0, finite
- * A slot >= n_slots is skipped and reported as SRH_ERR_BOUNDS.
+ * A slot >= n_slots is skipped and reported as SRH_ERR_BOUNDS. But for out being x,
+ * no row of an out overlaps a row of an x or of the other out (rows may lie between
+ * each other's, with one stride).
  */
 #define KV8_ROPE_PAIRS 0
 #define KV8_ROPE_HALVES 1
@@ -689,7 +691,8 @@ int kv8_append(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const
  * writes nothing, nor does one of more than 2^30 tiles of 128 tokens x 16 to 64 rows
  * of a KV head, far more than a minute of work. All of these: SRH_ERR_BOUNDS.
  *   d_q, d_out  bf16 [n_rows] rows of [n_heads][head_dim], 16-byte aligned, row
- *               strides in elements, multiples of 8; d_out is not d_q
+ *               strides in elements, multiples of 8; no row of d_out overlaps one
+ *               of d_q (rows may lie between each other's, with one stride)
  *   n_heads     a multiple of n_kv_heads; n_rows * n_heads <= 2^30
  *   scale       finite; window >= 0
  * Precision: fp32 scores, statistics and sums. Queries enter the products as

@@ -51,6 +51,28 @@ bool row_ok(long long stride, long long width, long long rows, bool out) {
     return !out || rows <= 1 || stride >= width;
 }
 
+// Rows of bf16 values in memory.
+struct Rows {
+    const uint16_t* p;
+    long long stride, n, width;      // elements, rows, elements
+};
+// Whether any row of a shares memory with a row of b. Rows of one stride may lie between
+// each other's; of different strides, ranges that cross count as shared.
+bool meet(const Rows& a, const Rows& b) {
+    using Wide = unsigned __int128;
+    if (a.n < 1 || b.n < 1) return false;
+    if (reinterpret_cast<uintptr_t>(a.p) > reinterpret_cast<uintptr_t>(b.p)) return meet(b, a);
+    const uint64_t apart = (reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) / sizeof(uint16_t);
+    if (apart >= (Wide)(a.n - 1) * (Wide)a.stride + (Wide)a.width) return false;
+    if (a.n == 1) return true;
+    if (b.n > 1 && b.stride != a.stride) return true;
+    if (a.stride == 0) return true;
+    // b's first row begins `d` behind a row of a; a's next one may reach into it
+    const uint64_t d = apart % (uint64_t)a.stride, before = apart / (uint64_t)a.stride;
+    if (d < (uint64_t)a.width) return true;
+    return d + (uint64_t)b.width > (uint64_t)a.stride && before + 1 < (uint64_t)a.n;
+}
+
 const char* config_error(const kv8_config* k) {
     if (!k) return "config is NULL";
     if (k->batch < 1 || k->batch > kv8::kMaxBatch) return "batch must be in [1, 4096]";
@@ -87,6 +109,19 @@ const char* heads_error(const kv8_heads& h, int n_tok, int head_dim) {
         return "row strides must be multiples of 8 (outputs' at least a row)";
     if (h.slot && (h.n_slots < 0 || !aligned(h.slot, 8))) return "n_slots must be >= 0, slots 8-byte aligned";
     if (h.out == h.x && (h.slot || h.x_row != h.out_row)) return "in place needs the same row stride and no slots";
+    return nullptr;
+}
+// Outputs of `h` on rows that anything else of the call reads or writes.
+const char* overlap_error(const kv8_heads& h, const kv8_heads& other, int n_tok, int head_dim) {
+    if (h.n_heads == 0) return nullptr;
+    const long long n_out = h.slot ? h.n_slots : n_tok;
+    const Rows out{h.out, h.out_row, n_out, (long long)h.n_heads * head_dim};
+    if (h.out != h.x && meet(out, {h.x, h.x_row, n_tok, out.width})) return "out overlaps x without being x";
+    if (other.n_heads == 0) return nullptr;
+    const long long width = (long long)other.n_heads * head_dim;
+    if (meet(out, {other.x, other.x_row, n_tok, width}) ||
+        meet(out, {other.out, other.out_row, other.slot ? other.n_slots : n_tok, width}))
+        return "the outputs of one kind of heads overlap the other's rows";
     return nullptr;
 }
 
@@ -189,6 +224,8 @@ int kv8_norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_to
     if (rot_dim && (!d_pos || !d_inv_freq || !aligned(d_pos, 4) || !aligned(d_inv_freq, 8)))
         return fail(c, SRH_ERR_INVALID, "d_pos and d_inv_freq must not be NULL, and aligned");
     if (n_tok == 0) return SRH_OK;
+    if (const char* why = overlap_error(a, b, n_tok, head_dim)) return fail(c, SRH_ERR_INVALID, why);
+    if (const char* why = overlap_error(b, a, n_tok, head_dim)) return fail(c, SRH_ERR_INVALID, why);
     KV8_DEVICE(c);
     const cudaError_t e = kv8::launch_norm_rope(*c, a, b, n_tok, head_dim, d_pos, d_inv_freq, rot_dim, rot_off, style, eps,
                                                 (cudaStream_t)stream);
@@ -231,7 +268,8 @@ int kv8_attend(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const
     const long long width = (long long)n_heads * c->cfg.head_dim;
     if (!row_ok(q_row, width, n_rows, false) || !row_ok(out_row, width, n_rows, true))
         return fail(c, SRH_ERR_INVALID, "row strides must be multiples of 8 (the output's at least a row)");
-    if (d_out == d_q) return fail(c, SRH_ERR_INVALID, "out must not be q");
+    if (meet({d_q, q_row, n_rows, width}, {d_out, out_row, n_rows, width}))
+        return fail(c, SRH_ERR_INVALID, "out must not overlap q");
     KV8_DEVICE(c);
     const cudaError_t e = kv8::launch_attend(*c, *pool, d_table, d_len, d_cu, n_req, d_q, q_row, n_rows, n_heads, scale,
                                              window, d_out, out_row, (cudaStream_t)stream);

@@ -1148,3 +1148,52 @@ def test_attend_leaves_out_requests_of_impossible_lengths(bad):
     assert c.check_error() == abi.SRH_ERR_BOUNDS
     assert (out[1:4] == 7).all() and torch.equal(out[:1], good[:1]) and torch.equal(out[4:], good[4:])
     c.close()
+
+
+def test_attend_refuses_an_output_that_overlaps_its_queries():
+    abi = _abi()
+    c, g = _filled([300, 77], 2, 128, 16, False, 161)
+    cu, n = _i32([0, 3, 5]), 5 * 8 * 128
+    flat = _bf16(g, 4 * n)
+    q = flat[n:2 * n].view(5, 8, 128)
+    for at in (n, n + 8, n - 8, n + 1024, 8, 2 * n - 8):    # the same rows, shifted either way by less than they hold
+        with pytest.raises(abi.SrhError, match="overlap"):
+            c.attend(q, cu, scale=0.06, out=flat[at:at + n].view(5, 8, 128))
+    wide = flat[:3 * n].view(5, 3, 1024)                    # rows between each other's
+    for qa, oa in ((0, 0), (0, 1000), (1000, 0), (8, 0), (1504, 2040)):
+        with pytest.raises(abi.SrhError, match="overlap"):
+            c.attend(wide.view(5, 3072)[:, qa:qa + 1024].view(5, 8, 128), cu, scale=0.06,
+                     out=wide.view(5, 3072)[:, oa:oa + 1024].view(5, 8, 128))
+    want, keep, row = None, q.reshape(5, 1024).clone(), wide.view(5, 3072)
+    for qa, oa in ((0, 1024), (2048, 0), (8, 1032), (2048, 1024)):
+        row[:, qa:qa + 1024] = keep
+        got = c.attend(row[:, qa:qa + 1024].view(5, 8, 128), cu, scale=0.06, out=row[:, oa:oa + 1024].view(5, 8, 128))
+        want = got.clone() if want is None else want
+        assert torch.equal(got, want) and torch.equal(row[:, qa:qa + 1024], keep)
+    assert c.check_error() == 0
+    c.close()
+
+
+def test_norm_refuses_outputs_that_overlap_other_rows():
+    abi = _abi()
+    g = _gen(171)
+    c = _paged(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=1, max_blocks=1)
+    row = _bf16(g, 6, 2048)                                 # 4 query heads, 2 key heads, room
+    q, k, slot = row[:, :512].view(6, 4, 128), row[:, 512:768].view(6, 2, 128), torch.arange(6, device="cuda")
+    at = lambda o, h: row[:, o:o + h * 128].view(6, h, 128)  # noqa: E731
+    new = lambda h: torch.empty((6, h, 128), device="cuda").bfloat16()  # noqa: E731
+    for kw in (dict(q=q, q_out=at(8, 4)), dict(q=at(256, 4), q_out=at(0, 4)), dict(q=q, k=k, q_out=at(264, 4)),
+               dict(q=q, k=k, q_out=at(1024, 4), k_out=at(1280, 2)), dict(q=q, k=k, k_out=at(0, 2)),
+               dict(q=q, k=k, q_out=at(768, 4), k_out=at(1272, 2)), dict(k=k, k_out=at(640, 2), k_slot=slot),
+               dict(q=q, k=k, q_out=q, k_out=q[:, :2]), dict(q=q, q_out=row.view(-1)[3072:3072 + 6 * 512].view(6, 4, 128))):
+        with pytest.raises(abi.SrhError, match="overlap|in place"):
+            c.norm_rope(**kw)
+    wq, wk = c.norm_rope(q, k, q_out=new(4), k_out=new(2))
+    # side by side in one row, in place beside the other, and with slots
+    a, b = c.norm_rope(q, k, q_out=at(768, 4), k_out=at(1280, 2))
+    assert torch.equal(a, wq) and torch.equal(b, wk)
+    _, b = c.norm_rope(None, k, k_out=at(1536, 2), k_slot=slot)
+    assert torch.equal(b, wk)
+    a, b = c.norm_rope(q, k, q_out=q, k_out=k)
+    assert torch.equal(a, wq) and torch.equal(b, wk) and c.check_error() == 0
+    c.close()
