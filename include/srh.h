@@ -665,7 +665,9 @@ int kv8_norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_to
  * left) into the cache.
  *   d_k, d_v  bf16 rows [n_rows] of [n_kv_heads][head_dim], 16-byte aligned,
  *             row strides in elements, multiples of 8; d_v ignored with shared_kv
- *   n_rows    rows of d_k / d_v: cu[n_req] <= n_rows
+ *   n_rows    rows of d_k / d_v: cu[n_req] <= n_rows. A request whose rows lie
+ *             outside them, or whose length is out of range or less than its rows,
+ *             is left out
  * Per (block, head): scale = 2^e with the smallest e for which the block's
  * largest magnitude is <= 448 * 2^e, code = e4m3(x / scale) (to nearest, ties to
  * even). A block that held tokens of the request before keeps the larger of its

@@ -122,7 +122,11 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
         if (tid == 0) first[a.n_req] = (int)blocks;
         __syncthreads();
     }
-    if (bad) atomicOr(a.err, kErrBounds);
+    // requests of an ascending cu touch no more blocks than there are rows; of a descending
+    // one, which share rows, they may touch more than `first` counts
+    const bool many = blocks > 0x7fffffffll;
+    if (bad || many) atomicOr(a.err, kErrBounds);
+    if (many) return;                                    // (every thread)
 
     const long long units = blocks * a.heads * a.parts;
     constexpr int kGroups = kThreads / GT;

@@ -1197,3 +1197,19 @@ def test_norm_refuses_outputs_that_overlap_other_rows():
     a, b = c.norm_rope(q, k, q_out=q, k_out=k)
     assert torch.equal(a, wq) and torch.equal(b, wk) and c.check_error() == 0
     c.close()
+
+
+def test_append_counts_no_further_than_its_blocks_go():
+    """2,048 of 4,096 requests name the same 17 million rows (one row, repeated): more blocks than an int counts. Refused as a
+    whole; no table entry is read, so none is set."""
+    abi = _abi()
+    n = (1 << 24) + 4096
+    mb = n // 16 + 1
+    buf = dict(table=torch.empty((4096, mb), dtype=torch.int32, device="cuda"))
+    c = _paged(batch=4096, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=4, max_blocks=mb, shared_kv=True, buffers=buf)
+    c.len.fill_(n)
+    k = torch.ones((1, 1, 128), device="cuda").bfloat16().expand(n, 1, 128)
+    c.append(k, None, _i32([0, n] * 2048 + [0]))
+    assert c.check_error() == abi.SRH_ERR_BOUNDS
+    assert (c.k_codes[0] == 0).all() and (c.k_scale[0] == 1).all()
+    c.close()
