@@ -11,7 +11,9 @@ codes and block scales (or adopts the caller's tensors). One serving step is
 
 and ``resize`` with shorter lengths gives rejected drafted tokens back. All work
 runs in the library's kernels (kv8_* of include/srh.h); PyTorch allocates
-tensors and names streams. Calls on one cache are ordered by the caller.
+tensors and names streams. Calls on one cache are ordered by the caller. A call
+on a ``stream`` of its own waits for nothing on the current one; the tensors that it
+is given may be let go as soon as it returns.
 """
 from __future__ import annotations
 
@@ -136,6 +138,14 @@ class PagedKV8:
         with torch.cuda.stream(s):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
+    def _keep(self, stream, *tensors) -> None:
+        """Memory of a call's tensors is not handed out again before ``stream`` is through with them."""
+        if stream is not None:
+            s = torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+
     def _rows(self, t: torch.Tensor, name: str, heads: Optional[int] = None, dim: Optional[int] = None) -> int:
         """Row stride (elements) of a bf16 [rows][heads][dim] tensor with dense rows."""
         if t.dtype not in _BF16 or t.dim() != 3 or t.get_device() != self._index:
@@ -192,6 +202,7 @@ class PagedKV8:
                                   n_new, self._s(stream))
         if rc:
             self._raise(rc, "kv8_resize")
+        self._keep(stream, new_len, cu, pos, slot)
         return cu, pos, slot
 
     def norm_rope(self, q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None, *, pos=None, inv_freq=None,
@@ -245,6 +256,7 @@ class PagedKV8:
                                          self._s(stream))
             if rc:
                 self._raise(rc, "kv8_norm_rope")
+            self._keep(stream, q, k, pos, inv_freq, q_weight, k_weight, q_slot, k_slot, *outs)
         return outs[0], outs[1]
 
     def append(self, k: torch.Tensor, v: Optional[torch.Tensor], cu: torch.Tensor, *, layer: int = 0, stream=None) -> None:
@@ -264,6 +276,7 @@ class PagedKV8:
                                       kr, None if v is None else v.data_ptr(), vr, k.shape[0], self._s(stream))
             if rc:
                 self._raise(rc, "kv8_append")
+            self._keep(stream, k, v, cu)
 
     def attend(self, q: torch.Tensor, cu: torch.Tensor, *, scale: float, window: int = 0, out=None, layer: int = 0,
                stream=None) -> torch.Tensor:
@@ -283,6 +296,7 @@ class PagedKV8:
                                       qr, q.shape[0], q.shape[1], scale, window, out.data_ptr(), orow, self._s(stream))
             if rc:
                 self._raise(rc, "kv8_attend")
+            self._keep(stream, q, cu, out)
         return out
 
     # ------------------------------------------------------------------ status

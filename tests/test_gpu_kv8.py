@@ -1213,3 +1213,69 @@ def test_append_counts_no_further_than_its_blocks_go():
     assert c.check_error() == abi.SRH_ERR_BOUNDS
     assert (c.k_codes[0] == 0).all() and (c.k_scale[0] == 1).all()
     c.close()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_tensors_of_a_call_on_another_stream_may_be_let_go(handle):
+    """Inputs that the caller drops while the call still waits on its stream: their memory is not handed out before."""
+    g = _gen(181)
+    c = _paged(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=40, max_blocks=20)
+    lens, n = [100, 60], 160
+    q, k, v = _bf16(g, n, 8, 128), _bf16(g, n, 2, 128), _bf16(g, n, 2, 128)
+    pos, freq, w = torch.arange(n, device="cuda").int(), torch.rand(64, device="cuda", dtype=torch.float64), torch.rand(128, device="cuda")
+
+    def step(side, s):
+        new = _i32(lens)
+        if side:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for _ in range(20):
+                    big @ big
+        cu, _, _ = c.resize(new, n, stream=s)
+        del new
+        a = [t.clone() for t in (q, k, v, pos, freq, w)]
+        if side:
+            side.wait_stream(torch.cuda.current_stream())
+        qq, kk = c.norm_rope(a[0], a[1], pos=a[3], inv_freq=a[4], rot_dim=128, q_weight=a[5], stream=s)
+        c.append(kk, a[2], cu, stream=s)
+        out = c.attend(qq, cu, scale=0.09, stream=s)
+        del a, cu, qq, kk
+        for m in (n * 1024, n * 256, n * 2, n, 64 * 4, 128 * 2, 6, 4, 2):          # what is free now is written over
+            for _ in range(6):
+                torch.full((m,), 77, dtype=torch.int16, device="cuda")
+                hold.append(torch.full((m,), 77, dtype=torch.int16, device="cuda"))
+        torch.cuda.synchronize()
+        assert c.check_error() == 0
+        return out
+
+    big, hold = torch.randn((8192, 8192), device="cuda").bfloat16(), []
+    want = step(None, None)
+    c.resize(_i32([0, 0]))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = step(side, side.cuda_stream if handle else side)
+    assert torch.equal(got, want)
+    c.close()
+
+
+def test_a_call_that_names_the_capturing_stream():
+    c, g = _filled([500, 77], 2, 128, 32, False, 191)
+    q, cu = _bf16(g, 2, 16, 128), _i32([0, 1, 2])
+    want, s = c.attend(q, cu, scale=0.08), torch.cuda.Stream()
+    for how in (s, s.cuda_stream):
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            twice = q * 2                                   # from the graph's own memory
+            out = c.attend(twice, cu, scale=0.04, stream=how)
+            del twice
+            again = c.attend(q, cu, scale=0.08, stream=how)
+        for _ in range(3):
+            out.zero_()
+            again.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(again, want)
+        del out, again, graph
+    assert c.check_error() == 0
+    c.close()
