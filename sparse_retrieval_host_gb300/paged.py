@@ -60,6 +60,8 @@ class PagedKV8:
             if "v_codes" in buf or "v_scale" in buf:
                 raise ValueError("a shared cache has one pool")
         dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError("the cache lives on a CUDA device")
         self.device = torch.device("cuda", torch.cuda.current_device() if dev.index is None else dev.index)
         self.batch, self.Hk, self.D, self.bs = batch, n_kv_heads, head_dim, block_tokens
         self.n_blocks, self.max_blocks, self.shared = n_blocks, max_blocks, bool(shared_kv)

@@ -53,3 +53,10 @@ def test_three_terms_hold_a_weight():
         rest = (rest.float() - (rest.view(torch.int16) & -256).view(torch.float16).float()).half()
     rest = rest.double() - rest.to(torch.float8_e5m2).double()
     assert (rest.abs() <= (2.0 ** -9 * h.double()).clamp(min=2.0 ** -17)).all()
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_a_cache_on_no_gpu_is_refused(device):
+    from sparse_retrieval_host_gb300.paged import PagedKV8
+    with pytest.raises(ValueError, match="CUDA device"):
+        PagedKV8(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=1, max_blocks=1, device=device)
