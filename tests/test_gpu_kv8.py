@@ -1279,3 +1279,48 @@ def test_a_call_that_names_the_capturing_stream():
         del out, again, graph
     assert c.check_error() == 0
     c.close()
+
+
+def _check_closely(c, q, cu, out, scale, window):
+    """Every value within what three e5m2 terms per weight allow, however many tokens there are: 2^-9 and fp16's 2^-11 of each
+    weight, 2^-27 of the row's largest contribution (2^-17 where that is at least 2^10), n / 32 additions for each of three
+    terms at 2^-23; scores as in _check_attend; bf16 output 2^-8."""
+    D, Hk, bs, G = c.D, c.Hk, c.bs, q.shape[1] // c.Hk
+    cul, ln = cu.tolist(), c.len.tolist()
+    for b in range(len(cul) - 1):
+        nq, n = cul[b + 1] - cul[b], ln[b]
+        if nq == 0 or n == 0:
+            continue
+        ids = c.table[b, :-(-n // bs)].long()
+        kc, vc = (t[0][ids].view(FP8).double().permute(1, 0, 2, 3).reshape(Hk, -1, D)[:, :n] for t in (c.k_codes, c.v_codes))
+        ks, vs = (t[0][ids].double().t().repeat_interleave(bs, 1)[:, None, :n] for t in (c.k_scale, c.v_scale))
+        y = q[cul[b]:cul[b + 1]].double().view(nq, Hk, G, D).permute(1, 2, 0, 3).reshape(Hk, G * nq, D)
+        pos = torch.arange(n - nq, n, device="cuda").repeat(G)[:, None]
+        t = torch.arange(n, device="cuda")
+        see = (t <= pos) & (t > pos - (window or n + nq))
+        s = torch.where(see, y @ (kc.transpose(1, 2) * ks) * scale, float("-inf"))
+        eps = ((D + 8) * 2.0 ** -24 * (y.abs() @ kc.abs().transpose(1, 2)) +
+               2.0 ** -17 * y.abs().amax(-1, keepdim=True) * kc.abs().sum(-1)[:, None]) * ks * abs(scale)
+        w = torch.where(pos < 0, 0.0, torch.softmax(s, -1)) * vs           # contributions per code
+        want, mag = w @ vc, w @ vc.abs()
+        tol = (2.0 ** -9 + 2.0 ** -10 + 3 * n / 32 * 2.0 ** -23 + 2 * (eps * see).amax(-1, keepdim=True)) * mag
+        tol += 2.0 ** -27 * w.amax(-1, keepdim=True) * (see.double() @ vc.abs()) + 2.0 ** -8 * want.abs()
+        got = out[cul[b]:cul[b + 1]].double().view(nq, Hk, G, D).permute(1, 2, 0, 3).reshape(Hk, G * nq, D)
+        bad = ~((got - want).abs() <= tol)
+        assert not bad.any(), (b, int(bad.sum()), float(((got - want).abs() - tol).max()))
+
+
+@pytest.mark.parametrize("H,Hk,D,shared,bs", [(16, 2, 128, False, 16), (48, 1, 128, True, 64), (8, 2, 256, False, 32),
+                                              (24, 1, 256, True, 128), (64, 1, 256, False, 64), (16, 1, 512, True, 16),
+                                              (32, 1, 512, False, 64), (64, 1, 512, True, 64)])
+@pytest.mark.parametrize("spread,window", [(0, 0), (3, 0), (2, 700)])
+def test_attend_is_as_close_over_long_requests(H, Hk, D, shared, bs, spread, window):
+    """Block scales 2^spread apart either way, so that a row's tiles differ by many powers of two and its reference moves."""
+    lens, nq = [20000, 3000, 129, 9000], [2, 40, 3, 1]
+    c, g = _filled(lens, Hk, D, bs, shared, H + D + spread, spread=spread)
+    q, cu = _bf16(g, 46, H, D), _i32([0, 2, 42, 45, 46])
+    scale = D ** -0.5 / 2
+    out = c.attend(q, cu, scale=scale, window=window)
+    assert c.check_error() == 0
+    _check_closely(c, q, cu, out, scale, window)
+    c.close()
