@@ -644,7 +644,8 @@ typedef struct {
  * t = pos * inv_freq[i] for pair i: dims 2i and 2i+1 (KV8_ROPE_PAIRS) or i and
  * i + rot_dim/2 (KV8_ROPE_HALVES) from rot_off. Queries and keys in one launch
  * (an indexer's queries and keys, or an attention's). The angle is reduced to
- * a turn in 64-bit fixed point, so far positions lose nothing.
+ * a turn in 64-bit fixed point, so far positions lose about 2^-52 of
+ * pos * inv_freq.
  *   d_pos       [n_tok] int32 (any value)
  *   d_inv_freq  [rot_dim / 2] double, finite; NULL only with rot_dim 0
  *   head_dim    8 .. 512, a multiple of 8; rot_dim a multiple of 16 and
@@ -673,8 +674,11 @@ int kv8_norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_to
  * even). A block that held tokens of the request before keeps the larger of its
  * scale and the new one; if it grows, the codes held are rescaled (exact but
  * for values that fall below e4m3's smallest normal). The first token of a
- * block starts its scale anew. Values that are not finite are stored as 0,
- * values beyond 448 * 2^64 saturate; both are reported as SRH_ERR_RANGE.
+ * block starts its scale anew; giving tokens of a begun block back (kv8_resize)
+ * does not lower its scale again or bring the codes' low bits back, so a rejected
+ * token of far larger values leaves that mark until the block is released.
+ * Values that are not finite are stored as 0, values beyond 448 * 2^64 saturate;
+ * both are reported as SRH_ERR_RANGE.
  * A block being written must belong to one request only (copy a shared, partly
  * filled block first).
  */

@@ -103,11 +103,11 @@ struct Shape {
         return (c / per) * kPart + t * kPitch + ((c % per ^ x) << 4);
     }
     // CTAs per SM: four hide more of a decode step's latencies than fewer with longer
-    // rings do (64 requests of up to 16,384 tokens: 201 us; three 207, two 221)
+    // rings do (64 requests of up to 16,384 tokens: 204 us; three 208, two 229)
     static constexpr int CTAS = DB == 1 ? (RT == 16 ? 4 : 2) : DB == 2 && RT == 16 ? 2 : 1;
     // rounds of chunks, where a CTA's switches between segments overlap other CTAs' tiles
-    // (alone on its SM a CTA is better off with one chunk: 64 requests of 32,768 latent
-    // rows 275 us, 329 in rounds; prompts of 512 tokens of 256-dim heads 646 and 676)
+    // (alone on its SM a CTA is better off with one chunk: 256 requests of up to 32,768
+    // latent rows 629 us, 677 in rounds; prompts of 512 tokens of 256-dim heads 715 and 739)
     static constexpr int ROUNDS = CTAS > 1 ? kRounds : 1;
     // 16 KB slots of the ring (128 tokens x 128 dims); K tile j + 1 is taken before V
     // tile j is given back, so two tiles must fit
@@ -116,15 +116,15 @@ struct Shape {
     // softmax: a thread holds CT columns of one token, CG groups of 4 warps share the
     // columns. (32 columns a thread, for 64-row tiles with two CTAs per SM, need more
     // than the 96 registers there are: a prompt chunk of 128-dim heads took 613 us
-    // with them and took 545 with tiles of 32 rows at the time, now 536.)
+    // with them and took 545 with tiles of 32 rows at the time, now 593.)
     static constexpr int CT = 16;
     static constexpr int CG = RT / CT;
     static constexpr int SOFT = 128 * CG;                  // softmax threads
     static constexpr int THREADS = SOFT + 64;
     // A segment's start and end take about as long as so many tiles, and are counted
-    // as such (4 against none: 16 requests of up to 5 drafted tokens 50 -> 46 us, the
-    // latent batch 160 -> 154; with four CTAs per SM they overlap others' tiles: 1
-    // against 4 in the decode batch, 199 against 205 us).
+    // as such (4 against none: 16 requests of up to 5 drafted tokens 50 -> 47 us, the
+    // latent batch 168 -> 162; with four CTAs per SM they overlap others' tiles: 1
+    // against 4 in the decode batch, 204 against 205 us).
     static constexpr int SWITCH = DB == 1 && RT == 16 ? 1 : 4;
     static constexpr int kOffQ = SLOTS * kSlotBytes;
     static constexpr int kOffP = kOffQ + kQBytes;
@@ -145,7 +145,7 @@ struct Args {
     int4* meta;
     int* ctrl;                                   // [0] chunks handed out, [1] chunks of this call
     uint32_t* err;
-    int n_req, n_rows, heads, kv_heads, group;   // group = heads / kv_heads
+    int n_req, n_rows, kv_heads, group;          // group = query heads / kv_heads
     int bs_log2, n_blocks, max_blocks;
     float scale_log2;
     unsigned long long per_group;                // ceil(2^64 / group); 0 for a group of 1
@@ -561,9 +561,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const int U = (int)total, most = (U + n_grid - 1) / n_grid;
         const int n_cta = U ? (U + most - 1) / most : 0;
         // rounds of smaller chunks only where their switches are few beside their units: from
-        // about 200 per CTA on (the prompt chunk, with 400: 536 us, 557 without; decode of
-        // 256-dim heads with 220: 689 and 699; of 128-dim heads with 245 equal, with 113
-        // 379 and 376, with 85 292 and 284)
+        // about 200 per CTA on (the prompt chunk, with 400: 593 us, 629 without; decode of
+        // 256-dim heads with 220: 683 and 687; of 128-dim heads with 245 710 and 713, with 113
+        // 389 and 386, with 85 301 and 292)
         const int rounds = S::ROUNDS > 1 && U / kRoundsFrom >= n_cta ? S::ROUNDS : 1;
         bs.before[i] = (int)(incl - mine);
         if (i == 0) {
@@ -1445,7 +1445,6 @@ cudaError_t launch_attend(const Cache& c, const kv8_pool& pool, const int32_t* t
     a.err = c.d_err;
     a.n_req = n_req;
     a.n_rows = n_rows;
-    a.heads = n_heads;
     a.kv_heads = c.cfg.n_kv_heads;
     a.group = n_heads / c.cfg.n_kv_heads;
     a.per_group = a.group == 1 ? 0 : ~0ull / (unsigned)a.group + 1;

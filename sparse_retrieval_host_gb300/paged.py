@@ -142,11 +142,10 @@ class PagedKV8:
 
     def _keep(self, stream, *tensors) -> None:
         """Memory of a call's tensors is not handed out again before ``stream`` is through with them."""
-        if stream is not None:
-            s = torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(s)
+        s = torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
 
     def _rows(self, t: torch.Tensor, name: str, heads: Optional[int] = None, dim: Optional[int] = None) -> int:
         """Row stride (elements) of a bf16 [rows][heads][dim] tensor with dense rows."""
@@ -204,7 +203,8 @@ class PagedKV8:
                                   n_new, self._s(stream))
         if rc:
             self._raise(rc, "kv8_resize")
-        self._keep(stream, new_len, cu, pos, slot)
+        if stream is not None:
+            self._keep(stream, new_len, cu, pos, slot)
         return cu, pos, slot
 
     def norm_rope(self, q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None, *, pos=None, inv_freq=None,
@@ -258,7 +258,8 @@ class PagedKV8:
                                          self._s(stream))
             if rc:
                 self._raise(rc, "kv8_norm_rope")
-            self._keep(stream, q, k, pos, inv_freq, q_weight, k_weight, q_slot, k_slot, *outs)
+            if stream is not None:
+                self._keep(stream, q, k, pos, inv_freq, q_weight, k_weight, q_slot, k_slot, *outs)
         return outs[0], outs[1]
 
     def append(self, k: torch.Tensor, v: Optional[torch.Tensor], cu: torch.Tensor, *, layer: int = 0, stream=None) -> None:
@@ -278,7 +279,8 @@ class PagedKV8:
                                       kr, None if v is None else v.data_ptr(), vr, k.shape[0], self._s(stream))
             if rc:
                 self._raise(rc, "kv8_append")
-            self._keep(stream, k, v, cu)
+            if stream is not None:
+                self._keep(stream, k, v, cu)
 
     def attend(self, q: torch.Tensor, cu: torch.Tensor, *, scale: float, window: int = 0, out=None, layer: int = 0,
                stream=None) -> torch.Tensor:
@@ -298,7 +300,8 @@ class PagedKV8:
                                       qr, q.shape[0], q.shape[1], scale, window, out.data_ptr(), orow, self._s(stream))
             if rc:
                 self._raise(rc, "kv8_attend")
-            self._keep(stream, q, cu, out)
+            if stream is not None:
+                self._keep(stream, q, cu, out)
         return out
 
     # ------------------------------------------------------------------ status
