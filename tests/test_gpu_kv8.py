@@ -1324,3 +1324,37 @@ def test_attend_is_as_close_over_long_requests(H, Hk, D, shared, bs, spread, win
     assert c.check_error() == 0
     _check_closely(c, q, cu, out, scale, window)
     c.close()
+
+
+@pytest.mark.parametrize("room", [60, 6000])
+def test_a_captured_resize_with_room(room):
+    """Growth with room for more tokens, shrinking and a refusal, replayed from one graph each with other lengths."""
+    abi = _abi()
+    c = _paged(batch=40, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=2000, max_blocks=300)
+    o = ResizeOracle(40, 16, 2000)
+    rng = np.random.default_rng(room)
+    new = torch.zeros(40, dtype=torch.int32, device="cuda")
+    out = (_i32([0] * 41), torch.full((room,), 9, dtype=torch.int32, device="cuda"),
+           torch.full((room,), 9, dtype=torch.int64, device="cuda"))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.resize(new, room, out=out)
+    for step in range(12):
+        want = np.array(o.len)
+        grow = rng.integers(0, max(2, 2 * room // 40), 40)
+        while grow.sum() > room:
+            grow[rng.integers(40)] = 0
+        want = want + grow if step % 3 != 2 else want // 3
+        if step % 4 == 3:                                   # no such length: refused
+            new.copy_(_i32([-1] + [1] * 39))
+            graph.replay()
+            assert c.check_error() == abi.SRH_ERR_BOUNDS and (out[2] < 0).all() and not out[0].any()
+        new.copy_(_i32(want.tolist()))
+        graph.replay()
+        cu, pos, slot = o.resize(want.tolist())
+        assert c.check_error() == abi.SRH_OK
+        assert out[0].tolist() == cu and out[1][:len(pos)].tolist() == pos and out[2][:len(pos)].tolist() == slot
+        assert (out[2][len(pos):] == -1).all()
+        _same_tables(c, o, 40)
+    c.close()
