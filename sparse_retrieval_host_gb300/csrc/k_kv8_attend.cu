@@ -757,7 +757,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         constexpr uint32_t id_pv = idesc_f32acc(0, 1, 1, 128, S::ON) | (1u << 10);   // both MN-major, B is e5m2
         constexpr uint32_t id_two = idesc_f32acc(0, 1, 1, 128, 2 * RT) | (1u << 10);
         const uint32_t r0 = smem_u32(sm);
-        const uint64_t qd = desc_sw128(smem_u32(sm + S::kOffQ), 16, 1024), pd = desc_parts<S::kPitch>(smem_u32(sm + S::kOffP), S::kPart);
+        const uint64_t qd = desc_sw128(smem_u32(sm + S::kOffQ), 16, 1024);
+        const uint64_t pd = desc_parts<S::kPitch>(smem_u32(sm + S::kOffP), S::kPart);
         uint32_t it = 0, g = 0, segs = 0;                  // blocks taken, token tiles, segments with tiles
         auto got = [&](uint64_t* bar, uint32_t parity) {
             return (bool)__all_sync(0xffffffffu, mbar_wait_abort(bar, parity, abort) > 0);
@@ -885,8 +886,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 for (int d = 0; d < DB; ++d) {
                     uint32_t hi, lo;
                     split4(__uint_as_float(qx[i][d].x << 16) * inv, __uint_as_float(qx[i][d].x & 0xffff0000u) * inv,
-                                 __uint_as_float(qx[i][d].y << 16) * inv, __uint_as_float(qx[i][d].y & 0xffff0000u) * inv,
-                                 &hi, &lo);
+                           __uint_as_float(qx[i][d].y << 16) * inv, __uint_as_float(qx[i][d].y & 0xffff0000u) * inv,
+                           &hi, &lo);
                     unsigned char* q = qsm + d * (N * 128) + (lane & 3) * 4;
                     *reinterpret_cast<uint32_t*>(q + sw128(r, lane >> 2)) = hi;
                     *reinterpret_cast<uint32_t*>(q + sw128(RT + r, lane >> 2)) = lo;

@@ -1153,23 +1153,24 @@ def test_attend_leaves_out_requests_of_impossible_lengths(bad):
 def test_attend_refuses_an_output_that_overlaps_its_queries():
     abi = _abi()
     c, g = _filled([300, 77], 2, 128, 16, False, 161)
-    cu, n = _i32([0, 3, 5]), 5 * 8 * 128
+    w = 6 * 128                                             # a row of 6 heads
+    cu, n = _i32([0, 3, 5]), 5 * w
     flat = _bf16(g, 4 * n)
-    q = flat[n:2 * n].view(5, 8, 128)
-    for at in (n, n + 8, n - 8, n + 1024, 8, 2 * n - 8):    # the same rows, shifted either way by less than they hold
+    q = flat[n:2 * n].view(5, 6, 128)
+    for at in (n, n + 8, n - 8, n + w, 8, 2 * n - 8):       # the same rows, shifted either way by less than they hold
         with pytest.raises(abi.SrhError, match="overlap"):
-            c.attend(q, cu, scale=0.06, out=flat[at:at + n].view(5, 8, 128))
-    wide = flat[:3 * n].view(5, 3, 1024)                    # rows between each other's
-    for qa, oa in ((0, 0), (0, 1000), (1000, 0), (8, 0), (1504, 2040)):
+            c.attend(q, cu, scale=0.06, out=flat[at:at + n].view(5, 6, 128))
+    row = flat[:3 * n].view(5, 3 * w)                       # rows between each other's
+    at = lambda o: row[:, o:o + w].view(5, 6, 128)  # noqa: E731
+    for qa, oa in ((0, 0), (0, w - 8), (w - 8, 0), (8, 0), (w + 352, 2 * w - 8)):
         with pytest.raises(abi.SrhError, match="overlap"):
-            c.attend(wide.view(5, 3072)[:, qa:qa + 1024].view(5, 8, 128), cu, scale=0.06,
-                     out=wide.view(5, 3072)[:, oa:oa + 1024].view(5, 8, 128))
-    want, keep, row = None, q.reshape(5, 1024).clone(), wide.view(5, 3072)
-    for qa, oa in ((0, 1024), (2048, 0), (8, 1032), (2048, 1024)):
-        row[:, qa:qa + 1024] = keep
-        got = c.attend(row[:, qa:qa + 1024].view(5, 8, 128), cu, scale=0.06, out=row[:, oa:oa + 1024].view(5, 8, 128))
+            c.attend(at(qa), cu, scale=0.06, out=at(oa))
+    want, keep = None, q.reshape(5, w).clone()
+    for qa, oa in ((0, w), (2 * w, 0), (8, w + 8), (2 * w, w)):
+        row[:, qa:qa + w] = keep
+        got = c.attend(at(qa), cu, scale=0.06, out=at(oa))
         want = got.clone() if want is None else want
-        assert torch.equal(got, want) and torch.equal(row[:, qa:qa + 1024], keep)
+        assert torch.equal(got, want) and torch.equal(row[:, qa:qa + w], keep)
     assert c.check_error() == 0
     c.close()
 
@@ -1185,7 +1186,7 @@ def test_norm_refuses_outputs_that_overlap_other_rows():
     for kw in (dict(q=q, q_out=at(8, 4)), dict(q=at(256, 4), q_out=at(0, 4)), dict(q=q, k=k, q_out=at(264, 4)),
                dict(q=q, k=k, q_out=at(1024, 4), k_out=at(1280, 2)), dict(q=q, k=k, k_out=at(0, 2)),
                dict(q=q, k=k, q_out=at(768, 4), k_out=at(1272, 2)), dict(k=k, k_out=at(640, 2), k_slot=slot),
-               dict(q=q, k=k, q_out=q, k_out=q[:, :2]), dict(q=q, q_out=row.view(-1)[3072:3072 + 6 * 512].view(6, 4, 128))):
+               dict(q=q, k=k, q_out=q, k_out=q[:, :2]), dict(q=q, q_out=row.view(-1)[2560:2560 + 6 * 512].view(6, 4, 128))):
         with pytest.raises(abi.SrhError, match="overlap|in place"):
             c.norm_rope(**kw)
     wq, wk = c.norm_rope(q, k, q_out=new(4), k_out=new(2))
