@@ -593,7 +593,7 @@ typedef struct {
 } kv8_pool;
 
 /* Makes a handle on the current device (scratch: 30, 30 or 40 MB with
- * head_dim 128, 256 or 512).
+ * head_dim 128, 256 or 512). Waits for the legacy stream; not during a capture.
  * Errors: SRH_ERR_INVALID, SRH_ERR_NOMEM, SRH_ERR_CUDA (kv8_last_error(NULL)). */
 int kv8_create(const kv8_config* cfg, kv8_cache** out);
 
@@ -651,6 +651,7 @@ typedef struct {
  *   head_dim    8 .. 512, a multiple of 8; rot_dim a multiple of 16 and
  *               rot_off of 8, rot_off + rot_dim <= head_dim
  *   eps         >= 0, finite
+ * Squares are summed in fp32: values beyond 2^59 overflow.
  * A slot >= n_slots is skipped and reported as SRH_ERR_BOUNDS. But for out being x,
  * no row of an out overlaps a row of an x or of the other out (rows may lie between
  * each other's, with one stride).
@@ -705,7 +706,9 @@ int kv8_append(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const
  * two e4m3 terms per value (bf16's 8 significant bits; a value below about
  * 2^-13 of its row's largest keeps 2^-21 of that largest), weights as three e5m2
  * terms each: within 2^-9 of the weight, or 2^-27 of the row's largest contribution
- * (weight times V's scale). Codes of tokens below len must
+ * (weight times V's scale). Scores are to lie within 10^30 of 0, and the V scales
+ * that a row sees within 2^96 of each other (tokens of still smaller ones may be
+ * missing in the softmax's sum). Codes of tokens below len must
  * not be NaN codes (kv8_append writes none); what lies behind a request's
  * length, in its last block or elsewhere, is not used.
  */

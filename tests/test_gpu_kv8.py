@@ -1359,3 +1359,18 @@ def test_a_captured_resize_with_room(room):
         assert (out[2][len(pos):] == -1).all()
         _same_tables(c, o, 40)
     c.close()
+
+
+@pytest.mark.parametrize("n_req,H,D,shared", [(4096, 2, 128, False), (700, 64, 512, True), (400, 40, 256, False), (300, 17, 512, False)])
+def test_attend_as_many_requests_as_there_may_be(n_req, H, D, shared):
+    rng = np.random.default_rng(n_req + D)
+    lens = rng.integers(0, 40, n_req)
+    nq = np.minimum(rng.integers(0, 3, n_req), lens)
+    nq[-1] = lens[-1] = 33
+    _attend(lens.tolist(), nq.tolist(), H, 1, D, 16, shared, seed=n_req, pad=2)
+
+
+@pytest.mark.parametrize("D,shared", [(128, True), (256, False), (512, True)])
+def test_attend_a_thousand_heads_on_one(D, shared):
+    _attend([300, 1, 77], [2, 1, 3], 1024, 1, D, 32, shared, seed=D, pad=1)
+    _attend([2000], [1], 1000, 1, D, 64, shared, seed=D + 1, window=150)
