@@ -662,6 +662,19 @@ int kv8_norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_to
                   const double* d_inv_freq, int rot_dim, int rot_off, int style, float eps, srh_stream_t stream);
 
 /*
+ * The same with positions of several axes (time, height, width of image and video
+ * tokens): pair i turns by pos * inv_freq[i] with pos = d_pos[axis[i] * pos_row + token].
+ *   d_pos     [n_axes] rows of [n_tok] int32, pos_row elements apart (>= n_tok, or 0: one row)
+ *   n_axes    1 .. 8
+ *   d_axis    [rot_dim / 2] uint8, each below n_axes; NULL only with rot_dim 0. A pair of
+ *             an axis that is none is not turned, and reported as SRH_ERR_BOUNDS
+ * Everything else as kv8_norm_rope (which is this with one axis).
+ */
+int kv8_norm_rope_axes(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_tok, int head_dim, const int32_t* d_pos,
+                       long long pos_row, int n_axes, const uint8_t* d_axis, const double* d_inv_freq, int rot_dim,
+                       int rot_off, int style, float eps, srh_stream_t stream);
+
+/*
  * Writes the last cu[b+1] - cu[b] tokens of each request (positions
  * len[b] - (cu[b+1] - cu[b]) .. len[b]-1, with d_len the lengths kv8_resize
  * left) into the cache.
@@ -713,6 +726,67 @@ int kv8_append(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const
  * length, in its last block or elsewhere, is not used.
  */
 int kv8_attend(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
+               int n_req, const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,
+               uint16_t* d_out, long long out_row, srh_stream_t stream);
+
+/*
+ * Rows back from the cache: tokens start[b] .. start[b] + (cu[b+1] - cu[b]) - 1 of request b
+ * into rows cu[b] .. cu[b+1]-1 of d_k and d_v, as bf16 (code * scale, rounded once).
+ *   d_start   [n_req] int32
+ *   d_k, d_v  bf16 [n_rows] rows of [n_kv_heads][head_dim], 16-byte aligned, row strides in
+ *             elements, multiples of 8, at least a row; d_v ignored with shared_kv. No row of
+ *             one overlaps a row of the other (rows may lie between each other's, with one stride)
+ * A row whose token lies outside [0, len[b]) or in a block that is none is left as it is, as are
+ * rows of a request whose length is out of range and those that cu names outside [0, n_rows).
+ * A call whose cu descends anywhere writes nothing. All of these: SRH_ERR_BOUNDS.
+ */
+int kv8_read(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_start,
+             const int32_t* d_cu, int n_req, uint16_t* d_k, long long k_row, uint16_t* d_v, long long v_row, int n_rows,
+             srh_stream_t stream);
+
+/*
+ * The same cache in 4 bits: layers of either width share a handle, its table, its lengths and
+ * its error word (kv8_resize and kv8_norm_rope serve both). Grouped heads of 128 or 256 dims
+ * with K and V apart; a handle of shared_kv or of 512-dim heads is refused with SRH_ERR_INVALID.
+ *   codes  uint8 [n_blocks][n_kv_heads][block_tokens][head_dim / 2], 16-byte aligned,
+ *          block_stride bytes from one block to the next: two codes of 0 .. 15 a byte, the
+ *          even dim in the low half
+ *   scale  bf16 [n_blocks][n_kv_heads][block_tokens][2], 16-byte aligned: a scale s and a
+ *          minimum m per (token, head); a value is m + code * s. s is finite and >= 0, m finite.
+ */
+typedef struct {
+    uint8_t* k_codes;
+    uint16_t* k_scale;
+    uint8_t* v_codes;
+    uint16_t* v_scale;
+    long long block_stride;  /* bytes between blocks of codes, a multiple of 16; 0: dense */
+} kv4_pool;
+
+/*
+ * kv8_append in 4 bits. Per (token, head): m = the row's smallest value, s = bf16((largest - m) / 15)
+ * (the division in fp32), code = (x - m) / s in fp32 to the nearest integer, ties to even, held
+ * to 0 .. 15 (0 where s is 0). Tokens held before are not touched. Values that are not finite
+ * count as 0, larger magnitudes than 2^120 as 2^120; both are reported as SRH_ERR_RANGE.
+ * Arguments, and what is left out, as in kv8_append; a call whose cu descends anywhere writes nothing.
+ */
+int kv4_append(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
+               int n_req, const uint16_t* d_k, long long k_row, const uint16_t* d_v, long long v_row, int n_rows,
+               srh_stream_t stream);
+
+/* kv8_read of a 4-bit pool: bf16(m + code * s), the sum in fp32. */
+int kv4_read(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_start,
+             const int32_t* d_cu, int n_req, uint16_t* d_k, long long k_row, uint16_t* d_v, long long v_row, int n_rows,
+             srh_stream_t stream);
+
+/*
+ * kv8_attend over a 4-bit pool; arguments, and what is left out or refused, as there.
+ * Precision: fp32 scores, statistics and sums. Queries enter the products as fp16 (a value below
+ * about 2^-28 of its row's largest loses bits), codes exactly. A weight times V's scale is
+ * rounded to fp16: within 2^-12 of it, or 2^-35 of the row's largest. V's scales are taken as at
+ * least 2^-64; those that a row sees are to lie within 2^96 of each other, scores within 10^30 of
+ * 0, values within 2^60.
+ */
+int kv4_attend(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
                int n_req, const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,
                uint16_t* d_out, long long out_row, srh_stream_t stream);
 

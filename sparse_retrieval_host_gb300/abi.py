@@ -89,6 +89,11 @@ class Kv8Pool(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("k_codes", "k_scale", "v_codes", "v_scale")]
 
 
+class Kv4Pool(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("k_codes", "k_scale", "v_codes", "v_scale")]
+    _fields_ += [("block_stride", ctypes.c_longlong)]
+
+
 class Kv8Heads(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("x_row", ctypes.c_longlong), ("out", ctypes.c_void_p),
                 ("out_row", ctypes.c_longlong), ("weight", ctypes.c_void_p), ("n_heads", ctypes.c_int),
@@ -144,8 +149,14 @@ SIGNATURES = [
     ("kv8_resize", _i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp]),
     ("kv8_norm_rope", _i, [_vp, ctypes.POINTER(Kv8Heads), ctypes.POINTER(Kv8Heads), _i, _i, _vp, _vp, _i, _i, _i, _f,
                            _vp]),
+    ("kv8_norm_rope_axes", _i, [_vp, ctypes.POINTER(Kv8Heads), ctypes.POINTER(Kv8Heads), _i, _i, _vp, _ll, _i, _vp, _vp,
+                                _i, _i, _i, _f, _vp]),
     ("kv8_append", _i, [_vp, ctypes.POINTER(Kv8Pool), _vp, _vp, _vp, _i, _vp, _ll, _vp, _ll, _i, _vp]),
     ("kv8_attend", _i, [_vp, ctypes.POINTER(Kv8Pool), _vp, _vp, _vp, _i, _vp, _ll, _i, _i, _f, _i, _vp, _ll, _vp]),
+    ("kv8_read", _i, [_vp, ctypes.POINTER(Kv8Pool), _vp, _vp, _vp, _vp, _i, _vp, _ll, _vp, _ll, _i, _vp]),
+    ("kv4_append", _i, [_vp, ctypes.POINTER(Kv4Pool), _vp, _vp, _vp, _i, _vp, _ll, _vp, _ll, _i, _vp]),
+    ("kv4_read", _i, [_vp, ctypes.POINTER(Kv4Pool), _vp, _vp, _vp, _vp, _i, _vp, _ll, _vp, _ll, _i, _vp]),
+    ("kv4_attend", _i, [_vp, ctypes.POINTER(Kv4Pool), _vp, _vp, _vp, _i, _vp, _ll, _i, _i, _f, _i, _vp, _ll, _vp]),
     ("kv8_check_error", _i, [_vp]),
     ("kv8_last_error", ctypes.c_char_p, [_vp]),
     ("srh_error_string", ctypes.c_char_p, [_i]),

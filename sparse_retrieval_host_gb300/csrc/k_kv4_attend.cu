@@ -1,0 +1,587 @@
+// Attention over the paged 4-bit cache (kv4_attend), for few query rows per KV head
+// (decode steps, drafted tokens).
+//
+//   o_r = sum_t w_rt V_t / sum_t w_rt,  w_rt = exp(scale <q_r, K_t>),
+//   K_t = km_t + ks_t n_t, V_t = vm_t + vs_t m_t, codes n, m in 0 .. 15
+//
+// A warp takes 16 tokens at a time, and their codes go from memory into the fragments of
+// mma.sync m16n8k16 (fp16) without a detour: tokens are the M dimension of S^T = n q^T, head
+// dims that of O^T = m^T p. (tcgen05 wants its operands unpacked in shared memory, whose
+// bandwidth, not HBM's, would bound a call of few rows: the products of 8 rows are a
+// sixth of what these instructions can do.)
+//
+// Codes need no conversion: a code in the low bits of an fp16 is the subnormal n 2^-24, and
+// tensor cores take subnormals as they are. (w & 0x000f000f) is thus two operands for one
+// instruction; (w & 0x00f000f0) is two more, 16 times as large, which the queries make up for
+// in the first product (dims 1, 3, 5, 7 of each 8 enter 16 times smaller) and the outputs' scale
+// in the second. Which dims meet in a k step does not matter as long as both operands agree.
+//
+// Scores: ks_t <q, n_t> + km_t sum(q), in fp32. Weights carry V's scale in the exponent,
+// u = s + log2 vs, p = 2^(u - ref) in fp16, and the minimum enters around the middle of the codes,
+//   O = sum p (m - 8) + sum (p / vs) (vm + 8 vs),
+// the second sum and the softmax's in fp32 by the threads: what p's rounding does to a token is
+// then relative to V's distance from the middle of its range (around vm it would be relative to
+// the whole range, and the same for all tokens where all weigh the same). The -8 is taken off by
+// sum p, of the rounded p, a row of ones in the second product.
+//
+// Work: a row tile is RT of the (token, head) rows that share a KV head of a request. Units are
+// (request, KV head, row tile, 128 tokens), counted on the device from the lengths and cut into
+// equal chunks, one per CTA; the CTA's warps take 16 tokens of each unit. The last CTA to arrive
+// of those that share an item adds its parts, in chunk order: results repeat bit for bit.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv8_internal.cuh"
+
+namespace srh {
+namespace kv8 {
+namespace {
+
+constexpr int kTile = 128;               // tokens per unit
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr float kLow = -1e30f;           // reference of a row that has seen no token
+constexpr float kHead = 10.f;            // log2 of the weight that a new reference gives a row's maximum
+constexpr float kRoom = 15.5f;           // a row's reference moves when a weight would pass 2^15.5
+constexpr float kLeastScale = 5.421010862427522e-20f;   // 2^-64
+constexpr int kMaxUnits = 1 << 30;
+
+// DB: head_dim / 128. NT: row tiles of 8 columns.
+template <int DB_, int NT_>
+struct Shape {
+    static constexpr int DB = DB_, NT = NT_, RT = 8 * NT, D = 128 * DB;
+    static constexpr int CTAS = DB * NT == 1 ? 2 : 1;
+    static constexpr int kPitch = D + 8;                       // floats of a row of the warps' outputs
+    static constexpr int kOutBytes = kWarps * RT * kPitch * 4;
+    static constexpr int kStatBytes = kWarps * RT * 8;         // reference and sum
+};
+
+struct Args {
+    const uint16_t* q;
+    uint16_t* out;
+    long long q_row, out_row, block_stride;
+    const int32_t* cu;
+    const int32_t* len;
+    const int32_t* table;
+    const uint8_t* kc;
+    const uint8_t* vc;
+    const uint32_t* ks;                          // (scale, minimum), bf16 each
+    const uint32_t* vs;
+    float* part_o;
+    float* part_ml;
+    int* arrived;
+    uint32_t* err;
+    int n_req, n_rows, kv_heads, group;          // group = query heads / kv_heads
+    int bs_log2, n_blocks, max_blocks;
+    float scale_log2;
+    int window;                                  // 0: none
+};
+
+struct Request {
+    int q0, nq, len;
+    int nrt;           // row tiles
+    int P;             // units of a row tile: what the longest takes
+};
+
+__device__ __forceinline__ int first_tile(const Args& a, int p_lo) {
+    return a.window ? max(0, p_lo - a.window + 1) / kTile : 0;
+}
+
+template <int RT>
+__device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
+    Request r;
+    const int c0 = a.cu[b], c1 = a.cu[b + 1], n = a.len[b], most = a.max_blocks << a.bs_log2;
+    r.q0 = min(max(c0, 0), a.n_rows);
+    r.nq = min(max(c1, r.q0), a.n_rows) - r.q0;               // (rows outside q are not there)
+    r.len = n;
+    if (c0 != r.q0 || c1 != r.q0 + r.nq) *bad = true;
+    if (n < 0 || n > most) {                                  // no such request
+        *bad = true;
+        r.nq = r.len = 0;
+    }
+    r.nrt = (r.nq * a.group + RT - 1) / RT;
+    const int all = max(1, (r.len + kTile - 1) / kTile);
+    r.P = r.nrt == 0 ? 0 : all;
+    if (r.nrt == 1) r.P = max(1, all - first_tile(a, r.len - r.nq));
+    else if (r.nrt > 1 && a.window) r.P = (int)min((long long)all, ((long long)a.window + RT / a.group + 1) / kTile + 2);
+    return r;
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    uint32_t r;
+    memcpy(&r, &h, 4);
+    return r;
+}
+// D += A B: A 16 x 16 (rows by lane / 4), B 16 x 8 (columns by lane / 4), fp16, fp32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of fp16, two to a lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <typename S>
+__global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid_constant__ Args a) {
+    constexpr int DB = S::DB, NT = S::NT, RT = S::RT, D = S::D;
+    extern __shared__ __align__(16) unsigned char sm[];
+    float* const outs = reinterpret_cast<float*>(sm);                       // [warp][row][kPitch]
+    float2* const stats = reinterpret_cast<float2*>(sm + S::kOutBytes);     // [warp][row]: reference, sum
+    int* const first = reinterpret_cast<int*>(sm + S::kOutBytes + S::kStatBytes);   // units before each request
+    __shared__ long long warp_sums[33];
+    __shared__ int last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+
+    // ------------------------------------------------------------ the units
+    bool bad = false, stop = false;
+    long long U64 = 0;
+    for (int base = 0; base < a.n_req; base += kThreads) {
+        const int b = base + tid;
+        long long mine = 0, total;
+        if (b < a.n_req) {
+            const Request r = request<RT>(a, b, &bad);
+            mine = (long long)r.nrt * r.P * a.kv_heads;
+            if (a.cu[b + 1] < a.cu[b]) stop = true;           // requests may share rows
+        }
+        const long long incl = block_scan(mine, warp_sums, &total);
+        if (b < a.n_req) first[b] = (int)(U64 + incl - mine);
+        U64 += total;
+    }
+    stop = __syncthreads_or(stop) || U64 > kMaxUnits;
+    if (blockIdx.x == 0 && (bad || (stop && tid == 0))) atomicOr(a.err, kErrBounds);
+    if (stop) return;
+    const int U = (int)U64, n_grid = gridDim.x, most = (U + n_grid - 1) / n_grid;
+    const int n_cta = U ? (U + most - 1) / most : 0;          // as few as keep the largest share the same
+    const int cta = blockIdx.x;
+    if (cta >= n_cta) return;
+    const int base = U / n_cta, rem = U - base * n_cta;
+    auto chunk_of = [&](int u) { return u < rem * (base + 1) ? u / (base + 1) : rem + (u - rem * (base + 1)) / base; };
+    const int bsz = 1 << a.bs_log2;
+
+    int u = cta * base + min(cta, rem);
+    const int u1 = u + base + (cta < rem);
+    while (u < u1) {
+        // -------------------------------------------------------- the segment
+        const int b = last_not_above(first, a.n_req, u);
+        const Request r = request<RT>(a, b, &bad);
+        const int in = u - first[b], item = in / r.P, at = in - item * r.P, n = min(r.P - at, u1 - u);
+        const int h = item / r.nrt, row0 = (item - h * r.nrt) * RT, nr = min(RT, r.nq * a.group - row0);
+        const int u_item = u - at, v0 = chunk_of(u_item), parts = chunk_of(u_item + r.P - 1) - v0 + 1;
+        u += n;
+        const int p0 = r.len - r.nq;                          // position of the request's first row
+        const int p_lo = p0 + row0 / a.group, p_hi = p0 + (row0 + nr - 1) / a.group;
+        const int t_first = first_tile(a, p_lo);
+        const int see_lo = a.window ? p_lo - a.window + 1 : 0;
+
+        // queries as B fragments: lane (g, c) holds dims 32 c .. of row g, per 8 dims two k steps
+        uint32_t q[NT][DB][16];
+        float qf[NT][2], qs[NT][2];                           // of rows 2 c and 2 c + 1: factor, sum
+        int pos[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int row = row0 + t * 8 + g, tok = row / a.group;
+            const bool on = t * 8 + g < nr;
+            const uint16_t* x = a.q + (size_t)(r.q0 + (on ? tok : 0)) * a.q_row +
+                                (size_t)(h * a.group + (on ? row - tok * a.group : 0)) * D;
+            uint4 w[DB][4];
+            uint32_t m = 0;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[d][i] = on ? __ldg(reinterpret_cast<const uint4*>(x + d * 128 + c * 32 + i * 8)) : make_uint4(0, 0, 0, 0);
+                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[d][i].x & 0x7fff7fffu, w[d][i].y & 0x7fff7fffu),
+                                             __vmaxu2(w[d][i].z & 0x7fff7fffu, w[d][i].w & 0x7fff7fffu)));
+                }
+            m = max(m & 0xffffu, m >> 16);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            // to a largest magnitude in [2^14, 2^15)
+            const int e = min(max((int)(m >> 7) - 127 - 14, -120), 120);
+            const float inv = __uint_as_float((uint32_t)(127 - e) << 23), inv16 = inv * 0.0625f;
+            float sum = 0.f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // dims 0 .. 7: pairs (k, k + 4) as the codes of a word lie
+                    const uint32_t v[4] = {w[d][i].x, w[d][i].y, w[d][i].z, w[d][i].w};
+                    q[t][d][4 * i] = half2_bits(bf_lo(v[0]) * inv, bf_lo(v[2]) * inv);
+                    q[t][d][4 * i + 1] = half2_bits(bf_hi(v[0]) * inv16, bf_hi(v[2]) * inv16);
+                    q[t][d][4 * i + 2] = half2_bits(bf_lo(v[1]) * inv, bf_lo(v[3]) * inv);
+                    q[t][d][4 * i + 3] = half2_bits(bf_hi(v[1]) * inv16, bf_hi(v[3]) * inv16);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum += bf_lo(v[k]) * inv + bf_hi(v[k]) * inv;
+                }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            // a row that is not finite has no result: NaN
+            const float f = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int from = (2 * c + i) * 4;
+                const float fr = __shfl_sync(0xffffffffu, f, from);
+                qf[t][i] = fr * 16777216.f;                   // codes come as n 2^-24
+                qs[t][i] = fr * __shfl_sync(0xffffffffu, sum, from);
+                const int k = t * 8 + 2 * c + i;
+                pos[t][i] = k < nr ? p0 + (row0 + k) / a.group : -1;
+            }
+        }
+
+        float o[NT][DB * 8][4], ones[NT][4], l[NT][2], mid[NT][2], ref[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int i = 0; i < DB * 8; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ones[t][k] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                l[t][k] = mid[t][k] = 0.f;
+                ref[t][k] = kLow;
+            }
+        }
+
+        for (int i = 0; i < n; ++i) {
+            const int t0 = (t_first + at + i) * kTile + warp * 16;
+            if (t0 > p_hi || t0 + 16 <= see_lo) continue;
+            const int id = __ldg(a.table + (size_t)b * a.max_blocks + (t0 >> a.bs_log2));
+            if (id < 0 || id >= a.n_blocks) {                 // a block that is none reads as absent
+                bad = true;
+                continue;
+            }
+            const size_t tok0 = (size_t)h << a.bs_log2 | (t0 & (bsz - 1));
+            const uint8_t* kp = a.kc + (size_t)id * a.block_stride + tok0 * (D / 2);
+            const uint8_t* vp = a.vc + (size_t)id * a.block_stride + tok0 * (D / 2);
+            const size_t sc = ((size_t)id * a.kv_heads << a.bs_log2) + tok0;
+            uint4 k[2][DB];
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                k[0][d] = __ldg(reinterpret_cast<const uint4*>(kp + g * (D / 2) + d * 64 + c * 16));
+                k[1][d] = __ldg(reinterpret_cast<const uint4*>(kp + (g + 8) * (D / 2) + d * 64 + c * 16));
+            }
+            uint32_t ksm[2] = {__ldg(a.ks + sc + g), __ldg(a.ks + sc + g + 8)};
+            uint32_t vsm[2] = {__ldg(a.vs + sc + g), __ldg(a.vs + sc + g + 8)};
+            // V: tokens 2 c, 2 c + 1, and 8 more on, dims 16 DB g ..
+            uint32_t v[4][2 * DB];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint8_t* p = vp + (2 * c + (j & 1) + 8 * (j >> 1)) * (D / 2) + g * 8 * DB;
+                if (DB == 1) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+                    v[j][0] = x.x;
+                    v[j][1] = x.y;
+                } else {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+                    v[j][0] = x.x;
+                    v[j][1] = x.y;
+                    v[j][2 * DB - 2] = x.z;
+                    v[j][2 * DB - 1] = x.w;
+                }
+            }
+
+            // scores
+            float s[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[t][j] = 0.f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const uint32_t w0[4] = {k[0][d].x, k[0][d].y, k[0][d].z, k[0][d].w};
+                const uint32_t w1[4] = {k[1][d].x, k[1][d].y, k[1][d].z, k[1][d].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        mma(s[t], w0[j] & 0x000f000fu, w1[j] & 0x000f000fu, w0[j] & 0x00f000f0u, w1[j] & 0x00f000f0u,
+                            q[t][d][4 * j], q[t][d][4 * j + 1]);
+                    const uint32_t x0 = w0[j] >> 8, x1 = w1[j] >> 8;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        mma(s[t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
+                            q[t][d][4 * j + 2], q[t][d][4 * j + 3]);
+                }
+            }
+            // exponents with V's scale, relative to the rows' references
+            float kss[2], km[2], lv[2], iv[2], cm[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool there = t0 + g + 8 * j < r.len;     // (what lies behind the request may be anything)
+                kss[j] = bf_lo(ksm[j]);
+                km[j] = bf_hi(ksm[j]);
+                const float vsc = fmaxf(bf_lo(vsm[j]), kLeastScale);
+                lv[j] = lg2(vsc);
+                iv[j] = there ? __fdividef(1.f, vsc) : 0.f;
+                cm[j] = there ? fmaf(8.f, vsc, bf_hi(vsm[j])) : 0.f;
+            }
+            const bool edge = t0 + 15 > p_lo || t0 <= p_hi - a.window;
+            float y[NT][4], top = kLow;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int col = j & 1, tk = j >> 1;
+                    float x = fmaf(s[t][j] * qf[t][col], kss[tk], fmaf(km[tk], qs[t][col], lv[tk]));
+                    if (a.window ? edge : t0 + 15 > p_lo) {
+                        const int tt = t0 + g + 8 * tk, p = pos[t][col];
+                        if (tt > p || (a.window && tt <= p - a.window)) x = -INFINITY;
+                    }
+                    y[t][j] = x;
+                    top = fmaxf(top, x - ref[t][col]);
+                }
+            if (__any_sync(0xffffffffu, top > kRoom)) {
+                // new references: the maximum of the 16 tokens per row
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float f[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float m = fmaxf(y[t][j], y[t][j + 2]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                        f[j] = 1.f;
+                        if (m - ref[t][j] > kHead) {          // every row that grew, while at it
+                            const float now = m - kHead;
+                            f[j] = ex2(ref[t][j] - now);
+                            ref[t][j] = now;
+                        }
+                        l[t][j] *= f[j];
+                        mid[t][j] *= f[j];
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) ones[t][x] *= f[x & 1];
+#pragma unroll
+                    for (int m = 0; m < DB * 8; ++m)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[t][m][x] *= f[x & 1];
+                }
+            }
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = ex2(y[t][j] - ref[t][j & 1]);
+                    const float x = w[j] * iv[j >> 1];
+                    l[t][j & 1] += x;
+                    mid[t][j & 1] = fmaf(x, cm[j >> 1], mid[t][j & 1]);
+                }
+                p[t][0] = transposed(half2_bits(w[0], w[1]));
+                p[t][1] = transposed(half2_bits(w[2], w[3]));
+                constexpr uint32_t one = 0x3c003c00u;
+                mma(ones[t], one, one, one, one, p[t][0], p[t][1]);
+            }
+            // outputs
+#pragma unroll
+            for (int j = 0; j < 2 * DB; ++j) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t x0 = __byte_perm(v[0][j], v[1][j], half ? 0x7632 : 0x5410);
+                    uint32_t x1 = __byte_perm(v[2][j], v[3][j], half ? 0x7632 : 0x5410);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            mma(o[t][j * 4 + half * 2 + m], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
+                                x1 & 0x00f000f0u, p[t][0], p[t][1]);
+                        x0 >>= 8;
+                        x1 >>= 8;
+                    }
+                }
+            }
+        }
+
+        // -------------------------------------------------------- the warps' sums together
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], x);
+                    mid[t][j] += __shfl_xor_sync(0xffffffffu, mid[t][j], x);
+                }
+                const int row = t * 8 + 2 * c + j;
+                if (g == 0) stats[warp * RT + row] = make_float2(ref[t][j], l[t][j]);
+                float* dst = outs + (warp * RT + row) * S::kPitch;
+#pragma unroll
+                for (int m = 0; m < DB * 8; ++m) {
+                    // o[m][j]: an even dim, n 2^-24; o[m][j + 2]: the next one, 16 times that
+                    const float add = fmaf(-8.f, ones[t][j], mid[t][j]);
+                    *reinterpret_cast<float2*>(dst + (m * 8 + g) * 2) =
+                        make_float2(fmaf(o[t][m][j], 16777216.f, add), fmaf(o[t][m][j + 2], 1048576.f, add));
+                }
+            }
+        }
+        __syncthreads();
+        const int slot = 2 * cta + (at == 0);                 // of a part: its chunk's last item, or its first
+        // two dims of a row per thread and turn
+        for (int x = tid; x < nr * (D / 2); x += kThreads) {
+            const int row = x / (D / 2), d = (x - row * (D / 2)) * 2;
+            const int in_g = d % (16 * DB), from = ((in_g >> 1) * 8 + d / (16 * DB)) * 2;
+            float m = kLow;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                if (stats[w * RT + row].y != 0.f) m = fmaxf(m, stats[w * RT + row].x);
+            float sum = 0.f;
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 st = stats[w * RT + row];
+                if (st.y == 0.f) continue;
+                const float f = ex2(st.x - m);
+                const float2 v = *reinterpret_cast<const float2*>(outs + (w * RT + row) * S::kPitch + from);
+                sum = fmaf(f, st.y, sum);
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+            }
+            if (parts == 1) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int rr = row0 + row, tok = rr / a.group;
+                const __nv_bfloat162 v = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)(r.q0 + tok) * a.out_row +
+                                                   (size_t)(h * a.group + rr - tok * a.group) * D + d) = v;
+            } else {
+                *reinterpret_cast<float2*>(a.part_o + ((size_t)slot * RT + row) * D + d) = acc;
+                if (d == 0) reinterpret_cast<float2*>(a.part_ml)[(size_t)slot * RT + row] = make_float2(m, sum);
+            }
+        }
+        if (parts > 1) {
+            // the last part to be written joins them all
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                last = atomicAdd(a.arrived + v0, 1) == parts - 1;
+                if (last) a.arrived[v0] = 0;                  // for the next call
+            }
+            __syncthreads();
+            if (last) {
+                __threadfence();
+                auto slot_of = [&](int i) { return (size_t)(2 * (v0 + i) + (i == 0)); };
+                for (int x = tid; x < nr * (D / 4); x += kThreads) {
+                    const int row = x / (D / 4), d = (x - row * (D / 4)) * 4;
+                    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+                    float m = kLow, sum = 0.f;
+                    for (int i = 0; i < parts; ++i) {
+                        const float2 st = __ldcg(&ml[slot_of(i) * RT + row]);
+                        if (st.y != 0.f) m = fmaxf(m, st.x);
+                    }
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int i = 0; i < parts; ++i) {
+                        const float2 st = __ldcg(&ml[slot_of(i) * RT + row]);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * RT + row) * D + d));
+                        if (st.y == 0.f) continue;            // a part with no weight does not count
+                        const float f = ex2(st.x - m);
+                        sum = fmaf(f, st.y, sum);
+                        acc.x = fmaf(f, v.x, acc.x);
+                        acc.y = fmaf(f, v.y, acc.y);
+                        acc.z = fmaf(f, v.z, acc.z);
+                        acc.w = fmaf(f, v.w, acc.w);
+                    }
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    const int rr = row0 + row, tok = rr / a.group;
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                    uint2 w;
+                    memcpy(&w.x, &lo, 4);
+                    memcpy(&w.y, &hi, 4);
+                    *reinterpret_cast<uint2*>(a.out + (size_t)(r.q0 + tok) * a.out_row +
+                                              (size_t)(h * a.group + rr - tok * a.group) * D + d) = w;
+                }
+            }
+        }
+        __syncthreads();                                      // the next segment's outputs take this one's place
+    }
+    if (bad) atomicOr(a.err, kErrBounds);
+}
+
+template <typename S>
+size_t smem_bytes(int n_req) {
+    return S::kOutBytes + S::kStatBytes + (size_t)n_req * sizeof(int);
+}
+
+template <typename S>
+cudaError_t run(const Cache& c, const Args& a, cudaStream_t st) {
+    const int grid = S::CTAS * c.sm_count;
+    if ((size_t)grid * 2 * S::RT * S::D > c.part_o_floats || (size_t)grid * 4 * S::RT > c.part_ml_floats || (size_t)grid > c.arrived_n)
+        return cudaErrorInvalidValue;
+    attend4_kernel<S><<<grid, kThreads, smem_bytes<S>(a.n_req), st>>>(a);
+    return cudaGetLastError();
+}
+template <typename S>
+cudaError_t set_one() {
+    return cudaFuncSetAttribute(attend4_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<S>(kMaxBatch));
+}
+
+}  // namespace
+
+size_t attend4_arrivals(int sm_count) { return (size_t)sm_count * 2; }
+
+cudaError_t set_attend4_attrs() {
+    cudaError_t e = set_one<Shape<1, 1>>();
+    if (e == cudaSuccess) e = set_one<Shape<1, 2>>();
+    if (e == cudaSuccess) e = set_one<Shape<2, 1>>();
+    return e;
+}
+
+cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* table, const int32_t* len,
+                           const int32_t* cu, int n_req, const uint16_t* q, long long q_row, int n_rows, int n_heads,
+                           float scale, int window, uint16_t* out, long long out_row, cudaStream_t st) {
+    Args a{};
+    a.q = q;
+    a.out = out;
+    a.q_row = q_row;
+    a.out_row = out_row;
+    a.block_stride = pool.block_stride;
+    a.cu = cu;
+    a.len = len;
+    a.table = table;
+    a.kc = pool.k_codes;
+    a.vc = pool.v_codes;
+    a.ks = reinterpret_cast<const uint32_t*>(pool.k_scale);
+    a.vs = reinterpret_cast<const uint32_t*>(pool.v_scale);
+    a.part_o = c.d_part_o;
+    a.part_ml = c.d_part_ml;
+    a.arrived = c.d_arrived;
+    a.err = c.d_err;
+    a.n_req = n_req;
+    a.n_rows = n_rows;
+    a.kv_heads = c.cfg.n_kv_heads;
+    a.group = n_heads / c.cfg.n_kv_heads;
+    a.bs_log2 = c.bs_log2;
+    a.n_blocks = c.cfg.n_blocks;
+    a.max_blocks = c.cfg.max_blocks;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.window = window < (1 << 30) ? window : 0;            // (a request is at most 2^30 tokens long)
+    // rows of an average request's KV head
+    const long long rows = (long long)a.group * ((n_rows + n_req - 1) / n_req);
+    if (c.cfg.head_dim == 256) return run<Shape<2, 1>>(c, a, st);
+    return rows <= 8 ? run<Shape<1, 1>>(c, a, st) : run<Shape<1, 2>>(c, a, st);
+}
+
+}  // namespace kv8
+}  // namespace srh

@@ -1,5 +1,5 @@
 // RMS norm of every query and key head with the position rotation in the same
-// pass (kv8_norm_rope).
+// pass (kv8_norm_rope; kv8_norm_rope_axes with a position per axis).
 //
 //   y = x / sqrt(mean(x^2) + eps) * w,  then for each rotated pair (a, b)
 //   a' = a cos t - b sin t,  b' = a sin t + b cos t,  t = pos * f_i.
@@ -25,6 +25,10 @@
 // the fraction's own 2^-64 is less), and 2^-26 of a turn as the fraction becomes
 // fp32: 1e-7 rad at position 10^6 with f_i = 1, where an fp32 angle is off by up to
 // 0.03.
+//
+// With several axes a token has up to 8 positions, a lane of its warp each, and a
+// pair of dims takes the one of its axis by a shuffle while the angles are made: the
+// rest of the kernel does not know of it.
 #include <cuda_bf16.h>
 
 #include "kv8_internal.cuh"
@@ -39,6 +43,9 @@ struct Args {
     kv8_heads part[2];
     const int32_t* pos;
     const double* inv_freq;
+    const uint8_t* axis;   // of each pair; NULL: one position per token
+    long long pos_row;
+    int n_axes;
     uint32_t* err;
     int n_tok;
     int vecs;          // head_dim / 8
@@ -96,10 +103,11 @@ __device__ __forceinline__ void load_w(const float* w, int e, float (&v)[8]) {
 
 // LPH lanes per head, VPL vectors of 8 values per lane; a group of lanes loads
 // HPG heads before it uses the first.
-template <int LPH, int VPL, int HPG, int CTAS>
+template <int LPH, int VPL, int HPG, int CTAS, bool AXES>
 __global__ void __launch_bounds__(kThreads, CTAS) norm_rope_kernel(const __grid_constant__ Args a) {
     constexpr int kWarps = kThreads / 32, G = 32 / LPH;    // heads of a warp at a time
     __shared__ unsigned long long step[256];               // turns per position, as 64-bit fractions
+    __shared__ uint8_t axis[256];
     __shared__ alignas(16) float cosv[kWarps][256], sinv[kWarps][256];
     const int tid = threadIdx.x, warp = tid >> 5;
     const int half = a.rot_dim >> 1;
@@ -107,6 +115,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) norm_rope_kernel(const __grid_
         double turn = a.inv_freq[i] * 0.15915494309189533576888;   // 1 / (2 pi)
         turn -= floor(turn);
         step[i] = (unsigned long long)(turn * 18446744073709551616.0);
+        if (AXES) {
+            int of = a.axis[i];
+            if (of >= a.n_axes) {       // no such axis: the pair stays as it is
+                if (blockIdx.x == 0) atomicOr(a.err, kErrBounds);
+                of = 0;
+                step[i] = 0;
+            }
+            axis[i] = (uint8_t)of;
+        }
     }
     __syncthreads();
     const int lane = tid % LPH, group = (tid & 31) / LPH;
@@ -123,16 +140,24 @@ __global__ void __launch_bounds__(kThreads, CTAS) norm_rope_kernel(const __grid_
     if (at0 >= at1) return;             // whole warps
     int t = (int)(at0 / heads), w0 = (int)(at0 - (long long)t * heads);
     int left = (int)(at1 - at0);
-    int pos = half ? a.pos[t] : 0;
+    // a token's position (AXES: lane i holds the one of axis i)
+    auto position = [&](int of) {
+        if (!AXES) return half ? a.pos[of] : 0;
+        return half && (tid & 31) < a.n_axes ? a.pos[(tid & 31) * a.pos_row + of] : 0;
+    };
+    int pos = position(t);
 #pragma unroll 1
     for (; left > 0; ++t, w0 = 0) {
         const int w1 = min(heads, w0 + left);
         left -= w1 - w0;
         const int here = pos;
-        if (half && left > 0) pos = a.pos[t + 1];
+        if (left > 0) pos = position(t + 1);
         __syncwarp();                   // the last token's angles have been read
-        for (int i = tid & 31; i < half; i += 32) {
-            const unsigned long long at = (unsigned long long)(long long)here * step[i];
+        for (int i0 = 0; i0 < half; i0 += 32) {
+            const int i = i0 + (tid & 31);
+            const int mine = AXES ? __shfl_sync(0xffffffffu, here, i < half ? axis[i] : 0) : here;
+            if (i >= half) break;
+            const unsigned long long at = (unsigned long long)(long long)mine * step[i];
             // the top 32 bits as a signed fraction of a turn, in units of half a turn
             float s, c;
             sincospif((float)(int)(uint32_t)(at >> 32) * 4.656612873077392578125e-10f, &s, &c);
@@ -259,16 +284,27 @@ __global__ void __launch_bounds__(kThreads, CTAS) norm_rope_kernel(const __grid_
     }
 }
 
+template <bool AXES>
+void launch_kernel(int lph, unsigned grid, const Args& a, cudaStream_t st) {
+    if (lph == 8) norm_rope_kernel<8, 1, 3, 8, AXES><<<grid, kThreads, 0, st>>>(a);
+    else if (lph == 16) norm_rope_kernel<16, 1, 3, 8, AXES><<<grid, kThreads, 0, st>>>(a);
+    else if (a.vecs <= 32) norm_rope_kernel<32, 1, 3, 8, AXES><<<grid, kThreads, 0, st>>>(a);
+    else norm_rope_kernel<32, 2, 2, 5, AXES><<<grid, kThreads, 0, st>>>(a);
+}
+
 }  // namespace
 
 cudaError_t launch_norm_rope(const Cache& c, const kv8_heads& q, const kv8_heads& k, int n_tok, int head_dim,
-                             const int32_t* pos, const double* inv_freq, int rot_dim, int rot_off, int style,
-                             float eps, cudaStream_t st) {
+                             const int32_t* pos, long long pos_row, int n_axes, const uint8_t* axis,
+                             const double* inv_freq, int rot_dim, int rot_off, int style, float eps, cudaStream_t st) {
     Args a{};
     a.part[0] = q;
     a.part[1] = k;
     a.pos = pos;
     a.inv_freq = inv_freq;
+    a.axis = axis;
+    a.pos_row = pos_row;
+    a.n_axes = n_axes;
     a.err = c.d_err;
     a.n_tok = n_tok;
     a.vecs = head_dim / 8;
@@ -291,10 +327,8 @@ cudaError_t launch_norm_rope(const Cache& c, const kv8_heads& q, const kv8_heads
     // than from loads of one warp (one prompt chunk of 6,143 tokens x 40 heads x 128:
     // 28.0 us with 3, 28.7 with 4, 28.2 with 2, 32 with 1; 6 CTAs with 4 28.2); two
     // vectors a lane need more registers, and a decode step is latency-bound either way
-    if (lph == 8) norm_rope_kernel<8, 1, 3, 8><<<grid, kThreads, 0, st>>>(a);
-    else if (lph == 16) norm_rope_kernel<16, 1, 3, 8><<<grid, kThreads, 0, st>>>(a);
-    else if (a.vecs <= 32) norm_rope_kernel<32, 1, 3, 8><<<grid, kThreads, 0, st>>>(a);
-    else norm_rope_kernel<32, 2, 2, 5><<<grid, kThreads, 0, st>>>(a);
+    if (axis) launch_kernel<true>(lph, grid, a, st);
+    else launch_kernel<false>(lph, grid, a, st);
     return cudaGetLastError();
 }
 

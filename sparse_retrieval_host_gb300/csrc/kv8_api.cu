@@ -99,6 +99,21 @@ const char* pool_error(const kv8_cache* c, const kv8_pool* p) {
     return nullptr;
 }
 
+// A 4-bit pool of this handle; null where it is sound.
+const char* pool4_error(const kv8_cache* c, const kv4_pool* p) {
+    if (c->cfg.shared_kv || c->cfg.head_dim > 256) return "4 bits are for 128- and 256-dim heads with K and V apart";
+    if (!p || !p->k_codes || !p->k_scale || !p->v_codes || !p->v_scale) return "pool pointers must not be NULL";
+    if (!aligned(p->k_codes, 16) || !aligned(p->v_codes, 16) || !aligned(p->k_scale, 16) || !aligned(p->v_scale, 16))
+        return "codes and scales must be 16-byte aligned";
+    const long long dense = (long long)c->cfg.n_kv_heads * c->cfg.block_tokens * c->cfg.head_dim / 2;
+    if (p->block_stride != 0 && (p->block_stride < dense || p->block_stride % 16 || p->block_stride >= (1ll << 39)))
+        return "block_stride must be 0 or a multiple of 16 that holds a block";
+    return nullptr;
+}
+long long stride4(const kv8_cache* c, const kv4_pool* p) {
+    return p->block_stride ? p->block_stride : (long long)c->cfg.n_kv_heads * c->cfg.block_tokens * c->cfg.head_dim / 2;
+}
+
 const char* heads_error(const kv8_heads& h, int n_tok, int head_dim) {
     if (h.n_heads < 0 || h.n_heads > 1024) return "n_heads must be in [0, 1024]";
     if (h.n_heads == 0) return nullptr;
@@ -151,6 +166,7 @@ int kv8_create(const kv8_config* cfg, kv8_cache** out) {
         if (!bit || !(set.load() & bit)) {
             e = kv8::set_attend_attrs();
             if (e == cudaSuccess) e = kv8::set_resize_attrs();
+            if (e == cudaSuccess) e = kv8::set_attend4_attrs();
             if (e == cudaSuccess) set.fetch_or(bit);
         }
     }
@@ -164,6 +180,9 @@ int kv8_create(const kv8_config* cfg, kv8_cache** out) {
         if (e == cudaSuccess) e = cudaMalloc(&c->d_meta, c->meta_n * sizeof(int4));
         if (e == cudaSuccess) e = cudaMalloc(&c->d_ctrl, 2 * sizeof(int));
         if (e == cudaSuccess) e = cudaMemset(c->d_ctrl, 0, 2 * sizeof(int));
+        c->arrived_n = kv8::attend4_arrivals(c->sm_count);
+        if (e == cudaSuccess) e = cudaMalloc(&c->d_arrived, c->arrived_n * sizeof(int));
+        if (e == cudaSuccess) e = cudaMemset(c->d_arrived, 0, c->arrived_n * sizeof(int));
         // the clears run on the legacy stream, which streams that do not block do not wait for
         if (e == cudaSuccess) e = cudaStreamSynchronize(0);
     }
@@ -187,6 +206,7 @@ void kv8_destroy(kv8_cache* c) {
         cudaFree(c->d_part_ml);
         cudaFree(c->d_meta);
         cudaFree(c->d_ctrl);
+        cudaFree(c->d_arrived);
     }
     delete c;
 }
@@ -205,9 +225,9 @@ int kv8_resize(kv8_cache* c, const int32_t* d_new_len, int n_req, int32_t* d_len
     return e == cudaSuccess ? SRH_OK : cuda_fail(c, e, "kv8_resize launch");
 }
 
-int kv8_norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_tok, int head_dim, const int32_t* d_pos,
-                  const double* d_inv_freq, int rot_dim, int rot_off, int style, float eps, srh_stream_t stream) {
-    if (!c) return SRH_ERR_INVALID;
+static int norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_tok, int head_dim, const int32_t* d_pos,
+                     long long pos_row, int n_axes, const uint8_t* d_axis, const double* d_inv_freq, int rot_dim, int rot_off,
+                     int style, float eps, srh_stream_t stream) {
     if (!q && !k) return fail(c, SRH_ERR_INVALID, "no heads");
     const kv8_heads none{};
     const kv8_heads a = q ? *q : none, b = k ? *k : none;
@@ -227,9 +247,25 @@ int kv8_norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_to
     if (const char* why = overlap_error(a, b, n_tok, head_dim)) return fail(c, SRH_ERR_INVALID, why);
     if (const char* why = overlap_error(b, a, n_tok, head_dim)) return fail(c, SRH_ERR_INVALID, why);
     KV8_DEVICE(c);
-    const cudaError_t e = kv8::launch_norm_rope(*c, a, b, n_tok, head_dim, d_pos, d_inv_freq, rot_dim, rot_off, style, eps,
-                                                (cudaStream_t)stream);
+    const cudaError_t e = kv8::launch_norm_rope(*c, a, b, n_tok, head_dim, d_pos, pos_row, n_axes, d_axis, d_inv_freq,
+                                                rot_dim, rot_off, style, eps, (cudaStream_t)stream);
     return e == cudaSuccess ? SRH_OK : cuda_fail(c, e, "kv8_norm_rope launch");
+}
+
+int kv8_norm_rope(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_tok, int head_dim, const int32_t* d_pos,
+                  const double* d_inv_freq, int rot_dim, int rot_off, int style, float eps, srh_stream_t stream) {
+    if (!c) return SRH_ERR_INVALID;
+    return norm_rope(c, q, k, n_tok, head_dim, d_pos, 0, 1, nullptr, d_inv_freq, rot_dim, rot_off, style, eps, stream);
+}
+
+int kv8_norm_rope_axes(kv8_cache* c, const kv8_heads* q, const kv8_heads* k, int n_tok, int head_dim, const int32_t* d_pos,
+                       long long pos_row, int n_axes, const uint8_t* d_axis, const double* d_inv_freq, int rot_dim,
+                       int rot_off, int style, float eps, srh_stream_t stream) {
+    if (!c) return SRH_ERR_INVALID;
+    if (n_axes < 1 || n_axes > 8) return fail(c, SRH_ERR_INVALID, "n_axes must be in [1, 8]");
+    if (pos_row != 0 && pos_row < n_tok) return fail(c, SRH_ERR_INVALID, "pos_row must be 0 or at least n_tok");
+    if (rot_dim && !d_axis) return fail(c, SRH_ERR_INVALID, "d_axis must not be NULL");
+    return norm_rope(c, q, k, n_tok, head_dim, d_pos, pos_row, n_axes, d_axis, d_inv_freq, rot_dim, rot_off, style, eps, stream);
 }
 
 int kv8_append(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
@@ -251,18 +287,20 @@ int kv8_append(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const
     return e == cudaSuccess ? SRH_OK : cuda_fail(c, e, "kv8_append launch");
 }
 
-int kv8_attend(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
-               int n_req, const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,
-               uint16_t* d_out, long long out_row, srh_stream_t stream) {
-    if (!c) return SRH_ERR_INVALID;
-    if (const char* why = pool_error(c, pool)) return fail(c, SRH_ERR_INVALID, why);
+// What kv8_attend and kv4_attend are given, but for the pool; *none: there are no rows.
+static int attend_args(kv8_cache* c, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu, int n_req,
+                       const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,
+                       uint16_t* d_out, long long out_row, bool* none) {
     if (n_req < 1 || n_req > c->cfg.batch) return fail(c, SRH_ERR_INVALID, "n_req must be in [1, batch]");
     if (n_rows < 0) return fail(c, SRH_ERR_INVALID, "n_rows must be >= 0");
     if (n_heads < 1 || n_heads % c->cfg.n_kv_heads) return fail(c, SRH_ERR_INVALID, "n_heads must be a multiple of n_kv_heads");
     if ((long long)n_rows * n_heads > (1ll << 30)) return fail(c, SRH_ERR_INVALID, "n_rows * n_heads must be <= 2^30");
     if (!std::isfinite(scale)) return fail(c, SRH_ERR_INVALID, "scale must be finite");
     if (window < 0) return fail(c, SRH_ERR_INVALID, "window must be >= 0");
-    if (n_rows == 0) return SRH_OK;
+    if (n_rows == 0) {
+        *none = true;
+        return SRH_OK;
+    }
     if (!d_table || !d_len || !d_cu || !d_q || !d_out) return fail(c, SRH_ERR_INVALID, "NULL pointer");
     if (!aligned(d_q, 16) || !aligned(d_out, 16)) return fail(c, SRH_ERR_INVALID, "q and out must be 16-byte aligned");
     const long long width = (long long)n_heads * c->cfg.head_dim;
@@ -270,10 +308,102 @@ int kv8_attend(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const
         return fail(c, SRH_ERR_INVALID, "row strides must be multiples of 8 (the output's at least a row)");
     if (meet({d_q, q_row, n_rows, width}, {d_out, out_row, n_rows, width}))
         return fail(c, SRH_ERR_INVALID, "out must not overlap q");
+    return SRH_OK;
+}
+
+int kv8_attend(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
+               int n_req, const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,
+               uint16_t* d_out, long long out_row, srh_stream_t stream) {
+    if (!c) return SRH_ERR_INVALID;
+    if (const char* why = pool_error(c, pool)) return fail(c, SRH_ERR_INVALID, why);
+    bool none = false;
+    if (const int rc = attend_args(c, d_table, d_len, d_cu, n_req, d_q, q_row, n_rows, n_heads, scale, window, d_out, out_row,
+                                   &none))
+        return rc;
+    if (none) return SRH_OK;
     KV8_DEVICE(c);
     const cudaError_t e = kv8::launch_attend(*c, *pool, d_table, d_len, d_cu, n_req, d_q, q_row, n_rows, n_heads, scale,
                                              window, d_out, out_row, (cudaStream_t)stream);
     return e == cudaSuccess ? SRH_OK : cuda_fail(c, e, "kv8_attend launch");
+}
+
+int kv4_attend(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
+               int n_req, const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,
+               uint16_t* d_out, long long out_row, srh_stream_t stream) {
+    if (!c) return SRH_ERR_INVALID;
+    if (const char* why = pool4_error(c, pool)) return fail(c, SRH_ERR_INVALID, why);
+    bool none = false;
+    if (const int rc = attend_args(c, d_table, d_len, d_cu, n_req, d_q, q_row, n_rows, n_heads, scale, window, d_out, out_row,
+                                   &none))
+        return rc;
+    if (none) return SRH_OK;
+    KV8_DEVICE(c);
+    kv4_pool p = *pool;
+    p.block_stride = stride4(c, pool);
+    const cudaError_t e = kv8::launch_attend4(*c, p, d_table, d_len, d_cu, n_req, d_q, q_row, n_rows, n_heads, scale, window,
+                                              d_out, out_row, (cudaStream_t)stream);
+    return e == cudaSuccess ? SRH_OK : cuda_fail(c, e, "kv4_attend launch");
+}
+
+int kv4_append(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
+               int n_req, const uint16_t* d_k, long long k_row, const uint16_t* d_v, long long v_row, int n_rows,
+               srh_stream_t stream) {
+    if (!c) return SRH_ERR_INVALID;
+    if (const char* why = pool4_error(c, pool)) return fail(c, SRH_ERR_INVALID, why);
+    if (n_req < 1 || n_req > c->cfg.batch) return fail(c, SRH_ERR_INVALID, "n_req must be in [1, batch]");
+    if (n_rows < 0) return fail(c, SRH_ERR_INVALID, "n_rows must be >= 0");
+    if (n_rows == 0) return SRH_OK;
+    if (!d_table || !d_len || !d_cu || !d_k || !d_v) return fail(c, SRH_ERR_INVALID, "NULL pointer");
+    if (!aligned(d_k, 16) || !aligned(d_v, 16)) return fail(c, SRH_ERR_INVALID, "rows must be 16-byte aligned");
+    if (!row_ok(k_row, 0, n_rows, false) || !row_ok(v_row, 0, n_rows, false))
+        return fail(c, SRH_ERR_INVALID, "row strides must be multiples of 8, >= 0");
+    KV8_DEVICE(c);
+    const kv8::Layer l{{{pool->k_codes, pool->k_scale, const_cast<uint16_t*>(d_k), k_row},
+                        {pool->v_codes, pool->v_scale, const_cast<uint16_t*>(d_v), v_row}},
+                       2, 4, stride4(c, pool)};
+    const cudaError_t e = kv8::launch_append4(*c, l, d_table, d_len, d_cu, n_req, n_rows, (cudaStream_t)stream);
+    return e == cudaSuccess ? SRH_OK : cuda_fail(c, e, "kv4_append launch");
+}
+
+// kv8_read and kv4_read, their pools checked.
+static int read_rows(kv8_cache* c, kv8::Layer l, const int32_t* d_table, const int32_t* d_len, const int32_t* d_start,
+                     const int32_t* d_cu, int n_req, int n_rows, srh_stream_t stream, const char* where) {
+    if (n_req < 1 || n_req > c->cfg.batch) return fail(c, SRH_ERR_INVALID, "n_req must be in [1, batch]");
+    if (n_rows < 0) return fail(c, SRH_ERR_INVALID, "n_rows must be >= 0");
+    if (n_rows == 0) return SRH_OK;
+    if (!d_table || !d_len || !d_start || !d_cu) return fail(c, SRH_ERR_INVALID, "NULL pointer");
+    const long long width = (long long)c->cfg.n_kv_heads * c->cfg.head_dim;
+    for (int i = 0; i < l.parts; ++i) {
+        if (!l.part[i].x) return fail(c, SRH_ERR_INVALID, "NULL pointer");
+        if (!aligned(l.part[i].x, 16)) return fail(c, SRH_ERR_INVALID, "rows must be 16-byte aligned");
+        if (!row_ok(l.part[i].x_row, width, n_rows, true))
+            return fail(c, SRH_ERR_INVALID, "row strides must be multiples of 8, at least a row");
+    }
+    if (l.parts == 2 && meet({l.part[0].x, l.part[0].x_row, n_rows, width}, {l.part[1].x, l.part[1].x_row, n_rows, width}))
+        return fail(c, SRH_ERR_INVALID, "rows of K and V must not overlap");
+    KV8_DEVICE(c);
+    const cudaError_t e = kv8::launch_read(*c, l, d_table, d_len, d_start, d_cu, n_req, n_rows, (cudaStream_t)stream);
+    return e == cudaSuccess ? SRH_OK : cuda_fail(c, e, where);
+}
+
+int kv8_read(kv8_cache* c, const kv8_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_start,
+             const int32_t* d_cu, int n_req, uint16_t* d_k, long long k_row, uint16_t* d_v, long long v_row, int n_rows,
+             srh_stream_t stream) {
+    if (!c) return SRH_ERR_INVALID;
+    if (const char* why = pool_error(c, pool)) return fail(c, SRH_ERR_INVALID, why);
+    return read_rows(c, {{{pool->k_codes, pool->k_scale, d_k, k_row}, {pool->v_codes, pool->v_scale, d_v, v_row}},
+                         c->cfg.shared_kv ? 1 : 2, 8, c->block_stride},
+                     d_table, d_len, d_start, d_cu, n_req, n_rows, stream, "kv8_read launch");
+}
+
+int kv4_read(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_start,
+             const int32_t* d_cu, int n_req, uint16_t* d_k, long long k_row, uint16_t* d_v, long long v_row, int n_rows,
+             srh_stream_t stream) {
+    if (!c) return SRH_ERR_INVALID;
+    if (const char* why = pool4_error(c, pool)) return fail(c, SRH_ERR_INVALID, why);
+    return read_rows(c, {{{pool->k_codes, pool->k_scale, d_k, k_row}, {pool->v_codes, pool->v_scale, d_v, v_row}}, 2, 4,
+                         stride4(c, pool)},
+                     d_table, d_len, d_start, d_cu, n_req, n_rows, stream, "kv4_read launch");
 }
 
 int kv8_check_error(kv8_cache* c) {
@@ -288,7 +418,7 @@ int kv8_check_error(kv8_cache* c) {
     if (w & kv8::kErrNoBlocks) return fail(c, SRH_ERR_NOMEM, "too few free blocks; the call changed nothing");
     if (w & kErrBounds) return fail(c, SRH_ERR_BOUNDS, "a length, table entry, cu value or slot was out of bounds");
     if (w & kErrTimeout) return fail(c, SRH_ERR_TIMEOUT, "a device wait timed out");
-    if (w & kErrRange) return fail(c, SRH_ERR_RANGE, "an appended value is not finite or beyond 448 * 2^64");
+    if (w & kErrRange) return fail(c, SRH_ERR_RANGE, "an appended value is not finite or too large (448 * 2^64 in 8 bits, 2^120 in 4)");
     return SRH_OK;
 }
 

@@ -22,6 +22,8 @@ struct Cache {
     float* d_part_ml = nullptr;     // their maxima and sums
     int4* d_meta = nullptr;         // split items, by the chunk that they begin in
     int* d_ctrl = nullptr;          // the attention's chunk counter and count
+    int* d_arrived = nullptr;       // parts of split items that are written (4-bit attention); zeros between calls
+    size_t arrived_n = 0;
     size_t part_o_floats = 0;       // sizes of the three, which the launcher checks
     size_t part_ml_floats = 0;
     size_t meta_n = 0;
@@ -39,14 +41,38 @@ cudaError_t launch_resize(const Cache& c, const int32_t* new_len, int n_req, int
                           int32_t* free_ids, int32_t* n_free, int32_t* cu, int32_t* pos, int64_t* slot, int cap,
                           cudaStream_t st);
 cudaError_t launch_norm_rope(const Cache& c, const kv8_heads& q, const kv8_heads& k, int n_tok, int head_dim,
-                             const int32_t* pos, const double* inv_freq, int rot_dim, int rot_off, int style,
-                             float eps, cudaStream_t st);
+                             const int32_t* pos, long long pos_row, int n_axes, const uint8_t* axis,
+                             const double* inv_freq, int rot_dim, int rot_off, int style, float eps, cudaStream_t st);
 cudaError_t launch_append(const Cache& c, const kv8_pool& pool, const int32_t* table, const int32_t* len,
                           const int32_t* cu, int n_req, const uint16_t* k, long long k_row, const uint16_t* v,
                           long long v_row, int n_rows, cudaStream_t st);
 cudaError_t launch_attend(const Cache& c, const kv8_pool& pool, const int32_t* table, const int32_t* len,
                           const int32_t* cu, int n_req, const uint16_t* q, long long q_row, int n_rows, int n_heads,
                           float scale, int window, uint16_t* out, long long out_row, cudaStream_t st);
+
+
+// Rows of a 4-bit pool (bits 4) or of an 8-bit one (bits 8).
+struct Part {
+    uint8_t* codes;
+    void* scale;
+    uint16_t* x;                    // bf16 rows
+    long long x_row;
+};
+struct Layer {
+    Part part[2];                   // K, V
+    int parts, bits;
+    long long block_stride;
+};
+cudaError_t launch_append4(const Cache& c, const Layer& l, const int32_t* table, const int32_t* len, const int32_t* cu,
+                           int n_req, int n_rows, cudaStream_t st);
+cudaError_t launch_read(const Cache& c, const Layer& l, const int32_t* table, const int32_t* len, const int32_t* start,
+                        const int32_t* cu, int n_req, int n_rows, cudaStream_t st);
+// Arrival counters that kv4_attend needs.
+size_t attend4_arrivals(int sm_count);
+cudaError_t set_attend4_attrs();
+cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* table, const int32_t* len,
+                           const int32_t* cu, int n_req, const uint16_t* q, long long q_row, int n_rows, int n_heads,
+                           float scale, int window, uint16_t* out, long long out_row, cudaStream_t st);
 
 #ifdef __CUDACC__
 // Inclusive sum over the CTA's threads (blockDim.x a multiple of 32, at most

@@ -1,4 +1,4 @@
-"""Paged 8-bit KV cache: requests of different lengths over one pool of blocks.
+"""Paged KV cache in 8 or 4 bits: requests of different lengths over one pool of blocks.
 
 ``PagedKV8`` owns a library handle (scratch, error word), the block table, the
 request lengths, the stack of free blocks and, per layer, the pools of e4m3
@@ -9,8 +9,9 @@ codes and block scales (or adopts the caller's tensors). One serving step is
     cache.append(k, v, cu)                             # rows into the cache
     out = cache.attend(q, cu, scale=...)               # attention over it
 
-and ``resize`` with shorter lengths gives rejected drafted tokens back. All work
-runs in the library's kernels (kv8_* of include/srh.h); PyTorch allocates
+and ``resize`` with shorter lengths gives rejected drafted tokens back; ``read`` brings
+rows of the cache back. ``PagedKV4`` is the same cache in 4 bits. All work
+runs in the library's kernels (kv8_* and kv4_* of include/srh.h); PyTorch allocates
 tensors and names streams. Calls on one cache are ordered by the caller. A call
 on a ``stream`` of its own waits for nothing on the current one; the tensors that it
 is given may be let go as soon as it returns.
@@ -65,21 +66,8 @@ class PagedKV8:
         self.device = torch.device("cuda", torch.cuda.current_device() if dev.index is None else dev.index)
         self.batch, self.Hk, self.D, self.bs = batch, n_kv_heads, head_dim, block_tokens
         self.n_blocks, self.max_blocks, self.shared = n_blocks, max_blocks, bool(shared_kv)
-        shape = (n_blocks, n_kv_heads, block_tokens, head_dim)
-        stride = 0
-        for name in ("k_codes", "v_codes"):
-            t = buf.get(name)
-            if t is None:
-                continue
-            inner = (block_tokens * head_dim, head_dim, 1)
-            if t.dtype != torch.uint8 or tuple(t.shape) != shape or t.stride()[1:] != inner or t.device != self.device:
-                raise ValueError(f"{name} must be uint8 {shape} on {self.device}, dense within a block")
-            if n_blocks > 1 and t.stride(0) < t[0].numel():
-                raise ValueError(f"{name}: blocks must not overlap")
-            if stride and n_blocks > 1 and t.stride(0) != stride:
-                raise ValueError("k_codes and v_codes must have the same block stride")
-            stride = t.stride(0) if n_blocks > 1 else 0
-        cfg = abi.Kv8Config(batch, n_kv_heads, head_dim, block_tokens, n_blocks, max_blocks, int(self.shared), stride)
+        stride = self._stride(buf)
+        cfg = abi.Kv8Config(batch, n_kv_heads, head_dim, block_tokens, n_blocks, max_blocks, int(self.shared), self._handle_stride(stride))
         with torch.cuda.device(self.device):
             self.cache = abi.kv8_create(cfg)
 
@@ -108,20 +96,54 @@ class PagedKV8:
                 c = buf.get(part + "_codes")
                 if c is None:
                     # the block stride of a given pool holds for both
-                    width = stride or n_kv_heads * block_tokens * head_dim
+                    width = stride or self._block[0] * self._block[1] * self._block[2]
                     c = torch.zeros((n_blocks, width), dtype=torch.uint8, device=self.device)
-                    c = c[:, :n_kv_heads * block_tokens * head_dim].view(shape)
+                    c = c[:, :self._block[0] * self._block[1] * self._block[2]].view((n_blocks, *self._block))
                 codes.append(c)
-                scale.append(tensor(part + "_scale", (n_blocks, n_kv_heads), torch.float32,
-                                    lambda: torch.ones((n_blocks, n_kv_heads), device=self.device)))
-            pool = abi.Kv8Pool(self.k_codes[-1].data_ptr(), self.k_scale[-1].data_ptr(),
-                               self.v_codes[-1].data_ptr(), self.v_scale[-1].data_ptr())
-            self._pool.append(ctypes.byref(pool))
+                shp, dtype = self._scale_form()
+                scale.append(tensor(part + "_scale", shp, dtype, lambda: torch.ones(shp, dtype=dtype, device=self.device)))
+            self._pool.append(ctypes.byref(self._pool_of(stride)))
         # what every call passes, taken once: the cache's own tensors stay where they are
         self._lib = abi.load()
         self._index = self.device.index
         self._table, self._len = self.table.data_ptr(), self.len.data_ptr()
         self._free, self._n_free = self.free.data_ptr(), self.n_free.data_ptr()
+        self._append, self._read, self._attend = (getattr(self._lib, name) for name in self._calls)
+
+    # ------------------------------------------------------------------ the pools' form
+    _calls = ("kv8_append", "kv8_read", "kv8_attend")
+
+    @property
+    def _block(self) -> tuple:
+        """A block of codes: heads, tokens, bytes of a row."""
+        return (self.Hk, self.bs, self.D)
+
+    def _scale_form(self) -> tuple:
+        return (self.n_blocks, self.Hk), torch.float32
+
+    def _handle_stride(self, stride: int) -> int:
+        return stride
+
+    def _pool_of(self, stride: int):
+        return abi.Kv8Pool(self.k_codes[-1].data_ptr(), self.k_scale[-1].data_ptr(),
+                           self.v_codes[-1].data_ptr(), self.v_scale[-1].data_ptr())
+
+    def _stride(self, buf: dict) -> int:
+        """The block stride of the pools given (0: dense), which are checked."""
+        shape, stride = (self.n_blocks, *self._block), 0
+        for name in ("k_codes", "v_codes"):
+            t = buf.get(name)
+            if t is None:
+                continue
+            inner = (shape[2] * shape[3], shape[3], 1)
+            if t.dtype != torch.uint8 or tuple(t.shape) != shape or t.stride()[1:] != inner or t.device != self.device:
+                raise ValueError(f"{name} must be uint8 {shape} on {self.device}, dense within a block")
+            if self.n_blocks > 1 and t.stride(0) < t[0].numel():
+                raise ValueError(f"{name}: blocks must not overlap")
+            if stride and self.n_blocks > 1 and t.stride(0) != stride:
+                raise ValueError("k_codes and v_codes must have the same block stride")
+            stride = t.stride(0) if self.n_blocks > 1 else 0
+        return stride
 
     # ------------------------------------------------------------------ checks
     def _raise(self, rc: int, where: str) -> None:
@@ -132,13 +154,14 @@ class PagedKV8:
             return _current_stream(self.device.index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def _empty(self, shape, dtype, stream) -> torch.Tensor:
+    def _empty(self, shape, dtype, stream, zero: bool = False) -> torch.Tensor:
         """A new output of a call on ``stream``: its memory belongs to that stream."""
+        make = torch.zeros if zero else torch.empty
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return make(shape, dtype=dtype, device=self.device)
         s = torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
         with torch.cuda.stream(s):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return make(shape, dtype=dtype, device=self.device)
 
     def _keep(self, stream, *tensors) -> None:
         """Memory of a call's tensors is not handed out again before ``stream`` is through with them."""
@@ -208,11 +231,13 @@ class PagedKV8:
         return cu, pos, slot
 
     def norm_rope(self, q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None, *, pos=None, inv_freq=None,
-                  rot_dim: int = 0, rot_off: int = 0, style: str = "pairs", eps: float = 1e-6, q_weight=None, k_weight=None,
+                  axis=None, rot_dim: int = 0, rot_off: int = 0, style: str = "pairs", eps: float = 1e-6, q_weight=None, k_weight=None,
                   q_out=None, k_out=None, q_slot=None, k_slot=None, stream=None):
         """RMS norm of every head of ``q`` and ``k`` (bf16 [tokens][heads][dim]; either
         may be None) and rotation of dims [rot_off, rot_off + rot_dim) by
-        ``pos`` * ``inv_freq`` (fp64 [rot_dim / 2]). ``*_slot`` (int64): token t's
+        ``pos`` * ``inv_freq`` (fp64 [rot_dim / 2]). With ``axis`` (uint8 [rot_dim / 2])
+        positions have several axes (time, height, width): ``pos`` is int32 [axes][tokens]
+        and pair i turns by its row axis[i]. ``*_slot`` (int64): token t's
         row goes to row slot[t] of ``*_out`` (negative: nowhere), which is then
         required. Returns (q_out, k_out)."""
         if style not in _STYLES:
@@ -224,7 +249,13 @@ class PagedKV8:
         if rot_dim:
             if pos is None or inv_freq is None:
                 raise ValueError("rot_dim needs pos and inv_freq")
-            self._ints(pos, "pos", n)
+            if axis is None:
+                self._ints(pos, "pos", n)
+            else:
+                if (pos.dtype != torch.int32 or pos.dim() != 2 or pos.get_device() != self._index or not 1 <= pos.shape[0] <= 8
+                        or pos.shape[1] != n or (n > 1 and pos.stride(1) != 1) or (pos.shape[0] > 1 and pos.stride(0) < n)):
+                    raise ValueError(f"pos must be int32 [axes][tokens] with dense rows on {self.device}, 1 to 8 axes")
+                self._ints(axis, "axis", rot_dim // 2, torch.uint8)
             self._ints(inv_freq, "inv_freq", rot_dim // 2, torch.float64)
         parts, outs = [], []
         for x, w, out, slot, name in ((q, q_weight, q_out, q_slot, "q"), (k, k_weight, k_out, k_slot, "k")):
@@ -253,13 +284,18 @@ class PagedKV8:
                                       0 if slot is None else out.shape[0]))
             outs.append(out)
         if n:
-            rc = self._lib.kv8_norm_rope(self.cache, parts[0], parts[1], n, d, pos.data_ptr() if rot_dim else None,
-                                         inv_freq.data_ptr() if rot_dim else None, rot_dim, rot_off, _STYLES[style], eps,
-                                         self._s(stream))
+            at = (pos.data_ptr(), inv_freq.data_ptr()) if rot_dim else (None, None)
+            if axis is None or not rot_dim:
+                rc = self._lib.kv8_norm_rope(self.cache, parts[0], parts[1], n, d, *at, rot_dim, rot_off, _STYLES[style], eps,
+                                             self._s(stream))
+            else:
+                rc = self._lib.kv8_norm_rope_axes(self.cache, parts[0], parts[1], n, d, at[0],
+                                                  pos.stride(0) if pos.shape[0] > 1 else n, pos.shape[0], axis.data_ptr(), at[1],
+                                                  rot_dim, rot_off, _STYLES[style], eps, self._s(stream))
             if rc:
                 self._raise(rc, "kv8_norm_rope")
             if stream is not None:
-                self._keep(stream, q, k, pos, inv_freq, q_weight, k_weight, q_slot, k_slot, *outs)
+                self._keep(stream, q, k, pos, inv_freq, axis, q_weight, k_weight, q_slot, k_slot, *outs)
         return outs[0], outs[1]
 
     def append(self, k: torch.Tensor, v: Optional[torch.Tensor], cu: torch.Tensor, *, layer: int = 0, stream=None) -> None:
@@ -275,10 +311,10 @@ class PagedKV8:
             if v.shape[0] != k.shape[0]:
                 raise ValueError("k and v must have the same rows")
         if k.shape[0]:
-            rc = self._lib.kv8_append(self.cache, self._pool[layer], self._table, self._len, cu.data_ptr(), n, k.data_ptr(),
+            rc = self._append(self.cache, self._pool[layer], self._table, self._len, cu.data_ptr(), n, k.data_ptr(),
                                       kr, None if v is None else v.data_ptr(), vr, k.shape[0], self._s(stream))
             if rc:
-                self._raise(rc, "kv8_append")
+                self._raise(rc, self._calls[0])
             if stream is not None:
                 self._keep(stream, k, v, cu)
 
@@ -296,13 +332,46 @@ class PagedKV8:
         else:
             orow = self._rows(out, "out", None, self.D)
         if q.shape[0]:
-            rc = self._lib.kv8_attend(self.cache, self._pool[layer], self._table, self._len, cu.data_ptr(), n, q.data_ptr(),
+            rc = self._attend(self.cache, self._pool[layer], self._table, self._len, cu.data_ptr(), n, q.data_ptr(),
                                       qr, q.shape[0], q.shape[1], scale, window, out.data_ptr(), orow, self._s(stream))
             if rc:
-                self._raise(rc, "kv8_attend")
+                self._raise(rc, self._calls[2])
             if stream is not None:
                 self._keep(stream, q, cu, out)
         return out
+
+    def read(self, start: torch.Tensor, cu: torch.Tensor, n_rows: int, *, k_out=None, v_out=None, layer: int = 0,
+             stream=None):
+        """Tokens ``start[b]`` .. ``start[b] + cu[b+1] - cu[b] - 1`` of each request (int32) back from the
+        cache, as rows ``cu[b]`` .. of ``k_out`` and ``v_out`` (bf16 [n_rows][n_kv_heads][head_dim]; new
+        ones, zeroed, where not given). Rows that no token of the cache belongs to are left as they are.
+        Returns (k_out, v_out), with v_out None when shared."""
+        n = self._requests(cu)
+        self._ints(start, "start", n)
+        if n_rows < 0:
+            raise ValueError("n_rows must be >= 0")
+        if self.shared and v_out is not None:
+            raise ValueError("a shared cache has one pool")
+        outs, rows = [], []
+        for out, name in ((k_out, "k_out"), (v_out, "v_out"))[:1 if self.shared else 2]:
+            if out is None:
+                out = self._empty((n_rows, self.Hk, self.D), torch.bfloat16, stream, zero=True)
+            rows.append(self._rows(out, name, self.Hk, self.D))
+            if out.shape[0] != n_rows:
+                raise ValueError(f"{name} must have n_rows rows")
+            outs.append(out)
+        if self.shared:
+            outs.append(None)
+            rows.append(0)
+        if n_rows:
+            rc = self._read(self.cache, self._pool[layer], self._table, self._len, start.data_ptr(), cu.data_ptr(), n,
+                            outs[0].data_ptr(), rows[0], None if self.shared else outs[1].data_ptr(), rows[1], n_rows,
+                            self._s(stream))
+            if rc:
+                self._raise(rc, self._calls[1])
+            if stream is not None:
+                self._keep(stream, start, cu, *outs)
+        return outs[0], outs[1]
 
     # ------------------------------------------------------------------ status
     def check_error(self) -> int:
@@ -319,3 +388,34 @@ class PagedKV8:
             self.close()
         except Exception:
             pass
+
+
+class PagedKV4(PagedKV8):
+    """The same cache in 4 bits: grouped heads of 128 or 256 dims, K and V apart. Codes are uint8
+    [n_blocks][n_kv_heads][block_tokens][head_dim / 2], the even dim in the low half of a byte, scales
+    bf16 [n_blocks][n_kv_heads][block_tokens][2]: a scale s and a minimum m per token and head, a value
+    is m + code * s. ``buffers`` as for PagedKV8, of these shapes. An appended row changes nothing
+    that is held; latent rows (``shared_kv``) are kept in 8 bits only."""
+
+    _calls = ("kv4_append", "kv4_read", "kv4_attend")
+
+    def __init__(self, *, head_dim: int, **kw):
+        if kw.get("shared_kv"):
+            raise ValueError("latent rows are kept in 8 bits")
+        if head_dim not in (128, 256):
+            raise ValueError("head_dim must be 128 or 256")
+        super().__init__(head_dim=head_dim, **kw)
+
+    @property
+    def _block(self) -> tuple:
+        return (self.Hk, self.bs, self.D // 2)
+
+    def _scale_form(self) -> tuple:
+        return (self.n_blocks, self.Hk, self.bs, 2), torch.bfloat16
+
+    def _handle_stride(self, stride: int) -> int:
+        return 0
+
+    def _pool_of(self, stride: int):
+        return abi.Kv4Pool(self.k_codes[-1].data_ptr(), self.k_scale[-1].data_ptr(),
+                           self.v_codes[-1].data_ptr(), self.v_scale[-1].data_ptr(), stride)

@@ -1,0 +1,825 @@
+"""The paged cache in 4 bits (kv4_*), rows read back (kv4_read, kv8_read) and the rotation by several axes against plain
+64-bit implementations, and a serving loop of them together."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+FP8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+def _abi():
+    from sparse_retrieval_host_gb300 import abi
+    return abi
+
+
+def _kv4(**kw):
+    from sparse_retrieval_host_gb300.paged import PagedKV4
+    return PagedKV4(**kw)
+
+
+def _kv8(**kw):
+    from sparse_retrieval_host_gb300.paged import PagedKV8
+    return PagedKV8(**kw)
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _bf16(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda").bfloat16()
+
+
+def _cu(counts):
+    return _i32([0] + list(np.cumsum(counts)))
+
+
+# ---------------------------------------------------------------------------------------------- the form of a row
+def _quantise(x):
+    """numpy float32 rows [..., D] of bf16 values -> codes, s, m by the documented steps."""
+    x = np.where(np.isfinite(x), x, np.float32(0)).astype(np.float32)
+    x = np.clip(x, -np.float32(2.0 ** 120), np.float32(2.0 ** 120))
+    lo, hi = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
+    s = torch.from_numpy(((hi - lo) / np.float32(15)).astype(np.float32)).bfloat16().float().numpy()
+    with np.errstate(divide="ignore", invalid="ignore"):
+        n = np.rint((x - lo) / s)
+    n = np.where(s > 0, np.clip(n, 0, 15), 0).astype(np.uint8)
+    return n, s[..., 0], lo[..., 0]
+
+
+def _codes(c, part, layer=0):
+    """Codes [n_blocks][heads][tokens][D] and (s, m) as fp64, of a 4-bit cache."""
+    b = (c.k_codes if part == "k" else c.v_codes)[layer]
+    sm = (c.k_scale if part == "k" else c.v_scale)[layer]
+    return torch.stack((b & 15, b >> 4), -1).flatten(-2), sm
+
+
+def _values(c, part, b, n, layer=0):
+    """Request b's first n tokens, fp64 [n][heads][D]."""
+    codes, sm = _codes(c, part, layer)
+    blk = c.table[b, :-(-n // c.bs)].long()
+    v = codes[blk].double() * sm[blk][..., :1].double() + sm[blk][..., 1:].double()
+    return v.transpose(1, 2).reshape(-1, c.Hk, c.D)[:n]
+
+
+def _filled(c, g, lens, spread=2, mean=0.3, layer=0):
+    """Fills a cache's tables and pools for lengths `lens` with quantised rows, by the test's own hand."""
+    bs = c.bs
+    need = [-(-n // bs) for n in lens]
+    ids = torch.randperm(c.n_blocks, generator=g, device="cuda")[:sum(need)].int()
+    at = 0
+    c.table.fill_(-1)
+    for b, k in enumerate(need):
+        c.table[b, :k] = ids[at:at + k]
+        at += k
+    c.len[:len(lens)] = _i32(lens)
+    for codes, scale in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale)):
+        codes[layer].copy_(torch.randint(0, 256, codes[layer].shape, generator=g, device="cuda", dtype=torch.uint8))
+        sh = scale[layer].shape[:-1]
+        s = 0.3 * torch.exp2(torch.randint(-spread, spread + 1, sh, generator=g, device="cuda").float())
+        m = -7.5 * s * (1 + 0.2 * torch.randn(sh, generator=g, device="cuda")) + mean
+        scale[layer].copy_(torch.stack((s, m), -1).bfloat16())
+
+
+# ---------------------------------------------------------------------------------------------- append
+@pytest.mark.parametrize("bs,Hk,D,news", [(16, 1, 128, [1]), (16, 8, 128, [1, 5, 0, 33]), (32, 2, 256, [70, 1, 16]),
+                                          (64, 3, 128, [129, 64, 2]), (128, 1, 256, [1] * 40), (16, 4, 128, [1, 0] * 600)])
+def test_append_is_exact(bs, Hk, D, news):
+    g = _gen(bs * Hk + len(news))
+    rng = np.random.default_rng(bs + D)
+    B = len(news)
+    olds = [int(v) for v in rng.integers(0, 3 * bs, B)]
+    lens = [a + b for a, b in zip(olds, news)]
+    most = max(-(-n // bs) for n in lens) + 1
+    c = _kv4(batch=B, n_kv_heads=Hk, head_dim=D, block_tokens=bs, n_blocks=sum(-(-n // bs) for n in lens) + 5, max_blocks=most)
+    _filled(c, g, lens)
+    T = sum(news)
+    big = _bf16(g, T + 2, 3 * Hk * D) * torch.exp2(torch.randint(-20, 20, (T + 2, 1), generator=g, device="cuda").float()).bfloat16()
+    k, v = big[:T, :Hk * D].view(T, Hk, D), big[:T, 2 * Hk * D:].view(T, Hk, D)      # strided rows
+    cu = _cu(news)
+    before = {p: [t.clone() for t in _codes(c, p)] for p in "kv"}
+    c.append(k, v, cu)
+    assert c.check_error() == 0
+    table = c.table.tolist()
+    for part, x in (("k", k), ("v", v)):
+        want_n, want_s = before[part][0].cpu().numpy(), before[part][1].float().cpu().numpy()
+        n, s, m = _quantise(x.float().cpu().numpy())
+        at = 0
+        for b in range(B):
+            for i in range(news[b]):
+                p = olds[b] + i
+                blk = table[b][p // bs]
+                want_n[blk, :, p % bs] = n[at]
+                want_s[blk, :, p % bs, 0], want_s[blk, :, p % bs, 1] = s[at], m[at]
+                at += 1
+        got_n, got_s = _codes(c, part)
+        assert np.array_equal(got_s.float().cpu().numpy(), want_s)
+        # (x - m) / s in fp32 on both sides
+        assert np.array_equal(got_n.cpu().numpy(), want_n)
+    c.close()
+
+
+def test_append_odd_values():
+    abi = _abi()
+    c = _kv4(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=2, max_blocks=2)
+    cu, _, _ = c.resize(_i32([8]), 8)
+    k = torch.zeros(8, 1, 128, device="cuda")
+    k[0] = 3.25                                    # all equal: s = 0
+    k[1, 0, 5] = float("inf")
+    k[2, 0, 6] = float("nan")
+    k[2, 0, 7] = 2.0
+    k[3, 0, :] = torch.linspace(-1, 1, 128)
+    k[4, 0, 0], k[4, 0, 1] = 3e38, -3e38
+    k[5, 0, 0] = 2.0 ** -130                       # differences that bf16 holds as subnormals only
+    k[6, 0, 0] = 2.0 ** -133 * 3
+    k[7, 0, 0] = -0.0
+    k = k.bfloat16()
+    c.append(k, k, cu)
+    assert c.check_error() == abi.SRH_ERR_RANGE and c.check_error() == 0
+    n, s, m = _quantise(k.float().cpu().numpy())
+    codes, sm = _codes(c, "k")
+    blk = int(c.table[0, 0])
+    assert np.array_equal(codes[blk, :, :8].transpose(0, 1).cpu().numpy(), n)
+    assert np.array_equal(sm[blk, :, :8, 0].t().float().cpu().numpy(), s)
+    assert np.array_equal(sm[blk, :, :8, 1].t().float().cpu().numpy(), m)
+    out, _ = c.read(_i32([0]), cu, 8)
+    assert bool(torch.isfinite(out).all()) and float(out[0].min()) == float(out[0].max()) == 3.25
+    c.close()
+
+
+@pytest.mark.parametrize("why", ["down", "rows", "short", "long", "negative", "entry"])
+def test_append_leaves_out_what_is_out_of_bounds(why):
+    abi = _abi()
+    g = _gen(11)
+    c = _kv4(batch=3, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=12, max_blocks=4)
+    _filled(c, g, [20, 40, 30])
+    cu, rows = [0, 4, 9, 12], 12
+    touched = {0, 1, 2}
+    if why == "down":
+        cu, touched = [0, 9, 4, 12], set()
+    if why == "rows":
+        cu, touched = [0, 4, 9, 13], {0, 1}
+    if why == "short":
+        c.len[1] = 4
+        touched = {0, 2}
+    if why == "long":
+        c.len[1] = 65
+        touched = {0, 2}
+    if why == "negative":
+        c.len[1] = -1
+        touched = {0, 2}
+    if why == "entry":
+        c.table[1, 2] = 12
+        touched = {0, 1, 2}
+    k = _bf16(g, rows, 2, 128)
+    before = [t.clone() for t in (*_codes(c, "k"), *_codes(c, "v"))]
+    c.append(k, k, _i32(cu))
+    assert c.check_error() == abi.SRH_ERR_BOUNDS
+    after = (*_codes(c, "k"), *_codes(c, "v"))
+    n, s, m = _quantise(k.float().cpu().numpy())
+    lens, table = c.len.tolist(), c.table.tolist()
+    want = [t.clone() for t in before]
+    for b in sorted(touched):
+        nq = cu[b + 1] - cu[b]
+        for i in range(nq):
+            p = lens[b] - nq + i
+            blk = table[b][p // 16]
+            if not 0 <= blk < 12:
+                continue
+            for j in (0, 2):
+                want[j][blk, :, p % 16] = torch.from_numpy(n[cu[b] + i]).cuda()
+                want[j + 1][blk, :, p % 16] = torch.from_numpy(np.stack((s[cu[b] + i], m[cu[b] + i]), -1)).cuda().bfloat16()
+    for x, y in zip(after, want):
+        assert torch.equal(x, y)
+    c.close()
+
+
+# ---------------------------------------------------------------------------------------------- read
+@pytest.mark.parametrize("bits,bs,Hk,D,shared", [(4, 16, 8, 128, False), (4, 128, 1, 256, False), (4, 32, 3, 128, False),
+                                                 (8, 16, 2, 128, False), (8, 64, 1, 512, True), (8, 32, 4, 256, False),
+                                                 (8, 16, 1, 512, False), (8, 128, 2, 128, True)])
+def test_read_is_exact(bits, bs, Hk, D, shared):
+    g = _gen(bits * bs + D)
+    lens, starts, counts = [70, 1, 0, 300, 33], [3, 0, 0, 0, 32], [64, 1, 0, 300, 1]
+    kw = dict(batch=6, n_kv_heads=Hk, head_dim=D, block_tokens=bs, n_blocks=60, max_blocks=30)
+    if bits == 4:
+        c = _kv4(**kw)
+        _filled(c, g, lens)
+    else:
+        c = _kv8(shared_kv=shared, **kw)
+        c.resize(_i32(lens))
+        for codes, scale in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale)):
+            x = (100 * torch.randn(codes[0].shape, generator=g, device="cuda")).clamp(-448, 448)
+            codes[0].copy_(x.to(FP8).view(torch.uint8))
+            scale[0].copy_(0.1 + torch.rand(scale[0].shape, generator=g, device="cuda"))
+    T = sum(counts)
+    outs = torch.full((T + 3, 2, Hk, D + 0), 7.0, device="cuda", dtype=torch.bfloat16)    # K and V rows side by side
+    k_out, v_out = outs[:, 0], outs[:, 1]
+    got = c.read(_i32(starts), _cu(counts), T + 3, k_out=k_out, v_out=None if shared else v_out)
+    assert c.check_error() == 0 and got[0] is k_out
+    for part, out in (("k", k_out),) if shared else (("k", k_out), ("v", v_out)):
+        at = 0
+        for b, n in enumerate(counts):
+            if bits == 4:
+                want = _values(c, part, b, lens[b])[starts[b]:starts[b] + n].float().bfloat16()
+            else:
+                codes, scale = (c.k_codes[0], c.k_scale[0]) if part == "k" else (c.v_codes[0], c.v_scale[0])
+                blk = c.table[b, :-(-lens[b] // bs)].long()
+                x = codes[blk].view(FP8).float() * scale[blk][..., None, None]
+                want = x.transpose(1, 2).reshape(-1, Hk, D)[starts[b]:starts[b] + n].bfloat16()
+            assert torch.equal(out[at:at + n], want), (part, b)
+            at += n
+        assert bool((out[T:] == 7).all())
+    if shared:
+        assert bool((v_out == 7).all()) and got[1] is None
+    else:
+        k2, v2 = c.read(_i32(starts), _cu(counts), T)
+        assert torch.equal(k2, k_out[:T]) and torch.equal(v2, v_out[:T])
+    c.close()
+
+
+@pytest.mark.parametrize("why", ["down", "behind", "before", "rows", "long", "entry"])
+def test_read_leaves_out_what_is_out_of_bounds(why):
+    abi = _abi()
+    g = _gen(5)
+    c = _kv4(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=12, max_blocks=4)
+    _filled(c, g, [20, 40])
+    start, cu, left = [0, 10], [0, 8, 20], set()
+    if why == "down":
+        cu, left = [8, 0, 20], set(range(20))
+    if why == "behind":
+        start, left = [14, 10], {6, 7}
+    if why == "before":
+        start, left = [0, -3], {8, 9, 10}
+    if why == "rows":
+        cu = [0, 8, 25]
+    if why == "long":
+        c.len[1] = 65
+        left = set(range(8, 20))
+    if why == "entry":
+        c.table[1, 1] = -1
+        left = set(range(14, 20))
+    full = _values(c, "k", 0, 20), _values(c, "k", 1, 40)
+    k, v = (torch.full((20, 2, 128), 7.0, device="cuda", dtype=torch.bfloat16) for _ in "kv")
+    c.read(_i32(start), _i32(cu), 20, k_out=k, v_out=v)
+    assert c.check_error() == abi.SRH_ERR_BOUNDS
+    for r in range(20):
+        b = int(r >= cu[1])
+        if r in left:
+            assert bool((k[r] == 7).all()) and bool((v[r] == 7).all()), r
+        else:
+            assert torch.equal(k[r], full[b][start[b] + r - cu[b]].float().bfloat16()), r
+    c.close()
+
+
+# ---------------------------------------------------------------------------------------------- attend
+def _attend_64(c, q, cu, scale, window=0, layer=0):
+    """(outputs, tolerance) in fp64. A row that sees nothing gives zeros.
+
+    The tolerance: bf16's rounding of the output, 2^-8 of it; the fp16 rounding of a weight times V's scale, at most 2^-11 of
+    it, on codes at most 8 from the middle; scores in fp32: a sum of 2 D products of up to |q| (|m| + 15 s) each, of which
+    each addition rounds by 2^-24, moves a weight by 2^-24 2 D sum|q| max|K| scale at the very worst (an eighth of that is
+    allowed: errors of a sum add up as a walk), and exponentials within 2^-21."""
+    cus, lens = cu.tolist(), c.len.tolist()
+    G = q.shape[1] // c.Hk
+    out, tol = torch.zeros(q.shape, dtype=torch.float64, device="cuda"), torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    for b in range(len(cus) - 1):
+        n, nq = lens[b], cus[b + 1] - cus[b]
+        if nq == 0:
+            continue
+        k, v = _values(c, "k", b, n, layer), _values(c, "v", b, n, layer)
+        sm = c.v_scale[layer][c.table[b, :-(-n // c.bs)].long()].double().transpose(1, 2).reshape(-1, c.Hk, 2)[:n]
+        pos = torch.arange(n - nq, n, device="cuda")[:, None]
+        t = torch.arange(n, device="cuda")[None]
+        see = (t <= pos) & ((t > pos - window) if window else (t >= 0))
+        x = q[cus[b]:cus[b + 1]].double().view(nq, c.Hk, G, c.D)
+        a = torch.einsum("ihgd,thd->hgit", x, k) * scale
+        a = a.masked_fill(~see, float("-inf"))
+        w = torch.softmax(a, -1)
+        w = torch.where(see.any(-1)[..., None], w, 0.0)
+        o = torch.einsum("hgit,thd->ihgd", w, v)
+        out[cus[b]:cus[b + 1]] = o.reshape(nq, -1, c.D)
+        if n == 0:
+            continue
+        rounding = 2.0 ** -11 * 8 * torch.einsum("hgit,th->ihg", w, sm[..., 0])[..., None]
+        reach = x.abs().sum(-1, keepdim=True) * k.abs().amax((0, 2))[None, :, None, None] * scale
+        scores = (2.0 ** -24 * c.D / 4 * reach / c.D ** 0.5 + 2.0 ** -20) * torch.einsum("hgit,thd->ihgd", w, v.abs()) * 2
+        tol[cus[b]:cus[b + 1]] = (2.0 ** -8 * o.abs() + rounding + scores).reshape(nq, -1, c.D)
+    return out, tol + 1e-30
+
+
+def _check(c, q, cu, out, scale, window=0, layer=0):
+    want, tol = _attend_64(c, q, cu, scale, window, layer)
+    rows = slice(int(cu[0]), int(cu[-1]))
+    err = (out.double() - want).abs()[rows]
+    assert bool(torch.isfinite(out[rows]).all())
+    assert bool((err <= tol[rows]).all()), float((err / tol[rows]).max())
+
+
+@pytest.mark.parametrize("Hk,G,D,bs,lens,news,window", [
+    (1, 1, 128, 16, [1], [1], 0),
+    (8, 4, 128, 64, [2000], [1], 0),
+    (2, 8, 128, 16, [300, 17, 1000, 128, 129], [1] * 5, 0),
+    (1, 5, 128, 32, [77, 500], [3, 4], 0),
+    (3, 7, 128, 128, [400, 90, 260], [5, 1, 60], 0),
+    (2, 16, 128, 16, [700, 64, 3], [1, 1, 1], 0),
+    (1, 32, 128, 64, [900], [2], 0),
+    (4, 4, 256, 16, [333, 40, 1200], [1, 2, 1], 0),
+    (1, 12, 256, 128, [600, 129], [1, 7], 0),
+    (2, 1, 256, 32, [64, 63, 65], [64, 63, 65], 0),
+    (2, 4, 128, 16, [300, 130], [300, 130], 0),
+    (1, 3, 128, 64, [1500, 200], [1, 40], 100),
+    (2, 2, 128, 16, [1000], [200], 1),
+    (1, 8, 128, 16, [5000, 31], [1, 9], 4096),
+    (2, 4, 256, 128, [3000, 260], [1, 30], 257),
+    (1, 6, 128, 16, [20000], [1], 0),
+    (1, 2, 128, 32, [90] * 60, [1] * 60, 0),
+])
+def test_attend(Hk, G, D, bs, lens, news, window):
+    g = _gen(Hk * 1000 + G * 100 + bs)
+    B = len(lens)
+    c = _kv4(batch=B, n_kv_heads=Hk, head_dim=D, block_tokens=bs, n_blocks=sum(-(-n // bs) for n in lens) + 3,
+             max_blocks=max(-(-n // bs) for n in lens))
+    _filled(c, g, lens)
+    T = sum(news)
+    big = _bf16(g, T, 2 * Hk * G * D) * 1.5
+    q = big[:, Hk * G * D:].view(T, Hk * G, D)
+    out = torch.full((T + 2, Hk * G + 1, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    view = out[:T, :Hk * G]
+    cu = _cu(news)
+    assert c.attend(q, cu, scale=D ** -0.5, window=window, out=view) is view
+    assert c.check_error() == 0
+    _check(c, q, cu, view, D ** -0.5, window)
+    assert bool((out[T:] == 9).all()) and bool((out[:, -1] == 9).all())
+    again = c.attend(q, cu, scale=D ** -0.5, window=window)
+    assert torch.equal(again, view)                # the same sums in the same order
+    c.close()
+
+
+def test_attend_many_requests_of_all_kinds():
+    rng = np.random.default_rng(3)
+    B = 700
+    lens = rng.integers(0, 200, B)
+    news = np.minimum(rng.integers(0, 4, B), lens)
+    lens[5], news[5] = 3000, 1
+    lens[600], news[600] = 700, 90
+    g = _gen(3)
+    c = _kv4(batch=B, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=int((-(-lens // 16)).sum()), max_blocks=200)
+    _filled(c, g, lens.tolist())
+    q = _bf16(g, int(news.sum()), 6, 128)
+    cu = _cu(news)
+    out = c.attend(q, cu, scale=0.1)
+    assert c.check_error() == 0
+    _check(c, q, cu, out, 0.1)
+    c.close()
+
+
+def test_attend_rows_that_see_nothing_give_zeros():
+    """More rows than tokens: the first ones lie before the request."""
+    g = _gen(8)
+    c = _kv4(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=8, max_blocks=4)
+    _filled(c, g, [3, 0])
+    q = _bf16(g, 9, 4, 128)
+    out = c.attend(q, _i32([0, 5, 9]), scale=0.1)
+    assert bool((out[:2] == 0).all()) and bool((out[5:] == 0).all()) and bool((out[2:5] != 0).any())
+    c.close()
+
+
+@pytest.mark.parametrize("why", ["down", "long", "entry", "rows"])
+def test_attend_leaves_out_what_is_out_of_bounds(why):
+    abi = _abi()
+    g = _gen(4)
+    c = _kv4(batch=3, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=60, max_blocks=20)
+    _filled(c, g, [200, 150, 90])
+    q = _bf16(g, 9, 8, 128)
+    cu = [0, 3, 5, 9]
+    out = torch.full((9, 8, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    if why == "down":
+        c.attend(q, _i32([0, 5, 3, 9]), scale=0.1, out=out)
+        assert c.check_error() == abi.SRH_ERR_BOUNDS and bool((out == 9).all())
+    elif why == "rows":
+        c.attend(q, _i32([0, 3, 5, 12]), scale=0.1, out=out)
+        assert c.check_error() == abi.SRH_ERR_BOUNDS
+        _check(c, q[:5], _i32([0, 3, 5]), out[:5], 0.1)
+    elif why == "long":
+        c.len[1] = 321
+        c.attend(q, _i32(cu), scale=0.1, out=out)
+        assert c.check_error() == abi.SRH_ERR_BOUNDS and bool((out[3:5] == 9).all())
+        c.len[1] = 0
+        _check(c, q[:3], _i32([0, 3]), out[:3], 0.1)
+    else:
+        c.table[1, 2] = 60                         # tokens 32 .. 47 of request 1 are absent
+        c.attend(q, _i32(cu), scale=0.1, out=out)
+        assert c.check_error() == abi.SRH_ERR_BOUNDS
+        c.table[1, 2] = 0
+        k, v = _values(c, "k", 1, 150), _values(c, "v", 1, 150)
+        keep = torch.tensor([t for t in range(149) if not 32 <= t < 48], device="cuda")
+        x = q[3].double().view(2, 4, 128)
+        w = torch.softmax(torch.einsum("hgd,thd->hgt", x, k[keep]) * 0.1, -1)
+        want = torch.einsum("hgt,thd->hgd", w, v[keep]).reshape(8, 128)
+        assert float((out[3].double() - want).abs().max()) < 2.0 ** -8 * float(want.abs().max()) + 0.01
+    c.close()
+
+
+def test_attend_whatever_lies_behind_a_request():
+    """Scales of NaN and infinity behind the length, in its last block and others, do not show."""
+    g = _gen(21)
+    c = _kv4(batch=2, n_kv_heads=2, head_dim=128, block_tokens=64, n_blocks=12, max_blocks=6)
+    lens = [133, 65]
+    _filled(c, g, lens)
+    q = _bf16(g, 3, 8, 128)
+    cu = _i32([0, 1, 3])
+    want = c.attend(q, cu, scale=0.1)
+    for scale in (c.k_scale[0], c.v_scale[0]):
+        kept = torch.zeros(12, 64, dtype=torch.bool, device="cuda")
+        for b, n in enumerate(lens):
+            for t in range(n):
+                kept[int(c.table[b, t // 64]), t % 64] = True
+        bad = ~kept[:, None, :, None]
+        odd = torch.tensor([float("nan"), float("inf")], device="cuda").bfloat16()
+        scale.copy_(torch.where(bad, odd, scale))
+    assert torch.equal(c.attend(q, cu, scale=0.1), want)
+    assert c.check_error() == 0
+    c.close()
+
+
+@pytest.mark.parametrize("offset", [0.0, 3.0])
+def test_attend_equal_weights(offset):
+    """Where all tokens weigh the same, every weight rounds the same way: the mean of many values that nearly cancel must not
+    show it. Per output: bf16's rounding, 2^-11 of the mean around V's middle, fp32 sums of 12,000 values of up to 7."""
+    g = _gen(77)
+    n = 12000
+    c = _kv4(batch=1, n_kv_heads=1, head_dim=128, block_tokens=32, n_blocks=400, max_blocks=400)
+    _filled(c, g, [n], spread=0, mean=offset)
+    c.v_scale[0][..., 0] = 0.3
+    c.v_scale[0][..., 1] = offset - 2.25
+    q = torch.zeros(1, 4, 128, device="cuda", dtype=torch.bfloat16)
+    out = c.attend(q, _i32([0, 1]), scale=0.1).double()
+    v = _values(c, "v", 0, n)[:, 0]
+    want = v.mean(0)
+    middle = float((c.v_scale[0][0, 0, 0, 1].double() + 8 * c.v_scale[0][0, 0, 0, 0].double()))
+    tol = 2.0 ** -8 * want.abs() + 2.0 ** -11 * (want - middle).abs() + 7 * 2.0 ** -20
+    assert bool(((out[0] - want).abs() <= tol).all())
+    c.close()
+
+
+@pytest.mark.parametrize("share", [0.5, 0.999])
+def test_attend_long_tail_behind_one_weight(share):
+    """One token with `share` of the weight in front of 30,000 equal ones that hold the rest between them."""
+    g = _gen(78)
+    n = 30001
+    c = _kv4(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=2000, max_blocks=2000)
+    _filled(c, g, [n], spread=0)
+    # K: one dim decides; all others hold 0
+    c.k_codes[0].zero_()
+    c.k_scale[0][..., 0] = 1.0
+    c.k_scale[0][..., 1] = 0.0
+    first = int(c.table[0, 0])
+    c.k_codes[0][first, 0, 0, 0] = 8               # token 0, dim 0
+    lead = math.log(share / (1 - share) * (n - 1))
+    q = torch.zeros(1, 1, 128, device="cuda", dtype=torch.bfloat16)
+    q[0, 0, 0] = lead / 8
+    out = c.attend(q, _i32([0, 1]), scale=1.0)
+    _check(c, q, _i32([0, 1]), out, 1.0)
+    v = _values(c, "v", 0, n)[:, 0]
+    assert float((v[1:].mean(0)).abs().max()) > 0.01
+    c.close()
+
+
+def test_attend_wide_scores_and_scales():
+    """Scores over hundreds, rows of all sizes, constant rows (scale 0) of V, queries of 2^-40 to 2^40."""
+    g = _gen(79)
+    c = _kv4(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=80, max_blocks=40)
+    _filled(c, g, [600, 333], spread=9)
+    c.v_scale[0][:, :, ::3, 0] = 0.0
+    q = _bf16(g, 4, 8, 128)
+    for k in (-40, 0, 6, 40):
+        x = (q.float() * 2.0 ** k).bfloat16()
+        scale = 0.1 * 2.0 ** -k * (1 if k != 6 else 32)
+        cu = _i32([0, 1, 4])
+        out = c.attend(x, cu, scale=scale)
+        _check(c, x, cu, out, scale)
+    c.close()
+
+
+def test_attend_a_row_that_is_not_finite_is_nan_alone():
+    g = _gen(80)
+    c = _kv4(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=40, max_blocks=40)
+    _filled(c, g, [500])
+    q = _bf16(g, 2, 4, 128)
+    q[0, 1, 7] = float("inf")
+    q[1, 2, 3] = float("nan")
+    out = c.attend(q, _i32([0, 2]), scale=0.1)
+    nan = torch.isnan(out).all(-1)
+    assert nan.tolist() == [[False, True, False, False], [False, False, True, False]]
+    q[0, 1, 7], q[1, 2, 3] = 0, 0
+    want = c.attend(q, _i32([0, 2]), scale=0.1)
+    assert torch.equal(out[~nan], want[~nan])
+    c.close()
+
+
+def test_codes_past_32_bit_offsets():
+    """Blocks 1.5 GB apart: offsets of codes pass 32 bits."""
+    g = _gen(81)
+    nb, stride = 5, 3 << 29
+    codes = [torch.zeros(nb * stride, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    views = [t.as_strided((nb, 2, 16, 64), (stride, 16 * 64, 64, 1)) for t in codes]
+    c = _kv4(batch=1, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=nb, max_blocks=nb,
+             buffers=dict(k_codes=views[0], v_codes=views[1]))
+    cu, _, _ = c.resize(_i32([75]), 75)
+    k, v = _bf16(g, 75, 2, 128), _bf16(g, 75, 2, 128)
+    c.append(k, v, cu)
+    kb, vb = c.read(_i32([0]), cu, 75)
+    assert float((kb.double() - k.double()).abs().max()) < 0.5 and float((vb.double() - v.double()).abs().max()) < 0.5
+    q = _bf16(g, 2, 4, 128)
+    out = c.attend(q, _i32([0, 2]), scale=0.1)
+    _check(c, q, _i32([0, 2]), out, 0.1)
+    c.close()
+
+
+def test_graph_follows_new_lengths():
+    g = _gen(82)
+    lens = [300, 50, 1000]
+    c = _kv4(batch=3, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=150, max_blocks=80)
+    c.resize(_i32(lens))
+    for codes, scale in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale)):
+        codes[0].copy_(torch.randint(0, 256, codes[0].shape, generator=g, device="cuda", dtype=torch.uint8))
+        scale[0][..., 0], scale[0][..., 1] = 0.3, -2.0
+    new, start = _i32(lens), _i32([0, 0, 0])
+    q, k, v = _bf16(g, 3, 8, 128), _bf16(g, 3, 2, 128), _bf16(g, 3, 2, 128)
+    out, kb, vb = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    cu, pos, slot = torch.empty(4, dtype=torch.int32, device="cuda"), _i32([0] * 3), torch.zeros(3, dtype=torch.int64, device="cuda")
+
+    def step():
+        start.copy_(c.len[:3])
+        c.resize(new, 3, out=(cu, pos, slot))
+        c.append(k, v, cu)
+        c.read(start, cu, 3, k_out=kb, v_out=vb)
+        c.attend(q, cu, scale=0.1, out=out)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        new += 1
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for add in ([1, 1, 1], [1, 0, 1], [0, 1, 0], [1, 1, 1]):
+        new += _i32(add)
+        k.copy_(_bf16(g, 3, 2, 128))
+        graph.replay()
+        assert c.check_error() == 0
+        t = sum(add)
+        assert int(cu[-1]) == t
+        _check(c, q, cu, out, 0.1)
+        assert float((kb[:t].double() - k[:t].double()).abs().max()) < 0.3
+    c.close()
+
+
+def test_calls_on_a_stream_of_their_own():
+    g = _gen(83)
+    c = _kv4(batch=1, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=150, max_blocks=150)
+    s = torch.cuda.Stream()
+    new = _i32([2000])
+    k, v, q = _bf16(g, 2000, 2, 128), _bf16(g, 2000, 2, 128), _bf16(g, 1, 8, 128)
+    torch.cuda.synchronize()
+    cu, _, _ = c.resize(new, 2000, stream=s)
+    c.append(k, v, cu, stream=s)
+    with torch.cuda.stream(s):
+        one, zero = _i32([0, 1]), _i32([0])
+    kb, vb = c.read(zero, cu, 2000, stream=s)
+    out = c.attend(q, one, scale=0.1, stream=s.cuda_stream)
+    s.synchronize()
+    _check(c, q, one, out, 0.1)
+    assert torch.equal(kb, _values(c, "k", 0, 2000).float().bfloat16()) and torch.equal(vb, _values(c, "v", 0, 2000).float().bfloat16())
+    c.close()
+
+
+def test_layers_of_both_widths_on_one_table():
+    """A 4-bit and an 8-bit pool on one handle's tables through the C entry points."""
+    abi = _abi()
+    g = _gen(84)
+    c4 = _kv4(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=20, max_blocks=10)
+    c8 = _kv8(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=20, max_blocks=10,
+              buffers=dict(table=c4.table, len=c4.len, free=c4.free, n_free=c4.n_free))
+    cu, _, _ = c4.resize(_i32([60, 100]), 160)
+    k, v = _bf16(g, 160, 2, 128), _bf16(g, 160, 2, 128)
+    c4.append(k, v, cu)
+    c8.append(k, v, cu)
+    q = _bf16(g, 2, 8, 128)
+    a, b = c4.attend(q, _i32([0, 1, 2]), scale=0.1), c8.attend(q, _i32([0, 1, 2]), scale=0.1)
+    _check(c4, q, _i32([0, 1, 2]), a, 0.1)
+    assert float((a.double() - b.double()).abs().max()) < 0.2
+    # the 8-bit pool through the 4-bit cache's handle
+    lib = abi.load()
+    k2 = torch.empty_like(k)
+    v2 = torch.empty_like(v)
+    start = _i32([0, 0])
+    assert lib.kv8_read(c4.cache, c8._pool[0], c4.table.data_ptr(), c4.len.data_ptr(), start.data_ptr(), cu.data_ptr(), 2,
+                        k2.data_ptr(), 256, v2.data_ptr(), 256, 160, torch.cuda.current_stream().cuda_stream) == 0
+    want = c8.read(start, cu, 160)
+    assert torch.equal(k2, want[0]) and torch.equal(v2, want[1])
+    c4.close()
+    c8.close()
+
+
+def test_refusals():
+    abi = _abi()
+    c = _kv4(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=20, max_blocks=10, layers=2)
+    g = _gen(1)
+    q, k = _bf16(g, 4, 8, 128), _bf16(g, 4, 2, 128)
+    cu, start = _i32([0, 2, 4]), _i32([0, 0])
+    for bad in (lambda: c.append(k, None, cu), lambda: c.append(k[:, :1], k, cu), lambda: c.append(k.float(), k, cu),
+                lambda: c.append(k, k[:3], cu), lambda: c.attend(q[:, :, :64], cu, scale=1.0),
+                lambda: c.attend(q, cu.long(), scale=1.0), lambda: c.read(start[:1], cu, 4), lambda: c.read(start, cu, -1),
+                lambda: c.read(start, cu, 4, k_out=k[:3]), lambda: c.read(start, cu, 4, v_out=k.float()),
+                lambda: c.read(start.cpu(), cu, 4)):
+        with pytest.raises(ValueError):
+            bad()
+    odd = torch.zeros(4, 7, 128, device="cuda", dtype=torch.bfloat16)
+    for bad in (lambda: c.attend(odd, cu, scale=1.0), lambda: c.attend(q, cu, scale=float("nan")),
+                lambda: c.attend(q, cu, scale=1.0, window=-1), lambda: c.attend(q, cu, scale=1.0, out=q),
+                lambda: c.read(start, cu, 4, k_out=k, v_out=k)):
+        with pytest.raises(abi.SrhError) as e:
+            bad()
+        assert e.value.code == abi.SRH_ERR_INVALID
+    lib = abi.load()
+    pool = abi.Kv4Pool(c.k_codes[0].data_ptr(), c.k_scale[0].data_ptr(), c.v_codes[0].data_ptr(), c.v_scale[0].data_ptr(), 0)
+
+    def append(p, handle=c.cache):
+        return lib.kv4_append(handle, p, c.table.data_ptr(), c.len.data_ptr(), cu.data_ptr(), 2, k.data_ptr(), 256,
+                              k.data_ptr(), 256, 4, 0)
+    for field, value in (("k_codes", 0), ("v_scale", 0), ("k_codes", pool.k_codes + 8), ("v_scale", pool.v_scale + 4),
+                         ("block_stride", 2 * 16 * 64 - 16), ("block_stride", 2 * 16 * 64 + 8), ("block_stride", 1 << 40)):
+        p = abi.Kv4Pool(*(getattr(pool, f) for f, _ in abi.Kv4Pool._fields_))
+        setattr(p, field, value)
+        assert append(p) == abi.SRH_ERR_INVALID, field
+    assert append(None) == abi.SRH_ERR_INVALID
+    shared = _kv8(batch=2, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=20, max_blocks=10, shared_kv=True)
+    assert append(pool, shared.cache) == abi.SRH_ERR_INVALID
+    wide = _kv8(batch=2, n_kv_heads=2, head_dim=512, block_tokens=16, n_blocks=20, max_blocks=10)
+    assert append(pool, wide.cache) == abi.SRH_ERR_INVALID
+    with pytest.raises(ValueError):
+        _kv4(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=4, max_blocks=4,
+             buffers=dict(k_codes=torch.zeros(4, 1, 16, 128, dtype=torch.uint8, device="cuda")))
+    with pytest.raises(ValueError):
+        _kv4(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=4, max_blocks=4,
+             buffers=dict(k_scale=torch.zeros(4, 1, dtype=torch.float32, device="cuda")))
+    assert c.check_error() == 0
+    for x in (c, shared, wide):
+        x.close()
+
+
+# ---------------------------------------------------------------------------------------------- rotation by several axes
+def _axes_64(x, w, pos, axis, freq, rot, off, style, eps):
+    x = x.double()
+    y = x / torch.sqrt(x.pow(2).mean(-1, keepdim=True) + eps) * w.double()
+    angle = pos.double()[axis.long()].t() * freq                # [tokens, pairs]
+    cos, sin = torch.cos(angle)[:, None], torch.sin(angle)[:, None]
+    i = torch.arange(rot // 2, device="cuda")
+    a, b = (off + 2 * i, off + 2 * i + 1) if style == "pairs" else (off + i, off + rot // 2 + i)
+    out = y.clone()
+    out[..., a] = y[..., a] * cos - y[..., b] * sin
+    out[..., b] = y[..., a] * sin + y[..., b] * cos
+    size = y.abs()
+    size[..., a] = size[..., b] = torch.sqrt(y[..., a] ** 2 + y[..., b] ** 2)
+    return out, size
+
+
+@pytest.mark.parametrize("T,H,Hk,D,rot,off,style,axes", [
+    (1, 4, 1, 128, 128, 0, "halves", 3), (77, 6, 2, 96, 32, 64, "pairs", 2), (300, 3, 3, 64, 64, 0, "halves", 8),
+    (50, 2, 1, 256, 256, 0, "pairs", 3), (33, 5, 1, 512, 64, 448, "halves", 4), (9, 2, 2, 512, 512, 0, "pairs", 1),
+    (2000, 8, 2, 128, 128, 0, "pairs", 3)])
+def test_rotation_by_axes(T, H, Hk, D, rot, off, style, axes):
+    """bf16's rounding (2^-8 of the result), the norm and the factors in fp32, cos and sin within 2^-22 and the angle's 2^-26
+    of a turn, of the pair's length."""
+    g = _gen(T + D)
+    c = _kv4(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=1, max_blocks=1)
+    q, k = _bf16(g, T, H, D), _bf16(g, T, Hk, D)
+    wq, wk = (1 + 0.1 * torch.randn(D, generator=g, device="cuda") for _ in "qk")
+    big = torch.randint(-5000, 100000, (axes, T + 5), generator=g, device="cuda", dtype=torch.int32)
+    pos = big[:, 2:T + 2]                                        # rows apart
+    axis = torch.randint(0, axes, (rot // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    freq = 10000.0 ** (-torch.arange(rot // 2, device="cuda", dtype=torch.float64) / (rot // 2))
+    qo, ko = c.norm_rope(q, k, pos=pos, axis=axis, inv_freq=freq, rot_dim=rot, rot_off=off, style=style, q_weight=wq, k_weight=wk)
+    assert c.check_error() == 0
+    for x, w, out in ((q, wq, qo), (k, wk, ko)):
+        want, size = _axes_64(x, w, pos, axis, freq, rot, off, style, 1e-6)
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -19 * size + 1e-30
+        assert bool(((out.double() - want).abs() <= tol).all())
+    # each axis the same positions: what one axis gives, bit for bit
+    same = pos[:1].expand(axes, T).contiguous()
+    q1, k1 = c.norm_rope(q, k, pos=same, axis=axis, inv_freq=freq, rot_dim=rot, rot_off=off, style=style, q_weight=wq, k_weight=wk)
+    q2, k2 = c.norm_rope(q, k, pos=same[0].contiguous(), inv_freq=freq, rot_dim=rot, rot_off=off, style=style, q_weight=wq, k_weight=wk)
+    assert torch.equal(q1, q2) and torch.equal(k1, k2)
+    # in place, and to slots
+    slot = torch.randperm(T + 3, generator=g, device="cuda")[:T]
+    slot[0] = -1
+    rows = torch.full((T + 3, Hk, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    x = q.clone()
+    c.norm_rope(x, k, pos=pos, axis=axis, inv_freq=freq, rot_dim=rot, rot_off=off, style=style, q_weight=wq, k_weight=wk, q_out=x,
+                k_out=rows, k_slot=slot)
+    assert torch.equal(x, qo) and torch.equal(rows[slot[1:]], ko[1:])
+    c.close()
+
+
+def test_rotation_by_axes_refusals_and_an_axis_that_is_none():
+    abi = _abi()
+    g = _gen(2)
+    c = _kv4(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=1, max_blocks=1)
+    q = _bf16(g, 5, 2, 64)
+    pos = torch.randint(0, 100, (3, 5), generator=g, device="cuda", dtype=torch.int32)
+    freq = torch.ones(32, dtype=torch.float64, device="cuda")
+    axis = torch.zeros(32, dtype=torch.uint8, device="cuda")
+    axis[7] = 3
+    out, _ = c.norm_rope(q, pos=pos, axis=axis, inv_freq=freq, rot_dim=64, style="pairs")
+    assert c.check_error() == abi.SRH_ERR_BOUNDS
+    still, _ = c.norm_rope(q)
+    turned, _ = c.norm_rope(q, pos=pos[0].contiguous(), inv_freq=freq, rot_dim=64, style="pairs")
+    turned[..., 14:16] = still[..., 14:16]
+    assert torch.equal(out, turned)
+    for kw in (dict(pos=pos, axis=axis.int()), dict(pos=pos, axis=axis[:31]), dict(pos=pos[0].contiguous(), axis=axis),
+               dict(pos=pos.long(), axis=axis), dict(pos=pos.repeat(3, 1), axis=axis), dict(pos=pos[:, :4], axis=axis),
+               dict(pos=pos.t().contiguous().t(), axis=axis), dict(pos=pos[:1].expand(3, 5), axis=axis)):
+        with pytest.raises(ValueError):
+            c.norm_rope(q, inv_freq=freq, rot_dim=64, style="pairs", **kw)
+    assert c.check_error() == 0
+    c.close()
+
+
+# ---------------------------------------------------------------------------------------------- all of them
+def test_serving_loop():
+    """Prompts of text and images, decode steps, drafts that are taken back, a prefix handed on to an 8-bit cache."""
+    rng = np.random.default_rng(9)
+    g = _gen(9)
+    B, Hk, G, D, bs, layers = 5, 2, 4, 128, 16, 2
+    c = _kv4(batch=B, n_kv_heads=Hk, head_dim=D, block_tokens=bs, n_blocks=120, max_blocks=30, layers=layers)
+    freq = 10000.0 ** (-torch.arange(D // 2, device="cuda", dtype=torch.float64) / (D // 2))
+    axis = (torch.arange(D // 2, device="cuda") % 3).to(torch.uint8)
+    lens = [0] * B
+    rows = [[[] for _ in range(B)] for _ in range(layers)]      # what each request's keys and values were
+    for step in range(8):
+        if step == 0:
+            new = rng.integers(1, 200, B)
+        elif step == 4:
+            new = rng.integers(20, 60, B)
+        else:
+            new = rng.integers(0, 6, B)
+        lens = [a + int(n) for a, n in zip(lens, new)]
+        T = int(new.sum())
+        cu, p, slot = c.resize(_i32(lens), T)
+        pos = torch.stack((p, p // 7, p % 7))
+        for layer in range(layers):
+            q, k, v = _bf16(g, T, Hk * G, D), _bf16(g, T, Hk, D), _bf16(g, T, Hk, D)
+            q, k = c.norm_rope(q, k, pos=pos, axis=axis, inv_freq=freq, rot_dim=D, style="halves")
+            c.append(k, v, cu, layer=layer)
+            out = c.attend(q, cu, scale=D ** -0.5, layer=layer)
+            assert c.check_error() == 0
+            _check(c, q, cu, out, D ** -0.5, layer=layer)
+            cl = cu.tolist()
+            for b in range(B):
+                rows[layer][b] += list(zip(k[cl[b]:cl[b + 1]], v[cl[b]:cl[b + 1]]))
+        if step % 3 == 2:                                       # some drafts go back
+            keep = [max(1, n - int(rng.integers(0, 4))) for n in lens]
+            c.resize(_i32(keep))
+            for layer in range(layers):
+                for b in range(B):
+                    del rows[layer][b][keep[b]:]
+            lens = keep
+    T = sum(lens)
+    cu, start = _cu(lens), _i32([0] * B)
+    c8 = _kv8(batch=B, n_kv_heads=Hk, head_dim=D, block_tokens=64, n_blocks=60, max_blocks=10)
+    to, _, _ = c8.resize(_i32(lens), T)
+    for layer in range(layers):
+        k, v = c.read(start, cu, T, layer=layer)
+        assert c.check_error() == 0
+        for got, i in ((k, 0), (v, 1)):
+            x = torch.stack([r[i] for b in range(B) for r in rows[layer][b]]).float()
+            s = ((x.amax(-1) - x.amin(-1)) / 15)[..., None]
+            # half a step (of a scale rounded by 2^-8, so that 15 steps may end half a step off), and bf16's rounding
+            assert bool(((got.float() - x).abs() <= s * (0.5 + 16 * 2.0 ** -8) + 2.0 ** -8 * x.abs() + 1e-6).all())
+        c8.append(k, v, to)
+        k8, v8 = c8.read(start, to, T)
+        assert c8.check_error() == 0
+        for a, b in ((k, k8), (v, v8)):
+            assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -4 * float(a.abs().max())
+    c.close()
+    c8.close()
