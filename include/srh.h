@@ -592,8 +592,8 @@ typedef struct {
     float* v_scale;
 } kv8_pool;
 
-/* Makes a handle on the current device (scratch: 30, 30 or 40 MB with
- * head_dim 128, 256 or 512). Waits for the legacy stream; not during a capture.
+/* Makes a handle on the current device (scratch: 45 MB with head_dim
+ * 128 or 256, K and V apart, else 30, 30 or 40 MB with 128, 256 or 512). Waits for the legacy stream; not during a capture.
  * Errors: SRH_ERR_INVALID, SRH_ERR_NOMEM, SRH_ERR_CUDA (kv8_last_error(NULL)). */
 int kv8_create(const kv8_config* cfg, kv8_cache** out);
 

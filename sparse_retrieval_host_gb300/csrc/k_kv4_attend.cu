@@ -24,27 +24,21 @@
 // the whole range, and the same for all tokens where all weigh the same). The -8 is taken off by
 // sum p, of the rounded p, a row of ones in the second product.
 //
-// Work: a row tile is RT of the (token, head) rows that share a KV head of a request. Units are
-// (request, KV head, row tile, 128 tokens), counted on the device from the lengths and cut into
-// equal chunks, one per CTA; the CTA's warps take 16 tokens of each unit. The last CTA to arrive
-// of those that share an item adds its parts, in chunk order: results repeat bit for bit.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "kv8_internal.cuh"
+// Work: see kv4_split.cuh; a CTA's warps take 16 tokens each of a unit's 128, each with references
+// and sums of its own, and add up at the end of a segment.
+#include "kv4_split.cuh"
 
 namespace srh {
 namespace kv8 {
 namespace {
 
-constexpr int kTile = 128;               // tokens per unit
+using namespace split;
+
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr float kLow = -1e30f;           // reference of a row that has seen no token
 constexpr float kHead = 10.f;            // log2 of the weight that a new reference gives a row's maximum
 constexpr float kRoom = 15.5f;           // a row's reference moves when a weight would pass 2^15.5
 constexpr float kLeastScale = 5.421010862427522e-20f;   // 2^-64
-constexpr int kMaxUnits = 1 << 30;
 
 // DB: head_dim / 128. NT: row tiles of 8 columns.
 template <int DB_, int NT_>
@@ -56,73 +50,9 @@ struct Shape {
     static constexpr int kStatBytes = kWarps * RT * 8;         // reference and sum
 };
 
-struct Args {
-    const uint16_t* q;
-    uint16_t* out;
-    long long q_row, out_row, block_stride;
-    const int32_t* cu;
-    const int32_t* len;
-    const int32_t* table;
-    const uint8_t* kc;
-    const uint8_t* vc;
-    const uint32_t* ks;                          // (scale, minimum), bf16 each
-    const uint32_t* vs;
-    float* part_o;
-    float* part_ml;
-    int* arrived;
-    uint32_t* err;
-    int n_req, n_rows, kv_heads, group;          // group = query heads / kv_heads
-    int bs_log2, n_blocks, max_blocks;
-    float scale_log2;
-    int window;                                  // 0: none
-};
-
-struct Request {
-    int q0, nq, len;
-    int nrt;           // row tiles
-    int P;             // units of a row tile: what the longest takes
-};
-
-__device__ __forceinline__ int first_tile(const Args& a, int p_lo) {
-    return a.window ? max(0, p_lo - a.window + 1) / kTile : 0;
-}
-
-template <int RT>
-__device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
-    Request r;
-    const int c0 = a.cu[b], c1 = a.cu[b + 1], n = a.len[b], most = a.max_blocks << a.bs_log2;
-    r.q0 = min(max(c0, 0), a.n_rows);
-    r.nq = min(max(c1, r.q0), a.n_rows) - r.q0;               // (rows outside q are not there)
-    r.len = n;
-    if (c0 != r.q0 || c1 != r.q0 + r.nq) *bad = true;
-    if (n < 0 || n > most) {                                  // no such request
-        *bad = true;
-        r.nq = r.len = 0;
-    }
-    r.nrt = (r.nq * a.group + RT - 1) / RT;
-    const int all = max(1, (r.len + kTile - 1) / kTile);
-    r.P = r.nrt == 0 ? 0 : all;
-    if (r.nrt == 1) r.P = max(1, all - first_tile(a, r.len - r.nq));
-    else if (r.nrt > 1 && a.window) r.P = (int)min((long long)all, ((long long)a.window + RT / a.group + 1) / kTile + 2);
-    return r;
-}
-
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ float lg2(float x) {
     float r;
     asm("lg2.approx.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    uint32_t r;
-    memcpy(&r, &h, 4);
     return r;
 }
 // D += A B: A 16 x 16 (rows by lane / 4), B 16 x 8 (columns by lane / 4), fp16, fp32 sums.
@@ -151,45 +81,20 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     __shared__ int last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
 
-    // ------------------------------------------------------------ the units
-    bool bad = false, stop = false;
-    long long U64 = 0;
-    for (int base = 0; base < a.n_req; base += kThreads) {
-        const int b = base + tid;
-        long long mine = 0, total;
-        if (b < a.n_req) {
-            const Request r = request<RT>(a, b, &bad);
-            mine = (long long)r.nrt * r.P * a.kv_heads;
-            if (a.cu[b + 1] < a.cu[b]) stop = true;           // requests may share rows
-        }
-        const long long incl = block_scan(mine, warp_sums, &total);
-        if (b < a.n_req) first[b] = (int)(U64 + incl - mine);
-        U64 += total;
+    Chunks ch;
+    if (!count<RT, false, kThreads>(a, first, warp_sums, &ch)) {
+        pdl_wait();
+        return;
     }
-    stop = __syncthreads_or(stop) || U64 > kMaxUnits;
-    if (blockIdx.x == 0 && (bad || (stop && tid == 0))) atomicOr(a.err, kErrBounds);
-    if (stop) return;
-    const int U = (int)U64, n_grid = gridDim.x, most = (U + n_grid - 1) / n_grid;
-    const int n_cta = U ? (U + most - 1) / most : 0;          // as few as keep the largest share the same
-    const int cta = blockIdx.x;
-    if (cta >= n_cta) return;
-    const int base = U / n_cta, rem = U - base * n_cta;
-    auto chunk_of = [&](int u) { return u < rem * (base + 1) ? u / (base + 1) : rem + (u - rem * (base + 1)) / base; };
-    const int bsz = 1 << a.bs_log2;
-
-    int u = cta * base + min(cta, rem);
-    const int u1 = u + base + (cta < rem);
-    while (u < u1) {
-        // -------------------------------------------------------- the segment
-        const int b = last_not_above(first, a.n_req, u);
-        const Request r = request<RT>(a, b, &bad);
-        const int in = u - first[b], item = in / r.P, at = in - item * r.P, n = min(r.P - at, u1 - u);
-        const int h = item / r.nrt, row0 = (item - h * r.nrt) * RT, nr = min(RT, r.nq * a.group - row0);
-        const int u_item = u - at, v0 = chunk_of(u_item), parts = chunk_of(u_item + r.P - 1) - v0 + 1;
-        u += n;
-        const int p0 = r.len - r.nq;                          // position of the request's first row
+    const int cta = blockIdx.x, bsz = 1 << a.bs_log2;
+    bool bad = false;
+    int u = ch.begin(cta);
+    const int u1 = ch.begin(cta + 1);
+    Segment s;
+    while (next_segment<RT, false>(a, first, ch, cta, &u, u1, &s)) {
+        const int row0 = s.row0, nr = s.nr, h = s.h, parts = s.parts;
+        const int p0 = s.len - s.nq;                          // position of the request's first row
         const int p_lo = p0 + row0 / a.group, p_hi = p0 + (row0 + nr - 1) / a.group;
-        const int t_first = first_tile(a, p_lo);
         const int see_lo = a.window ? p_lo - a.window + 1 : 0;
 
         // queries as B fragments: lane (g, c) holds dims 32 c .. of row g, per 8 dims two k steps
@@ -200,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
         for (int t = 0; t < NT; ++t) {
             const int row = row0 + t * 8 + g, tok = row / a.group;
             const bool on = t * 8 + g < nr;
-            const uint16_t* x = a.q + (size_t)(r.q0 + (on ? tok : 0)) * a.q_row +
+            const uint16_t* x = a.q + (size_t)(s.q0 + (on ? tok : 0)) * a.q_row +
                                 (size_t)(h * a.group + (on ? row - tok * a.group : 0)) * D;
             uint4 w[DB][4];
             uint32_t m = 0;
@@ -263,10 +168,10 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             }
         }
 
-        for (int i = 0; i < n; ++i) {
-            const int t0 = (t_first + at + i) * kTile + warp * 16;
+        for (int i = 0; i < s.n; ++i) {
+            const int t0 = (s.t0 + i) * kTile + warp * 16;
             if (t0 > p_hi || t0 + 16 <= see_lo) continue;
-            const int id = __ldg(a.table + (size_t)b * a.max_blocks + (t0 >> a.bs_log2));
+            const int id = __ldg(a.table + (size_t)s.b * a.max_blocks + (t0 >> a.bs_log2));
             if (id < 0 || id >= a.n_blocks) {                 // a block that is none reads as absent
                 bad = true;
                 continue;
@@ -302,11 +207,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             }
 
             // scores
-            float s[NT][4];
+            float sc4[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[t][j] = 0.f;
+                for (int j = 0; j < 4; ++j) sc4[t][j] = 0.f;
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
                 const uint32_t w0[4] = {k[0][d].x, k[0][d].y, k[0][d].z, k[0][d].w};
@@ -315,12 +220,12 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                 for (int j = 0; j < 4; ++j) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        mma(s[t], w0[j] & 0x000f000fu, w1[j] & 0x000f000fu, w0[j] & 0x00f000f0u, w1[j] & 0x00f000f0u,
+                        mma(sc4[t], w0[j] & 0x000f000fu, w1[j] & 0x000f000fu, w0[j] & 0x00f000f0u, w1[j] & 0x00f000f0u,
                             q[t][d][4 * j], q[t][d][4 * j + 1]);
                     const uint32_t x0 = w0[j] >> 8, x1 = w1[j] >> 8;
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        mma(s[t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
+                        mma(sc4[t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
                             q[t][d][4 * j + 2], q[t][d][4 * j + 3]);
                 }
             }
@@ -328,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             float kss[2], km[2], lv[2], iv[2], cm[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bool there = t0 + g + 8 * j < r.len;     // (what lies behind the request may be anything)
+                const bool there = t0 + g + 8 * j < s.len;     // (what lies behind the request may be anything)
                 kss[j] = bf_lo(ksm[j]);
                 km[j] = bf_hi(ksm[j]);
                 const float vsc = fmaxf(bf_lo(vsm[j]), kLeastScale);
@@ -336,15 +241,15 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                 iv[j] = there ? __fdividef(1.f, vsc) : 0.f;
                 cm[j] = there ? fmaf(8.f, vsc, bf_hi(vsm[j])) : 0.f;
             }
-            const bool edge = t0 + 15 > p_lo || t0 <= p_hi - a.window;
+            const bool edge = t0 + 15 > p_lo || (a.window && t0 <= p_hi - a.window);
             float y[NT][4], top = kLow;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int col = j & 1, tk = j >> 1;
-                    float x = fmaf(s[t][j] * qf[t][col], kss[tk], fmaf(km[tk], qs[t][col], lv[tk]));
-                    if (a.window ? edge : t0 + 15 > p_lo) {
+                    float x = fmaf(sc4[t][j] * qf[t][col], kss[tk], fmaf(km[tk], qs[t][col], lv[tk]));
+                    if (edge) {
                         const int tt = t0 + g + 8 * tk, p = pos[t][col];
                         if (tt > p || (a.window && tt <= p - a.window)) x = -INFINITY;
                     }
@@ -437,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             }
         }
         __syncthreads();
-        const int slot = 2 * cta + (at == 0);                 // of a part: its chunk's last item, or its first
+        const size_t slot = slot_of(s.v0, s.part);
         // two dims of a row per thread and turn
         for (int x = tid; x < nr * (D / 2); x += kThreads) {
             const int row = x / (D / 2), d = (x - row * (D / 2)) * 2;
@@ -462,11 +367,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 const int rr = row0 + row, tok = rr / a.group;
                 const __nv_bfloat162 v = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-                *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)(r.q0 + tok) * a.out_row +
+                *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)(s.q0 + tok) * a.out_row +
                                                    (size_t)(h * a.group + rr - tok * a.group) * D + d) = v;
             } else {
-                *reinterpret_cast<float2*>(a.part_o + ((size_t)slot * RT + row) * D + d) = acc;
-                if (d == 0) reinterpret_cast<float2*>(a.part_ml)[(size_t)slot * RT + row] = make_float2(m, sum);
+                *reinterpret_cast<float2*>(a.part_o + (slot * RT + row) * D + d) = acc;
+                if (d == 0) reinterpret_cast<float2*>(a.part_ml)[slot * RT + row] = make_float2(m, sum);
             }
         }
         if (parts > 1) {
@@ -474,49 +379,19 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                last = atomicAdd(a.arrived + v0, 1) == parts - 1;
-                if (last) a.arrived[v0] = 0;                  // for the next call
+                last = atomicAdd(a.arrived + s.v0, 1) == parts - 1;
+                if (last) a.arrived[s.v0] = 0;                // for the next call
             }
             __syncthreads();
             if (last) {
                 __threadfence();
-                auto slot_of = [&](int i) { return (size_t)(2 * (v0 + i) + (i == 0)); };
-                for (int x = tid; x < nr * (D / 4); x += kThreads) {
-                    const int row = x / (D / 4), d = (x - row * (D / 4)) * 4;
-                    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-                    float m = kLow, sum = 0.f;
-                    for (int i = 0; i < parts; ++i) {
-                        const float2 st = __ldcg(&ml[slot_of(i) * RT + row]);
-                        if (st.y != 0.f) m = fmaxf(m, st.x);
-                    }
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int i = 0; i < parts; ++i) {
-                        const float2 st = __ldcg(&ml[slot_of(i) * RT + row]);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * RT + row) * D + d));
-                        if (st.y == 0.f) continue;            // a part with no weight does not count
-                        const float f = ex2(st.x - m);
-                        sum = fmaf(f, st.y, sum);
-                        acc.x = fmaf(f, v.x, acc.x);
-                        acc.y = fmaf(f, v.y, acc.y);
-                        acc.z = fmaf(f, v.z, acc.z);
-                        acc.w = fmaf(f, v.w, acc.w);
-                    }
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    const int rr = row0 + row, tok = rr / a.group;
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-                    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-                    uint2 w;
-                    memcpy(&w.x, &lo, 4);
-                    memcpy(&w.y, &hi, 4);
-                    *reinterpret_cast<uint2*>(a.out + (size_t)(r.q0 + tok) * a.out_row +
-                                              (size_t)(h * a.group + rr - tok * a.group) * D + d) = w;
-                }
+                join<RT, D>(a, s, tid, kThreads);
             }
         }
         __syncthreads();                                      // the next segment's outputs take this one's place
     }
     if (bad) atomicOr(a.err, kErrBounds);
+    pdl_wait();                          // this kernel is not over before the one that it runs beside
 }
 
 template <typename S>
@@ -525,26 +400,41 @@ size_t smem_bytes(int n_req) {
 }
 
 template <typename S>
-cudaError_t run(const Cache& c, const Args& a, cudaStream_t st) {
+cudaError_t run(const Cache& c, Args a, bool beside, cudaStream_t st) {
     const int grid = S::CTAS * c.sm_count;
-    if ((size_t)grid * 2 * S::RT * S::D > c.part_o_floats || (size_t)grid * 4 * S::RT > c.part_ml_floats || (size_t)grid > c.arrived_n)
+    size_t o = 0, ml = 0;
+    chunk4_scratch(c.sm_count, &o, &ml);
+    // (behind what the kernel beside it has)
+    a.part_o = c.d_part_o + o;
+    a.part_ml = c.d_part_ml + ml;
+    a.arrived = c.d_arrived + c.sm_count;
+    if (o + (size_t)grid * 2 * S::RT * S::D > c.part_o_floats || ml + (size_t)grid * 4 * S::RT > c.part_ml_floats ||
+        (size_t)c.sm_count + grid > c.arrived_n)
         return cudaErrorInvalidValue;
-    attend4_kernel<S><<<grid, kThreads, smem_bytes<S>(a.n_req), st>>>(a);
-    return cudaGetLastError();
+    return launch_k(attend4_kernel<S>, dim3(grid), dim3(kThreads), smem_bytes<S>(a.n_req), st, beside, a);
 }
 template <typename S>
 cudaError_t set_one() {
     return cudaFuncSetAttribute(attend4_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<S>(kMaxBatch));
 }
 
+// Rows per KV head up to which a request goes by this kernel where the other one runs too.
+constexpr int kFew = 16;
+
 }  // namespace
 
-size_t attend4_arrivals(int sm_count) { return (size_t)sm_count * 2; }
+void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* arrivals) {
+    chunk4_scratch(sm_count, o_floats, ml_floats);
+    *o_floats += (size_t)sm_count * 2 * 2 * 16 * 128;
+    *ml_floats += (size_t)sm_count * 2 * 4 * 16;
+    *arrivals = (size_t)sm_count * 3;
+}
 
 cudaError_t set_attend4_attrs() {
     cudaError_t e = set_one<Shape<1, 1>>();
     if (e == cudaSuccess) e = set_one<Shape<1, 2>>();
     if (e == cudaSuccess) e = set_one<Shape<2, 1>>();
+    if (e == cudaSuccess) e = set_chunk4_attrs();
     return e;
 }
 
@@ -572,15 +462,26 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
     a.n_rows = n_rows;
     a.kv_heads = c.cfg.n_kv_heads;
     a.group = n_heads / c.cfg.n_kv_heads;
+    a.rows_lo = 0;
+    a.rows_hi = 1 << 30;
     a.bs_log2 = c.bs_log2;
     a.n_blocks = c.cfg.n_blocks;
     a.max_blocks = c.cfg.max_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.window = window < (1 << 30) ? window : 0;            // (a request is at most 2^30 tokens long)
-    // rows of an average request's KV head
-    const long long rows = (long long)a.group * ((n_rows + n_req - 1) / n_req);
-    if (c.cfg.head_dim == 256) return run<Shape<2, 1>>(c, a, st);
-    return rows <= 8 ? run<Shape<1, 1>>(c, a, st) : run<Shape<1, 2>>(c, a, st);
+    if (c.cfg.head_dim == 256) return run<Shape<2, 1>>(c, a, false, st);
+    const long long all = (long long)a.group * n_rows;
+    // One token per request, as the host sees it: this kernel alone. Otherwise requests of more
+    // than kFew rows go by the other one, in the same call, as only the device knows which those are.
+    const bool beside = all > kFew && (n_rows > n_req || a.group > kFew);
+    if (beside) {
+        Args big = a;
+        big.rows_lo = a.rows_hi = kFew;
+        const cudaError_t e = launch_chunk4(c.sm_count, big, st);
+        if (e != cudaSuccess) return e;
+    }
+    const long long rows = beside ? kFew : (long long)a.group * ((n_rows + n_req - 1) / n_req);
+    return rows <= 8 ? run<Shape<1, 1>>(c, a, beside, st) : run<Shape<1, 2>>(c, a, beside, st);
 }
 
 }  // namespace kv8

@@ -99,9 +99,11 @@ const char* pool_error(const kv8_cache* c, const kv8_pool* p) {
     return nullptr;
 }
 
+bool takes_4_bits(const kv8_config& k) { return !k.shared_kv && k.head_dim <= 256; }
+
 // A 4-bit pool of this handle; null where it is sound.
 const char* pool4_error(const kv8_cache* c, const kv4_pool* p) {
-    if (c->cfg.shared_kv || c->cfg.head_dim > 256) return "4 bits are for 128- and 256-dim heads with K and V apart";
+    if (!takes_4_bits(c->cfg)) return "4 bits are for 128- and 256-dim heads with K and V apart";
     if (!p || !p->k_codes || !p->k_scale || !p->v_codes || !p->v_scale) return "pool pointers must not be NULL";
     if (!aligned(p->k_codes, 16) || !aligned(p->v_codes, 16) || !aligned(p->k_scale, 16) || !aligned(p->v_scale, 16))
         return "codes and scales must be 16-byte aligned";
@@ -173,6 +175,12 @@ int kv8_create(const kv8_config* cfg, kv8_cache** out) {
     if (e == cudaSuccess) {
         where = "device scratch";
         kv8::attend_scratch(c->sm_count, cfg->head_dim, &c->part_o_floats, &c->part_ml_floats, &c->meta_n);
+        if (takes_4_bits(*cfg)) {
+            size_t o = 0, ml = 0;
+            kv8::attend4_scratch(c->sm_count, &o, &ml, &c->arrived_n);
+            if (o > c->part_o_floats) c->part_o_floats = o;
+            if (ml > c->part_ml_floats) c->part_ml_floats = ml;
+        }
         e = cudaMalloc(&c->d_err, sizeof(uint32_t));
         if (e == cudaSuccess) e = cudaMemset(c->d_err, 0, sizeof(uint32_t));
         if (e == cudaSuccess) e = cudaMalloc(&c->d_part_o, c->part_o_floats * sizeof(float));
@@ -180,9 +188,10 @@ int kv8_create(const kv8_config* cfg, kv8_cache** out) {
         if (e == cudaSuccess) e = cudaMalloc(&c->d_meta, c->meta_n * sizeof(int4));
         if (e == cudaSuccess) e = cudaMalloc(&c->d_ctrl, 2 * sizeof(int));
         if (e == cudaSuccess) e = cudaMemset(c->d_ctrl, 0, 2 * sizeof(int));
-        c->arrived_n = kv8::attend4_arrivals(c->sm_count);
-        if (e == cudaSuccess) e = cudaMalloc(&c->d_arrived, c->arrived_n * sizeof(int));
-        if (e == cudaSuccess) e = cudaMemset(c->d_arrived, 0, c->arrived_n * sizeof(int));
+        if (c->arrived_n) {
+            if (e == cudaSuccess) e = cudaMalloc(&c->d_arrived, c->arrived_n * sizeof(int));
+            if (e == cudaSuccess) e = cudaMemset(c->d_arrived, 0, c->arrived_n * sizeof(int));
+        }
         // the clears run on the legacy stream, which streams that do not block do not wait for
         if (e == cudaSuccess) e = cudaStreamSynchronize(0);
     }
@@ -413,6 +422,8 @@ int kv8_check_error(kv8_cache* c) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemcpy(&w, c->d_err, sizeof w, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess) e = cudaMemset(c->d_err, 0, sizeof w);
+    // a call that gave up may have left parts that nobody joined
+    if (e == cudaSuccess && (w & kErrTimeout) && c->arrived_n) e = cudaMemset(c->d_arrived, 0, c->arrived_n * sizeof(int));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(c, e, "kv8_check_error");
     if (w & kv8::kErrNoBlocks) return fail(c, SRH_ERR_NOMEM, "too few free blocks; the call changed nothing");

@@ -67,8 +67,8 @@ cudaError_t launch_append4(const Cache& c, const Layer& l, const int32_t* table,
                            int n_req, int n_rows, cudaStream_t st);
 cudaError_t launch_read(const Cache& c, const Layer& l, const int32_t* table, const int32_t* len, const int32_t* start,
                         const int32_t* cu, int n_req, int n_rows, cudaStream_t st);
-// Arrival counters that kv4_attend needs.
-size_t attend4_arrivals(int sm_count);
+// What kv4_attend needs of the scratch, and arrival counters.
+void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* arrivals);
 cudaError_t set_attend4_attrs();
 cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* table, const int32_t* len,
                            const int32_t* cu, int n_req, const uint16_t* q, long long q_row, int n_rows, int n_heads,

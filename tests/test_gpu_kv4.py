@@ -296,7 +296,9 @@ def _attend_64(c, q, cu, scale, window=0, layer=0):
     The tolerance: bf16's rounding of the output, 2^-8 of it; the fp16 rounding of a weight times V's scale, at most 2^-11 of
     it, on codes at most 8 from the middle; scores in fp32: a sum of 2 D products of up to |q| (|m| + 15 s) each, of which
     each addition rounds by 2^-24, moves a weight by 2^-24 2 D sum|q| max|K| scale at the very worst (an eighth of that is
-    allowed: errors of a sum add up as a walk), and exponentials within 2^-21."""
+    allowed: errors of a sum add up as a walk), and exponentials within 2^-21. Where many rows share a KV head, keys and
+    values are rounded to fp16, 2^-12 of each at most: a score of D such products moves by 2^-12 |q| max|K| scale as a walk of
+    equal steps (four times that is allowed), and a weight by as much of itself."""
     cus, lens = cu.tolist(), c.len.tolist()
     G = q.shape[1] // c.Hk
     out, tol = torch.zeros(q.shape, dtype=torch.float64, device="cuda"), torch.zeros(q.shape, dtype=torch.float64, device="cuda")
@@ -319,8 +321,11 @@ def _attend_64(c, q, cu, scale, window=0, layer=0):
         if n == 0:
             continue
         rounding = 2.0 ** -11 * 8 * torch.einsum("hgit,th->ihg", w, sm[..., 0])[..., None]
-        reach = x.abs().sum(-1, keepdim=True) * k.abs().amax((0, 2))[None, :, None, None] * scale
+        reach = x.abs().sum(-1, keepdim=True) * k.abs().amax((0, 2))[None, :, None, None] * abs(scale)
         scores = (2.0 ** -24 * c.D / 4 * reach / c.D ** 0.5 + 2.0 ** -20) * torch.einsum("hgit,thd->ihgd", w, v.abs()) * 2
+        if nq * G > 16 and c.D == 128:
+            walk = 2.0 ** -10 * x.square().sum(-1, keepdim=True).sqrt() * k.abs().amax((0, 2))[None, :, None, None] * abs(scale)
+            scores = scores + (2 * walk + 2.0 ** -12) * torch.einsum("hgit,thd->ihgd", w, v.abs())
         tol[cus[b]:cus[b + 1]] = (2.0 ** -8 * o.abs() + rounding + scores).reshape(nq, -1, c.D)
     return out, tol + 1e-30
 
@@ -351,6 +356,14 @@ def _check(c, q, cu, out, scale, window=0, layer=0):
     (2, 4, 256, 128, [3000, 260], [1, 30], 257),
     (1, 6, 128, 16, [20000], [1], 0),
     (1, 2, 128, 32, [90] * 60, [1] * 60, 0),
+    (1, 1, 128, 16, [17], [17], 0),
+    (1, 1, 128, 64, [128, 129, 127, 256, 257, 1000], [128, 129, 127, 256, 257, 255], 0),
+    (2, 8, 128, 128, [4000, 200, 5], [40, 16, 3], 0),
+    (8, 4, 128, 64, [1500, 700, 64], [300, 1, 64], 0),
+    (1, 24, 128, 16, [9000], [1], 0),
+    (1, 3, 128, 32, [2000, 130], [700, 100], 300),
+    (4, 16, 128, 16, [513, 100], [33, 1], 64),
+    (1, 300, 128, 16, [260, 3], [2, 1], 0),
 ])
 def test_attend(Hk, G, D, bs, lens, news, window):
     g = _gen(Hk * 1000 + G * 100 + bs)
