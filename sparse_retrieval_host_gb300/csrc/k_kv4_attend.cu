@@ -48,6 +48,10 @@ struct Shape {
     static constexpr int kPitch = D + 8;                       // floats of a row of the warps' outputs
     static constexpr int kOutBytes = kWarps * RT * kPitch * 4;
     static constexpr int kStatBytes = kWarps * RT * 8;         // reference and sum
+    static constexpr int kCodes = 16 * D / 2;                  // 16 tokens of K or V
+    static constexpr int kStage = 2 * kCodes + 128;            // and their scales
+    static constexpr int STAGES = DB == 1 ? 4 : 3;             // of each warp's ring
+    static constexpr int kRing = kWarps * STAGES * kStage;
 };
 
 __device__ __forceinline__ float lg2(float x) {
@@ -69,6 +73,29 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     return r;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// Where 16-byte piece p of token row t lies among the 16 rows of a stage, so that the reads below meet no
+// bank twice: of K 8 rows x 4 pieces at a time (128-byte rows: 2 rows x 4), of V rows 2 c
+// of four c, 32 bytes each.
+template <int DB>
+__device__ __forceinline__ uint32_t k_at(uint32_t t, uint32_t p) {
+    return DB == 1 ? t * 64 + p * 16 : t * 128 + ((p ^ ((t & 1) << 2)) << 4);
+}
+template <int DB>
+__device__ __forceinline__ uint32_t v_at(uint32_t t, uint32_t p) {
+    if (DB == 2) return t * 128 + ((p ^ (((t >> 1) & 3) << 1)) << 4);
+    const uint32_t r = (t & 8) | ((t & 1) << 2) | ((t >> 1) & 3);
+    return r * 64 + ((p ^ (r & 2)) << 4);
+}
+
 // ---------------------------------------------------------------- the kernel
 template <typename S>
 __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid_constant__ Args a) {
@@ -76,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     extern __shared__ __align__(16) unsigned char sm[];
     float* const outs = reinterpret_cast<float*>(sm);                       // [warp][row][kPitch]
     float2* const stats = reinterpret_cast<float2*>(sm + S::kOutBytes);     // [warp][row]: reference, sum
-    int* const first = reinterpret_cast<int*>(sm + S::kOutBytes + S::kStatBytes);   // units before each request
+    int* const first = reinterpret_cast<int*>(sm + S::kOutBytes + S::kStatBytes + S::kRing);   // units before each request
     __shared__ long long warp_sums[33];
     __shared__ int last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -90,12 +117,64 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     bool bad = false;
     int u = ch.begin(cta);
     const int u1 = ch.begin(cta + 1);
+
+    // -------------------------------------------------------- the warp's ring
+    // A step is the warp's 16 tokens of one unit. Blocks of 32 steps are held a lane each.
+    unsigned char* const ring = sm + S::kOutBytes + S::kStatBytes + warp * (S::STAGES * S::kStage);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    int ids = -1, ids_next = -1;
+    uint32_t absent = 0;                                      // of the last 32 steps asked for, a bit each (by step % 32)
+    auto blocks = [&](const Segment& s, int from) -> int {    // this lane's of steps from ..
+        const int t0 = (s.t0 + from + lane) * kTile + warp * 16;
+        if (from + lane >= s.n || t0 >= s.len) return -1;     // none there
+        return __ldg(a.table + (size_t)s.b * a.max_blocks + (t0 >> a.bs_log2));
+    };
+    auto ask = [&](const Segment& s, int i) {                 // step i into its stage
+        if (i < s.n) {
+            if ((i & 31) == 0 && i > 0) {
+                ids = ids_next;
+                ids_next = blocks(s, i + 32);
+            }
+            const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+            const int t0 = (s.t0 + i) * kTile + warp * 16;
+            // (what no row sees may have been given up)
+            const bool see = t0 <= s.p_hi && (!a.window || t0 + 15 > s.p_lo - a.window);
+            const bool there = see && id >= 0 && id < a.n_blocks;
+            absent = there ? absent & ~(1u << (i & 31)) : absent | 1u << (i & 31);
+            if (there) {
+                const size_t tok0 = (size_t)s.h << a.bs_log2 | (t0 & (bsz - 1));
+                const uint8_t* kp = a.kc + (size_t)id * a.block_stride + tok0 * (D / 2);
+                const uint8_t* vp = a.vc + (size_t)id * a.block_stride + tok0 * (D / 2);
+                const uint32_t to = ring_at + (i % S::STAGES) * S::kStage;
+                constexpr int P = 4 * DB;                     // pieces of a row
+#pragma unroll
+                for (int j = 0; j < S::kCodes / 512; ++j) {
+                    const uint32_t x = lane + 32 * j;
+                    copy16(to + k_at<DB>(x / P, x % P), kp + x * 16);
+                    copy16(to + S::kCodes + v_at<DB>(x / P, x % P), vp + x * 16);
+                }
+                const size_t sc = ((size_t)id * a.kv_heads << a.bs_log2) + tok0;
+                if (lane < 8) copy16(to + 2 * S::kCodes + lane * 16, (lane < 4 ? a.ks + sc : a.vs + sc - 16) + lane * 4);
+            } else if (see) {
+                bad = true;
+            }
+        }
+        copy_commit();
+    };
+    auto ask_first = [&](const Segment& s) {
+        ids = blocks(s, 0);
+        ids_next = blocks(s, 32);
+#pragma unroll
+        for (int i = 0; i < S::STAGES - 1; ++i) ask(s, i);
+    };
+
     Segment s;
-    while (next_segment<RT, false>(a, first, ch, cta, &u, u1, &s)) {
+    bool more = next_segment<RT, false>(a, first, ch, cta, &u, u1, &s);
+    if (more) ask_first(s);
+    while (more) {
         const int row0 = s.row0, nr = s.nr, h = s.h, parts = s.parts;
         const int p0 = s.len - s.nq;                          // position of the request's first row
-        const int p_lo = p0 + row0 / a.group, p_hi = p0 + (row0 + nr - 1) / a.group;
-        const int see_lo = a.window ? p_lo - a.window + 1 : 0;
+        const int p_lo = s.p_lo, p_hi = s.p_hi;
 
         // queries as B fragments: lane (g, c) holds dims 32 c .. of row g, per 8 dims two k steps
         uint32_t q[NT][DB][16];
@@ -170,35 +249,30 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
 
         for (int i = 0; i < s.n; ++i) {
             const int t0 = (s.t0 + i) * kTile + warp * 16;
-            if (t0 > p_hi || t0 + 16 <= see_lo) continue;
-            const int id = __ldg(a.table + (size_t)s.b * a.max_blocks + (t0 >> a.bs_log2));
-            if (id < 0 || id >= a.n_blocks) {                 // a block that is none reads as absent
-                bad = true;
-                continue;
-            }
-            const size_t tok0 = (size_t)h << a.bs_log2 | (t0 & (bsz - 1));
-            const uint8_t* kp = a.kc + (size_t)id * a.block_stride + tok0 * (D / 2);
-            const uint8_t* vp = a.vc + (size_t)id * a.block_stride + tok0 * (D / 2);
-            const size_t sc = ((size_t)id * a.kv_heads << a.bs_log2) + tok0;
+            copy_wait<S::STAGES - 2>();
+            __syncwarp();                                     // step i is there; step i - 1 has been read
+            ask(s, i + S::STAGES - 1);
+            if (absent >> (i & 31) & 1) continue;             // (a block that is none reads as absent)
+            const unsigned char* const st = ring + (i % S::STAGES) * S::kStage;
             uint4 k[2][DB];
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
-                k[0][d] = __ldg(reinterpret_cast<const uint4*>(kp + g * (D / 2) + d * 64 + c * 16));
-                k[1][d] = __ldg(reinterpret_cast<const uint4*>(kp + (g + 8) * (D / 2) + d * 64 + c * 16));
+                k[0][d] = *reinterpret_cast<const uint4*>(st + k_at<DB>(g, 4 * d + c));
+                k[1][d] = *reinterpret_cast<const uint4*>(st + k_at<DB>(g + 8, 4 * d + c));
             }
-            uint32_t ksm[2] = {__ldg(a.ks + sc + g), __ldg(a.ks + sc + g + 8)};
-            uint32_t vsm[2] = {__ldg(a.vs + sc + g), __ldg(a.vs + sc + g + 8)};
+            const uint32_t* const scales = reinterpret_cast<const uint32_t*>(st + 2 * S::kCodes);
+            const uint32_t ksm[2] = {scales[g], scales[g + 8]}, vsm[2] = {scales[16 + g], scales[24 + g]};
             // V: tokens 2 c, 2 c + 1, and 8 more on, dims 16 DB g ..
             uint32_t v[4][2 * DB];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint8_t* p = vp + (2 * c + (j & 1) + 8 * (j >> 1)) * (D / 2) + g * 8 * DB;
+                const uint32_t t = 2 * c + (j & 1) + 8 * (j >> 1);
                 if (DB == 1) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+                    const uint2 x = *reinterpret_cast<const uint2*>(st + S::kCodes + v_at<DB>(t, g >> 1) + (g & 1) * 8);
                     v[j][0] = x.x;
                     v[j][1] = x.y;
                 } else {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+                    const uint4 x = *reinterpret_cast<const uint4*>(st + S::kCodes + v_at<DB>(t, g));
                     v[j][0] = x.x;
                     v[j][1] = x.y;
                     v[j][2 * DB - 2] = x.z;
@@ -207,11 +281,11 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             }
 
             // scores
-            float sc4[NT][4];
+            float sc4[NT][4], sc4b[NT][4];                    // two chains
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sc4[t][j] = 0.f;
+                for (int j = 0; j < 4; ++j) sc4[t][j] = sc4b[t][j] = 0.f;
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
                 const uint32_t w0[4] = {k[0][d].x, k[0][d].y, k[0][d].z, k[0][d].w};
@@ -225,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                     const uint32_t x0 = w0[j] >> 8, x1 = w1[j] >> 8;
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        mma(sc4[t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
+                        mma(sc4b[t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
                             q[t][d][4 * j + 2], q[t][d][4 * j + 3]);
                 }
             }
@@ -248,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int col = j & 1, tk = j >> 1;
-                    float x = fmaf(sc4[t][j] * qf[t][col], kss[tk], fmaf(km[tk], qs[t][col], lv[tk]));
+                    float x = fmaf((sc4[t][j] + sc4b[t][j]) * qf[t][col], kss[tk], fmaf(km[tk], qs[t][col], lv[tk]));
                     if (edge) {
                         const int tt = t0 + g + 8 * tk, p = pos[t][col];
                         if (tt > p || (a.window && tt <= p - a.window)) x = -INFINITY;
@@ -319,6 +393,12 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             }
         }
 
+        // the next segment's first steps on their way
+        Segment then;
+        __syncwarp();
+        more = next_segment<RT, false>(a, first, ch, cta, &u, u1, &then);
+        if (more) ask_first(then);
+
         // -------------------------------------------------------- the warps' sums together
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -375,28 +455,22 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             }
         }
         if (parts > 1) {
-            // the last part to be written joins them all
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                last = atomicAdd(a.arrived + s.v0, 1) == parts - 1;
-                if (last) a.arrived[s.v0] = 0;                // for the next call
-            }
-            __syncthreads();
-            if (last) {
-                __threadfence();
-                join<RT, D>(a, s, tid, kThreads);
-            }
+            finish<RT, D>(a, s, tid, kThreads, &last, [] {
+                __syncthreads();
+                return true;
+            });
         }
         __syncthreads();                                      // the next segment's outputs take this one's place
+        s = then;
     }
+    copy_wait<0>();
     if (bad) atomicOr(a.err, kErrBounds);
     pdl_wait();                          // this kernel is not over before the one that it runs beside
 }
 
 template <typename S>
 size_t smem_bytes(int n_req) {
-    return S::kOutBytes + S::kStatBytes + (size_t)n_req * sizeof(int);
+    return S::kOutBytes + S::kStatBytes + S::kRing + (size_t)n_req * sizeof(int);
 }
 
 template <typename S>
@@ -407,9 +481,10 @@ cudaError_t run(const Cache& c, Args a, bool beside, cudaStream_t st) {
     // (behind what the kernel beside it has)
     a.part_o = c.d_part_o + o;
     a.part_ml = c.d_part_ml + ml;
-    a.arrived = c.d_arrived + c.sm_count;
+    a.arrived = c.d_arrived + 3 * c.sm_count;
+    a.arrived_n = grid;
     if (o + (size_t)grid * 2 * S::RT * S::D > c.part_o_floats || ml + (size_t)grid * 4 * S::RT > c.part_ml_floats ||
-        (size_t)c.sm_count + grid > c.arrived_n)
+        3 * ((size_t)c.sm_count + grid) > c.arrived_n)
         return cudaErrorInvalidValue;
     return launch_k(attend4_kernel<S>, dim3(grid), dim3(kThreads), smem_bytes<S>(a.n_req), st, beside, a);
 }
@@ -427,7 +502,7 @@ void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* 
     chunk4_scratch(sm_count, o_floats, ml_floats);
     *o_floats += (size_t)sm_count * 2 * 2 * 16 * 128;
     *ml_floats += (size_t)sm_count * 2 * 4 * 16;
-    *arrivals = (size_t)sm_count * 3;
+    *arrivals = (size_t)sm_count * 9;
 }
 
 cudaError_t set_attend4_attrs() {

@@ -52,7 +52,7 @@ struct Bars {
     uint64_t drain;
     long long warp_sums[33];
     uint32_t tmem_base;
-    int abort, last, any;
+    int abort, last;
     uint32_t most[2][2][4];              // [K, V][tile & 1][warp]: largest magnitude
     alignas(16) uint32_t there[kInfo][4];            // tokens that exist, a bit each
     float k_factor[kInfo];               // 2^(e - 14)
@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
         while (ok && next_segment<kRT, true>(a, first, ch, cta, &u, u1, &s)) {
             auto block_of = [&](int tile) -> int {
                 const int tok = tile * kTile + t;
-                if (tok >= s.len) return -1;
+                // (what no row sees may have been given up)
+                if (tok > s.p_hi || (a.window && tok <= s.p_lo - a.window)) return -1;
                 const int id = __ldg(a.table + (size_t)s.b * a.max_blocks + (tok >> a.bs_log2));
                 if (id >= 0 && id < a.n_blocks) return id;
                 bad = true;
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                 fence_async_smem();
                 warp_arrive(&bs.q_full, lane);
             }
-            const int lane_lo = p0 + (s.row0 + (both ? i * 128 : 0)) / a.group, lane_hi = p0 + (s.row0 + s.nr - 1) / a.group;
+            const int lane_lo = p0 + (s.row0 + (both ? i * 128 : 0)) / a.group, lane_hi = s.p_hi;
             const int win = a.window ? a.window : 1 << 30;
             float ref = kLow, l = 0.f;
             const int n = both ? s.n : (s.n + 1 - i) / 2;
@@ -502,19 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             tc_fence_before();
             if (s.parts > 1) {
                 if (on && (both || i == 0)) reinterpret_cast<float2*>(a.part_ml)[slot * kRT + row] = make_float2(m, sum);
-                __threadfence();
-                ok = meet();
+                ok = finish<kRT, kD>(a, s, tid, 256, &bs.last, meet);
                 if (!ok) break;
-                if (tid == 0) {
-                    bs.last = atomicAdd(a.arrived + s.v0, 1) == s.parts - 1;
-                    if (bs.last) a.arrived[s.v0] = 0;          // for the next call
-                }
-                ok = meet();
-                if (!ok) break;
-                if (bs.last) {
-                    __threadfence();
-                    join<kRT, kD>(a, s, tid, 256);
-                }
             }
         }
     }
@@ -542,7 +532,8 @@ cudaError_t set_chunk4_attrs() {
     return cudaFuncSetAttribute(chunk4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxBatch));
 }
 
-cudaError_t launch_chunk4(int sm_count, const Args& a, cudaStream_t st) {
+cudaError_t launch_chunk4(int sm_count, Args a, cudaStream_t st) {
+    a.arrived_n = sm_count;
     chunk4_kernel<<<sm_count, kThreads, smem_bytes(a.n_req), st>>>(a);
     return cudaGetLastError();
 }

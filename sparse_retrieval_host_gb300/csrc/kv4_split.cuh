@@ -36,7 +36,8 @@ struct Args {
     const uint32_t* vs;
     float* part_o;
     float* part_ml;
-    int* arrived;
+    int* arrived;                                // [3][arrived_n], zeros between calls
+    int arrived_n;                               // CTAs at most
     uint32_t* err;
     int n_req, n_rows, kv_heads, group;          // group = query heads / kv_heads
     int rows_lo, rows_hi;                        // takes requests of rows_lo < rows <= rows_hi per KV head
@@ -105,6 +106,7 @@ __device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
 struct Segment {
     int b, h, row0, nr;      // rows of the row tile in the request's (token, head) order
     int q0, nq, len;
+    int p_lo, p_hi;          // positions of the first and the last row
     int t0, n;               // first token tile, and tiles to run (0: no row sees any)
     int v0, parts, part;     // the chunk in which the row tile begins, chunks that share it, this one's place
 };
@@ -173,6 +175,8 @@ __device__ __forceinline__ bool next_segment(const Args& a, const int* first, co
         s->q0 = r.q0;
         s->nq = r.nq;
         s->len = r.len;
+        s->p_lo = r.len - r.nq + s->row0 / a.group;
+        s->p_hi = r.len - r.nq + (s->row0 + s->nr - 1) / a.group;
         s->v0 = ch.of(u_rt);
         s->parts = ch.of(u_rt + n - 1) - s->v0 + 1;
         s->part = v - s->v0;
@@ -207,41 +211,86 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 
 constexpr float kLow = -1e30f;           // reference of a row that has seen no token
 
-// The parts of a row tile together into `out`, by threads tid of T: part i has reference m_i, sum
-// l_i and outputs O_i of each row; out = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in order.
-template <int RT, int D>
-__device__ __forceinline__ void join(const Args& a, const Segment& s, int tid, int T) {
-    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-    for (int x = tid; x < s.nr * (D / 4); x += T) {
-        const int row = x / (D / 4), d = (x - row * (D / 4)) * 4;
+// Parts i0, i0 + step, .. (cnt of them) of a row tile together, by threads tid of T: part i has
+// reference m_i, sum l_i and outputs O_i of each row, and sum 2^(m_i - m) O_i, sum 2^(m_i - m) l_i, in order,
+// become `out` (FINAL) or part i0. `sync` is the threads' barrier (false: give up).
+template <int RT, int D, bool FINAL, class Sync>
+__device__ __forceinline__ bool join(const Args& a, const Segment& s, int i0, int step, int cnt, int tid, int T, Sync sync) {
+    float2* const ml = reinterpret_cast<float2*>(a.part_ml);
+    // rows of one thread at most, so that a part's statistics are read before they are written
+    for (int x0 = 0; x0 < s.nr * (D / 4); x0 += T) {
+        const int x = x0 + tid, row = x / (D / 4), d = (x - row * (D / 4)) * 4;
+        const bool on = row < s.nr;
         float m = kLow, sum = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < s.parts; ++i) {
-            const float2 st = __ldcg(&ml[slot_of(s.v0, i) * RT + row]);
-            if (st.y != 0.f) m = fmaxf(m, st.x);
-        }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < s.parts; ++i) {
-            const float2 st = __ldcg(&ml[slot_of(s.v0, i) * RT + row]);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot_of(s.v0, i) * RT + row) * D + d));
-            if (st.y == 0.f) continue;                        // a part with no weight does not count
-            const float f = ex2(st.x - m);
-            sum = fmaf(f, st.y, sum);
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
+        if (on) {
+#pragma unroll 8
+            for (int i = 0; i < cnt; ++i) {
+                const float2 st = __ldcg(&ml[slot_of(s.v0, i0 + i * step) * RT + row]);
+                if (st.y != 0.f) m = fmaxf(m, st.x);
+            }
+#pragma unroll 8
+            for (int i = 0; i < cnt; ++i) {
+                const size_t at = slot_of(s.v0, i0 + i * step) * RT + row;
+                const float2 st = __ldcg(&ml[at]);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + d));
+                if (st.y == 0.f) continue;                    // a part with no weight does not count
+                const float f = ex2(st.x - m);
+                sum = fmaf(f, st.y, sum);
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z);
+                acc.w = fmaf(f, v.w, acc.w);
+            }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int rr = s.row0 + row, tok = rr / a.group;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-        uint2 w;
-        memcpy(&w.x, &lo, 4);
-        memcpy(&w.y, &hi, 4);
-        *reinterpret_cast<uint2*>(a.out + (size_t)(s.q0 + tok) * a.out_row + (size_t)(s.h * a.group + rr - tok * a.group) * D + d) = w;
+        if (FINAL) {
+            if (!on) continue;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int rr = s.row0 + row, tok = rr / a.group;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            uint2 w;
+            memcpy(&w.x, &lo, 4);
+            memcpy(&w.y, &hi, 4);
+            *reinterpret_cast<uint2*>(a.out + (size_t)(s.q0 + tok) * a.out_row + (size_t)(s.h * a.group + rr - tok * a.group) * D + d) = w;
+        } else {
+            const size_t at = slot_of(s.v0, i0) * RT + row;
+            if (!sync()) return false;
+            if (!on) continue;
+            *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
+            if (d == 0) ml[at] = make_float2(m, sum);
+        }
     }
+    return true;
+}
+
+// After a part's sums are written: the last of up to kFan neighbours to get here joins them, the last
+// group of neighbours the groups (parts of one long request are as many as CTAs, and one SM would
+// read them for longer than they took). Counters: of a row tile's first group by its chunk, of
+// the others by theirs, and of its groups; back to zero for the next call.
+constexpr int kFan = 12;
+template <int RT, int D, class Sync>
+__device__ __forceinline__ bool finish(const Args& a, const Segment& s, int tid, int T, int* flag, Sync sync) {
+    const int k = s.part / kFan, i0 = k * kFan, cnt = min(kFan, s.parts - i0), groups = (s.parts + kFan - 1) / kFan;
+    auto last_of = [&](int* counter, int n) -> int {          // 1: this CTA is the last, -1: give up
+        __threadfence();
+        if (!sync()) return -1;
+        if (tid == 0) {
+            *flag = atomicAdd(counter, 1) == n - 1;
+            if (*flag) *counter = 0;
+        }
+        if (!sync()) return -1;
+        const int last = *reinterpret_cast<volatile int*>(flag);
+        __threadfence();
+        return last;
+    };
+    const int mine = last_of(a.arrived + (k == 0 ? s.v0 : a.arrived_n + s.v0 + i0), cnt);
+    if (mine <= 0) return mine == 0;
+    if (groups == 1) return join<RT, D, true>(a, s, i0, 1, cnt, tid, T, sync);
+    if (!join<RT, D, false>(a, s, i0, 1, cnt, tid, T, sync)) return false;
+    const int all = last_of(a.arrived + 2 * a.arrived_n + s.v0, groups);
+    if (all <= 0) return all == 0;
+    return join<RT, D, true>(a, s, 0, kFan, groups, tid, T, sync);
 }
 
 }  // namespace split
@@ -249,7 +298,7 @@ __device__ __forceinline__ void join(const Args& a, const Segment& s, int tid, i
 // The kernel of many rows per KV head: its share of the handle's scratch (the first), and its launch.
 void chunk4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats);
 cudaError_t set_chunk4_attrs();
-cudaError_t launch_chunk4(int sm_count, const split::Args& a, cudaStream_t st);
+cudaError_t launch_chunk4(int sm_count, split::Args a, cudaStream_t st);
 
 }  // namespace kv8
 }  // namespace srh

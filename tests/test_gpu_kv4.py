@@ -836,3 +836,34 @@ def test_serving_loop():
             assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -4 * float(a.abs().max())
     c.close()
     c8.close()
+
+
+@pytest.mark.parametrize("G,news", [(4, 1), (4, 30)])
+def test_blocks_given_up_behind_a_window(G, news):
+    """Table entries that no query sees any more may be gone: they are not reported."""
+    g = _gen(85)
+    c = _kv4(batch=1, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=70, max_blocks=64)
+    _filled(c, g, [1000])
+    q = _bf16(g, news, 2 * G, 128)
+    cu = _i32([0, news])
+    want = c.attend(q, cu, scale=0.1, window=200)
+    c.table[0, :(1000 - news - 199) // 16] = -1
+    c.table[0, 63:] = -1
+    out = c.attend(q, cu, scale=0.1, window=200)
+    assert c.check_error() == 0 and torch.equal(out, want)
+    c.close()
+
+
+@pytest.mark.parametrize("Hk,G,n,news", [(1, 8, 60000, 1), (1, 8, 60000, 5), (1, 16, 100000, 1), (1, 4, 40000, 60)])
+def test_one_long_request_over_all_parts(Hk, G, n, news):
+    """Parts of many CTAs, joined in groups."""
+    g = _gen(86)
+    c = _kv4(batch=1, n_kv_heads=Hk, head_dim=128, block_tokens=64, n_blocks=n // 64 + 1, max_blocks=n // 64 + 1)
+    _filled(c, g, [n])
+    q = _bf16(g, news, Hk * G, 128)
+    cu = _i32([0, news])
+    out = c.attend(q, cu, scale=0.1)
+    _check(c, q, cu, out, 0.1)
+    for _ in range(3):
+        assert torch.equal(c.attend(q, cu, scale=0.1), out)
+    c.close()
