@@ -56,12 +56,55 @@ struct Shape {
 
 __device__ __forceinline__ float lg2(float x) {
     float r;
-    asm("lg2.approx.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+// Pairs of fp32 values in one 64-bit register (one instruction for both).
+using u64 = unsigned long long;
+__device__ __forceinline__ u64 pack(float a, float b) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(u64 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(r) : "r"(at));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(at));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at));
     return r;
 }
 // D += A B: A 16 x 16 (rows by lane / 4), B 16 x 8 (columns by lane / 4), fp16, fp32 sums.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -119,53 +162,66 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     const int u1 = ch.begin(cta + 1);
 
     // -------------------------------------------------------- the warp's ring
-    // A step is the warp's 16 tokens of one unit. Blocks of 32 steps are held a lane each.
-    unsigned char* const ring = sm + S::kOutBytes + S::kStatBytes + warp * (S::STAGES * S::kStage);
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-    int ids = -1, ids_next = -1;
+    // A step is the warp's 16 tokens of one tile; tokens t_of + 128 i of steps i < steps.
+    // The blocks of 32 steps are held a lane each.
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + S::kOutBytes + S::kStatBytes + warp * (S::STAGES * S::kStage));
+    constexpr int P = 4 * DB, kRowsAt = 32 / P;               // 16-byte pieces of a row; rows that the lanes copy at once
+    const uint32_t k_to = k_at<DB>(lane / P, lane % P);
+    uint32_t v_to[S::kCodes / 512];
+#pragma unroll
+    for (int j = 0; j < S::kCodes / 512; ++j) v_to[j] = S::kCodes + v_at<DB>(lane / P + j * kRowsAt, lane % P);
+    const uint32_t* const scale_src = (lane < 4 ? a.ks : a.vs - 16) + lane * 4;
+    const uint8_t *k_src = nullptr, *v_src = nullptr;         // this lane's, at the head's first token
+    const int32_t* table = nullptr;
+    int head_tok = 0, t_of = 0, steps = 0, ids = -1, ids_next = -1;
+    uint32_t in = 0;                                          // stage that is filled next, in bytes
     uint32_t absent = 0;                                      // of the last 32 steps asked for, a bit each (by step % 32)
-    auto blocks = [&](const Segment& s, int from) -> int {    // this lane's of steps from ..
-        const int t0 = (s.t0 + from + lane) * kTile + warp * 16;
-        if (from + lane >= s.n || t0 >= s.len) return -1;     // none there
-        return __ldg(a.table + (size_t)s.b * a.max_blocks + (t0 >> a.bs_log2));
+    auto blocks = [&](int from) -> int {                      // this lane's of steps from ..
+        return from + lane < steps ? __ldg(table + ((t_of + (from + lane) * kTile) >> a.bs_log2)) : -1;
     };
-    auto ask = [&](const Segment& s, int i) {                 // step i into its stage
-        if (i < s.n) {
+    auto ask = [&](int i) {                                   // step i into its stage
+        if (i < steps) {
             if ((i & 31) == 0 && i > 0) {
                 ids = ids_next;
-                ids_next = blocks(s, i + 32);
+                ids_next = blocks(i + 32);
             }
             const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-            const int t0 = (s.t0 + i) * kTile + warp * 16;
-            // (what no row sees may have been given up)
-            const bool see = t0 <= s.p_hi && (!a.window || t0 + 15 > s.p_lo - a.window);
-            const bool there = see && id >= 0 && id < a.n_blocks;
-            absent = there ? absent & ~(1u << (i & 31)) : absent | 1u << (i & 31);
+            const bool there = (uint32_t)id < (uint32_t)a.n_blocks;
+            const uint32_t bit = 1u << (i & 31);
+            absent = there ? absent & ~bit : absent | bit;    // (a block that is none reads as absent)
             if (there) {
-                const size_t tok0 = (size_t)s.h << a.bs_log2 | (t0 & (bsz - 1));
-                const uint8_t* kp = a.kc + (size_t)id * a.block_stride + tok0 * (D / 2);
-                const uint8_t* vp = a.vc + (size_t)id * a.block_stride + tok0 * (D / 2);
-                const uint32_t to = ring_at + (i % S::STAGES) * S::kStage;
-                constexpr int P = 4 * DB;                     // pieces of a row
+                const int at = (t_of + i * kTile) & (bsz - 1);
+                const long long off = (long long)id * a.block_stride + at * (D / 2);
+                const uint32_t to = ring + in;
 #pragma unroll
                 for (int j = 0; j < S::kCodes / 512; ++j) {
-                    const uint32_t x = lane + 32 * j;
-                    copy16(to + k_at<DB>(x / P, x % P), kp + x * 16);
-                    copy16(to + S::kCodes + v_at<DB>(x / P, x % P), vp + x * 16);
+                    copy16(to + k_to + j * 512, k_src + off + j * 512);
+                    copy16(to + v_to[j], v_src + off + j * 512);
                 }
-                const size_t sc = ((size_t)id * a.kv_heads << a.bs_log2) + tok0;
-                if (lane < 8) copy16(to + 2 * S::kCodes + lane * 16, (lane < 4 ? a.ks + sc : a.vs + sc - 16) + lane * 4);
-            } else if (see) {
+                if (lane < 8)
+                    copy16(to + 2 * S::kCodes + lane * 16, scale_src + (((size_t)id * a.kv_heads << a.bs_log2) + (head_tok + at)));
+            } else {
                 bad = true;
             }
         }
+        in = in == (S::STAGES - 1) * S::kStage ? 0 : in + S::kStage;
         copy_commit();
     };
     auto ask_first = [&](const Segment& s) {
-        ids = blocks(s, 0);
-        ids_next = blocks(s, 32);
+        // the steps that some row sees (what none sees may have been given up)
+        const int t0 = s.t0 * kTile + warp * 16, t1 = min((s.t0 + s.n - 1) * kTile + warp * 16, s.p_hi);
+        const int skip = a.window && t0 + 15 <= s.p_lo - a.window ? (s.p_lo - a.window - t0 - 15) / kTile + 1 : 0;
+        t_of = t0 + skip * kTile;
+        steps = s.n > 0 && t_of <= t1 ? (t1 - t_of) / kTile + 1 : 0;
+        head_tok = s.h << a.bs_log2;
+        k_src = a.kc + (size_t)head_tok * (D / 2) + lane * 16;
+        v_src = a.vc + (size_t)head_tok * (D / 2) + lane * 16;
+        table = a.table + (size_t)s.b * a.max_blocks;
+        in = 0;
+        ids = blocks(0);
+        ids_next = blocks(32);
 #pragma unroll
-        for (int i = 0; i < S::STAGES - 1; ++i) ask(s, i);
+        for (int i = 0; i < S::STAGES - 1; ++i) ask(i);
     };
 
     Segment s;
@@ -174,11 +230,10 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     while (more) {
         const int row0 = s.row0, nr = s.nr, h = s.h, parts = s.parts;
         const int p0 = s.len - s.nq;                          // position of the request's first row
-        const int p_lo = s.p_lo, p_hi = s.p_hi;
 
         // queries as B fragments: lane (g, c) holds dims 32 c .. of row g, per 8 dims two k steps
         uint32_t q[NT][DB][16];
-        float qf[NT][2], qs[NT][2];                           // of rows 2 c and 2 c + 1: factor, sum
+        u64 qf[NT], qs[NT];                                   // of rows 2 c and 2 c + 1: factor, sum
         int pos[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -220,18 +275,21 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             // a row that is not finite has no result: NaN
             const float f = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+            float fr[2], sr[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int from = (2 * c + i) * 4;
-                const float fr = __shfl_sync(0xffffffffu, f, from);
-                qf[t][i] = fr * 16777216.f;                   // codes come as n 2^-24
-                qs[t][i] = fr * __shfl_sync(0xffffffffu, sum, from);
-                const int k = t * 8 + 2 * c + i;
+                const int from = (2 * c + i) * 4, k = t * 8 + 2 * c + i;
+                fr[i] = __shfl_sync(0xffffffffu, f, from);
+                sr[i] = fr[i] * __shfl_sync(0xffffffffu, sum, from);
                 pos[t][i] = k < nr ? p0 + (row0 + k) / a.group : -1;
             }
+            qf[t] = pack(fr[0] * 16777216.f, fr[1] * 16777216.f);      // codes come as n 2^-24
+            qs[t] = pack(sr[0], sr[1]);
         }
 
-        float o[NT][DB * 8][4], ones[NT][4], l[NT][2], mid[NT][2], ref[NT][2];
+        float o[NT][DB * 8][4], ones[NT][4];
+        u64 l2[NT], mid2[NT], nref[NT];                       // sums; minus the references
+        uint32_t with_ref = 0;                                // rows that have one, or are none, a bit each
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -240,39 +298,47 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                 for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) ones[t][k] = 0.f;
+            l2[t] = mid2[t] = 0;
+            nref[t] = 0;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                l[t][k] = mid[t][k] = 0.f;
-                ref[t][k] = kLow;
-            }
+            for (int k = 0; k < 2; ++k)
+                if (t * 8 + 2 * c + k >= nr) with_ref |= 1u << (2 * t + k);
         }
+        bool wait_ref = __any_sync(0xffffffffu, with_ref != (1u << (2 * NT)) - 1);
 
-        for (int i = 0; i < s.n; ++i) {
-            const int t0 = (s.t0 + i) * kTile + warp * 16;
+        const int n = steps, t_first = t_of;
+        uint32_t next = 0;                                    // stage that is read next, in bytes
+        for (int i = 0; i < n; ++i) {
+            const int t0 = t_first + i * kTile;
             copy_wait<S::STAGES - 2>();
             __syncwarp();                                     // step i is there; step i - 1 has been read
-            ask(s, i + S::STAGES - 1);
-            if (absent >> (i & 31) & 1) continue;             // (a block that is none reads as absent)
-            const unsigned char* const st = ring + (i % S::STAGES) * S::kStage;
+            ask(i + S::STAGES - 1);
+            const uint32_t st = ring + next;
+            next = next == (S::STAGES - 1) * S::kStage ? 0 : next + S::kStage;
+            if (absent >> (i & 31) & 1) continue;
             uint4 k[2][DB];
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
-                k[0][d] = *reinterpret_cast<const uint4*>(st + k_at<DB>(g, 4 * d + c));
-                k[1][d] = *reinterpret_cast<const uint4*>(st + k_at<DB>(g + 8, 4 * d + c));
+                k[0][d] = lds128(st + k_at<DB>(g, 4 * d + c));
+                k[1][d] = lds128(st + k_at<DB>(g, 4 * d + c) + 8 * (D / 2));
             }
-            const uint32_t* const scales = reinterpret_cast<const uint32_t*>(st + 2 * S::kCodes);
-            const uint32_t ksm[2] = {scales[g], scales[g + 8]}, vsm[2] = {scales[16 + g], scales[24 + g]};
+            uint32_t ksm[2], vsm[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ksm[j] = lds32(st + 2 * S::kCodes + g * 4 + j * 32);
+                vsm[j] = lds32(st + 2 * S::kCodes + 64 + g * 4 + j * 32);
+            }
             // V: tokens 2 c, 2 c + 1, and 8 more on, dims 16 DB g ..
             uint32_t v[4][2 * DB];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t t = 2 * c + (j & 1) + 8 * (j >> 1);
+                const uint32_t at = st + S::kCodes + v_at<DB>(2 * c + (j & 1), DB == 1 ? g >> 1 : g) + (j >> 1) * (8 * D / 2);
                 if (DB == 1) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(st + S::kCodes + v_at<DB>(t, g >> 1) + (g & 1) * 8);
+                    const uint2 x = lds64(at + (g & 1) * 8);
                     v[j][0] = x.x;
                     v[j][1] = x.y;
                 } else {
-                    const uint4 x = *reinterpret_cast<const uint4*>(st + S::kCodes + v_at<DB>(t, g));
+                    const uint4 x = lds128(at);
                     v[j][0] = x.x;
                     v[j][1] = x.y;
                     v[j][2 * DB - 2] = x.z;
@@ -304,51 +370,65 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                 }
             }
             // exponents with V's scale, relative to the rows' references
-            float kss[2], km[2], lv[2], iv[2], cm[2];
+            u64 ks2[2], km2[2], lv2[2], iv2[2], cm2[2];       // of tokens g and g + 8
+            const bool tail = t0 + 16 > s.len;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bool there = t0 + g + 8 * j < s.len;     // (what lies behind the request may be anything)
-                kss[j] = bf_lo(ksm[j]);
-                km[j] = bf_hi(ksm[j]);
-                const float vsc = fmaxf(bf_lo(vsm[j]), kLeastScale);
-                lv[j] = lg2(vsc);
-                iv[j] = there ? __fdividef(1.f, vsc) : 0.f;
-                cm[j] = there ? fmaf(8.f, vsc, bf_hi(vsm[j])) : 0.f;
+                const float vsc = fmaxf(bf_lo(vsm[j]), kLeastScale), lv = lg2(vsc);
+                float iv = rcp(vsc), cm = fmaf(8.f, vsc, bf_hi(vsm[j])) * iv;
+                // (what lies behind the request may be anything)
+                if (tail && t0 + g + 8 * j >= s.len) iv = cm = 0.f;
+                const float ksc = bf_lo(ksm[j]), km = bf_hi(ksm[j]);
+                ks2[j] = pack(ksc, ksc);
+                km2[j] = pack(km, km);
+                lv2[j] = pack(lv, lv);
+                iv2[j] = pack(iv, iv);
+                cm2[j] = pack(cm, cm);
             }
-            const bool edge = t0 + 15 > p_lo || (a.window && t0 <= p_hi - a.window);
+            const bool edge = t0 + 15 > s.p_lo || (a.window && t0 <= s.p_hi - a.window);
             float y[NT][4], top = kLow;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = j & 1, tk = j >> 1;
-                    float x = fmaf((sc4[t][j] + sc4b[t][j]) * qf[t][col], kss[tk], fmaf(km[tk], qs[t][col], lv[tk]));
+                for (int j = 0; j < 2; ++j) {
+                    const u64 acc = add2(pack(sc4[t][2 * j], sc4[t][2 * j + 1]), pack(sc4b[t][2 * j], sc4b[t][2 * j + 1]));
+                    const u64 b2 = add2(fma2(km2[j], qs[t], lv2[j]), nref[t]);
+                    unpack(fma2(mul2(acc, qf[t]), ks2[j], b2), y[t][2 * j], y[t][2 * j + 1]);
                     if (edge) {
-                        const int tt = t0 + g + 8 * tk, p = pos[t][col];
-                        if (tt > p || (a.window && tt <= p - a.window)) x = -INFINITY;
+                        const int tt = t0 + g + 8 * j;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (tt > pos[t][x] || (a.window && tt <= pos[t][x] - a.window)) y[t][2 * j + x] = -INFINITY;
                     }
-                    y[t][j] = x;
-                    top = fmaxf(top, x - ref[t][col]);
+                    top = fmaxf(top, fmaxf(y[t][2 * j], y[t][2 * j + 1]));
                 }
-            if (__any_sync(0xffffffffu, top > kRoom)) {
+            if (__any_sync(0xffffffffu, top > kRoom) || wait_ref) {
                 // new references: the maximum of the 16 tokens per row
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    float f[2];
+                    float f[2], nr2[2];
+                    unpack(nref[t], nr2[0], nr2[1]);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
+                        const uint32_t bit = 1u << (2 * t + j);
                         float m = fmaxf(y[t][j], y[t][j + 2]);
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
                         f[j] = 1.f;
-                        if (m - ref[t][j] > kHead) {          // every row that grew, while at it
-                            const float now = m - kHead;
-                            f[j] = ex2(ref[t][j] - now);
-                            ref[t][j] = now;
+                        // every row that grew, while at it; a row's first tokens bring it its first one
+                        if (m > kHead || (!(with_ref & bit) && m != -INFINITY)) {
+                            const float by = kHead - m;
+                            f[j] = with_ref & bit ? ex2(by) : 0.f;
+                            nr2[j] += by;
+                            y[t][j] += by;
+                            y[t][j + 2] += by;
+                            with_ref |= bit;
                         }
-                        l[t][j] *= f[j];
-                        mid[t][j] *= f[j];
                     }
+                    const u64 f2 = pack(f[0], f[1]);
+                    nref[t] = pack(nr2[0], nr2[1]);
+                    l2[t] = mul2(l2[t], f2);
+                    mid2[t] = mul2(mid2[t], f2);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) ones[t][x] *= f[x & 1];
 #pragma unroll
@@ -356,20 +436,19 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
 #pragma unroll
                         for (int x = 0; x < 4; ++x) o[t][m][x] *= f[x & 1];
                 }
+                wait_ref = __any_sync(0xffffffffu, with_ref != (1u << (2 * NT)) - 1);
             }
             uint32_t p[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                float w[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    w[j] = ex2(y[t][j] - ref[t][j & 1]);
-                    const float x = w[j] * iv[j >> 1];
-                    l[t][j & 1] += x;
-                    mid[t][j & 1] = fmaf(x, cm[j >> 1], mid[t][j & 1]);
+                for (int j = 0; j < 2; ++j) {
+                    const float w0 = ex2(y[t][2 * j]), w1 = ex2(y[t][2 * j + 1]);
+                    const u64 w2 = pack(w0, w1);
+                    l2[t] = fma2(w2, iv2[j], l2[t]);
+                    mid2[t] = fma2(w2, cm2[j], mid2[t]);
+                    p[t][j] = transposed(half2_bits(w0, w1));
                 }
-                p[t][0] = transposed(half2_bits(w[0], w[1]));
-                p[t][1] = transposed(half2_bits(w[2], w[3]));
                 constexpr uint32_t one = 0x3c003c00u;
                 mma(ones[t], one, one, one, one, p[t][0], p[t][1]);
             }
@@ -396,26 +475,31 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
         // the next segment's first steps on their way
         Segment then;
         __syncwarp();
+
         more = next_segment<RT, false>(a, first, ch, cta, &u, u1, &then);
         if (more) ask_first(then);
 
         // -------------------------------------------------------- the warps' sums together
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+            float l[2], mid[2], nr2[2];
+            unpack(l2[t], l[0], l[1]);
+            unpack(mid2[t], mid[0], mid[1]);
+            unpack(nref[t], nr2[0], nr2[1]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) {
-                    l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], x);
-                    mid[t][j] += __shfl_xor_sync(0xffffffffu, mid[t][j], x);
+                    l[j] += __shfl_xor_sync(0xffffffffu, l[j], x);
+                    mid[j] += __shfl_xor_sync(0xffffffffu, mid[j], x);
                 }
                 const int row = t * 8 + 2 * c + j;
-                if (g == 0) stats[warp * RT + row] = make_float2(ref[t][j], l[t][j]);
+                if (g == 0) stats[warp * RT + row] = make_float2(-nr2[j], l[j]);
                 float* dst = outs + (warp * RT + row) * S::kPitch;
 #pragma unroll
                 for (int m = 0; m < DB * 8; ++m) {
                     // o[m][j]: an even dim, n 2^-24; o[m][j + 2]: the next one, 16 times that
-                    const float add = fmaf(-8.f, ones[t][j], mid[t][j]);
+                    const float add = fmaf(-8.f, ones[t][j], mid[j]);
                     *reinterpret_cast<float2*>(dst + (m * 8 + g) * 2) =
                         make_float2(fmaf(o[t][m][j], 16777216.f, add), fmaf(o[t][m][j + 2], 1048576.f, add));
                 }
