@@ -34,7 +34,7 @@ namespace {
 
 using namespace split;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kHead = 10.f;            // log2 of the weight that a new reference gives a row's maximum
 constexpr float kRoom = 15.5f;           // a row's reference moves when a weight would pass 2^15.5
@@ -44,13 +44,17 @@ constexpr float kLeastScale = 5.421010862427522e-20f;   // 2^-64
 template <int DB_, int NT_>
 struct Shape {
     static constexpr int DB = DB_, NT = NT_, RT = 8 * NT, D = 128 * DB;
-    static constexpr int CTAS = DB * NT == 1 ? 2 : 1;
+    static constexpr int CTAS = DB == 1 ? (NT == 1 ? 4 : 2) : 2;
     static constexpr int kPitch = D + 8;                       // floats of a row of the warps' outputs
     static constexpr int kOutBytes = kWarps * RT * kPitch * 4;
     static constexpr int kStatBytes = kWarps * RT * 8;         // reference and sum
-    static constexpr int kCodes = 16 * D / 2;                  // 16 tokens of K or V
-    static constexpr int kStage = 2 * kCodes + 128;            // and their scales
-    static constexpr int STAGES = DB == 1 ? 4 : 3;             // of each warp's ring
+    // A step of a warp is SUB times 16 tokens: two, so that what a step costs beside its products is
+    // shared, where the registers are there.
+    static constexpr int SUB = DB == 1 ? 2 : 1;
+    static constexpr int kTokens = 16 * SUB, kStride = kWarps * kTokens;     // of a warp's step, of the CTA's
+    static constexpr int kCodes = kTokens * D / 2;             // bytes of K or V in a step
+    static constexpr int kStage = 2 * kCodes + 8 * kTokens;    // and their scales
+    static constexpr int STAGES = DB == 1 ? 2 : 4;             // of each warp's ring
     static constexpr int kRing = kWarps * STAGES * kStage;
 };
 
@@ -142,7 +146,7 @@ __device__ __forceinline__ uint32_t v_at(uint32_t t, uint32_t p) {
 // ---------------------------------------------------------------- the kernel
 template <typename S>
 __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid_constant__ Args a) {
-    constexpr int DB = S::DB, NT = S::NT, RT = S::RT, D = S::D;
+    constexpr int DB = S::DB, NT = S::NT, RT = S::RT, D = S::D, SUB = S::SUB;
     extern __shared__ __align__(16) unsigned char sm[];
     float* const outs = reinterpret_cast<float*>(sm);                       // [warp][row][kPitch]
     float2* const stats = reinterpret_cast<float2*>(sm + S::kOutBytes);     // [warp][row]: reference, sum
@@ -162,66 +166,84 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     const int u1 = ch.begin(cta + 1);
 
     // -------------------------------------------------------- the warp's ring
-    // A step is the warp's 16 tokens of one tile; tokens t_of + 128 i of steps i < steps.
-    // The blocks of 32 steps are held a lane each.
+    // Step i takes tokens t_of + kStride i ..; the blocks of the next 32 times 16 tokens are held a
+    // lane each.
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + S::kOutBytes + S::kStatBytes + warp * (S::STAGES * S::kStage));
-    constexpr int P = 4 * DB, kRowsAt = 32 / P;               // 16-byte pieces of a row; rows that the lanes copy at once
-    const uint32_t k_to = k_at<DB>(lane / P, lane % P);
-    uint32_t v_to[S::kCodes / 512];
-#pragma unroll
-    for (int j = 0; j < S::kCodes / 512; ++j) v_to[j] = S::kCodes + v_at<DB>(lane / P + j * kRowsAt, lane % P);
-    const uint32_t* const scale_src = (lane < 4 ? a.ks : a.vs - 16) + lane * 4;
-    const uint8_t *k_src = nullptr, *v_src = nullptr;         // this lane's, at the head's first token
+    constexpr int P = 4 * DB, kCopies = S::kCodes / 512;      // 16-byte pieces of a row, and of K a lane
+    constexpr int kScaleLanes = S::kTokens / 4;
+    const uint32_t k_to = k_at<DB>(lane / P, lane % P), v_to = v_at<DB>(lane / P, lane % P);
+    const uint32_t* const scale_src = (lane < kScaleLanes ? a.ks : a.vs - S::kTokens) + lane * 4;
+    const bool small = SUB == 2 && bsz == 16;                 // a step has two blocks
+    const uint8_t* k_src = nullptr;                           // this lane's, at the head's first token
+    const long long v_off = a.vc - a.kc;
     const int32_t* table = nullptr;
-    int head_tok = 0, t_of = 0, steps = 0, ids = -1, ids_next = -1;
-    uint32_t in = 0;                                          // stage that is filled next, in bytes
-    uint32_t absent = 0;                                      // of the last 32 steps asked for, a bit each (by step % 32)
-    auto blocks = [&](int from) -> int {                      // this lane's of steps from ..
-        return from + lane < steps ? __ldg(table + ((t_of + (from + lane) * kTile) >> a.bs_log2)) : -1;
+    int head_tok = 0, t_of = 0, p_last = 0, see_first = 0, steps = 0, ids = -1, ids_next = -1;
+    uint32_t absent = 0;                                      // of the last 32 times 16 tokens asked for, a bit each
+    auto blocks = [&](int from) -> int {                      // this lane's of 16 tokens, from step ..
+        const int t = t_of + (from + lane / SUB) * S::kStride + (lane % SUB) * 16;
+        return from + lane / SUB < steps && t <= p_last ? __ldg(table + (t >> a.bs_log2)) : -1;
     };
-    auto ask = [&](int i) {                                   // step i into its stage
+    auto ask = [&](int i, uint32_t stage) {                   // step i into its stage
         if (i < steps) {
-            if ((i & 31) == 0 && i > 0) {
+            if ((i & (32 / SUB - 1)) == 0 && i > 0) {
                 ids = ids_next;
-                ids_next = blocks(i + 32);
+                ids_next = blocks(i + 32 / SUB);
             }
-            const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-            const bool there = (uint32_t)id < (uint32_t)a.n_blocks;
-            const uint32_t bit = 1u << (i & 31);
-            absent = there ? absent & ~bit : absent | bit;    // (a block that is none reads as absent)
-            if (there) {
-                const int at = (t_of + i * kTile) & (bsz - 1);
-                const long long off = (long long)id * a.block_stride + at * (D / 2);
-                const uint32_t to = ring + in;
+            const uint32_t to = ring + stage;
+            const int at = (t_of + i * S::kStride) & (bsz - 1);
 #pragma unroll
-                for (int j = 0; j < S::kCodes / 512; ++j) {
-                    copy16(to + k_to + j * 512, k_src + off + j * 512);
-                    copy16(to + v_to[j], v_src + off + j * 512);
+            for (int sub = 0; sub < SUB; ++sub) {
+                if (sub > 0 && !small) break;
+                const int j = (i * SUB + sub) & 31;
+                const int id = __shfl_sync(0xffffffffu, ids, j);
+                const bool there = (uint32_t)id < (uint32_t)a.n_blocks;
+                const uint32_t bit = (SUB == 2 && !small ? 3u : 1u) << j;
+                absent = there ? absent & ~bit : absent | bit;        // (a block that is none reads as absent)
+                if (!there) {
+                    const int t = t_of + i * S::kStride + sub * 16;
+                    if (!small || (t <= p_last && t + 15 >= see_first)) bad = true;
+                    continue;
                 }
-                if (lane < 8)
-                    copy16(to + 2 * S::kCodes + lane * 16, scale_src + (((size_t)id * a.kv_heads << a.bs_log2) + (head_tok + at)));
-            } else {
-                bad = true;
+                const uint8_t* const kp = k_src + ((long long)id * a.block_stride + at * (D / 2));
+                const uint8_t* const vp = kp + v_off;
+                const uint32_t* const sp = scale_src + (((size_t)id * a.kv_heads << a.bs_log2) + (head_tok + at));
+                if (SUB == 2 && small) {
+                    // 16 tokens: half of the copies, and of the scales' lanes
+#pragma unroll
+                    for (int x = 0; x < kCopies / 2; ++x) {
+                        copy16(to + k_to + sub * (S::kCodes / 2) + x * 512, kp + x * 512);
+                        copy16(to + v_to + S::kCodes + sub * (S::kCodes / 2) + x * 512, vp + x * 512);
+                    }
+                    if (lane < 2 * kScaleLanes && (lane % kScaleLanes) < 4) copy16(to + 2 * S::kCodes + lane * 16 + sub * 64, sp);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < kCopies; ++x) {
+                        copy16(to + k_to + x * 512, kp + x * 512);
+                        copy16(to + (DB == 1 ? v_to : v_at<DB>(lane / P + x * (32 / P), lane % P) - x * 512) + S::kCodes + x * 512,
+                               vp + x * 512);
+                    }
+                    if (lane < 2 * kScaleLanes) copy16(to + 2 * S::kCodes + lane * 16, sp);
+                }
             }
         }
-        in = in == (S::STAGES - 1) * S::kStage ? 0 : in + S::kStage;
         copy_commit();
     };
     auto ask_first = [&](const Segment& s) {
         // the steps that some row sees (what none sees may have been given up)
-        const int t0 = s.t0 * kTile + warp * 16, t1 = min((s.t0 + s.n - 1) * kTile + warp * 16, s.p_hi);
-        const int skip = a.window && t0 + 15 <= s.p_lo - a.window ? (s.p_lo - a.window - t0 - 15) / kTile + 1 : 0;
-        t_of = t0 + skip * kTile;
-        steps = s.n > 0 && t_of <= t1 ? (t1 - t_of) / kTile + 1 : 0;
+        const int t0 = s.t0 * kTile + warp * S::kTokens, t1 = min((s.t0 + s.n) * kTile - 1, s.p_hi);
+        const int gone = s.p_lo - a.window - t0;              // tokens from t0 on that no row sees any more, less one
+        const int skip = a.window && gone >= S::kTokens - 1 ? (gone - S::kTokens + 1) / S::kStride + 1 : 0;
+        t_of = t0 + skip * S::kStride;
+        p_last = s.p_hi;
+        see_first = a.window ? s.p_lo - a.window + 1 : 0;
+        steps = s.n > 0 && t_of <= t1 ? (t1 - t_of) / S::kStride + 1 : 0;
         head_tok = s.h << a.bs_log2;
         k_src = a.kc + (size_t)head_tok * (D / 2) + lane * 16;
-        v_src = a.vc + (size_t)head_tok * (D / 2) + lane * 16;
         table = a.table + (size_t)s.b * a.max_blocks;
-        in = 0;
         ids = blocks(0);
-        ids_next = blocks(32);
+        ids_next = blocks(32 / SUB);
 #pragma unroll
-        for (int i = 0; i < S::STAGES - 1; ++i) ask(i);
+        for (int i = 0; i < S::STAGES - 1; ++i) ask(i, i * S::kStage);
     };
 
     Segment s;
@@ -306,104 +328,81 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
         }
         bool wait_ref = __any_sync(0xffffffffu, with_ref != (1u << (2 * NT)) - 1);
 
-        const int n = steps, t_first = t_of;
-        uint32_t next = 0;                                    // stage that is read next, in bytes
-        for (int i = 0; i < n; ++i) {
-            const int t0 = t_first + i * kTile;
+        const int n = steps;
+        int t0 = t_of;
+        uint32_t out_of = 0, into = (S::STAGES - 1) * S::kStage;      // stages that are read and filled next, in bytes
+        for (int i = 0; i < n; ++i, t0 += S::kStride) {
             copy_wait<S::STAGES - 2>();
             __syncwarp();                                     // step i is there; step i - 1 has been read
-            ask(i + S::STAGES - 1);
-            const uint32_t st = ring + next;
-            next = next == (S::STAGES - 1) * S::kStage ? 0 : next + S::kStage;
-            if (absent >> (i & 31) & 1) continue;
-            uint4 k[2][DB];
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                k[0][d] = lds128(st + k_at<DB>(g, 4 * d + c));
-                k[1][d] = lds128(st + k_at<DB>(g, 4 * d + c) + 8 * (D / 2));
-            }
-            uint32_t ksm[2], vsm[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ksm[j] = lds32(st + 2 * S::kCodes + g * 4 + j * 32);
-                vsm[j] = lds32(st + 2 * S::kCodes + 64 + g * 4 + j * 32);
-            }
-            // V: tokens 2 c, 2 c + 1, and 8 more on, dims 16 DB g ..
-            uint32_t v[4][2 * DB];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = st + S::kCodes + v_at<DB>(2 * c + (j & 1), DB == 1 ? g >> 1 : g) + (j >> 1) * (8 * D / 2);
-                if (DB == 1) {
-                    const uint2 x = lds64(at + (g & 1) * 8);
-                    v[j][0] = x.x;
-                    v[j][1] = x.y;
-                } else {
-                    const uint4 x = lds128(at);
-                    v[j][0] = x.x;
-                    v[j][1] = x.y;
-                    v[j][2 * DB - 2] = x.z;
-                    v[j][2 * DB - 1] = x.w;
-                }
-            }
+            ask(i + S::STAGES - 1, into);
+            const uint32_t st = ring + out_of;
+            into = out_of;
+            out_of = out_of == (S::STAGES - 1) * S::kStage ? 0 : out_of + S::kStage;
+            const uint32_t off = absent >> (i * SUB & 31);    // 16 tokens that are not there, a bit each
+            if ((off & ((1u << SUB) - 1)) == (1u << SUB) - 1) continue;
+            const bool odd = t0 + S::kTokens - 1 > s.p_lo || (a.window && t0 <= s.p_hi - a.window) || (off & ((1u << SUB) - 1));
 
             // scores
-            float sc4[NT][4], sc4b[NT][4];                    // two chains
+            float x[SUB][NT][4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sc4[t][j] = sc4b[t][j] = 0.f;
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const uint32_t w0[4] = {k[0][d].x, k[0][d].y, k[0][d].z, k[0][d].w};
-                const uint32_t w1[4] = {k[1][d].x, k[1][d].y, k[1][d].z, k[1][d].w};
+                    for (int j = 0; j < 4; ++j) x[u][t][j] = 0.f;
+                const uint32_t kp = st + u * (S::kCodes / SUB);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int d = 0; d < DB; ++d) {
+                    const uint4 k0 = lds128(kp + k_at<DB>(g, 4 * d + c)), k1 = lds128(kp + k_at<DB>(g, 4 * d + c) + 8 * (D / 2));
+                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        mma(sc4[t], w0[j] & 0x000f000fu, w1[j] & 0x000f000fu, w0[j] & 0x00f000f0u, w1[j] & 0x00f000f0u,
-                            q[t][d][4 * j], q[t][d][4 * j + 1]);
-                    const uint32_t x0 = w0[j] >> 8, x1 = w1[j] >> 8;
+                    for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        mma(sc4b[t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
-                            q[t][d][4 * j + 2], q[t][d][4 * j + 3]);
+                        for (int t = 0; t < NT; ++t)
+                            mma(x[u][t], w0[j] & 0x000f000fu, w1[j] & 0x000f000fu, w0[j] & 0x00f000f0u, w1[j] & 0x00f000f0u,
+                                q[t][d][4 * j], q[t][d][4 * j + 1]);
+                        const uint32_t x0 = w0[j] >> 8, x1 = w1[j] >> 8;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            mma(x[u][t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
+                                q[t][d][4 * j + 2], q[t][d][4 * j + 3]);
+                    }
                 }
             }
             // exponents with V's scale, relative to the rows' references
-            u64 ks2[2], km2[2], lv2[2], iv2[2], cm2[2];       // of tokens g and g + 8
-            const bool tail = t0 + 16 > s.len;
+            float iv[SUB][2], cm[SUB][2];                     // of tokens g and g + 8
+            float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float vsc = fmaxf(bf_lo(vsm[j]), kLeastScale), lv = lg2(vsc);
-                float iv = rcp(vsc), cm = fmaf(8.f, vsc, bf_hi(vsm[j])) * iv;
-                // (what lies behind the request may be anything)
-                if (tail && t0 + g + 8 * j >= s.len) iv = cm = 0.f;
-                const float ksc = bf_lo(ksm[j]), km = bf_hi(ksm[j]);
-                ks2[j] = pack(ksc, ksc);
-                km2[j] = pack(km, km);
-                lv2[j] = pack(lv, lv);
-                iv2[j] = pack(iv, iv);
-                cm2[j] = pack(cm, cm);
-            }
-            const bool edge = t0 + 15 > s.p_lo || (a.window && t0 <= s.p_hi - a.window);
-            float y[NT][4], top = kLow;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int u = 0; u < SUB; ++u)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const u64 acc = add2(pack(sc4[t][2 * j], sc4[t][2 * j + 1]), pack(sc4b[t][2 * j], sc4b[t][2 * j + 1]));
-                    const u64 b2 = add2(fma2(km2[j], qs[t], lv2[j]), nref[t]);
-                    unpack(fma2(mul2(acc, qf[t]), ks2[j], b2), y[t][2 * j], y[t][2 * j + 1]);
-                    if (edge) {
-                        const int tt = t0 + g + 8 * j;
+                    const uint32_t at = st + 2 * S::kCodes + (u * 16 + j * 8 + g) * 4;
+                    const uint32_t ksm = lds32(at), vsm = lds32(at + 4 * S::kTokens);
+                    const float vsc = fmaxf(bf_lo(vsm), kLeastScale), lv = lg2(vsc);
+                    iv[u][j] = rcp(vsc);
+                    cm[u][j] = fmaf(8.f, vsc, bf_hi(vsm)) * iv[u][j];
+                    const u64 ks2 = pack(bf_lo(ksm), bf_lo(ksm)), km2 = pack(bf_hi(ksm), bf_hi(ksm)), lv2 = pack(lv, lv);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            if (tt > pos[t][x] || (a.window && tt <= pos[t][x] - a.window)) y[t][2 * j + x] = -INFINITY;
+                    for (int t = 0; t < NT; ++t) {
+                        const u64 b2 = add2(fma2(km2, qs[t], lv2), nref[t]);
+                        unpack(fma2(mul2(pack(x[u][t][2 * j], x[u][t][2 * j + 1]), qf[t]), ks2, b2), x[u][t][2 * j], x[u][t][2 * j + 1]);
                     }
-                    top = fmaxf(top, fmaxf(y[t][2 * j], y[t][2 * j + 1]));
+                    if (odd) {
+                        // (what lies behind the request, or in no block, may be anything)
+                        const int tt = t0 + u * 16 + g + 8 * j;
+                        const bool none = tt >= s.len || (off >> u & 1);
+                        if (none) iv[u][j] = cm[u][j] = 0.f;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                if (none || tt > pos[t][r] || (a.window && tt <= pos[t][r] - a.window)) x[u][t][2 * j + r] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) top = fmaxf(top, fmaxf(x[u][t][2 * j], x[u][t][2 * j + 1]));
                 }
             if (__any_sync(0xffffffffu, top > kRoom) || wait_ref) {
-                // new references: the maximum of the 16 tokens per row
+                // new references: the maximum of the step's tokens per row
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     float f[2], nr2[2];
@@ -411,17 +410,22 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t bit = 1u << (2 * t + j);
-                        float m = fmaxf(y[t][j], y[t][j + 2]);
+                        float m = -INFINITY;
 #pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                        for (int u = 0; u < SUB; ++u) m = fmaxf(m, fmaxf(x[u][t][j], x[u][t][j + 2]));
+#pragma unroll
+                        for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
                         f[j] = 1.f;
                         // every row that grew, while at it; a row's first tokens bring it its first one
                         if (m > kHead || (!(with_ref & bit) && m != -INFINITY)) {
                             const float by = kHead - m;
                             f[j] = with_ref & bit ? ex2(by) : 0.f;
                             nr2[j] += by;
-                            y[t][j] += by;
-                            y[t][j + 2] += by;
+#pragma unroll
+                            for (int u = 0; u < SUB; ++u) {
+                                x[u][t][j] += by;
+                                x[u][t][j + 2] += by;
+                            }
                             with_ref |= bit;
                         }
                     }
@@ -430,43 +434,63 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                     l2[t] = mul2(l2[t], f2);
                     mid2[t] = mul2(mid2[t], f2);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) ones[t][x] *= f[x & 1];
+                    for (int w = 0; w < 4; ++w) ones[t][w] *= f[w & 1];
 #pragma unroll
                     for (int m = 0; m < DB * 8; ++m)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o[t][m][x] *= f[x & 1];
+                        for (int w = 0; w < 4; ++w) o[t][m][w] *= f[w & 1];
                 }
                 wait_ref = __any_sync(0xffffffffu, with_ref != (1u << (2 * NT)) - 1);
             }
-            uint32_t p[NT][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t p[NT][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float w0 = ex2(y[t][2 * j]), w1 = ex2(y[t][2 * j + 1]);
-                    const u64 w2 = pack(w0, w1);
-                    l2[t] = fma2(w2, iv2[j], l2[t]);
-                    mid2[t] = fma2(w2, cm2[j], mid2[t]);
-                    p[t][j] = transposed(half2_bits(w0, w1));
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float w0 = ex2(x[u][t][2 * j]), w1 = ex2(x[u][t][2 * j + 1]);
+                        const u64 w2 = pack(w0, w1);
+                        l2[t] = fma2(w2, pack(iv[u][j], iv[u][j]), l2[t]);
+                        mid2[t] = fma2(w2, pack(cm[u][j], cm[u][j]), mid2[t]);
+                        p[t][j] = transposed(half2_bits(w0, w1));
+                    }
+                    constexpr uint32_t one = 0x3c003c00u;
+                    mma(ones[t], one, one, one, one, p[t][0], p[t][1]);
                 }
-                constexpr uint32_t one = 0x3c003c00u;
-                mma(ones[t], one, one, one, one, p[t][0], p[t][1]);
-            }
-            // outputs
+                // outputs. V: tokens 2 c, 2 c + 1, and 8 more on, dims 16 DB g ..
+                uint32_t v[4][2 * DB];
 #pragma unroll
-            for (int j = 0; j < 2 * DB; ++j) {
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t at = st + S::kCodes + u * (S::kCodes / SUB) + v_at<DB>(2 * c + (j & 1), DB == 1 ? g >> 1 : g) +
+                                        (j >> 1) * (8 * D / 2);
+                    if (DB == 1) {
+                        const uint2 w = lds64(at + (g & 1) * 8);
+                        v[j][0] = w.x;
+                        v[j][1] = w.y;
+                    } else {
+                        const uint4 w = lds128(at);
+                        v[j][0] = w.x;
+                        v[j][1] = w.y;
+                        v[j][2 * DB - 2] = w.z;
+                        v[j][2 * DB - 1] = w.w;
+                    }
+                }
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t x0 = __byte_perm(v[0][j], v[1][j], half ? 0x7632 : 0x5410);
-                    uint32_t x1 = __byte_perm(v[2][j], v[3][j], half ? 0x7632 : 0x5410);
+                for (int j = 0; j < 2 * DB; ++j) {
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t x0 = __byte_perm(v[0][j], v[1][j], half ? 0x7632 : 0x5410);
+                        uint32_t x1 = __byte_perm(v[2][j], v[3][j], half ? 0x7632 : 0x5410);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            mma(o[t][j * 4 + half * 2 + m], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
-                                x1 & 0x00f000f0u, p[t][0], p[t][1]);
-                        x0 >>= 8;
-                        x1 >>= 8;
+                        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                mma(o[t][j * 4 + half * 2 + m], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
+                                    x1 & 0x00f000f0u, p[t][0], p[t][1]);
+                            x0 >>= 8;
+                            x1 >>= 8;
+                        }
                     }
                 }
             }
@@ -584,9 +608,9 @@ constexpr int kFew = 16;
 
 void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* arrivals) {
     chunk4_scratch(sm_count, o_floats, ml_floats);
-    *o_floats += (size_t)sm_count * 2 * 2 * 16 * 128;
-    *ml_floats += (size_t)sm_count * 2 * 4 * 16;
-    *arrivals = (size_t)sm_count * 9;
+    *o_floats += (size_t)sm_count * 4 * 2 * 16 * 128;
+    *ml_floats += (size_t)sm_count * 4 * 4 * 16;
+    *arrivals = (size_t)sm_count * 15;
 }
 
 cudaError_t set_attend4_attrs() {
