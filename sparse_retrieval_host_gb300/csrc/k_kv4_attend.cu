@@ -44,8 +44,8 @@ constexpr float kLeastScale = 5.421010862427522e-20f;   // 2^-64
 template <int DB_, int NT_>
 struct Shape {
     static constexpr int DB = DB_, NT = NT_, RT = 8 * NT, D = 128 * DB;
-    static constexpr int CTAS = DB == 1 ? (NT == 1 ? 4 : 2) : 2;
-    static constexpr int kPitch = D + 8;                       // floats of a row of the warps' outputs
+    static constexpr int CTAS = DB == 1 ? (NT == 1 ? 3 : 2) : 2;
+    static constexpr int kPitch = D + 4;                       // floats of a row of the warps' outputs
     static constexpr int kOutBytes = kWarps * RT * kPitch * 4;
     static constexpr int kStatBytes = kWarps * RT * 8;         // reference and sum
     // A step of a warp is SUB times 16 tokens: two, so that what a step costs beside its products is
@@ -56,6 +56,11 @@ struct Shape {
     static constexpr int kStage = 2 * kCodes + 8 * kTokens;    // and their scales
     static constexpr int STAGES = DB == 1 ? 2 : 4;             // of each warp's ring
     static constexpr int kRing = kWarps * STAGES * kStage;
+    // Queries as operands, and factor, sum and position of each row; twice, as the next segment's are
+    // made while this one's outputs are.
+    static constexpr int kQBytes = NT * DB * 2048, kRowBytes = RT * 16;
+    static constexpr int kOffStat = kOutBytes, kOffRing = kOffStat + kStatBytes, kOffQ = kOffRing + kRing;
+    static constexpr int kOffRow = kOffQ + 2 * kQBytes, kOffFirst = kOffRow + 2 * kRowBytes;
 };
 
 __device__ __forceinline__ float lg2(float x) {
@@ -113,6 +118,11 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // The transpose of an 8 x 8 matrix of fp16, two to a lane.
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
     uint32_t r;
@@ -149,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     constexpr int DB = S::DB, NT = S::NT, RT = S::RT, D = S::D, SUB = S::SUB;
     extern __shared__ __align__(16) unsigned char sm[];
     float* const outs = reinterpret_cast<float*>(sm);                       // [warp][row][kPitch]
-    float2* const stats = reinterpret_cast<float2*>(sm + S::kOutBytes);     // [warp][row]: reference, sum
-    int* const first = reinterpret_cast<int*>(sm + S::kOutBytes + S::kStatBytes + S::kRing);   // units before each request
+    float2* const stats = reinterpret_cast<float2*>(sm + S::kOffStat);      // [warp][row]: reference, sum
+    int* const first = reinterpret_cast<int*>(sm + S::kOffFirst);   // units before each request
     __shared__ long long warp_sums[33];
     __shared__ int last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     // -------------------------------------------------------- the warp's ring
     // Step i takes tokens t_of + kStride i ..; the blocks of the next 32 times 16 tokens are held a
     // lane each.
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + S::kOutBytes + S::kStatBytes + warp * (S::STAGES * S::kStage));
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + S::kOffRing + warp * (S::STAGES * S::kStage));
     constexpr int P = 4 * DB, kCopies = S::kCodes / 512;      // 16-byte pieces of a row, and of K a lane
     constexpr int kScaleLanes = S::kTokens / 4;
     const uint32_t k_to = k_at<DB>(lane / P, lane % P), v_to = v_at<DB>(lane / P, lane % P);
@@ -246,23 +256,14 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
         for (int i = 0; i < S::STAGES - 1; ++i) ask(i, i * S::kStage);
     };
 
-    Segment s;
-    bool more = next_segment<RT, false>(a, first, ch, cta, &u, u1, &s);
-    if (more) ask_first(s);
-    while (more) {
-        const int row0 = s.row0, nr = s.nr, h = s.h, parts = s.parts;
-        const int p0 = s.len - s.nq;                          // position of the request's first row
-
-        // queries as B fragments: lane (g, c) holds dims 32 c .. of row g, per 8 dims two k steps
-        uint32_t q[NT][DB][16];
-        u64 qf[NT], qs[NT];                                   // of rows 2 c and 2 c + 1: factor, sum
-        int pos[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int row = row0 + t * 8 + g, tok = row / a.group;
-            const bool on = t * 8 + g < nr;
+    // A segment's queries as B fragments: lane (g, c) holds dims 32 c .. of row g, per 8 dims two k steps.
+    // A warp makes those of 8 rows.
+    auto stage = [&](const Segment& s, int to) {
+        for (int t = warp; t < NT; t += kWarps) {
+            const int row = s.row0 + t * 8 + g, tok = row / a.group;
+            const bool on = t * 8 + g < s.nr;
             const uint16_t* x = a.q + (size_t)(s.q0 + (on ? tok : 0)) * a.q_row +
-                                (size_t)(h * a.group + (on ? row - tok * a.group : 0)) * D;
+                                (size_t)(s.h * a.group + (on ? row - tok * a.group : 0)) * D;
             uint4 w[DB][4];
             uint32_t m = 0;
 #pragma unroll
@@ -280,16 +281,17 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             const int e = min(max((int)(m >> 7) - 127 - 14, -120), 120);
             const float inv = __uint_as_float((uint32_t)(127 - e) << 23), inv16 = inv * 0.0625f;
             float sum = 0.f;
+            uint4* const q = reinterpret_cast<uint4*>(sm + S::kOffQ + to * S::kQBytes) + t * DB * 128 + lane;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // dims 0 .. 7: pairs (k, k + 4) as the codes of a word lie
                     const uint32_t v[4] = {w[d][i].x, w[d][i].y, w[d][i].z, w[d][i].w};
-                    q[t][d][4 * i] = half2_bits(bf_lo(v[0]) * inv, bf_lo(v[2]) * inv);
-                    q[t][d][4 * i + 1] = half2_bits(bf_hi(v[0]) * inv16, bf_hi(v[2]) * inv16);
-                    q[t][d][4 * i + 2] = half2_bits(bf_lo(v[1]) * inv, bf_lo(v[3]) * inv);
-                    q[t][d][4 * i + 3] = half2_bits(bf_hi(v[1]) * inv16, bf_hi(v[3]) * inv16);
+                    q[(d * 4 + i) * 32] = make_uint4(half2_bits(bf_lo(v[0]) * inv, bf_lo(v[2]) * inv),
+                                                     half2_bits(bf_hi(v[0]) * inv16, bf_hi(v[2]) * inv16),
+                                                     half2_bits(bf_lo(v[1]) * inv, bf_lo(v[3]) * inv),
+                                                     half2_bits(bf_hi(v[1]) * inv16, bf_hi(v[3]) * inv16));
 #pragma unroll
                     for (int k = 0; k < 4; ++k) sum += bf_lo(v[k]) * inv + bf_hi(v[k]) * inv;
                 }
@@ -297,17 +299,33 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             // a row that is not finite has no result: NaN
             const float f = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
-            float fr[2], sr[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int from = (2 * c + i) * 4, k = t * 8 + 2 * c + i;
-                fr[i] = __shfl_sync(0xffffffffu, f, from);
-                sr[i] = fr[i] * __shfl_sync(0xffffffffu, sum, from);
-                pos[t][i] = k < nr ? p0 + (row0 + k) / a.group : -1;
-            }
-            qf[t] = pack(fr[0] * 16777216.f, fr[1] * 16777216.f);      // codes come as n 2^-24
-            qs[t] = pack(sr[0], sr[1]);
+            if (c == 0)      // (codes come as n 2^-24)
+                reinterpret_cast<float4*>(sm + S::kOffRow + to * S::kRowBytes)[t * 8 + g] =
+                    make_float4(f * 16777216.f, f * sum, __int_as_float(on ? s.len - s.nq + tok : -1), 0.f);
         }
+    };
+
+    Segment s;
+    bool more = next_segment<RT, false>(a, first, ch, cta, &u, u1, &s);
+    if (more) {
+        ask_first(s);
+        stage(s, 0);
+    }
+    __syncthreads();
+    for (int turn = 0; more; turn ^= 1) {
+        const int row0 = s.row0, nr = s.nr, h = s.h, parts = s.parts;
+        u64 qf[NT], qs[NT];                                   // of rows 2 c and 2 c + 1: factor, sum
+        int pos[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float4* const at = reinterpret_cast<const float4*>(sm + S::kOffRow + turn * S::kRowBytes) + t * 8 + 2 * c;
+            const float4 x = at[0], y = at[1];
+            qf[t] = pack(x.x, y.x);
+            qs[t] = pack(x.y, y.y);
+            pos[t][0] = __float_as_int(x.z);
+            pos[t][1] = __float_as_int(y.z);
+        }
+        const uint32_t q_at = (uint32_t)__cvta_generic_to_shared(sm + S::kOffQ + turn * S::kQBytes) + lane * 16;
 
         float o[NT][DB * 8][4], ones[NT][4];
         u64 l2[NT], mid2[NT], nref[NT];                       // sums; minus the references
@@ -345,33 +363,42 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             // scores
             float x[SUB][NT][4];
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) {
+            for (int d = 0; d < DB; ++d) {
+                uint32_t w0[SUB][4], w1[SUB][4];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int u = 0; u < SUB; ++u) {
+                    const uint32_t kp = st + u * (S::kCodes / SUB) + k_at<DB>(g, 4 * d + c);
+                    const uint4 k0 = lds128(kp), k1 = lds128(kp + 8 * (D / 2));
+                    w0[u][0] = k0.x, w0[u][1] = k0.y, w0[u][2] = k0.z, w0[u][3] = k0.w;
+                    w1[u][0] = k1.x, w1[u][1] = k1.y, w1[u][2] = k1.z, w1[u][3] = k1.w;
+                }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[u][t][j] = 0.f;
-                const uint32_t kp = st + u * (S::kCodes / SUB);
+                for (int j = 0; j < 4; ++j) {
+                    uint4 q[NT];
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const uint4 k0 = lds128(kp + k_at<DB>(g, 4 * d + c)), k1 = lds128(kp + k_at<DB>(g, 4 * d + c) + 8 * (D / 2));
-                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+                    for (int t = 0; t < NT; ++t) q[t] = lds128(q_at + ((t * DB + d) * 4 + j) * 512);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            if (d == 0 && j == 0)
+                                mma_first(x[u][t], w0[u][j] & 0x000f000fu, w1[u][j] & 0x000f000fu, w0[u][j] & 0x00f000f0u,
+                                          w1[u][j] & 0x00f000f0u, q[t].x, q[t].y);
+                            else
+                                mma(x[u][t], w0[u][j] & 0x000f000fu, w1[u][j] & 0x000f000fu, w0[u][j] & 0x00f000f0u,
+                                    w1[u][j] & 0x00f000f0u, q[t].x, q[t].y);
+                        }
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        const uint32_t x0 = w0[u][j] >> 8, x1 = w1[u][j] >> 8;
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
-                            mma(x[u][t], w0[j] & 0x000f000fu, w1[j] & 0x000f000fu, w0[j] & 0x00f000f0u, w1[j] & 0x00f000f0u,
-                                q[t][d][4 * j], q[t][d][4 * j + 1]);
-                        const uint32_t x0 = w0[j] >> 8, x1 = w1[j] >> 8;
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            mma(x[u][t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
-                                q[t][d][4 * j + 2], q[t][d][4 * j + 3]);
+                            mma(x[u][t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, q[t].z, q[t].w);
                     }
                 }
             }
             // exponents with V's scale, relative to the rows' references
             float iv[SUB][2], cm[SUB][2];                     // of tokens g and g + 8
-            float top = -INFINITY;
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -387,8 +414,13 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                         const u64 b2 = add2(fma2(km2, qs[t], lv2), nref[t]);
                         unpack(fma2(mul2(pack(x[u][t][2 * j], x[u][t][2 * j + 1]), qf[t]), ks2, b2), x[u][t][2 * j], x[u][t][2 * j + 1]);
                     }
-                    if (odd) {
-                        // (what lies behind the request, or in no block, may be anything)
+                }
+            if (odd) {
+                // (what lies behind the request, or in no block, may be anything)
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
                         const int tt = t0 + u * 16 + g + 8 * j;
                         const bool none = tt >= s.len || (off >> u & 1);
                         if (none) iv[u][j] = cm[u][j] = 0.f;
@@ -398,9 +430,13 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                             for (int r = 0; r < 2; ++r)
                                 if (none || tt > pos[t][r] || (a.window && tt <= pos[t][r] - a.window)) x[u][t][2 * j + r] = -INFINITY;
                     }
+            }
+            float top = -INFINITY;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) top = fmaxf(top, fmaxf(x[u][t][2 * j], x[u][t][2 * j + 1]));
-                }
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    top = fmaxf(fmaxf(top, fmaxf(x[u][t][0], x[u][t][1])), fmaxf(x[u][t][2], x[u][t][3]));
             if (__any_sync(0xffffffffu, top > kRoom) || wait_ref) {
                 // new references: the maximum of the step's tokens per row
 #pragma unroll
@@ -501,7 +537,10 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
         __syncwarp();
 
         more = next_segment<RT, false>(a, first, ch, cta, &u, u1, &then);
-        if (more) ask_first(then);
+        if (more) {
+            ask_first(then);
+            stage(then, turn ^ 1);
+        }
 
         // -------------------------------------------------------- the warps' sums together
 #pragma unroll
@@ -578,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
 
 template <typename S>
 size_t smem_bytes(int n_req) {
-    return S::kOutBytes + S::kStatBytes + S::kRing + (size_t)n_req * sizeof(int);
+    return S::kOffFirst + (size_t)n_req * sizeof(int);
 }
 
 template <typename S>
