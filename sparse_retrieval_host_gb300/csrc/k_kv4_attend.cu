@@ -47,6 +47,7 @@ struct Shape {
     static constexpr int CTAS = DB == 1 ? (NT == 1 ? 3 : 2) : 2;
     static constexpr int kPitch = D + 4;                       // floats of a row of the warps' outputs
     static constexpr int kOutBytes = kWarps * RT * kPitch * 4;
+    static constexpr int SW = 3;                               // units that stand for a segment's start and end
     static constexpr int kStatBytes = kWarps * RT * 8;         // reference and sum
     // A step of a warp is SUB times 16 tokens: two, so that what a step costs beside its products is
     // shared, where the registers are there.
@@ -71,29 +72,6 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ float rcp(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-    return r;
-}
-// Pairs of fp32 values in one 64-bit register (one instruction for both).
-using u64 = unsigned long long;
-__device__ __forceinline__ u64 pack(float a, float b) {
-    u64 r;
-    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack(u64 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-    u64 r;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-    u64 r;
-    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-    u64 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
@@ -166,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
 
     Chunks ch;
-    if (!count<RT, false, kThreads>(a, first, warp_sums, &ch)) {
+    if (!count<RT, false, S::SW, kThreads>(a, first, warp_sums, &ch)) {
         pdl_wait();
         return;
     }
@@ -260,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     // A warp makes those of 8 rows.
     auto stage = [&](const Segment& s, int to) {
         for (int t = warp; t < NT; t += kWarps) {
-            const int row = s.row0 + t * 8 + g, tok = row / a.group;
+            const int row = s.row0 + t * 8 + g, tok = by_group(a, row);
             const bool on = t * 8 + g < s.nr;
             const uint16_t* x = a.q + (size_t)(s.q0 + (on ? tok : 0)) * a.q_row +
                                 (size_t)(s.h * a.group + (on ? row - tok * a.group : 0)) * D;
@@ -306,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     };
 
     Segment s;
-    bool more = next_segment<RT, false>(a, first, ch, cta, &u, u1, &s);
+    bool more = next_segment<RT, false, S::SW>(a, first, ch, cta, &u, u1, &s);
     if (more) {
         ask_first(s);
         stage(s, 0);
@@ -536,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
         Segment then;
         __syncwarp();
 
-        more = next_segment<RT, false>(a, first, ch, cta, &u, u1, &then);
+        more = next_segment<RT, false, S::SW>(a, first, ch, cta, &u, u1, &then);
         if (more) {
             ask_first(then);
             stage(then, turn ^ 1);
@@ -592,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             }
             if (parts == 1) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const int rr = row0 + row, tok = rr / a.group;
+                const int rr = row0 + row, tok = by_group(a, rr);
                 const __nv_bfloat162 v = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
                 *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)(s.q0 + tok) * a.out_row +
                                                    (size_t)(h * a.group + rr - tok * a.group) * D + d) = v;
@@ -602,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             }
         }
         if (parts > 1) {
+            __syncthreads();
             finish<RT, D>(a, s, tid, kThreads, &last, [] {
                 __syncthreads();
                 return true;
@@ -628,10 +607,9 @@ cudaError_t run(const Cache& c, Args a, bool beside, cudaStream_t st) {
     // (behind what the kernel beside it has)
     a.part_o = c.d_part_o + o;
     a.part_ml = c.d_part_ml + ml;
-    a.arrived = c.d_arrived + 3 * c.sm_count;
     a.arrived_n = grid;
     if (o + (size_t)grid * 2 * S::RT * S::D > c.part_o_floats || ml + (size_t)grid * 4 * S::RT > c.part_ml_floats ||
-        3 * ((size_t)c.sm_count + grid) > c.arrived_n)
+        3 * (size_t)grid > c.arrived_n)
         return cudaErrorInvalidValue;
     return launch_k(attend4_kernel<S>, dim3(grid), dim3(kThreads), smem_bytes<S>(a.n_req), st, beside, a);
 }
@@ -647,9 +625,9 @@ constexpr int kFew = 16;
 
 void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* arrivals) {
     chunk4_scratch(sm_count, o_floats, ml_floats);
-    *o_floats += (size_t)sm_count * 4 * 2 * 16 * 128;
-    *ml_floats += (size_t)sm_count * 4 * 4 * 16;
-    *arrivals = (size_t)sm_count * 15;
+    *o_floats += (size_t)sm_count * 2 * 2 * 16 * 128;
+    *ml_floats += (size_t)sm_count * 2 * 4 * 16;
+    *arrivals = (size_t)sm_count * 9;
 }
 
 cudaError_t set_attend4_attrs() {
@@ -679,11 +657,14 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
     a.part_o = c.d_part_o;
     a.part_ml = c.d_part_ml;
     a.arrived = c.d_arrived;
+    a.meta = c.d_meta;
+    a.ctrl = c.d_ctrl;
     a.err = c.d_err;
     a.n_req = n_req;
     a.n_rows = n_rows;
     a.kv_heads = c.cfg.n_kv_heads;
     a.group = n_heads / c.cfg.n_kv_heads;
+    a.per_group = a.group == 1 ? 0 : ~0ull / (unsigned)a.group + 1;
     a.rows_lo = 0;
     a.rows_hi = 1 << 30;
     a.bs_log2 = c.bs_log2;
@@ -703,7 +684,9 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
         if (e != cudaSuccess) return e;
     }
     const long long rows = beside ? kFew : (long long)a.group * ((n_rows + n_req - 1) / n_req);
-    return rows <= 8 ? run<Shape<1, 1>>(c, a, beside, st) : run<Shape<1, 2>>(c, a, beside, st);
+    cudaError_t e = rows <= 8 ? run<Shape<1, 1>>(c, a, beside, st) : run<Shape<1, 2>>(c, a, beside, st);
+    if (beside && e == cudaSuccess) e = launch_join4(c.sm_count, a, st);
+    return e;
 }
 
 }  // namespace kv8

@@ -18,8 +18,8 @@
 // 2,048 of shared memory (QK reads both operands: 1,024; PV one: 512; expanding writes 512): no unit
 // is free, the floor of one is that of all.
 //
-// Roles: warps 0-3 and 4-7 softmax of the two lanes, 8-11 expand K, 12-15 V (a thread a token, the
-// next tile's codes in registers), 16 issues the MMAs. All waits are on mbarriers and bounded.
+// Roles: warps 0-3 and 4-7 softmax of the two lanes, 8-11 expand K and V (a thread a token, the next
+// tile's codes in registers), 12 issues the MMAs: 13 warps, so that a thread has 128 registers. All waits are on mbarriers and bounded.
 #include "kv4_split.cuh"
 #include "umma.cuh"
 
@@ -31,12 +31,15 @@ using namespace umma;
 using namespace split;
 
 constexpr int kRT = 256, kD = 128;
-constexpr int kThreads = 17 * 32;
+constexpr int kExpand = 8, kIssue = 12, kPlan = 13;   // first warp that expands; those that issue MMAs and find segments
+constexpr int kThreads = (kPlan + 1) * 32;
 constexpr int kHalf = 16384;             // 128 rows of 64 fp16 values
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kOffK = 2 * kTileBytes;    // behind Q of the two lanes
 constexpr int kOffV = kOffK + 2 * kTileBytes;
 constexpr int kOffBars = kOffV + 2 * kTileBytes;
+constexpr int kSwitch = 8;               // half tiles that a row tile's start and end take the time of
+constexpr int kSegs = 4;                 // segments found ahead of their use
 constexpr int kInfo = 4;                 // tiles whose exponents are held
 constexpr float kHead = 10.f;            // log2 of the weight that a new reference gives a row's maximum
 constexpr float kRoom = 15.5f;           // a row's reference moves when a weight would pass 2^15.5
@@ -45,19 +48,22 @@ constexpr int kTop = 14;                 // exponent of the largest fp16 value o
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t k_info[kInfo], v_info[kInfo];   // a tile's exponent (and which tokens there are) is written
-    uint64_t max_in[2];                  // K's / V's warps have given a tile's maxima
+    uint64_t max_in;                     // the expanding warps have given a tile's maxima
     uint64_t s_full[2], p_full[2];       // of each lane: scores are in TMEM, weights are
     uint64_t q_full, o_full;             // queries are in shared memory; outputs are complete
     uint64_t met[2];                     // the softmax warps meet
     uint64_t drain;
+    uint64_t seg_full[kSegs], seg_empty[kSegs];   // a segment is found; every other warp has done with it
+    Segment seg[kSegs];                  // h < 0: no more
     long long warp_sums[33];
     uint32_t tmem_base;
-    int abort, last;
+    int abort;
     uint32_t most[2][2][4];              // [K, V][tile & 1][warp]: largest magnitude
     alignas(16) uint32_t there[kInfo][4];            // tokens that exist, a bit each
     float k_factor[kInfo];               // 2^(e - 14)
     int v_exp[kInfo];                    // e
     float2 stat[2][128];                 // reference and sum of each lane's rows
+    float factor[2][128];                // of each lane's rows' scores
 };
 
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -105,11 +111,26 @@ __device__ __forceinline__ uint4 values8(uint32_t w, __half2 s, __half2 s16, __h
     r.w = bits(__hfma2(__hsub2(as_half2((x & 0x00f000f0u) | 0x64006400u), k), s16, m));
     return r;
 }
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ float4 lds_float4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     uint32_t r;
     memcpy(&r, &h, 4);
     return r;
+}
+
+// Values of tokens whose bit is not set become `none`.
+__device__ __forceinline__ void mask32(uint32_t seen, float (&x)[32], float none) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        if (!(seen >> k & 1)) x[k] = none;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_constant__ Args a) {
@@ -127,7 +148,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             mbar_init(&bs.k_empty[i], 1);
             mbar_init(&bs.v_full[i], 4);
             mbar_init(&bs.v_empty[i], 1);
-            mbar_init(&bs.max_in[i], 4);
             mbar_init(&bs.s_full[i], 1);
             mbar_init(&bs.p_full[i], 4);
             mbar_init(&bs.met[i], 8);
@@ -136,41 +156,72 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             mbar_init(&bs.k_info[i], 4);
             mbar_init(&bs.v_info[i], 4);
         }
+        mbar_init(&bs.max_in, 4);
         mbar_init(&bs.q_full, 8);
         mbar_init(&bs.o_full, 1);
         mbar_init(&bs.drain, 1);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(&bs.seg_full[i], 1);
+            mbar_init(&bs.seg_empty[i], kPlan);
+        }
         bs.abort = 0;
         fence_mbar_init();
     }
     Chunks ch;
-    if (!count<kRT, true, kThreads>(a, first, bs.warp_sums, &ch)) return;      // every thread
-    if (warp == 16) tmem_alloc(&bs.tmem_base, 512);
+    if (!count<kRT, true, kSwitch, kThreads>(a, first, bs.warp_sums, &ch)) {            // every thread
+        if (blockIdx.x == 0 && tid == 0) a.ctrl[1] = 0;
+        return;
+    }
+    if (tid == 0) {
+        a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);            // no row tile goes on from this chunk, so far
+        if (blockIdx.x == 0) a.ctrl[1] = ch.n;
+    }
+    if (warp == kIssue) tmem_alloc(&bs.tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bs.tmem_base;                        // S of the lanes at 0 and 128, O at 256 and 384
     const int cta = blockIdx.x;
-    int u = ch.begin(cta);
-    const int u1 = ch.begin(cta + 1);
     bool ok = true;
-    Segment s;
     uint32_t G = 0;                                            // tiles before this segment
     // (what a warp does after a failed wait, all its lanes do)
     auto got = [&](uint64_t* bar, uint32_t parity) {
         return (bool)__all_sync(0xffffffffu, mbar_wait_abort(bar, parity & 1, abort) > 0);
     };
 
-    if (warp >= 8 && warp < 16) {
+    // segment k, once it is found; false: there are no more, or the wait failed
+    auto take = [&](uint32_t k) {
+        ok = got(&bs.seg_full[k % kSegs], k / kSegs);
+        return ok && bs.seg[k % kSegs].h >= 0;
+    };
+    auto release = [&](uint32_t k) { warp_arrive(&bs.seg_empty[k % kSegs], lane); };
+
+    if (warp == kPlan) {
+        // ======================================================== segments, and their queries into L2
+        int u = ch.begin(cta);
+        const int u1 = ch.begin(cta + 1);
+        bool more = true;
+        for (uint32_t k = 0; ok && more; ++k) {
+            Segment s;
+            more = next_segment<kRT, true, kSwitch>(a, first, ch, cta, &u, u1, &s);
+            if (!more) s.h = -1;
+            ok = k < kSegs || got(&bs.seg_empty[k % kSegs], k / kSegs + 1);
+            if (!ok) break;
+            if (lane == 0) bs.seg[k % kSegs] = s;
+            warp_arrive(&bs.seg_full[k % kSegs], lane);
+            for (int r = lane; more && r < s.nr; r += 32) {
+                const int tok = by_group(a, s.row0 + r);
+                const uint16_t* x = a.q + (size_t)(s.q0 + tok) * a.q_row + (size_t)(s.h * a.group + s.row0 + r - tok * a.group) * kD;
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(x));
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(x + 64));
+            }
+        }
+    } else if (warp >= kExpand && warp < kIssue) {
         // ======================================================== codes to values
-        const int which = warp >= 12, t = tid & 127;
-        const uint8_t* const codes = which ? a.vc : a.kc;
-        const uint32_t* const scales = which ? a.vs : a.ks;
-        uint64_t* const full = which ? bs.v_full : bs.k_full;
-        uint64_t* const empty = which ? bs.v_empty : bs.k_empty;
-        uint64_t* const info = which ? bs.v_info : bs.k_info;
-        unsigned char* const ring = sm + (which ? kOffV : kOffK);
+        const int t = tid & 127;
         bool bad = false;
-        while (ok && next_segment<kRT, true>(a, first, ch, cta, &u, u1, &s)) {
+        for (uint32_t k = 0; ok && take(k); ++k) {
+            const Segment& s = bs.seg[k % kSegs];
             auto block_of = [&](int tile) -> int {
                 const int tok = tile * kTile + t;
                 // (what no row sees may have been given up)
@@ -180,71 +231,91 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                 bad = true;
                 return -1;
             };
-            uint4 next[4] = {};
-            uint32_t sm_next = 0;
+            uint4 next[2][4] = {};                             // K, V
+            uint32_t sm_next[2] = {};
             auto load = [&](int tile, int id) {
                 const int at = (tile * kTile + t) & ((1 << a.bs_log2) - 1);
                 const size_t tok = (size_t)s.h << a.bs_log2 | at;
-                const uint4* p = reinterpret_cast<const uint4*>(codes + (size_t)max(id, 0) * a.block_stride + tok * (kD / 2));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) next[i] = id >= 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
-                sm_next = id >= 0 ? __ldg(scales + ((size_t)id * a.kv_heads << a.bs_log2) + tok) : 0;
+                for (int which = 0; which < 2; ++which) {
+                    const uint4* p = reinterpret_cast<const uint4*>((which ? a.vc : a.kc) + (size_t)max(id, 0) * a.block_stride +
+                                                                    tok * (kD / 2));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) next[which][i] = id >= 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+                    sm_next[which] = id >= 0 ? __ldg((which ? a.vs : a.ks) + ((size_t)id * a.kv_heads << a.bs_log2) + tok) : 0;
+                }
             };
             int id = s.n > 0 ? block_of(s.t0) : -1, id1 = s.n > 1 ? block_of(s.t0 + 1) : -1;
             if (s.n > 0) load(s.t0, id);
             for (int j = 0; ok && j < s.n; ++j) {
                 const uint32_t g = G + j;
-                const uint4 w[4] = {next[0], next[1], next[2], next[3]};
-                const float sv = bf_lo(sm_next), mv = bf_hi(sm_next);
-                const bool there = id >= 0;
-                id = id1;
-                if (j + 1 < s.n) load(s.t0 + j + 1, id);
-                id1 = j + 2 < s.n ? block_of(s.t0 + j + 2) : -1;
-                // the tile's largest magnitude
-                const uint32_t mag = __float_as_uint(fmaxf(fabsf(mv), fabsf(fmaf(15.f, sv, mv))));
-                const uint32_t top = __reduce_max_sync(0xffffffffu, mag);
-                if (lane == 0) bs.most[which][g & 1][warp & 3] = top;
-                const uint32_t on = __ballot_sync(0xffffffffu, there);
-                warp_arrive(&bs.max_in[which], lane);
-                ok = got(&bs.max_in[which], g);
-                if (!ok) break;
-                const uint32_t* most = bs.most[which][g & 1];
-                const uint32_t all = max(max(most[0], most[1]), max(most[2], most[3]));
-                const int e = min(max((int)(all >> 23) - 127, -100), 100);
-                // (tile g - 4's exponent has been read: its products are done, or stage g & 1 would not come free)
-                ok = g < 2 || got(&empty[g & 1], (g >> 1) + 1);
-                if (!ok) break;
-                if (lane == 0) {
-                    if (which) bs.v_exp[g % kInfo] = e;
-                    else {
-                        bs.k_factor[g % kInfo] = pow2(e - kTop);
-                        bs.there[g % kInfo][warp & 3] = on;
+                // the tile's largest magnitudes
+                float sv[2], mv[2];
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    sv[which] = bf_lo(sm_next[which]);
+                    mv[which] = bf_hi(sm_next[which]);
+                    const uint32_t mag = __float_as_uint(fmaxf(fabsf(mv[which]), fabsf(fmaf(15.f, sv[which], mv[which]))));
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, mag);
+                    if (lane == 0) bs.most[which][g & 1][warp & 3] = top;
+                }
+                const uint32_t on = __ballot_sync(0xffffffffu, id >= 0);
+                warp_arrive(&bs.max_in, lane);
+                ok = got(&bs.max_in, g);
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    if (!ok) break;
+                    const uint32_t* most = bs.most[which][g & 1];
+                    const uint32_t all = max(max(most[0], most[1]), max(most[2], most[3]));
+                    const int e = min(max((int)(all >> 23) - 127, -100), 100);
+                    // (tile g - 4's exponent has been read: its products are done, or stage g & 1 would not come free)
+                    ok = g < 2 || got(which ? &bs.v_empty[g & 1] : &bs.k_empty[g & 1], (g >> 1) + 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (which) bs.v_exp[g % kInfo] = e;
+                        else {
+                            bs.k_factor[g % kInfo] = pow2(e - kTop);
+                            bs.there[g % kInfo][warp & 3] = on;
+                        }
                     }
+                    warp_arrive(which ? &bs.v_info[g % kInfo] : &bs.k_info[g % kInfo], lane);
+                    const float f = pow2(kTop - e);
+                    const __half2 s2 = __float2half2_rn(sv[which] * f), s16 = __float2half2_rn(sv[which] * f * 0.0625f),
+                                  m2 = __float2half2_rn(mv[which] * f);
+                    const uint32_t to = smem_u32(sm) + (which ? kOffV : kOffK) + (g & 1) * kTileBytes;
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {              // (rolled, by moving what is left to the front)
+                        const uint4 x = next[which][0];
+                        const uint32_t half = to + (i >> 1) * kHalf;
+                        sts128(half + sw128(t, (i & 1) * 4), values8(x.x, s2, s16, m2));
+                        sts128(half + sw128(t, (i & 1) * 4 + 1), values8(x.y, s2, s16, m2));
+                        sts128(half + sw128(t, (i & 1) * 4 + 2), values8(x.z, s2, s16, m2));
+                        sts128(half + sw128(t, (i & 1) * 4 + 3), values8(x.w, s2, s16, m2));
+                        next[which][0] = next[which][1];
+                        next[which][1] = next[which][2];
+                        next[which][2] = next[which][3];
+                    }
+                    fence_async_smem();
+                    warp_arrive(which ? &bs.v_full[g & 1] : &bs.k_full[g & 1], lane);
+                    // (the next tile's, while others work on this one)
+                    if (which == 1 && j + 1 < s.n) load(s.t0 + j + 1, id1);
                 }
-                warp_arrive(&info[g % kInfo], lane);
-                const float f = pow2(kTop - e);
-                const __half2 s2 = __float2half2_rn(sv * f), s16 = __float2half2_rn(sv * f * 0.0625f), m2 = __float2half2_rn(mv * f);
-                unsigned char* const to = ring + (g & 1) * kTileBytes;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<uint4*>(to + (i >> 1) * kHalf + sw128(t, (i & 1) * 4 + k)) = values8(x[k], s2, s16, m2);
-                }
-                fence_async_smem();
-                warp_arrive(&full[g & 1], lane);
+                id = id1;
+                id1 = j + 2 < s.n ? block_of(s.t0 + j + 2) : -1;
             }
             G += s.n;
+            release(k);
         }
         if (bad) atomicOr(a.err, kErrBounds);
-    } else if (warp == 16) {
+    } else if (warp == kIssue) {
         // ======================================================== MMA issue
         constexpr uint32_t id_qk = idesc_f32acc(0, 0, 0, 128, kTile);     // fp16, both K-major
         constexpr uint32_t id_pv = idesc_f32acc(0, 0, 1, 128, kD);        // V with its dims contiguous
         const uint32_t q0 = smem_u32(sm), k0 = smem_u32(sm + kOffK), v0 = smem_u32(sm + kOffV);
         uint32_t steps[2] = {0, 0}, segs = 0;                  // weights taken of each lane, segments with tiles
-        while (ok && next_segment<kRT, true>(a, first, ch, cta, &u, u1, &s)) {
+        for (uint32_t seg = 0; ok && take(seg); ++seg) {
+            const Segment s = bs.seg[seg % kSegs];
+            release(seg);
             if (s.n == 0) continue;
             const bool both = s.nr > 128;                      // both lanes take every tile
             const int n[2] = {both ? s.n : (s.n + 1) / 2, both ? s.n : s.n / 2};
@@ -311,41 +382,50 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             warp_arrive(bar, lane);
             return got(bar, meets++ >> 1);
         };
-        while (ok && next_segment<kRT, true>(a, first, ch, cta, &u, u1, &s)) {
+        for (uint32_t seg = 0; ok && take(seg); ++seg) {
+            const Segment& s = bs.seg[seg % kSegs];
             const bool both = s.nr > 128;
             const int row = both ? i * 128 + t : t;            // in the row tile
-            const int tok = (s.row0 + row) / a.group;          // of the request's new tokens
+            const int tok = by_group(a, s.row0 + row);          // of the request's new tokens
             const bool on = row < s.nr;
-            const size_t head = (size_t)(s.h * a.group + s.row0 + row - tok * a.group) * kD;
+            const int head = (s.h * a.group + s.row0 + row - tok * a.group) * kD;
             const int p0 = s.len - s.nq, pos = on ? p0 + tok : -1;
             float factor = 0.f;                                // of this row's scores
             if (s.n > 0) {
-                const uint4* x = reinterpret_cast<const uint4*>(a.q + (size_t)(s.q0 + (on ? tok : 0)) * a.q_row + (on ? head : 0));
-                uint32_t m = 0;
+                // the warp's 32 rows, two at a time with 16 bytes a lane
+                const long long q_at = (long long)(s.q0 + tok) * a.q_row + head;
+                uint4 v[16];
+                const int c16 = lane & 15, r0 = (both ? i * 128 : 0) + (warp & 3) * 32;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const uint4 v = on ? __ldg(x + k) : make_uint4(0, 0, 0, 0);
-                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                for (int y = 0; y < 16; ++y) {
+                    const int from = 2 * y + (lane >> 4);
+                    const long long at = __shfl_sync(0xffffffffu, q_at, from);
+                    v[y] = r0 + from < s.nr ? __ldg(reinterpret_cast<const uint4*>(a.q + at) + c16) : make_uint4(0, 0, 0, 0);
                 }
-                m = max(m & 0xffffu, m >> 16);
-                const int e = min(max((int)(m >> 7) - 127 - kTop, -120), 120);
-                // a row that is not finite has no result: NaN
-                factor = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e) * fabsf(a.scale_log2);
-                if (both || i == 0) {
-                    const float inv = a.scale_log2 < 0.f ? -pow2(-e) : pow2(-e);
-#pragma unroll 4
-                    for (int k = 0; k < 16; ++k) {
-                        const uint4 v = on ? __ldg(x + k) : make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(sm + i * kTileBytes + (k >> 3) * kHalf + sw128(t, k & 7)) =
-                            make_uint4(half2_bits(bf_lo(v.x) * inv, bf_lo(v.z) * inv), half2_bits(bf_hi(v.x) * inv, bf_hi(v.z) * inv),
-                                       half2_bits(bf_lo(v.y) * inv, bf_lo(v.w) * inv), half2_bits(bf_hi(v.y) * inv, bf_hi(v.w) * inv));
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    const int r = 2 * y + (lane >> 4);         // of the warp's
+                    uint32_t m = __vmaxu2(__vmaxu2(v[y].x & 0x7fff7fffu, v[y].y & 0x7fff7fffu),
+                                          __vmaxu2(v[y].z & 0x7fff7fffu, v[y].w & 0x7fff7fffu));
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    m = max(m & 0xffffu, m >> 16);
+                    const int e = min(max((int)(m >> 7) - 127 - kTop, -120), 120);
+                    // a row that is not finite has no result: NaN
+                    if (c16 == 0)
+                        bs.factor[i][(warp & 3) * 32 + r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e) * fabsf(a.scale_log2);
+                    if (both || i == 0) {
+                        const float inv = a.scale_log2 < 0.f ? -pow2(-e) : pow2(-e);
+                        sts128(smem_u32(sm) + i * kTileBytes + (c16 >> 3) * kHalf + sw128((warp & 3) * 32 + r, c16 & 7),
+                               make_uint4(half2_bits(bf_lo(v[y].x) * inv, bf_lo(v[y].z) * inv), half2_bits(bf_hi(v[y].x) * inv, bf_hi(v[y].z) * inv),
+                                          half2_bits(bf_lo(v[y].y) * inv, bf_lo(v[y].w) * inv), half2_bits(bf_hi(v[y].y) * inv, bf_hi(v[y].w) * inv)));
                     }
                 }
                 fence_async_smem();
                 warp_arrive(&bs.q_full, lane);
+                factor = bs.factor[i][t];
             }
-            const int lane_lo = p0 + (s.row0 + (both ? i * 128 : 0)) / a.group, lane_hi = s.p_hi;
+            const int lane_lo = p0 + by_group(a, s.row0 + (both ? i * 128 : 0)), lane_hi = s.p_hi;
             const int win = a.window ? a.window : 1 << 30;
             float ref = kLow, l = 0.f;
             const int n = both ? s.n : (s.n + 1 - i) / 2;
@@ -369,23 +449,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                     if (hi < 0 || lo > 31) return 0;
                     return w & (0xffffffffu >> (31 - min(hi, 31))) & (0xffffffffu << max(lo, 0));
                 };
-                float top = -INFINITY;
-#pragma unroll
+                // Loops that are not unrolled: four roles' code has to share the instruction caches.
+                float tops[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float x[32];
                     tmem_ld<32>(my_s + c * 32, x);
                     tmem_ld_wait();
                     tmem_regs_ready_n<32>(x);
-                    if (edge) {
-                        const uint32_t w = seen(c);
+                    if (edge) mask32(seen(c), x, -INFINITY);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(w >> k & 1)) x[k] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) top = max3(top, x[k], x[k + 1]);
+                    for (int k = 0; k < 32; k += 2) tops[k >> 1 & 1] = max3(tops[k >> 1 & 1], x[k], x[k + 1]);
                 }
-                const float most = top == -INFINITY ? top : fmaf(top, sc, (float)ve);
+                const float top = fmaxf(tops[0], tops[1]), most = top == -INFINITY ? top : fmaf(top, sc, (float)ve);
                 float fac = 1.f;
                 if (most - ref > kRoom) {
                     const float now = most - kHead;
@@ -396,41 +472,41 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                 if (j > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
                     // (the products before this tile's scores are complete)
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        float o[16];
-                        tmem_ld<16>(my_o + c * 16, o);
+                    for (int c = 0; c < 4; ++c) {
+                        float o[32];
+                        tmem_ld<32>(my_o + c * 32, o);
                         tmem_ld_wait();
-                        tmem_regs_ready_n<16>(o);
+                        tmem_regs_ready_n<32>(o);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] *= fac;
-                        tmem_st<16>(my_o + c * 16, o);
+                        for (int k = 0; k < 32; ++k) o[k] *= fac;
+                        tmem_st<16>(my_o + c * 32, reinterpret_cast<const float(&)[16]>(o[0]));
+                        tmem_st<16>(my_o + c * 32 + 16, reinterpret_cast<const float(&)[16]>(o[16]));
                     }
                 }
-                const float add = (float)ve - ref;
-                float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
+                const u64 sc2 = pack(sc, sc), to2 = pack((float)ve - ref, (float)ve - ref);
+                u64 sums[2] = {0, 0};
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float x[32], p[16];
                     tmem_ld<32>(my_s + c * 32, x);
                     tmem_ld_wait();
                     tmem_regs_ready_n<32>(x);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] = ex2(fmaf(x[k], sc, add));
-                    if (edge) {
-                        const uint32_t w = seen(c);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(w >> k & 1)) x[k] = 0.f;
-                    }
+                    for (int k = 0; k < 32; k += 2) unpack(fma2(pack(x[k], x[k + 1]), sc2, to2), x[k], x[k + 1]);
+                    if (edge) mask32(seen(c), x, -INFINITY);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        sum0 += x[k];
-                        sum1 += x[k + 1];
-                        p[k / 2] = __uint_as_float(half2_bits(x[k], x[k + 1]));
+                        const float e0 = ex2(x[k]), e1 = ex2(x[k + 1]);
+                        sums[k >> 1 & 1] = add2(sums[k >> 1 & 1], pack(e0, e1));
+                        p[k / 2] = __uint_as_float(half2_bits(e0, e1));
                     }
                     tmem_st<16>(my_s + c * 16, p);             // over scores that have been read
                 }
-                l = fmaf(sum0 + sum1, pow2(-ve), l);
+                {
+                    float s0, s1;
+                    unpack(add2(sums[0], sums[1]), s0, s1);
+                    l = fmaf(s0 + s1, pow2(-ve), l);
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 warp_arrive(&bs.p_full[i], lane);
@@ -457,55 +533,73 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             }
             const float inv = sum == 0.f ? 0.f : s.parts == 1 ? pow2(-kTop) / sum : pow2(-kTop);
             const size_t slot = slot_of(s.v0, s.part);
-            uint16_t* const out = a.out + (size_t)(s.q0 + tok) * a.out_row + head;
-            float* const part = a.part_o + (slot * kRT + row) * kD;
-            // a lane's own columns of its rows, or half of them of the rows that both have
-            const int c0 = both ? 0 : i * 8, c1 = both ? 16 : c0 + 8;
-#pragma unroll 1
-            for (int c = c0; c < c1; c += 2) {
-                float o[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = 0.f;
-                if (s.n > 0) {
-                    tmem_ld<16>(both ? my_o + c * 8 : tmem + base + 256 + c * 8, o);
-                    tmem_ld_wait();
-                    tmem_regs_ready_n<16>(o);
-                    if (!both) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = f0 == 0.f ? 0.f : o[k] * f0;
-                        if (s.n > 1) {
-                            float o1[16];
-                            tmem_ld<16>(tmem + base + 384 + c * 8, o1);
-                            tmem_ld_wait();
-                            tmem_regs_ready_n<16>(o1);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if (f1 != 0.f) o[k] = fmaf(o1[k], f1, o[k]);
-                        }
-                    }
-                }
-                if (!on) continue;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = inv == 0.f ? 0.f : o[k] * inv;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    // columns hold dims 0, 4, 1, 5, 2, 6, 3, 7 of each 8
-                    const float* v = o + 8 * k;
-                    const int d = (c + k) * 8;
-                    if (s.parts == 1) {
-                        *reinterpret_cast<uint4*>(out + d) = make_uint4(bf2(v[0], v[2]), bf2(v[4], v[6]), bf2(v[1], v[3]), bf2(v[5], v[7]));
-                    } else {
-                        *reinterpret_cast<float4*>(part + d) = make_float4(v[0], v[2], v[4], v[6]);
-                        *reinterpret_cast<float4*>(part + d + 4) = make_float4(v[1], v[3], v[5], v[7]);
-                    }
-                }
-            }
-            tc_fence_before();
             if (s.parts > 1) {
                 if (on && (both || i == 0)) reinterpret_cast<float2*>(a.part_ml)[slot * kRT + row] = make_float2(m, sum);
-                ok = finish<kRT, kD>(a, s, tid, 256, &bs.last, meet);
-                if (!ok) break;
+                if (tid == 0 && s.part == 0) a.meta[cta] = make_int4(s.parts | s.nr << 12, s.q0, s.row0, s.h);
             }
+            // A lane's own columns of its rows, or half of them of the rows that both have: 64 at a time through the
+            // warp's 8 KB of what held Q, so that rows go out in whole lines (a thread writing its own row: 6 us).
+            const uint32_t own = smem_u32(sm) + warp * 8192;   // [32 rows][16 pieces], a row's turned by its number
+            const long long out_at = (long long)(s.q0 + tok) * a.out_row + head;
+            const int first_row = (both ? i * 128 : 0) + (warp & 3) * 32;
+#pragma unroll 1
+            for (int half = both ? 0 : i; half < (both ? 2 : i + 1); ++half) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float o[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = 0.f;
+                    if (s.n > 0) {
+                        const uint32_t col = half * 64 + c * 16;
+                        tmem_ld<16>((both ? my_o : tmem + base + 256) + col, o);
+                        tmem_ld_wait();
+                        tmem_regs_ready_n<16>(o);
+                        if (!both) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = f0 == 0.f ? 0.f : o[k] * f0;
+                            if (s.n > 1) {
+                                float o1[16];
+                                tmem_ld<16>(tmem + base + 384 + col, o1);
+                                tmem_ld_wait();
+                                tmem_regs_ready_n<16>(o1);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (f1 != 0.f) o[k] = fmaf(o1[k], f1, o[k]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = inv == 0.f ? 0.f : o[k] * inv;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // columns hold dims 0, 4, 1, 5, 2, 6, 3, 7 of each 8
+                        const float* v = o + 8 * k;
+                        const int piece = c * 4 + 2 * k;
+                        sts128(own + lane * 256 + ((piece ^ (lane & 15)) << 4),
+                               make_uint4(__float_as_uint(v[0]), __float_as_uint(v[2]), __float_as_uint(v[4]), __float_as_uint(v[6])));
+                        sts128(own + lane * 256 + ((piece + 1 ^ (lane & 15)) << 4),
+                               make_uint4(__float_as_uint(v[1]), __float_as_uint(v[3]), __float_as_uint(v[5]), __float_as_uint(v[7])));
+                    }
+                }
+                __syncwarp();
+#pragma unroll 4
+                for (int y = 0; y < 32; y += 2) {
+                    const int r = y + (lane >> 4), c4 = lane & 15, to = first_row + r;
+                    const float4 v = lds_float4(own + r * 256 + ((c4 ^ (r & 15)) << 4));
+                    const long long at = __shfl_sync(0xffffffffu, out_at, r);
+                    if (to >= s.nr) continue;
+                    const int d = half * 64 + c4 * 4;
+                    if (s.parts == 1) {
+                        *reinterpret_cast<uint2*>(a.out + at + d) = make_uint2(bf2(v.x, v.y), bf2(v.z, v.w));
+                    } else {
+                        *reinterpret_cast<float4*>(a.part_o + (slot * kRT + to) * kD + d) = v;
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            release(seg);
+            ok = meet();                                       // Q's place is free for the next queries
         }
     }
 
@@ -513,9 +607,124 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
     tc_fence_before();
     const bool failed = __syncthreads_or(!ok);
     if (failed && tid == 0) atomicOr(a.err, kErrTimeout);
-    if (warp == 16) {
+    if (warp == kIssue) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+// The parts of split row tiles together, in chunk order: part i has reference m_i, sum l_i and outputs O_i of each
+// row, out = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i. A job is 32 rows, a warp and a 16-byte piece per lane
+// each, four rows under way; of many parts (one long request) 4 rows, whose parts the warps share. (The last
+// CTA to write its part joining them took 40 to 80 us for 256 rows, by itself.)
+constexpr int kJoinThreads = 256, kFewParts = 12, kMostChunks = 512;
+__global__ void __launch_bounds__(kJoinThreads) join4_kernel(const __grid_constant__ Args a) {
+    __shared__ long long warp_sums[33];
+    __shared__ int4 item[kMostChunks];
+    __shared__ int jobs_before[kMostChunks], begins[kMostChunks];
+    __shared__ float4 acc_s[8][4][32];
+    __shared__ float sum_s[8][4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
+    const int n = min(a.ctrl[1], kMostChunks);
+    int n_items = 0, n_jobs = 0;
+    for (int base = 0; base < n; base += kJoinThreads) {
+        const int v = base + tid;
+        int4 it = v < n ? __ldcg(&a.meta[v]) : make_int4(0, 0, 0, 0);
+        int parts = it.x & 0xfff;
+        const int nr = it.x >> 12;
+        if (parts > n - v || nr > kRT) parts = 0;              // (a call that gave up)
+        const int jobs = parts == 0 ? 0 : parts <= kFewParts ? (nr + 31) / 32 : (nr + 3) / 4;
+        long long total;
+        const long long incl = block_scan(jobs ? (1ll << 32) + jobs : 0, warp_sums, &total);
+        if (jobs) {
+            const int k = n_items + (int)(incl >> 32) - 1;
+            item[k] = it;
+            begins[k] = v;
+            jobs_before[k] = n_jobs + (int)(incl & 0xffffffff) - jobs;
+        }
+        n_items += (int)(total >> 32);
+        n_jobs += (int)(total & 0xffffffff);
+    }
+    __syncthreads();
+    const float2* const ml = reinterpret_cast<const float2*>(a.part_ml);
+    for (int job = blockIdx.x; job < n_jobs; job += gridDim.x) {
+        const int k = last_not_above(jobs_before, n_items, job);
+        const int4 it = item[k];
+        const int parts = it.x & 0xfff, nr = it.x >> 12, v0 = begins[k], at = job - jobs_before[k];
+        const bool few = parts <= kFewParts;
+        // four rows of this warp's, and its parts of them
+        const int r0 = few ? at * 32 + warp * 4 : at * 4;
+        const int i0 = few ? 0 : parts * warp / 8, i1 = few ? parts : parts * (warp + 1) / 8;
+        float m[4], sum[4];
+        float4 acc[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            // the row's largest reference, of all its parts: a lane each
+            m[y] = kLow;
+            for (int i = lane; i < parts && r0 + y < nr; i += 32) {
+                const float2 st = __ldcg(&ml[slot_of(v0, i) * kRT + r0 + y]);
+                if (st.y != 0.f) m[y] = fmaxf(m[y], st.x);
+            }
+            sum[y] = 0.f;
+            acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m[y] = fmaxf(m[y], __shfl_xor_sync(0xffffffffu, m[y], o));
+#pragma unroll 4
+        for (int i = i0; i < i1; ++i) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const size_t row = slot_of(v0, i) * kRT + min(r0 + y, nr - 1);
+                const float2 st = __ldcg(&ml[row]);
+                const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * kD) + lane);
+                const float f = st.y != 0.f ? ex2(st.x - m[y]) : 0.f;
+                sum[y] = fmaf(f, st.y, sum[y]);
+                // (a part with no weight does not count, whatever it holds)
+                acc[y].x = f != 0.f ? fmaf(f, o.x, acc[y].x) : acc[y].x;
+                acc[y].y = f != 0.f ? fmaf(f, o.y, acc[y].y) : acc[y].y;
+                acc[y].z = f != 0.f ? fmaf(f, o.z, acc[y].z) : acc[y].z;
+                acc[y].w = f != 0.f ? fmaf(f, o.w, acc[y].w) : acc[y].w;
+            }
+        }
+        if (!few) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                acc_s[warp][y][lane] = acc[y];
+                if (lane == 0) sum_s[warp][y] = sum[y];
+            }
+            __syncthreads();
+            if (warp < 4) {
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                float l = 0.f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    const float4 o = acc_s[w][warp][lane];
+                    t.x += o.x;
+                    t.y += o.y;
+                    t.z += o.z;
+                    t.w += o.w;
+                    l += sum_s[w][warp];
+                }
+                acc[0] = t;
+                sum[0] = l;
+            }
+            __syncthreads();
+            if (warp >= 4) continue;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if (!few && y > 0) break;
+            const int row = few ? r0 + y : r0 + warp;
+            if (row >= nr) continue;
+            const float inv = sum[y] == 0.f ? 0.f : 1.f / sum[y];
+            const int rr = it.z + row, tok = by_group(a, rr);
+            *reinterpret_cast<uint2*>(a.out + (size_t)(it.y + tok) * a.out_row + (size_t)(it.w * a.group + rr - tok * a.group) * kD +
+                                      lane * 4) =
+                make_uint2(bf2(acc[y].x * inv, acc[y].y * inv), bf2(acc[y].z * inv, acc[y].w * inv));
+        }
     }
 }
 
@@ -532,10 +741,13 @@ cudaError_t set_chunk4_attrs() {
     return cudaFuncSetAttribute(chunk4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxBatch));
 }
 
-cudaError_t launch_chunk4(int sm_count, Args a, cudaStream_t st) {
-    a.arrived_n = sm_count;
+cudaError_t launch_chunk4(int sm_count, const Args& a, cudaStream_t st) {
+    if (sm_count > kMostChunks) return cudaErrorInvalidValue;
     chunk4_kernel<<<sm_count, kThreads, smem_bytes(a.n_req), st>>>(a);
     return cudaGetLastError();
+}
+cudaError_t launch_join4(int sm_count, const Args& a, cudaStream_t st) {
+    return launch_k(join4_kernel, dim3((unsigned)(4 * sm_count)), dim3(kJoinThreads), 0, st, true, a);
 }
 
 }  // namespace kv8

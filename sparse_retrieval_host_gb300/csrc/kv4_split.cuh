@@ -5,7 +5,8 @@
 // nrt - 1 - k of a causal request together see about as many tokens whatever k is: pairs of them are
 // items of equal work, P units each, in the order (request, KV head, pair, units of the later row
 // tile, then of the earlier, then nothing). A unit is a tile of 128 tokens, or half of one
-// where a row tile is more than half full (HALVES: the matrix products of the other half of its rows).
+// where a row tile is more than half full (HALVES: the matrix products of the other half of its rows);
+// SW units before a row tile's first stand for what its start and end cost.
 // The U units are cut into chunks of equal numbers, one per CTA. A row tile whose units fall
 // into several chunks leaves partial sums; the last CTA to write its part joins them in chunk order.
 #pragma once
@@ -38,8 +39,12 @@ struct Args {
     float* part_ml;
     int* arrived;                                // [3][arrived_n], zeros between calls
     int arrived_n;                               // CTAs at most
+    int4* meta;                                  // split row tiles by the chunk that they begin in, for the join: (parts |
+                                                 // rows << 12, first row of q and out, row, KV head)
+    int* ctrl;                                   // [1]: chunks of this call
     uint32_t* err;
     int n_req, n_rows, kv_heads, group;          // group = query heads / kv_heads
+    unsigned long long per_group;                // ceil(2^64 / group); 0 for a group of 1
     int rows_lo, rows_hi;                        // takes requests of rows_lo < rows <= rows_hi per KV head
     int bs_log2, n_blocks, max_blocks;
     float scale_log2;
@@ -53,11 +58,17 @@ struct Request {
     int P;             // units of a pair: at least what its two row tiles take
 };
 
+// x / group for 0 <= x < 2^32: with m = ceil(2^64 / group), x m / 2^64 exceeds x / group
+// by less than x / 2^64, which is less than the 1 / group up to the next integer.
+__device__ __forceinline__ int by_group(const Args& a, int x) {
+    return a.group == 1 ? x : (int)__umul64hi((unsigned long long)(uint32_t)x, a.per_group);
+}
+
 // Token tiles that any row of row tile rt sees, from *first on (0: none; it has its zeros to write).
 template <int RT>
 __device__ __forceinline__ int tiles_of(const Args& a, const Request& r, int rt, int* first) {
     const int c = r.len - r.nq;                                    // position of the first query
-    const int p_lo = c + rt * RT / a.group, p_hi = c + min(r.nq - 1, ((rt + 1) * RT - 1) / a.group);
+    const int p_lo = c + by_group(a, rt * RT), p_hi = c + min(r.nq - 1, by_group(a, (rt + 1) * RT - 1));
     *first = a.window ? max(0, p_lo - a.window + 1) / kTile : 0;
     return max(0, (p_hi < 0 ? 0 : p_hi / kTile + 1) - *first);
 }
@@ -65,13 +76,13 @@ template <int RT, bool HALVES>
 __device__ __forceinline__ int weight(const Args& a, const Request& r, int rt) {
     return HALVES && r.nq * a.group - rt * RT > RT / 2 ? 2 : 1;
 }
-template <int RT, bool HALVES>
+template <int RT, bool HALVES, int SW>
 __device__ __forceinline__ int units_of(const Args& a, const Request& r, int rt) {
     int first;
-    return max(1, tiles_of<RT>(a, r, rt, &first)) * weight<RT, HALVES>(a, r, rt);
+    return max(1, tiles_of<RT>(a, r, rt, &first)) * weight<RT, HALVES>(a, r, rt) + SW;
 }
 
-template <int RT, bool HALVES>
+template <int RT, bool HALVES, int SW>
 __device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
     Request r;
     const int c0 = a.cu[b], c1 = a.cu[b + 1], n = a.len[b], most = a.max_blocks << a.bs_log2;
@@ -91,13 +102,13 @@ __device__ __forceinline__ Request request(const Args& a, int b, bool* bad) {
     constexpr int W = HALVES ? 2 : 1;
     const int c = r.len - r.nq, all = max(1, (r.len + kTile - 1) / kTile);
     if (r.nrt <= 2) {
-        r.P = units_of<RT, HALVES>(a, r, 0) + (r.nrt == 2 ? units_of<RT, HALVES>(a, r, 1) : 0);
+        r.P = units_of<RT, HALVES, SW>(a, r, 0) + (r.nrt == 2 ? units_of<RT, HALVES, SW>(a, r, 1) : 0);
     } else if (a.window || c < 0) {
-        r.P = 2 * W * (int)min((long long)all, ((long long)(a.window ? a.window : all * kTile) + RT / a.group + 1) / kTile + 2);
+        r.P = 2 * W * (int)min((long long)all, ((long long)(a.window ? a.window : all * kTile) + RT / a.group + 1) / kTile + 2) + 2 * SW;
     } else {
         // positions of the last rows of k and nrt - 1 - k add up to those of 0 and of a full last row
         // tile, or one more: so do their tiles
-        r.P = W * ((c + (RT - 1) / a.group) / kTile + (c + (int)(((long long)r.nrt * RT - 1) / a.group)) / kTile + 3);
+        r.P = W * ((c + (RT - 1) / a.group) / kTile + (c + (int)(((long long)r.nrt * RT - 1) / a.group)) / kTile + 3) + 2 * SW;
     }
     return r;
 }
@@ -121,7 +132,7 @@ struct Chunks {
 
 // The units before each request into `first`, by all T threads of the CTA; false where this CTA has
 // nothing to do. `warp_sums` as for block_scan.
-template <int RT, bool HALVES, int T>
+template <int RT, bool HALVES, int SW, int T>
 __device__ __forceinline__ bool count(const Args& a, int* first, long long* warp_sums, Chunks* ch) {
     const int tid = threadIdx.x;
     bool bad = false, stop = false;
@@ -130,7 +141,7 @@ __device__ __forceinline__ bool count(const Args& a, int* first, long long* warp
         const int b = base + tid;
         long long mine = 0, total;
         if (b < a.n_req) {
-            const Request r = request<RT, HALVES>(a, b, &bad);
+            const Request r = request<RT, HALVES, SW>(a, b, &bad);
             mine = (long long)r.pairs * r.P * a.kv_heads;
             if (a.cu[b + 1] < a.cu[b]) stop = true;           // requests may share rows
         }
@@ -149,43 +160,46 @@ __device__ __forceinline__ bool count(const Args& a, int* first, long long* warp
 }
 
 // The segment at unit *u of chunk v (which ends at u1); moves *u on. False: none there.
-template <int RT, bool HALVES>
+template <int RT, bool HALVES, int SW>
 __device__ __forceinline__ bool next_segment(const Args& a, const int* first, const Chunks& ch, int v, int* u, int u1, Segment* s) {
     while (*u < u1) {
         bool bad = false;                                     // (reported by count)
         s->b = last_not_above(first, a.n_req, *u);
-        const Request r = request<RT, HALVES>(a, s->b, &bad);
+        const Request r = request<RT, HALVES, SW>(a, s->b, &bad);
         const int in = *u - first[s->b], pair = in / r.P, o = in - pair * r.P;
         s->h = pair / r.pairs;
         const int k = pair - s->h * r.pairs, late = r.nrt - 1 - k;
-        const int n_late = units_of<RT, HALVES>(a, r, late);
+        const int n_late = units_of<RT, HALVES, SW>(a, r, late);
         int rt = late, at = o, n = n_late;
         if (o >= n_late) {
             rt = k;
             at = o - n_late;
-            n = k < late ? units_of<RT, HALVES>(a, r, k) : 0;
+            n = k < late ? units_of<RT, HALVES, SW>(a, r, k) : 0;
         }
         if (at >= n) {                                        // what a pair has too many
             *u += min(r.P - o, u1 - *u);
             continue;
         }
+        // its first SW units stand for its start and end: chunks that only have some of those have no part
         const int take = min(n - at, u1 - *u), u_rt = *u - at;
+        *u += take;
+        if (at + take <= SW) continue;
         s->row0 = rt * RT;
         s->nr = min(RT, r.nq * a.group - s->row0);
         s->q0 = r.q0;
         s->nq = r.nq;
         s->len = r.len;
-        s->p_lo = r.len - r.nq + s->row0 / a.group;
-        s->p_hi = r.len - r.nq + (s->row0 + s->nr - 1) / a.group;
-        s->v0 = ch.of(u_rt);
+        s->p_lo = r.len - r.nq + by_group(a, s->row0);
+        s->p_hi = r.len - r.nq + by_group(a, s->row0 + s->nr - 1);
+        s->v0 = ch.of(u_rt + SW);
         s->parts = ch.of(u_rt + n - 1) - s->v0 + 1;
         s->part = v - s->v0;
         int t_first;
         const int W = weight<RT, HALVES>(a, r, rt), tiles = tiles_of<RT>(a, r, rt, &t_first);
-        const int lo = min(tiles, (at + W - 1) / W), hi = min(tiles, (at + take + W - 1) / W);
+        const int from = max(0, at - SW), to = at + take - SW;
+        const int lo = min(tiles, (from + W - 1) / W), hi = min(tiles, (to + W - 1) / W);
         s->t0 = t_first + lo;
         s->n = hi - lo;
-        *u += take;
         return true;
     }
     return false;
@@ -202,6 +216,29 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// Pairs of fp32 values in one 64-bit register (one instruction for both).
+using u64 = unsigned long long;
+__device__ __forceinline__ u64 pack(float a, float b) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(u64 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     uint32_t r;
@@ -246,7 +283,7 @@ __device__ __forceinline__ bool join(const Args& a, const Segment& s, int i0, in
         if (FINAL) {
             if (!on) continue;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int rr = s.row0 + row, tok = rr / a.group;
+            const int rr = s.row0 + row, tok = by_group(a, rr);
             const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
             const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
             uint2 w;
@@ -264,30 +301,30 @@ __device__ __forceinline__ bool join(const Args& a, const Segment& s, int i0, in
     return true;
 }
 
-// After a part's sums are written: the last of up to kFan neighbours to get here joins them, the last
-// group of neighbours the groups (parts of one long request are as many as CTAs, and one SM would
-// read them for longer than they took). Counters: of a row tile's first group by its chunk, of
-// the others by theirs, and of its groups; back to zero for the next call.
+// After a part's sums are written and the threads that wrote them have met: the last of up to kFan
+// neighbours to get here joins them, the last group of neighbours the groups (parts of one long request
+// are as many as CTAs, and one SM would read them for longer than they took). Counters: of a row tile's
+// first group by its chunk, of the others by theirs, and of its groups; back to zero for the next call.
+// Threads tid of T take part, `sync` is their barrier.
 constexpr int kFan = 12;
 template <int RT, int D, class Sync>
-__device__ __forceinline__ bool finish(const Args& a, const Segment& s, int tid, int T, int* flag, Sync sync) {
+__device__ __forceinline__ bool finish(const Args& a, const Segment& s, int tid, int T, volatile int* flag, Sync sync) {
     const int k = s.part / kFan, i0 = k * kFan, cnt = min(kFan, s.parts - i0), groups = (s.parts + kFan - 1) / kFan;
     auto last_of = [&](int* counter, int n) -> int {          // 1: this CTA is the last, -1: give up
-        __threadfence();
-        if (!sync()) return -1;
         if (tid == 0) {
-            *flag = atomicAdd(counter, 1) == n - 1;
-            if (*flag) *counter = 0;
+            __threadfence();                                  // (what this thread has seen written is ordered with it)
+            const bool last = atomicAdd(counter, 1) == n - 1;
+            if (last) *counter = 0;
+            __threadfence();
+            *flag = last;
         }
         if (!sync()) return -1;
-        const int last = *reinterpret_cast<volatile int*>(flag);
-        __threadfence();
-        return last;
+        return *flag;
     };
     const int mine = last_of(a.arrived + (k == 0 ? s.v0 : a.arrived_n + s.v0 + i0), cnt);
     if (mine <= 0) return mine == 0;
     if (groups == 1) return join<RT, D, true>(a, s, i0, 1, cnt, tid, T, sync);
-    if (!join<RT, D, false>(a, s, i0, 1, cnt, tid, T, sync)) return false;
+    if (!join<RT, D, false>(a, s, i0, 1, cnt, tid, T, sync) || !sync()) return false;
     const int all = last_of(a.arrived + 2 * a.arrived_n + s.v0, groups);
     if (all <= 0) return all == 0;
     return join<RT, D, true>(a, s, 0, kFan, groups, tid, T, sync);
@@ -298,7 +335,9 @@ __device__ __forceinline__ bool finish(const Args& a, const Segment& s, int tid,
 // The kernel of many rows per KV head: its share of the handle's scratch (the first), and its launch.
 void chunk4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats);
 cudaError_t set_chunk4_attrs();
-cudaError_t launch_chunk4(int sm_count, split::Args a, cudaStream_t st);
+cudaError_t launch_chunk4(int sm_count, const split::Args& a, cudaStream_t st);
+// .. and of what joins its parts, after the kernel of few rows that runs beside it.
+cudaError_t launch_join4(int sm_count, const split::Args& a, cudaStream_t st);
 
 }  // namespace kv8
 }  // namespace srh
