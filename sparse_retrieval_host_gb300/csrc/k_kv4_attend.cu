@@ -619,7 +619,7 @@ cudaError_t set_one() {
 }
 
 // Rows per KV head up to which a request goes by this kernel where the other one runs too.
-constexpr int kFew = 16;
+constexpr int kFew = 8;
 
 }  // namespace
 
@@ -632,7 +632,6 @@ void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* 
 
 cudaError_t set_attend4_attrs() {
     cudaError_t e = set_one<Shape<1, 1>>();
-    if (e == cudaSuccess) e = set_one<Shape<1, 2>>();
     if (e == cudaSuccess) e = set_one<Shape<2, 1>>();
     if (e == cudaSuccess) e = set_chunk4_attrs();
     return e;
@@ -683,8 +682,8 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
         const cudaError_t e = launch_chunk4(c.sm_count, big, st);
         if (e != cudaSuccess) return e;
     }
-    const long long rows = beside ? kFew : (long long)a.group * ((n_rows + n_req - 1) / n_req);
-    cudaError_t e = rows <= 8 ? run<Shape<1, 1>>(c, a, beside, st) : run<Shape<1, 2>>(c, a, beside, st);
+    // (with more heads than that a group, none is left for this one)
+    cudaError_t e = a.group > kFew && beside ? cudaSuccess : run<Shape<1, 1>>(c, a, beside, st);
     if (beside && e == cudaSuccess) e = launch_join4(c.sm_count, a, st);
     return e;
 }

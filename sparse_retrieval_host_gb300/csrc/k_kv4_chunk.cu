@@ -18,8 +18,8 @@
 // 2,048 of shared memory (QK reads both operands: 1,024; PV one: 512; expanding writes 512): no unit
 // is free, the floor of one is that of all.
 //
-// Roles: warps 0-3 and 4-7 softmax of the two lanes, 8-11 expand K and V (a thread a token, the next
-// tile's codes in registers), 12 issues the MMAs: 13 warps, so that a thread has 128 registers. All waits are on mbarriers and bounded.
+// Roles: warps 0-3 and 4-7 softmax of the two lanes, 8-11 expand K, 12-15 V (a thread a token, the
+// next tile's codes in registers), 16 issues the MMAs, 17 finds the segments. All waits are on mbarriers and bounded.
 #include "kv4_split.cuh"
 #include "umma.cuh"
 
@@ -31,7 +31,7 @@ using namespace umma;
 using namespace split;
 
 constexpr int kRT = 256, kD = 128;
-constexpr int kExpand = 8, kIssue = 12, kPlan = 13;   // first warp that expands; those that issue MMAs and find segments
+constexpr int kExpand = 8, kIssue = 16, kPlan = 17;   // first warp that expands; those that issue MMAs and find segments
 constexpr int kThreads = (kPlan + 1) * 32;
 constexpr int kHalf = 16384;             // 128 rows of 64 fp16 values
 constexpr int kTileBytes = 2 * kHalf;
@@ -48,7 +48,7 @@ constexpr int kTop = 14;                 // exponent of the largest fp16 value o
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t k_info[kInfo], v_info[kInfo];   // a tile's exponent (and which tokens there are) is written
-    uint64_t max_in;                     // the expanding warps have given a tile's maxima
+    uint64_t max_in[2];                  // K's / V's warps have given a tile's maxima
     uint64_t s_full[2], p_full[2];       // of each lane: scores are in TMEM, weights are
     uint64_t q_full, o_full;             // queries are in shared memory; outputs are complete
     uint64_t met[2];                     // the softmax warps meet
@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             mbar_init(&bs.k_info[i], 4);
             mbar_init(&bs.v_info[i], 4);
         }
-        mbar_init(&bs.max_in, 4);
+        mbar_init(&bs.max_in[0], 4);
+        mbar_init(&bs.max_in[1], 4);
         mbar_init(&bs.q_full, 8);
         mbar_init(&bs.o_full, 1);
         mbar_init(&bs.drain, 1);
@@ -218,92 +219,82 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
         }
     } else if (warp >= kExpand && warp < kIssue) {
         // ======================================================== codes to values
-        const int t = tid & 127;
+        const int which = warp >= kExpand + 4, t = tid & 127;          // K or V, token of the tile
+        const uint8_t* const codes = which ? a.vc : a.kc;
+        const uint32_t* const scales = which ? a.vs : a.ks;
+        uint64_t* const full = which ? bs.v_full : bs.k_full;
+        uint64_t* const empty = which ? bs.v_empty : bs.k_empty;
+        uint64_t* const info = which ? bs.v_info : bs.k_info;
+        const uint32_t ring = smem_u32(sm) + (which ? kOffV : kOffK);
         bool bad = false;
         for (uint32_t k = 0; ok && take(k); ++k) {
             const Segment& s = bs.seg[k % kSegs];
+            const int n = s.n, first_tile = s.t0, p_hi = s.p_hi, head_tok = s.h << a.bs_log2;
+            const int see_first = a.window ? s.p_lo - a.window + 1 : 0;
+            const int32_t* const table = a.table + (size_t)s.b * a.max_blocks;
             auto block_of = [&](int tile) -> int {
                 const int tok = tile * kTile + t;
                 // (what no row sees may have been given up)
-                if (tok > s.p_hi || (a.window && tok <= s.p_lo - a.window)) return -1;
-                const int id = __ldg(a.table + (size_t)s.b * a.max_blocks + (tok >> a.bs_log2));
+                if (tok > p_hi || tok < see_first) return -1;
+                const int id = __ldg(table + (tok >> a.bs_log2));
                 if (id >= 0 && id < a.n_blocks) return id;
                 bad = true;
                 return -1;
             };
-            uint4 next[2][4] = {};                             // K, V
-            uint32_t sm_next[2] = {};
+            uint4 next[4] = {};
+            uint32_t sm_next = 0;
             auto load = [&](int tile, int id) {
-                const int at = (tile * kTile + t) & ((1 << a.bs_log2) - 1);
-                const size_t tok = (size_t)s.h << a.bs_log2 | at;
+                const int tok = head_tok | ((tile * kTile + t) & ((1 << a.bs_log2) - 1));
+                const uint4* p = reinterpret_cast<const uint4*>(codes + (size_t)max(id, 0) * a.block_stride + tok * (kD / 2));
 #pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    const uint4* p = reinterpret_cast<const uint4*>((which ? a.vc : a.kc) + (size_t)max(id, 0) * a.block_stride +
-                                                                    tok * (kD / 2));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) next[which][i] = id >= 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
-                    sm_next[which] = id >= 0 ? __ldg((which ? a.vs : a.ks) + ((size_t)id * a.kv_heads << a.bs_log2) + tok) : 0;
-                }
+                for (int i = 0; i < 4; ++i) next[i] = id >= 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
+                sm_next = id >= 0 ? __ldg(scales + ((size_t)id * a.kv_heads << a.bs_log2) + tok) : 0;
             };
-            int id = s.n > 0 ? block_of(s.t0) : -1, id1 = s.n > 1 ? block_of(s.t0 + 1) : -1;
-            if (s.n > 0) load(s.t0, id);
-            for (int j = 0; ok && j < s.n; ++j) {
+            int id = n > 0 ? block_of(first_tile) : -1, id1 = n > 1 ? block_of(first_tile + 1) : -1;
+            if (n > 0) load(first_tile, id);
+            for (int j = 0; ok && j < n; ++j) {
                 const uint32_t g = G + j;
-                // the tile's largest magnitudes
-                float sv[2], mv[2];
-#pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    sv[which] = bf_lo(sm_next[which]);
-                    mv[which] = bf_hi(sm_next[which]);
-                    const uint32_t mag = __float_as_uint(fmaxf(fabsf(mv[which]), fabsf(fmaf(15.f, sv[which], mv[which]))));
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, mag);
-                    if (lane == 0) bs.most[which][g & 1][warp & 3] = top;
-                }
-                const uint32_t on = __ballot_sync(0xffffffffu, id >= 0);
-                warp_arrive(&bs.max_in, lane);
-                ok = got(&bs.max_in, g);
-#pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    if (!ok) break;
-                    const uint32_t* most = bs.most[which][g & 1];
-                    const uint32_t all = max(max(most[0], most[1]), max(most[2], most[3]));
-                    const int e = min(max((int)(all >> 23) - 127, -100), 100);
-                    // (tile g - 4's exponent has been read: its products are done, or stage g & 1 would not come free)
-                    ok = g < 2 || got(which ? &bs.v_empty[g & 1] : &bs.k_empty[g & 1], (g >> 1) + 1);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (which) bs.v_exp[g % kInfo] = e;
-                        else {
-                            bs.k_factor[g % kInfo] = pow2(e - kTop);
-                            bs.there[g % kInfo][warp & 3] = on;
-                        }
-                    }
-                    warp_arrive(which ? &bs.v_info[g % kInfo] : &bs.k_info[g % kInfo], lane);
-                    const float f = pow2(kTop - e);
-                    const __half2 s2 = __float2half2_rn(sv[which] * f), s16 = __float2half2_rn(sv[which] * f * 0.0625f),
-                                  m2 = __float2half2_rn(mv[which] * f);
-                    const uint32_t to = smem_u32(sm) + (which ? kOffV : kOffK) + (g & 1) * kTileBytes;
-#pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {              // (rolled, by moving what is left to the front)
-                        const uint4 x = next[which][0];
-                        const uint32_t half = to + (i >> 1) * kHalf;
-                        sts128(half + sw128(t, (i & 1) * 4), values8(x.x, s2, s16, m2));
-                        sts128(half + sw128(t, (i & 1) * 4 + 1), values8(x.y, s2, s16, m2));
-                        sts128(half + sw128(t, (i & 1) * 4 + 2), values8(x.z, s2, s16, m2));
-                        sts128(half + sw128(t, (i & 1) * 4 + 3), values8(x.w, s2, s16, m2));
-                        next[which][0] = next[which][1];
-                        next[which][1] = next[which][2];
-                        next[which][2] = next[which][3];
-                    }
-                    fence_async_smem();
-                    warp_arrive(which ? &bs.v_full[g & 1] : &bs.k_full[g & 1], lane);
-                    // (the next tile's, while others work on this one)
-                    if (which == 1 && j + 1 < s.n) load(s.t0 + j + 1, id1);
-                }
+                const uint4 w[4] = {next[0], next[1], next[2], next[3]};
+                const float sv = bf_lo(sm_next), mv = bf_hi(sm_next);
+                const bool there = id >= 0;
                 id = id1;
-                id1 = j + 2 < s.n ? block_of(s.t0 + j + 2) : -1;
+                if (j + 1 < n) load(first_tile + j + 1, id);
+                id1 = j + 2 < n ? block_of(first_tile + j + 2) : -1;
+                // the tile's largest magnitude
+                const uint32_t mag = __float_as_uint(fmaxf(fabsf(mv), fabsf(fmaf(15.f, sv, mv))));
+                const uint32_t top = __reduce_max_sync(0xffffffffu, mag);
+                if (lane == 0) bs.most[which][g & 1][warp & 3] = top;
+                const uint32_t on = __ballot_sync(0xffffffffu, there);
+                warp_arrive(&bs.max_in[which], lane);
+                ok = got(&bs.max_in[which], g);
+                if (!ok) break;
+                const uint32_t* most = bs.most[which][g & 1];
+                const uint32_t all = max(max(most[0], most[1]), max(most[2], most[3]));
+                const int e = min(max((int)(all >> 23) - 127, -100), 100);
+                const float f = pow2(kTop - e);
+                const __half2 s2 = __float2half2_rn(sv * f), s16 = __float2half2_rn(sv * f * 0.0625f), m2 = __float2half2_rn(mv * f);
+                // (tile g - 4's exponent has been read: its products are done, or stage g & 1 would not come free)
+                ok = g < 2 || got(&empty[g & 1], (g >> 1) + 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    if (which) bs.v_exp[g % kInfo] = e;
+                    else {
+                        bs.k_factor[g % kInfo] = pow2(e - kTop);
+                        bs.there[g % kInfo][warp & 3] = on;
+                    }
+                }
+                warp_arrive(&info[g % kInfo], lane);
+                const uint32_t to = ring + (g & 1) * kTileBytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sts128(to + (i >> 1) * kHalf + sw128(t, (i & 1) * 4 + k), values8(x[k], s2, s16, m2));
+                }
+                fence_async_smem();
+                warp_arrive(&full[g & 1], lane);
             }
-            G += s.n;
+            G += n;
             release(k);
         }
         if (bad) atomicOr(a.err, kErrBounds);
