@@ -1,5 +1,5 @@
 // Attention over the paged 4-bit cache (kv4_attend), for few query rows per KV head
-// (decode steps, drafted tokens).
+// (decode steps), and for any number of rows of 256-dim heads.
 //
 //   o_r = sum_t w_rt V_t / sum_t w_rt,  w_rt = exp(scale <q_r, K_t>),
 //   K_t = km_t + ks_t n_t, V_t = vm_t + vs_t m_t, codes n, m in 0 .. 15
@@ -40,11 +40,12 @@ constexpr float kHead = 10.f;            // log2 of the weight that a new refere
 constexpr float kRoom = 15.5f;           // a row's reference moves when a weight would pass 2^15.5
 constexpr float kLeastScale = 5.421010862427522e-20f;   // 2^-64
 
-// DB: head_dim / 128. NT: row tiles of 8 columns.
-template <int DB_, int NT_>
+// DB: head_dim / 128. A warp has NT groups of 8 rows: one (see kFew).
+template <int DB_>
 struct Shape {
-    static constexpr int DB = DB_, NT = NT_, RT = 8 * NT, D = 128 * DB;
-    static constexpr int CTAS = DB == 1 ? (NT == 1 ? 3 : 2) : 2;
+    static constexpr int DB = DB_, NT = 1, RT = 8 * NT, D = 128 * DB;
+    // (with four CTAs 128 registers a thread, which spill: the decode batch 152 us, 142 with three)
+    static constexpr int CTAS = DB == 1 ? 3 : 2;
     static constexpr int kPitch = D + 4;                       // floats of a row of the warps' outputs
     static constexpr int kOutBytes = kWarps * RT * kPitch * 4;
     static constexpr int SW = 3;                               // units that stand for a segment's start and end
@@ -618,7 +619,8 @@ cudaError_t set_one() {
     return cudaFuncSetAttribute(attend4_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<S>(kMaxBatch));
 }
 
-// Rows per KV head up to which a request goes by this kernel where the other one runs too.
+// Rows per KV head up to which a request goes by this kernel where the other one runs too: a tile of 128 tokens costs an
+// SM 0.5 us for up to 8 rows here, 2.0 for 9 to 16 (as two groups of columns with 254 registers), and 1.2 there for up to 128.
 constexpr int kFew = 8;
 
 }  // namespace
@@ -631,8 +633,8 @@ void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* 
 }
 
 cudaError_t set_attend4_attrs() {
-    cudaError_t e = set_one<Shape<1, 1>>();
-    if (e == cudaSuccess) e = set_one<Shape<2, 1>>();
+    cudaError_t e = set_one<Shape<1>>();
+    if (e == cudaSuccess) e = set_one<Shape<2>>();
     if (e == cudaSuccess) e = set_chunk4_attrs();
     return e;
 }
@@ -671,7 +673,7 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
     a.max_blocks = c.cfg.max_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.window = window < (1 << 30) ? window : 0;            // (a request is at most 2^30 tokens long)
-    if (c.cfg.head_dim == 256) return run<Shape<2, 1>>(c, a, false, st);
+    if (c.cfg.head_dim == 256) return run<Shape<2>>(c, a, false, st);
     const long long all = (long long)a.group * n_rows;
     // One token per request, as the host sees it: this kernel alone. Otherwise requests of more
     // than kFew rows go by the other one, in the same call, as only the device knows which those are.
@@ -683,7 +685,7 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
         if (e != cudaSuccess) return e;
     }
     // (with more heads than that a group, none is left for this one)
-    cudaError_t e = a.group > kFew && beside ? cudaSuccess : run<Shape<1, 1>>(c, a, beside, st);
+    cudaError_t e = a.group > kFew && beside ? cudaSuccess : run<Shape<1>>(c, a, beside, st);
     if (beside && e == cudaSuccess) e = launch_join4(c.sm_count, a, st);
     return e;
 }

@@ -4,7 +4,7 @@
 // Rows are the M dimension of both products, S = Q K^T and O = P V. Codes become fp16 values in
 // shared memory once per tile of 128 tokens and are used by up to 256 rows:
 //   k = (m + n s) 2^(14 - e), e the exponent of the tile's largest magnitude,
-// one rounding of 2^-12 per value (or 2^-40 of the tile's largest); the power of two goes into
+// one rounding, 2^-11 of the value at most (or 2^-39 of the tile's largest); the power of two goes into
 // the scores' factor, V's into the exponent u = score + e of the weights 2^(u - ref), which are rounded to
 // fp16, and is taken out of the softmax's sums again. A thread holds a row, so maxima and sums
 // need no exchange; a row's reference moves only when a weight would pass 2^15.5.
@@ -475,6 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                     }
                 }
                 const u64 sc2 = pack(sc, sc), to2 = pack((float)ve - ref, (float)ve - ref);
+                // (scores so large that a difference of two in fp32 may pass the room that it should keep)
+                const bool far = __any_sync(0xffffffffu, fabsf(ref) > 1e6f && ref != kLow);
                 u64 sums[2] = {0, 0};
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
@@ -484,6 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                     tmem_regs_ready_n<32>(x);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) unpack(fma2(pack(x[k], x[k + 1]), sc2, to2), x[k], x[k + 1]);
+                    if (far) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] = x[k] > kRoom ? kRoom : x[k];   // (a NaN stays)
+                    }
                     if (edge) mask32(seen(c), x, -INFINITY);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
