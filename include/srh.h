@@ -785,7 +785,8 @@ int kv4_read(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const i
  * is rounded to fp16: within 2^-11 of it, or 2^-35 of the row's largest. Codes enter exactly where a
  * request has up to 8 query rows per KV head, and where head_dim is 256; else keys and values do, rounded to fp16:
  * within 2^-11 of each, or 2^-39 of the largest of its 128 tokens. V's scales are taken as at least 2^-64;
- * those that a row sees are to lie within 2^96 of each other, scores within 10^30 of 0, values within 2^60.
+ * those that a row sees are to lie within 2^96 of each other, scores within 10^30 of 0, keys within
+ * 2^60, and the V values that a row sees, summed by magnitude in a dim, within 2^47.
  */
 int kv4_attend(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
                int n_req, const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,

@@ -4,7 +4,7 @@
 //   o_r = sum_t w_rt V_t / sum_t w_rt,  w_rt = exp(scale <q_r, K_t>),
 //   K_t = km_t + ks_t n_t, V_t = vm_t + vs_t m_t, codes n, m in 0 .. 15
 //
-// A warp takes 16 tokens at a time, and their codes go from memory into the fragments of
+// A warp takes 16 tokens at a time (two such steps together for 128-dim heads), and their codes go from memory into the fragments of
 // mma.sync m16n8k16 (fp16) without a detour: tokens are the M dimension of S^T = n q^T, head
 // dims that of O^T = m^T p. (tcgen05 wants its operands unpacked in shared memory, whose
 // bandwidth, not HBM's, would bound a call of few rows: the products of 8 rows are a
@@ -24,8 +24,13 @@
 // the whole range, and the same for all tokens where all weigh the same). The -8 is taken off by
 // sum p, of the rounded p, a row of ones in the second product.
 //
-// Work: see kv4_split.cuh; a CTA's warps take 16 tokens each of a unit's 128, each with references
+// Work: see kv4_split.cuh; a CTA's warps take 16 tokens (32) in turn of a unit's 128, each with references
 // and sums of its own, and add up at the end of a segment.
+//
+// Measured: 64 requests of up to 16,384 tokens, 32 / 8 heads of 128: 138 us, 0.72 of the copy rate over the codes' bytes. The
+// arithmetic without loads takes 130 (some 285 instructions per 16 tokens of a warp, ALU 48 % busy, tensor pipe 24 %), loads alone 113
+// to 134: both have to overlap almost wholly. Steps of 32 tokens instead of 16 took 174 us to 156, queries in
+// shared memory and three CTAs per SM 156 to 142.
 #include "kv4_split.cuh"
 
 namespace srh {

@@ -20,6 +20,11 @@
 //
 // Roles: warps 0-3 and 4-7 softmax of the two lanes, 8-11 expand K, 12-15 V (a thread a token, the
 // next tile's codes in registers), 16 issues the MMAs, 17 finds the segments. All waits are on mbarriers and bounded.
+//
+// Measured: four prompts of up to 1,024 tokens on up to 8,192, 32 / 8 heads of 128: 339 us with the join, 0.36 of the fp16 rate;
+// some 4,400 cycles a full tile. Of those a warp's 128 columns from TMEM cost about 300 each time (they are read twice, once
+// for the maximum and once for the weights: 96 registers hold 32 columns), the exponentials of a scheduler's two
+// warps 1,580; the tensor pipe is busy for 33 %. Scores in registers (152 of them, by setmaxnreg): 386 us.
 #include "kv4_split.cuh"
 #include "umma.cuh"
 

@@ -967,3 +967,18 @@ def test_the_largest_batch():
         _check(one, x, _i32([0, x.shape[0]]), out[cl[b]:cl[b + 1]], 0.1)
         one.close()
     c.close()
+
+
+@pytest.mark.parametrize("G,D", [(4, 128), (20, 128), (4, 256)])
+def test_attend_constant_rows_of_large_values(G, D):
+    """V rows without a scale, 600 values of up to 2^36 (2^45.3 in sum; 2^47 is allowed)."""
+    g = _gen(90)
+    c = _kv4(batch=1, n_kv_heads=1, head_dim=D, block_tokens=16, n_blocks=40, max_blocks=40)
+    _filled(c, g, [600])
+    c.v_scale[0][..., 0] = 0.0
+    c.v_scale[0][..., 1] = (torch.rand(c.v_scale[0].shape[:-1], generator=g, device="cuda") * 2.0 ** 36).bfloat16()
+    q = _bf16(g, 2, G, D)
+    cu = _i32([0, 2])
+    out = c.attend(q, cu, scale=0.1)
+    _check(c, q, cu, out, 0.1)
+    c.close()
