@@ -1,5 +1,5 @@
 // Attention over the paged 4-bit cache (kv4_attend), for few query rows per KV head
-// (decode steps), and for any number of rows of 256-dim heads.
+// (decode steps, drafted tokens of small groups).
 //
 //   o_r = sum_t w_rt V_t / sum_t w_rt,  w_rt = exp(scale <q_r, K_t>),
 //   K_t = km_t + ks_t n_t, V_t = vm_t + vs_t m_t, codes n, m in 0 .. 15
@@ -45,7 +45,8 @@ constexpr float kHead = 10.f;            // log2 of the weight that a new refere
 constexpr float kRoom = 15.5f;           // a row's reference moves when a weight would pass 2^15.5
 constexpr float kLeastScale = 5.421010862427522e-20f;   // 2^-64
 
-// DB: head_dim / 128. A warp has NT groups of 8 rows: one (see kFew).
+// DB: head_dim / 128. A warp has NT groups of 8 rows: one (two take 254 registers, and 2.0 us for 9 to 16 rows against 1.0 of two
+// row tiles that read the codes twice, the second time from L2).
 template <int DB_>
 struct Shape {
     static constexpr int DB = DB_, NT = 1, RT = 8 * NT, D = 128 * DB;
@@ -624,9 +625,12 @@ cudaError_t set_one() {
     return cudaFuncSetAttribute(attend4_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<S>(kMaxBatch));
 }
 
-// Rows per KV head up to which a request goes by this kernel where the other one runs too: a tile of 128 tokens costs an
-// SM 0.5 us for up to 8 rows here, 2.0 for 9 to 16 (as two groups of columns with 254 registers), and 1.2 there for up to 128.
-constexpr int kFew = 8;
+// Rows per KV head up to which a request goes by this kernel where the other one runs too. A tile of 128 tokens costs an
+// SM some 0.5 us per 8 rows here, and 1.2 there for up to 128: 64 requests of up to 16,384 tokens with 16 heads a group take 265 us
+// here and 510 there, 8 with 24 heads 73 and 79. Of 256 dims 1.0 per 8 rows against 2.3 (with two lanes that share few
+// units more): 24 requests of 8,192 tokens with 32 heads a group 113 us here and 128 there.
+constexpr int kFew = 24;
+constexpr int kFewWide = 32;
 
 }  // namespace
 
@@ -678,20 +682,21 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
     a.max_blocks = c.cfg.max_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.window = window < (1 << 30) ? window : 0;            // (a request is at most 2^30 tokens long)
-    if (c.cfg.head_dim == 256) return run<Shape<2>>(c, a, false, st);
+    const int dim = c.cfg.head_dim, few = dim == 128 ? kFew : kFewWide;
     const long long all = (long long)a.group * n_rows;
     // One token per request, as the host sees it: this kernel alone. Otherwise requests of more
-    // than kFew rows go by the other one, in the same call, as only the device knows which those are.
-    const bool beside = all > kFew && (n_rows > n_req || a.group > kFew);
+    // than `few` rows go by the other one, in the same call, as only the device knows which those are.
+    const bool beside = all > few && (n_rows > n_req || a.group > few);
     if (beside) {
         Args big = a;
-        big.rows_lo = a.rows_hi = kFew;
-        const cudaError_t e = launch_chunk4(c.sm_count, big, st);
+        big.rows_lo = a.rows_hi = few;
+        const cudaError_t e = launch_chunk4(c.sm_count, dim, big, st);
         if (e != cudaSuccess) return e;
     }
+    cudaError_t e = cudaSuccess;
     // (with more heads than that a group, none is left for this one)
-    cudaError_t e = a.group > kFew && beside ? cudaSuccess : run<Shape<1>>(c, a, beside, st);
-    if (beside && e == cudaSuccess) e = launch_join4(c.sm_count, a, st);
+    if (!beside || a.group <= few) e = dim == 128 ? run<Shape<1>>(c, a, beside, st) : run<Shape<2>>(c, a, beside, st);
+    if (beside && e == cudaSuccess) e = launch_join4(c.sm_count, dim, a, st);
     return e;
 }
 

@@ -1,5 +1,5 @@
 // Attention over the paged 4-bit cache (kv4_attend) for requests of many query rows per KV head
-// (prompt chunks, drafts of wide groups): 128-dim heads on the 5th-generation tensor cores.
+// (prompt chunks, drafts of wide groups) on the 5th-generation tensor cores.
 //
 // Rows are the M dimension of both products, S = Q K^T and O = P V. Codes become fp16 values in
 // shared memory once per tile of 128 tokens and are used by up to 256 rows:
@@ -12,7 +12,10 @@
 // A CTA runs two lanes of 128 rows, each with its own S and O in TMEM (P lies over S), so that one
 // lane's exponentials run beside the other's products. Of a row tile of more than 128 rows the lanes
 // take the two halves, tile by tile of the same tokens; of one of up to 128 rows they take the same
-// rows and every other tile, and add up at the end.
+// rows and every other tile, and add up at the end. Of 256 dims a row tile has 128 rows and K and V one stage each: both
+// lanes take every tile of the same rows, each with all scores and weights and half of V's dims, as O has 256 columns and
+// TMEM room for them and two S only that way (the third of the products and half of the exponentials that are made
+// twice cost as much as twice the rows of 128 dims would).
 //
 // Per 128 tokens x 256 rows: 2,048 cycles of MMA at the fp16 rate, 2,048 of exponentials (16 a cycle),
 // 2,048 of shared memory (QK reads both operands: 1,024; PV one: 512; expanding writes 512): no unit
@@ -21,10 +24,11 @@
 // Roles: warps 0-3 and 4-7 softmax of the two lanes, 8-11 expand K, 12-15 V (a thread a token, the
 // next tile's codes in registers), 16 issues the MMAs, 17 finds the segments. All waits are on mbarriers and bounded.
 //
-// Measured: four prompts of up to 1,024 tokens on up to 8,192, 32 / 8 heads of 128: 339 us with the join, 0.36 of the fp16 rate;
+// Measured: four prompts of up to 1,024 tokens on up to 8,192, 32 / 8 heads of 128: 328 us with the join, 0.37 of the fp16 rate;
 // some 4,400 cycles a full tile. Of those a warp's 128 columns from TMEM cost about 300 each time (they are read twice, once
 // for the maximum and once for the weights: 96 registers hold 32 columns), the exponentials of a scheduler's two
-// warps 1,580; the tensor pipe is busy for 33 %. Scores in registers (152 of them, by setmaxnreg): 386 us.
+// warps 1,580; the tensor pipe is busy for 33 %. Scores in registers (152 of them, by setmaxnreg): 386 us. Of as
+// many products with 16 / 4 heads of 256: 416 us (8 rows at a time by the kernel of few rows: 1,463).
 #include "kv4_split.cuh"
 #include "umma.cuh"
 
@@ -35,7 +39,6 @@ namespace {
 using namespace umma;
 using namespace split;
 
-constexpr int kRT = 256, kD = 128;
 constexpr int kExpand = 8, kIssue = 16, kPlan = 17;   // first warp that expands; those that issue MMAs and find segments
 constexpr int kThreads = (kPlan + 1) * 32;
 constexpr int kHalf = 16384;             // 128 rows of 64 fp16 values
@@ -43,7 +46,15 @@ constexpr int kTileBytes = 2 * kHalf;
 constexpr int kOffK = 2 * kTileBytes;    // behind Q of the two lanes
 constexpr int kOffV = kOffK + 2 * kTileBytes;
 constexpr int kOffBars = kOffV + 2 * kTileBytes;
-constexpr int kSwitch = 8;               // half tiles that a row tile's start and end take the time of
+// DB: head_dim / 128.
+template <int DB_>
+struct Form {
+    static constexpr int DB = DB_, RT = 256 / DB, D = 128 * DB;
+    static constexpr bool HALVES = DB == 1;
+    static constexpr int SW = DB == 1 ? 8 : 4;                 // units (half tiles; tiles) that a row tile's start and end take the time of
+    static constexpr int ST = 2 / DB;                          // stages of K and of V
+    static constexpr int kStage = DB * kTileBytes;
+};
 constexpr int kSegs = 4;                 // segments found ahead of their use
 constexpr int kInfo = 4;                 // tiles whose exponents are held
 constexpr float kHead = 10.f;            // log2 of the weight that a new reference gives a row's maximum
@@ -138,7 +149,10 @@ __device__ __forceinline__ void mask32(uint32_t seen, float (&x)[32], float none
         if (!(seen >> k & 1)) x[k] = none;
 }
 
+template <int DB>
 __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_constant__ Args a) {
+    using F = Form<DB>;
+    constexpr int kRT = F::RT, kD = F::D, ST = F::ST;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     Bars& bs = *reinterpret_cast<Bars*>(sm + kOffBars);
@@ -174,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
         fence_mbar_init();
     }
     Chunks ch;
-    if (!count<kRT, true, kSwitch, kThreads>(a, first, bs.warp_sums, &ch)) {            // every thread
+    if (!count<kRT, F::HALVES, F::SW, kThreads>(a, first, bs.warp_sums, &ch)) {            // every thread
         if (blockIdx.x == 0 && tid == 0) a.ctrl[1] = 0;
         return;
     }
@@ -209,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
         bool more = true;
         for (uint32_t k = 0; ok && more; ++k) {
             Segment s;
-            more = next_segment<kRT, true, kSwitch>(a, first, ch, cta, &u, u1, &s);
+            more = next_segment<kRT, F::HALVES, F::SW>(a, first, ch, cta, &u, u1, &s);
             if (!more) s.h = -1;
             ok = k < kSegs || got(&bs.seg_empty[k % kSegs], k / kSegs + 1);
             if (!ok) break;
@@ -218,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             for (int r = lane; more && r < s.nr; r += 32) {
                 const int tok = by_group(a, s.row0 + r);
                 const uint16_t* x = a.q + (size_t)(s.q0 + tok) * a.q_row + (size_t)(s.h * a.group + s.row0 + r - tok * a.group) * kD;
-                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(x));
-                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(x + 64));
+#pragma unroll
+                for (int d = 0; d < kD; d += 64) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(x + d));
             }
         }
     } else if (warp >= kExpand && warp < kIssue) {
@@ -248,22 +262,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             };
             uint4 next[4] = {};
             uint32_t sm_next = 0;
-            auto load = [&](int tile, int id) {
+            auto load = [&](int tile, int id, int part) {      // 128 dims
                 const int tok = head_tok | ((tile * kTile + t) & ((1 << a.bs_log2) - 1));
-                const uint4* p = reinterpret_cast<const uint4*>(codes + (size_t)max(id, 0) * a.block_stride + tok * (kD / 2));
+                const uint4* p = reinterpret_cast<const uint4*>(codes + (size_t)max(id, 0) * a.block_stride + tok * (kD / 2) + part * 64);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) next[i] = id >= 0 ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
-                sm_next = id >= 0 ? __ldg(scales + ((size_t)id * a.kv_heads << a.bs_log2) + tok) : 0;
+                if (part == 0) sm_next = id >= 0 ? __ldg(scales + ((size_t)id * a.kv_heads << a.bs_log2) + tok) : 0;
             };
             int id = n > 0 ? block_of(first_tile) : -1, id1 = n > 1 ? block_of(first_tile + 1) : -1;
-            if (n > 0) load(first_tile, id);
+            if (n > 0) load(first_tile, id, 0);
             for (int j = 0; ok && j < n; ++j) {
                 const uint32_t g = G + j;
-                const uint4 w[4] = {next[0], next[1], next[2], next[3]};
+                uint4 w[4] = {next[0], next[1], next[2], next[3]};
                 const float sv = bf_lo(sm_next), mv = bf_hi(sm_next);
                 const bool there = id >= 0;
+                if (DB == 2) load(first_tile + j, id, 1);
                 id = id1;
-                if (j + 1 < n) load(first_tile + j + 1, id);
+                if (DB == 1 && j + 1 < n) load(first_tile + j + 1, id, 0);
                 id1 = j + 2 < n ? block_of(first_tile + j + 2) : -1;
                 // the tile's largest magnitude
                 const uint32_t mag = __float_as_uint(fmaxf(fabsf(mv), fabsf(fmaf(15.f, sv, mv))));
@@ -278,26 +293,40 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                 const int e = min(max((int)(all >> 23) - 127, -100), 100);
                 const float f = pow2(kTop - e);
                 const __half2 s2 = __float2half2_rn(sv * f), s16 = __float2half2_rn(sv * f * 0.0625f), m2 = __float2half2_rn(mv * f);
-                // (tile g - 4's exponent has been read: its products are done, or stage g & 1 would not come free)
-                ok = g < 2 || got(&empty[g & 1], (g >> 1) + 1);
+                auto publish = [&] {
+                    if (lane == 0) {
+                        if (which) bs.v_exp[g % kInfo] = e;
+                        else {
+                            bs.k_factor[g % kInfo] = pow2(e - kTop);
+                            bs.there[g % kInfo][warp & 3] = on;
+                        }
+                    }
+                    warp_arrive(&info[g % kInfo], lane);
+                };
+                // (tile g - 4's exponent has been read. Of one stage: tile g - 2's products are done, and those of a lane's
+                // queries come after its weights of tile g - 3; it need not wait for the stage, which lane 1 has longest)
+                if (ST == 1) publish();
+                ok = g < ST || got(&empty[g % ST], g / ST + 1);
                 if (!ok) break;
-                if (lane == 0) {
-                    if (which) bs.v_exp[g % kInfo] = e;
-                    else {
-                        bs.k_factor[g % kInfo] = pow2(e - kTop);
-                        bs.there[g % kInfo][warp & 3] = on;
+                // (of two: tile g - 4's products are done, or the stage would not come free)
+                if (ST == 2) publish();
+#pragma unroll 1
+                for (int part = 0; part < DB; ++part) {
+                    const uint32_t to = ring + (g % ST) * F::kStage + part * kTileBytes;
+                    if (part == 1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = next[i];
+                        if (j + 1 < n) load(first_tile + j + 1, id, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) sts128(to + (i >> 1) * kHalf + sw128(t, (i & 1) * 4 + k), values8(x[k], s2, s16, m2));
                     }
                 }
-                warp_arrive(&info[g % kInfo], lane);
-                const uint32_t to = ring + (g & 1) * kTileBytes;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sts128(to + (i >> 1) * kHalf + sw128(t, (i & 1) * 4 + k), values8(x[k], s2, s16, m2));
-                }
                 fence_async_smem();
-                warp_arrive(&full[g & 1], lane);
+                warp_arrive(&full[g % ST], lane);
             }
             G += n;
             release(k);
@@ -306,24 +335,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
     } else if (warp == kIssue) {
         // ======================================================== MMA issue
         constexpr uint32_t id_qk = idesc_f32acc(0, 0, 0, 128, kTile);     // fp16, both K-major
-        constexpr uint32_t id_pv = idesc_f32acc(0, 0, 1, 128, kD);        // V with its dims contiguous
+        constexpr uint32_t id_pv = idesc_f32acc(0, 0, 1, 128, 128);       // V with its dims contiguous
         const uint32_t q0 = smem_u32(sm), k0 = smem_u32(sm + kOffK), v0 = smem_u32(sm + kOffV);
         uint32_t steps[2] = {0, 0}, segs = 0;                  // weights taken of each lane, segments with tiles
         for (uint32_t seg = 0; ok && take(seg); ++seg) {
             const Segment s = bs.seg[seg % kSegs];
             release(seg);
             if (s.n == 0) continue;
-            const bool both = s.nr > 128;                      // both lanes take every tile
+            const bool both = DB == 2 || s.nr > 128;           // both lanes take every tile
+            const bool rows = DB == 1 && both;                 // .. of rows of their own
             const int n[2] = {both ? s.n : (s.n + 1) / 2, both ? s.n : s.n / 2};
             auto tile = [&](int i, int j) { return G + (both ? j : 2 * j + i); };
             auto qk = [&](int i, int j) -> bool {
-                const uint32_t g = tile(i, j), st = g & 1;
-                if (!got(&bs.k_full[st], g >> 1)) return false;
+                const uint32_t g = tile(i, j), st = g % ST;
+                if (!got(&bs.k_full[st], g / ST)) return false;
                 tc_fence_after();
-                const uint32_t qa = q0 + (both ? i : 0) * kTileBytes, kb = k0 + st * kTileBytes;
+                const uint32_t qa = q0 + (rows ? i : 0) * kTileBytes, kb = k0 + st * F::kStage;
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
+                    for (int kk = 0; kk < 8 * DB; ++kk) {
                         const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
                         mma_f16kind(tmem + i * 128, desc_sw128(qa + off, 16, 1024), desc_sw128(kb + off, 16, 1024), id_qk, kk > 0);
                     }
@@ -334,11 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                 return true;
             };
             auto pv = [&](int i, int j) -> bool {
-                const uint32_t g = tile(i, j), st = g & 1;
-                if (!got(&bs.v_full[st], g >> 1) || !got(&bs.p_full[i], steps[i])) return false;
+                const uint32_t g = tile(i, j), st = g % ST;
+                if (!got(&bs.v_full[st], g / ST) || !got(&bs.p_full[i], steps[i])) return false;
                 ++steps[i];
                 tc_fence_after();
-                const uint32_t vb = v0 + st * kTileBytes;
+                const uint32_t vb = v0 + st * F::kStage + (DB == 2 ? i * kTileBytes : 0);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
@@ -380,48 +410,52 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
         };
         for (uint32_t seg = 0; ok && take(seg); ++seg) {
             const Segment& s = bs.seg[seg % kSegs];
-            const bool both = s.nr > 128;
-            const int row = both ? i * 128 + t : t;            // in the row tile
+            const bool both = DB == 2 || s.nr > 128, rows = DB == 1 && both;
+            const int row = rows ? i * 128 + t : t;            // in the row tile
             const int tok = by_group(a, s.row0 + row);          // of the request's new tokens
             const bool on = row < s.nr;
             const int head = (s.h * a.group + s.row0 + row - tok * a.group) * kD;
             const int p0 = s.len - s.nq, pos = on ? p0 + tok : -1;
             float factor = 0.f;                                // of this row's scores
             if (s.n > 0) {
-                // the warp's 32 rows, two at a time with 16 bytes a lane
+                // the warp's 32 rows, two (of 256 dims one) at a time with 16 bytes a lane
+                constexpr int kLanes = 16 * DB;
                 const long long q_at = (long long)(s.q0 + tok) * a.q_row + head;
                 uint4 v[16];
-                const int c16 = lane & 15, r0 = (both ? i * 128 : 0) + (warp & 3) * 32;
+                const int piece = lane & (kLanes - 1), r0 = (rows ? i * 128 : 0) + (warp & 3) * 32;
+#pragma unroll 1
+                for (int y0 = 0; y0 < DB; ++y0) {
 #pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    const int from = 2 * y + (lane >> 4);
-                    const long long at = __shfl_sync(0xffffffffu, q_at, from);
-                    v[y] = r0 + from < s.nr ? __ldg(reinterpret_cast<const uint4*>(a.q + at) + c16) : make_uint4(0, 0, 0, 0);
-                }
+                    for (int y = 0; y < 16; ++y) {
+                        const int from = DB == 1 ? 2 * y + (lane >> 4) : y0 * 16 + y;
+                        const long long at = __shfl_sync(0xffffffffu, q_at, from);
+                        v[y] = r0 + from < s.nr ? __ldg(reinterpret_cast<const uint4*>(a.q + at) + piece) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    const int r = 2 * y + (lane >> 4);         // of the warp's
-                    uint32_t m = __vmaxu2(__vmaxu2(v[y].x & 0x7fff7fffu, v[y].y & 0x7fff7fffu),
-                                          __vmaxu2(v[y].z & 0x7fff7fffu, v[y].w & 0x7fff7fffu));
+                    for (int y = 0; y < 16; ++y) {
+                        const int r = DB == 1 ? 2 * y + (lane >> 4) : y0 * 16 + y;     // of the warp's
+                        uint32_t m = __vmaxu2(__vmaxu2(v[y].x & 0x7fff7fffu, v[y].y & 0x7fff7fffu),
+                                              __vmaxu2(v[y].z & 0x7fff7fffu, v[y].w & 0x7fff7fffu));
 #pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    m = max(m & 0xffffu, m >> 16);
-                    const int e = min(max((int)(m >> 7) - 127 - kTop, -120), 120);
-                    // a row that is not finite has no result: NaN
-                    if (c16 == 0)
-                        bs.factor[i][(warp & 3) * 32 + r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e) * fabsf(a.scale_log2);
-                    if (both || i == 0) {
-                        const float inv = a.scale_log2 < 0.f ? -pow2(-e) : pow2(-e);
-                        sts128(smem_u32(sm) + i * kTileBytes + (c16 >> 3) * kHalf + sw128((warp & 3) * 32 + r, c16 & 7),
-                               make_uint4(half2_bits(bf_lo(v[y].x) * inv, bf_lo(v[y].z) * inv), half2_bits(bf_hi(v[y].x) * inv, bf_hi(v[y].z) * inv),
-                                          half2_bits(bf_lo(v[y].y) * inv, bf_lo(v[y].w) * inv), half2_bits(bf_hi(v[y].y) * inv, bf_hi(v[y].w) * inv)));
+                        for (int o = kLanes / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        m = max(m & 0xffffu, m >> 16);
+                        const int e = min(max((int)(m >> 7) - 127 - kTop, -120), 120);
+                        // a row that is not finite has no result: NaN
+                        if (piece == 0)
+                            bs.factor[i][(warp & 3) * 32 + r] = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e) * fabsf(a.scale_log2);
+                        if (rows || i == 0) {
+                            const float inv = a.scale_log2 < 0.f ? -pow2(-e) : pow2(-e);
+                            sts128(smem_u32(sm) + i * kTileBytes + (piece >> 3) * kHalf + sw128((warp & 3) * 32 + r, piece & 7),
+                                   make_uint4(half2_bits(bf_lo(v[y].x) * inv, bf_lo(v[y].z) * inv), half2_bits(bf_hi(v[y].x) * inv, bf_hi(v[y].z) * inv),
+                                              half2_bits(bf_lo(v[y].y) * inv, bf_lo(v[y].w) * inv), half2_bits(bf_hi(v[y].y) * inv, bf_hi(v[y].w) * inv)));
+                        }
                     }
                 }
                 fence_async_smem();
                 warp_arrive(&bs.q_full, lane);
                 factor = bs.factor[i][t];
             }
-            const int lane_lo = p0 + by_group(a, s.row0 + (both ? i * 128 : 0)), lane_hi = s.p_hi;
+            const int lane_lo = p0 + by_group(a, s.row0 + (rows ? i * 128 : 0)), lane_hi = s.p_hi;
             const int win = a.window ? a.window : 1 << 30;
             float ref = kLow, l = 0.f;
             const int n = both ? s.n : (s.n + 1 - i) / 2;
@@ -480,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                     }
                 }
                 const u64 sc2 = pack(sc, sc), to2 = pack((float)ve - ref, (float)ve - ref);
-                // (scores so large that a difference of two in fp32 may pass the room that it should keep)
+                // Scores so large that ref's rounding counts are taken as above, rounded before the difference: the row's
+                // largest would lose its weight else.
                 const bool far = __any_sync(0xffffffffu, fabsf(ref) > 1e6f && ref != kLow);
                 u64 sums[2] = {0, 0};
 #pragma unroll 1
@@ -489,11 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                     tmem_ld<32>(my_s + c * 32, x);
                     tmem_ld_wait();
                     tmem_regs_ready_n<32>(x);
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) unpack(fma2(pack(x[k], x[k + 1]), sc2, to2), x[k], x[k + 1]);
                     if (far) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = x[k] > kRoom ? kRoom : x[k];   // (a NaN stays)
+                        for (int k = 0; k < 32; ++k) x[k] = fmaf(x[k], sc, (float)ve) - ref;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) unpack(fma2(pack(x[k], x[k + 1]), sc2, to2), x[k], x[k + 1]);
                     }
                     if (edge) mask32(seen(c), x, -INFINITY);
 #pragma unroll
@@ -536,14 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
             const float inv = sum == 0.f ? 0.f : s.parts == 1 ? pow2(-kTop) / sum : pow2(-kTop);
             const size_t slot = slot_of(s.v0, s.part);
             if (s.parts > 1) {
-                if (on && (both || i == 0)) reinterpret_cast<float2*>(a.part_ml)[slot * kRT + row] = make_float2(m, sum);
+                if (on && (rows || i == 0)) reinterpret_cast<float2*>(a.part_ml)[slot * kRT + row] = make_float2(m, sum);
                 if (tid == 0 && s.part == 0) a.meta[cta] = make_int4(s.parts | s.nr << 12, s.q0, s.row0, s.h);
             }
             // A lane's own columns of its rows, or half of them of the rows that both have: 64 at a time through the
             // warp's 8 KB of what held Q, so that rows go out in whole lines (a thread writing its own row: 6 us).
             const uint32_t own = smem_u32(sm) + warp * 8192;   // [32 rows][16 pieces], a row's turned by its number
             const long long out_at = (long long)(s.q0 + tok) * a.out_row + head;
-            const int first_row = (both ? i * 128 : 0) + (warp & 3) * 32;
+            const int first_row = (rows ? i * 128 : 0) + (warp & 3) * 32;
 #pragma unroll 1
             for (int half = both ? 0 : i; half < (both ? 2 : i + 1); ++half) {
 #pragma unroll 1
@@ -590,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                     const float4 v = lds_float4(own + r * 256 + ((c4 ^ (r & 15)) << 4));
                     const long long at = __shfl_sync(0xffffffffu, out_at, r);
                     if (to >= s.nr) continue;
-                    const int d = half * 64 + c4 * 4;
+                    const int d = (DB == 2 ? i * 128 : 0) + half * 64 + c4 * 4;
                     if (s.parts == 1) {
                         *reinterpret_cast<uint2*>(a.out + at + d) = make_uint2(bf2(v.x, v.y), bf2(v.z, v.w));
                     } else {
@@ -620,7 +656,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
 // each, four rows under way; of many parts (one long request) 4 rows, whose parts the warps share. (The last
 // CTA to write its part joining them took 40 to 80 us for 256 rows, by itself.)
 constexpr int kJoinThreads = 256, kFewParts = 12, kMostChunks = 512;
+template <int DB>
 __global__ void __launch_bounds__(kJoinThreads) join4_kernel(const __grid_constant__ Args a) {
+    constexpr int kRT = Form<DB>::RT, kD = Form<DB>::D;
     __shared__ long long warp_sums[33];
     __shared__ int4 item[kMostChunks];
     __shared__ int jobs_before[kMostChunks], begins[kMostChunks];
@@ -636,7 +674,7 @@ __global__ void __launch_bounds__(kJoinThreads) join4_kernel(const __grid_consta
         int parts = it.x & 0xfff;
         const int nr = it.x >> 12;
         if (parts > n - v || nr > kRT) parts = 0;              // (a call that gave up)
-        const int jobs = parts == 0 ? 0 : parts <= kFewParts ? (nr + 31) / 32 : (nr + 3) / 4;
+        const int jobs = DB * (parts == 0 ? 0 : parts <= kFewParts ? (nr + 31) / 32 : (nr + 3) / 4);
         long long total;
         const long long incl = block_scan(jobs ? (1ll << 32) + jobs : 0, warp_sums, &total);
         if (jobs) {
@@ -653,7 +691,8 @@ __global__ void __launch_bounds__(kJoinThreads) join4_kernel(const __grid_consta
     for (int job = blockIdx.x; job < n_jobs; job += gridDim.x) {
         const int k = last_not_above(jobs_before, n_items, job);
         const int4 it = item[k];
-        const int parts = it.x & 0xfff, nr = it.x >> 12, v0 = begins[k], at = job - jobs_before[k];
+        const int parts = it.x & 0xfff, nr = it.x >> 12, v0 = begins[k], j = job - jobs_before[k], at = j / DB;
+        const int d0 = DB == 2 ? (j & 1) * 128 : 0;            // of the 128 dims of this job
         const bool few = parts <= kFewParts;
         // four rows of this warp's, and its parts of them
         const int r0 = few ? at * 32 + warp * 4 : at * 4;
@@ -681,7 +720,7 @@ __global__ void __launch_bounds__(kJoinThreads) join4_kernel(const __grid_consta
             for (int y = 0; y < 4; ++y) {
                 const size_t row = slot_of(v0, i) * kRT + min(r0 + y, nr - 1);
                 const float2 st = __ldcg(&ml[row]);
-                const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * kD) + lane);
+                const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * kD + d0) + lane);
                 const float f = st.y != 0.f ? ex2(st.x - m[y]) : 0.f;
                 sum[y] = fmaf(f, st.y, sum[y]);
                 // (a part with no weight does not count, whatever it holds)
@@ -724,7 +763,7 @@ __global__ void __launch_bounds__(kJoinThreads) join4_kernel(const __grid_consta
             const float inv = sum[y] == 0.f ? 0.f : 1.f / sum[y];
             const int rr = it.z + row, tok = by_group(a, rr);
             *reinterpret_cast<uint2*>(a.out + (size_t)(it.y + tok) * a.out_row + (size_t)(it.w * a.group + rr - tok * a.group) * kD +
-                                      lane * 4) =
+                                      d0 + lane * 4) =
                 make_uint2(bf2(acc[y].x * inv, acc[y].y * inv), bf2(acc[y].z * inv, acc[y].w * inv));
         }
     }
@@ -735,21 +774,26 @@ int smem_bytes(int n_req) { return kOffBars + (int)sizeof(Bars) + n_req * (int)s
 }  // namespace
 
 void chunk4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats) {
-    *o_floats = (size_t)sm_count * 2 * kRT * kD;
-    *ml_floats = (size_t)sm_count * 4 * kRT;
+    static_assert(Form<1>::RT * Form<1>::D == Form<2>::RT * Form<2>::D, "parts of one size");
+    *o_floats = (size_t)sm_count * 2 * Form<1>::RT * Form<1>::D;
+    *ml_floats = (size_t)sm_count * 4 * Form<1>::RT;
 }
 
 cudaError_t set_chunk4_attrs() {
-    return cudaFuncSetAttribute(chunk4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxBatch));
+    cudaError_t e = cudaFuncSetAttribute(chunk4_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxBatch));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk4_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxBatch));
+    return e;
 }
 
-cudaError_t launch_chunk4(int sm_count, const Args& a, cudaStream_t st) {
+cudaError_t launch_chunk4(int sm_count, int head_dim, const Args& a, cudaStream_t st) {
     if (sm_count > kMostChunks) return cudaErrorInvalidValue;
-    chunk4_kernel<<<sm_count, kThreads, smem_bytes(a.n_req), st>>>(a);
+    if (head_dim == 128) chunk4_kernel<1><<<sm_count, kThreads, smem_bytes(a.n_req), st>>>(a);
+    else chunk4_kernel<2><<<sm_count, kThreads, smem_bytes(a.n_req), st>>>(a);
     return cudaGetLastError();
 }
-cudaError_t launch_join4(int sm_count, const Args& a, cudaStream_t st) {
-    return launch_k(join4_kernel, dim3((unsigned)(4 * sm_count)), dim3(kJoinThreads), 0, st, true, a);
+cudaError_t launch_join4(int sm_count, int head_dim, const Args& a, cudaStream_t st) {
+    return launch_k(head_dim == 128 ? join4_kernel<1> : join4_kernel<2>, dim3((unsigned)(4 * sm_count)), dim3(kJoinThreads), 0, st,
+                    true, a);
 }
 
 }  // namespace kv8

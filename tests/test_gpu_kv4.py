@@ -323,7 +323,7 @@ def _attend_64(c, q, cu, scale, window=0, layer=0):
         rounding = 2.0 ** -11 * 8 * torch.einsum("hgit,th->ihg", w, sm[..., 0])[..., None]
         reach = x.abs().sum(-1, keepdim=True) * k.abs().amax((0, 2))[None, :, None, None] * abs(scale)
         scores = (2.0 ** -24 * c.D / 4 * reach / c.D ** 0.5 + 2.0 ** -20) * torch.einsum("hgit,thd->ihgd", w, v.abs()) * 2
-        if nq * G > 8 and c.D == 128:
+        if nq * G > (24 if c.D == 128 else 32):
             walk = 2.0 ** -9 * x.square().sum(-1, keepdim=True).sqrt() * k.abs().amax((0, 2))[None, :, None, None] * abs(scale)
             scores = scores + (2 * walk + 2.0 ** -11) * torch.einsum("hgit,thd->ihgd", w, v.abs())
         tol[cus[b]:cus[b + 1]] = (2.0 ** -8 * o.abs() + rounding + scores).reshape(nq, -1, c.D)
@@ -364,6 +364,17 @@ def _check(c, q, cu, out, scale, window=0, layer=0):
     (1, 3, 128, 32, [2000, 130], [700, 100], 300),
     (4, 16, 128, 16, [513, 100], [33, 1], 64),
     (1, 300, 128, 16, [260, 3], [2, 1], 0),
+    (1, 3, 256, 16, [2000, 129], [700, 129], 0),
+    (2, 8, 256, 64, [513, 4000, 200], [33, 300, 1], 0),
+    (4, 4, 256, 32, [3000], [1000], 300),
+    (1, 20, 256, 128, [260, 9000], [1, 7], 0),
+    (1, 17, 256, 16, [9000], [1], 0),
+    (1, 129, 256, 16, [300, 20], [1, 2], 0),
+    (8, 2, 256, 32, [1, 128, 129, 127, 640], [1, 64, 65, 127, 640], 0),
+    (1, 24, 128, 16, [700, 300], [1, 2], 0),
+    (2, 25, 128, 32, [700, 3000], [1, 1], 0),
+    (2, 33, 256, 32, [700, 3000], [1, 1], 0),
+    (1, 1, 256, 16, [4000, 100], [600, 33], 256),
 ])
 def test_attend(Hk, G, D, bs, lens, news, window):
     g = _gen(Hk * 1000 + G * 100 + bs)
@@ -404,7 +415,7 @@ def test_attend_many_requests_of_all_kinds():
     c.close()
 
 
-@pytest.mark.parametrize("heads", [2, 4, 32])
+@pytest.mark.parametrize("heads", [2, 4, 32, 96])
 def test_attend_rows_that_see_nothing_give_zeros(heads):
     """More rows than tokens: the first ones lie before the request."""
     g = _gen(8)
@@ -452,7 +463,7 @@ def test_attend_leaves_out_what_is_out_of_bounds(why):
     c.close()
 
 
-@pytest.mark.parametrize("heads", [8, 24])
+@pytest.mark.parametrize("heads", [8, 24, 96])
 def test_attend_whatever_lies_behind_a_request(heads):
     """Scales of NaN and infinity behind the length, in its last block and others, do not show."""
     g = _gen(21)
@@ -476,10 +487,10 @@ def test_attend_whatever_lies_behind_a_request(heads):
 
 
 @pytest.mark.parametrize("offset", [0.0, 3.0])
-@pytest.mark.parametrize("heads", [4, 24])
+@pytest.mark.parametrize("heads", [4, 24, 40])
 def test_attend_equal_weights(offset, heads):
     """Where all tokens weigh the same, every weight rounds the same way: the mean of many values that nearly cancel must not
-    show it. Per output: bf16's rounding, 2^-11 of the mean around V's middle, fp32 sums of 12,000 values of up to 7. With 24
+    show it. Per output: bf16's rounding, 2^-11 of the mean around V's middle, fp32 sums of 12,000 values of up to 7. With 40
     heads values are rounded to fp16 (2^-11 of each, and all weights alike: 2^-11 of the mean)."""
     g = _gen(77)
     n = 12000
@@ -493,13 +504,13 @@ def test_attend_equal_weights(offset, heads):
     want = v.mean(0)
     middle = float((c.v_scale[0][0, 0, 0, 1].double() + 8 * c.v_scale[0][0, 0, 0, 0].double()))
     tol = 2.0 ** -8 * want.abs() + 2.0 ** -11 * (want - middle).abs() + 7 * 2.0 ** -20
-    if heads > 8:
+    if heads > 24:
         tol = 2.0 ** -8 * want.abs() + 2.0 ** -11 * want.abs() + 2.0 ** -11 * v.abs().mean(0) + 7 * 2.0 ** -20
     assert bool(((out[0] - want).abs() <= tol).all())
     c.close()
 
 
-@pytest.mark.parametrize("heads", [1, 20])
+@pytest.mark.parametrize("heads", [1, 20, 40])
 @pytest.mark.parametrize("share", [0.5, 0.999])
 def test_attend_long_tail_behind_one_weight(share, heads):
     """One token with `share` of the weight in front of 30,000 equal ones that hold the rest between them."""
@@ -523,7 +534,7 @@ def test_attend_long_tail_behind_one_weight(share, heads):
     c.close()
 
 
-@pytest.mark.parametrize("G,D", [(2, 128), (12, 128), (3, 256)])
+@pytest.mark.parametrize("G,D", [(2, 128), (12, 128), (40, 128), (3, 256), (24, 256), (40, 256)])
 def test_attend_wide_scores_and_scales(G, D):
     """Scores over hundreds, rows of all sizes, constant rows (scale 0) of V, queries of 2^-40 to 2^40, scores of 10^14, scales
     below 0 and of 0."""
@@ -880,15 +891,16 @@ def test_one_long_request_over_all_parts(Hk, G, n, news):
     c.close()
 
 
-def test_a_mixed_batch_captured_and_replayed_with_other_lengths():
+@pytest.mark.parametrize("D", [128, 256])
+def test_a_mixed_batch_captured_and_replayed_with_other_lengths(D):
     """A mixed batch through both kernels in a captured call, replayed with other lengths; rows behind the last request stay."""
     g = _gen(87)
     B = 9
     lens, news = [900, 40, 700, 300, 1, 2000, 64, 512, 130], [200, 1, 1, 90, 1, 3, 64, 0, 1]
-    c = _kv4(batch=B, n_kv_heads=2, head_dim=128, block_tokens=16, n_blocks=400, max_blocks=150)
+    c = _kv4(batch=B, n_kv_heads=2, head_dim=D, block_tokens=16, n_blocks=400, max_blocks=150)
     _filled(c, g, lens)
     T = sum(news)
-    q = _bf16(g, T + 40, 8, 128)
+    q = _bf16(g, T + 40, 8, D)
     cu = _cu(news)
     out = torch.full_like(q, 9.0)
     s = torch.cuda.Stream()
@@ -969,7 +981,7 @@ def test_the_largest_batch():
     c.close()
 
 
-@pytest.mark.parametrize("G,D", [(4, 128), (20, 128), (4, 256)])
+@pytest.mark.parametrize("G,D", [(4, 128), (20, 128), (40, 128), (4, 256), (20, 256), (40, 256)])
 def test_attend_constant_rows_of_large_values(G, D):
     """V rows without a scale, 600 values of up to 2^36 (2^45.3 in sum; 2^47 is allowed)."""
     g = _gen(90)
