@@ -994,3 +994,175 @@ def test_attend_constant_rows_of_large_values(G, D):
     out = c.attend(q, cu, scale=0.1)
     _check(c, q, cu, out, 0.1)
     c.close()
+
+
+# ---------------------------------------------------------------------------------------------- attend, closely
+def _few(D):
+    """Query rows per KV head up to which a request's codes enter the products as they are."""
+    return 24 if D == 128 else 32
+
+
+def _close_64(c, q, cu, scale, window=0, gone=()):
+    """(outputs, tolerance) in fp64, of requests whose keys and values lie well within fp16's range. `gone`: (request, token) that
+    are absent.
+
+    Where a request has more than _few rows per KV head keys and values are rounded to fp16 first, as documented, here too
+    (scaled by 2^8, away from fp16's subnormals, as the kernel scales by its own power of two); what is left then, per output:
+      2^-8 |o|             bf16's rounding;
+      2^-11 sum w |v|      a weight's rounding to fp16 (as it is where codes enter exactly: of w s |n - 8|, n - 8 at most 8);
+      sum w d |v - o|      d: what a score is off by. fp32 sums of D products, 16 at a time, two roundings or truncations of
+                           2^-23 of all magnitudes each (codes enter as s <q, n> + m sum q, of larger magnitudes);
+                           2^-22 of the score itself for the factors and the difference from the reference; 2^-19 for
+                           logarithm, exponential and reciprocal;
+      n / 8 2^-23 sum w |v|  fp32 sums of n weighted values, 16 at a time;
+      2^-30 max |v|        weights below 2^-35 of the row's largest."""
+    cus, lens = cu.tolist(), c.len.tolist()
+    Hk, D, G = c.Hk, c.D, q.shape[1] // c.Hk
+    out, tol = (torch.zeros(q.shape, dtype=torch.float64, device="cuda") for _ in "ot")
+    for b in range(len(cus) - 1):
+        n, nq = lens[b], cus[b + 1] - cus[b]
+        if nq == 0 or n == 0:
+            continue
+        many = nq * G > _few(D)
+        k, v = _values(c, "k", b, n), _values(c, "v", b, n)
+        blk = c.table[b, :-(-n // c.bs)].long()
+        ksm, vsm = (t[0][blk].double().transpose(1, 2).reshape(-1, Hk, 2)[:n].abs() for t in (c.k_scale, c.v_scale))
+        mid = (vsm[..., :1] * 8).expand(n, Hk, D)
+        size_k, size_v = k.abs(), v.abs()
+        if many:
+            k, v = ((x * 256).half().double() / 256 for x in (k, v))
+            mid = size_v
+        else:
+            size_k = (k.abs() + 2 * ksm[..., 1:])
+            size_v = size_v + 2 * mid
+        pos = torch.arange(n - nq, n, device="cuda")[:, None]
+        t = torch.arange(n, device="cuda")[None]
+        see = (t <= pos) & ((t > pos - window) if window else (t >= 0))
+        for r, tok in gone:
+            if r == b:
+                see[:, tok] = False
+        for h in range(Hk):
+            x = q[cus[b]:cus[b + 1], h * G:(h + 1) * G].double()
+            a = torch.einsum("igd,td->igt", x, k[:, h]) * scale
+            d = torch.einsum("igd,td->igt", x.abs(), size_k[:, h]) * (abs(scale) * D / 8 * 2.0 ** -23) + 2.0 ** -22 * a.abs() + 2.0 ** -19
+            w = torch.softmax(a.masked_fill(~see[:, None], float("-inf")), -1)
+            w = torch.where(see.any(-1)[:, None, None], w, 0.0)
+            o = w @ v[:, h]
+            e = 2.0 ** -8 * o.abs() + (2.0 ** -11 * (w @ mid[:, h])) + n / 8 * 2.0 ** -23 * (w @ size_v[:, h])
+            e += (w * d) @ v[:, h].abs() + (w * d).sum(-1, keepdim=True) * o.abs()
+            e += 2.0 ** -30 * size_v[:, h].amax()
+            out[cus[b]:cus[b + 1], h * G:(h + 1) * G] = o
+            tol[cus[b]:cus[b + 1], h * G:(h + 1) * G] = e
+    return out, tol
+
+
+def _check_close(c, q, cu, out, scale, window=0, gone=()):
+    want, tol = _close_64(c, q, cu, scale, window, gone)
+    rows = slice(int(cu[0]), int(cu[-1]))
+    bad = ~((out.double() - want).abs() <= tol)[rows]
+    assert not bool(bad.any()), (int(bad.sum()), [int(i) for i in torch.nonzero(bad)[0]],
+                                 float(((out.double() - want).abs() / (tol + 1e-300))[rows].nan_to_num(1e30).max()))
+
+
+_SHAPES = [
+    # few rows per KV head
+    (2, 4, 128, 16, [300, 129, 128, 1], [5, 5, 1, 1], 0),
+    (2, 8, 128, 64, [1000], [3], 100),
+    (8, 1, 128, 16, [400, 17], [20, 17], 33),
+    (1, 24, 128, 32, [6000], [1], 0),
+    (2, 4, 256, 16, [300, 257], [7, 8], 0),
+    (1, 8, 256, 32, [700], [4], 65),
+    # up to a row tile's half: lanes take every other tile of tokens
+    (2, 25, 128, 32, [300, 9000], [1, 1], 0),
+    (1, 8, 128, 128, [4000, 200], [13, 16], 0),
+    (4, 4, 128, 16, [900, 129], [30, 32], 200),
+    (2, 8, 256, 64, [513, 4000], [12, 16], 0),
+    (1, 40, 256, 16, [300], [3], 64),
+    # more
+    (2, 4, 128, 16, [700, 260], [300, 130], 0),
+    (1, 300, 128, 16, [260, 3], [2, 1], 0),
+    (2, 1, 128, 64, [1000, 520], [400, 515], 150),
+    (1, 3, 256, 16, [2000, 129], [200, 129], 0),
+    (2, 1, 256, 128, [600], [600], 256),
+    # both kernels in one call
+    (2, 4, 128, 32, [700, 260, 40], [100, 1, 5], 0),
+    (2, 4, 256, 16, [700, 260, 40], [100, 1, 5], 90),
+]
+
+
+def _shape(case, seed):
+    Hk, G, D, bs, lens, news, window = case
+    g = _gen(seed)
+    c = _kv4(batch=len(lens), n_kv_heads=Hk, head_dim=D, block_tokens=bs, n_blocks=sum(-(-n // bs) for n in lens) + 3,
+             max_blocks=max(-(-n // bs) for n in lens))
+    _filled(c, g, lens)
+    return g, c, _cu(news)
+
+
+@pytest.mark.parametrize("case", _SHAPES)
+def test_attend_closely(case):
+    """Outputs within what the documented roundings explain: a token lost or a few percent of the sums show."""
+    g, c, cu = _shape(case, 92)
+    Hk, G, D, _, _, news, window = case
+    q = _bf16(g, sum(news), Hk * G, D)
+    out = c.attend(q, cu, scale=D ** -0.5, window=window)
+    assert c.check_error() == 0
+    _check_close(c, q, cu, out, D ** -0.5, window)
+    c.close()
+
+
+@pytest.mark.parametrize("case", _SHAPES)
+def test_attend_each_query_finds_its_token(case):
+    """Keys of random signs and queries that are one of them, so that a token has nearly all the weight: a row's own, the one behind
+    it, the first of its window and the one before, the edges of tiles, any. One token too many or too few is another answer."""
+    g, c, cu = _shape(case, 93)
+    Hk, G, D, bs, lens, news, window = case
+    rng = np.random.default_rng(93)
+    c.k_codes[0].copy_(torch.randint(0, 2, c.k_codes[0].shape, generator=g, device="cuda", dtype=torch.uint8) * 15 +
+                       torch.randint(0, 2, c.k_codes[0].shape, generator=g, device="cuda", dtype=torch.uint8) * 240)
+    c.k_scale[0][..., 0] = 0.125
+    c.k_scale[0][..., 1] = -0.9375
+    q = torch.zeros(sum(news), Hk * G, D, device="cuda", dtype=torch.bfloat16)
+    at = 0
+    for b, (n, nq) in enumerate(zip(lens, news)):
+        k = torch.sign(_values(c, "k", b, n)).bfloat16()
+        w = window or n
+        aim = np.zeros((nq, Hk, G), dtype=np.int64)
+        for i in range(nq):
+            p = n - nq + i
+            some = [p, p + 1, p - w + 1, p - w, p // 128 * 128, p // 128 * 128 - 1, (p - w + 1) // 128 * 128, n - nq, 0]
+            some = [t for t in some if 0 <= t < n]
+            for h in range(Hk):
+                for r in range(G):
+                    aim[i, h, r] = some[rng.integers(len(some))] if rng.random() < 0.6 else rng.integers(0, n)
+        aim = torch.from_numpy(aim).cuda()
+        for h in range(Hk):
+            q[at:at + nq, h * G:(h + 1) * G] = k[aim[:, h], h]
+        at += nq
+    out = c.attend(q, cu, scale=1.0, window=window)
+    assert c.check_error() == 0
+    _check_close(c, q, cu, out, 1.0, window)
+    c.close()
+
+
+@pytest.mark.parametrize("case", [_SHAPES[i] for i in (0, 4, 6, 8, 9, 11, 12, 14, 16)])
+@pytest.mark.parametrize("entry", ["none", "beyond"])
+def test_attend_blocks_that_are_not_there(case, entry):
+    """Table entries that are no block, in what rows see: those tokens are absent, and reported."""
+    g, c, cu = _shape(case, 94)
+    Hk, G, D, bs, lens, news, window = case
+    gone = []
+    for b, n in enumerate(lens):
+        for j in {0, (n - 1) // bs // 2, max(0, (n - 130) // bs), max(0, (n - 1) // bs - 1)}:
+            if (j + 1) * bs >= n or (window and (j + 1) * bs <= n - news[b] - window + 1):
+                continue                               # (a last block stays: each row sees something)
+            c.table[b, j] = -1 if entry == "none" else c.n_blocks
+            gone += [(b, t) for t in range(j * bs, (j + 1) * bs)]
+    assert gone
+    q = _bf16(g, sum(news), Hk * G, D)
+    out = c.attend(q, cu, scale=D ** -0.5, window=window)
+    assert c.check_error() == _abi().SRH_ERR_BOUNDS
+    for b in range(len(lens)):                         # (the values of absent tokens, which do not count)
+        c.table[b].clamp_(0, c.n_blocks - 1)
+    _check_close(c, q, cu, out, D ** -0.5, window, gone)
+    c.close()
