@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                 if (!ok) break;
                 const uint32_t* most = bs.most[which][g & 1];
                 const uint32_t all = max(max(most[0], most[1]), max(most[2], most[3]));
-                const int e = min(max((int)(all >> 23) - 127, -100), 100);
+                // (V's as in the kernel of few rows: of all zeros weights would be 2^100 in the softmax's sum, too many for fp32)
+                const int e = min(max((int)(all >> 23) - 127, which ? -64 : -100), 100);
                 const float f = pow2(kTop - e);
                 const __half2 s2 = __float2half2_rn(sv * f), s16 = __float2half2_rn(sv * f * 0.0625f), m2 = __float2half2_rn(mv * f);
                 auto publish = [&] {

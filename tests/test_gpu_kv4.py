@@ -1166,3 +1166,31 @@ def test_attend_blocks_that_are_not_there(case, entry):
         c.table[b].clamp_(0, c.n_blocks - 1)
     _check_close(c, q, cu, out, D ** -0.5, window, gone)
     c.close()
+
+
+@pytest.mark.parametrize("D,G,nq", [(128, 4, 1), (128, 32, 1), (128, 40, 4), (256, 40, 1)])
+@pytest.mark.parametrize("B", [1, 160])
+def test_attend_a_long_prefix_of_zero_values(B, D, G, nq):
+    """35,000 tokens whose values are all 0, with scores 5 (log2) higher behind the first tile, before 5,000 of ordinary values: in one
+    CTA's share of a request (160 requests over the same blocks) and over many."""
+    g = _gen(95)
+    n, zero = 40000, 35072
+    c = _kv4(batch=B, n_kv_heads=1, head_dim=D, block_tokens=64, n_blocks=n // 64, max_blocks=n // 64)
+    _filled(c, g, [n], spread=0, mean=3.0)
+    c.table[:] = torch.arange(n // 64, dtype=torch.int32, device="cuda")
+    c.len.fill_(n)
+    c.k_codes[0].zero_()
+    c.k_scale[0][..., 0] = 1.0
+    c.k_scale[0][..., 1] = 0.0
+    c.k_codes[0][2:, 0, :, 0] = 8                      # dim 0 of the tokens from 128 on
+    c.v_scale[0][:zero // 64] = 0.0
+    q = torch.zeros(B * nq, G, D, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = 5 * math.log(2) / 8
+    out = c.attend(q, _i32([b * nq for b in range(B + 1)]), scale=1.0)
+    assert c.check_error() == 0
+    c.len[1:] = 0
+    want, tol = _close_64(c, q[:nq], _i32([0, nq]), 1.0)
+    assert float(want.abs().min()) > 0.05
+    err = (out.view(B, nq, G, D).double() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    c.close()
