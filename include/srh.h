@@ -787,6 +787,7 @@ int kv4_read(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const i
  * within 2^-11 of each, or 2^-39 of the largest of its 128 tokens (of 2^-64, if V's is smaller). V's scales are taken as at least 2^-64;
  * those that a row sees are to lie within 2^96 of each other, scores within 10^30 of 0, keys within
  * 2^60, and the V values that a row sees, summed by magnitude in a dim, within 2^47.
+ * A block that every row's window has passed is not used, whatever its entry is and whatever it holds.
  */
 int kv4_attend(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,
                int n_req, const uint16_t* d_q, long long q_row, int n_rows, int n_heads, float scale, int window,

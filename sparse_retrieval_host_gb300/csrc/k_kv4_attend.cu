@@ -401,13 +401,13 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                     }
                 }
             if (odd) {
-                // (what lies behind the request, or in no block, may be anything)
+                // (what lies behind the request, in no block, or in one that every row's window has passed, may be anything)
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int tt = t0 + u * 16 + g + 8 * j;
-                        const bool none = tt >= s.len || (off >> u & 1);
+                        const bool none = tt >= s.len || tt < see_first || (off >> u & 1);
                         if (none) iv[u][j] = cm[u][j] = 0.f;
 #pragma unroll
                         for (int t = 0; t < NT; ++t)

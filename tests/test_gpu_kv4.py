@@ -1194,3 +1194,24 @@ def test_attend_a_long_prefix_of_zero_values(B, D, G, nq):
     err = (out.view(B, nq, G, D).double() - want).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
     c.close()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("G,news", [(4, 1), (8, 2), (40, 1)])
+def test_blocks_behind_a_window_may_hold_anything(G, news, D):
+    """Blocks that no query sees any more may have gone to someone else, who has not written every row: scales of NaN and infinity
+    in them do not show, 16 tokens before the first that is seen."""
+    g = _gen(96)
+    c = _kv4(batch=1, n_kv_heads=2, head_dim=D, block_tokens=16, n_blocks=70, max_blocks=64)
+    q, cu = _bf16(g, news, 2 * G, D), _i32([0, news])
+    for first in range(784, 848, 16):                  # the first token that is seen
+        _filled(c, g, [1000])
+        window = 1000 - news + 1 - first
+        want = c.attend(q, cu, scale=0.1, window=window)
+        spare = sorted(set(range(70)) - set(c.table[0].tolist()))[0]
+        odd = torch.tensor([float("nan"), float("inf")], device="cuda").bfloat16()
+        c.k_scale[0][spare], c.v_scale[0][spare] = odd, odd
+        c.table[0, :first // 16] = spare
+        out = c.attend(q, cu, scale=0.1, window=window)
+        assert c.check_error() == 0 and torch.equal(out, want)
+    c.close()
