@@ -784,8 +784,8 @@ int kv4_read(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const i
  * about 2^-28 of its row's largest loses bits). A weight (times V's scale, or V's largest magnitude among 128 tokens)
  * is rounded to fp16: within 2^-11 of it, or 2^-35 of the row's largest. Codes enter exactly where a
  * request has up to 24 query rows per KV head (32 where head_dim is 256); else keys and values do, rounded to fp16:
- * within 2^-11 of each, or 2^-39 of the largest of its 128 tokens (of 2^-64, if V's is smaller). V's scales are taken as at least 2^-64;
- * those that a row sees are to lie within 2^96 of each other, scores within 10^30 of 0, keys within
+ * within 2^-11 of each plus 2^-34 of the largest of its 128 tokens (of 2^-64, if V's is smaller). V's scales are taken as
+ * at least 2^-64; those that a row sees are to lie within 2^96 of each other, scores within 10^30 of 0, keys within
  * 2^60, and the V values that a row sees, summed by magnitude in a dim, within 2^47.
  * A block that every row's window has passed is not used, whatever its entry is and whatever it holds.
  */

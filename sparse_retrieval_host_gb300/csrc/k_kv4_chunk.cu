@@ -4,9 +4,9 @@
 // Rows are the M dimension of both products, S = Q K^T and O = P V. Codes become fp16 values in
 // shared memory once per tile of 128 tokens and are used by up to 256 rows:
 //   k = (m + n s) 2^(14 - e), e the exponent of the tile's largest magnitude,
-// one rounding, 2^-11 of the value at most (or 2^-39 of the tile's largest); the power of two goes into
-// the scores' factor, V's into the exponent u = score + e of the weights 2^(u - ref), which are rounded to
-// fp16, and is taken out of the softmax's sums again. A thread holds a row, so maxima and sums
+// one rounding, 2^-11 of the value at most, plus 16 steps of 2^-39 of the tile's largest where s and m become subnormal;
+// the power of two goes into the scores' factor, V's into the exponent u = score + e of the weights 2^(u - ref), which
+// are rounded to fp16, and is taken out of the softmax's sums again. A thread holds a row, so maxima and sums
 // need no exchange; a row's reference moves only when a weight would pass 2^15.5.
 //
 // A CTA runs two lanes of 128 rows, each with its own S and O in TMEM (P lies over S), so that one
@@ -115,16 +115,17 @@ __device__ __forceinline__ uint32_t bits(__half2 h) {
     return w;
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-// The eight values of a word of codes, as pairs (i, i + 4). A code in the low bits of 1024 is
-// exact there; without the 1024 it is n, or 16 n.
-__device__ __forceinline__ uint4 values8(uint32_t w, __half2 s, __half2 s16, __half2 m) {
-    const __half2 k = __float2half2_rn(1024.f);
+// The eight values of a word of codes, as pairs (i, i + 4). A code in the low bits of 1024, or four bits
+// up in those of 64, is exact there, and n without the 1024 or the 64 (without the product by s as 16 n times s / 16, whose
+// bits a small s loses).
+__device__ __forceinline__ uint4 values8(uint32_t w, __half2 s, __half2 m) {
+    const __half2 k = __float2half2_rn(1024.f), k16 = __float2half2_rn(64.f);
     const uint32_t x = w >> 8;
     uint4 r;
     r.x = bits(__hfma2(__hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), k), s, m));
-    r.y = bits(__hfma2(__hsub2(as_half2((w & 0x00f000f0u) | 0x64006400u), k), s16, m));
+    r.y = bits(__hfma2(__hsub2(as_half2((w & 0x00f000f0u) | 0x54005400u), k16), s, m));
     r.z = bits(__hfma2(__hsub2(as_half2((x & 0x000f000fu) | 0x64006400u), k), s, m));
-    r.w = bits(__hfma2(__hsub2(as_half2((x & 0x00f000f0u) | 0x64006400u), k), s16, m));
+    r.w = bits(__hfma2(__hsub2(as_half2((x & 0x00f000f0u) | 0x54005400u), k16), s, m));
     return r;
 }
 __device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                 // (V's as in the kernel of few rows: of all zeros weights would be 2^100 in the softmax's sum, too many for fp32)
                 const int e = min(max((int)(all >> 23) - 127, which ? -64 : -100), 100);
                 const float f = pow2(kTop - e);
-                const __half2 s2 = __float2half2_rn(sv * f), s16 = __float2half2_rn(sv * f * 0.0625f), m2 = __float2half2_rn(mv * f);
+                const __half2 s2 = __float2half2_rn(sv * f), m2 = __float2half2_rn(mv * f);
                 auto publish = [&] {
                     if (lane == 0) {
                         if (which) bs.v_exp[g % kInfo] = e;
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk4_kernel(const __grid_consta
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) sts128(to + (i >> 1) * kHalf + sw128(t, (i & 1) * 4 + k), values8(x[k], s2, s16, m2));
+                        for (int k = 0; k < 4; ++k) sts128(to + (i >> 1) * kHalf + sw128(t, (i & 1) * 4 + k), values8(x[k], s2, m2));
                     }
                 }
                 fence_async_smem();

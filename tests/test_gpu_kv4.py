@@ -1215,3 +1215,29 @@ def test_blocks_behind_a_window_may_hold_anything(G, news, D):
         out = c.attend(q, cu, scale=0.1, window=window)
         assert c.check_error() == 0 and torch.equal(out, want)
     c.close()
+
+
+@pytest.mark.parametrize("D,G", [(128, 4), (128, 40), (128, 150), (256, 40)])
+def test_attend_small_values_beside_large_ones(D, G):
+    """A row that only sees a token 2^-28 as large as its neighbour: values are within 2^-11, or 2^-34 of the tile's largest."""
+    c = _kv4(batch=1, n_kv_heads=1, head_dim=D, block_tokens=16, n_blocks=1, max_blocks=1)
+    c.resize(_i32([2]))
+    blk = int(c.table[0, 0])
+    for t in (c.k_codes[0], c.k_scale[0], c.v_codes[0], c.v_scale[0]):
+        t.zero_()
+    c.k_scale[0][blk, 0, :, 0] = 1.0
+    c.k_codes[0][blk, 0, 0, 0] = 15                    # token 0, dim 0
+    g = _gen(97)
+    c.v_codes[0][blk, 0, :2] = torch.randint(0, 256, (2, D // 2), generator=g, device="cuda", dtype=torch.uint8)
+    c.v_scale[0][blk, 0, 0, 0] = 0.125
+    c.v_scale[0][blk, 0, 1, 0] = 1.125 * 2.0 ** -32
+    q = torch.zeros(1, G, D, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = -20                                    # token 0 weighs e^-300
+    out = c.attend(q, _i32([0, 1]), scale=1.0)
+    v = _values(c, "v", 0, 2)[:, 0]
+    tol = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -11) * v[1].abs() + 2.0 ** -34 * v[0].abs().max()
+    if G <= _few(D):                                   # (codes enter as n - 8)
+        tol = (2.0 ** -8 + 2.0 ** -11) * v[1].abs() + 2.0 ** -11 * 8 * 1.125 * 2.0 ** -32
+    err = (out[0].double() - v[1]).abs()
+    assert bool((err <= tol).all()), float((err / (tol + 1e-300)).max())
+    c.close()
