@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             if (__any_sync(0xffffffffu, max(both & 0x7fffu, both >> 16 & 0x7fffu) > kLimit)) {
                 const uint4 was = w;
                 w = make_uint4(tame2(w.x), tame2(w.y), tame2(w.z), tame2(w.w));
-                if (was.x != w.x || was.y != w.y || was.z != w.z || was.w != w.w) odd = true;
+                // (a row that belongs to no request may hold anything)
+                if (on && (was.x != w.x || was.y != w.y || was.z != w.z || was.w != w.w)) odd = true;
                 both = reach();
             }
             const float m = bf_lo(both), top = -bf_hi(both);

@@ -1241,3 +1241,42 @@ def test_attend_small_values_beside_large_ones(D, G):
     err = (out[0].double() - v[1]).abs()
     assert bool((err <= tol).all()), float((err / (tol + 1e-300)).max())
     c.close()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("B", [3, 40])
+def test_append_rows_of_no_request_are_not_reported(B, D):
+    """Rows before the first request and behind the last one may hold anything: nothing of them is stored, nothing is reported."""
+    g = _gen(91)
+    c = _kv4(batch=B, n_kv_heads=2, head_dim=D, block_tokens=16, n_blocks=2 * B + 2, max_blocks=4)
+    _filled(c, g, [20] * B)
+    news = [2 + b % 3 for b in range(B)]
+    T = sum(news)
+    k, v = _bf16(g, T + 12, 2, D), _bf16(g, T + 12, 2, D)
+    for x, odd in ((k, float("nan")), (v, float("inf"))):
+        x[:5] = odd
+        x[T + 5:] = -odd
+    k[T + 6], v[2] = 3e38, -3e38
+    cu = _cu(news) + 5
+    before = [t.clone() for t in (*_codes(c, "k"), *_codes(c, "v"))]
+    c.append(k, v, cu)
+    assert c.check_error() == 0
+    kb, vb = c.read(_i32([20 - n for n in news]), cu, T + 12)
+    assert c.check_error() == 0
+    for a, b in ((kb, k), (vb, v)):
+        assert bool((a[:5] == 0).all()) and bool((a[T + 5:] == 0).all())
+        x = b[5:T + 5].float()
+        step = ((x.amax(-1) - x.amin(-1)) / 15)[..., None]
+        assert bool(((a[5:T + 5].float() - x).abs() <= step * (0.5 + 16 * 2.0 ** -8) + 2.0 ** -8 * x.abs()).all())
+    # nothing but the requests' tokens has changed
+    table = c.table.tolist()
+    for t, was in zip((*_codes(c, "k"), *_codes(c, "v")), before):
+        for b in range(B):
+            for p in range(20 - news[b], 20):
+                was[table[b][p // 16], :, p % 16] = t[table[b][p // 16], :, p % 16]
+        assert torch.equal(t, was)
+    # one of a request's own is
+    k[5, 1, 3] = float("nan")
+    c.append(k, v, cu)
+    assert c.check_error() == _abi().SRH_ERR_RANGE
+    c.close()
