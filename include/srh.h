@@ -787,6 +787,11 @@ int kv4_read(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const i
  * within 2^-11 of each plus 2^-34 of the largest of its 128 tokens (of 2^-64, if V's is smaller). V's scales are taken as
  * at least 2^-64; those that a row sees are to lie within 2^96 of each other, scores within 10^30 of 0, keys within
  * 2^60, and the V values that a row sees, summed by magnitude in a dim, within 2^47.
+ * Which requests have how many rows only the device knows. A call of as many rows as requests, or of fewer while they are at
+ * most 128 per KV head, is taken for a decode step (one token each); one of fewer that are more than 128 costs 4 us more than
+ * if only requests with tokens were named. Results are the same whatever the rows turn out to be, but a prompt alone among as many
+ * requests as it has tokens takes up to some five times as long as with n_rows > n_req: name the requests that have tokens (their
+ * rows of table, len and cu), or let q have one row more.
  * A block that every row's window has passed is not used, whatever its entry is and whatever it holds.
  */
 int kv4_attend(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const int32_t* d_len, const int32_t* d_cu,

@@ -631,6 +631,11 @@ cudaError_t set_one() {
 // units more): 24 requests of 8,192 tokens with 32 heads a group 113 us here and 128 there.
 constexpr int kFew = 24;
 constexpr int kFewWide = 32;
+// Rows per KV head of a whole call up to which idle table rows (fewer rows than requests) make no difference. A call of no more rows
+// than requests is a decode step as a rule, and launching both kernels costs one 4 us (20 to 140 us long); but it may be a
+// prompt whose neighbours have no tokens, which only the device knows. On 16,384 tokens one of 128 rows a KV head takes 66 us
+// here and 34 there (on 2,048 22 and 29), of 256 116 and 48, of 4,096 1,586 and 293.
+constexpr int kIdle = 128;
 
 }  // namespace
 
@@ -684,9 +689,10 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
     a.window = window < (1 << 30) ? window : 0;            // (a request is at most 2^30 tokens long)
     const int dim = c.cfg.head_dim, few = dim == 128 ? kFew : kFewWide;
     const long long all = (long long)a.group * n_rows;
-    // One token per request, as the host sees it: this kernel alone. Otherwise requests of more
+    // One token per request, as far as the host can see: this kernel alone. Otherwise requests of more
     // than `few` rows go by the other one, in the same call, as only the device knows which those are.
-    const bool beside = all > few && (n_rows > n_req || a.group > few);
+    const bool idle = n_rows < n_req;
+    const bool beside = all > few && (n_rows > n_req || a.group > few || (idle && all > kIdle));
     if (beside) {
         Args big = a;
         big.rows_lo = a.rows_hi = few;
@@ -694,8 +700,9 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = cudaSuccess;
-    // (with more heads than that a group, none is left for this one)
-    if (!beside || a.group <= few) e = dim == 128 ? run<Shape<1>>(c, a, beside, st) : run<Shape<2>>(c, a, beside, st);
+    // (with more heads than that a group, none is left for this one; in a decode step the other has nothing to run beside)
+    const bool early = beside && !idle;
+    if (!beside || a.group <= few) e = dim == 128 ? run<Shape<1>>(c, a, early, st) : run<Shape<2>>(c, a, early, st);
     if (beside && e == cudaSuccess) e = launch_join4(c.sm_count, dim, a, st);
     return e;
 }

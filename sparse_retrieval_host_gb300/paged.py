@@ -395,7 +395,9 @@ class PagedKV4(PagedKV8):
     [n_blocks][n_kv_heads][block_tokens][head_dim / 2], the even dim in the low half of a byte, scales
     bf16 [n_blocks][n_kv_heads][block_tokens][2]: a scale s and a minimum m per token and head, a value
     is m + code * s. ``buffers`` as for PagedKV8, of these shapes. An appended row changes nothing
-    that is held; latent rows (``shared_kv``) are kept in 8 bits only."""
+    that is held; latent rows (``shared_kv``) are kept in 8 bits only. ``attend`` takes a call of as
+    many rows as ``cu`` has requests for a decode step: a prompt alone among idle requests is quicker with
+    a row more in ``q`` (see kv4_attend in include/srh.h)."""
 
     _calls = ("kv4_append", "kv4_read", "kv4_attend")
 

@@ -1280,3 +1280,26 @@ def test_append_rows_of_no_request_are_not_reported(B, D):
     c.append(k, v, cu)
     assert c.check_error() == _abi().SRH_ERR_RANGE
     c.close()
+
+
+@pytest.mark.parametrize("D,new", [(128, 60), (128, 63), (256, 40), (256, 63), (128, 64), (128, 30), (256, 64), (256, 20)])
+def test_idle_rows_of_the_table_change_nothing(D, new):
+    """A prompt among 63 table rows that have no new tokens. Of more than 128 rows per KV head, and of fewer than the table's: the
+    same kernels, and so the same bits, as by itself."""
+    g = _gen(98)
+    c = _kv4(batch=64, n_kv_heads=2, head_dim=D, block_tokens=16, n_blocks=900, max_blocks=80)
+    _filled(c, g, [100] * 40 + [1200] + [100] * 23)
+    q = _bf16(g, new, 8, D)
+    cu = _cu([0] * 40 + [new] + [0] * 23)
+    out = c.attend(q, cu, scale=0.1)
+    assert c.check_error() == 0
+    _check(c, q, cu, out, 0.1)
+    one = _kv4(batch=1, n_kv_heads=2, head_dim=D, block_tokens=16, n_blocks=900, max_blocks=80,
+               buffers=dict(k_codes=c.k_codes[0], v_codes=c.v_codes[0], k_scale=c.k_scale[0], v_scale=c.v_scale[0],
+                            table=c.table[40:41].contiguous(), len=c.len[40:41].contiguous()))
+    alone = one.attend(q, _i32([0, new]), scale=0.1)
+    _check_close(one, q, _i32([0, new]), alone, 0.1)
+    if 128 < new * 4 and new < 64:
+        assert bool((out == alone).all())
+    one.close()
+    c.close()
