@@ -1303,3 +1303,60 @@ def test_idle_rows_of_the_table_change_nothing(D, new):
         assert bool((out == alone).all())
     one.close()
     c.close()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_layers_of_both_widths_attend_on_one_handle(D):
+    """Attention over 8-bit and 4-bit pools in turn on one handle, whose scratch they share: the bits that handles of their own
+    give, captured and replayed too."""
+    abi = _abi()
+    g = _gen(99)
+    lens, news = [3000, 200, 700, 40], [1, 130, 9, 1]
+    kw = dict(batch=4, n_kv_heads=2, head_dim=D, block_tokens=32, n_blocks=160, max_blocks=100)
+    c4 = _kv4(**kw)
+    _filled(c4, g, lens)
+    c8 = _kv8(buffers=dict(table=c4.table, len=c4.len), **kw)
+    for codes, scale in ((c8.k_codes, c8.k_scale), (c8.v_codes, c8.v_scale)):
+        codes[0].copy_(torch.randn(codes[0].shape, generator=g, device="cuda").to(FP8).view(torch.uint8))
+        scale[0].fill_(0.5)
+    T = sum(news)
+    q, cu = _bf16(g, T, 8, D), _cu(news)
+    one = _i32([0, 1, 2, 3, 4])                        # a decode step
+    want = [(c4.attend(q, x, scale=0.1), c8.attend(q, x, scale=0.1)) for x in (cu, one)]
+    lib = abi.load()
+    outs = [[torch.zeros_like(q) for _ in range(2)] for _ in range(2)]
+
+    def call(fn, pool, x, out):
+        rows = T if x is cu else 4
+        assert fn(c8.cache, pool, c4.table.data_ptr(), c4.len.data_ptr(), x.data_ptr(), 4, q.data_ptr(), 8 * D, rows, 8, 0.1, 0,
+                  out.data_ptr(), 8 * D, torch.cuda.current_stream().cuda_stream) == 0
+
+    def step():
+        for (a, b), x in zip(outs, (cu, one)):
+            call(lib.kv4_attend, c4._pool[0], x, a)
+            call(lib.kv8_attend, c8._pool[0], x, b)
+            call(lib.kv4_attend, c4._pool[0], x, a)
+
+    def check():
+        assert c8.check_error() == 0
+        for got, exp, rows in zip(outs, want, (T, 4)):
+            for a, b in zip(got, exp):
+                assert torch.equal(a[:rows], b[:rows])
+                a.zero_()
+
+    for _ in range(3):
+        step()
+        check()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        graph.replay()
+        check()
+    c4.close()
+    c8.close()
