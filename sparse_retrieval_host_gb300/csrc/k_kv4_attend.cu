@@ -609,8 +609,8 @@ size_t smem_bytes(int n_req) {
 template <typename S>
 cudaError_t run(const Cache& c, Args a, bool beside, cudaStream_t st) {
     const int grid = S::CTAS * c.sm_count;
-    size_t o = 0, ml = 0;
-    chunk4_scratch(c.sm_count, &o, &ml);
+    size_t o = 0, ml = 0, meta = 0;
+    chunk4_scratch(c.sm_count, &o, &ml, &meta);
     // (behind what the kernel beside it has)
     a.part_o = c.d_part_o + o;
     a.part_ml = c.d_part_ml + ml;
@@ -639,8 +639,8 @@ constexpr int kIdle = 128;
 
 }  // namespace
 
-void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* arrivals) {
-    chunk4_scratch(sm_count, o_floats, ml_floats);
+void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* meta, size_t* arrivals) {
+    chunk4_scratch(sm_count, o_floats, ml_floats, meta);
     *o_floats += (size_t)sm_count * 2 * 2 * 16 * 128;
     *ml_floats += (size_t)sm_count * 2 * 4 * 16;
     *arrivals = (size_t)sm_count * 9;
@@ -694,6 +694,9 @@ cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* 
     const bool idle = n_rows < n_req;
     const bool beside = all > few && (n_rows > n_req || a.group > few || (idle && all > kIdle));
     if (beside) {
+        size_t o = 0, ml = 0, meta = 0;
+        chunk4_scratch(c.sm_count, &o, &ml, &meta);
+        if (o > c.part_o_floats || ml > c.part_ml_floats || meta > c.meta_n) return cudaErrorInvalidValue;
         Args big = a;
         big.rows_lo = a.rows_hi = few;
         const cudaError_t e = launch_chunk4(c.sm_count, dim, big, st);

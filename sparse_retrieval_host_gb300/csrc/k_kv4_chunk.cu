@@ -775,10 +775,11 @@ int smem_bytes(int n_req) { return kOffBars + (int)sizeof(Bars) + n_req * (int)s
 
 }  // namespace
 
-void chunk4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats) {
+void chunk4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* meta) {
     static_assert(Form<1>::RT * Form<1>::D == Form<2>::RT * Form<2>::D, "parts of one size");
     *o_floats = (size_t)sm_count * 2 * Form<1>::RT * Form<1>::D;
     *ml_floats = (size_t)sm_count * 4 * Form<1>::RT;
+    *meta = (size_t)sm_count;            // a chunk per CTA
 }
 
 cudaError_t set_chunk4_attrs() {

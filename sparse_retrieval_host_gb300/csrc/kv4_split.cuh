@@ -335,8 +335,9 @@ __device__ __forceinline__ bool finish(const Args& a, const Segment& s, int tid,
 
 }  // namespace split
 
-// The kernel of many rows per KV head: its share of the handle's scratch (the first), and its launch.
-void chunk4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats);
+// The kernel of many rows per KV head: its share of the handle's scratch (the first), and its launch, which leaves it to the
+// caller to check that it is there.
+void chunk4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* meta);
 cudaError_t set_chunk4_attrs();
 cudaError_t launch_chunk4(int sm_count, int head_dim, const split::Args& a, cudaStream_t st);
 // .. and of what joins its parts, after the kernel of few rows that runs beside it.

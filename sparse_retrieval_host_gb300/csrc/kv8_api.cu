@@ -176,10 +176,11 @@ int kv8_create(const kv8_config* cfg, kv8_cache** out) {
         where = "device scratch";
         kv8::attend_scratch(c->sm_count, cfg->head_dim, &c->part_o_floats, &c->part_ml_floats, &c->meta_n);
         if (takes_4_bits(*cfg)) {
-            size_t o = 0, ml = 0;
-            kv8::attend4_scratch(c->sm_count, &o, &ml, &c->arrived_n);
+            size_t o = 0, ml = 0, meta = 0;
+            kv8::attend4_scratch(c->sm_count, &o, &ml, &meta, &c->arrived_n);
             if (o > c->part_o_floats) c->part_o_floats = o;
             if (ml > c->part_ml_floats) c->part_ml_floats = ml;
+            if (meta > c->meta_n) c->meta_n = meta;
         }
         e = cudaMalloc(&c->d_err, sizeof(uint32_t));
         if (e == cudaSuccess) e = cudaMemset(c->d_err, 0, sizeof(uint32_t));

@@ -24,7 +24,7 @@ struct Cache {
     int* d_ctrl = nullptr;          // the attention's chunk counter and count
     int* d_arrived = nullptr;       // parts of split items that are written (4-bit attention); zeros between calls
     size_t arrived_n = 0;
-    size_t part_o_floats = 0;       // sizes of the three, which the launcher checks
+    size_t part_o_floats = 0;       // sizes of the three, which the launchers check
     size_t part_ml_floats = 0;
     size_t meta_n = 0;
     char last_error[256] = {0};
@@ -68,7 +68,7 @@ cudaError_t launch_append4(const Cache& c, const Layer& l, const int32_t* table,
 cudaError_t launch_read(const Cache& c, const Layer& l, const int32_t* table, const int32_t* len, const int32_t* start,
                         const int32_t* cu, int n_req, int n_rows, cudaStream_t st);
 // What kv4_attend needs of the scratch, and arrival counters.
-void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* arrivals);
+void attend4_scratch(int sm_count, size_t* o_floats, size_t* ml_floats, size_t* meta, size_t* arrivals);
 cudaError_t set_attend4_attrs();
 cudaError_t launch_attend4(const Cache& c, const kv4_pool& pool, const int32_t* table, const int32_t* len,
                            const int32_t* cu, int n_req, const uint16_t* q, long long q_row, int n_rows, int n_heads,
