@@ -45,11 +45,11 @@ constexpr float kHead = 10.f;            // log2 of the weight that a new refere
 constexpr float kRoom = 15.5f;           // a row's reference moves when a weight would pass 2^15.5
 constexpr float kLeastScale = 5.421010862427522e-20f;   // 2^-64
 
-// DB: head_dim / 128. A warp has NT groups of 8 rows: one (two take 254 registers, and 2.0 us for 9 to 16 rows against 1.0 of two
+// DB: head_dim / 128. A row tile has 8 rows (16 took 254 registers, and 2.0 us for 9 to 16 rows against 1.0 of two
 // row tiles that read the codes twice, the second time from L2).
 template <int DB_>
 struct Shape {
-    static constexpr int DB = DB_, NT = 1, RT = 8 * NT, D = 128 * DB;
+    static constexpr int DB = DB_, RT = 8, D = 128 * DB;
     // (with four CTAs 128 registers a thread, which spill: the decode batch 152 us, 142 with three)
     static constexpr int CTAS = DB == 1 ? 3 : 2;
     static constexpr int kPitch = D + 4;                       // floats of a row of the warps' outputs
@@ -66,7 +66,7 @@ struct Shape {
     static constexpr int kRing = kWarps * STAGES * kStage;
     // Queries as operands, and factor, sum and position of each row; twice, as the next segment's are
     // made while this one's outputs are.
-    static constexpr int kQBytes = NT * DB * 2048, kRowBytes = RT * 16;
+    static constexpr int kQBytes = DB * 2048, kRowBytes = RT * 16;
     static constexpr int kOffStat = kOutBytes, kOffRing = kOffStat + kStatBytes, kOffQ = kOffRing + kRing;
     static constexpr int kOffRow = kOffQ + 2 * kQBytes, kOffFirst = kOffRow + 2 * kRowBytes;
 };
@@ -141,7 +141,7 @@ __device__ __forceinline__ uint32_t v_at(uint32_t t, uint32_t p) {
 // ---------------------------------------------------------------- the kernel
 template <typename S>
 __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid_constant__ Args a) {
-    constexpr int DB = S::DB, NT = S::NT, RT = S::RT, D = S::D, SUB = S::SUB;
+    constexpr int DB = S::DB, RT = S::RT, D = S::D, SUB = S::SUB;
     extern __shared__ __align__(16) unsigned char sm[];
     float* const outs = reinterpret_cast<float*>(sm);                       // [warp][row][kPitch]
     float2* const stats = reinterpret_cast<float2*>(sm + S::kOffStat);      // [warp][row]: reference, sum
@@ -242,52 +242,51 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     };
 
     // A segment's queries as B fragments: lane (g, c) holds dims 32 c .. of row g, per 8 dims two k steps.
-    // A warp makes those of 8 rows.
+    // One warp makes them.
     auto stage = [&](const Segment& s, int to) {
-        for (int t = warp; t < NT; t += kWarps) {
-            const int row = s.row0 + t * 8 + g, tok = by_group(a, row);
-            const bool on = t * 8 + g < s.nr;
-            const uint16_t* x = a.q + (size_t)(s.q0 + (on ? tok : 0)) * a.q_row +
-                                (size_t)(s.h * a.group + (on ? row - tok * a.group : 0)) * D;
-            uint4 w[DB][4];
-            uint32_t m = 0;
+        if (warp != 0) return;
+        const int row = s.row0 + g, tok = by_group(a, row);
+        const bool on = g < s.nr;
+        const uint16_t* x = a.q + (size_t)(s.q0 + (on ? tok : 0)) * a.q_row +
+                            (size_t)(s.h * a.group + (on ? row - tok * a.group : 0)) * D;
+        uint4 w[DB][4];
+        uint32_t m = 0;
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[d][i] = on ? __ldg(reinterpret_cast<const uint4*>(x + d * 128 + c * 32 + i * 8)) : make_uint4(0, 0, 0, 0);
-                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[d][i].x & 0x7fff7fffu, w[d][i].y & 0x7fff7fffu),
-                                             __vmaxu2(w[d][i].z & 0x7fff7fffu, w[d][i].w & 0x7fff7fffu)));
-                }
-            m = max(m & 0xffffu, m >> 16);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            // to a largest magnitude in [2^14, 2^15)
-            const int e = min(max((int)(m >> 7) - 127 - 14, -120), 120);
-            const float inv = __uint_as_float((uint32_t)(127 - e) << 23), inv16 = inv * 0.0625f;
-            float sum = 0.f;
-            uint4* const q = reinterpret_cast<uint4*>(sm + S::kOffQ + to * S::kQBytes) + t * DB * 128 + lane;
+            for (int i = 0; i < 4; ++i) {
+                w[d][i] = on ? __ldg(reinterpret_cast<const uint4*>(x + d * 128 + c * 32 + i * 8)) : make_uint4(0, 0, 0, 0);
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[d][i].x & 0x7fff7fffu, w[d][i].y & 0x7fff7fffu),
+                                         __vmaxu2(w[d][i].z & 0x7fff7fffu, w[d][i].w & 0x7fff7fffu)));
+            }
+        m = max(m & 0xffffu, m >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // to a largest magnitude in [2^14, 2^15)
+        const int e = min(max((int)(m >> 7) - 127 - 14, -120), 120);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23), inv16 = inv * 0.0625f;
+        float sum = 0.f;
+        uint4* const q = reinterpret_cast<uint4*>(sm + S::kOffQ + to * S::kQBytes) + lane;
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // dims 0 .. 7: pairs (k, k + 4) as the codes of a word lie
-                    const uint32_t v[4] = {w[d][i].x, w[d][i].y, w[d][i].z, w[d][i].w};
-                    q[(d * 4 + i) * 32] = make_uint4(half2_bits(bf_lo(v[0]) * inv, bf_lo(v[2]) * inv),
-                                                     half2_bits(bf_hi(v[0]) * inv16, bf_hi(v[2]) * inv16),
-                                                     half2_bits(bf_lo(v[1]) * inv, bf_lo(v[3]) * inv),
-                                                     half2_bits(bf_hi(v[1]) * inv16, bf_hi(v[3]) * inv16));
+            for (int i = 0; i < 4; ++i) {
+                // dims 0 .. 7: pairs (k, k + 4) as the codes of a word lie
+                const uint32_t v[4] = {w[d][i].x, w[d][i].y, w[d][i].z, w[d][i].w};
+                q[(d * 4 + i) * 32] = make_uint4(half2_bits(bf_lo(v[0]) * inv, bf_lo(v[2]) * inv),
+                                                 half2_bits(bf_hi(v[0]) * inv16, bf_hi(v[2]) * inv16),
+                                                 half2_bits(bf_lo(v[1]) * inv, bf_lo(v[3]) * inv),
+                                                 half2_bits(bf_hi(v[1]) * inv16, bf_hi(v[3]) * inv16));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sum += bf_lo(v[k]) * inv + bf_hi(v[k]) * inv;
-                }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            // a row that is not finite has no result: NaN
-            const float f = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
-            if (c == 0)      // (codes come as n 2^-24)
-                reinterpret_cast<float4*>(sm + S::kOffRow + to * S::kRowBytes)[t * 8 + g] =
-                    make_float4(f * 16777216.f, f * sum, __int_as_float(on ? s.len - s.nq + tok : -1), 0.f);
-        }
+                for (int k = 0; k < 4; ++k) sum += bf_lo(v[k]) * inv + bf_hi(v[k]) * inv;
+            }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        // a row that is not finite has no result: NaN
+        const float f = m >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+        if (c == 0)      // (codes come as n 2^-24)
+            reinterpret_cast<float4*>(sm + S::kOffRow + to * S::kRowBytes)[g] =
+                make_float4(f * 16777216.f, f * sum, __int_as_float(on ? s.len - s.nq + tok : -1), 0.f);
     };
 
     Segment s;
@@ -299,37 +298,26 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
     __syncthreads();
     for (int turn = 0; more; turn ^= 1) {
         const int row0 = s.row0, nr = s.nr, h = s.h, parts = s.parts;
-        u64 qf[NT], qs[NT];                                   // of rows 2 c and 2 c + 1: factor, sum
-        int pos[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const float4* const at = reinterpret_cast<const float4*>(sm + S::kOffRow + turn * S::kRowBytes) + t * 8 + 2 * c;
-            const float4 x = at[0], y = at[1];
-            qf[t] = pack(x.x, y.x);
-            qs[t] = pack(x.y, y.y);
-            pos[t][0] = __float_as_int(x.z);
-            pos[t][1] = __float_as_int(y.z);
-        }
+        // of rows 2 c and 2 c + 1: factor, sum, position
+        const float4* const row_at = reinterpret_cast<const float4*>(sm + S::kOffRow + turn * S::kRowBytes) + 2 * c;
+        const float4 r0 = row_at[0], r1 = row_at[1];
+        const u64 qf = pack(r0.x, r1.x), qs = pack(r0.y, r1.y);
+        const int pos[2] = {__float_as_int(r0.z), __float_as_int(r1.z)};
         const uint32_t q_at = (uint32_t)__cvta_generic_to_shared(sm + S::kOffQ + turn * S::kQBytes) + lane * 16;
 
-        float o[NT][DB * 8][4], ones[NT][4];
-        u64 l2[NT], mid2[NT], nref[NT];                       // sums; minus the references
+        float o[DB * 8][4], ones[4];
+        u64 l2 = 0, mid2 = 0, nref = 0;                       // sums; minus the references
         uint32_t with_ref = 0;                                // rows that have one, or are none, a bit each
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int i = 0; i < DB * 8; ++i)
 #pragma unroll
-            for (int i = 0; i < DB * 8; ++i)
+            for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
+        for (int k = 0; k < 4; ++k) ones[k] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) ones[t][k] = 0.f;
-            l2[t] = mid2[t] = 0;
-            nref[t] = 0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (t * 8 + 2 * c + k >= nr) with_ref |= 1u << (2 * t + k);
-        }
-        bool wait_ref = __any_sync(0xffffffffu, with_ref != (1u << (2 * NT)) - 1);
+        for (int k = 0; k < 2; ++k)
+            if (2 * c + k >= nr) with_ref |= 1u << k;
+        bool wait_ref = __any_sync(0xffffffffu, with_ref != 3u);
 
         const int n = steps;
         int t0 = t_of;
@@ -346,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
             const bool odd = t0 + S::kTokens - 1 > s.p_lo || (a.window && t0 <= s.p_hi - a.window) || (off & ((1u << SUB) - 1));
 
             // scores
-            float x[SUB][NT][4];
+            float x[SUB][4];
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
                 uint32_t w0[SUB][4], w1[SUB][4];
@@ -359,26 +347,20 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    uint4 q[NT];
+                    const uint4 q = lds128(q_at + (d * 4 + j) * 512);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) q[t] = lds128(q_at + ((t * DB + d) * 4 + j) * 512);
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            if (d == 0 && j == 0)
-                                mma_first(x[u][t], w0[u][j] & 0x000f000fu, w1[u][j] & 0x000f000fu, w0[u][j] & 0x00f000f0u,
-                                          w1[u][j] & 0x00f000f0u, q[t].x, q[t].y);
-                            else
-                                mma(x[u][t], w0[u][j] & 0x000f000fu, w1[u][j] & 0x000f000fu, w0[u][j] & 0x00f000f0u,
-                                    w1[u][j] & 0x00f000f0u, q[t].x, q[t].y);
-                        }
+                    for (int u = 0; u < SUB; ++u) {
+                        if (d == 0 && j == 0)
+                            mma_first(x[u], w0[u][j] & 0x000f000fu, w1[u][j] & 0x000f000fu, w0[u][j] & 0x00f000f0u,
+                                      w1[u][j] & 0x00f000f0u, q.x, q.y);
+                        else
+                            mma(x[u], w0[u][j] & 0x000f000fu, w1[u][j] & 0x000f000fu, w0[u][j] & 0x00f000f0u,
+                                w1[u][j] & 0x00f000f0u, q.x, q.y);
+                    }
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
                         const uint32_t x0 = w0[u][j] >> 8, x1 = w1[u][j] >> 8;
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            mma(x[u][t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, q[t].z, q[t].w);
+                        mma(x[u], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, q.z, q.w);
                     }
                 }
             }
@@ -394,11 +376,8 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                     iv[u][j] = rcp(vsc);
                     cm[u][j] = fmaf(8.f, vsc, bf_hi(vsm)) * iv[u][j];
                     const u64 ks2 = pack(bf_lo(ksm), bf_lo(ksm)), km2 = pack(bf_hi(ksm), bf_hi(ksm)), lv2 = pack(lv, lv);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const u64 b2 = add2(fma2(km2, qs[t], lv2), nref[t]);
-                        unpack(fma2(mul2(pack(x[u][t][2 * j], x[u][t][2 * j + 1]), qf[t]), ks2, b2), x[u][t][2 * j], x[u][t][2 * j + 1]);
-                    }
+                    const u64 b2 = add2(fma2(km2, qs, lv2), nref);
+                    unpack(fma2(mul2(pack(x[u][2 * j], x[u][2 * j + 1]), qf), ks2, b2), x[u][2 * j], x[u][2 * j + 1]);
                 }
             if (odd) {
                 // (what lies behind the request, in no block, or in one that every row's window has passed, may be anything)
@@ -410,75 +389,64 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                         const bool none = tt >= s.len || tt < see_first || (off >> u & 1);
                         if (none) iv[u][j] = cm[u][j] = 0.f;
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r)
-                                if (none || tt > pos[t][r] || (a.window && tt <= pos[t][r] - a.window)) x[u][t][2 * j + r] = -INFINITY;
+                        for (int r = 0; r < 2; ++r)
+                            if (none || tt > pos[r] || (a.window && tt <= pos[r] - a.window)) x[u][2 * j + r] = -INFINITY;
                     }
             }
             float top = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    top = fmaxf(fmaxf(top, fmaxf(x[u][t][0], x[u][t][1])), fmaxf(x[u][t][2], x[u][t][3]));
+            for (int u = 0; u < SUB; ++u) top = fmaxf(fmaxf(top, fmaxf(x[u][0], x[u][1])), fmaxf(x[u][2], x[u][3]));
             if (__any_sync(0xffffffffu, top > kRoom) || wait_ref) {
                 // new references: the maximum of the step's tokens per row
+                float f[2], nr2[2];
+                unpack(nref, nr2[0], nr2[1]);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float f[2], nr2[2];
-                    unpack(nref[t], nr2[0], nr2[1]);
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t bit = 1u << j;
+                    float m = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t bit = 1u << (2 * t + j);
-                        float m = -INFINITY;
+                    for (int u = 0; u < SUB; ++u) m = fmaxf(m, fmaxf(x[u][j], x[u][j + 2]));
 #pragma unroll
-                        for (int u = 0; u < SUB; ++u) m = fmaxf(m, fmaxf(x[u][t][j], x[u][t][j + 2]));
+                    for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+                    f[j] = 1.f;
+                    // every row that grew, while at it; a row's first tokens bring it its first one
+                    if (m > kHead || (!(with_ref & bit) && m != -INFINITY)) {
+                        const float by = kHead - m;
+                        f[j] = with_ref & bit ? ex2(by) : 0.f;
+                        nr2[j] += by;
 #pragma unroll
-                        for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-                        f[j] = 1.f;
-                        // every row that grew, while at it; a row's first tokens bring it its first one
-                        if (m > kHead || (!(with_ref & bit) && m != -INFINITY)) {
-                            const float by = kHead - m;
-                            f[j] = with_ref & bit ? ex2(by) : 0.f;
-                            nr2[j] += by;
-#pragma unroll
-                            for (int u = 0; u < SUB; ++u) {
-                                x[u][t][j] += by;
-                                x[u][t][j + 2] += by;
-                            }
-                            with_ref |= bit;
+                        for (int u = 0; u < SUB; ++u) {
+                            x[u][j] += by;
+                            x[u][j + 2] += by;
                         }
+                        with_ref |= bit;
                     }
-                    const u64 f2 = pack(f[0], f[1]);
-                    nref[t] = pack(nr2[0], nr2[1]);
-                    l2[t] = mul2(l2[t], f2);
-                    mid2[t] = mul2(mid2[t], f2);
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) ones[t][w] *= f[w & 1];
-#pragma unroll
-                    for (int m = 0; m < DB * 8; ++m)
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) o[t][m][w] *= f[w & 1];
                 }
-                wait_ref = __any_sync(0xffffffffu, with_ref != (1u << (2 * NT)) - 1);
+                const u64 f2 = pack(f[0], f[1]);
+                nref = pack(nr2[0], nr2[1]);
+                l2 = mul2(l2, f2);
+                mid2 = mul2(mid2, f2);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) ones[w] *= f[w & 1];
+#pragma unroll
+                for (int m = 0; m < DB * 8; ++m)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) o[m][w] *= f[w & 1];
+                wait_ref = __any_sync(0xffffffffu, with_ref != 3u);
             }
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
-                uint32_t p[NT][2];
+                uint32_t p[2];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float w0 = ex2(x[u][t][2 * j]), w1 = ex2(x[u][t][2 * j + 1]);
-                        const u64 w2 = pack(w0, w1);
-                        l2[t] = fma2(w2, pack(iv[u][j], iv[u][j]), l2[t]);
-                        mid2[t] = fma2(w2, pack(cm[u][j], cm[u][j]), mid2[t]);
-                        p[t][j] = transposed(half2_bits(w0, w1));
-                    }
-                    constexpr uint32_t one = 0x3c003c00u;
-                    mma(ones[t], one, one, one, one, p[t][0], p[t][1]);
+                for (int j = 0; j < 2; ++j) {
+                    const float w0 = ex2(x[u][2 * j]), w1 = ex2(x[u][2 * j + 1]);
+                    const u64 w2 = pack(w0, w1);
+                    l2 = fma2(w2, pack(iv[u][j], iv[u][j]), l2);
+                    mid2 = fma2(w2, pack(cm[u][j], cm[u][j]), mid2);
+                    p[j] = transposed(half2_bits(w0, w1));
                 }
+                constexpr uint32_t one = 0x3c003c00u;
+                mma(ones, one, one, one, one, p[0], p[1]);
                 // outputs. V: tokens 2 c, 2 c + 1, and 8 more on, dims 16 DB g ..
                 uint32_t v[4][2 * DB];
 #pragma unroll
@@ -505,10 +473,8 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
                         uint32_t x1 = __byte_perm(v[2][j], v[3][j], half ? 0x7632 : 0x5410);
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
-#pragma unroll
-                            for (int t = 0; t < NT; ++t)
-                                mma(o[t][j * 4 + half * 2 + m], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
-                                    x1 & 0x00f000f0u, p[t][0], p[t][1]);
+                            mma(o[j * 4 + half * 2 + m], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu,
+                                x1 & 0x00f000f0u, p[0], p[1]);
                             x0 >>= 8;
                             x1 >>= 8;
                         }
@@ -528,29 +494,26 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
         }
 
         // -------------------------------------------------------- the warps' sums together
+        float l[2], mid[2], nr2[2];
+        unpack(l2, l[0], l[1]);
+        unpack(mid2, mid[0], mid[1]);
+        unpack(nref, nr2[0], nr2[1]);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float l[2], mid[2], nr2[2];
-            unpack(l2[t], l[0], l[1]);
-            unpack(mid2[t], mid[0], mid[1]);
-            unpack(nref[t], nr2[0], nr2[1]);
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int x = 4; x < 32; x <<= 1) {
+                l[j] += __shfl_xor_sync(0xffffffffu, l[j], x);
+                mid[j] += __shfl_xor_sync(0xffffffffu, mid[j], x);
+            }
+            const int row = 2 * c + j;
+            if (g == 0) stats[warp * RT + row] = make_float2(-nr2[j], l[j]);
+            float* dst = outs + (warp * RT + row) * S::kPitch;
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) {
-                    l[j] += __shfl_xor_sync(0xffffffffu, l[j], x);
-                    mid[j] += __shfl_xor_sync(0xffffffffu, mid[j], x);
-                }
-                const int row = t * 8 + 2 * c + j;
-                if (g == 0) stats[warp * RT + row] = make_float2(-nr2[j], l[j]);
-                float* dst = outs + (warp * RT + row) * S::kPitch;
-#pragma unroll
-                for (int m = 0; m < DB * 8; ++m) {
-                    // o[m][j]: an even dim, n 2^-24; o[m][j + 2]: the next one, 16 times that
-                    const float add = fmaf(-8.f, ones[t][j], mid[j]);
-                    *reinterpret_cast<float2*>(dst + (m * 8 + g) * 2) =
-                        make_float2(fmaf(o[t][m][j], 16777216.f, add), fmaf(o[t][m][j + 2], 1048576.f, add));
-                }
+            for (int m = 0; m < DB * 8; ++m) {
+                // o[m][j]: an even dim, n 2^-24; o[m][j + 2]: the next one, 16 times that
+                const float add = fmaf(-8.f, ones[j], mid[j]);
+                *reinterpret_cast<float2*>(dst + (m * 8 + g) * 2) =
+                    make_float2(fmaf(o[m][j], 16777216.f, add), fmaf(o[m][j + 2], 1048576.f, add));
             }
         }
         __syncthreads();
@@ -588,10 +551,7 @@ __global__ void __launch_bounds__(kThreads, S::CTAS) attend4_kernel(const __grid
         }
         if (parts > 1) {
             __syncthreads();
-            finish<RT, D>(a, s, tid, kThreads, &last, [] {
-                __syncthreads();
-                return true;
-            });
+            finish<RT, D>(a, s, tid, kThreads, &last);
         }
         __syncthreads();                                      // the next segment's outputs take this one's place
         s = then;

@@ -8,7 +8,8 @@
 // where a row tile is more than half full (HALVES: the matrix products of the other half of its rows);
 // SW units before a row tile's first stand for what its start and end cost.
 // The U units are cut into chunks of equal numbers, one per CTA. A row tile whose units fall
-// into several chunks leaves partial sums; the last CTA to write its part joins them in chunk order.
+// into several chunks leaves partial sums, which are joined in chunk order: of few rows by the last CTA to write its part
+// (finish), of many by a kernel of their own.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -253,9 +254,9 @@ constexpr float kLow = -1e30f;           // reference of a row that has seen no 
 
 // Parts i0, i0 + step, .. (cnt of them) of a row tile together, by threads tid of T: part i has
 // reference m_i, sum l_i and outputs O_i of each row, and sum 2^(m_i - m) O_i, sum 2^(m_i - m) l_i, in order,
-// become `out` (FINAL) or part i0. `sync` is the threads' barrier (false: give up).
-template <int RT, int D, bool FINAL, class Sync>
-__device__ __forceinline__ bool join(const Args& a, const Segment& s, int i0, int step, int cnt, int tid, int T, Sync sync) {
+// become `out` (FINAL) or part i0. All T threads of the CTA take part.
+template <int RT, int D, bool FINAL>
+__device__ __forceinline__ void join(const Args& a, const Segment& s, int i0, int step, int cnt, int tid, int T) {
     float2* const ml = reinterpret_cast<float2*>(a.part_ml);
     // rows of one thread at most, so that a part's statistics are read before they are written
     for (int x0 = 0; x0 < s.nr * (D / 4); x0 += T) {
@@ -295,25 +296,24 @@ __device__ __forceinline__ bool join(const Args& a, const Segment& s, int i0, in
             *reinterpret_cast<uint2*>(a.out + (size_t)(s.q0 + tok) * a.out_row + (size_t)(s.h * a.group + rr - tok * a.group) * D + d) = w;
         } else {
             const size_t at = slot_of(s.v0, i0) * RT + row;
-            if (!sync()) return false;
+            __syncthreads();
             if (!on) continue;
             *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
             if (d == 0) ml[at] = make_float2(m, sum);
         }
     }
-    return true;
 }
 
 // After a part's sums are written and the threads that wrote them have met: the last of up to kFan
 // neighbours to get here joins them, the last group of neighbours the groups (parts of one long request
 // are as many as CTAs, and one SM would read them for longer than they took). Counters: of a row tile's
 // first group by its chunk, of the others by theirs, and of its groups; back to zero for the next call.
-// Threads tid of T take part, `sync` is their barrier.
+// All T threads of the CTA take part.
 constexpr int kFan = 12;
-template <int RT, int D, class Sync>
-__device__ __forceinline__ bool finish(const Args& a, const Segment& s, int tid, int T, volatile int* flag, Sync sync) {
+template <int RT, int D>
+__device__ __forceinline__ void finish(const Args& a, const Segment& s, int tid, int T, volatile int* flag) {
     const int k = s.part / kFan, i0 = k * kFan, cnt = min(kFan, s.parts - i0), groups = (s.parts + kFan - 1) / kFan;
-    auto last_of = [&](int* counter, int n) -> int {          // 1: this CTA is the last, -1: give up
+    auto last_of = [&](int* counter, int n) -> bool {         // this CTA is the last
         if (tid == 0) {
             __threadfence();                                  // (what this thread has seen written is ordered with it)
             const bool last = atomicAdd(counter, 1) == n - 1;
@@ -321,16 +321,17 @@ __device__ __forceinline__ bool finish(const Args& a, const Segment& s, int tid,
             __threadfence();
             *flag = last;
         }
-        if (!sync()) return -1;
+        __syncthreads();
         return *flag;
     };
-    const int mine = last_of(a.arrived + (k == 0 ? s.v0 : a.arrived_n + s.v0 + i0), cnt);
-    if (mine <= 0) return mine == 0;
-    if (groups == 1) return join<RT, D, true>(a, s, i0, 1, cnt, tid, T, sync);
-    if (!join<RT, D, false>(a, s, i0, 1, cnt, tid, T, sync) || !sync()) return false;
-    const int all = last_of(a.arrived + 2 * a.arrived_n + s.v0, groups);
-    if (all <= 0) return all == 0;
-    return join<RT, D, true>(a, s, 0, kFan, groups, tid, T, sync);
+    if (!last_of(a.arrived + (k == 0 ? s.v0 : a.arrived_n + s.v0 + i0), cnt)) return;
+    if (groups == 1) {
+        join<RT, D, true>(a, s, i0, 1, cnt, tid, T);
+        return;
+    }
+    join<RT, D, false>(a, s, i0, 1, cnt, tid, T);
+    __syncthreads();
+    if (last_of(a.arrived + 2 * a.arrived_n + s.v0, groups)) join<RT, D, true>(a, s, 0, kFan, groups, tid, T);
 }
 
 }  // namespace split

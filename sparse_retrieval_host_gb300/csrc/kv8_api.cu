@@ -423,8 +423,6 @@ int kv8_check_error(kv8_cache* c) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemcpy(&w, c->d_err, sizeof w, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess) e = cudaMemset(c->d_err, 0, sizeof w);
-    // a call that gave up may have left parts that nobody joined
-    if (e == cudaSuccess && (w & kErrTimeout) && c->arrived_n) e = cudaMemset(c->d_arrived, 0, c->arrived_n * sizeof(int));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(c, e, "kv8_check_error");
     if (w & kv8::kErrNoBlocks) return fail(c, SRH_ERR_NOMEM, "too few free blocks; the call changed nothing");
