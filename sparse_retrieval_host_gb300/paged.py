@@ -416,7 +416,9 @@ class PagedKV4(PagedKV8):
         return (self.n_blocks, self.Hk, self.bs, 2), torch.bfloat16
 
     def _handle_stride(self, stride: int) -> int:
-        return 0
+        if stride % 16:
+            raise ValueError("blocks of codes must lie a multiple of 16 bytes apart")
+        return 0                         # the handle's own is the 8-bit pools'
 
     def _pool_of(self, stride: int):
         return abi.Kv4Pool(self.k_codes[-1].data_ptr(), self.k_scale[-1].data_ptr(),

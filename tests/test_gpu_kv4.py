@@ -1360,3 +1360,13 @@ def test_layers_of_both_widths_attend_on_one_handle(D):
         check()
     c4.close()
     c8.close()
+
+
+def test_pools_whose_blocks_are_not_16_bytes_apart_are_refused_at_once():
+    """As PagedKV8 refuses them: when the cache is made, not by its first call."""
+    kw = dict(batch=1, n_kv_heads=1, head_dim=128, block_tokens=16, n_blocks=4, max_blocks=4)
+    for make, width in ((_kv4, 64), (_kv8, 128)):
+        n = 16 * width + 8
+        codes = torch.zeros(4 * n, dtype=torch.uint8, device="cuda").as_strided((4, 1, 16, width), (n, 16 * width, width, 1))
+        with pytest.raises((ValueError, _abi().SrhError)):
+            make(buffers=dict(k_codes=codes), **kw)
