@@ -785,8 +785,8 @@ int kv4_read(kv8_cache* c, const kv4_pool* pool, const int32_t* d_table, const i
  * is rounded to fp16: within 2^-11 of it, or 2^-35 of the row's largest. Codes enter exactly where a
  * request has up to 24 query rows per KV head (32 where head_dim is 256); else keys and values do, rounded to fp16:
  * within 2^-11 of each plus 2^-34 of the largest of its 128 tokens (of 2^-64, if V's is smaller). V's scales are taken as
- * at least 2^-64; those that a row sees are to lie within 2^96 of each other, scores within 10^30 of 0, keys within
- * 2^60, and the V values that a row sees, summed by magnitude in a dim, within 2^47.
+ * at least 2^-64; those that a row sees are to lie within 2^96 of each other, scores within 10^30 of 0, queries
+ * within 2^100, keys within 2^60, and the V values that a row sees, summed by magnitude in a dim, within 2^47.
  * Which requests have how many rows only the device knows. A call of as many rows as requests, or of fewer while they are at
  * most 128 per KV head, is taken for a decode step (one token each); one of fewer that are more than 128 costs 4 us more than
  * if only requests with tokens were named. Results are the same whatever the rows turn out to be, but a prompt alone among as many

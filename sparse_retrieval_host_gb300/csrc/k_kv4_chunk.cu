@@ -17,18 +17,19 @@
 // TMEM room for them and two S only that way (the third of the products and half of the exponentials that are made
 // twice cost as much as twice the rows of 128 dims would).
 //
-// Per 128 tokens x 256 rows: 2,048 cycles of MMA at the fp16 rate, 2,048 of exponentials (16 a cycle),
-// 2,048 of shared memory (QK reads both operands: 1,024; PV one: 512; expanding writes 512): no unit
-// is free, the floor of one is that of all.
+// Per 128 tokens x 256 rows: 2,048 cycles of MMA at the fp16 rate, 1,024 of exponentials (32 a cycle, measured),
+// 2,048 of shared memory (QK reads both operands: 1,024; PV one: 512; expanding writes 512).
 //
 // Roles: warps 0-3 and 4-7 softmax of the two lanes, 8-11 expand K, 12-15 V (a thread a token, the
 // next tile's codes in registers), 16 issues the MMAs, 17 finds the segments. All waits are on mbarriers and bounded.
 //
-// Measured: four prompts of up to 1,024 tokens on up to 8,192, 32 / 8 heads of 128: 328 us with the join, 0.37 of the fp16 rate;
+// Measured: four prompts of up to 1,024 tokens on up to 8,192, 32 / 8 heads of 128: 326 us with the join, 0.38 of the fp16 rate;
 // some 4,400 cycles a full tile. Of those a warp's 128 columns from TMEM cost about 300 each time (they are read twice, once
-// for the maximum and once for the weights: 96 registers hold 32 columns), the exponentials of a scheduler's two
-// warps 1,580; the tensor pipe is busy for 33 %. Scores in registers (152 of them, by setmaxnreg): 386 us. Of as
-// many products with 16 / 4 heads of 256: 416 us (8 rows at a time by the kernel of few rows: 1,463).
+// for the maximum and once for the weights: 96 registers hold 32 columns; 56 bytes are spilled, 36 of 256 dims), the
+// scores of a scheduler's two warps on their way to weights 1,580. The tensor pipe is busy for 33 % of the kernel's time, which is
+// thus 6,100 cycles a tile: starts and ends of the three to four row tiles of a CTA, and the wait for the last CTA, are the rest. Scores
+// in registers (152 of them, by setmaxnreg): 386 us. Of as many products with 16 / 4 heads of 256: 416 us (8 rows at a time by
+// the kernel of few rows: 1,463).
 #include "kv4_split.cuh"
 #include "umma.cuh"
 

@@ -1370,3 +1370,18 @@ def test_pools_whose_blocks_are_not_16_bytes_apart_are_refused_at_once():
         codes = torch.zeros(4 * n, dtype=torch.uint8, device="cuda").as_strided((4, 1, 16, width), (n, 16 * width, width, 1))
         with pytest.raises((ValueError, _abi().SrhError)):
             make(buffers=dict(k_codes=codes), **kw)
+
+
+@pytest.mark.parametrize("G,D", [(4, 128), (40, 128), (4, 256), (40, 256)])
+def test_attend_queries_of_any_size(G, D):
+    """Queries of 2^-98 and 2^98 with scales that make up for it: the bits of ordinary ones."""
+    g = _gen(100)
+    c = _kv4(batch=1, n_kv_heads=2, head_dim=D, block_tokens=16, n_blocks=20, max_blocks=20)
+    _filled(c, g, [300])
+    q, cu = _bf16(g, 2, 2 * G, D), _i32([0, 2])
+    want = c.attend(q, cu, scale=0.0625)
+    _check_close(c, q, cu, want, 0.0625)
+    for k in (-98, 98):
+        out = c.attend((q.double() * 2.0 ** k).bfloat16(), cu, scale=0.0625 * 2.0 ** -k)
+        assert bool((out == want).all())
+    c.close()
